@@ -1,0 +1,433 @@
+"""Python binding of the block operators of libs6 (include/s6_block.h): the
+multi-head selective scan with its gradients and single-token step, and the
+norms before and after it.
+
+As in ``s6``: argument marshalling only, torch device tensors in and out, work
+enqueued on the current stream of the tensors' device.  ``HeadsScan``,
+``AddNorm`` and ``GatedNorm`` are the same operators for torch autograd.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import s6
+from .s6 import _DT, _check, _opt, _ptr, _req
+
+S6_DELTA_SOFTPLUS, S6_UNIT_INPUT, S6_GATE_AFTER = 1, 4, 8
+MAX_DSTATE = 128
+
+
+class HeadsDims(ctypes.Structure):
+    """s6_heads_dims of include/s6_block.h."""
+
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "seqlen", "heads", "headdim", "groups", "dstate", "x_batch", "x_token", "delta_batch",
+                 "delta_token", "b_batch", "b_token", "c_batch", "c_token")]
+
+
+_lib = None
+
+
+def _load():
+    global _lib
+    if _lib is None:
+        lib = s6.load_library()
+        i64, vp, i32, f32, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        dims, szp = ctypes.POINTER(HeadsDims), ctypes.POINTER(ctypes.c_size_t)
+        ws = [vp, sz, vp]  # workspace, workspace_bytes, stream
+        for name, args in {
+            "s6_heads_scan_fwd": [dims, i32, i32] + [vp] * 10 + ws,
+            "s6_heads_scan_fwd_workspace_size": [dims, i32, szp],
+            "s6_heads_scan_bwd": [dims, i32, i32] + [vp] * 18 + ws,
+            "s6_heads_scan_bwd_workspace_size": [dims, i32, szp],
+            "s6_heads_state_update": [dims, i32, i32] + [vp] * 10,
+            "s6_add_norm_fwd": [i64, i64, i32, i32, vp, i64, vp, vp, vp, f32, f32, vp, vp, vp],
+            "s6_add_norm_bwd": [i64, i64, i32, i32, vp, vp, vp, vp, i64, vp, vp, f32, f32, vp, vp, vp, vp] + ws,
+            "s6_add_norm_bwd_workspace_size": [i64, i64, szp],
+            "s6_gated_norm_fwd": [i64, i64, i64, i32, i32, vp, i64, vp, i64, vp, f32, vp, vp],
+            "s6_gated_norm_bwd": [i64, i64, i64, i32, i32, vp, vp, i64, vp, i64, vp, f32, vp, vp, vp] + ws,
+            "s6_gated_norm_bwd_workspace_size": [i64, i64, i64, szp],
+        }.items():
+            fn = getattr(lib, name)
+            fn.restype = i32
+            fn.argtypes = args
+        _lib = lib
+    return _lib
+
+
+def _stream(like):
+    return torch.cuda.current_stream(like.device).cuda_stream
+
+
+def _same_device(first, *others):
+    """The kernels run on the device of `first`: every tensor has to be there."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _workspace(query, like):
+    """(tensor, pointer, bytes) of a fresh workspace on the current stream."""
+    out = ctypes.c_size_t(0)
+    _check(query(ctypes.byref(out)))
+    if out.value == 0:
+        return None, None, 0
+    t = torch.empty(out.value, dtype=torch.uint8, device=like.device)
+    return t, t.data_ptr(), out.value
+
+
+def _dtype(t, name="x"):
+    if t.dtype not in _DT:
+        raise ValueError(f"unsupported {name} dtype {t.dtype}")
+    return t.dtype
+
+
+def _rows(t, name, shape, dtype, inner):
+    """(batch stride, token stride) of a device tensor whose last `inner`
+    dimensions are contiguous: the leading ones may be strided (slices of
+    wider rows)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.numel() == 0:
+        return (0,) * (len(shape) - inner)
+    st = t.stride()
+    want = 1
+    for i in range(len(shape) - 1, len(shape) - 1 - inner, -1):
+        if shape[i] != 1 and st[i] != want:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        want *= shape[i]
+    lead = len(shape) - inner
+    # a stride along a single element is never taken
+    return tuple(st[i] if shape[i] > 1 else max(want, 0) for i in range(lead))
+
+
+def _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, tokens):
+    dt = _dtype(x)
+    if x.dim() != (4 if tokens else 3) or Bm is None or Bm.dim() != x.dim():
+        raise ValueError("x is (batch, seqlen, heads, headdim), Bm and Cm (batch, seqlen, groups, dstate); without "
+                         "seqlen for a single token")
+    lead = tuple(x.shape[:2]) if tokens else (x.shape[0],)
+    heads, headdim = x.shape[-2:]
+    groups, dstate = Bm.shape[-2:]
+    xs = _rows(x, "x", x.shape, dt, 2)
+    bs = _rows(Bm, "Bm", (*lead, groups, dstate), dt, 2)
+    cs = _rows(Cm, "Cm", (*lead, groups, dstate), dt, 2)
+    if delta is None:
+        if delta_bias is not None or delta_softplus:
+            raise ValueError("delta_bias and delta_softplus need a delta")
+        ds = (0, 0)
+    else:
+        ds = _rows(delta, "delta", (*lead, heads), dt, 1)
+    _req(A, "A", (heads,), torch.float32)
+    _opt(D, "D", (heads,), torch.float32)
+    _opt(delta_bias, "delta_bias", (heads,), torch.float32)
+    _same_device(x, delta, A, Bm, Cm, D, delta_bias)
+    pad = (lambda s: s) if tokens else (lambda s: (s[0], 0))
+    dims = HeadsDims(lead[0], lead[1] if tokens else 1, heads, headdim, groups, dstate,
+                     *pad(xs), *pad(ds), *pad(bs), *pad(cs))
+    flags = (S6_DELTA_SOFTPLUS if delta_softplus else 0) | (S6_UNIT_INPUT if unit_input else 0)
+    return dims, _DT[dt], flags
+
+
+def _state(t, name, x):
+    return _opt(t, name, (x.shape[0], x.shape[-2], x.shape[-1], t.shape[-1] if t is not None else 0), torch.float32)
+
+
+def heads_scan_fwd(x, delta, A, Bm, Cm, D=None, h0=None, return_last_state=False, delta_bias=None,
+                   delta_softplus=False, unit_input=False, y=None, h_last=None):
+    """Multi-head selective scan (linear attention with a decay per head).
+    x: (batch, L, heads, headdim); delta: (batch, L, heads) or None (a step of
+    1: one fixed decay exp(A) per head); Bm, Cm: (batch, L, groups, N), N <=
+    128, groups a divisor of heads; A, D, delta_bias: (heads,) fp32; h0:
+    (batch, heads, headdim, N) fp32.  x, delta, Bm, Cm share one dtype
+    (float32 or bfloat16) and may be slices of wider rows.  unit_input: the
+    input term is x B instead of step x B.  Returns y like x (contiguous), and
+    h_last (batch, heads, headdim, N) fp32 if requested."""
+    dims, dt, flags = _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, True)
+    sshape = (dims.batch, dims.heads, dims.headdim, dims.dstate)
+    _opt(h0, "h0", sshape, torch.float32)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _req(y, "y", x.shape, x.dtype)
+    if return_last_state and h_last is None:
+        h_last = torch.empty(sshape, dtype=torch.float32, device=x.device)
+    _opt(h_last, "h_last", sshape, torch.float32)
+    _same_device(x, h0, y, h_last)
+    lib = _load()
+    ref = ctypes.byref(dims)
+    with torch.cuda.device(x.device):
+        keep, wsp, wsn = _workspace(lambda out: lib.s6_heads_scan_fwd_workspace_size(ref, dt, out), x)
+        rc = lib.s6_heads_scan_fwd(ref, dt, flags, _ptr(x), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(Bm), _ptr(Cm),
+                                   _ptr(D), _ptr(h0), _ptr(y), _ptr(h_last), wsp, wsn, _stream(x))
+    del keep
+    _check(rc)
+    return (y, h_last) if return_last_state else y
+
+
+def heads_scan_bwd(x, delta, A, Bm, Cm, dy, D=None, h0=None, dh_last=None, delta_bias=None, delta_softplus=False,
+                   unit_input=False):
+    """Gradients of <dy, y> + <dh_last, h_last> for heads_scan_fwd with the
+    same inputs.  dy: like y, contiguous; dh_last: like h_last or None.
+    Returns a dict: dx, ddelta (where delta is given), dBm, dCm in the input
+    dtype; dA, and where their input is given dD, ddelta_bias, dh0 in fp32."""
+    dims, dt, flags = _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, True)
+    sshape = (dims.batch, dims.heads, dims.headdim, dims.dstate)
+    _opt(h0, "h0", sshape, torch.float32)
+    _opt(dh_last, "dh_last", sshape, torch.float32)
+    _req(dy, "dy", x.shape, x.dtype)
+    _same_device(x, h0, dh_last, dy)
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=x.device)  # noqa: E731
+    g = {"dx": new(x), "dBm": new(Bm), "dCm": new(Cm), "dA": new(A)}
+    for name, t in (("ddelta", delta), ("dD", D), ("ddelta_bias", delta_bias), ("dh0", h0)):
+        if t is not None:
+            g[name] = new(t)
+    lib = _load()
+    ref = ctypes.byref(dims)
+    with torch.cuda.device(x.device):
+        keep, wsp, wsn = _workspace(lambda out: lib.s6_heads_scan_bwd_workspace_size(ref, dt, out), x)
+        rc = lib.s6_heads_scan_bwd(ref, dt, flags, _ptr(x), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(Bm), _ptr(Cm),
+                                   _ptr(D), _ptr(h0), _ptr(dy), _ptr(dh_last), _ptr(g["dx"]), _ptr(g.get("ddelta")),
+                                   _ptr(g["dA"]), _ptr(g["dBm"]), _ptr(g["dCm"]), _ptr(g.get("dD")),
+                                   _ptr(g.get("dh0")), _ptr(g.get("ddelta_bias")), wsp, wsn, _stream(x))
+    del keep
+    _check(rc)
+    return g
+
+
+def heads_state_update(h, x, delta, A, Bm, Cm, D=None, delta_bias=None, delta_softplus=False, unit_input=False, y=None):
+    """One token of every sequence: h (batch, heads, headdim, N) fp32 is
+    advanced in place; x: (batch, heads, headdim), delta: (batch, heads) or
+    None, Bm, Cm: (batch, groups, N).  Returns y (batch, heads, headdim) in
+    x's dtype."""
+    dims, dt, flags = _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, False)
+    _req(h, "h", (dims.batch, dims.heads, dims.headdim, dims.dstate), torch.float32)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _req(y, "y", x.shape, x.dtype)
+    _same_device(x, h, y)
+    with torch.cuda.device(x.device):
+        rc = _load().s6_heads_state_update(ctypes.byref(dims), dt, flags, _ptr(h), _ptr(x), _ptr(delta),
+                                           _ptr(delta_bias), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(y), _stream(x))
+    _check(rc)
+    return y
+
+
+def _flat(t, name, shape, dtype):
+    """Row stride of a (..., dim) device tensor seen as rows of dim elements."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    dim = shape[-1]
+    if t.is_contiguous():
+        return dim
+    st = t.stride()
+    if dim > 1 and st[-1] != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    stride = None  # one stride for all rows: that of the last leading dimension, the others a multiple of it
+    size = 1
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] == 1:
+            continue
+        if stride is None:
+            stride = st[i]
+        elif st[i] != stride * size:
+            raise ValueError(f"{name}'s rows must lie at one stride")
+        size *= shape[i]
+    if stride is not None and stride < dim:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return dim if stride is None else stride
+
+
+def _count(shape):
+    n = 1
+    for v in shape[:-1]:
+        n *= v
+    return n
+
+
+def add_norm_fwd(x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5, residual_dtype=None, out=None,
+                 residual_out=None):
+    """Residual add, residual scale and RMS norm before a block: r' = residual
+    + scale * gamma * x, out = r' / sqrt(mean(r'^2) + eps) * weight over the
+    last dimension.  x may be a slice of wider rows; weight, gamma: (dim,)
+    fp32; residual: like x, in x's dtype or float32 (None: no residual yet, r'
+    in residual_dtype, float32 unless given).  Returns (out in x's dtype,
+    r' in the residual's dtype); residual_out may be the residual itself."""
+    dt = _dtype(x)
+    stride = _flat(x, "x", x.shape, dt)
+    rt = residual.dtype if residual is not None else residual_dtype or torch.float32
+    if rt not in (torch.float32, dt):
+        raise ValueError(f"residual dtype {rt}: expected float32 or {dt}")
+    dim = x.shape[-1]
+    _opt(residual, "residual", x.shape, rt)
+    _req(weight, "weight", (dim,), torch.float32)
+    _opt(gamma, "gamma", (dim,), torch.float32)
+    if out is None:
+        out = torch.empty(x.shape, dtype=dt, device=x.device)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=rt, device=x.device)
+    _req(out, "out", x.shape, dt)
+    _req(residual_out, "residual_out", x.shape, rt)
+    _same_device(x, weight, residual, gamma, out, residual_out)
+    with torch.cuda.device(x.device):
+        rc = _load().s6_add_norm_fwd(_count(x.shape), dim, _DT[dt], _DT[rt], _ptr(x), stride, _ptr(residual),
+                                     _ptr(weight), _ptr(gamma), scale, eps, _ptr(out), _ptr(residual_out), _stream(x))
+    _check(rc)
+    return out, residual_out
+
+
+def add_norm_bwd(dout, residual_out, weight, dresidual_out=None, x=None, gamma=None, scale=1.0, eps=1e-5):
+    """Gradients of <dout, out> + <dresidual_out, r'> for add_norm_fwd, from
+    the r' it returned.  Returns a dict: dx (dout's dtype), dresidual (r''s
+    dtype), dweight, and dgamma where gamma is given (then x is needed)."""
+    dt = _dtype(dout, "dout")
+    rt = residual_out.dtype
+    dim = dout.shape[-1]
+    if rt not in (torch.float32, dt):
+        raise ValueError(f"residual_out dtype {rt}: expected float32 or {dt}")
+    _req(dout, "dout", dout.shape, dt)
+    _req(residual_out, "residual_out", dout.shape, rt)
+    _opt(dresidual_out, "dresidual_out", dout.shape, rt)
+    _req(weight, "weight", (dim,), torch.float32)
+    _opt(gamma, "gamma", (dim,), torch.float32)
+    stride = dim
+    if gamma is not None:
+        stride = _flat(x, "x", dout.shape, dt)
+    _same_device(dout, residual_out, dresidual_out, weight, gamma, x)
+    g = {"dx": torch.empty(dout.shape, dtype=dt, device=dout.device),
+         "dresidual": torch.empty(dout.shape, dtype=rt, device=dout.device),
+         "dweight": torch.empty_like(weight)}
+    if gamma is not None:
+        g["dgamma"] = torch.empty_like(gamma)
+    lib = _load()
+    rows = _count(dout.shape)
+    with torch.cuda.device(dout.device):
+        keep, wsp, wsn = _workspace(lambda o: lib.s6_add_norm_bwd_workspace_size(rows, dim, o), dout)
+        rc = lib.s6_add_norm_bwd(rows, dim, _DT[dt], _DT[rt], _ptr(dout), _ptr(dresidual_out), _ptr(residual_out),
+                                 _ptr(x) if gamma is not None else None, stride, _ptr(weight), _ptr(gamma), scale, eps,
+                                 _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]), _ptr(g.get("dgamma")), wsp,
+                                 wsn, _stream(dout))
+    del keep
+    _check(rc)
+    return g
+
+
+def _gated_args(y, z, weight, groups):
+    dt = _dtype(y, "y")
+    dim = y.shape[-1]
+    if groups < 1 or dim % groups:
+        raise ValueError(f"{groups} groups do not divide {dim} columns")
+    _req(weight, "weight", (dim,), torch.float32)
+    _same_device(y, z, weight)
+    return dt, dim, _flat(y, "y", y.shape, dt), dim if z is None else _flat(z, "z", y.shape, dt)
+
+
+def gated_norm_fwd(y, z, weight, groups=1, gate_after=False, eps=1e-5, out=None):
+    """SiLU gate and RMS norm after the scan, over groups of the last
+    dimension: rms(y * SiLU(z)) * weight, or rms(y) * weight * SiLU(z) with
+    gate_after.  y and z (None: no gate) may be slices of wider rows.  Returns
+    a contiguous tensor in y's dtype."""
+    dt, dim, ys, zs = _gated_args(y, z, weight, groups)
+    if out is None:
+        out = torch.empty(y.shape, dtype=dt, device=y.device)
+    _req(out, "out", y.shape, dt)
+    _same_device(y, out)
+    with torch.cuda.device(y.device):
+        rc = _load().s6_gated_norm_fwd(_count(y.shape), dim, groups, _DT[dt], S6_GATE_AFTER if gate_after else 0,
+                                       _ptr(y), ys, _ptr(z), zs, _ptr(weight), eps, _ptr(out), _stream(y))
+    _check(rc)
+    return out
+
+
+def gated_norm_bwd(dout, y, z, weight, groups=1, gate_after=False, eps=1e-5):
+    """Gradients of <dout, out> for gated_norm_fwd: a dict of dy, dz (where z
+    is given) in y's dtype and dweight in fp32."""
+    dt, dim, ys, zs = _gated_args(y, z, weight, groups)
+    _req(dout, "dout", y.shape, dt)
+    _same_device(y, dout)
+    g = {"dy": torch.empty(y.shape, dtype=dt, device=y.device), "dweight": torch.empty_like(weight)}
+    if z is not None:
+        g["dz"] = torch.empty(y.shape, dtype=dt, device=y.device)
+    lib = _load()
+    rows = _count(y.shape)
+    with torch.cuda.device(y.device):
+        keep, wsp, wsn = _workspace(lambda o: lib.s6_gated_norm_bwd_workspace_size(rows, dim, groups, o), y)
+        rc = lib.s6_gated_norm_bwd(rows, dim, groups, _DT[dt], S6_GATE_AFTER if gate_after else 0, _ptr(dout), _ptr(y),
+                                   ys, _ptr(z), zs, _ptr(weight), eps, _ptr(g["dy"]), _ptr(g.get("dz")),
+                                   _ptr(g["dweight"]), wsp, wsn, _stream(y))
+    del keep
+    _check(rc)
+    return g
+
+
+class HeadsScan(torch.autograd.Function):
+    """heads_scan_fwd with its gradients: y, h_last = HeadsScan.apply(x, delta,
+    A, Bm, Cm, D, h0, delta_bias, delta_softplus, unit_input).  delta, D, h0 and
+    delta_bias may be None.  The backward recomputes the states."""
+
+    @staticmethod
+    def forward(ctx, x, delta, A, Bm, Cm, D=None, h0=None, delta_bias=None, delta_softplus=False, unit_input=False):
+        ctx.save_for_backward(x, delta, A, Bm, Cm, D, h0, delta_bias)
+        ctx.opts = dict(delta_softplus=delta_softplus, unit_input=unit_input)
+        ctx.set_materialize_grads(False)
+        return heads_scan_fwd(x, delta, A, Bm, Cm, D=D, h0=h0, return_last_state=True, delta_bias=delta_bias, **ctx.opts)
+
+    @staticmethod
+    def backward(ctx, dy, dh_last):
+        x, delta, A, Bm, Cm, D, h0, delta_bias = ctx.saved_tensors
+        dy = torch.zeros_like(x, memory_format=torch.contiguous_format) if dy is None else dy.contiguous()
+        g = heads_scan_bwd(x, delta, A, Bm, Cm, dy, D=D, h0=h0, delta_bias=delta_bias,
+                           dh_last=None if dh_last is None else dh_last.contiguous(), **ctx.opts)
+        return (g["dx"], g.get("ddelta"), g["dA"], g["dBm"], g["dCm"], g.get("dD"), g.get("dh0"), g.get("ddelta_bias"),
+                None, None)
+
+
+class AddNorm(torch.autograd.Function):
+    """add_norm_fwd with its gradients: out, r' = AddNorm.apply(x, weight,
+    residual, gamma, scale, eps); residual and gamma may be None."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5):
+        out, res = add_norm_fwd(x, weight, residual=residual, gamma=gamma, scale=scale, eps=eps)
+        ctx.save_for_backward(res, weight, gamma, x if gamma is not None else None)
+        ctx.scale, ctx.eps, ctx.has_residual, ctx.dt = scale, eps, residual is not None, x.dtype
+        ctx.set_materialize_grads(False)
+        return out, res
+
+    @staticmethod
+    def backward(ctx, dout, dres):
+        res, weight, gamma, x = ctx.saved_tensors
+        dout = torch.zeros(res.shape, dtype=ctx.dt, device=res.device) if dout is None else dout.contiguous()
+        g = add_norm_bwd(dout, res, weight, dresidual_out=None if dres is None else dres.contiguous(), x=x, gamma=gamma,
+                         scale=ctx.scale, eps=ctx.eps)
+        return g["dx"], g["dweight"], g["dresidual"] if ctx.has_residual else None, g.get("dgamma"), None, None
+
+
+class GatedNorm(torch.autograd.Function):
+    """gated_norm_fwd with its gradients: out = GatedNorm.apply(y, z, weight,
+    groups, gate_after, eps); z may be None."""
+
+    @staticmethod
+    def forward(ctx, y, z, weight, groups=1, gate_after=False, eps=1e-5):
+        ctx.save_for_backward(y, z, weight)
+        ctx.opts = dict(groups=groups, gate_after=gate_after, eps=eps)
+        return gated_norm_fwd(y, z, weight, **ctx.opts)
+
+    @staticmethod
+    def backward(ctx, dout):
+        y, z, weight = ctx.saved_tensors
+        g = gated_norm_bwd(dout.contiguous(), y, z, weight, **ctx.opts)
+        return g["dy"], g.get("dz"), g["dweight"], None, None, None

@@ -16,9 +16,12 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("scan.hip", "scan_ext.hip", "scan_conv.hip", "scan_hold.hip",
-                                                    "step.hip", "bwd.hip", "ssd.hip", "common.hip")]
+                                                    "step.hip", "bwd.hip", "ssd.hip", "common.hip",
+                                                    "heads_fwd.hip", "heads_state.hip", "heads_bwd.hip",
+                                                    "heads_step.hip", "norm.hip")]
 HEADERS = [os.path.join(CSRC, "s6_internal.h"), os.path.join(CSRC, "scan_kernel.h"),
-           os.path.join(ROOT, "include", "s6.h")]
+           os.path.join(CSRC, "block_internal.h"), os.path.join(CSRC, "heads_kernel.h"),
+           os.path.join(ROOT, "include", "s6.h"), os.path.join(ROOT, "include", "s6_block.h")]
 LIB = os.path.join(PKG, "libs6.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # Packed FP32 instructions are switched off: hipcc would otherwise pair

@@ -1,0 +1,690 @@
+// heads_bwd.hip -- gradients of the multi-head scan (s6_heads_scan_bwd).
+//
+// With the adjoint L_t = dy_t C_t^T + e^{a_{t+1}} L_{t+1} of the state (a_t =
+// s_t A):
+//   dx_t = w_t L_t B_t + D dy_t     dB_t = sum over heads of w_t L_t^T x_t
+//   dC_t = sum over heads of S_t^T dy_t             dw_t = x_t . L_t B_t
+//   G_t = <L_t, e^{a_t} S_{t-1}>    (gradient of a_t)
+//   ds_t = A G_t + dw_t,  dA = sum s_t G_t,  dD = sum x_t . dy_t
+// In a block of Q tokens, S entering it and L entering it from its end, with
+// c the running sum of the log decays, E_ts = (dy_t . x_s)(C_t . B_s) e^{c_t - c_s}:
+//   dx_s = sum_{t>=s} (C_t . B_s) e^{c_t - c_s} w_s dy_t + w_s e^{c_Q - c_s} L B_s + D dy_s
+//   dC_t = sum_s P_ts B_s + e^{c_t} S^T dy_t,   P_ts = (dy_t . x_s) e^{c_t - c_s} w_s
+//   dB_s = sum_t P_ts C_t + w_s e^{c_Q - c_s} L^T x_s
+//   G_t  = sum_{u >= t > s} w_s E_us                      (both inside)
+//        + sum_{u >= t} e^{c_u} dy_u . S C_u              (from before the block)
+//        + sum_{s < t} w_s e^{c_Q - c_s} x_s . L B_s      (to after the block)
+//        + e^{c_Q} <L, S>                                 (through it)
+// The four parts of G are sums of like terms, not differences of running
+// totals over the sequence, so G keeps its relative accuracy where the decay
+// is strong.
+//
+// Two phases.  s6_heads_state_kernel walks the sequence in both directions
+// and stores S and L entering every block (bf16 inputs: as two bf16 planes in
+// operand order).  Then a workgroup of eight waves owns one block of one
+// sequence and a run of a group's heads: B, C, their Gram matrix and the
+// sums over heads -- dB, dC and P -- stay on chip while it goes through the
+// heads, so x, dy and the states are read once and dx is written once.  The
+// block is Q = 128 tokens for bf16 (64 for fp32, whose tiles are twice the
+// size): the states are 8 bytes per state element and block against 6 Q bytes
+// per channel of x, dy and dx, and 160 KB of LDS hold no more.
+//
+// Waves: wave w owns the 16 state columns n of strip w % NS in the products
+// with S and L (dC, dB: rows n, columns t), all of them in registers, and
+// for dx the channel tile w % 4 of every second token tile.
+#include "heads_kernel.h"
+
+namespace s6i {
+
+namespace {
+
+template <typename In>
+constexpr int kBQ = sizeof(In) == 2 ? 128 : 64;  // tokens per block (kBlockTokens of heads_state.hip)
+
+struct HeadsBwdArgs {
+  HeadsArgs h;
+  void* dx;
+  void* ddelta;           // or null
+  void* dB;
+  void* dC;
+  float* parts;           // (3, batch * nblk, heads): dA, dD, dbias per block
+  float* bc;              // (nhb, 2, batch * L, groups, NT) partial dB, dC, or null (one head run)
+  int64_t nblk, rows;
+  int groups, nhb, hpb;   // head runs of a group and heads per run
+  int want_d, want_bias;
+};
+
+// Offsets in LDS (bytes).
+template <typename In, int NT>
+struct BwdLds {
+  static constexpr int Q = kBQ<In>;
+  static constexpr int NTT = Q / 16, H = NTT / 2, NTILE = NTT * (NTT + 1) / 2;
+  static constexpr int NFRAG = H * (H + 1);
+  static constexpr int XP = kTP + kPad, BP = NT + kPad;
+  static constexpr int NS = NT / 16;
+  static constexpr int bs = 0;
+  static constexpr int cm = bs + Q * BP * (int)sizeof(In);
+  static constexpr int xs = cm + Q * BP * (int)sizeof(In);
+  static constexpr int ys = xs + Q * XP * (int)sizeof(In);
+  static constexpr int lm = ys + Q * XP * (int)sizeof(In);
+  static constexpr int mf = lm + NT * XP * (int)sizeof(In);
+  static constexpr int rp = mf + NFRAG * 512 * (int)sizeof(In);  // row sums of the tiles
+  static constexpr int cp = rp + NTILE * 16 * 4;                 // column sums
+  static constexpr int yp = cp + NTILE * 16 * 4;                 // dy . S C by strip
+  static constexpr int up = yp + NS * Q * 4;                     // x . L B by strip
+  static constexpr int cs = up + NS * Q * 4;
+  static constexpr int ec = cs + Q * 4;
+  static constexpr int ww = ec + Q * 4;
+  static constexpr int wd = ww + Q * 4;
+  static constexpr int th = wd + Q * 4;    // <L, S> by strip
+  static constexpr int dd = th + 8 * 4;    // x . dy by diagonal tile
+  static constexpr int total = dd + 8 * 4;
+  static_assert(total <= 163840, "LDS");
+};
+
+// First operand of the decayed Gram matrix's column tile J, in units of 512
+// elements: the token pairs kk = J/2 .. H - 1 follow.
+template <int H>
+__device__ __forceinline__ int frag_at(int J, int kk) {
+  const int m = J >> 1;
+  return 2 * m * H - m * (m - 1) + ((J & 1) ? H - m : 0) + kk - m;
+}
+
+template <typename In, int NT, bool VEC>
+__global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
+  using O = BwdLds<In, NT>;
+  constexpr int Q = O::Q, NTT = O::NTT, H = O::H, XP = O::XP, BP = O::BP, NS = O::NS, NK = NT / 32;
+  constexpr int TPN = 8 / NS, TT = NTT / TPN;       // token parts of the strips, tiles per part
+  constexpr int SLOTS = (O::NTILE + 7) / 8;         // Gram tiles per wave
+  constexpr int PL = Q / 64;                        // tokens per lane of wave 0
+  extern __shared__ __align__(16) char lds[];
+  In* bs = reinterpret_cast<In*>(lds + O::bs);
+  In* cm = reinterpret_cast<In*>(lds + O::cm);
+  In* xs = reinterpret_cast<In*>(lds + O::xs);
+  In* ys = reinterpret_cast<In*>(lds + O::ys);
+  In* lm = reinterpret_cast<In*>(lds + O::lm);
+  In* mf = reinterpret_cast<In*>(lds + O::mf);
+  float* rp = reinterpret_cast<float*>(lds + O::rp);
+  float* cp = reinterpret_cast<float*>(lds + O::cp);
+  float* yp = reinterpret_cast<float*>(lds + O::yp);
+  float* up = reinterpret_cast<float*>(lds + O::up);
+  float* cs = reinterpret_cast<float*>(lds + O::cs);
+  float* ec = reinterpret_cast<float*>(lds + O::ec);
+  float* ww = reinterpret_cast<float*>(lds + O::ww);
+  float* wd = reinterpret_cast<float*>(lds + O::wd);
+  float* th = reinterpret_cast<float*>(lds + O::th);
+  float* ddp = reinterpret_cast<float*>(lds + O::dd);
+
+  const HeadsArgs& a = ba.h;
+  int64_t id = blockIdx.x;
+  const int64_t blk = id % ba.nblk;
+  id /= ba.nblk;
+  const int hb = (int)(id % ba.nhb);
+  id /= ba.nhb;
+  const int grp = (int)(id % ba.groups);
+  const int64_t b = id / ba.groups;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int ns = wv % NS, tp = wv / NS;
+  const int64_t t0 = blk * Q;
+  const int rows = (int)(a.L - t0 < Q ? a.L - t0 : Q);
+  const int64_t hp = (int64_t)a.heads * a.headdim;
+  const int hd0 = grp * a.hpg + hb * ba.hpb;
+  const int hd1 = hb * ba.hpb + ba.hpb < a.hpg ? hd0 + ba.hpb : (grp + 1) * a.hpg;
+
+  {
+    TileRegs<In, Q, NT, 512, VEC> br, cr;
+    br.load(static_cast<const In*>(a.Bm) + b * a.b_batch + t0 * a.b_token + (int64_t)grp * a.dstate, a.b_token, rows,
+            a.dstate);
+    cr.load(static_cast<const In*>(a.Cm) + b * a.c_batch + t0 * a.c_token + (int64_t)grp * a.dstate, a.c_token, rows,
+            a.dstate);
+    br.store(bs, BP);
+    cr.store(cm, BP);
+  }
+  for (int i = threadIdx.x; i < O::NFRAG * 512; i += 512) mf[i] = In(0);  // halves above the diagonal stay 0
+
+  TileRegs<In, Q, kTP, 512, VEC> xr, yr;
+  float draw[PL];
+  auto issue = [&](int hd, int pt) {
+    const bool on = hd < hd1;
+    const int cols = a.headdim - pt * kTP;
+    const int64_t col = (int64_t)hd * a.headdim + pt * kTP;
+    xr.load(static_cast<const In*>(a.x) + b * a.x_batch + t0 * a.x_token + col, a.x_token, on ? rows : 0,
+            cols < kTP ? cols : kTP);
+    yr.load(static_cast<const In*>(a.dy) + (b * a.L + t0) * hp + col, hp, on ? rows : 0, cols < kTP ? cols : kTP);
+    if (a.delta && wv == 0 && on) {
+#pragma unroll
+      for (int k = 0; k < PL; ++k)
+        if (k * 64 + lane < rows)
+          draw[k] = to_f32(static_cast<const In*>(a.delta)[b * a.d_batch + (t0 + k * 64 + lane) * a.d_token + hd]);
+    }
+  };
+  issue(hd0, 0);
+  __syncthreads();
+
+  // Gram tiles of this wave (rows t of tile I, columns s of tile J <= I)
+  int tI[SLOTS], tJ[SLOTS];
+  f32x4 CB[SLOTS], P[SLOTS];
+#pragma unroll
+  for (int k = 0; k < SLOTS; ++k) {
+    const int n = 8 * k + wv;
+    int I = 0;
+#pragma unroll
+    for (int i = 1; i < NTT; ++i) I += n >= i * (i + 1) / 2 ? 1 : 0;
+    tI[k] = I;
+    tJ[k] = n - I * (I + 1) / 2;
+    CB[k] = P[k] = f32x4{0, 0, 0, 0};
+    if (n < O::NTILE) {
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk)
+        CB[k] = mma(row_frag(cm, BP, 16 * I + c, kk, g), row_frag(bs, BP, 16 * tJ[k] + c, kk, g), CB[k]);
+    }
+  }
+  f32x4 dC[TT], dB[TT];
+#pragma unroll
+  for (int i = 0; i < TT; ++i) dC[i] = dB[i] = f32x4{0, 0, 0, 0};
+
+  float acc_g[PL], acc_ds[PL], acc_d = 0.0f;  // wave 0: sums over the channel tiles of a head
+#pragma unroll
+  for (int k = 0; k < PL; ++k) acc_g[k] = acc_ds[k] = 0.0f;
+
+  for (int hd = hd0; hd < hd1; ++hd) {
+    const float bias = a.dbias ? a.dbias[hd] : 0.0f;
+    const float Ah = a.A[hd], a2 = Ah * kLog2e;
+    const float dsk = a.D ? a.D[hd] : 0.0f;
+    for (int pt = 0; pt < a.ptiles; ++pt) {
+      const bool last_pt = pt + 1 == a.ptiles;
+      const int p0 = pt * kTP, pleft = a.headdim - p0;
+      xr.store(xs, XP);
+      yr.store(ys, XP);
+      float sv[PL], vd[PL];  // wave 0: the tokens' steps and their derivatives
+      if (wv == 0) {
+        float base = 0.0f, cl[PL];
+#pragma unroll
+        for (int k = 0; k < PL; ++k) {
+          const bool on = k * 64 + lane < rows;
+          const float v = (on && a.delta ? draw[k] : 0.0f) + bias;
+          sv[k] = on ? step_of(a, draw[k], bias) : 0.0f;
+          vd[k] = a.softplus ? fast_rcp(1.0f + fast_exp2(-v * kLog2e)) : 1.0f;
+          cl[k] = base + wave_scan(on ? clamp_log2(sv[k] * a2) : 0.0f);
+          base = last_lane(cl[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < PL; ++k) {
+          const int t = k * 64 + lane;
+          cs[t] = cl[k];
+          ec[t] = fast_exp2(cl[k]);
+          ww[t] = t < rows ? (a.unit ? 1.0f : sv[k]) : 0.0f;
+          wd[t] = fast_exp2(base - cl[k]);
+        }
+      }
+      // states entering the block: this wave's strip of n, all 64 channels
+      Pair<In> Sf[2], Lf[2];
+      {
+        const int64_t row = ((b * a.heads + hd) * (int64_t)a.ptiles + pt);
+        constexpr int64_t kTile = (int64_t)kTP * NT * (sizeof(In) == 2 ? 2 : 1);
+        const In* sp = static_cast<const In*>(a.planes) + (blk * ba.rows + row) * kTile;
+        const In* lp = sp + ba.nblk * ba.rows * kTile;
+#pragma unroll
+        for (int pp = 0; pp < 2; ++pp) {
+          const int64_t at = ((ns * 2 + pp) * 64) * 8;
+          Sf[pp].hi = lane_frag(sp + at, lane);
+          Lf[pp].hi = lane_frag(lp + at, lane);
+          if constexpr (sizeof(In) == 2) {
+            Sf[pp].lo = lane_frag(sp + kTP * NT + at, lane);
+            Lf[pp].lo = lane_frag(lp + kTP * NT + at, lane);
+          }
+        }
+      }
+      __syncthreads();
+      issue(last_pt ? hd + 1 : hd, last_pt ? 0 : pt + 1);
+
+      // inside the block
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k) {
+        const int n = 8 * k + wv;
+        if (n < O::NTILE) {
+          const int I = tI[k], J = tJ[k];
+          f32x4 X = {0, 0, 0, 0};
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+            X = mma(row_frag(ys, XP, 16 * I + c, kk, g), row_frag(xs, XP, 16 * J + c, kk, g), X);
+          const float4 ct4 = *reinterpret_cast<const float4*>(cs + 16 * I + 4 * g);
+          const float ct[4] = {ct4.x, ct4.y, ct4.z, ct4.w};
+          const float cj = cs[16 * J + c], wj = ww[16 * J + c];
+          float m[4], er[4], col = 0.0f, diag = 0.0f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const bool on = I != J || 4 * g + r >= c;
+            const float l = fast_exp2(ct[r] - cj);
+            const float m0 = on ? CB[k][r] * l : 0.0f;
+            const float e0 = on ? m0 * X[r] : 0.0f;
+            m[r] = m0 * wj;
+            er[r] = e0 * wj;
+            col += e0;
+            P[k][r] += on ? X[r] * (l * wj) : 0.0f;
+            if (I == J && 4 * g + r == c) diag = X[r];
+          }
+          store_vec<In, 4>(mf + frag_at<H>(J, I >> 1) * 512 + lane * 8 + 4 * (I & 1), m);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) er[r] = row_sum(er[r]);
+          if (c == 0) store_vec<float, 4>(rp + n * 16 + 4 * g, er);
+          col = half_sum(pair_row_sum(col));
+          if (g == 0) cp[n * 16 + c] = col;
+          if (I == J && ba.want_d) {
+            diag = wave_sum(diag);
+            if (lane == 0) ddp[I] = diag;
+          }
+        }
+      }
+      if (tp == 0) {
+#pragma unroll
+        for (int pp = 0; pp < 2; ++pp) {  // L by rows n: the operand's order is the tile row's order
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = frag_f32(Lf[pp].hi, e);
+          store_vec<In, 8>(lm + (16 * ns + c) * XP + 32 * pp + 8 * g, f);
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float sf = frag_f32(Sf[pp].hi, e), lf = frag_f32(Lf[pp].hi, e);
+            if constexpr (sizeof(In) == 2) { sf += frag_f32(Sf[pp].lo, e); lf += frag_f32(Lf[pp].lo, e); }
+            s = __builtin_fmaf(sf, lf, s);
+          }
+        s = wave_sum(s);
+        if (lane == 0) th[ns] = s;
+      }
+      __syncthreads();
+
+      // from before and to after the block
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        const int t = 16 * (tp * TT + i) + c;
+        f32x4 U = {0, 0, 0, 0}, V = {0, 0, 0, 0};
+#pragma unroll
+        for (int pp = 0; pp < 2; ++pp) {
+          U = mma_pair(Sf[pp], row_frag(ys, XP, t, pp, g), U);
+          V = mma_pair(Lf[pp], row_frag(xs, XP, t, pp, g), V);
+        }
+        float cv[4], bv[4], sy = 0.0f, su = 0.0f;
+        row_four(cm, BP, t, 4 * ns + g, cv);
+        row_four(bs, BP, t, 4 * ns + g, bv);
+        const float e = ec[t], f = wd[t], fw = ww[t] * f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sy = __builtin_fmaf(cv[r], U[r], sy);
+          su = __builtin_fmaf(bv[r], V[r], su);
+          dC[i][r] = __builtin_fmaf(e, U[r], dC[i][r]);
+          dB[i][r] = __builtin_fmaf(fw, V[r], dB[i][r]);
+        }
+        sy = half_sum(pair_row_sum(sy));
+        su = half_sum(pair_row_sum(su));
+        if (g == 0) {
+          yp[ns * Q + t] = e * sy;
+          up[ns * Q + t] = f * su;
+        }
+      }
+
+      // dx, transposed: channels of tile q, tokens of tiles J
+      {
+        const int q = wv & 3;
+        Frag<In> lq[NK], yq[H];
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) lq[kk] = col_frag(lm, XP, q, kk, g, c);
+#pragma unroll
+        for (int kk = 0; kk < H; ++kk) yq[kk] = col_frag(ys, XP, q, kk, g, c);
+        const int p = 16 * q + 4 * g;
+#pragma unroll
+        for (int i = 0; i < NTT / 2; ++i) {
+          const int J = 2 * i + (wv >> 2), s = 16 * J + c;
+          f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+          for (int kk = 0; kk < NK; ++kk) acc = mma(lq[kk], row_frag(bs, BP, s, kk, g), acc);
+          acc *= ww[s] * wd[s];
+#pragma unroll
+          for (int kk = i; kk < H; ++kk) acc = mma(yq[kk], lane_frag(mf + frag_at<H>(J, kk) * 512, lane), acc);
+          float dyv[4], o[4];
+          row_four(ys, XP, s, 4 * q + g, dyv);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(dsk, dyv[r], acc[r]);
+          if (s < rows) {
+            In* dp = static_cast<In*>(ba.dx) + (b * a.L + t0 + s) * hp + (int64_t)hd * a.headdim + p0 + p;
+            if constexpr (VEC) {
+              if (p < pleft) store_vec<In, 4>(dp, o);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (p + r < pleft) dp[r] = from_f32<In>(o[r]);
+            }
+          }
+        }
+      }
+      __syncthreads();
+
+      // wave 0: the decay's and the step's gradients; the others go on to
+      // stage the next tile (nothing that is read here is written before the
+      // next barrier but by wave 0 itself)
+      if (wv == 0) {
+        float R[PL], K[PL], Yi[PL], Ui[PL];
+#pragma unroll
+        for (int k = 0; k < PL; ++k) {
+          const int t = k * 64 + lane, I = t >> 4, e = t & 15;
+          R[k] = K[k] = Yi[k] = Ui[k] = 0.0f;
+#pragma unroll
+          for (int J = 0; J < NTT; ++J) {
+            if (J <= I) R[k] += rp[(I * (I + 1) / 2 + J) * 16 + e];
+            if (J >= I) K[k] += cp[(J * (J + 1) / 2 + I) * 16 + e];
+          }
+#pragma unroll
+          for (int n = 0; n < NS; ++n) { Yi[k] += yp[n * Q + t]; Ui[k] += up[n * Q + t]; }
+        }
+        float through = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) through += th[n];
+        through *= ec[Q - 1];
+        float in0 = 0.0f, y0 = 0.0f, u0 = 0.0f;  // running totals of the 64-token halves
+        float in[PL], ysum[PL], usum[PL];
+#pragma unroll
+        for (int k = 0; k < PL; ++k) {
+          const float w = ww[k * 64 + lane];
+          const float di = w * K[k] - R[k], du = w * Ui[k];
+          const float si = wave_scan(di), sy = wave_scan(Yi[k]), su = wave_scan(du);
+          in[k] = in0 + (si - di);        // exclusive
+          usum[k] = u0 + (su - du);       // exclusive
+          ysum[k] = y0 + (sy - Yi[k]);    // exclusive; the suffix is the total less this
+          in0 += last_lane(si); u0 += last_lane(su); y0 += last_lane(sy);
+        }
+#pragma unroll
+        for (int k = 0; k < PL; ++k) {
+          const float G = (in[k] + usum[k]) + ((y0 - ysum[k]) + through);
+          acc_g[k] += G;
+          acc_ds[k] = __builtin_fmaf(Ah, G, acc_ds[k]) + (a.unit ? 0.0f : K[k] + Ui[k]);
+        }
+        if (ba.want_d) {
+#pragma unroll
+          for (int I = 0; I < NTT; ++I) acc_d += ddp[I];
+        }
+        if (last_pt) {
+          float sa = 0.0f, sb = 0.0f;
+#pragma unroll
+          for (int k = 0; k < PL; ++k) {
+            const int t = k * 64 + lane;
+            const float dv = acc_ds[k] * vd[k];
+            if (t < rows) {
+              sa = __builtin_fmaf(sv[k], acc_g[k], sa);
+              sb += dv;
+              if (ba.ddelta)
+                static_cast<In*>(ba.ddelta)[(b * a.L + t0 + t) * a.heads + hd] = from_f32<In>(dv);
+            }
+            acc_g[k] = acc_ds[k] = 0.0f;
+          }
+          sa = wave_sum(sa);
+          sb = wave_sum(sb);
+          if (lane == 0) {
+            const int64_t n = a.batch * ba.nblk, at = (b * ba.nblk + blk) * a.heads + hd;
+            ba.parts[at] = sa;
+            ba.parts[n * a.heads + at] = acc_d;
+            ba.parts[2 * n * a.heads + at] = sb;
+          }
+          acc_d = 0.0f;
+        }
+      }
+    }
+  }
+
+  // dC += P B and dB += P^T C with P summed over the heads (x and dy are done:
+  // every wave is past the last barrier), P rounded to the input type
+  {
+    constexpr int PP = Q + kPad;
+    In* pm = xs;
+    static_assert(Q * PP <= 2 * Q * XP, "P fits x and dy");
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+      if (8 * k + wv < O::NTILE) {
+        const int at = chunk_at(4 * tJ[k] + (c >> 2)) + (c & 3);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pm[(16 * tI[k] + 4 * g + r) * PP + at] = from_f32<In>(P[k][r]);
+      }
+    }
+    if (wv < H) {  // the tile right of an even diagonal tile shares an operand with it
+      const int at = chunk_at(4 * (2 * wv + 1) + (c >> 2)) + (c & 3);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) pm[(32 * wv + 4 * g + r) * PP + at] = In(0);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const int it = tp * TT + i;
+      for (int kk = 0; kk <= it / 2; ++kk)
+        dC[i] = mma(col_frag(bs, BP, ns, kk, g, c), row_frag(pm, PP, 16 * it + c, kk, g), dC[i]);
+      for (int kk = it / 2; kk < H; ++kk)
+        dB[i] = mma(col_frag(cm, BP, ns, kk, g, c), col_frag(pm, PP, it, kk, g, c), dB[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const int t = 16 * (tp * TT + i) + c, n = 16 * ns + 4 * g;
+      if (t < rows) {
+        const int64_t tok = b * a.L + t0 + t;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float f[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) f[r] = m ? dC[i][r] : dB[i][r];
+          if (ba.bc) {
+            store_vec<float, 4>(ba.bc + (((int64_t)(hb * 2 + m) * a.batch * a.L + tok) * ba.groups + grp) * NT + n, f);
+          } else {
+            In* o = static_cast<In*>(m ? ba.dC : ba.dB) + (tok * ba.groups + grp) * a.dstate + n;
+            if constexpr (VEC) {
+              if (n < a.dstate) store_vec<In, 4>(o, f);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (n + r < a.dstate) o[r] = from_f32<In>(f[r]);
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+// dB, dC: the head runs' parts added in order, four states per thread.
+template <typename In>
+__global__ __launch_bounds__(256) void s6_heads_sum_bc(const float* bc, In* dB, In* dC, int64_t rows, int NT, int N,
+                                                       int nhb) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = NT / 4;
+  const int64_t row = i / per;
+  const int n = (int)(i % per) * 4;
+  if (row >= rows || n >= N) return;
+  const int m = blockIdx.y;
+  float s[4] = {0, 0, 0, 0};
+  for (int h = 0; h < nhb; ++h) {
+    float v[4];
+    load_vec<float, 4>(bc + ((int64_t)(h * 2 + m) * rows + row) * NT + n, v);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r] += v[r];
+  }
+  In* o = (m ? dC : dB) + row * N + n;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (n + r < N) o[r] = from_f32<In>(s[r]);
+}
+
+// dA, dD, dbias: the blocks' parts of one head added in a fixed order.
+__global__ __launch_bounds__(256) void s6_heads_sum_parts(const float* parts, float* dA, float* dD, float* dbias,
+                                                          int64_t n, int heads) {
+  __shared__ float buf[4];
+  const int hd = blockIdx.x, m = blockIdx.y;
+  float* o = m == 0 ? dA : m == 1 ? dD : dbias;
+  if (!o) return;
+  float s = 0.0f;
+  for (int64_t i = threadIdx.x; i < n; i += 256) s += parts[((int64_t)m * n + i) * heads + hd];
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) o[hd] = (buf[0] + buf[1]) + (buf[2] + buf[3]);
+}
+
+struct BwdWs {
+  int64_t nblk, nseg, seg_len;
+  int nhb, hpb;
+  size_t planes, agg, sd, hin, parts, bc, total;
+};
+
+// Head runs of a group: one workgroup fits a CU, so a launch takes
+// ceil(workgroups / CUs) rounds of a run's heads; the setup of a block and
+// the parts' sums weigh about one head more per run.
+void head_runs(int64_t blocks, int64_t hpg, int* nhb, int* hpb) {
+  const int64_t cus = cu_count();
+  double best = 0.0;
+  *nhb = 1;
+  *hpb = (int)hpg;
+  for (int64_t n = 1; n <= hpg && n <= 64; ++n) {
+    const int64_t per = (hpg + n - 1) / n, runs = (hpg + per - 1) / per;
+    const double cost = (double)((blocks * runs + cus - 1) / cus) * (double)(per + 1);
+    if (n == 1 || cost < best) {
+      best = cost;
+      *nhb = (int)runs;
+      *hpb = (int)per;
+    }
+  }
+}
+
+BwdWs bwd_ws(const s6_heads_dims& d, const HeadsPlan& p, int in_dtype) {
+  BwdWs o;
+  const int64_t q = in_dtype == S6_BF16 ? kBQ<uint16_t> : kBQ<float>;
+  o.nblk = (d.seqlen + q - 1) / q;
+  head_runs(d.batch * d.groups * o.nblk, d.heads / d.groups, &o.nhb, &o.hpb);
+  heads_segments(2 * p.rows, d.seqlen, q, &o.nseg, &o.seg_len);
+  const size_t tile = (size_t)p.rows * kTP * p.NT * sizeof(float);  // bf16: two planes of two bytes
+  o.planes = 0;
+  o.agg = up256(2 * (size_t)o.nblk * tile);
+  o.sd = o.agg + (o.nseg > 1 ? up256(2 * (size_t)o.nseg * tile) : 0);
+  o.hin = o.sd + (o.nseg > 1 ? up256(2 * (size_t)o.nseg * p.rows * sizeof(float)) : 0);
+  o.parts = o.hin + (o.nseg > 1 ? up256(2 * (size_t)o.nseg * tile) : 0);
+  o.bc = o.parts + up256(3 * (size_t)d.batch * o.nblk * d.heads * sizeof(float));
+  o.total = o.bc + (o.nhb > 1 ? up256((size_t)o.nhb * 2 * d.batch * d.seqlen * d.groups * p.NT * sizeof(float)) : 0);
+  return o;
+}
+
+template <typename In, int NT, bool VEC>
+int launch_bwd_v(const HeadsBwdArgs& a, hipStream_t st) {
+  const auto kern = s6_heads_bwd_kernel<In, NT, VEC>;
+  constexpr int lds = BwdLds<In, NT>::total;
+  if constexpr (lds > 65536)
+    S6_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds),
+           "s6_heads_bwd_kernel LDS size");
+  const int64_t n = a.nblk * a.nhb * a.groups * a.h.batch;
+  hipLaunchKernelGGL(kern, dim3((unsigned)n), dim3(512), lds, st, a);
+  S6_HIP(hipGetLastError(), "s6_heads_bwd_kernel launch");
+  return S6_OK;
+}
+template <typename In, int NT>
+int launch_bwd_n(const HeadsBwdArgs& a, bool vec, hipStream_t st) {
+  return vec ? launch_bwd_v<In, NT, true>(a, st) : launch_bwd_v<In, NT, false>(a, st);
+}
+template <typename In>
+int launch_bwd_in(const HeadsBwdArgs& a, const HeadsPlan& p, bool vec, hipStream_t st) {
+  if (p.NT == 32) return launch_bwd_n<In, 32>(a, vec, st);
+  if (p.NT == 64) return launch_bwd_n<In, 64>(a, vec, st);
+  return launch_bwd_n<In, 128>(a, vec, st);
+}
+
+template <typename In>
+int launch_sums(const HeadsBwdArgs& a, const HeadsPlan& p, float* dA, float* dD, float* dbias, hipStream_t st) {
+  if (a.bc) {
+    const int64_t rows = a.h.batch * a.h.L * a.groups, n = rows * (p.NT / 4);
+    hipLaunchKernelGGL((s6_heads_sum_bc<In>), dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, st, a.bc,
+                       static_cast<In*>(a.dB), static_cast<In*>(a.dC), rows, p.NT, a.h.dstate, a.nhb);
+    S6_HIP(hipGetLastError(), "s6_heads_sum_bc launch");
+  }
+  hipLaunchKernelGGL(s6_heads_sum_parts, dim3((unsigned)a.h.heads, 3), dim3(256), 0, st, a.parts, dA, dD, dbias,
+                     a.h.batch * a.nblk, a.h.heads);
+  S6_HIP(hipGetLastError(), "s6_heads_sum_parts launch");
+  return S6_OK;
+}
+
+}  // namespace
+
+}  // namespace s6i
+
+using namespace s6i;
+
+extern "C" {
+
+int s6_heads_scan_bwd_workspace_size(const s6_heads_dims* d, int in_dtype, size_t* bytes) {
+  if (!bytes) return S6_ERR_NULL;
+  const int rc = check_heads(d, in_dtype, 0, false, false, true);
+  if (rc) return rc;
+  *bytes = 0;
+  if (d->batch == 0 || d->heads == 0 || d->seqlen == 0) return S6_OK;
+  *bytes = bwd_ws(*d, heads_plan(*d, in_dtype, nullptr, nullptr, nullptr, nullptr), in_dtype).total;
+  return S6_OK;
+}
+
+int s6_heads_scan_bwd(const s6_heads_dims* d, int in_dtype, int flags, const void* x, const void* delta,
+                      const float* delta_bias, const float* A, const void* Bm, const void* Cm, const float* D,
+                      const float* h0, const void* dy, const float* dh_last, void* dx, void* ddelta, float* dA,
+                      void* dBm, void* dCm, float* dD, float* dh0, float* ddelta_bias, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int rc = check_heads(d, in_dtype, flags, delta != nullptr, delta_bias != nullptr, true);
+  if (rc) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const int64_t len = d->batch * d->seqlen;
+  const size_t esz = in_dtype == S6_BF16 ? 2 : 4;
+  const bool work = len > 0 && d->heads > 0;
+  if (d->heads > 0 && !dA) return S6_ERR_NULL;
+  if (work && (!x || !A || !Bm || !Cm || !dy || !dx || !dBm || !dCm || (delta && !ddelta))) return S6_ERR_NULL;
+  const void* ins[] = {x, delta, Bm, Cm, dy, dx, ddelta, dBm, dCm};
+  for (const void* p : ins)
+    if (!aligned(p, esz)) return S6_ERR_ALIGN;
+  const void* f32s[] = {delta_bias, A, D, h0, dh_last, dA, dD, dh0, ddelta_bias};
+  for (const void* p : f32s)
+    if (!aligned(p, 4)) return S6_ERR_ALIGN;
+  if (!work) {  // empty sums
+    fill(dA, 0.0f, d->heads, st);
+    fill(dD, 0.0f, d->heads, st);
+    fill(ddelta_bias, 0.0f, d->heads, st);
+    S6_HIP(hipGetLastError(), "fill launch");
+    return dh0 ? launch_copy_state(dh_last, dh0, d->batch * d->heads * d->headdim * d->dstate, st) : S6_OK;
+  }
+  const HeadsPlan p = heads_plan(*d, in_dtype, x, Bm, Cm, dy);
+  const BwdWs ws = bwd_ws(*d, p, in_dtype);
+  if (ws.nblk * ws.nhb * d->groups * d->batch > INT32_MAX) return S6_ERR_SHAPE;
+  if (!workspace || workspace_bytes < ws.total) return S6_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return S6_ERR_ALIGN;
+  char* w = static_cast<char*>(workspace);
+  HeadsBwdArgs ba;
+  memset(&ba, 0, sizeof(ba));
+  ba.h = heads_args(*d, p, flags, x, delta, delta_bias, A, Bm, Cm, D, h0);
+  HeadsArgs& a = ba.h;
+  a.dy = dy; a.dh_last = dh_last; a.dh0 = dh0;
+  a.nseg = ws.nseg; a.seg_len = ws.seg_len;
+  if (ws.nseg > 1) {
+    a.agg = reinterpret_cast<float*>(w + ws.agg);
+    a.sd = reinterpret_cast<float*>(w + ws.sd);
+    rc = launch_heads_state(in_dtype, a, p, 0, 2, st);
+    a.hin = reinterpret_cast<float*>(w + ws.hin);
+    if (rc == S6_OK) rc = launch_heads_fold(a, p, 2, st);
+    if (rc) return rc;
+  }
+  a.planes = w + ws.planes;
+  rc = launch_heads_state(in_dtype, a, p, 1, 2, st);
+  if (rc) return rc;
+  ba.dx = dx; ba.ddelta = ddelta; ba.dB = dBm; ba.dC = dCm;
+  ba.parts = reinterpret_cast<float*>(w + ws.parts);
+  ba.bc = ws.nhb > 1 ? reinterpret_cast<float*>(w + ws.bc) : nullptr;
+  ba.nblk = ws.nblk; ba.rows = p.rows; ba.groups = (int)d->groups; ba.nhb = ws.nhb; ba.hpb = ws.hpb;
+  ba.want_d = dD != nullptr; ba.want_bias = ddelta_bias != nullptr;
+  // dx, dB and dC are stored four values at a time
+  const bool vec = p.vec && aligned(dx, 4 * esz) && aligned(dBm, 4 * esz) && aligned(dCm, 4 * esz);
+  rc = in_dtype == S6_BF16 ? launch_bwd_in<uint16_t>(ba, p, vec, st) : launch_bwd_in<float>(ba, p, vec, st);
+  if (rc) return rc;
+  return in_dtype == S6_BF16 ? launch_sums<uint16_t>(ba, p, dA, dD, ddelta_bias, st)
+                             : launch_sums<float>(ba, p, dA, dD, ddelta_bias, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,371 @@
+// heads_fwd.hip -- the multi-head scan over whole sequences
+// (s6_heads_scan_fwd) and the launch plan shared by the heads entry points.
+//
+// In chunks of Q = 64 tokens, c the running sum of the log decays s A in the
+// chunk:
+//   y_t = sum_{s<=t} (C_t . B_s) e^{c_t - c_s} w_s x_s + e^{c_t} S C_t + D x_t
+//   S  <- e^{c_Q} S + sum_s (w_s e^{c_Q - c_s} x_s) B_s^T
+// so each chunk is four matrix products: the Gram matrix C B^T (its lower
+// half), its decayed form times x, the entering state times C, and the chunk's
+// own part of the state.  x is read and y written once; the state never
+// leaves the registers.
+//
+// A workgroup of four waves owns one row (64 channels of one head of one
+// sequence) and walks it; wave w owns channels 16 w .. 16 w + 15 of the
+// output and of the state (NT x 16 in registers, rows n).  Results are made
+// transposed (channels x tokens), so that a lane stores four channels of one
+// token, the decay of its token is one scalar per lane, and the state's
+// registers are the operand of the product with C as they are.  The decayed
+// Gram tiles are shared out among the waves and meet in LDS in operand order.
+#include "heads_kernel.h"
+
+namespace s6i {
+
+namespace {
+
+template <typename In, int NT, bool VEC>
+__global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
+  constexpr int kXP = kTP + kPad, kBP = NT + kPad;
+  constexpr int NQ = NT / 16, NK = NT / 32;
+  extern __shared__ __align__(16) char lds[];
+  In* xs = reinterpret_cast<In*>(lds);
+  In* bs = xs + kHQ * kXP;
+  In* cm = bs + kHQ * kBP;
+  In* pf = cm + kHQ * kBP;                                // [4 t tiles][2][lane][8]
+  float* cs = reinterpret_cast<float*>(pf + 4 * 2 * 512);  // running log2 decay
+  float* ec = cs + kHQ;                                   // its exponential
+  float* ww = ec + kHQ;                                   // input weight
+  float* wd = ww + kHQ;                                   // weight decayed to the chunk's end
+  int* bad = reinterpret_cast<int*>(wd + kHQ);            // first token whose input is not finite
+  int* any = bad + kTP;
+  // consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of
+  // rows, whose B and C come through one L2
+  const int64_t nrows = gridDim.x;
+  const int64_t rid = nrows % 8 == 0 ? (blockIdx.x % 8) * (nrows / 8) + blockIdx.x / 8 : blockIdx.x;
+  const HeadRow hr = head_row(a, rid);
+  const int64_t seg = blockIdx.y;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int p0 = hr.pt * kTP, pleft = a.headdim - p0;
+  const int64_t t_lo = seg * a.seg_len;
+  const int64_t t_hi = t_lo + a.seg_len < a.L ? t_lo + a.seg_len : a.L;
+  const int64_t hp = (int64_t)a.heads * a.headdim;
+  const In* X = static_cast<const In*>(a.x) + hr.b * a.x_batch + (int64_t)hr.hd * a.headdim + p0;
+  const In* B = static_cast<const In*>(a.Bm) + hr.b * a.b_batch + (int64_t)hr.grp * a.dstate;
+  const In* C = static_cast<const In*>(a.Cm) + hr.b * a.c_batch + (int64_t)hr.grp * a.dstate;
+  const In* dl = a.delta ? static_cast<const In*>(a.delta) + hr.b * a.d_batch + hr.hd : nullptr;
+  In* Y = static_cast<In*>(a.y) + hr.b * a.L * hp + (int64_t)hr.hd * a.headdim + p0;
+  const float bias = a.dbias ? a.dbias[hr.hd] : 0.0f;
+  const float a2 = a.A[hr.hd] * kLog2e;
+  const float dsk = a.D ? a.D[hr.hd] : 0.0f;
+
+  if (threadIdx.x < kTP) bad[threadIdx.x] = kHQ;
+  if (threadIdx.x == 0) *any = 0;
+  for (int i = threadIdx.x; i < 4 * 2 * 512; i += 256) pf[i] = In(0);  // tiles above the diagonal stay 0
+
+  // state tiles: rows n = 16 q + 4 g + r, column p = 16 wv + c
+  f32x4 S[NQ];
+  const int64_t srow = (hr.b * a.heads + hr.hd) * (int64_t)a.headdim + p0;
+  const int ps = 16 * wv + c;
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    S[q] = f32x4{0, 0, 0, 0};
+    const int n = 16 * q + 4 * g;
+    if (a.hin) {
+      float v[4];
+      load_vec<float, 4>(a.hin + (seg * nrows + hr.row) * (int64_t)(kTP * NT) + ps * NT + n, v);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[q][r] = v[r];
+    } else if (a.h0 && ps < pleft) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < a.dstate) S[q][r] = a.h0[(srow + ps) * a.dstate + n + r];
+    }
+  }
+
+  TileRegs<In, kHQ, kTP, 256, VEC> xr;
+  TileRegs<In, kHQ, NT, 256, VEC> br, cr;
+  float draw = 0.0f;
+  auto issue = [&](int64_t t0) {
+    const int rows = t0 >= t_hi ? 0 : (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ);
+    xr.load(X + t0 * a.x_token, a.x_token, rows, pleft < kTP ? pleft : kTP);
+    br.load(B + t0 * a.b_token, a.b_token, rows, a.dstate);
+    cr.load(C + t0 * a.c_token, a.c_token, rows, a.dstate);
+    if (dl && (int)threadIdx.x < rows) draw = to_f32(dl[(t0 + threadIdx.x) * a.d_token]);
+  };
+  issue(t_lo);
+  __syncthreads();
+  for (int64_t t0 = t_lo; t0 < t_hi; t0 += kHQ) {
+    const int rows = (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ);
+    // An input that is not finite would reach earlier tokens through the
+    // zeros of the Gram matrix (0 x inf): it is taken out here and its channel
+    // set to NaN from its token on.
+    xr.clean(bad, any);
+    xr.store(xs, kXP);
+    br.store(bs, kBP);
+    cr.store(cm, kBP);
+    if (wv == 0) {
+      const bool on = lane < rows;
+      const float s = on ? step_of(a, draw, bias) : 0.0f;
+      const float v = wave_scan(on ? clamp_log2(s * a2) : 0.0f);
+      const float w = on ? (a.unit ? 1.0f : s) : 0.0f;
+      cs[lane] = v;
+      ec[lane] = fast_exp2(v);
+      ww[lane] = w;
+      wd[lane] = w * fast_exp2(last_lane(v) - v);
+    }
+    __syncthreads();
+    issue(t0 + kHQ);
+
+    // decayed Gram tiles (rows s of tile J, columns t of tile I), J <= I
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int id = 4 * k + wv;
+      if (id < 10) {
+        const int I = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0;
+        const int J = id - I * (I + 1) / 2;
+        f32x4 G = {0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk)
+          G = mma(row_frag(bs, kBP, 16 * J + c, kk, g), row_frag(cm, kBP, 16 * I + c, kk, g), G);
+        const float ct = cs[16 * I + c];
+        const float4 cv = *reinterpret_cast<const float4*>(cs + 16 * J + 4 * g);
+        const float4 wv4 = *reinterpret_cast<const float4*>(ww + 16 * J + 4 * g);
+        const float cj[4] = {cv.x, cv.y, cv.z, cv.w}, wj[4] = {wv4.x, wv4.y, wv4.z, wv4.w};
+        float p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          p[r] = I != J || c >= 4 * g + r ? G[r] * (fast_exp2(ct - cj[r]) * wj[r]) : 0.0f;
+        store_vec<In, 4>(pf + ((I * 2 + (J >> 1)) * 64 + lane) * 8 + 4 * (J & 1), p);
+      }
+    }
+    __syncthreads();
+
+    Frag<In> xf[2];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) xf[kk] = col_frag(xs, kXP, wv, kk, g, c);
+    {
+      Frag<In> sf[NK];
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = S[2 * kk + (e >> 2)][e & 3];
+        to_frag(f, sf[kk]);  // bf16: y is rounded to bf16 anyway
+      }
+      const bool dirty = *any != 0;
+#pragma unroll
+      for (int I = 0; I < 4; ++I) {
+        f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) acc = mma(sf[kk], row_frag(cm, kBP, 16 * I + c, kk, g), acc);
+        const int t = 16 * I + c;
+        acc *= ec[t];
+#pragma unroll
+        for (int kk = 0; kk <= I / 2; ++kk) acc = mma(xf[kk], lane_frag(pf + (I * 2 + kk) * 512, lane), acc);
+        float xv[4], o[4];
+        row_four(xs, kXP, t, 4 * wv + g, xv);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(dsk, xv[r], acc[r]);
+        const int p = 16 * wv + 4 * g;
+        if (dirty) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (t >= bad[p + r]) o[r] = __builtin_nanf("");
+        }
+        if (t < rows) {
+          In* yp = Y + (t0 + t) * hp + p;
+          if constexpr (VEC) {
+            if (p < pleft) store_vec<In, 4>(yp, o);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (p + r < pleft) yp[r] = from_f32<In>(o[r]);
+          }
+        }
+      }
+      if (dirty && bad[ps] < kHQ) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) S[q] = f32x4{1, 1, 1, 1} * __builtin_nanf("");
+      }
+    }
+
+    const float dec = ec[kHQ - 1];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) S[q] *= dec;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const float4 w0 = *reinterpret_cast<const float4*>(wd + 32 * kk + 4 * g);
+      const float4 w1 = *reinterpret_cast<const float4*>(wd + 32 * kk + 16 + 4 * g);
+      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = frag_f32(xf[kk], e) * w[e];
+      Pair<In> xd;
+      to_pair(f, xd);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) S[q] = mma_pair(col_frag(bs, kBP, q, kk, g, c), xd, S[q]);
+    }
+    __syncthreads();
+  }
+
+  if (a.h_last && seg == a.nseg - 1 && ps < pleft) {
+    float* o = a.h_last + (srow + ps) * a.dstate;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int n = 16 * q + 4 * g;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < a.dstate) o[n + r] = S[q][r];
+    }
+  }
+}
+
+template <typename In, int NT>
+constexpr int scan_lds() {
+  return (int)sizeof(In) * (kHQ * (kTP + kPad) + 2 * kHQ * (NT + kPad) + 4096) + 4 * (4 * kHQ + kTP + 4);
+}
+
+template <typename In, int NT, bool VEC>
+int launch_scan_v(const HeadsArgs& a, const HeadsPlan& p, hipStream_t st) {
+  const auto kern = s6_heads_scan_kernel<In, NT, VEC>;
+  constexpr int lds = scan_lds<In, NT>();
+  if constexpr (lds > 65536)
+    S6_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds),
+           "s6_heads_scan_kernel LDS size");
+  hipLaunchKernelGGL(kern, dim3((unsigned)p.rows, (unsigned)a.nseg), dim3(256), lds, st, a);
+  S6_HIP(hipGetLastError(), "s6_heads_scan_kernel launch");
+  return S6_OK;
+}
+template <typename In, int NT>
+int launch_scan_n(const HeadsArgs& a, const HeadsPlan& p, hipStream_t st) {
+  return p.vec ? launch_scan_v<In, NT, true>(a, p, st) : launch_scan_v<In, NT, false>(a, p, st);
+}
+template <typename In>
+int launch_scan_in(const HeadsArgs& a, const HeadsPlan& p, hipStream_t st) {
+  if (p.NT == 32) return launch_scan_n<In, 32>(a, p, st);
+  if (p.NT == 64) return launch_scan_n<In, 64>(a, p, st);
+  return launch_scan_n<In, 128>(a, p, st);
+}
+
+// Segment states of the forward in the workspace.
+struct FwdWs {
+  int64_t nseg, seg_len;
+  size_t agg, sd, hin, total;
+};
+FwdWs fwd_ws(const s6_heads_dims& d, const HeadsPlan& p) {
+  FwdWs o;
+  heads_segments(p.rows, d.seqlen, kHQ, &o.nseg, &o.seg_len);
+  o.agg = o.sd = o.hin = o.total = 0;
+  if (o.nseg > 1) {
+    const size_t tile = (size_t)p.rows * kTP * p.NT * sizeof(float);
+    o.sd = up256((size_t)o.nseg * tile);
+    o.hin = o.sd + up256((size_t)o.nseg * p.rows * sizeof(float));
+    o.total = o.hin + up256((size_t)o.nseg * tile);
+  }
+  return o;
+}
+
+}  // namespace
+
+HeadsPlan heads_plan(const s6_heads_dims& d, int in_dtype, const void* x, const void* Bm, const void* Cm,
+                     const void* dy) {
+  HeadsPlan p;
+  p.NT = d.dstate > 64 ? 128 : d.dstate > 32 ? 64 : 32;
+  p.ptiles = (d.headdim + kTP - 1) / kTP;
+  p.rows = d.batch * d.heads * p.ptiles;
+  const int64_t u = in_dtype == S6_BF16 ? 8 : 4;  // elements of 16 bytes
+  p.vec = d.headdim % 8 == 0 && d.dstate % 8 == 0 && d.x_batch % u == 0 && d.x_token % u == 0 && d.b_batch % u == 0 &&
+          d.b_token % u == 0 && d.c_batch % u == 0 && d.c_token % u == 0 && aligned(x, 16) && aligned(Bm, 16) &&
+          aligned(Cm, 16) && aligned(dy, 16);
+  return p;
+}
+
+HeadsArgs heads_args(const s6_heads_dims& d, const HeadsPlan& p, int flags, const void* x, const void* delta,
+                     const float* dbias, const float* A, const void* Bm, const void* Cm, const float* D,
+                     const float* h0) {
+  HeadsArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.delta = delta; a.dbias = dbias; a.A = A; a.Bm = Bm; a.Cm = Cm; a.D = D; a.h0 = h0;
+  a.softplus = (flags & S6_DELTA_SOFTPLUS) != 0;
+  a.unit = (flags & S6_UNIT_INPUT) != 0;
+  a.heads = (int)d.heads; a.headdim = (int)d.headdim; a.ptiles = (int)p.ptiles; a.hpg = (int)(d.heads / d.groups);
+  a.dstate = (int)d.dstate;
+  a.batch = d.batch; a.L = d.seqlen;
+  a.x_batch = d.x_batch; a.x_token = d.x_token; a.d_batch = d.delta_batch; a.d_token = d.delta_token;
+  a.b_batch = d.b_batch; a.b_token = d.b_token; a.c_batch = d.c_batch; a.c_token = d.c_token;
+  return a;
+}
+
+// Few rows leave CUs idle: with fewer rows than one workgroup per CU the
+// sequence is cut into segments, enough for two workgroups per CU, of at
+// least four chunks each.
+void heads_segments(int64_t rows, int64_t L, int64_t unit, int64_t* nseg, int64_t* seg_len) {
+  *nseg = 1;
+  *seg_len = L;
+  const int64_t cus = cu_count();
+  if (rows <= 0 || rows >= cus) return;
+  int64_t s = 2 * cus / rows;
+  const int64_t most = L / (4 * kHQ);
+  if (s > most) s = most;
+  if (s <= 1) return;
+  const int64_t len = ((L + s - 1) / s + unit - 1) / unit * unit;
+  *nseg = (L + len - 1) / len;
+  *seg_len = *nseg > 1 ? len : L;
+}
+
+}  // namespace s6i
+
+using namespace s6i;
+
+extern "C" {
+
+int s6_heads_scan_fwd_workspace_size(const s6_heads_dims* d, int in_dtype, size_t* bytes) {
+  if (!bytes) return S6_ERR_NULL;
+  const int rc = check_heads(d, in_dtype, 0, false, false, true);
+  if (rc) return rc;
+  *bytes = 0;
+  if (d->batch == 0 || d->heads == 0 || d->seqlen == 0) return S6_OK;
+  *bytes = fwd_ws(*d, heads_plan(*d, in_dtype, nullptr, nullptr, nullptr, nullptr)).total;
+  return S6_OK;
+}
+
+int s6_heads_scan_fwd(const s6_heads_dims* d, int in_dtype, int flags, const void* x, const void* delta,
+                      const float* delta_bias, const float* A, const void* Bm, const void* Cm, const float* D,
+                      const float* h0, void* y, float* h_last, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_heads(d, in_dtype, flags, delta != nullptr, delta_bias != nullptr, true);
+  if (rc) return rc;
+  if (d->batch == 0 || d->heads == 0) return S6_OK;
+  const size_t esz = in_dtype == S6_BF16 ? 2 : 4;
+  if (d->seqlen > 0 && (!x || !A || !Bm || !Cm || !y)) return S6_ERR_NULL;
+  const void* ins[] = {x, delta, Bm, Cm, y};
+  for (const void* p : ins)
+    if (!aligned(p, esz)) return S6_ERR_ALIGN;
+  const void* f32s[] = {delta_bias, A, D, h0, h_last};
+  for (const void* p : f32s)
+    if (!aligned(p, 4)) return S6_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (d->seqlen == 0)
+    return h_last ? launch_copy_state(h0, h_last, d->batch * d->heads * d->headdim * d->dstate, st) : S6_OK;
+  HeadsPlan p = heads_plan(*d, in_dtype, x, Bm, Cm, nullptr);
+  // y is stored four channels at a time
+  p.vec = p.vec && aligned(y, 4 * esz);
+  const FwdWs ws = fwd_ws(*d, p);
+  if (ws.total > 0) {
+    if (!workspace || workspace_bytes < ws.total) return S6_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return S6_ERR_ALIGN;
+  }
+  HeadsArgs a = heads_args(*d, p, flags, x, delta, delta_bias, A, Bm, Cm, D, h0);
+  a.y = y; a.h_last = h_last; a.nseg = ws.nseg; a.seg_len = ws.seg_len;
+  if (ws.nseg > 1) {
+    char* w = static_cast<char*>(workspace);
+    a.agg = reinterpret_cast<float*>(w + ws.agg);
+    a.sd = reinterpret_cast<float*>(w + ws.sd);
+    a.hin = reinterpret_cast<float*>(w + ws.hin);
+    rc = launch_heads_state(in_dtype, a, p, 0, 1, st);
+    if (rc == S6_OK) rc = launch_heads_fold(a, p, 1, st);
+    if (rc) return rc;
+  }
+  return in_dtype == S6_BF16 ? launch_scan_in<uint16_t>(a, p, st) : launch_scan_in<float>(a, p, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,203 @@
+"""The C ABI of the block operators without a GPU: libs6.so exports what
+include/s6_block.h declares, and its argument checks (before any HIP call)
+return the documented codes.  Every call here fails its checks or has no work
+that would be launched."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "s6_block.h")
+LIB = os.path.join(ROOT, "selective_state_space_63_amd", "libs6.so")
+
+OK, NULL, SHAPE, DTYPE, UNSUP, ALIGN, FLAGS, WS = 0, -1, -2, -3, -4, -5, -7, -8
+P = ctypes.c_void_p(1 << 20)          # aligned, never dereferenced
+ODD = ctypes.c_void_p((1 << 20) + 1)
+HALF = ctypes.c_void_p((1 << 20) + 2)  # aligned for bf16, not for fp32
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(LIB):
+        from selective_state_space_63_amd import build
+        build.build(LIB)
+    from selective_state_space_63_amd import block
+    return block._load()
+
+
+def declared():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    return sorted(set(re.findall(r"^int (s6_\w+)\(", text, flags=re.M)))
+
+
+def test_every_declared_symbol_is_exported_and_bound(lib):
+    out = subprocess.run(["nm", "-D", "--defined-only", LIB], capture_output=True, text=True, check=True).stdout
+    exported = {line.split()[-1] for line in out.splitlines() if " T " in line}
+    names = declared()
+    assert len(names) == 11 and not [n for n in names if n not in exported]
+    for n in names:
+        assert getattr(lib, n).argtypes is not None, n
+
+
+def test_header_compiles_as_c(tmp_path):
+    src = tmp_path / "t.c"
+    src.write_text('#include "s6_block.h"\nint main(void) { s6_heads_dims d = {0}; return (int)d.batch; }\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), "-c", "-o",
+                    str(tmp_path / "t.o"), str(src)], check=True)
+
+
+def dims(batch=2, seqlen=32, heads=4, headdim=16, groups=2, dstate=8, **kw):
+    from selective_state_space_63_amd.block import HeadsDims
+    d = HeadsDims(batch, seqlen, heads, headdim, groups, dstate, seqlen * heads * headdim, heads * headdim,
+                  seqlen * heads, heads, seqlen * groups * dstate, groups * dstate, seqlen * groups * dstate,
+                  groups * dstate)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def fwd(lib, d, dt=1, flags=0, x=P, delta=P, bias=None, A=P, B=P, C=P, D=None, h0=None, y=P, hl=None, ws=None, n=0):
+    return lib.s6_heads_scan_fwd(ctypes.byref(d) if d else None, dt, flags, x, delta, bias, A, B, C, D, h0, y, hl, ws, n,
+                                 None)
+
+
+def bwd(lib, d, dt=1, flags=0, x=P, delta=P, bias=None, dy=P, dx=P, dd=P, dA=P, dB=P, dC=P, h0=None, ws=None, n=0):
+    return lib.s6_heads_scan_bwd(ctypes.byref(d), dt, flags, x, delta, bias, P, P, P, None, h0, dy, None, dx, dd, dA, dB,
+                                 dC, None, None, None, ws, n, None)
+
+
+def step(lib, d, dt=1, flags=0, h=P, x=P, delta=P, bias=None, y=P):
+    return lib.s6_heads_state_update(ctypes.byref(d), dt, flags, h, x, delta, bias, P, P, P, None, y, None)
+
+
+@pytest.mark.parametrize("call", [fwd, bwd, step], ids=["fwd", "bwd", "step"])
+def test_heads_common_checks(lib, call):
+    """Sizes, types and flags, alike for the three entry points."""
+    assert call(lib, dims(), dt=2) == DTYPE
+    assert call(lib, dims(), flags=2) == FLAGS
+    assert call(lib, dims(), flags=8) == FLAGS
+    assert call(lib, dims(), flags=1, delta=None) == NULL      # softplus of nothing
+    assert call(lib, dims(), bias=P, delta=None) == NULL
+    assert call(lib, dims(batch=-1)) == SHAPE
+    assert call(lib, dims(heads=-4)) == SHAPE
+    assert call(lib, dims(headdim=0)) == SHAPE
+    assert call(lib, dims(groups=0)) == SHAPE
+    assert call(lib, dims(heads=5)) == SHAPE                    # groups do not divide the heads
+    assert call(lib, dims(dstate=0)) == UNSUP
+    assert call(lib, dims(dstate=129)) == UNSUP
+    assert call(lib, dims(batch=1 << 40, heads=1 << 20)) == SHAPE
+    assert call(lib, dims(headdim=1 << 40)) == SHAPE
+    assert call(lib, dims(x_batch=-1)) == SHAPE
+    assert call(lib, dims(x_batch=1 << 62)) == SHAPE
+    assert call(lib, dims(), x=None) == NULL
+    assert call(lib, dims(), x=ODD) == ALIGN
+    assert call(lib, dims(), dt=0, x=HALF) == ALIGN
+    assert call(lib, dims(batch=0)) == OK or call is bwd        # bwd would fill dA
+
+
+def test_heads_sequence_checks(lib):
+    for call in (fwd, bwd):
+        assert call(lib, dims(seqlen=-1)) == SHAPE
+        assert call(lib, dims(b_token=-2)) == SHAPE
+        assert call(lib, dims(c_token=1 << 60)) == SHAPE
+    assert fwd(lib, None) == NULL
+    for k in ("A", "B", "C", "y"):
+        assert fwd(lib, dims(), **{k: None}) == NULL, k
+    assert fwd(lib, dims(), h0=HALF) == ALIGN
+    assert fwd(lib, dims(), bias=HALF) == ALIGN
+    assert fwd(lib, dims(heads=0, groups=1)) == OK
+    for k in ("dy", "dx", "dd", "dA", "dB", "dC"):
+        assert bwd(lib, dims(), **{k: None}) == NULL, k
+    assert bwd(lib, dims(), dA=HALF) == ALIGN
+    assert bwd(lib, dims()) == WS
+    assert bwd(lib, dims(), ws=P, n=256) == WS
+    assert bwd(lib, dims(), ws=ctypes.c_void_p((1 << 20) + 64), n=1 << 40) == ALIGN
+    assert step(lib, dims(), h=None) == NULL
+    assert step(lib, dims(), h=HALF) == ALIGN
+    assert step(lib, dims(), y=None) == NULL
+
+
+def size(fn, *args):
+    out = ctypes.c_size_t(77)
+    return fn(*args, ctypes.byref(out)), out.value
+
+
+def test_heads_workspace(lib):
+    q = lib.s6_heads_scan_fwd_workspace_size
+    big = dims(batch=8, seqlen=2048, heads=80, headdim=64, groups=1, dstate=128)
+    assert size(q, ctypes.byref(big), 1) == (OK, 0)             # 640 rows fill 256 CUs
+    few = dims(batch=1, seqlen=8192, heads=4, headdim=64, groups=1, dstate=64)
+    rc, n = size(q, ctypes.byref(few), 1)
+    assert rc == OK and n > 0
+    assert fwd(lib, few) == WS
+    assert fwd(lib, few, ws=P, n=n - 1) == WS
+    assert fwd(lib, few, ws=ctypes.c_void_p((1 << 20) + 128), n=n) == ALIGN
+    assert size(q, ctypes.byref(dims(seqlen=0)), 1) == (OK, 0)
+    assert q(ctypes.byref(dims()), 1, None) == NULL
+    assert size(q, ctypes.byref(dims(dstate=200)), 1)[0] == UNSUP
+    q = lib.s6_heads_scan_bwd_workspace_size
+    rc, n = size(q, ctypes.byref(big), 1)
+    # the states entering every block of 128 tokens and their adjoints: 8 bytes each
+    assert rc == OK and n >= 16 * 640 * 64 * 128 * 8
+    assert size(q, ctypes.byref(dims()), 7)[0] == DTYPE
+
+
+def test_add_norm_checks(lib):
+    def f(rows=4, dim=16, dt=1, rt=0, x=P, st=16, r=P, w=P, g=None, out=P, ro=P):
+        return lib.s6_add_norm_fwd(rows, dim, dt, rt, x, st, r, w, g, 1.0, 1e-5, out, ro, None)
+
+    assert f(dt=3) == DTYPE and f(rt=3) == DTYPE and f(dt=0, rt=1) == DTYPE
+    assert f(rows=-1) == SHAPE and f(dim=0) == SHAPE and f(st=15) == SHAPE and f(rows=1 << 40, dim=1 << 30) == SHAPE
+    assert f(x=None) == NULL and f(w=None) == NULL and f(out=None) == NULL and f(ro=None) == NULL
+    assert f(x=ODD) == ALIGN and f(r=HALF) == ALIGN and f(g=HALF) == ALIGN
+    assert f(rows=0) == OK
+
+    def b(rows=4, dim=16, dt=1, rt=0, do=P, dr=None, res=P, x=P, st=16, w=P, g=None, dx=P, dres=P, dw=P, dg=None, ws=None,
+          n=0):
+        return lib.s6_add_norm_bwd(rows, dim, dt, rt, do, dr, res, x, st, w, g, 1.0, 1e-5, dx, dres, dw, dg, ws, n, None)
+
+    assert b(dt=3) == DTYPE and b(dim=0) == SHAPE and b(st=3) == SHAPE
+    assert b(do=None) == NULL and b(res=None) == NULL and b(dx=None, dres=None, dw=None) == NULL
+    assert b(g=P) == NULL and b(dg=P) == NULL and b(g=P, dg=P, x=None) == NULL
+    assert b(dres=HALF) == ALIGN
+    assert b() == WS and b(ws=P, n=255) == WS and b(ws=ctypes.c_void_p((1 << 20) + 16), n=1 << 20) == ALIGN
+    rc, n = size(lib.s6_add_norm_bwd_workspace_size, 4, 16)
+    assert rc == OK and n >= 2 * 4 * 16 * 4
+    assert size(lib.s6_add_norm_bwd_workspace_size, 0, 16) == (OK, 0)
+
+
+def test_gated_norm_checks(lib):
+    def f(rows=4, dim=16, g=2, dt=1, fl=0, y=P, ys=16, z=P, zs=16, w=P, out=P):
+        return lib.s6_gated_norm_fwd(rows, dim, g, dt, fl, y, ys, z, zs, w, 1e-5, out, None)
+
+    assert f(dt=-1) == DTYPE and f(g=3) == SHAPE and f(g=0) == SHAPE and f(zs=4) == SHAPE and f(fl=1) == FLAGS
+    assert f(y=None) == NULL and f(w=None) == NULL and f(out=None) == NULL
+    assert f(z=ODD) == ALIGN and f(w=HALF) == ALIGN
+    assert f(rows=0) == OK
+
+    def b(dz=P, dy=P, z=P, dw=P, ws=None, n=0, fl=0):
+        return lib.s6_gated_norm_bwd(4, 16, 2, 1, fl, P, P, 16, z, 16, P, 1e-5, dy, dz, dw, ws, n, None)
+
+    assert b(dz=None) == NULL and b(dy=None) == NULL and b(fl=4) == FLAGS and b(dy=ODD) == ALIGN
+    assert b() == WS and b(ws=P, n=16) == WS
+
+
+def test_binding_refuses(lib):
+    """Shapes, types, layouts and devices that the entry points do not take."""
+    torch = pytest.importorskip("torch")
+    from selective_state_space_63_amd import block
+    x, B = torch.zeros(1, 4, 2, 8), torch.zeros(1, 4, 1, 4)
+    A = torch.zeros(2)
+    with pytest.raises(ValueError, match="device"):
+        block.heads_scan_fwd(x, None, A, B, B)
+    with pytest.raises(ValueError, match="dtype"):
+        block.heads_scan_fwd(x.half(), None, A, B, B)
+    with pytest.raises(ValueError):
+        block.heads_scan_fwd(x[0], None, A, B, B)
+    with pytest.raises(ValueError, match="device"):
+        block.add_norm_fwd(x, torch.ones(8))
+    with pytest.raises(ValueError, match="groups"):
+        block.gated_norm_fwd(x, x, torch.ones(8), groups=3)

@@ -1,0 +1,408 @@
+"""The multi-head scan, its gradients and its single-token step
+(include/s6_block.h) against the plain 64-bit reference.
+
+Bars, as multiples of each value's magnitude m (the sum of its terms'
+absolute values), derived from the arithmetic:
+  fp32 inputs: sums of up to about 200 terms and a few roundings per term,
+    and decays off by 2^-24 times the exponents of a chunk (up to about 100):
+    2^-16 m.
+  bf16 inputs, results rounded to bf16: each term meets one rounding of the
+    decayed Gram matrix or the state (2^-9), the result one more (2^-9); a
+    sum over heads one more of the summed Gram gradients: 3 * 2^-9 m.
+  bf16 inputs, results kept in fp32: a factor in two bf16 parts is within
+    2^-17, and a term meets at most two of those beside the fp32 errors above:
+    2^-15 m.
+"""
+import numpy as np
+import pytest
+
+import block_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F32_BAR, BF16_BAR, KEPT_BAR = 2.0 ** -16, 3 * 2.0 ** -9, 2.0 ** -15
+
+
+@pytest.fixture(scope="module")
+def torch_cuda():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from selective_state_space_63_amd import s6
+    s6.load_library()
+    return torch
+
+
+def bar(dtype, kept=False):
+    return F32_BAR if dtype == "f32" else KEPT_BAR if kept else BF16_BAR
+
+
+def close(got, want, mag, bound, what):
+    got = got.detach().double().cpu().numpy()
+    assert got.shape == want.shape, what
+    assert np.isfinite(got).all(), what
+    err = np.abs(got - want)
+    worst = float(np.max(err / np.maximum(mag, 1e-30))) if err.size else 0.0
+    assert worst <= bound, f"{what}: {worst:.3e} of the magnitude, bar {bound:.3e}"
+
+
+def case(torch, b, L, H, P, G, N, dtype, step="softplus", h0=False, seed=0, packed=False, pad=0):
+    """Device inputs and the same values in 64 bits."""
+    g = np.random.default_rng([seed, b, L, H, P, G, N])
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    put = lambda a, t=torch.float32: torch.from_numpy(np.ascontiguousarray(a, np.float32)).cuda().to(t)  # noqa: E731
+    if packed:  # one row of x, B, C and `pad` more elements
+        row = put(g.standard_normal((b, L, pad + H * P + 2 * G * N)), dt)
+        x = row[..., pad:pad + H * P].unflatten(-1, (H, P))
+        B, C = (row[..., pad + H * P + k * G * N:pad + H * P + (k + 1) * G * N].unflatten(-1, (G, N)) for k in (0, 1))
+    else:
+        x, B, C = (put(g.standard_normal(s), dt) for s in ((b, L, H, P), (b, L, G, N), (b, L, G, N)))
+    bias = delta = None
+    level = np.exp(g.uniform(np.log(1e-3), np.log(0.3), H))
+    A = -np.exp(g.uniform(0, np.log(16.0), H))
+    if step == "softplus":
+        delta, bias = put(0.5 * g.standard_normal((b, L, H)), dt), put(np.log(np.expm1(level)))
+    elif step == "delta":
+        delta = put(level * np.exp(0.5 * g.standard_normal((b, L, H))), dt)
+    else:
+        A = -level
+    d = dict(x=x, delta=delta, A=put(A), Bm=B, Cm=C, D=put(g.standard_normal(H)), bias=bias,
+             h0=put(g.standard_normal((b, H, P, N))) if h0 else None)
+    n = {k: None if v is None else v.double().cpu().numpy() for k, v in d.items()}
+    return d, n
+
+
+def opts(d, step, unit):
+    return dict(D=d["D"], h0=d["h0"], delta_bias=d["bias"], delta_softplus=step == "softplus", unit_input=unit)
+
+
+def fwd(d, step, unit=False, **kw):
+    from selective_state_space_63_amd import block
+    return block.heads_scan_fwd(d["x"], d["delta"], d["A"], d["Bm"], d["Cm"], return_last_state=True,
+                                **{**opts(d, step, unit), **kw})
+
+
+SHAPES = [
+    # batch, L, heads, headdim, groups, dstate, dtype, step, unit, h0, packed, pad
+    (1, 1, 1, 1, 1, 1, "f32", "softplus", False, True, False, 0),
+    (1, 1, 2, 64, 1, 128, "bf16", "delta", False, False, False, 0),
+    (2, 2, 3, 7, 3, 3, "bf16", "softplus", False, True, False, 0),
+    (2, 63, 4, 64, 2, 64, "bf16", "softplus", False, True, True, 0),
+    (1, 64, 2, 64, 1, 128, "bf16", "softplus", True, False, True, 0),
+    (1, 65, 2, 64, 1, 32, "f32", "delta", False, True, True, 0),
+    (3, 127, 6, 40, 2, 24, "bf16", "none", True, True, False, 0),
+    (1, 128, 2, 128, 2, 128, "bf16", "softplus", False, True, False, 0),
+    (1, 129, 2, 130, 1, 100, "bf16", "delta", False, False, False, 0),   # three channel tiles, odd widths
+    (2, 200, 3, 65, 1, 33, "f32", "softplus", False, True, False, 0),
+    (2, 200, 4, 64, 4, 16, "bf16", "softplus", False, False, True, 3),   # rows at odd addresses
+    (2, 190, 2, 8, 1, 128, "f32", "none", False, True, True, 8),
+    # few long rows: cut into segments, the last one partial
+    (1, 1100, 1, 24, 1, 20, "bf16", "softplus", False, True, False, 0),
+    (1, 1536, 2, 64, 1, 64, "f32", "delta", True, True, False, 0),
+]
+IDS = lambda s: "x".join(map(str, s[:6])) + "-" + "-".join(map(str, s[6:]))  # noqa: E731
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_scan(torch_cuda, shape):
+    b, L, H, P, G, N, dtype, step, unit, h0, packed, pad = shape
+    print(f"[case] heads scan {shape}", flush=True)
+    d, n = case(torch_cuda, b, L, H, P, G, N, dtype, step, h0, 1, packed, pad)
+    y, hl = fwd(d, step, unit)
+    torch_cuda.cuda.synchronize()
+    assert y.dtype == d["x"].dtype and y.is_contiguous()
+    ry, my, rh, mh = ref.scan(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], n["D"], n["h0"], n["bias"],
+                              step == "softplus", unit)
+    close(y, ry, my, bar(dtype), "y")
+    close(hl, rh, mh, bar(dtype, True), "h_last")
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_gradients(torch_cuda, shape):
+    from selective_state_space_63_amd import block
+    b, L, H, P, G, N, dtype, step, unit, h0, packed, pad = shape
+    print(f"[case] heads scan gradients {shape}", flush=True)
+    torch = torch_cuda
+    d, n = case(torch, b, L, H, P, G, N, dtype, step, h0, 2, packed, pad)
+    g = np.random.default_rng(3)
+    dy = torch.from_numpy(g.standard_normal((b, L, H, P)).astype(np.float32)).cuda().to(d["x"].dtype)
+    dh = torch.from_numpy(g.standard_normal((b, H, P, N)).astype(np.float32)).cuda() if h0 else None
+    got = block.heads_scan_bwd(d["x"], d["delta"], d["A"], d["Bm"], d["Cm"], dy, dh_last=dh, **opts(d, step, unit))
+    torch.cuda.synchronize()
+    want = ref.scan_bwd(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], dy.double().cpu().numpy(), n["D"], n["h0"],
+                        None if dh is None else dh.double().cpu().numpy(), n["bias"], step == "softplus", unit)
+    names = {"dx", "dA", "dBm", "dCm", "dD"}
+    names |= {"ddelta"} if d["delta"] is not None else set()
+    names |= {"ddelta_bias"} if d["bias"] is not None else set()
+    names |= {"dh0"} if h0 else set()
+    assert set(got) == names
+    for k in sorted(names):
+        like = {"dx": "x", "dBm": "Bm", "dCm": "Cm", "ddelta": "delta"}.get(k)
+        assert got[k].dtype == (d[like].dtype if like else torch.float32), k
+        close(got[k], *want[k], bar(dtype, like is None), k)
+
+
+def test_gradients_against_differences(torch_cuda):
+    """Every gradient against central differences of the 64-bit forward along
+    random directions (fp32 inputs).  The differences are exact to about h^2
+    = 1e-10 and 1e-16 / h = 1e-11; the gradients to 2^-16 of the magnitude."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    d, n = case(torch, 2, 70, 4, 12, 2, 9, "f32", "softplus", True, 7)
+    g = np.random.default_rng(8)
+    dy, dh = g.standard_normal((2, 70, 4, 12)).astype(np.float32), g.standard_normal((2, 4, 12, 9)).astype(np.float32)
+    got = block.heads_scan_bwd(d["x"], d["delta"], d["A"], d["Bm"], d["Cm"], torch.from_numpy(dy).cuda(),
+                               dh_last=torch.from_numpy(dh).cuda(), **opts(d, "softplus", False))
+    mags = ref.scan_bwd(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], dy.astype(np.float64), n["D"], n["h0"],
+                        dh.astype(np.float64), n["bias"], True)
+
+    def loss(v):
+        y, _, hl, _ = ref.scan(v["x"], v["delta"], v["A"], v["Bm"], v["Cm"], v["D"], v["h0"], v["bias"], True)
+        return (y * dy).sum() + (hl * dh).sum()
+
+    h = 1e-5
+    for k, name in (("x", "dx"), ("delta", "ddelta"), ("A", "dA"), ("Bm", "dBm"), ("Cm", "dCm"), ("D", "dD"),
+                    ("h0", "dh0"), ("bias", "ddelta_bias")):
+        v = g.choice([-1.0, 1.0], n[k].shape)
+        diff = (loss({**n, k: n[k] + h * v}) - loss({**n, k: n[k] - h * v})) / (2 * h)
+        own = float((got[name].double().cpu().numpy() * v).sum())
+        assert abs(own - diff) <= F32_BAR * mags[name][1].sum() + 1e-6, (k, own, diff)
+
+
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[1] < 1000], ids=IDS)
+def test_step(torch_cuda, shape):
+    """One token on a given state; every sequence length of the list gives a
+    batch size here."""
+    from selective_state_space_63_amd import block
+    b, L, H, P, G, N, dtype, step, unit, _, packed, pad = shape
+    print(f"[case] heads step {shape}", flush=True)
+    d, n = case(torch_cuda, L, 1, H, P, G, N, dtype, step, True, 4, packed, pad)
+    one = lambda t: None if t is None else t[:, 0]  # noqa: E731
+    h = d["h0"].clone()
+    y = block.heads_state_update(h, one(d["x"]), one(d["delta"]), d["A"], one(d["Bm"]), one(d["Cm"]), D=d["D"],
+                                 delta_bias=d["bias"], delta_softplus=step == "softplus", unit_input=unit)
+    torch_cuda.cuda.synchronize()
+    ry, my, rh, mh = ref.scan(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], n["D"], n["h0"], n["bias"],
+                              step == "softplus", unit)
+    close(y, ry[:, 0], my[:, 0], bar(dtype), "y")
+    close(h, rh, mh, F32_BAR, "h")  # fp32 arithmetic on either type
+
+
+def test_prompt_then_tokens(torch_cuda):
+    """A prompt scanned to its state and continued token by token gives what
+    the scan of the whole sequence gives."""
+    from selective_state_space_63_amd import block
+    d, n = case(torch_cuda, 2, 150, 4, 64, 2, 64, "bf16", "softplus", False, 5)
+    cut = lambda a, b: {k: (v[:, a:b] if k in ("x", "delta", "Bm", "Cm") else v) for k, v in d.items()}  # noqa: E731
+    ys, h = fwd(cut(0, 100), "softplus")
+    out = [ys]
+    for t in range(100, 150):
+        one = {k: v[:, t] for k, v in d.items() if k in ("x", "delta", "Bm", "Cm")}
+        out.append(block.heads_state_update(h, one["x"], one["delta"], d["A"], one["Bm"], one["Cm"], D=d["D"],
+                                            delta_bias=d["bias"], delta_softplus=True)[:, None])
+    ry, my, rh, mh = ref.scan(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], n["D"], None, n["bias"], True)
+    close(torch_cuda.cat(out, 1), ry, my, BF16_BAR, "y")
+    close(h, rh, mh, KEPT_BAR, "h")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_reset_tokens(torch_cuda, dtype):
+    """A token with s A far below -100 starts a sequence anew: the tokens
+    from it on are those of a sequence of their own, without a state before
+    it (with a unit input, so that only the decay sees the step)."""
+    torch = torch_cuda
+    d, n = case(torch, 1, 140, 2, 64, 1, 64, dtype, "delta", True, 6)
+    d["delta"][:, 50] = 3.0e3
+    d["delta"][:, 97] = 1.0e30
+    y, hl = fwd(d, "delta", True)
+    for lo, hi in ((50, 97), (97, 140)):
+        part = {k: (v[:, lo:hi] if k in ("x", "Bm", "Cm") else v) for k, v in n.items()}
+        dl = n["delta"][:, lo:hi].copy()
+        dl[:, 0] = 0.0
+        ry, my, rh, mh = ref.scan(part["x"], dl, part["A"], part["Bm"], part["Cm"], part["D"], None, None, False, True)
+        close(y[:, lo:hi], ry, my, bar(dtype), f"y from {lo}")
+    close(hl, rh, mh, bar(dtype, True), "h_last")
+
+
+def test_infinite_decay(torch_cuda):
+    """A head with A = -inf keeps nothing: y_t = w_t x_t (B_t . C_t) + D x_t,
+    and its state is the last token's."""
+    torch = torch_cuda
+    d, n = case(torch, 2, 90, 2, 16, 1, 16, "f32", "delta", True, 9)
+    d["A"][1] = float("-inf")
+    y, hl = fwd(d, "delta")
+    w = n["delta"][:, :, 1, None] * n["x"][:, :, 1]
+    bc = (n["Bm"][:, :, 0] * n["Cm"][:, :, 0])
+    want = w * bc.sum(-1)[..., None] + n["D"][1] * n["x"][:, :, 1]
+    mag = np.abs(w) * np.abs(bc).sum(-1)[..., None] + np.abs(n["D"][1] * n["x"][:, :, 1])
+    close(y[:, :, 1], want, mag, F32_BAR, "y")
+    last = w[:, -1, :, None] * n["Bm"][:, -1, 0, None]
+    close(hl[:, 1], last, np.abs(last), F32_BAR, "h_last")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["x", "delta", "Bm", "Cm"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_later_tokens_do_not_reach_earlier_ones(torch_cuda, dtype, name, value):
+    """Values that are not finite in a sequence's tail (padding that was never
+    written) leave every earlier token's output as it is."""
+    torch = torch_cuda
+    d, n = case(torch, 1, 100, 2, 64, 1, 64, dtype, "delta", True, 10)
+    y0, _ = fwd(d, "delta")
+    d[name] = d[name].clone()
+    d[name][:, 83:] = value
+    y1, hl = fwd(d, "delta")
+    torch.cuda.synchronize()
+    assert torch.equal(y0[:, :83], y1[:, :83])
+    if name != "Cm" and not (name == "delta" and value == float("inf")):
+        assert not torch.isfinite(hl).any()
+    if name == "x":
+        assert not torch.isfinite(y1[:, 83:]).any()
+
+
+def test_one_channel_not_finite(torch_cuda):
+    """One channel's infinite input leaves the other channels alone."""
+    torch = torch_cuda
+    d, n = case(torch, 1, 100, 2, 64, 1, 32, "bf16", "delta", False, 11)
+    y0, h0 = fwd(d, "delta")
+    d["x"][0, 40, 1, 5] = float("inf")
+    y1, h1 = fwd(d, "delta")
+    keep = torch.ones(2, 64, dtype=torch.bool, device="cuda")
+    keep[1, 5] = False
+    assert torch.equal(y0[:, :, keep], y1[:, :, keep]) and torch.equal(h0[:, keep], h1[:, keep])
+    assert torch.equal(y0[:, :40], y1[:, :40])
+    assert not torch.isfinite(y1[0, 40:, 1, 5]).any()
+
+
+def test_zero_steps_keep_the_state(torch_cuda):
+    d, n = case(torch_cuda, 2, 77, 3, 20, 1, 12, "f32", "delta", True, 12)
+    d["delta"].zero_()
+    y, hl = fwd(d, "delta")
+    assert torch_cuda.equal(hl, d["h0"])
+
+
+def test_no_tokens_and_no_rows(torch_cuda):
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    d, _ = case(torch, 2, 0, 3, 8, 1, 4, "bf16", "softplus", True, 13)
+    y, hl = fwd(d, "softplus")
+    assert y.shape == (2, 0, 3, 8) and torch.equal(hl, d["h0"])
+    _, hl = fwd({**d, "h0": None}, "softplus")
+    assert torch.equal(hl, torch.zeros_like(hl))
+    dh = torch.randn_like(d["h0"])
+    g = block.heads_scan_bwd(d["x"], d["delta"], d["A"], d["Bm"], d["Cm"], torch.empty_like(d["x"]), dh_last=dh,
+                             **opts(d, "softplus", False))
+    assert torch.equal(g["dh0"], dh)
+    for k in ("dA", "dD", "ddelta_bias"):
+        assert torch.equal(g[k], torch.zeros(3, device="cuda")), k
+    d, _ = case(torch, 0, 5, 3, 8, 1, 4, "bf16", "softplus", False, 14)
+    y, hl = fwd(d, "softplus")
+    assert y.shape == (0, 5, 3, 8) and hl.shape == (0, 3, 8, 4)
+
+
+def test_same_bits_and_other_stream(torch_cuda):
+    """Repeated calls give the same bits, also on another stream with work
+    before it that the inputs depend on."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    d, _ = case(torch, 2, 700, 4, 64, 2, 64, "bf16", "softplus", True, 15)
+    dy = torch.randn(d["x"].shape, device="cuda").to(torch.bfloat16)
+
+    def once():
+        y, hl = fwd(d, "softplus")
+        g = block.heads_scan_bwd(d["x"], d["delta"], d["A"], d["Bm"], d["Cm"], dy, **opts(d, "softplus", False))
+        return [y, hl] + [g[k] for k in sorted(g)]
+
+    a = once()
+    torch.cuda.synchronize()
+    keep = d["x"]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        d["x"] = keep * 1.0
+        for _ in range(20):  # a queue of work that writes x last
+            d["x"].mul_(-1.0)
+        b = once()
+    s.synchronize()
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+
+
+def test_graph(torch_cuda):
+    """Captured once, replayed on new inputs with eager work in between."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    d, _ = case(torch, 1, 300, 2, 64, 1, 64, "bf16", "softplus", False, 16)
+    dy = torch.randn(d["x"].shape, device="cuda").to(torch.bfloat16)
+    h = torch.randn(1, 2, 64, 64, device="cuda")
+    y1 = torch.empty_like(d["x"][:, 0])
+
+    def once():
+        y, hl = fwd(d, "softplus")
+        g = block.heads_scan_bwd(d["x"], d["delta"], d["A"], d["Bm"], d["Cm"], dy, **opts(d, "softplus", False))
+        block.heads_state_update(h, d["x"][:, 0], d["delta"][:, 0], d["A"], d["Bm"][:, 0], d["Cm"][:, 0], D=d["D"],
+                                 delta_bias=d["bias"], delta_softplus=True, y=y1)
+        return [y, hl, y1, h] + [g[k] for k in sorted(g)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        once()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = once()
+    for i in range(3):
+        d["x"].copy_(torch.randn_like(d["x"]))
+        h0 = torch.randn_like(h)
+        h.copy_(h0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        h.copy_(h0)
+        for u, v in zip(once(), got):
+            assert torch.equal(u, v), i
+
+
+def test_autograd(torch_cuda):
+    """HeadsScan against the binding's gradients, with slices as inputs and an
+    unused final state."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    d, _ = case(torch, 2, 90, 4, 16, 2, 16, "bf16", "softplus", True, 17, packed=True)
+    leaf = {k: d[k].detach().clone().requires_grad_() for k in ("x", "delta", "A", "Bm", "Cm", "D", "h0", "bias")}
+    y, _ = block.HeadsScan.apply(*(leaf[k] for k in ("x", "delta", "A", "Bm", "Cm", "D", "h0", "bias")), True, False)
+    dy = torch.randn(y.shape, device="cuda").to(y.dtype)
+    y.backward(dy)
+    g = block.heads_scan_bwd(d["x"].contiguous(), d["delta"], d["A"], d["Bm"].contiguous(), d["Cm"].contiguous(), dy,
+                             **opts(d, "softplus", False))
+    for k, name in (("x", "dx"), ("delta", "ddelta"), ("A", "dA"), ("Bm", "dBm"), ("Cm", "dCm"), ("D", "dD"),
+                    ("h0", "dh0"), ("bias", "ddelta_bias")):
+        assert torch.equal(leaf[k].grad, g[name]), k
+
+
+def test_offsets_past_32_bits(torch_cuda):
+    """States of over 2^31 elements, and sequences whose rows end beyond 2^31
+    elements: the far end is right."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    b, H, P, N = 33000, 8, 64, 128
+    h = torch.zeros(b, H, P, N, device="cuda")  # 2.2e9 elements
+    x = torch.randn(b, H, P, device="cuda").to(torch.bfloat16)
+    B = torch.randn(b, 1, N, device="cuda").to(torch.bfloat16)
+    dl = torch.rand(b, H, device="cuda").to(torch.bfloat16)
+    A = -torch.ones(H, device="cuda")
+    block.heads_state_update(h, x, dl, A, B, B)
+    want = (dl[-3:].float()[..., None] * x[-3:].float())[..., None] * B[-3:].float()[:, :, None]
+    assert torch.allclose(h[-3:], want, rtol=1e-5, atol=1e-6)
+    del h
+    L, H = (1 << 20) + 37, 33
+    x = torch.randn(1, L, H, 64, device="cuda", dtype=torch.bfloat16)  # 2.2e9 elements
+    B = torch.randn(1, L, 1, 16, device="cuda").to(torch.bfloat16)
+    dl = torch.full((1, L, H), 0.25, device="cuda", dtype=torch.bfloat16)
+    A = -torch.ones(H, device="cuda")
+    y = block.heads_scan_fwd(x, dl, A, B, B)
+    # 400 tokens of decay e^-0.25 leave e^-100 of what was before
+    tail = block.heads_scan_fwd(x[:, -500:], dl[:, -500:], A, B[:, -500:], B[:, -500:])
+    d = (y[:, -100:].float() - tail[:, -100:].float()).abs().max()
+    assert float(d) <= 2 * BF16_BAR * float(y[:, -100:].float().abs().max())
