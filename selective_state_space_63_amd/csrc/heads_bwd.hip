@@ -123,7 +123,8 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   id /= ba.nhb;
   const int grp = (int)(id % ba.groups);
   const int64_t b = id / ba.groups;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int lane0 = threadIdx.x & 63, wv = wave_index(), g0 = lane0 >> 4, c0 = lane0 & 15;
+  int lane = lane0, g = g0, c = c0;
   const int ns = wv % NS, tp = wv / NS;
   const int64_t t0 = blk * Q;
   const int rows = (int)(a.L - t0 < Q ? a.L - t0 : Q);
@@ -193,6 +194,11 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
     const float dsk = a.D ? a.D[hd] : 0.0f;
     for (int pt = 0; pt < a.ptiles; ++pt) {
       const bool last_pt = pt + 1 == a.ptiles;
+      // LDS addresses are formed again in every turn: kept across it they
+      // would not leave room for the sums
+      lane = lane0;
+      asm volatile("" : "+v"(lane));
+      g = lane >> 4; c = lane & 15;
       const int p0 = pt * kTP, pleft = a.headdim - p0;
       xr.store(xs, XP);
       yr.store(ys, XP);
@@ -275,6 +281,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
             if (lane == 0) ddp[I] = diag;
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (tp == 0) {
 #pragma unroll
@@ -325,6 +332,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
           yp[ns * Q + t] = e * sy;
           up[ns * Q + t] = f * su;
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
 
       // dx, transposed: channels of tile q, tokens of tiles J
@@ -359,6 +367,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
                 if (p + r < pleft) dp[r] = from_f32<In>(o[r]);
             }
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
       __syncthreads();

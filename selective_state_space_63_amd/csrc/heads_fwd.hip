@@ -44,7 +44,7 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
   const int64_t rid = nrows % 8 == 0 ? (blockIdx.x % 8) * (nrows / 8) + blockIdx.x / 8 : blockIdx.x;
   const HeadRow hr = head_row(a, rid);
   const int64_t seg = blockIdx.y;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int lane = threadIdx.x & 63, wv = wave_index(), g = lane >> 4, c = lane & 15;
   const int p0 = hr.pt * kTP, pleft = a.headdim - p0;
   const int64_t t_lo = seg * a.seg_len;
   const int64_t t_hi = t_lo + a.seg_len < a.L ? t_lo + a.seg_len : a.L;

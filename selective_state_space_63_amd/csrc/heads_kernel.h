@@ -262,6 +262,9 @@ struct TileRegs {
 };
 
 // ------------------------------------------------------------ the chunk --
+// Index of the wave in its workgroup, in a scalar register.
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // Inclusive sum over the 64 lanes of a wave.
 __device__ __forceinline__ float wave_scan(float v) {
   v += dpp_f<0x111>(v);  // row_shr:1, 2, 4, 8

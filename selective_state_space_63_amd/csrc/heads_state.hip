@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void s6_heads_state_kernel(HeadsArgs a, int mo
   const int64_t nrows = gridDim.x;
   const int dir = blockIdx.z;
   const int64_t seg = mode == 0 && dir ? blockIdx.y + 1 : blockIdx.y;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int lane = threadIdx.x & 63, wv = wave_index(), g = lane >> 4, c = lane & 15;
   const int pp = wv & 1, nh = wv >> 1;
   const int p0 = hr.pt * kTP, pleft = a.headdim - p0;
   const int64_t t_lo = seg * a.seg_len;
