@@ -144,7 +144,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   for (int i = threadIdx.x; i < O::NFRAG * 512; i += 512) mf[i] = In(0);  // halves above the diagonal stay 0
 
   TileRegs<In, Q, kTP, 512, VEC> xr, yr;
-  float draw[PL];
+  In draw[PL];  // as loaded: a conversion there would wait for every load before it
   auto issue = [&](int hd, int pt) {
     const bool on = hd < hd1;
     const int cols = a.headdim - pt * kTP;
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
 #pragma unroll
       for (int k = 0; k < PL; ++k)
         if (k * 64 + lane < rows)
-          draw[k] = to_f32(static_cast<const In*>(a.delta)[b * a.d_batch + (t0 + k * 64 + lane) * a.d_token + hd]);
+          draw[k] = static_cast<const In*>(a.delta)[b * a.d_batch + (t0 + k * 64 + lane) * a.d_token + hd];
     }
   };
   issue(hd0, 0);
@@ -208,8 +208,8 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
 #pragma unroll
         for (int k = 0; k < PL; ++k) {
           const bool on = k * 64 + lane < rows;
-          const float v = (on && a.delta ? draw[k] : 0.0f) + bias;
-          sv[k] = on ? step_of(a, draw[k], bias) : 0.0f;
+          const float v = (on && a.delta ? to_f32(draw[k]) : 0.0f) + bias;
+          sv[k] = on ? step_of(a, to_f32(draw[k]), bias) : 0.0f;
           vd[k] = a.softplus ? fast_rcp(1.0f + fast_exp2(-v * kLog2e)) : 1.0f;
           cl[k] = base + wave_scan(on ? clamp_log2(sv[k] * a2) : 0.0f);
           base = last_lane(cl[k]);

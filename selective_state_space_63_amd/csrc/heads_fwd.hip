@@ -84,13 +84,13 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
 
   TileRegs<In, kHQ, kTP, 256, VEC> xr;
   TileRegs<In, kHQ, NT, 256, VEC> br, cr;
-  float draw = 0.0f;
+  In draw = In(0);  // as loaded: a conversion here would wait for every load before it
   auto issue = [&](int64_t t0) {
     const int rows = t0 >= t_hi ? 0 : (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ);
     xr.load(X + t0 * a.x_token, a.x_token, rows, pleft < kTP ? pleft : kTP);
     br.load(B + t0 * a.b_token, a.b_token, rows, a.dstate);
     cr.load(C + t0 * a.c_token, a.c_token, rows, a.dstate);
-    if (dl && (int)threadIdx.x < rows) draw = to_f32(dl[(t0 + threadIdx.x) * a.d_token]);
+    if (dl && (int)threadIdx.x < rows) draw = dl[(t0 + threadIdx.x) * a.d_token];
   };
   issue(t_lo);
   __syncthreads();
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
     cr.store(cm, kBP);
     if (wv == 0) {
       const bool on = lane < rows;
-      const float s = on ? step_of(a, draw, bias) : 0.0f;
+      const float s = on ? step_of(a, to_f32(draw), bias) : 0.0f;
       const float v = wave_scan(on ? clamp_log2(s * a2) : 0.0f);
       const float w = on ? (a.unit ? 1.0f : s) : 0.0f;
       cs[lane] = v;

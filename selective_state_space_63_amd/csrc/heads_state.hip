@@ -82,13 +82,13 @@ __global__ __launch_bounds__(256) void s6_heads_state_kernel(HeadsArgs a, int mo
 
   TileRegs<In, kHQ, kTP, 256, VEC> xr;
   TileRegs<In, kHQ, NT, 256, VEC> br;
-  float draw = 0.0f;
+  In draw = In(0);  // as loaded: a conversion here would wait for every load before it
   auto issue = [&](int64_t k) {
     const int64_t t0 = t_lo + k * kHQ;
     const int rows = k < 0 || k >= nch ? 0 : (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ);
     xr.load(X + t0 * xt, xt, rows, pleft < kTP ? pleft : kTP);
     br.load(B + t0 * bt, bt, rows, a.dstate);
-    if (dl && (int)threadIdx.x < rows) draw = to_f32(dl[(t0 + threadIdx.x) * a.d_token]);
+    if (dl && (int)threadIdx.x < rows) draw = dl[(t0 + threadIdx.x) * a.d_token];
   };
   const int64_t first = dir ? nch - 1 : 0, step = dir ? -1 : 1;
   issue(first);
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256) void s6_heads_state_kernel(HeadsArgs a, int mo
     br.store(bs, kBP);
     if (wv == 0) {
       const bool on = lane < rows;
-      const float s = on ? step_of(a, draw, bias) : 0.0f;
+      const float s = on ? step_of(a, to_f32(draw), bias) : 0.0f;
       const float cs = wave_scan(on ? clamp_log2(s * a2) : 0.0f);
       const float cq = last_lane(cs);
       const float w = on ? (a.unit ? 1.0f : s) : 0.0f;
