@@ -60,14 +60,17 @@ struct BwdLds {
   static constexpr int Q = kBQ<In>;
   static constexpr int NTT = Q / 16, H = NTT / 2, NTILE = NTT * (NTT + 1) / 2;
   static constexpr int NFRAG = H * (H + 1);
-  static constexpr int XP = kTP + kPad, BP = NT + kPad;
+  using XT = RowTile<In, kTP>;   // x, dy: by tokens
+  using BT = RowTile<In, NT>;    // B, C: by tokens
+  using LT = ColTile<In, kTP>;   // L: by states, read down its columns
+  using PT = RowTile<In, Q>;     // P at the end, in the place of x and dy
   static constexpr int NS = NT / 16;
   static constexpr int bs = 0;
-  static constexpr int cm = bs + Q * BP * (int)sizeof(In);
-  static constexpr int xs = cm + Q * BP * (int)sizeof(In);
-  static constexpr int ys = xs + Q * XP * (int)sizeof(In);
-  static constexpr int lm = ys + Q * XP * (int)sizeof(In);
-  static constexpr int mf = lm + NT * XP * (int)sizeof(In);
+  static constexpr int cm = bs + BT::size(Q) * (int)sizeof(In);
+  static constexpr int xs = cm + BT::size(Q) * (int)sizeof(In);
+  static constexpr int ys = xs + XT::size(Q) * (int)sizeof(In);
+  static constexpr int lm = ys + XT::size(Q) * (int)sizeof(In);
+  static constexpr int mf = lm + LT::size(NT) * (int)sizeof(In);
   static constexpr int rp = mf + NFRAG * 512 * (int)sizeof(In);  // row sums of the tiles
   static constexpr int cp = rp + NTILE * 16 * 4;                 // column sums
   static constexpr int yp = cp + NTILE * 16 * 4;                 // dy . S C by strip
@@ -93,16 +96,14 @@ __device__ __forceinline__ int frag_at(int J, int kk) {
 template <typename In, int NT, bool VEC>
 __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   using O = BwdLds<In, NT>;
-  constexpr int Q = O::Q, NTT = O::NTT, H = O::H, XP = O::XP, BP = O::BP, NS = O::NS, NK = NT / 32;
+  constexpr int Q = O::Q, NTT = O::NTT, H = O::H, NS = O::NS, NK = NT / 32;
   constexpr int TPN = 8 / NS, TT = NTT / TPN;       // token parts of the strips, tiles per part
   constexpr int SLOTS = (O::NTILE + 7) / 8;         // Gram tiles per wave
   constexpr int PL = Q / 64;                        // tokens per lane of wave 0
   extern __shared__ __align__(16) char lds[];
-  In* bs = reinterpret_cast<In*>(lds + O::bs);
-  In* cm = reinterpret_cast<In*>(lds + O::cm);
-  In* xs = reinterpret_cast<In*>(lds + O::xs);
-  In* ys = reinterpret_cast<In*>(lds + O::ys);
-  In* lm = reinterpret_cast<In*>(lds + O::lm);
+  const typename O::BT bs{reinterpret_cast<In*>(lds + O::bs)}, cm{reinterpret_cast<In*>(lds + O::cm)};
+  const typename O::XT xs{reinterpret_cast<In*>(lds + O::xs)}, ys{reinterpret_cast<In*>(lds + O::ys)};
+  const typename O::LT lm{reinterpret_cast<In*>(lds + O::lm)};
   In* mf = reinterpret_cast<In*>(lds + O::mf);
   float* rp = reinterpret_cast<float*>(lds + O::rp);
   float* cp = reinterpret_cast<float*>(lds + O::cp);
@@ -138,8 +139,10 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
             a.dstate);
     cr.load(static_cast<const In*>(a.Cm) + b * a.c_batch + t0 * a.c_token + (int64_t)grp * a.dstate, a.c_token, rows,
             a.dstate);
-    br.store(bs, BP);
-    cr.store(cm, BP);
+    br.mask(rows, a.dstate);
+    cr.mask(rows, a.dstate);
+    br.store(bs);
+    cr.store(cm);
   }
   for (int i = threadIdx.x; i < O::NFRAG * 512; i += 512) mf[i] = In(0);  // halves above the diagonal stay 0
 
@@ -177,7 +180,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
     if (n < O::NTILE) {
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk)
-        CB[k] = mma(row_frag(cm, BP, 16 * I + c, kk, g), row_frag(bs, BP, 16 * tJ[k] + c, kk, g), CB[k]);
+        CB[k] = mma(cm.row(16 * I + c, kk, g), bs.row(16 * tJ[k] + c, kk, g), CB[k]);
     }
   }
   f32x4 dC[TT], dB[TT];
@@ -200,8 +203,10 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       asm volatile("" : "+v"(lane));
       g = lane >> 4; c = lane & 15;
       const int p0 = pt * kTP, pleft = a.headdim - p0;
-      xr.store(xs, XP);
-      yr.store(ys, XP);
+      xr.mask(rows, pleft < kTP ? pleft : kTP);
+      yr.mask(rows, pleft < kTP ? pleft : kTP);
+      xr.store(xs);
+      yr.store(ys);
       float sv[PL], vd[PL];  // wave 0: the tokens' steps and their derivatives
       if (wv == 0) {
         float base = 0.0f, cl[PL];
@@ -253,7 +258,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
           f32x4 X = {0, 0, 0, 0};
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
-            X = mma(row_frag(ys, XP, 16 * I + c, kk, g), row_frag(xs, XP, 16 * J + c, kk, g), X);
+            X = mma(ys.row(16 * I + c, kk, g), xs.row(16 * J + c, kk, g), X);
           const float4 ct4 = *reinterpret_cast<const float4*>(cs + 16 * I + 4 * g);
           const float ct[4] = {ct4.x, ct4.y, ct4.z, ct4.w};
           const float cj = cs[16 * J + c], wj = ww[16 * J + c];
@@ -285,11 +290,12 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       }
       if (tp == 0) {
 #pragma unroll
-        for (int pp = 0; pp < 2; ++pp) {  // L by rows n: the operand's order is the tile row's order
-          float f[8];
+        for (int pp = 0; pp < 2; ++pp) {
+          float f[4], h[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = frag_f32(Lf[pp].hi, e);
-          store_vec<In, 8>(lm + (16 * ns + c) * XP + 32 * pp + 8 * g, f);
+          for (int e = 0; e < 4; ++e) { f[e] = frag_f32(Lf[pp].hi, e); h[e] = frag_f32(Lf[pp].hi, 4 + e); }
+          store_vec<In, 4>(lm.t + lm.at(16 * ns + c, 8 * pp + g), f);
+          store_vec<In, 4>(lm.t + lm.at(16 * ns + c, 8 * pp + 4 + g), h);
         }
         float s = 0.0f;
 #pragma unroll
@@ -312,12 +318,12 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
         f32x4 U = {0, 0, 0, 0}, V = {0, 0, 0, 0};
 #pragma unroll
         for (int pp = 0; pp < 2; ++pp) {
-          U = mma_pair(Sf[pp], row_frag(ys, XP, t, pp, g), U);
-          V = mma_pair(Lf[pp], row_frag(xs, XP, t, pp, g), V);
+          U = mma_pair(Sf[pp], ys.row(t, pp, g), U);
+          V = mma_pair(Lf[pp], xs.row(t, pp, g), V);
         }
         float cv[4], bv[4], sy = 0.0f, su = 0.0f;
-        row_four(cm, BP, t, 4 * ns + g, cv);
-        row_four(bs, BP, t, 4 * ns + g, bv);
+        cm.four(t, 4 * ns + g, cv);
+        bs.four(t, 4 * ns + g, bv);
         const float e = ec[t], f = wd[t], fw = ww[t] * f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -340,21 +346,21 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
         const int q = wv & 3;
         Frag<In> lq[NK], yq[H];
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) lq[kk] = col_frag(lm, XP, q, kk, g, c);
+        for (int kk = 0; kk < NK; ++kk) lq[kk] = lm.col(q, kk, g, c);
 #pragma unroll
-        for (int kk = 0; kk < H; ++kk) yq[kk] = col_frag(ys, XP, q, kk, g, c);
+        for (int kk = 0; kk < H; ++kk) yq[kk] = ys.col(q, kk, g, c);
         const int p = 16 * q + 4 * g;
 #pragma unroll
         for (int i = 0; i < NTT / 2; ++i) {
           const int J = 2 * i + (wv >> 2), s = 16 * J + c;
           f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-          for (int kk = 0; kk < NK; ++kk) acc = mma(lq[kk], row_frag(bs, BP, s, kk, g), acc);
+          for (int kk = 0; kk < NK; ++kk) acc = mma(lq[kk], bs.row(s, kk, g), acc);
           acc *= ww[s] * wd[s];
 #pragma unroll
           for (int kk = i; kk < H; ++kk) acc = mma(yq[kk], lane_frag(mf + frag_at<H>(J, kk) * 512, lane), acc);
           float dyv[4], o[4];
-          row_four(ys, XP, s, 4 * q + g, dyv);
+          ys.four(s, 4 * q + g, dyv);
 #pragma unroll
           for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(dsk, dyv[r], acc[r]);
           if (s < rows) {
@@ -446,30 +452,28 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   // dC += P B and dB += P^T C with P summed over the heads (x and dy are done:
   // every wave is past the last barrier), P rounded to the input type
   {
-    constexpr int PP = Q + kPad;
-    In* pm = xs;
-    static_assert(Q * PP <= 2 * Q * XP, "P fits x and dy");
+    const typename O::PT pm{xs.t};
+    static_assert(O::PT::size(Q) <= 2 * O::XT::size(Q), "P fits x and dy");
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k) {
       if (8 * k + wv < O::NTILE) {
-        const int at = chunk_at(4 * tJ[k] + (c >> 2)) + (c & 3);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) pm[(16 * tI[k] + 4 * g + r) * PP + at] = from_f32<In>(P[k][r]);
+        for (int r = 0; r < 4; ++r)
+          pm.t[pm.at(16 * tI[k] + 4 * g + r, 4 * tJ[k] + (c >> 2)) + (c & 3)] = from_f32<In>(P[k][r]);
       }
     }
     if (wv < H) {  // the tile right of an even diagonal tile shares an operand with it
-      const int at = chunk_at(4 * (2 * wv + 1) + (c >> 2)) + (c & 3);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) pm[(32 * wv + 4 * g + r) * PP + at] = In(0);
+      for (int r = 0; r < 4; ++r) pm.t[pm.at(32 * wv + 4 * g + r, 4 * (2 * wv + 1) + (c >> 2)) + (c & 3)] = In(0);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       const int it = tp * TT + i;
       for (int kk = 0; kk <= it / 2; ++kk)
-        dC[i] = mma(col_frag(bs, BP, ns, kk, g, c), row_frag(pm, PP, 16 * it + c, kk, g), dC[i]);
+        dC[i] = mma(bs.col(ns, kk, g, c), pm.row(16 * it + c, kk, g), dC[i]);
       for (int kk = it / 2; kk < H; ++kk)
-        dB[i] = mma(col_frag(cm, BP, ns, kk, g, c), col_frag(pm, PP, it, kk, g, c), dB[i]);
+        dB[i] = mma(cm.col(ns, kk, g, c), pm.col(it, kk, g, c), dB[i]);
     }
 #pragma unroll
     for (int i = 0; i < TT; ++i) {

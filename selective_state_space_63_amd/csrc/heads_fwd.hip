@@ -23,20 +23,32 @@ namespace s6i {
 
 namespace {
 
+// Offsets in LDS (bytes).
+template <typename In, int NT>
+struct ScanLds {
+  using XT = ColTile<In, kTP>;
+  using BT = ColTile<In, NT>;
+  using CT = RowTile<In, NT>;
+  static constexpr int xs = 0;
+  static constexpr int bs = xs + XT::size(kHQ) * (int)sizeof(In);
+  static constexpr int cm = bs + BT::size(kHQ) * (int)sizeof(In);
+  static constexpr int pf = cm + CT::size(kHQ) * (int)sizeof(In);
+  static constexpr int tok = pf + 4096 * (int)sizeof(In);
+  static constexpr int bad = tok + 2 * 4 * kHQ * 4;
+  static constexpr int total = bad + (kTP + 4) * 4;
+};
+
 template <typename In, int NT, bool VEC>
-__global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
-  constexpr int kXP = kTP + kPad, kBP = NT + kPad;
+__global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_heads_scan_kernel(HeadsArgs a) {
   constexpr int NQ = NT / 16, NK = NT / 32;
+  using L = ScanLds<In, NT>;
   extern __shared__ __align__(16) char lds[];
-  In* xs = reinterpret_cast<In*>(lds);
-  In* bs = xs + kHQ * kXP;
-  In* cm = bs + kHQ * kBP;
-  In* pf = cm + kHQ * kBP;                                // [4 t tiles][2][lane][8]
-  float* cs = reinterpret_cast<float*>(pf + 4 * 2 * 512);  // running log2 decay
-  float* ec = cs + kHQ;                                   // its exponential
-  float* ww = ec + kHQ;                                   // input weight
-  float* wd = ww + kHQ;                                   // weight decayed to the chunk's end
-  int* bad = reinterpret_cast<int*>(wd + kHQ);            // first token whose input is not finite
+  const typename L::XT xs{reinterpret_cast<In*>(lds + L::xs)};
+  const typename L::BT bs{reinterpret_cast<In*>(lds + L::bs)};
+  const typename L::CT cm{reinterpret_cast<In*>(lds + L::cm)};
+  In* pf = reinterpret_cast<In*>(lds + L::pf);             // [4 t tiles][2][lane][8]
+  float* tok = reinterpret_cast<float*>(lds + L::tok);     // per-token values, two chunks' worth
+  int* bad = reinterpret_cast<int*>(lds + L::bad);         // first token whose input is not finite
   int* any = bad + kTP;
   // consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of
   // rows, whose B and C come through one L2
@@ -44,7 +56,8 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
   const int64_t rid = nrows % 8 == 0 ? (blockIdx.x % 8) * (nrows / 8) + blockIdx.x / 8 : blockIdx.x;
   const HeadRow hr = head_row(a, rid);
   const int64_t seg = blockIdx.y;
-  const int lane = threadIdx.x & 63, wv = wave_index(), g = lane >> 4, c = lane & 15;
+  const int lane0 = threadIdx.x & 63, wv = wave_index();
+  int lane = lane0, g = lane >> 4, c = lane & 15;
   const int p0 = hr.pt * kTP, pleft = a.headdim - p0;
   const int64_t t_lo = seg * a.seg_len;
   const int64_t t_hi = t_lo + a.seg_len < a.L ? t_lo + a.seg_len : a.L;
@@ -84,37 +97,62 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
 
   TileRegs<In, kHQ, kTP, 256, VEC> xr;
   TileRegs<In, kHQ, NT, 256, VEC> br, cr;
-  In draw = In(0);  // as loaded: a conversion here would wait for every load before it
+  auto rows_at = [&](int64_t t0) { return t0 >= t_hi ? 0 : (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ); };
   auto issue = [&](int64_t t0) {
-    const int rows = t0 >= t_hi ? 0 : (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ);
+    const int rows = rows_at(t0);
     xr.load(X + t0 * a.x_token, a.x_token, rows, pleft < kTP ? pleft : kTP);
     br.load(B + t0 * a.b_token, a.b_token, rows, a.dstate);
     cr.load(C + t0 * a.c_token, a.c_token, rows, a.dstate);
-    if (dl && (int)threadIdx.x < rows) draw = dl[(t0 + threadIdx.x) * a.d_token];
   };
+  // The last wave (it has the fewest Gram tiles) forms the tokens' decays and
+  // weights a chunk ahead, from steps loaded two chunks ahead: running log2
+  // decay, its exponential, input weight, weight decayed to the chunk's end.
+  In draw = In(0);  // as loaded: a conversion here would wait for every load before it
+  auto issue_step = [&](int64_t t0) {
+    if (wv == 3 && dl && lane < rows_at(t0)) draw = dl[(t0 + lane) * a.d_token];
+  };
+  auto decays = [&](int64_t t0, int buf) {
+    if (wv != 3) return;
+    const bool on = lane < rows_at(t0);
+    const float s = on ? step_of(a, to_f32(draw), bias) : 0.0f;
+    const float v = wave_scan(on ? clamp_log2(s * a2) : 0.0f);
+    const float w = on ? (a.unit ? 1.0f : s) : 0.0f;
+    float* o = tok + buf * 4 * kHQ;
+    o[lane] = v;
+    o[kHQ + lane] = fast_exp2(v);
+    o[2 * kHQ + lane] = w;
+    o[3 * kHQ + lane] = w * fast_exp2(last_lane(v) - v);
+  };
+  issue_step(t_lo);
   issue(t_lo);
+  decays(t_lo, 0);
+  issue_step(t_lo + kHQ);
   __syncthreads();
-  for (int64_t t0 = t_lo; t0 < t_hi; t0 += kHQ) {
-    const int rows = (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ);
+  int buf = 0;
+  for (int64_t t0 = t_lo; t0 < t_hi; t0 += kHQ, buf ^= 1) {
+    const int rows = rows_at(t0);
+    // LDS addresses are formed again in every turn: kept across it they would
+    // cost a workgroup per CU
+    lane = lane0;
+    asm volatile("" : "+v"(lane));
+    g = lane >> 4; c = lane & 15;
+    const float* cs = tok + buf * 4 * kHQ;
+    const float *ec = cs + kHQ, *ww = cs + 2 * kHQ, *wd = cs + 3 * kHQ;
     // An input that is not finite would reach earlier tokens through the
     // zeros of the Gram matrix (0 x inf): it is taken out here and its channel
     // set to NaN from its token on.
+    const int cols = pleft < kTP ? pleft : kTP;
+    xr.mask(rows, cols);
+    br.mask(rows, a.dstate);
+    cr.mask(rows, a.dstate);
     xr.clean(bad, any);
-    xr.store(xs, kXP);
-    br.store(bs, kBP);
-    cr.store(cm, kBP);
-    if (wv == 0) {
-      const bool on = lane < rows;
-      const float s = on ? step_of(a, to_f32(draw), bias) : 0.0f;
-      const float v = wave_scan(on ? clamp_log2(s * a2) : 0.0f);
-      const float w = on ? (a.unit ? 1.0f : s) : 0.0f;
-      cs[lane] = v;
-      ec[lane] = fast_exp2(v);
-      ww[lane] = w;
-      wd[lane] = w * fast_exp2(last_lane(v) - v);
-    }
+    xr.store(xs);
+    br.store(bs);
+    cr.store(cm);
     __syncthreads();
     issue(t0 + kHQ);
+    decays(t0 + kHQ, buf ^ 1);
+    issue_step(t0 + 2 * kHQ);
 
     // decayed Gram tiles (rows s of tile J, columns t of tile I), J <= I
 #pragma unroll
@@ -126,7 +164,7 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
         f32x4 G = {0, 0, 0, 0};
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk)
-          G = mma(row_frag(bs, kBP, 16 * J + c, kk, g), row_frag(cm, kBP, 16 * I + c, kk, g), G);
+          G = mma(bs.row(16 * J + c, kk, g), cm.row(16 * I + c, kk, g), G);
         const float ct = cs[16 * I + c];
         const float4 cv = *reinterpret_cast<const float4*>(cs + 16 * J + 4 * g);
         const float4 wv4 = *reinterpret_cast<const float4*>(ww + 16 * J + 4 * g);
@@ -142,7 +180,7 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
 
     Frag<In> xf[2];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) xf[kk] = col_frag(xs, kXP, wv, kk, g, c);
+    for (int kk = 0; kk < 2; ++kk) xf[kk] = xs.col(wv, kk, g, c);
     {
       Frag<In> sf[NK];
 #pragma unroll
@@ -157,13 +195,13 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
       for (int I = 0; I < 4; ++I) {
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) acc = mma(sf[kk], row_frag(cm, kBP, 16 * I + c, kk, g), acc);
+        for (int kk = 0; kk < NK; ++kk) acc = mma(sf[kk], cm.row(16 * I + c, kk, g), acc);
         const int t = 16 * I + c;
         acc *= ec[t];
 #pragma unroll
         for (int kk = 0; kk <= I / 2; ++kk) acc = mma(xf[kk], lane_frag(pf + (I * 2 + kk) * 512, lane), acc);
         float xv[4], o[4];
-        row_four(xs, kXP, t, 4 * wv + g, xv);
+        xs.four(t, 4 * wv + g, xv);
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(dsk, xv[r], acc[r]);
         const int p = 16 * wv + 4 * g;
@@ -203,7 +241,7 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
       Pair<In> xd;
       to_pair(f, xd);
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) S[q] = mma_pair(col_frag(bs, kBP, q, kk, g, c), xd, S[q]);
+      for (int q = 0; q < NQ; ++q) S[q] = mma_pair(bs.col(q, kk, g, c), xd, S[q]);
     }
     __syncthreads();
   }
@@ -220,15 +258,10 @@ __global__ __launch_bounds__(256) void s6_heads_scan_kernel(HeadsArgs a) {
   }
 }
 
-template <typename In, int NT>
-constexpr int scan_lds() {
-  return (int)sizeof(In) * (kHQ * (kTP + kPad) + 2 * kHQ * (NT + kPad) + 4096) + 4 * (4 * kHQ + kTP + 4);
-}
-
 template <typename In, int NT, bool VEC>
 int launch_scan_v(const HeadsArgs& a, const HeadsPlan& p, hipStream_t st) {
   const auto kern = s6_heads_scan_kernel<In, NT, VEC>;
-  constexpr int lds = scan_lds<In, NT>();
+  constexpr int lds = ScanLds<In, NT>::total;
   if constexpr (lds > 65536)
     S6_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds),
            "s6_heads_scan_kernel LDS size");

@@ -8,10 +8,17 @@
 //   k = 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3,
 // which is what two stacked results (rows 0-15 and 16-31) hold per lane.  So a
 // result -- a tile of the state, or of the decayed Gram matrix -- becomes an
-// operand of the next product in registers, without a shuffle.  LDS tiles
-// keep their columns in that order (chunks of four: 0, 4, 1, 5, 2, 6, 3, 7 of
-// each 32), so an operand along a row is one 16-byte read per lane; an operand
-// down a column is read with the transposing LDS read.
+// operand of the next product in registers, without a shuffle.
+//
+// LDS tiles come in two layouts.  RowTile, for operands along its rows: the
+// columns of each 32 lie in the order of K above (chunks of four: 0, 4, 1, 5,
+// 2, 6, 3, 7), so an operand is one 16-byte read per lane, and rows are an odd
+// number of 16-byte units apart, so the 16 rows of a read meet no bank twice.
+// ColTile, for operands down its columns (read with the transposing LDS
+// read: 16 lanes fetch 32 bytes of each of four rows): columns in order, no
+// padding, the 32-byte units of a row XORed with the row's low two bits and
+// the 8-byte chunks of a unit with the next two, so four rows of a unit and 16
+// rows of a chunk each cover all banks.
 //
 // bf16: one 16 x 16 x 32 matrix instruction.  fp32: eight 16 x 16 x 4 ones.
 #ifndef S6_HEADS_KERNEL_H_
@@ -89,62 +96,109 @@ __device__ __forceinline__ f32x4 mma_pair(const Pair<float>& a, const Frag<float
 __device__ __forceinline__ f32x4 mma_pair(const Frag<float>& a, const Pair<float>& b, f32x4 d) { return mma(a, b.hi, d); }
 
 // ------------------------------------------------------------- LDS tiles --
-// Offset of the four-column chunk m (columns 4 m .. 4 m + 3) in a tile row.
-__device__ __forceinline__ int chunk_at(int m) { return (m & ~7) * 4 + ((m & 3) * 2 + ((m >> 2) & 1)) * 4; }
-
-// K = columns 32 kk .. 32 kk + 31 of row `row`.
-__device__ __forceinline__ Frag<uint16_t> row_frag(const uint16_t* t, int pitch, int row, int kk, int g) {
+// Eight consecutive values of LDS as an operand.
+__device__ __forceinline__ Frag<uint16_t> eight(const uint16_t* p) {
   Frag<uint16_t> o;
-  o.v = *reinterpret_cast<const bf16x8*>(t + row * pitch + 32 * kk + 8 * g);
+  o.v = *reinterpret_cast<const bf16x8*>(p);
   return o;
 }
-__device__ __forceinline__ Frag<float> row_frag(const float* t, int pitch, int row, int kk, int g) {
+__device__ __forceinline__ Frag<float> eight(const float* p) {
   Frag<float> o;
-  const float4* p = reinterpret_cast<const float4*>(t + row * pitch + 32 * kk + 8 * g);
-  const float4 x = p[0], y = p[1];
-  o.v[0] = x.x; o.v[1] = x.y; o.v[2] = x.z; o.v[3] = x.w;
-  o.v[4] = y.x; o.v[5] = y.y; o.v[6] = y.z; o.v[7] = y.w;
+  load_vec<float, 8>(p, o.v);
   return o;
 }
-
-// K = rows 32 kk .. 32 kk + 31 of column 16 q + c.  bf16: the transposing
-// read gives each lane four rows of its column, from 8-byte pieces that the
-// 16 lanes of a group fetch (lane i: row i / 4 of the four, chunk i % 4 of the
-// sixteen columns).
-__device__ __forceinline__ Frag<uint16_t> col_frag(const uint16_t* t, int pitch, int q, int kk, int g, int c) {
-  const uint16_t* p = t + (32 * kk + 4 * g + (c >> 2)) * pitch + chunk_at(4 * q + (c & 3));
-  typedef __attribute__((address_space(3))) s16x4* lds4;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uint16_t*)p);
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uint16_t*)(p + 16 * pitch));
+// Four and four.
+__device__ __forceinline__ Frag<uint16_t> four_four(const uint16_t* p, const uint16_t* q) {
+  const s16x4 a = *reinterpret_cast<const s16x4*>(p), b = *reinterpret_cast<const s16x4*>(q);
   Frag<uint16_t> o;
   o.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   return o;
 }
-__device__ __forceinline__ Frag<float> col_frag(const float* t, int pitch, int q, int kk, int g, int c) {
-  const float* p = t + (32 * kk + 4 * g) * pitch + chunk_at(4 * q + (c >> 2)) + (c & 3);
+__device__ __forceinline__ Frag<float> four_four(const float* p, const float* q) {
   Frag<float> o;
+  float a[4], b[4];
+  load_vec<float, 4>(p, a);
+  load_vec<float, 4>(q, b);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    o.v[j] = p[j * pitch];
-    o.v[4 + j] = p[(16 + j) * pitch];
-  }
+  for (int j = 0; j < 4; ++j) { o.v[j] = a[j]; o.v[4 + j] = b[j]; }
+  return o;
+}
+// Rows r0 .. r0 + 3 and r0 + 16 .. r0 + 19 (r0 = 4 g of the group) of one column.
+// bf16: the transposing read gives each lane four rows of its column, from
+// 8-byte chunks that the 16 lanes of a group fetch (lane c: row c / 4 of the
+// four, chunk c % 4 of the sixteen columns); `p` is the lane's chunk, `d` the
+// distance of 16 rows.
+__device__ __forceinline__ Frag<uint16_t> tr_read(const uint16_t* p, int d) {
+  typedef __attribute__((address_space(3))) s16x4* lds4;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uint16_t*)p);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uint16_t*)(p + d));
+  Frag<uint16_t> o;
+  o.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   return o;
 }
 
-// Four columns 4 m .. 4 m + 3 of a row as floats.
-template <typename In>
-__device__ __forceinline__ void row_four(const In* t, int pitch, int row, int m, float (&f)[4]) {
-  load_vec<In, 4>(t + row * pitch + chunk_at(m), f);
-}
+// A tile of COLS columns, for operands along its rows.
+template <typename In, int COLS>
+struct RowTile {
+  static constexpr int kPitch = COLS + kPad;
+  static constexpr int size(int rows) { return rows * kPitch; }
+  In* t;
+  // chunk m: columns 4 m .. 4 m + 3
+  static __device__ __forceinline__ int at(int row, int m) {
+    return row * kPitch + (m & ~7) * 4 + ((m & 3) * 2 + ((m >> 2) & 1)) * 4;
+  }
+  // K = columns 32 kk .. + 31 of a row
+  __device__ __forceinline__ Frag<In> row(int r, int kk, int g) const { return eight(t + r * kPitch + 32 * kk + 8 * g); }
+  // K = rows 32 kk .. + 31 of column 16 q + c
+  __device__ __forceinline__ Frag<In> col(int q, int kk, int g, int c) const {
+    if constexpr (sizeof(In) == 2) {
+      return tr_read(t + at(32 * kk + 4 * g + (c >> 2), 4 * q + (c & 3)), 16 * kPitch);
+    } else {
+      Frag<In> o;
+      const In* p = t + at(32 * kk + 4 * g, 4 * q + (c >> 2)) + (c & 3);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { o.v[j] = p[j * kPitch]; o.v[4 + j] = p[(16 + j) * kPitch]; }
+      return o;
+    }
+  }
+  // columns 4 m .. 4 m + 3 of a row as floats
+  __device__ __forceinline__ void four(int r, int m, float (&f)[4]) const { load_vec<In, 4>(t + at(r, m), f); }
+};
+
+// A tile of COLS columns, for operands down its columns.
+template <typename In, int COLS>
+struct ColTile {
+  static constexpr int kPitch = COLS;
+  static constexpr int size(int rows) { return rows * kPitch; }
+  In* t;
+  static __device__ __forceinline__ int at(int row, int m) {
+    const int x = COLS >= 64 ? row & 3 : (row >> 1) & 1;
+    return row * COLS + 4 * (4 * ((m >> 2) ^ x) + ((m & 3) ^ ((row >> 2) & 3)));
+  }
+  __device__ __forceinline__ Frag<In> row(int r, int kk, int g) const {
+    return four_four(t + at(r, 8 * kk + g), t + at(r, 8 * kk + 4 + g));
+  }
+  __device__ __forceinline__ Frag<In> col(int q, int kk, int g, int c) const {
+    if constexpr (sizeof(In) == 2) {
+      return tr_read(t + at(32 * kk + 4 * g + (c >> 2), 4 * q + (c & 3)), 16 * COLS);
+    } else {
+      Frag<In> o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const In* p = t + at(32 * kk + 4 * g + j, 4 * q + (c >> 2)) + (c & 3);
+        o.v[j] = p[0];
+        o.v[4 + j] = p[16 * COLS];
+      }
+      return o;
+    }
+  }
+  __device__ __forceinline__ void four(int r, int m, float (&f)[4]) const { load_vec<In, 4>(t + at(r, m), f); }
+};
 
 // An operand kept in LDS as such: 8 values per lane.
-__device__ __forceinline__ Frag<uint16_t> lane_frag(const uint16_t* p, int lane) {
-  Frag<uint16_t> o;
-  o.v = *reinterpret_cast<const bf16x8*>(p + 8 * lane);
-  return o;
-}
-__device__ __forceinline__ Frag<float> lane_frag(const float* p, int lane) {
-  return row_frag(p + 8 * lane, 0, 0, 0, 0);
+template <typename In>
+__device__ __forceinline__ Frag<In> lane_frag(const In* p, int lane) {
+  return eight(p + 8 * lane);
 }
 
 // -------------------------------------------- global to LDS, by registers --
@@ -154,7 +208,11 @@ struct Piece;
 template <>
 struct Piece<uint16_t> {
   uint4 v;
-  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  // the first n values stay, the others become 0
+  __device__ __forceinline__ void keep(int n) {
+    auto part = [&](uint32_t w, int i) { return w & (n >= 2 * i + 2 ? ~0u : n == 2 * i + 1 ? 0xffffu : 0u); };
+    v = make_uint4(part(v.x, 0), part(v.y, 1), part(v.z, 2), part(v.w, 3));
+  }
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void set(const uint16_t (&e)[8]) {
     v = make_uint4(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16), e[4] | ((uint32_t)e[5] << 16),
@@ -165,9 +223,20 @@ struct Piece<uint16_t> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) { e[2 * j] = (uint16_t)w[j]; e[2 * j + 1] = (uint16_t)(w[j] >> 16); }
   }
-  __device__ __forceinline__ void store(uint16_t* row, int i) const {
-    *reinterpret_cast<uint2*>(row + chunk_at(2 * i)) = make_uint2(v.x, v.y);
-    *reinterpret_cast<uint2*>(row + chunk_at(2 * i + 1)) = make_uint2(v.z, v.w);
+  // columns 8 i .. 8 i + 7 of a tile row
+  template <int COLS>
+  __device__ __forceinline__ void put(const RowTile<uint16_t, COLS>& d, int row, int i) const {
+    *reinterpret_cast<uint2*>(d.t + d.at(row, 2 * i)) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(d.t + d.at(row, 2 * i + 1)) = make_uint2(v.z, v.w);
+  }
+  template <int COLS>
+  __device__ __forceinline__ void put(const ColTile<uint16_t, COLS>& d, int row, int i) const {
+    // the two chunks are neighbours, in the order that bit 2 of the row says
+    // (a swap by XOR: a select of the halves becomes one of addresses, which
+    // sends the whole tile through scratch memory)
+    const uint32_t m = 0u - (uint32_t)((row >> 2) & 1);
+    const uint32_t a = (v.x ^ v.z) & m, b = (v.y ^ v.w) & m;
+    *reinterpret_cast<uint4*>(d.t + (d.at(row, 2 * i) & ~7)) = make_uint4(v.x ^ a, v.y ^ b, v.z ^ a, v.w ^ b);
   }
   // an exponent of all ones somewhere: adding 1 to it carries into the sign
   __device__ __forceinline__ bool nonfinite() const {
@@ -179,7 +248,10 @@ struct Piece<uint16_t> {
 template <>
 struct Piece<float> {
   float4 a, b;
-  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ void keep(int n) {
+    a = make_float4(n > 0 ? a.x : 0.0f, n > 1 ? a.y : 0.0f, n > 2 ? a.z : 0.0f, n > 3 ? a.w : 0.0f);
+    b = make_float4(n > 4 ? b.x : 0.0f, n > 5 ? b.y : 0.0f, n > 6 ? b.z : 0.0f, n > 7 ? b.w : 0.0f);
+  }
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
@@ -191,9 +263,10 @@ struct Piece<float> {
   __device__ __forceinline__ void get(float (&e)[8]) const {
     e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w; e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
   }
-  __device__ __forceinline__ void store(float* row, int i) const {
-    *reinterpret_cast<float4*>(row + chunk_at(2 * i)) = a;
-    *reinterpret_cast<float4*>(row + chunk_at(2 * i + 1)) = b;
+  template <typename Tile>
+  __device__ __forceinline__ void put(const Tile& d, int row, int i) const {
+    *reinterpret_cast<float4*>(d.t + d.at(row, 2 * i)) = a;
+    *reinterpret_cast<float4*>(d.t + d.at(row, 2 * i + 1)) = b;
   }
   static __device__ __forceinline__ bool bad(float e) { return (__float_as_uint(e) & 0x7f800000u) == 0x7f800000u; }
   __device__ __forceinline__ bool nonfinite() const {
@@ -202,42 +275,47 @@ struct Piece<float> {
 };
 
 // A ROWS x COLS tile through the registers of THREADS threads: load() issues
-// the global loads (rows past the sequence and columns past the width are
-// zero), store() writes the LDS tile.  VEC: 16-byte loads (rows 16-byte
-// aligned, width a multiple of 8).
+// the global loads, mask() zeroes what lies past the sequence or the width,
+// store() writes the LDS tile.  VEC: 16-byte loads (rows 16-byte aligned, width
+// a multiple of 8); their addresses are held inside the tensor instead of
+// skipped, so that a full tile takes no branches.
 template <typename In, int ROWS, int COLS, int THREADS, bool VEC>
 struct TileRegs {
   static constexpr int kPer = COLS / 8;                       // pieces of a row
   static constexpr int kN = (ROWS * kPer + THREADS - 1) / THREADS;
   Piece<In> r[kN];
-  // base: row 0, column 0 of the tile; `rows` of it are in the sequence and
-  // `cols` columns are in the width
+  static __device__ __forceinline__ int row_of(int k) { return (k * THREADS + (int)threadIdx.x) / kPer; }
+  static __device__ __forceinline__ int col_of(int k) { return (k * THREADS + (int)threadIdx.x) % kPer * 8; }
+  // base: row 0, column 0 of the tile; `rows` of it are in the sequence (0:
+  // nothing is loaded) and `cols` >= 1 columns are in the width
   __device__ __forceinline__ void load(const In* base, int64_t stride, int rows, int cols) {
+    if (rows == 0) return;
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int id = k * THREADS + threadIdx.x;
-      const int row = id / kPer, col = (id % kPer) * 8;
-      r[k].zero();
-      if (row < rows && row < ROWS) {
-        const In* p = base + (int64_t)row * stride + col;
-        if constexpr (VEC) {
-          if (col < cols) r[k].load(p);
-        } else {
-          In e[8];
+      int row = row_of(k), col = col_of(k);
+      row = row < rows ? row : rows - 1;
+      if constexpr (VEC) {
+        col = col < cols ? col : cols - 8;
+        r[k].load(base + (int64_t)row * stride + col);
+      } else {
+        const In* p = base + (int64_t)row * stride;
+        In e[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] = col + j < cols ? p[j] : In(0);
-          r[k].set(e);
-        }
+        for (int j = 0; j < 8; ++j) e[j] = p[col + j < cols ? col + j : cols - 1];
+        r[k].set(e);
       }
     }
   }
-  __device__ __forceinline__ void store(In* tile, int pitch) const {
+  __device__ __forceinline__ void mask(int rows, int cols) {
+    if (rows >= ROWS && cols >= COLS) return;
 #pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      const int id = k * THREADS + threadIdx.x;
-      const int row = id / kPer;
-      if (ROWS * kPer % THREADS == 0 || row < ROWS) r[k].store(tile + row * pitch, id % kPer);
-    }
+    for (int k = 0; k < kN; ++k) r[k].keep(row_of(k) < rows ? cols - col_of(k) : 0);
+  }
+  template <typename Tile>
+  __device__ __forceinline__ void store(const Tile& tile) const {
+#pragma unroll
+    for (int k = 0; k < kN; ++k)
+      if (ROWS * kPer % THREADS == 0 || row_of(k) < ROWS) r[k].put(tile, row_of(k), col_of(k) / 8);
   }
   // Values that are not finite become 0; first[column] receives the first
   // row that held one, *any is set.  Returns whether there was one.
@@ -245,14 +323,13 @@ struct TileRegs {
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
       if (r[k].nonfinite()) {
-        const int id = k * THREADS + threadIdx.x;
         In e[8];
         r[k].get(e);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (Piece<In>::bad(e[j])) {
             e[j] = In(0);
-            atomicMin(first + (id % kPer) * 8 + j, id / kPer);
+            atomicMin(first + col_of(k) + j, row_of(k));
           }
         r[k].set(e);
         *any = 1;

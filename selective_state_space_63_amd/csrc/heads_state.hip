@@ -24,18 +24,22 @@ template <typename In>
 constexpr int kBlockTokens = sizeof(In) == 2 ? 128 : 64;
 
 template <typename In, int NT, bool VEC>
-__global__ __launch_bounds__(256) void s6_heads_state_kernel(HeadsArgs a, int mode) {
-  constexpr int kXP = kTP + kPad, kBP = NT + kPad;
+__global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 4 : 2) : 1) void s6_heads_state_kernel(HeadsArgs a, int mode) {
   constexpr int NW = NT / 32;  // state tiles of 16 columns per wave and channel tile
-  __shared__ __align__(16) In xs[kHQ * kXP];
-  __shared__ __align__(16) In bs[kHQ * kBP];
+  using XT = ColTile<In, kTP>;
+  using BT = ColTile<In, NT>;
+  __shared__ __align__(16) In xmem[XT::size(kHQ)];
+  __shared__ __align__(16) In bmem[BT::size(kHQ)];
+  const XT xs{xmem};
+  const BT bs{bmem};
   __shared__ __align__(16) float wt[kHQ];
   __shared__ float total_s;
   const HeadRow hr = head_row(a, blockIdx.x);
   const int64_t nrows = gridDim.x;
   const int dir = blockIdx.z;
   const int64_t seg = mode == 0 && dir ? blockIdx.y + 1 : blockIdx.y;
-  const int lane = threadIdx.x & 63, wv = wave_index(), g = lane >> 4, c = lane & 15;
+  const int lane0 = threadIdx.x & 63, wv = wave_index();
+  int lane = lane0, g = lane >> 4, c = lane & 15;
   const int pp = wv & 1, nh = wv >> 1;
   const int p0 = hr.pt * kTP, pleft = a.headdim - p0;
   const int64_t t_lo = seg * a.seg_len;
@@ -97,6 +101,9 @@ __global__ __launch_bounds__(256) void s6_heads_state_kernel(HeadsArgs a, int mo
   for (int64_t i = 0, k = first; i < nch; ++i, k += step) {
     const int64_t t0 = t_lo + k * kHQ;
     const int rows = (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ);
+    lane = lane0;  // LDS addresses are formed again in every turn, which leaves room for a fourth workgroup per CU
+    asm volatile("" : "+v"(lane));
+    g = lane >> 4; c = lane & 15;
     // the state entering a stored block, from its near end
     const bool enter = dir ? ((k + 1) % kPerBlock == 0 || k == nch - 1) : k % kPerBlock == 0;
     if (mode == 1 && a.planes && enter) {
@@ -120,8 +127,10 @@ __global__ __launch_bounds__(256) void s6_heads_state_kernel(HeadsArgs a, int mo
         }
       }
     }
-    xr.store(xs, kXP);
-    br.store(bs, kBP);
+    xr.mask(rows, pleft < kTP ? pleft : kTP);
+    br.mask(rows, a.dstate);
+    xr.store(xs);
+    br.store(bs);
     if (wv == 0) {
       const bool on = lane < rows;
       const float s = on ? step_of(a, to_f32(draw), bias) : 0.0f;
@@ -148,7 +157,7 @@ __global__ __launch_bounds__(256) void s6_heads_state_kernel(HeadsArgs a, int mo
       Pair<In> xd[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const Frag<In> xf = col_frag(xs, kXP, 2 * pp + j, kk, g, c);
+        const Frag<In> xf = xs.col(2 * pp + j, kk, g, c);
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = frag_f32(xf, e) * w[e];
@@ -156,7 +165,7 @@ __global__ __launch_bounds__(256) void s6_heads_state_kernel(HeadsArgs a, int mo
       }
 #pragma unroll
       for (int q = 0; q < NW; ++q) {
-        const Frag<In> bf = col_frag(bs, kBP, nh * NW + q, kk, g, c);
+        const Frag<In> bf = bs.col(nh * NW + q, kk, g, c);
 #pragma unroll
         for (int j = 0; j < 2; ++j) T[q][j] = mma_pair(xd[j], bf, T[q][j]);
       }
