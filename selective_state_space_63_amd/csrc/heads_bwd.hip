@@ -166,6 +166,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   __syncthreads();
 
   // Gram tiles of this wave (rows t of tile I, columns s of tile J <= I)
+  const int b_row = O::BT::row_lane(g, c);
   int tI[SLOTS], tJ[SLOTS];
   f32x4 CB[SLOTS], P[SLOTS];
 #pragma unroll
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
     if (n < O::NTILE) {
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk)
-        CB[k] = mma(cm.row(16 * I + c, kk, g), bs.row(16 * tJ[k] + c, kk, g), CB[k]);
+        CB[k] = mma(cm.row(b_row, 16 * I, kk), bs.row(b_row, 16 * tJ[k], kk), CB[k]);
     }
   }
   f32x4 dC[TT], dB[TT];
@@ -202,6 +203,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       lane = lane0;
       asm volatile("" : "+v"(lane));
       g = lane >> 4; c = lane & 15;
+      const int x_row = O::XT::row_lane(g, c), b_row = O::BT::row_lane(g, c);
       const int p0 = pt * kTP, pleft = a.headdim - p0;
       xr.mask(rows, pleft < kTP ? pleft : kTP);
       yr.mask(rows, pleft < kTP ? pleft : kTP);
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
           f32x4 X = {0, 0, 0, 0};
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
-            X = mma(ys.row(16 * I + c, kk, g), xs.row(16 * J + c, kk, g), X);
+            X = mma(ys.row(x_row, 16 * I, kk), xs.row(x_row, 16 * J, kk), X);
           const float4 ct4 = *reinterpret_cast<const float4*>(cs + 16 * I + 4 * g);
           const float ct[4] = {ct4.x, ct4.y, ct4.z, ct4.w};
           const float cj = cs[16 * J + c], wj = ww[16 * J + c];
@@ -318,8 +320,8 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
         f32x4 U = {0, 0, 0, 0}, V = {0, 0, 0, 0};
 #pragma unroll
         for (int pp = 0; pp < 2; ++pp) {
-          U = mma_pair(Sf[pp], ys.row(t, pp, g), U);
-          V = mma_pair(Lf[pp], xs.row(t, pp, g), V);
+          U = mma_pair(Sf[pp], ys.row(x_row, t - c, pp), U);
+          V = mma_pair(Lf[pp], xs.row(x_row, t - c, pp), V);
         }
         float cv[4], bv[4], sy = 0.0f, su = 0.0f;
         cm.four(t, 4 * ns + g, cv);
@@ -344,9 +346,10 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       // dx, transposed: channels of tile q, tokens of tiles J
       {
         const int q = wv & 3;
+        const auto l_col = O::LT::col_lane(g, c);
         Frag<In> lq[NK], yq[H];
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) lq[kk] = lm.col(q, kk, g, c);
+        for (int kk = 0; kk < NK; ++kk) lq[kk] = lm.col(l_col, q, kk, g, c);
 #pragma unroll
         for (int kk = 0; kk < H; ++kk) yq[kk] = ys.col(q, kk, g, c);
         const int p = 16 * q + 4 * g;
@@ -355,7 +358,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
           const int J = 2 * i + (wv >> 2), s = 16 * J + c;
           f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-          for (int kk = 0; kk < NK; ++kk) acc = mma(lq[kk], bs.row(s, kk, g), acc);
+          for (int kk = 0; kk < NK; ++kk) acc = mma(lq[kk], bs.row(b_row, 16 * J, kk), acc);
           acc *= ww[s] * wd[s];
 #pragma unroll
           for (int kk = i; kk < H; ++kk) acc = mma(yq[kk], lane_frag(mf + frag_at<H>(J, kk) * 512, lane), acc);
@@ -467,11 +470,12 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       for (int r = 0; r < 4; ++r) pm.t[pm.at(32 * wv + 4 * g + r, 4 * (2 * wv + 1) + (c >> 2)) + (c & 3)] = In(0);
     }
     __syncthreads();
+    const int p_row = O::PT::row_lane(g, c);
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       const int it = tp * TT + i;
       for (int kk = 0; kk <= it / 2; ++kk)
-        dC[i] = mma(bs.col(ns, kk, g, c), pm.row(16 * it + c, kk, g), dC[i]);
+        dC[i] = mma(bs.col(ns, kk, g, c), pm.row(p_row, 16 * it, kk), dC[i]);
       for (int kk = it / 2; kk < H; ++kk)
         dB[i] = mma(cm.col(ns, kk, g, c), pm.col(it, kk, g, c), dB[i]);
     }

@@ -56,8 +56,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   const int64_t rid = nrows % 8 == 0 ? (blockIdx.x % 8) * (nrows / 8) + blockIdx.x / 8 : blockIdx.x;
   const HeadRow hr = head_row(a, rid);
   const int64_t seg = blockIdx.y;
-  const int lane0 = threadIdx.x & 63, wv = wave_index();
-  int lane = lane0, g = lane >> 4, c = lane & 15;
+  const int lane = threadIdx.x & 63, wv = wave_index(), g = lane >> 4, c = lane & 15;
   const int p0 = hr.pt * kTP, pleft = a.headdim - p0;
   const int64_t t_lo = seg * a.seg_len;
   const int64_t t_hi = t_lo + a.seg_len < a.L ? t_lo + a.seg_len : a.L;
@@ -129,13 +128,15 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   issue_step(t_lo + kHQ);
   __syncthreads();
   int buf = 0;
+  const uint32_t y_off = ((uint32_t)c * (uint32_t)hp + 16 * wv + 4 * g) * (uint32_t)sizeof(In);
+  // lane parts of the LDS addresses; x's column tile is the wave's own
+  int b_row = L::BT::row_lane(g, c), b_col = L::BT::col_lane(g, c), c_row = L::CT::row_lane(g, c);
+  const int x_col = L::XT::col_lane(g, c);
   for (int64_t t0 = t_lo; t0 < t_hi; t0 += kHQ, buf ^= 1) {
     const int rows = rows_at(t0);
-    // LDS addresses are formed again in every turn: kept across it they would
+    // the units' XORs are done in every turn: their results kept over it would
     // cost a workgroup per CU
-    lane = lane0;
-    asm volatile("" : "+v"(lane));
-    g = lane >> 4; c = lane & 15;
+    asm volatile("" : "+v"(b_row), "+v"(b_col), "+v"(c_row));
     const float* cs = tok + buf * 4 * kHQ;
     const float *ec = cs + kHQ, *ww = cs + 2 * kHQ, *wd = cs + 3 * kHQ;
     // An input that is not finite would reach earlier tokens through the
@@ -158,13 +159,15 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const int id = 4 * k + wv;
-      if (id < 10) {
-        const int I = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0;
+      if (k < 2 || id < 10) {
+        int I = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0;
+        I = __builtin_amdgcn_readfirstlane(I);
+        asm volatile("" : "+s"(I));  // addresses of the tile are formed here, not kept over the loop
         const int J = id - I * (I + 1) / 2;
         f32x4 G = {0, 0, 0, 0};
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk)
-          G = mma(bs.row(16 * J + c, kk, g), cm.row(16 * I + c, kk, g), G);
+          G = mma(bs.row(b_row, 16 * J, kk), cm.row(c_row, 16 * I, kk), G);
         const float ct = cs[16 * I + c];
         const float4 cv = *reinterpret_cast<const float4*>(cs + 16 * J + 4 * g);
         const float4 wv4 = *reinterpret_cast<const float4*>(ww + 16 * J + 4 * g);
@@ -180,7 +183,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
 
     Frag<In> xf[2];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) xf[kk] = xs.col(wv, kk, g, c);
+    for (int kk = 0; kk < 2; ++kk) xf[kk] = xs.col(x_col, wv, kk, g, c);
     {
       Frag<In> sf[NK];
 #pragma unroll
@@ -191,33 +194,43 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
         to_frag(f, sf[kk]);  // bf16: y is rounded to bf16 anyway
       }
       const bool dirty = *any != 0;
+      float o[4][4];
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) acc = mma(sf[kk], cm.row(16 * I + c, kk, g), acc);
-        const int t = 16 * I + c;
-        acc *= ec[t];
+        for (int kk = 0; kk < NK; ++kk) acc = mma(sf[kk], cm.row(c_row, 16 * I, kk), acc);
+        acc *= ec[16 * I + c];
 #pragma unroll
         for (int kk = 0; kk <= I / 2; ++kk) acc = mma(xf[kk], lane_frag(pf + (I * 2 + kk) * 512, lane), acc);
-        float xv[4], o[4];
-        xs.four(t, 4 * wv + g, xv);
+        float xv[4];
+        xs.four(16 * I + c, 4 * wv + g, xv);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(dsk, xv[r], acc[r]);
-        const int p = 16 * wv + 4 * g;
-        if (dirty) {
+        for (int r = 0; r < 4; ++r) o[I][r] = __builtin_fmaf(dsk, xv[r], acc[r]);
+      }
+      const int p = 16 * wv + 4 * g;
+      if (dirty) {
+#pragma unroll
+        for (int I = 0; I < 4; ++I)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (t >= bad[p + r]) o[r] = __builtin_nanf("");
-        }
-        if (t < rows) {
-          In* yp = Y + (t0 + t) * hp + p;
+            if (16 * I + c >= bad[p + r]) o[I][r] = __builtin_nanf("");
+      }
+      const bool full = VEC && rows == kHQ && pleft >= kTP;
+#pragma unroll
+      for (int I = 0; I < 4; ++I) {
+        char* yb = reinterpret_cast<char*>(Y + (t0 + 16 * I) * hp);
+        asm volatile("" : "+s"(yb));
+        In* yp = reinterpret_cast<In*>(yb + y_off);
+        if (full) {
+          store_vec<In, 4>(yp, o[I]);
+        } else if (16 * I + c < rows) {
           if constexpr (VEC) {
-            if (p < pleft) store_vec<In, 4>(yp, o);
+            if (p < pleft) store_vec<In, 4>(yp, o[I]);
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              if (p + r < pleft) yp[r] = from_f32<In>(o[r]);
+              if (p + r < pleft) yp[r] = from_f32<In>(o[I][r]);
           }
         }
       }
@@ -241,7 +254,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
       Pair<In> xd;
       to_pair(f, xd);
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) S[q] = mma_pair(bs.col(q, kk, g, c), xd, S[q]);
+      for (int q = 0; q < NQ; ++q) S[q] = mma_pair(bs.col(b_col, q, kk, g, c), xd, S[q]);
     }
     __syncthreads();
   }
@@ -310,6 +323,9 @@ HeadsPlan heads_plan(const s6_heads_dims& d, int in_dtype, const void* x, const 
   p.vec = d.headdim % 8 == 0 && d.dstate % 8 == 0 && d.x_batch % u == 0 && d.x_token % u == 0 && d.b_batch % u == 0 &&
           d.b_token % u == 0 && d.c_batch % u == 0 && d.c_token % u == 0 && aligned(x, 16) && aligned(Bm, 16) &&
           aligned(Cm, 16) && aligned(dy, 16);
+  // offsets within a tile of up to 128 rows in 32 bits
+  const int64_t strides[] = {d.x_token, d.b_token, d.c_token};
+  for (int64_t s : strides) p.vec = p.vec && s < (int64_t(1) << 31) / (128 * 4);
   return p;
 }
 

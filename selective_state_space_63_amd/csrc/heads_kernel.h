@@ -10,15 +10,17 @@
 // result -- a tile of the state, or of the decayed Gram matrix -- becomes an
 // operand of the next product in registers, without a shuffle.
 //
-// LDS tiles come in two layouts.  RowTile, for operands along its rows: the
-// columns of each 32 lie in the order of K above (chunks of four: 0, 4, 1, 5,
-// 2, 6, 3, 7), so an operand is one 16-byte read per lane, and rows are an odd
-// number of 16-byte units apart, so the 16 rows of a read meet no bank twice.
-// ColTile, for operands down its columns (read with the transposing LDS
-// read: 16 lanes fetch 32 bytes of each of four rows): columns in order, no
-// padding, the 32-byte units of a row XORed with the row's low two bits and
-// the 8-byte chunks of a unit with the next two, so four rows of a unit and 16
-// rows of a chunk each cover all banks.
+// LDS tiles come in two layouts, both without padding.  RowTile, for operands
+// along its rows: the columns of each 32 lie in the order of K above (chunks of
+// four: 0, 4, 1, 5, 2, 6, 3, 7), so an operand is one 16-byte read per lane.
+// ColTile, for operands down its columns (read with the transposing LDS read:
+// 16 lanes fetch 32 bytes of each of four rows): columns in order.  The
+// 16-byte (RowTile) or 32-byte units of a row are XORed with bits of the row
+// so that no read meets a bank twice.  Measured with SQ_LDS_BANK_CONFLICT on
+// each access alone (cycles per instruction, bf16): a 16-byte read takes 4
+// when lanes 0-3, 12-15, 20-27 cover all 64 banks (and the three like sets),
+// an 8-byte or transposing read 2 when lanes 0-31 do; writes take 16 lanes of
+// 8 bytes or 8 of 16 over 32 banks per cycle.
 //
 // bf16: one 16 x 16 x 32 matrix instruction.  fp32: eight 16 x 16 x 4 ones.
 #ifndef S6_HEADS_KERNEL_H_
@@ -33,7 +35,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTP = 64;      // channels of a head per workgroup (a wider head is several tiles)
 constexpr int kHQ = 64;      // tokens per chunk of the scan
-constexpr int kPad = 8;      // LDS row padding in elements (rows an odd number of 16-byte units apart)
 
 template <typename In>
 struct Frag;
@@ -137,27 +138,41 @@ __device__ __forceinline__ Frag<uint16_t> tr_read(const uint16_t* p, int d) {
   return o;
 }
 
-// A tile of COLS columns, for operands along its rows.
+// A tile of COLS columns, for operands along its rows.  An address is a
+// lane's part XORed with the unit; `lane` below is that part.
 template <typename In, int COLS>
 struct RowTile {
-  static constexpr int kPitch = COLS + kPad;
-  static constexpr int size(int rows) { return rows * kPitch; }
+  static constexpr int size(int rows) { return rows * COLS; }
+  static constexpr int kU = COLS / 8;  // units of 8 columns
+  static_assert(kU == 4 || kU == 8 || kU == 16, "the rows' XOR");
   In* t;
+  static __device__ __forceinline__ int mix(int row) {
+    if constexpr (kU == 16) return row & 15;
+    if constexpr (kU == 8) return ((row >> 1) & 7) ^ (row & 1);
+    // 0, 2, 3, 1: two neighbours' units and the other two's, XORed with 1, are all four
+    return ((row >> 2) & 1) * 2 ^ ((row >> 3) & 1) * 3;
+  }
   // chunk m: columns 4 m .. 4 m + 3
   static __device__ __forceinline__ int at(int row, int m) {
-    return row * kPitch + (m & ~7) * 4 + ((m & 3) * 2 + ((m >> 2) & 1)) * 4;
+    return row * COLS + 8 * ((((m & ~7) >> 1) + (m & 3)) ^ mix(row)) + 4 * ((m >> 2) & 1);
   }
-  // K = columns 32 kk .. + 31 of a row
-  __device__ __forceinline__ Frag<In> row(int r, int kk, int g) const { return eight(t + r * kPitch + 32 * kk + 8 * g); }
+  static __device__ __forceinline__ int row_lane(int g, int c) { return c * COLS + 8 * (g ^ mix(c)); }
+  // K = columns 32 kk .. + 31 of row r + c (r a multiple of 16)
+  __device__ __forceinline__ Frag<In> row(int lane, int r, int kk) const {
+    return eight(t + (lane ^ (32 * kk)) + r * COLS);
+  }
   // K = rows 32 kk .. + 31 of column 16 q + c
   __device__ __forceinline__ Frag<In> col(int q, int kk, int g, int c) const {
     if constexpr (sizeof(In) == 2) {
-      return tr_read(t + at(32 * kk + 4 * g + (c >> 2), 4 * q + (c & 3)), 16 * kPitch);
+      return tr_read(t + at(4 * g + (c >> 2), 4 * q + (c & 3)) + 32 * kk * COLS, 16 * COLS);
     } else {
       Frag<In> o;
-      const In* p = t + at(32 * kk + 4 * g, 4 * q + (c >> 2)) + (c & 3);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) { o.v[j] = p[j * kPitch]; o.v[4 + j] = p[(16 + j) * kPitch]; }
+      for (int j = 0; j < 4; ++j) {
+        const In* p = t + at(32 * kk + 4 * g + j, 4 * q + (c >> 2)) + (c & 3);
+        o.v[j] = p[0];
+        o.v[4 + j] = p[16 * COLS];
+      }
       return o;
     }
   }
@@ -168,19 +183,24 @@ struct RowTile {
 // A tile of COLS columns, for operands down its columns.
 template <typename In, int COLS>
 struct ColTile {
-  static constexpr int kPitch = COLS;
-  static constexpr int size(int rows) { return rows * kPitch; }
+  static constexpr int size(int rows) { return rows * COLS; }
   In* t;
+  static __device__ __forceinline__ int mix(int row) {  // of the units of 16 columns
+    return COLS >= 128 ? row & 7 : COLS >= 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+  }
   static __device__ __forceinline__ int at(int row, int m) {
-    const int x = COLS >= 64 ? row & 3 : (row >> 1) & 1;
-    return row * COLS + 4 * (4 * ((m >> 2) ^ x) + ((m & 3) ^ ((row >> 2) & 3)));
+    return row * COLS + 16 * ((m >> 2) ^ mix(row)) + 4 * ((m & 3) ^ (2 * ((row >> 3) & 1)));
   }
-  __device__ __forceinline__ Frag<In> row(int r, int kk, int g) const {
-    return four_four(t + at(r, 8 * kk + g), t + at(r, 8 * kk + 4 + g));
+  static __device__ __forceinline__ int row_lane(int g, int c) { return at(c, g); }
+  static __device__ __forceinline__ int col_lane(int g, int c) { return at(4 * g + (c >> 2), c & 3); }
+  // K = columns 32 kk .. + 31 of row r + c (r a multiple of 16)
+  __device__ __forceinline__ Frag<In> row(int lane, int r, int kk) const {
+    return four_four(t + (lane ^ (32 * kk)) + r * COLS, t + (lane ^ (32 * kk + 16)) + r * COLS);
   }
-  __device__ __forceinline__ Frag<In> col(int q, int kk, int g, int c) const {
+  // K = rows 32 kk .. + 31 of column 16 q + c
+  __device__ __forceinline__ Frag<In> col(int lane, int q, int kk, int g, int c) const {
     if constexpr (sizeof(In) == 2) {
-      return tr_read(t + at(32 * kk + 4 * g + (c >> 2), 4 * q + (c & 3)), 16 * COLS);
+      return tr_read(t + (lane ^ (16 * q)) + 32 * kk * COLS, 16 * COLS);
     } else {
       Frag<In> o;
 #pragma unroll
@@ -231,12 +251,7 @@ struct Piece<uint16_t> {
   }
   template <int COLS>
   __device__ __forceinline__ void put(const ColTile<uint16_t, COLS>& d, int row, int i) const {
-    // the two chunks are neighbours, in the order that bit 2 of the row says
-    // (a swap by XOR: a select of the halves becomes one of addresses, which
-    // sends the whole tile through scratch memory)
-    const uint32_t m = 0u - (uint32_t)((row >> 2) & 1);
-    const uint32_t a = (v.x ^ v.z) & m, b = (v.y ^ v.w) & m;
-    *reinterpret_cast<uint4*>(d.t + (d.at(row, 2 * i) & ~7)) = make_uint4(v.x ^ a, v.y ^ b, v.z ^ a, v.w ^ b);
+    *reinterpret_cast<uint4*>(d.t + d.at(row, 2 * i)) = v;
   }
   // an exponent of all ones somewhere: adding 1 to it carries into the sign
   __device__ __forceinline__ bool nonfinite() const {
@@ -284,15 +299,45 @@ struct TileRegs {
   static constexpr int kPer = COLS / 8;                       // pieces of a row
   static constexpr int kN = (ROWS * kPer + THREADS - 1) / THREADS;
   Piece<In> r[kN];
-  static __device__ __forceinline__ int row_of(int k) { return (k * THREADS + (int)threadIdx.x) / kPer; }
-  static __device__ __forceinline__ int col_of(int k) { return (k * THREADS + (int)threadIdx.x) % kPer * 8; }
+  static_assert(THREADS % kPer == 0, "a thread keeps its columns");
+  // Rows of 16 pieces are taken as two halves, so that 16 lanes write halves of
+  // two rows (a RowTile's 8-byte writes then meet no bank twice).
+  static __device__ __forceinline__ int row_of(int k, int tid = threadIdx.x) {
+    const int r = kPer == 16 ? (tid >> 5) * 2 + ((tid >> 3) & 1) : tid / kPer;
+    return r + k * (THREADS / kPer);
+  }
+  static __device__ __forceinline__ int col_of(int tid = threadIdx.x) {
+    return (kPer == 16 ? (tid & 7) + ((tid >> 4) & 1) * 8 : tid % kPer) * 8;
+  }
+  // The thread's index as a value formed here: what is rarely needed is then
+  // not kept in registers over a loop.
+  static __device__ __forceinline__ int fresh_tid() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+  }
   // base: row 0, column 0 of the tile; `rows` of it are in the sequence (0:
-  // nothing is loaded) and `cols` >= 1 columns are in the width
+  // nothing is loaded) and `cols` >= 1 columns are in the width.  A whole tile
+  // is loaded from scalar bases and one 32-bit offset of the thread (the host
+  // sends strides for which it would not fit to the other form).
   __device__ __forceinline__ void load(const In* base, int64_t stride, int rows, int cols) {
     if (rows == 0) return;
+    if constexpr (VEC && ROWS * kPer % THREADS == 0) {
+      if (rows == ROWS && cols >= COLS) {
+        const uint32_t off = ((uint32_t)row_of(0) * (uint32_t)stride + (uint32_t)col_of()) * (uint32_t)sizeof(In);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          const char* p = reinterpret_cast<const char*>(base + (int64_t)(k * (THREADS / kPer)) * stride);
+          asm volatile("" : "+s"(p));  // a scalar base in every turn, not a pointer per thread carried along
+          r[k].load(reinterpret_cast<const In*>(p + off));
+        }
+        return;
+      }
+    }
+    const int tid = fresh_tid();
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      int row = row_of(k), col = col_of(k);
+      int row = row_of(k, tid), col = col_of(tid);
       row = row < rows ? row : rows - 1;
       if constexpr (VEC) {
         col = col < cols ? col : cols - 8;
@@ -308,14 +353,15 @@ struct TileRegs {
   }
   __device__ __forceinline__ void mask(int rows, int cols) {
     if (rows >= ROWS && cols >= COLS) return;
+    const int tid = fresh_tid();
 #pragma unroll
-    for (int k = 0; k < kN; ++k) r[k].keep(row_of(k) < rows ? cols - col_of(k) : 0);
+    for (int k = 0; k < kN; ++k) r[k].keep(row_of(k, tid) < rows ? cols - col_of(tid) : 0);
   }
   template <typename Tile>
   __device__ __forceinline__ void store(const Tile& tile) const {
 #pragma unroll
     for (int k = 0; k < kN; ++k)
-      if (ROWS * kPer % THREADS == 0 || row_of(k) < ROWS) r[k].put(tile, row_of(k), col_of(k) / 8);
+      if (ROWS * kPer % THREADS == 0 || row_of(k) < ROWS) r[k].put(tile, row_of(k), col_of() / 8);
   }
   // Values that are not finite become 0; first[column] receives the first
   // row that held one, *any is set.  Returns whether there was one.
@@ -323,13 +369,14 @@ struct TileRegs {
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
       if (r[k].nonfinite()) {
+        const int tid = fresh_tid();
         In e[8];
         r[k].get(e);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (Piece<In>::bad(e[j])) {
             e[j] = In(0);
-            atomicMin(first + col_of(k) + j, row_of(k));
+            atomicMin(first + col_of(tid) + j, row_of(k, tid));
           }
         r[k].set(e);
         *any = 1;

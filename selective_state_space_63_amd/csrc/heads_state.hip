@@ -24,7 +24,7 @@ template <typename In>
 constexpr int kBlockTokens = sizeof(In) == 2 ? 128 : 64;
 
 template <typename In, int NT, bool VEC>
-__global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 4 : 2) : 1) void s6_heads_state_kernel(HeadsArgs a, int mode) {
+__global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_heads_state_kernel(HeadsArgs a, int mode) {
   constexpr int NW = NT / 32;  // state tiles of 16 columns per wave and channel tile
   using XT = ColTile<In, kTP>;
   using BT = ColTile<In, NT>;
@@ -38,8 +38,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 4 : 2) : 1) void s6_h
   const int64_t nrows = gridDim.x;
   const int dir = blockIdx.z;
   const int64_t seg = mode == 0 && dir ? blockIdx.y + 1 : blockIdx.y;
-  const int lane0 = threadIdx.x & 63, wv = wave_index();
-  int lane = lane0, g = lane >> 4, c = lane & 15;
+  const int lane = threadIdx.x & 63, wv = wave_index(), g = lane >> 4, c = lane & 15;
   const int pp = wv & 1, nh = wv >> 1;
   const int p0 = hr.pt * kTP, pleft = a.headdim - p0;
   const int64_t t_lo = seg * a.seg_len;
@@ -84,6 +83,8 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 4 : 2) : 1) void s6_h
         T[i][j][r] = v;
       }
 
+  int x_col = XT::col_lane(g, c), b_col = BT::col_lane(g, c);  // lane parts of the LDS addresses
+
   TileRegs<In, kHQ, kTP, 256, VEC> xr;
   TileRegs<In, kHQ, NT, 256, VEC> br;
   In draw = In(0);  // as loaded: a conversion here would wait for every load before it
@@ -101,9 +102,6 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 4 : 2) : 1) void s6_h
   for (int64_t i = 0, k = first; i < nch; ++i, k += step) {
     const int64_t t0 = t_lo + k * kHQ;
     const int rows = (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ);
-    lane = lane0;  // LDS addresses are formed again in every turn, which leaves room for a fourth workgroup per CU
-    asm volatile("" : "+v"(lane));
-    g = lane >> 4; c = lane & 15;
     // the state entering a stored block, from its near end
     const bool enter = dir ? ((k + 1) % kPerBlock == 0 || k == nch - 1) : k % kPerBlock == 0;
     if (mode == 1 && a.planes && enter) {
@@ -157,7 +155,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 4 : 2) : 1) void s6_h
       Pair<In> xd[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const Frag<In> xf = xs.col(2 * pp + j, kk, g, c);
+        const Frag<In> xf = xs.col(x_col, 2 * pp + j, kk, g, c);
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = frag_f32(xf, e) * w[e];
@@ -165,7 +163,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 4 : 2) : 1) void s6_h
       }
 #pragma unroll
       for (int q = 0; q < NW; ++q) {
-        const Frag<In> bf = bs.col(nh * NW + q, kk, g, c);
+        const Frag<In> bf = bs.col(b_col, nh * NW + q, kk, g, c);
 #pragma unroll
         for (int j = 0; j < 2; ++j) T[q][j] = mma_pair(xd[j], bf, T[q][j]);
       }
