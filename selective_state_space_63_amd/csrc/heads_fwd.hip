@@ -219,12 +219,10 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
       const bool full = VEC && rows == kHQ && pleft >= kTP;
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
-        char* yb = reinterpret_cast<char*>(Y + (t0 + 16 * I) * hp);
-        asm volatile("" : "+s"(yb));
-        In* yp = reinterpret_cast<In*>(yb + y_off);
         if (full) {
-          store_vec<In, 4>(yp, o[I]);
+          store_four<In>(scalar_base(Y + (t0 + 16 * I) * hp) + y_off, o[I]);
         } else if (16 * I + c < rows) {
+          In* yp = Y + (t0 + 16 * I + c) * hp + p;
           if constexpr (VEC) {
             if (p < pleft) store_vec<In, 4>(yp, o[I]);
           } else {

@@ -222,6 +222,29 @@ __device__ __forceinline__ Frag<In> lane_frag(const In* p, int lane) {
 }
 
 // -------------------------------------------- global to LDS, by registers --
+// A wave-uniform address as a scalar base formed here: with a 32-bit offset of
+// the lane beside it, instead of a 64-bit pointer per lane carried over a loop.
+// (The address space is named again: behind the asm the compiler would take
+// the pointer for a generic one, and flat accesses wait on LDS too.)
+typedef char __attribute__((address_space(1)))* gbytes;
+__device__ __forceinline__ gbytes scalar_base(const void* p) {
+  uint64_t v = reinterpret_cast<uint64_t>(p);
+  asm volatile("" : "+s"(v));
+  return reinterpret_cast<gbytes>(v);
+}
+typedef unsigned int gu32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int gu32x4 __attribute__((ext_vector_type(4)));
+typedef float gf32x4 __attribute__((ext_vector_type(4)));
+
+// Four values in the input type.
+template <typename In>
+__device__ __forceinline__ void store_four(gbytes p, const float (&f)[4]) {
+  if constexpr (sizeof(In) == 2)
+    *reinterpret_cast<gu32x2 __attribute__((address_space(1)))*>(p) = gu32x2{bf_pack(f[0], f[1]), bf_pack(f[2], f[3])};
+  else
+    *reinterpret_cast<gf32x4 __attribute__((address_space(1)))*>(p) = gf32x4{f[0], f[1], f[2], f[3]};
+}
+
 // Eight consecutive columns of one row.
 template <typename In>
 struct Piece;
@@ -234,6 +257,10 @@ struct Piece<uint16_t> {
     v = make_uint4(part(v.x, 0), part(v.y, 1), part(v.z, 2), part(v.w, 3));
   }
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_at(gbytes p) {
+    const gu32x4 w = *reinterpret_cast<const gu32x4 __attribute__((address_space(1)))*>(p);
+    v = make_uint4(w.x, w.y, w.z, w.w);
+  }
   __device__ __forceinline__ void set(const uint16_t (&e)[8]) {
     v = make_uint4(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16), e[4] | ((uint32_t)e[5] << 16),
                    e[6] | ((uint32_t)e[7] << 16));
@@ -270,6 +297,12 @@ struct Piece<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void load_at(gbytes p) {
+    const auto* q = reinterpret_cast<const gf32x4 __attribute__((address_space(1)))*>(p);
+    const gf32x4 x = q[0], y = q[1];
+    a = make_float4(x.x, x.y, x.z, x.w);
+    b = make_float4(y.x, y.y, y.z, y.w);
   }
   __device__ __forceinline__ void set(const float (&e)[8]) {
     a = make_float4(e[0], e[1], e[2], e[3]);
@@ -327,9 +360,7 @@ struct TileRegs {
         const uint32_t off = ((uint32_t)row_of(0) * (uint32_t)stride + (uint32_t)col_of()) * (uint32_t)sizeof(In);
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
-          const char* p = reinterpret_cast<const char*>(base + (int64_t)(k * (THREADS / kPer)) * stride);
-          asm volatile("" : "+s"(p));  // a scalar base in every turn, not a pointer per thread carried along
-          r[k].load(reinterpret_cast<const In*>(p + off));
+          r[k].load_at(scalar_base(base + (int64_t)(k * (THREADS / kPer)) * stride) + off);
         }
         return;
       }
