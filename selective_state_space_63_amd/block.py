@@ -9,11 +9,12 @@ enqueued on the current stream of the tensors' device.  ``HeadsScan``,
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
 from . import s6
-from .s6 import _DT, _check, _opt, _ptr, _req
+from .s6 import _DT, _check
 
 S6_DELTA_SOFTPLUS, S6_UNIT_INPUT, S6_GATE_AFTER = 1, 4, 8
 MAX_DSTATE = 128
@@ -57,21 +58,50 @@ def _load():
     return _lib
 
 
-def _stream(like):
-    return torch.cuda.current_stream(like.device).cuda_stream
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle of the current stream without a Stream object around it, where
+# this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _launch(fn, like, *args):
+    """fn(*args, stream) on `like`'s device and its current stream."""
+    index = like.device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc:
+        _check(rc)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _same_device(first, *others):
     """The kernels run on the device of `first`: every tensor has to be there."""
+    d = first.device
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+        if t is not None and t.device != d:
+            raise ValueError(f"tensors on {d} and {t.device}")
 
 
-def _workspace(query, like):
+def _workspace(query, like, *args):
     """(tensor, pointer, bytes) of a fresh workspace on the current stream."""
     out = ctypes.c_size_t(0)
-    _check(query(ctypes.byref(out)))
+    index = like.device.index
+    if torch.cuda.current_device() == index:
+        rc = query(*args, ctypes.byref(out))
+    else:
+        with torch.cuda.device(index):
+            rc = query(*args, ctypes.byref(out))
+    if rc:
+        _check(rc)
     if out.value == 0:
         return None, None, 0
     t = torch.empty(out.value, dtype=torch.uint8, device=like.device)
@@ -84,29 +114,46 @@ def _dtype(t, name="x"):
     return t.dtype
 
 
-def _rows(t, name, shape, dtype, inner):
-    """(batch stride, token stride) of a device tensor whose last `inner`
-    dimensions are contiguous: the leading ones may be strided (slices of
-    wider rows)."""
+def _need(t, name, shape, dtype):
+    """A device tensor of this shape and type (the shape as a tuple or Size)."""
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.numel() == 0:
-        return (0,) * (len(shape) - inner)
+    return t
+
+
+def _whole(t, name, shape, dtype=torch.float32):
+    """As _need, and contiguous; None passes."""
+    if t is None:
+        return
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        _need(t, name, shape, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name, shape, dtype, inner):
+    """Strides of the leading dimensions of a device tensor whose last
+    `inner` dimensions are contiguous: the leading ones may be strided (slices
+    of wider rows)."""
+    if t is None or t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        _need(t, name, shape, dtype)
     st = t.stride()
+    if t.is_contiguous():
+        return st[:-inner]
+    lead = len(shape) - inner
     want = 1
-    for i in range(len(shape) - 1, len(shape) - 1 - inner, -1):
-        if shape[i] != 1 and st[i] != want:
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if st[i] != want and shape[i] != 1:
             raise ValueError(f"{name}'s rows must be contiguous")
         want *= shape[i]
-    lead = len(shape) - inner
     # a stride along a single element is never taken
-    return tuple(st[i] if shape[i] > 1 else max(want, 0) for i in range(lead))
+    return tuple(v if n > 1 else want for v, n in zip(st, shape[:lead]))
 
 
 def _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, tokens):
@@ -114,31 +161,30 @@ def _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, 
     if x.dim() != (4 if tokens else 3) or Bm is None or Bm.dim() != x.dim():
         raise ValueError("x is (batch, seqlen, heads, headdim), Bm and Cm (batch, seqlen, groups, dstate); without "
                          "seqlen for a single token")
-    lead = tuple(x.shape[:2]) if tokens else (x.shape[0],)
-    heads, headdim = x.shape[-2:]
-    groups, dstate = Bm.shape[-2:]
-    xs = _rows(x, "x", x.shape, dt, 2)
-    bs = _rows(Bm, "Bm", (*lead, groups, dstate), dt, 2)
-    cs = _rows(Cm, "Cm", (*lead, groups, dstate), dt, 2)
+    shape = x.shape
+    lead, (heads, headdim), (groups, dstate) = shape[:-2], shape[-2:], Bm.shape[-2:]
+    gshape = (*lead, groups, dstate)
+    xs = _rows(x, "x", shape, dt, 2)
+    bs = _rows(Bm, "Bm", gshape, dt, 2)
+    cs = _rows(Cm, "Cm", gshape, dt, 2)
     if delta is None:
         if delta_bias is not None or delta_softplus:
             raise ValueError("delta_bias and delta_softplus need a delta")
-        ds = (0, 0)
+        ds = (0, 0) if tokens else (0,)
     else:
         ds = _rows(delta, "delta", (*lead, heads), dt, 1)
-    _req(A, "A", (heads,), torch.float32)
-    _opt(D, "D", (heads,), torch.float32)
-    _opt(delta_bias, "delta_bias", (heads,), torch.float32)
+    if A is None:
+        raise ValueError("A is required")
+    _whole(A, "A", (heads,))
+    _whole(D, "D", (heads,))
+    _whole(delta_bias, "delta_bias", (heads,))
     _same_device(x, delta, A, Bm, Cm, D, delta_bias)
-    pad = (lambda s: s) if tokens else (lambda s: (s[0], 0))
-    dims = HeadsDims(lead[0], lead[1] if tokens else 1, heads, headdim, groups, dstate,
-                     *pad(xs), *pad(ds), *pad(bs), *pad(cs))
+    if tokens:
+        dims = HeadsDims(*lead, heads, headdim, groups, dstate, *xs, *ds, *bs, *cs)
+    else:
+        dims = HeadsDims(lead[0], 1, heads, headdim, groups, dstate, xs[0], 0, ds[0], 0, bs[0], 0, cs[0], 0)
     flags = (S6_DELTA_SOFTPLUS if delta_softplus else 0) | (S6_UNIT_INPUT if unit_input else 0)
     return dims, _DT[dt], flags
-
-
-def _state(t, name, x):
-    return _opt(t, name, (x.shape[0], x.shape[-2], x.shape[-1], t.shape[-1] if t is not None else 0), torch.float32)
 
 
 def heads_scan_fwd(x, delta, A, Bm, Cm, D=None, h0=None, return_last_state=False, delta_bias=None,
@@ -153,22 +199,20 @@ def heads_scan_fwd(x, delta, A, Bm, Cm, D=None, h0=None, return_last_state=False
     h_last (batch, heads, headdim, N) fp32 if requested."""
     dims, dt, flags = _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, True)
     sshape = (dims.batch, dims.heads, dims.headdim, dims.dstate)
-    _opt(h0, "h0", sshape, torch.float32)
+    _whole(h0, "h0", sshape)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _req(y, "y", x.shape, x.dtype)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _whole(y, "y", x.shape, x.dtype)
     if return_last_state and h_last is None:
         h_last = torch.empty(sshape, dtype=torch.float32, device=x.device)
-    _opt(h_last, "h_last", sshape, torch.float32)
+    _whole(h_last, "h_last", sshape)
     _same_device(x, h0, y, h_last)
     lib = _load()
     ref = ctypes.byref(dims)
-    with torch.cuda.device(x.device):
-        keep, wsp, wsn = _workspace(lambda out: lib.s6_heads_scan_fwd_workspace_size(ref, dt, out), x)
-        rc = lib.s6_heads_scan_fwd(ref, dt, flags, _ptr(x), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(Bm), _ptr(Cm),
-                                   _ptr(D), _ptr(h0), _ptr(y), _ptr(h_last), wsp, wsn, _stream(x))
+    keep, wsp, wsn = _workspace(lib.s6_heads_scan_fwd_workspace_size, x, ref, dt)
+    _launch(lib.s6_heads_scan_fwd, x, ref, dt, flags, _at(x), _at(delta), _at(delta_bias), _at(A), _at(Bm), _at(Cm),
+            _at(D), _at(h0), _at(y), _at(h_last), wsp, wsn)
     del keep
-    _check(rc)
     return (y, h_last) if return_last_state else y
 
 
@@ -180,25 +224,22 @@ def heads_scan_bwd(x, delta, A, Bm, Cm, dy, D=None, h0=None, dh_last=None, delta
     dtype; dA, and where their input is given dD, ddelta_bias, dh0 in fp32."""
     dims, dt, flags = _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, True)
     sshape = (dims.batch, dims.heads, dims.headdim, dims.dstate)
-    _opt(h0, "h0", sshape, torch.float32)
-    _opt(dh_last, "dh_last", sshape, torch.float32)
-    _req(dy, "dy", x.shape, x.dtype)
+    _whole(h0, "h0", sshape)
+    _whole(dh_last, "dh_last", sshape)
+    _whole(_need(dy, "dy", x.shape, x.dtype), "dy", x.shape, x.dtype)
     _same_device(x, h0, dh_last, dy)
-    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=x.device)  # noqa: E731
+    new = lambda t: torch.empty_like(t, memory_format=torch.contiguous_format)  # noqa: E731
     g = {"dx": new(x), "dBm": new(Bm), "dCm": new(Cm), "dA": new(A)}
     for name, t in (("ddelta", delta), ("dD", D), ("ddelta_bias", delta_bias), ("dh0", h0)):
         if t is not None:
             g[name] = new(t)
     lib = _load()
     ref = ctypes.byref(dims)
-    with torch.cuda.device(x.device):
-        keep, wsp, wsn = _workspace(lambda out: lib.s6_heads_scan_bwd_workspace_size(ref, dt, out), x)
-        rc = lib.s6_heads_scan_bwd(ref, dt, flags, _ptr(x), _ptr(delta), _ptr(delta_bias), _ptr(A), _ptr(Bm), _ptr(Cm),
-                                   _ptr(D), _ptr(h0), _ptr(dy), _ptr(dh_last), _ptr(g["dx"]), _ptr(g.get("ddelta")),
-                                   _ptr(g["dA"]), _ptr(g["dBm"]), _ptr(g["dCm"]), _ptr(g.get("dD")),
-                                   _ptr(g.get("dh0")), _ptr(g.get("ddelta_bias")), wsp, wsn, _stream(x))
+    keep, wsp, wsn = _workspace(lib.s6_heads_scan_bwd_workspace_size, x, ref, dt)
+    _launch(lib.s6_heads_scan_bwd, x, ref, dt, flags, _at(x), _at(delta), _at(delta_bias), _at(A), _at(Bm), _at(Cm),
+            _at(D), _at(h0), _at(dy), _at(dh_last), _at(g["dx"]), _at(g.get("ddelta")), _at(g["dA"]), _at(g["dBm"]),
+            _at(g["dCm"]), _at(g.get("dD")), _at(g.get("dh0")), _at(g.get("ddelta_bias")), wsp, wsn)
     del keep
-    _check(rc)
     return g
 
 
@@ -208,28 +249,27 @@ def heads_state_update(h, x, delta, A, Bm, Cm, D=None, delta_bias=None, delta_so
     None, Bm, Cm: (batch, groups, N).  Returns y (batch, heads, headdim) in
     x's dtype."""
     dims, dt, flags = _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, False)
-    _req(h, "h", (dims.batch, dims.heads, dims.headdim, dims.dstate), torch.float32)
+    sshape = (*x.shape, Bm.shape[-1])
+    _whole(_need(h, "h", sshape, torch.float32), "h", sshape)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _req(y, "y", x.shape, x.dtype)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _whole(y, "y", x.shape, x.dtype)
     _same_device(x, h, y)
-    with torch.cuda.device(x.device):
-        rc = _load().s6_heads_state_update(ctypes.byref(dims), dt, flags, _ptr(h), _ptr(x), _ptr(delta),
-                                           _ptr(delta_bias), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(y), _stream(x))
-    _check(rc)
+    _launch(_load().s6_heads_state_update, x, ctypes.byref(dims), dt, flags, _at(h), _at(x), _at(delta),
+            _at(delta_bias), _at(A), _at(Bm), _at(Cm), _at(D), _at(y))
     return y
+
+
+def _weight(w, dim):
+    if w is None:
+        raise ValueError("weight is required")
+    _whole(w, "weight", (dim,))
 
 
 def _flat(t, name, shape, dtype):
     """Row stride of a (..., dim) device tensor seen as rows of dim elements."""
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    _need(t, name, shape, dtype)
     dim = shape[-1]
     if t.is_contiguous():
         return dim
@@ -251,13 +291,6 @@ def _flat(t, name, shape, dtype):
     return dim if stride is None else stride
 
 
-def _count(shape):
-    n = 1
-    for v in shape[:-1]:
-        n *= v
-    return n
-
-
 def add_norm_fwd(x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5, residual_dtype=None, out=None,
                  residual_out=None):
     """Residual add, residual scale and RMS norm before a block: r' = residual
@@ -272,20 +305,20 @@ def add_norm_fwd(x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5, resi
     if rt not in (torch.float32, dt):
         raise ValueError(f"residual dtype {rt}: expected float32 or {dt}")
     dim = x.shape[-1]
-    _opt(residual, "residual", x.shape, rt)
-    _req(weight, "weight", (dim,), torch.float32)
-    _opt(gamma, "gamma", (dim,), torch.float32)
+    _whole(residual, "residual", x.shape, rt)
+    _weight(weight, dim)
+    _whole(gamma, "gamma", (dim,))
     if out is None:
-        out = torch.empty(x.shape, dtype=dt, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _whole(out, "out", x.shape, dt)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=rt, device=x.device)
-    _req(out, "out", x.shape, dt)
-    _req(residual_out, "residual_out", x.shape, rt)
+        residual_out = torch.empty_like(x, dtype=rt, memory_format=torch.contiguous_format)
+    else:
+        _whole(residual_out, "residual_out", x.shape, rt)
     _same_device(x, weight, residual, gamma, out, residual_out)
-    with torch.cuda.device(x.device):
-        rc = _load().s6_add_norm_fwd(_count(x.shape), dim, _DT[dt], _DT[rt], _ptr(x), stride, _ptr(residual),
-                                     _ptr(weight), _ptr(gamma), scale, eps, _ptr(out), _ptr(residual_out), _stream(x))
-    _check(rc)
+    _launch(_load().s6_add_norm_fwd, x, math.prod(x.shape[:-1]), dim, _DT[dt], _DT[rt], _at(x), stride, _at(residual),
+            _at(weight), _at(gamma), scale, eps, _at(out), _at(residual_out))
     return out, residual_out
 
 
@@ -298,30 +331,25 @@ def add_norm_bwd(dout, residual_out, weight, dresidual_out=None, x=None, gamma=N
     dim = dout.shape[-1]
     if rt not in (torch.float32, dt):
         raise ValueError(f"residual_out dtype {rt}: expected float32 or {dt}")
-    _req(dout, "dout", dout.shape, dt)
-    _req(residual_out, "residual_out", dout.shape, rt)
-    _opt(dresidual_out, "dresidual_out", dout.shape, rt)
-    _req(weight, "weight", (dim,), torch.float32)
-    _opt(gamma, "gamma", (dim,), torch.float32)
+    _whole(_need(dout, "dout", dout.shape, dt), "dout", dout.shape, dt)
+    _whole(residual_out, "residual_out", dout.shape, rt)
+    _whole(dresidual_out, "dresidual_out", dout.shape, rt)
+    _weight(weight, dim)
+    _whole(gamma, "gamma", (dim,))
     stride = dim
     if gamma is not None:
         stride = _flat(x, "x", dout.shape, dt)
     _same_device(dout, residual_out, dresidual_out, weight, gamma, x)
-    g = {"dx": torch.empty(dout.shape, dtype=dt, device=dout.device),
-         "dresidual": torch.empty(dout.shape, dtype=rt, device=dout.device),
-         "dweight": torch.empty_like(weight)}
+    g = {"dx": torch.empty_like(dout), "dresidual": torch.empty_like(residual_out), "dweight": torch.empty_like(weight)}
     if gamma is not None:
         g["dgamma"] = torch.empty_like(gamma)
     lib = _load()
-    rows = _count(dout.shape)
-    with torch.cuda.device(dout.device):
-        keep, wsp, wsn = _workspace(lambda o: lib.s6_add_norm_bwd_workspace_size(rows, dim, o), dout)
-        rc = lib.s6_add_norm_bwd(rows, dim, _DT[dt], _DT[rt], _ptr(dout), _ptr(dresidual_out), _ptr(residual_out),
-                                 _ptr(x) if gamma is not None else None, stride, _ptr(weight), _ptr(gamma), scale, eps,
-                                 _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]), _ptr(g.get("dgamma")), wsp,
-                                 wsn, _stream(dout))
+    rows = math.prod(dout.shape[:-1])
+    keep, wsp, wsn = _workspace(lib.s6_add_norm_bwd_workspace_size, dout, rows, dim)
+    _launch(lib.s6_add_norm_bwd, dout, rows, dim, _DT[dt], _DT[rt], _at(dout), _at(dresidual_out), _at(residual_out),
+            _at(x) if gamma is not None else None, stride, _at(weight), _at(gamma), scale, eps, _at(g["dx"]),
+            _at(g["dresidual"]), _at(g["dweight"]), _at(g.get("dgamma")), wsp, wsn)
     del keep
-    _check(rc)
     return g
 
 
@@ -330,9 +358,11 @@ def _gated_args(y, z, weight, groups):
     dim = y.shape[-1]
     if groups < 1 or dim % groups:
         raise ValueError(f"{groups} groups do not divide {dim} columns")
-    _req(weight, "weight", (dim,), torch.float32)
+    ys = _flat(y, "y", y.shape, dt)
+    zs = dim if z is None else _flat(z, "z", y.shape, dt)
+    _weight(weight, dim)
     _same_device(y, z, weight)
-    return dt, dim, _flat(y, "y", y.shape, dt), dim if z is None else _flat(z, "z", y.shape, dt)
+    return dt, dim, ys, zs
 
 
 def gated_norm_fwd(y, z, weight, groups=1, gate_after=False, eps=1e-5, out=None):
@@ -342,13 +372,12 @@ def gated_norm_fwd(y, z, weight, groups=1, gate_after=False, eps=1e-5, out=None)
     a contiguous tensor in y's dtype."""
     dt, dim, ys, zs = _gated_args(y, z, weight, groups)
     if out is None:
-        out = torch.empty(y.shape, dtype=dt, device=y.device)
-    _req(out, "out", y.shape, dt)
-    _same_device(y, out)
-    with torch.cuda.device(y.device):
-        rc = _load().s6_gated_norm_fwd(_count(y.shape), dim, groups, _DT[dt], S6_GATE_AFTER if gate_after else 0,
-                                       _ptr(y), ys, _ptr(z), zs, _ptr(weight), eps, _ptr(out), _stream(y))
-    _check(rc)
+        out = torch.empty_like(y, memory_format=torch.contiguous_format)
+    else:
+        _whole(out, "out", y.shape, dt)
+        _same_device(y, out)
+    _launch(_load().s6_gated_norm_fwd, y, math.prod(y.shape[:-1]), dim, groups, _DT[dt],
+            S6_GATE_AFTER if gate_after else 0, _at(y), ys, _at(z), zs, _at(weight), eps, _at(out))
     return out
 
 
@@ -356,20 +385,17 @@ def gated_norm_bwd(dout, y, z, weight, groups=1, gate_after=False, eps=1e-5):
     """Gradients of <dout, out> for gated_norm_fwd: a dict of dy, dz (where z
     is given) in y's dtype and dweight in fp32."""
     dt, dim, ys, zs = _gated_args(y, z, weight, groups)
-    _req(dout, "dout", y.shape, dt)
+    _whole(_need(dout, "dout", y.shape, dt), "dout", y.shape, dt)
     _same_device(y, dout)
-    g = {"dy": torch.empty(y.shape, dtype=dt, device=y.device), "dweight": torch.empty_like(weight)}
+    g = {"dy": torch.empty_like(dout), "dweight": torch.empty_like(weight)}
     if z is not None:
-        g["dz"] = torch.empty(y.shape, dtype=dt, device=y.device)
+        g["dz"] = torch.empty_like(dout)
     lib = _load()
-    rows = _count(y.shape)
-    with torch.cuda.device(y.device):
-        keep, wsp, wsn = _workspace(lambda o: lib.s6_gated_norm_bwd_workspace_size(rows, dim, groups, o), y)
-        rc = lib.s6_gated_norm_bwd(rows, dim, groups, _DT[dt], S6_GATE_AFTER if gate_after else 0, _ptr(dout), _ptr(y),
-                                   ys, _ptr(z), zs, _ptr(weight), eps, _ptr(g["dy"]), _ptr(g.get("dz")),
-                                   _ptr(g["dweight"]), wsp, wsn, _stream(y))
+    rows = math.prod(y.shape[:-1])
+    keep, wsp, wsn = _workspace(lib.s6_gated_norm_bwd_workspace_size, y, rows, dim, groups)
+    _launch(lib.s6_gated_norm_bwd, y, rows, dim, groups, _DT[dt], S6_GATE_AFTER if gate_after else 0, _at(dout),
+            _at(y), ys, _at(z), zs, _at(weight), eps, _at(g["dy"]), _at(g.get("dz")), _at(g["dweight"]), wsp, wsn)
     del keep
-    _check(rc)
     return g
 
 
