@@ -11,25 +11,23 @@
 // the row's threads once and writes its outputs: the kernels are bound by
 // HBM.  Sums and statistics are fp32.
 //
-// Layout: TPR threads (a wave, or a workgroup of four) per row, K pieces of V
-// consecutive values per thread in registers (V = 8: 16-byte accesses; V = 1
-// where a width, stride or pointer does not allow them); rows wider than K V
-// TPR read the rest again in the second phase.  A thread keeps its columns
-// over the rows it walks, so weights are read once per thread and the column
-// sums (dw, dgamma) stay in registers until the end; their per-thread-group
-// parts are then added in a fixed order by s6_norm_colsum.
+// Layout: a row is a workgroup's (as many waves as hold it), or, for narrow
+// rows, a wave's with four rows per workgroup.  Each thread keeps K pieces of V
+// consecutive values in registers (V = 8: 16-byte accesses; V = 1 where a
+// width, stride or pointer does not allow them); rows wider than that read the
+// rest again in the second phase.  A thread keeps its columns over the rows it
+// walks, so weights are read once per thread and the column sums (dw, dgamma)
+// stay in registers until the end; the row walkers' parts are then added in a
+// fixed order by s6_norm_colsum.  The next row's loads are issued before the
+// current row's sums meet.
 #include "block_internal.h"
 
 namespace s6i {
 
 namespace {
 
-constexpr int kK = 4;  // register pieces per thread
-
-// Most row walkers where column sums are taken (a walker leaves one part of
-// them): 512 workgroups either way, of four waves with a row each for rows
-// that a wave holds, of four waves on one row for wider ones.
-int64_t most_parts(int64_t width, int tpr) { return width <= (int64_t)kK * 64 * 8 && tpr == 64 ? 2048 : 512; }
+constexpr int kMaxT = 1024;        // threads of a workgroup
+constexpr int64_t kParts = 1024;   // most row walkers where column sums are taken (each leaves a part)
 
 struct NormArgs {
   int64_t rows, dim, gd;        // gd: width of a group (dim for the add norm)
@@ -50,53 +48,85 @@ struct NormArgs {
   float* dg;                    // parts (walkers, dim), nullable
 };
 
-// Sum of two values over the TPR threads of a row.  For TPR = 256 the four
-// waves meet in LDS; the buffer alternates between two halves, so one barrier
-// per row is enough (a wave writes half i again only after the barrier of
-// half i + 1, which every wave reaches after reading half i).
-template <int TPR>
-__device__ __forceinline__ void row_sum2(float& s, float& t, float (*buf)[2][4], int par) {
-  s = wave_sum(s);
-  t = wave_sum(t);
-  if constexpr (TPR > 64) {
-    const int w = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) { buf[par][0][w] = s; buf[par][1][w] = t; }
-    __syncthreads();
-    s = (buf[par][0][0] + buf[par][0][1]) + (buf[par][0][2] + buf[par][0][3]);
-    t = (buf[par][1][0] + buf[par][1][1]) + (buf[par][1][2] + buf[par][1][3]);
+// V values of a row as loaded.
+template <typename T, int V>
+struct Raw {
+  T e[V];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (V == 1) {
+      e[0] = *p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < (int)(V * sizeof(T)) / 16; ++i)
+        reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
   }
-}
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = to_f32(e[j]);
+  }
+  // What is formed from the values before is formed again after this, instead
+  // of being kept in registers as floats.
+  __device__ __forceinline__ void again() {
+    if constexpr (V > 1) {
+      uint32_t w[V * sizeof(T) / 4];
+      __builtin_memcpy(w, e, sizeof(e));
+#pragma unroll
+      for (int i = 0; i < (int)(V * sizeof(T)) / 4; ++i) asm volatile("" : "+v"(w[i]));
+      __builtin_memcpy(e, w, sizeof(e));
+    }
+  }
+};
 
 __device__ __forceinline__ float sigmoid_f(float z) { return fast_rcp(1.0f + fast_exp2(-z * kLog2e)); }
 
-// Walker `wk` of `nw` takes rows wk, wk + nw, ...: every walker of a
-// workgroup makes the same number of turns (barriers), masked past the end.
+// The rows that a thread walks: wk, wk + nw, ...; every walker of a workgroup
+// makes the same number of turns (barriers), masked past the end.  t of tpr:
+// the thread in its row.
 struct Walk {
   int64_t wk, nw, turns;
-  int t;
+  int t, tpr;
 };
-template <int TPR>
+template <bool MULTI>
 __device__ __forceinline__ Walk walk_of(int64_t rows) {
   Walk o;
-  constexpr int per = 256 / TPR;
+  const int per = MULTI ? 4 : 1;
+  o.tpr = MULTI ? 64 : (int)blockDim.x;
   o.nw = (int64_t)gridDim.x * per;
-  o.wk = (int64_t)blockIdx.x * per + threadIdx.x / TPR;
+  o.wk = (int64_t)blockIdx.x * per + (MULTI ? threadIdx.x >> 6 : 0);
   o.turns = (rows + o.nw - 1) / o.nw;
-  o.t = threadIdx.x % TPR;
+  o.t = MULTI ? threadIdx.x & 63 : threadIdx.x;
   return o;
 }
 
+// Sums of two values over the threads of a row.  The waves of a workgroup
+// meet in LDS; the buffer alternates between two halves, so one barrier per
+// row is enough (a wave writes half i again only after the barrier of half
+// i + 1, which every wave reaches after reading half i).
+template <bool MULTI>
+__device__ __forceinline__ void row_sum2(float& s, float& t, float (*buf)[2][kMaxT / 64], int par) {
+  s = wave_sum(s);
+  t = wave_sum(t);
+  if constexpr (!MULTI) {
+    const int w = threadIdx.x >> 6, n = blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) { buf[par][0][w] = s; buf[par][1][w] = t; }
+    __syncthreads();
+    s = t = 0.0f;
+    for (int i = 0; i < n; ++i) { s += buf[par][0][i]; t += buf[par][1][i]; }
+  }
+}
+
 // ------------------------------------------------------------- add norm --
-template <typename In, typename Res, int V, int TPR>
-__global__ __launch_bounds__(256) void s6_add_norm_kernel(NormArgs a) {
-  __shared__ float buf[2][2][4];
-  const Walk wk = walk_of<TPR>(a.rows);
+template <typename In, typename Res, int V, int K, bool MULTI, bool WIDE>
+__global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_add_norm_kernel(NormArgs a) {
+  __shared__ float buf[2][2][kMaxT / 64];
+  const Walk wk = walk_of<MULTI>(a.rows);
   const int64_t np = (a.dim + V - 1) / V;  // pieces of a row
   const float inv_d = 1.0f / (float)a.dim;
-  float w[kK][V], ga[kK][V];
+  float w[K][V], ga[K][V];
 #pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int64_t i = (int64_t)k * TPR + wk.t;
+  for (int k = 0; k < K; ++k) {
+    const int64_t i = (int64_t)k * wk.tpr + wk.t;
 #pragma unroll
     for (int j = 0; j < V; ++j) ga[k][j] = a.scale;
     if (i < np) {
@@ -108,6 +138,22 @@ __global__ __launch_bounds__(256) void s6_add_norm_kernel(NormArgs a) {
       }
     }
   }
+  Raw<In, V> xr[K];
+  Raw<Res, V> rr[K];
+  auto issue = [&](int64_t row) {
+    if (row >= a.rows) return;
+    const In* x = static_cast<const In*>(a.a) + row * a.a_stride;
+    const Res* r = static_cast<const Res*>(a.b) + row * a.dim;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      if (i < np) {
+        xr[k].load(x + i * V);
+        if (a.b) rr[k].load(r + i * V);
+      }
+    }
+  };
+  issue(wk.wk);
   for (int64_t q = 0; q < wk.turns; ++q) {
     const int64_t row = q * wk.nw + wk.wk;
     const bool on = row < a.rows;
@@ -115,60 +161,56 @@ __global__ __launch_bounds__(256) void s6_add_norm_kernel(NormArgs a) {
     const Res* r = a.b ? static_cast<const Res*>(a.b) + row * a.dim : nullptr;
     In* out = static_cast<In*>(a.o1) + row * a.dim;
     Res* ro = static_cast<Res*>(a.o2) + row * a.dim;
-    float u[kK][V], rv[kK][V];
+    float u[K][V];
     float s = 0.0f, unused = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
       if (on && i < np) {
-        load_vec<In, V>(x + i * V, u[k]);
-        if (r) load_vec<Res, V>(r + i * V, rv[k]);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
-      if (on && i < np) {
+        float rv[V];
+        xr[k].get(u[k]);
+        if (r) rr[k].get(rv);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          u[k][j] = r ? __builtin_fmaf(ga[k][j], u[k][j], rv[k][j]) : ga[k][j] * u[k][j];
+          u[k][j] = r ? __builtin_fmaf(ga[k][j], u[k][j], rv[j]) : ga[k][j] * u[k][j];
           s = __builtin_fmaf(u[k][j], u[k][j], s);
         }
         store_vec<Res, V>(ro + i * V, u[k]);
       }
     }
-    // the sum of a piece past the registers: r' is formed again for out, from
-    // x and the residual, so it is stored in the second phase (residual_out
-    // may be the residual's buffer)
+    issue(row + wk.nw);
+    // a piece past the registers: r' is formed again for out, from x and the
+    // residual, so it is stored in the second phase (residual_out may be the
+    // residual's buffer)
     auto wide = [&](int64_t i, float (&v)[V]) {
-      float rr[V], gg[V];
+      float rv[V], gg[V];
       load_vec<In, V>(x + i * V, v);
-      if (r) load_vec<Res, V>(r + i * V, rr);
+      if (r) load_vec<Res, V>(r + i * V, rv);
       if (a.gamma) load_vec<float, V>(a.gamma + i * V, gg);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float g = a.gamma ? gg[j] * a.scale : a.scale;
-        v[j] = r ? __builtin_fmaf(g, v[j], rr[j]) : g * v[j];
+        v[j] = r ? __builtin_fmaf(g, v[j], rv[j]) : g * v[j];
       }
     };
-    for (int64_t i = (int64_t)kK * TPR + wk.t; on && i < np; i += TPR) {
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
       float v[V];
       wide(i, v);
 #pragma unroll
       for (int j = 0; j < V; ++j) s = __builtin_fmaf(v[j], v[j], s);
     }
-    row_sum2<TPR>(s, unused, buf, (int)(q & 1));
+    row_sum2<MULTI>(s, unused, buf, (int)(q & 1));
     const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(s, inv_d, a.eps));
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
       if (on && i < np) {
 #pragma unroll
         for (int j = 0; j < V; ++j) u[k][j] = u[k][j] * inv * w[k][j];
         store_vec<In, V>(out + i * V, u[k]);
       }
     }
-    for (int64_t i = (int64_t)kK * TPR + wk.t; on && i < np; i += TPR) {
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
       float v[V], ww[V];
       wide(i, v);
       load_vec<float, V>(a.w + i * V, ww);
@@ -191,16 +233,16 @@ __device__ __forceinline__ void part_add(float* p, const float (&v)[V], bool fir
   store_vec<float, V>(p, o);
 }
 
-template <typename In, typename Res, int V, int TPR>
-__global__ __launch_bounds__(256) void s6_add_norm_bwd_kernel(NormArgs a) {
-  __shared__ float buf[2][2][4];
-  const Walk wk = walk_of<TPR>(a.rows);
+template <typename In, typename Res, int V, int K, bool MULTI, bool WIDE>
+__global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_add_norm_bwd_kernel(NormArgs a) {
+  __shared__ float buf[2][2][kMaxT / 64];
+  const Walk wk = walk_of<MULTI>(a.rows);
   const int64_t np = (a.dim + V - 1) / V;
   const float inv_d = 1.0f / (float)a.dim;
-  float w[kK][V], ga[kK][V], dw[kK][V], dg[kK][V];
+  float w[K][V], ga[K][V], dw[K][V], dg[K][V];
 #pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int64_t i = (int64_t)k * TPR + wk.t;
+  for (int k = 0; k < K; ++k) {
+    const int64_t i = (int64_t)k * wk.tpr + wk.t;
 #pragma unroll
     for (int j = 0; j < V; ++j) { ga[k][j] = a.scale; dw[k][j] = dg[k][j] = 0.0f; }
     if (i < np) {
@@ -212,6 +254,22 @@ __global__ __launch_bounds__(256) void s6_add_norm_bwd_kernel(NormArgs a) {
       }
     }
   }
+  Raw<In, V> dr_[K], xr[K];
+  Raw<Res, V> ur[K], er[K];
+  auto issue = [&](int64_t row) {
+    if (row >= a.rows) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      if (i < np) {
+        ur[k].load(static_cast<const Res*>(a.res) + row * a.dim + i * V);
+        dr_[k].load(static_cast<const In*>(a.dout) + row * a.dim + i * V);
+        if (a.dres) er[k].load(static_cast<const Res*>(a.dres) + row * a.dim + i * V);
+        if (a.dg) xr[k].load(static_cast<const In*>(a.a) + row * a.a_stride + i * V);
+      }
+    }
+  };
+  issue(wk.wk);
   for (int64_t q = 0; q < wk.turns; ++q) {
     const int64_t row = q * wk.nw + wk.wk;
     const bool on = row < a.rows;
@@ -222,28 +280,26 @@ __global__ __launch_bounds__(256) void s6_add_norm_bwd_kernel(NormArgs a) {
     const In* x = static_cast<const In*>(a.a) + row * a.a_stride;
     In* dx = a.o1 ? static_cast<In*>(a.o1) + at : nullptr;
     Res* dr = a.o2 ? static_cast<Res*>(a.o2) + at : nullptr;
-    float u[kK][V], d[kK][V], e[kK][V];
+    Raw<In, V> dc[K], xc[K];
+    Raw<Res, V> uc[K], ec[K];
     float s = 0.0f, t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      dc[k] = dr_[k]; xc[k] = xr[k]; uc[k] = ur[k]; ec[k] = er[k];
       if (on && i < np) {
-        load_vec<Res, V>(res + i * V, u[k]);
-        load_vec<In, V>(dout + i * V, d[k]);
-        if (dres) load_vec<Res, V>(dres + i * V, e[k]);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
-      if (on && i < np)
+        float u[V], d[V];
+        uc[k].get(u);
+        dc[k].get(d);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          s = __builtin_fmaf(u[k][j], u[k][j], s);
-          t = __builtin_fmaf(d[k][j] * w[k][j], u[k][j], t);
+          s = __builtin_fmaf(u[j], u[j], s);
+          t = __builtin_fmaf(d[j] * w[k][j], u[j], t);
         }
+      }
     }
-    for (int64_t i = (int64_t)kK * TPR + wk.t; on && i < np; i += TPR) {
+    issue(row + wk.nw);
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
       float uu[V], dd[V], ww[V];
       load_vec<Res, V>(res + i * V, uu);
       load_vec<In, V>(dout + i * V, dd);
@@ -254,13 +310,12 @@ __global__ __launch_bounds__(256) void s6_add_norm_bwd_kernel(NormArgs a) {
         t = __builtin_fmaf(dd[j] * ww[j], uu[j], t);
       }
     }
-    row_sum2<TPR>(s, t, buf, (int)(q & 1));
+    row_sum2<MULTI>(s, t, buf, (int)(q & 1));
     const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(s, inv_d, a.eps));
     const float m = inv * inv * (t * inv_d);  // u i m = u m, with m including both factors i
-    auto grads = [&](int64_t i, const float (&uu)[V], const float (&dd)[V], const float (&ee)[V], const float (&ww)[V],
-                     const float (&gg)[V], float (&pw)[V], float (&pg)[V]) {
-      float o[V], xv[V];
-      if (a.dg) load_vec<In, V>(x + i * V, xv);
+    auto grads = [&](int64_t i, const float (&uu)[V], const float (&dd)[V], const float (&ee)[V], const float (&xx)[V],
+                     const float (&ww)[V], const float (&gg)[V], float (&pw)[V], float (&pg)[V]) {
+      float o[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         pw[j] = dd[j] * (uu[j] * inv);
@@ -269,39 +324,45 @@ __global__ __launch_bounds__(256) void s6_add_norm_bwd_kernel(NormArgs a) {
       if (dr) store_vec<Res, V>(dr + i * V, o);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        pg[j] = a.dg ? a.scale * (o[j] * xv[j]) : 0.0f;
+        pg[j] = a.dg ? a.scale * (o[j] * xx[j]) : 0.0f;
         o[j] *= gg[j];
       }
       if (dx) store_vec<In, V>(dx + i * V, o);
     };
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
       if (on && i < np) {
-        float pw[V], pg[V];
-        grads(i, u[k], d[k], e[k], w[k], ga[k], pw, pg);
+        float u[V], d[V], e[V], xv[V], pw[V], pg[V];
+        dc[k].again();
+        uc[k].get(u);
+        dc[k].get(d);
+        ec[k].get(e);
+        xc[k].get(xv);
+        grads(i, u, d, e, xv, w[k], ga[k], pw, pg);
 #pragma unroll
         for (int j = 0; j < V; ++j) { dw[k][j] += pw[j]; dg[k][j] += pg[j]; }
       }
     }
-    for (int64_t i = (int64_t)kK * TPR + wk.t; on && i < np; i += TPR) {
-      float uu[V], dd[V], ee[V], ww[V], gg[V], pw[V], pg[V];
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
+      float uu[V], dd[V], ee[V], xx[V], ww[V], gg[V], pw[V], pg[V];
       load_vec<Res, V>(res + i * V, uu);
       load_vec<In, V>(dout + i * V, dd);
       if (dres) load_vec<Res, V>(dres + i * V, ee);
+      if (a.dg) load_vec<In, V>(x + i * V, xx);
       load_vec<float, V>(a.w + i * V, ww);
       if (a.gamma) load_vec<float, V>(a.gamma + i * V, gg);
 #pragma unroll
       for (int j = 0; j < V; ++j) gg[j] = a.gamma ? gg[j] * a.scale : a.scale;
-      grads(i, uu, dd, ee, ww, gg, pw, pg);
+      grads(i, uu, dd, ee, xx, ww, gg, pw, pg);
       if (a.dw) part_add<V>(a.dw + wk.wk * a.dim + i * V, pw, q == 0);
       if (a.dg) part_add<V>(a.dg + wk.wk * a.dim + i * V, pg, q == 0);
     }
   }
   if (wk.wk >= a.rows) return;  // no row of its own: its part is not read
 #pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int64_t i = (int64_t)k * TPR + wk.t;
+  for (int k = 0; k < K; ++k) {
+    const int64_t i = (int64_t)k * wk.tpr + wk.t;
     if (i < np) {
       if (a.dw) store_vec<float, V>(a.dw + wk.wk * a.dim + i * V, dw[k]);
       if (a.dg) store_vec<float, V>(a.dg + wk.wk * a.dim + i * V, dg[k]);
@@ -311,34 +372,48 @@ __global__ __launch_bounds__(256) void s6_add_norm_bwd_kernel(NormArgs a) {
 
 // ----------------------------------------------------------- gated norm --
 // blockIdx.y: the group.
-template <typename In, int V, int TPR>
-__global__ __launch_bounds__(256) void s6_gated_norm_kernel(NormArgs a) {
-  __shared__ float buf[2][2][4];
-  const Walk wk = walk_of<TPR>(a.rows);
+template <typename In, int V, int K, bool MULTI, bool WIDE>
+__global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_gated_norm_kernel(NormArgs a) {
+  __shared__ float buf[2][2][kMaxT / 64];
+  const Walk wk = walk_of<MULTI>(a.rows);
   const int64_t np = (a.gd + V - 1) / V, g0 = (int64_t)blockIdx.y * a.gd;
   const float inv_d = 1.0f / (float)a.gd;
-  float w[kK][V];
+  float w[K][V];
 #pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int64_t i = (int64_t)k * TPR + wk.t;
+  for (int k = 0; k < K; ++k) {
+    const int64_t i = (int64_t)k * wk.tpr + wk.t;
     if (i < np) load_vec<float, V>(a.w + g0 + i * V, w[k]);
   }
+  Raw<In, V> yr[K], zr[K];
+  auto issue = [&](int64_t row) {
+    if (row >= a.rows) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      if (i < np) {
+        yr[k].load(static_cast<const In*>(a.a) + row * a.a_stride + g0 + i * V);
+        if (a.b) zr[k].load(static_cast<const In*>(a.b) + row * a.b_stride + g0 + i * V);
+      }
+    }
+  };
+  issue(wk.wk);
   for (int64_t q = 0; q < wk.turns; ++q) {
     const int64_t row = q * wk.nw + wk.wk;
     const bool on = row < a.rows;
     const In* y = static_cast<const In*>(a.a) + row * a.a_stride + g0;
     const In* z = a.b ? static_cast<const In*>(a.b) + row * a.b_stride + g0 : nullptr;
     In* out = static_cast<In*>(a.o1) + row * a.dim + g0;
-    float u[kK][V], zv[kK][V];
+    float u[K][V], zv[K][V];
     float s = 0.0f, unused = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
       if (on && i < np) {
-        load_vec<In, V>(y + i * V, u[k]);
-        if (z) load_vec<In, V>(z + i * V, zv[k]);
+        yr[k].get(u[k]);
+        if (z) zr[k].get(zv[k]);
       }
     }
+    issue(row + wk.nw);
     // what the norm sees, and the factor applied after it
     auto gate = [&](float (&v)[V], float (&f)[V]) {
 #pragma unroll
@@ -349,15 +424,15 @@ __global__ __launch_bounds__(256) void s6_gated_norm_kernel(NormArgs a) {
       }
     };
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
       if (on && i < np) {
         gate(u[k], zv[k]);
 #pragma unroll
         for (int j = 0; j < V; ++j) s = __builtin_fmaf(u[k][j], u[k][j], s);
       }
     }
-    for (int64_t i = (int64_t)kK * TPR + wk.t; on && i < np; i += TPR) {
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
       float v[V], f[V];
       load_vec<In, V>(y + i * V, v);
       if (z) load_vec<In, V>(z + i * V, f);
@@ -365,18 +440,18 @@ __global__ __launch_bounds__(256) void s6_gated_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) s = __builtin_fmaf(v[j], v[j], s);
     }
-    row_sum2<TPR>(s, unused, buf, (int)(q & 1));
+    row_sum2<MULTI>(s, unused, buf, (int)(q & 1));
     const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(s, inv_d, a.eps));
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
       if (on && i < np) {
 #pragma unroll
         for (int j = 0; j < V; ++j) u[k][j] = u[k][j] * inv * w[k][j] * zv[k][j];
         store_vec<In, V>(out + i * V, u[k]);
       }
     }
-    for (int64_t i = (int64_t)kK * TPR + wk.t; on && i < np; i += TPR) {
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
       float v[V], f[V], ww[V];
       load_vec<In, V>(y + i * V, v);
       if (z) load_vec<In, V>(z + i * V, f);
@@ -389,20 +464,34 @@ __global__ __launch_bounds__(256) void s6_gated_norm_kernel(NormArgs a) {
   }
 }
 
-template <typename In, int V, int TPR>
-__global__ __launch_bounds__(256) void s6_gated_norm_bwd_kernel(NormArgs a) {
-  __shared__ float buf[2][2][4];
-  const Walk wk = walk_of<TPR>(a.rows);
+template <typename In, int V, int K, bool MULTI, bool WIDE>
+__global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_gated_norm_bwd_kernel(NormArgs a) {
+  __shared__ float buf[2][2][kMaxT / 64];
+  const Walk wk = walk_of<MULTI>(a.rows);
   const int64_t np = (a.gd + V - 1) / V, g0 = (int64_t)blockIdx.y * a.gd;
   const float inv_d = 1.0f / (float)a.gd;
-  float w[kK][V], dw[kK][V];
+  float w[K][V], dw[K][V];
 #pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int64_t i = (int64_t)k * TPR + wk.t;
+  for (int k = 0; k < K; ++k) {
+    const int64_t i = (int64_t)k * wk.tpr + wk.t;
 #pragma unroll
     for (int j = 0; j < V; ++j) dw[k][j] = 0.0f;
     if (i < np) load_vec<float, V>(a.w + g0 + i * V, w[k]);
   }
+  Raw<In, V> yr[K], zr[K], dr_[K];
+  auto issue = [&](int64_t row) {
+    if (row >= a.rows) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      if (i < np) {
+        yr[k].load(static_cast<const In*>(a.a) + row * a.a_stride + g0 + i * V);
+        dr_[k].load(static_cast<const In*>(a.dout) + row * a.dim + g0 + i * V);
+        if (a.b) zr[k].load(static_cast<const In*>(a.b) + row * a.b_stride + g0 + i * V);
+      }
+    }
+  };
+  issue(wk.wk);
   for (int64_t q = 0; q < wk.turns; ++q) {
     const int64_t row = q * wk.nw + wk.wk;
     const bool on = row < a.rows;
@@ -411,17 +500,8 @@ __global__ __launch_bounds__(256) void s6_gated_norm_bwd_kernel(NormArgs a) {
     const In* dout = static_cast<const In*>(a.dout) + row * a.dim + g0;
     In* dy = static_cast<In*>(a.o1) + row * a.dim + g0;
     In* dz = z ? static_cast<In*>(a.o2) + row * a.dim + g0 : nullptr;
-    float yv[kK][V], zv[kK][V], d[kK][V];
+    Raw<In, V> yc[K], zc[K], dc[K];
     float s = 0.0f, t = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
-      if (on && i < np) {
-        load_vec<In, V>(y + i * V, yv[k]);
-        load_vec<In, V>(dout + i * V, d[k]);
-        if (z) load_vec<In, V>(z + i * V, zv[k]);
-      }
-    }
     // u: what the norm sees; dh: the gradient of its output u i (before w)
     auto sums = [&](const float (&yy)[V], const float (&zz)[V], const float (&dd)[V], const float (&ww)[V]) {
 #pragma unroll
@@ -434,11 +514,19 @@ __global__ __launch_bounds__(256) void s6_gated_norm_bwd_kernel(NormArgs a) {
       }
     };
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
-      if (on && i < np) sums(yv[k], zv[k], d[k], w[k]);
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      yc[k] = yr[k]; zc[k] = zr[k]; dc[k] = dr_[k];
+      if (on && i < np) {
+        float yv[V], zv[V], d[V];
+        yc[k].get(yv);
+        zc[k].get(zv);
+        dc[k].get(d);
+        sums(yv, zv, d, w[k]);
+      }
     }
-    for (int64_t i = (int64_t)kK * TPR + wk.t; on && i < np; i += TPR) {
+    issue(row + wk.nw);
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
       float yy[V], zz[V], dd[V], ww[V];
       load_vec<In, V>(y + i * V, yy);
       load_vec<In, V>(dout + i * V, dd);
@@ -446,7 +534,7 @@ __global__ __launch_bounds__(256) void s6_gated_norm_bwd_kernel(NormArgs a) {
       load_vec<float, V>(a.w + g0 + i * V, ww);
       sums(yy, zz, dd, ww);
     }
-    row_sum2<TPR>(s, t, buf, (int)(q & 1));
+    row_sum2<MULTI>(s, t, buf, (int)(q & 1));
     const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(s, inv_d, a.eps));
     const float m = inv * inv * (t * inv_d);
     auto grads = [&](int64_t i, const float (&yy)[V], const float (&zz)[V], const float (&dd)[V], const float (&ww)[V],
@@ -468,16 +556,22 @@ __global__ __launch_bounds__(256) void s6_gated_norm_bwd_kernel(NormArgs a) {
       if (dz) store_vec<In, V>(dz + i * V, oz);
     };
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int64_t i = (int64_t)k * TPR + wk.t;
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
       if (on && i < np) {
-        float pw[V];
-        grads(i, yv[k], zv[k], d[k], w[k], pw);
+        float yv[V], zv[V], d[V], pw[V];
+        yc[k].again();
+        zc[k].again();
+        dc[k].again();
+        yc[k].get(yv);
+        zc[k].get(zv);
+        dc[k].get(d);
+        grads(i, yv, zv, d, w[k], pw);
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[k][j] += pw[j];
       }
     }
-    for (int64_t i = (int64_t)kK * TPR + wk.t; on && i < np; i += TPR) {
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
       float yy[V], zz[V], dd[V], ww[V], pw[V];
       load_vec<In, V>(y + i * V, yy);
       load_vec<In, V>(dout + i * V, dd);
@@ -489,59 +583,90 @@ __global__ __launch_bounds__(256) void s6_gated_norm_bwd_kernel(NormArgs a) {
   }
   if (wk.wk >= a.rows || !a.dw) return;
 #pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int64_t i = (int64_t)k * TPR + wk.t;
+  for (int k = 0; k < K; ++k) {
+    const int64_t i = (int64_t)k * wk.tpr + wk.t;
     if (i < np) store_vec<float, V>(a.dw + wk.wk * a.dim + g0 + i * V, dw[k]);
   }
 }
 
-// out[c] = sum over parts of part[p][c], in a fixed order: 16 threads per
-// column take every 16th part, then their sums are added.  blockIdx.y picks
-// one of two (parts, out) pairs.
+// out[c] = sum over parts of part[p][c], in a fixed order: 64 threads per
+// column take every 64th part, then their sums are added.  blockIdx.y picks
+// one of two (parts, out) pairs.  16 columns per workgroup (64 contiguous
+// bytes of each part): enough workgroups for the few thousand columns there
+// are (64 columns with 16 threads each took 27 us for 1024 parts of 2 x 2560).
 __global__ __launch_bounds__(1024) void s6_norm_colsum(const float* p0, float* o0, const float* p1, float* o1,
                                                        int64_t parts, int64_t dim) {
-  __shared__ float buf[16][64];
+  __shared__ float buf[64][17];
   const float* p = blockIdx.y ? p1 : p0;
   float* o = blockIdx.y ? o1 : o0;
   if (!o) return;
-  const int l = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + l;
+  const int l = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + l;
   float s = 0.0f;
-  if (c < dim)
-    for (int64_t i = r; i < parts; i += 16) s += p[i * dim + c];
+  if (c < dim) {
+#pragma unroll 4
+    for (int64_t i = r; i < parts; i += 64) s += p[i * dim + c];
+  }
   buf[r][l] = s;
   __syncthreads();
-  if (r == 0 && c < dim) {
-    s = buf[0][l];
-    for (int i = 1; i < 16; ++i) s += buf[i][l];
-    o[c] = s;
+  if (threadIdx.x < 256) {  // 16 threads per column
+    const int cc = threadIdx.x >> 4, k = threadIdx.x & 15;
+    s = (buf[k][cc] + buf[k + 16][cc]) + (buf[k + 32][cc] + buf[k + 48][cc]);
+    s = row_sum(s);
+    const int64_t co = (int64_t)blockIdx.x * 16 + cc;
+    if (k == 0 && co < dim) o[co] = s;
   }
 }
 
-// Threads per row: a wave where its registers hold the row (512 values with
-// 16-byte pieces per register piece), else a workgroup.
-int tpr_of(int64_t width, bool vec) { return width <= (int64_t)kK * 64 * (vec ? 8 : 1) ? 64 : 256; }
-
-// Workgroups along the rows: at most most_parts walkers where column sums are
-// taken, else enough for every CU to hold eight.
-int64_t walk_blocks(int64_t rows, int64_t width, int tpr, bool sums) {
-  const int64_t per = 256 / tpr;
-  const int64_t need = (rows + per - 1) / per;
-  const int64_t most = sums ? most_parts(width, tpr) / per : (int64_t)cu_count() * 8;
-  return need < most ? need : most;
+// How rows of `width` values are shared out: the pieces' size and number per
+// thread, threads of a workgroup, rows per workgroup.
+struct NormPlan {
+  bool vec, multi, wide;  // wide: a row does not fit the registers
+  int K, threads, per;
+  int64_t blocks;
+};
+// A wave per row up to 512 values (256 without 16-byte accesses); above, one
+// piece per thread (four single values without 16-byte accesses) up to 1024
+// threads; wider rows take 512 threads of two pieces and read the rest again.
+// More threads with fewer values each leave room for more waves: with 256
+// threads of up to four pieces, the training pass of 16384 rows of 2560 took
+// 383 us (200 VGPRs and more, 1 or 2 waves per SIMD).
+NormPlan norm_plan(int64_t rows, int64_t width, bool vec, bool sums) {
+  NormPlan p;
+  p.vec = vec;
+  const int64_t np = vec ? width / 8 : width;
+  p.K = vec ? (np <= kMaxT ? 1 : 2) : 4;
+  p.multi = np <= 64 * p.K;
+  const int64_t most_t = p.K == 2 ? 512 : kMaxT;
+  int64_t t = (np + p.K - 1) / p.K;
+  t = (t + 63) / 64 * 64;
+  p.threads = p.multi ? 256 : (int)(t < most_t ? t : most_t);
+  p.per = p.multi ? 4 : 1;
+  p.wide = !p.multi && np > (int64_t)p.K * p.threads;
+  const int64_t need = (rows + p.per - 1) / p.per;
+  // enough workgroups to fill the CUs with 2048 threads each, where column sums
+  // are taken at most kParts walkers
+  int64_t most = (int64_t)cu_count() * (2048 / p.threads);
+  if (sums && most > kParts / p.per) most = kParts / p.per;
+  p.blocks = need < most ? need : most;
+  return p;
 }
 
-#define S6_LAUNCH_NORM(kernel, ...)                                                                              \
-  do {                                                                                                           \
-    if (vec && tpr == 64) hipLaunchKernelGGL((kernel<__VA_ARGS__, 8, 64>), grid, dim3(256), 0, st, a);           \
-    else if (vec) hipLaunchKernelGGL((kernel<__VA_ARGS__, 8, 256>), grid, dim3(256), 0, st, a);                  \
-    else if (tpr == 64) hipLaunchKernelGGL((kernel<__VA_ARGS__, 1, 64>), grid, dim3(256), 0, st, a);             \
-    else hipLaunchKernelGGL((kernel<__VA_ARGS__, 1, 256>), grid, dim3(256), 0, st, a);                           \
-    S6_HIP(hipGetLastError(), #kernel " launch");                                                                \
+#define S6_LAUNCH_NORM(kernel, ...)                                                                            \
+  do {                                                                                                         \
+    const dim3 block((unsigned)p.threads);                                                                     \
+    if (!p.vec) {                                                                                              \
+      if (p.multi) hipLaunchKernelGGL((kernel<__VA_ARGS__, 1, 4, true, false>), grid, block, 0, st, a);        \
+      else if (!p.wide) hipLaunchKernelGGL((kernel<__VA_ARGS__, 1, 4, false, false>), grid, block, 0, st, a);  \
+      else hipLaunchKernelGGL((kernel<__VA_ARGS__, 1, 4, false, true>), grid, block, 0, st, a);                \
+    } else if (p.multi) hipLaunchKernelGGL((kernel<__VA_ARGS__, 8, 1, true, false>), grid, block, 0, st, a);   \
+    else if (p.K == 1) hipLaunchKernelGGL((kernel<__VA_ARGS__, 8, 1, false, false>), grid, block, 0, st, a);   \
+    else hipLaunchKernelGGL((kernel<__VA_ARGS__, 8, 2, false, true>), grid, block, 0, st, a);                  \
+    S6_HIP(hipGetLastError(), #kernel " launch");                                                              \
   } while (0)
 
 int launch_colsum(const float* p0, float* o0, const float* p1, float* o1, int64_t parts, int64_t dim, hipStream_t st) {
-  hipLaunchKernelGGL(s6_norm_colsum, dim3((unsigned)((dim + 63) / 64), 2), dim3(1024), 0, st, p0, o0, p1, o1, parts,
+  hipLaunchKernelGGL(s6_norm_colsum, dim3((unsigned)((dim + 15) / 16), 2), dim3(1024), 0, st, p0, o0, p1, o1, parts,
                      dim);
   S6_HIP(hipGetLastError(), "s6_norm_colsum launch");
   return S6_OK;
@@ -561,10 +686,9 @@ int check_norm(int64_t rows, int64_t dim, int64_t groups, int in_dtype, int64_t 
 // Rows start on 16-byte boundaries.
 bool row_vec(const void* p, int64_t stride, size_t esz) { return aligned(p, 16) && (stride * (int64_t)esz) % 16 == 0; }
 
-// Room for the parts of one column sum over groups of `width` columns.
-size_t part_bytes(int64_t rows, int64_t dim, int64_t width) {
-  const int64_t most = most_parts(width, 64);
-  return up256((size_t)(rows < most ? rows : most) * (size_t)dim * sizeof(float));
+// Room for the parts of one column sum.
+size_t part_bytes(int64_t rows, int64_t dim) {
+  return up256((size_t)(rows < kParts ? rows : kParts) * (size_t)dim * sizeof(float));
 }
 
 }  // namespace
@@ -593,8 +717,8 @@ int s6_add_norm_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, cons
   memset(&a, 0, sizeof(a));
   a.rows = rows; a.dim = dim; a.gd = dim; a.a = x; a.a_stride = x_stride; a.b = residual; a.w = weight; a.gamma = gamma;
   a.scale = scale; a.eps = eps; a.o1 = out; a.o2 = residual_out;
-  const int tpr = tpr_of(dim, vec);
-  const dim3 grid((unsigned)walk_blocks(rows, dim, tpr, false));
+  const NormPlan p = norm_plan(rows, dim, vec, false);
+  const dim3 grid((unsigned)p.blocks);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (in_dtype == S6_F32) S6_LAUNCH_NORM(s6_add_norm_kernel, float, float);
   else if (res_dtype == S6_F32) S6_LAUNCH_NORM(s6_add_norm_kernel, uint16_t, float);
@@ -606,7 +730,7 @@ int s6_add_norm_bwd_workspace_size(int64_t rows, int64_t dim, size_t* bytes) {
   if (!bytes) return S6_ERR_NULL;
   const int rc = check_norm(rows, dim, 1, S6_F32, dim, dim);
   if (rc) return rc;
-  *bytes = rows ? 2 * part_bytes(rows, dim, dim) : 0;
+  *bytes = rows ? 2 * part_bytes(rows, dim) : 0;
   return S6_OK;
 }
 
@@ -631,7 +755,7 @@ int s6_add_norm_bwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, cons
       !aligned(residual_out, rsz) || !aligned(dresidual, rsz) || !aligned(weight, 4) || !aligned(gamma, 4) ||
       !aligned(dweight, 4) || !aligned(dgamma, 4))
     return S6_ERR_ALIGN;
-  const size_t part = part_bytes(rows, dim, dim);
+  const size_t part = part_bytes(rows, dim);
   const bool sums = dweight || dgamma;
   if (sums) {
     if (!workspace || workspace_bytes < 2 * part) return S6_ERR_WORKSPACE;
@@ -646,14 +770,13 @@ int s6_add_norm_bwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, cons
   a.res = residual_out; a.w = weight; a.gamma = gamma; a.scale = scale; a.eps = eps; a.o1 = dx; a.o2 = dresidual;
   a.dw = dweight ? static_cast<float*>(workspace) : nullptr;
   a.dg = dgamma ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part) : nullptr;
-  const int tpr = tpr_of(dim, vec);
-  const int64_t blocks = walk_blocks(rows, dim, tpr, sums);
-  const dim3 grid((unsigned)blocks);
+  const NormPlan p = norm_plan(rows, dim, vec, sums);
+  const dim3 grid((unsigned)p.blocks);
   if (in_dtype == S6_F32) S6_LAUNCH_NORM(s6_add_norm_bwd_kernel, float, float);
   else if (res_dtype == S6_F32) S6_LAUNCH_NORM(s6_add_norm_bwd_kernel, uint16_t, float);
   else S6_LAUNCH_NORM(s6_add_norm_bwd_kernel, uint16_t, uint16_t);
   if (!sums) return S6_OK;
-  const int64_t walkers = blocks * (256 / tpr), parts = walkers < rows ? walkers : rows;
+  const int64_t walkers = p.blocks * p.per, parts = walkers < rows ? walkers : rows;
   return launch_colsum(a.dw, dweight, a.dg, dgamma, parts, dim, st);
 }
 
@@ -673,8 +796,8 @@ int s6_gated_norm_fwd(int64_t rows, int64_t dim, int64_t groups, int in_dtype, i
   memset(&a, 0, sizeof(a));
   a.rows = rows; a.dim = dim; a.gd = dim / groups; a.a = y; a.a_stride = y_stride; a.b = z; a.b_stride = z_stride;
   a.w = weight; a.eps = eps; a.after = (flags & S6_GATE_AFTER) != 0; a.o1 = out;
-  const int tpr = tpr_of(a.gd, vec);
-  const dim3 grid((unsigned)walk_blocks(rows, dim, tpr, false), (unsigned)groups);
+  const NormPlan p = norm_plan(rows, a.gd, vec, false);
+  const dim3 grid((unsigned)p.blocks, (unsigned)groups);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (in_dtype == S6_F32) S6_LAUNCH_NORM(s6_gated_norm_kernel, float);
   else S6_LAUNCH_NORM(s6_gated_norm_kernel, uint16_t);
@@ -685,7 +808,7 @@ int s6_gated_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t groups, 
   if (!bytes) return S6_ERR_NULL;
   const int rc = check_norm(rows, dim, groups, S6_F32, dim, dim);
   if (rc) return rc;
-  *bytes = rows ? part_bytes(rows, dim, dim / groups) : 0;
+  *bytes = rows ? part_bytes(rows, dim) : 0;
   return S6_OK;
 }
 
@@ -707,7 +830,7 @@ int s6_gated_norm_bwd(int64_t rows, int64_t dim, int64_t groups, int in_dtype, i
       !aligned(weight, 4) || !aligned(dweight, 4))
     return S6_ERR_ALIGN;
   if (dweight) {
-    if (!workspace || workspace_bytes < part_bytes(rows, dim, dim / groups)) return S6_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < part_bytes(rows, dim)) return S6_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return S6_ERR_ALIGN;
   }
   const bool vec = (dim / groups) % 8 == 0 && aligned(dout, 16) && row_vec(y, y_stride, esz) &&
@@ -717,13 +840,12 @@ int s6_gated_norm_bwd(int64_t rows, int64_t dim, int64_t groups, int in_dtype, i
   a.rows = rows; a.dim = dim; a.gd = dim / groups; a.a = y; a.a_stride = y_stride; a.b = z; a.b_stride = z_stride;
   a.dout = dout; a.w = weight; a.eps = eps; a.after = (flags & S6_GATE_AFTER) != 0; a.o1 = dy; a.o2 = dz;
   a.dw = dweight ? static_cast<float*>(workspace) : nullptr;
-  const int tpr = tpr_of(a.gd, vec);
-  const int64_t blocks = walk_blocks(rows, a.gd, tpr, dweight != nullptr);
-  const dim3 grid((unsigned)blocks, (unsigned)groups);
+  const NormPlan p = norm_plan(rows, a.gd, vec, dweight != nullptr);
+  const dim3 grid((unsigned)p.blocks, (unsigned)groups);
   if (in_dtype == S6_F32) S6_LAUNCH_NORM(s6_gated_norm_bwd_kernel, float);
   else S6_LAUNCH_NORM(s6_gated_norm_bwd_kernel, uint16_t);
   if (!dweight) return S6_OK;
-  const int64_t walkers = blocks * (256 / tpr), parts = walkers < rows ? walkers : rows;
+  const int64_t walkers = p.blocks * p.per, parts = walkers < rows ? walkers : rows;
   return launch_colsum(a.dw, dweight, nullptr, nullptr, parts, dim, st);
 }
 
