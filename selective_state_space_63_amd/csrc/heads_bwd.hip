@@ -71,16 +71,13 @@ struct BwdLds {
   static constexpr int ys = xs + XT::size(Q) * (int)sizeof(In);
   static constexpr int lm = ys + XT::size(Q) * (int)sizeof(In);
   static constexpr int mf = lm + LT::size(NT) * (int)sizeof(In);
-  static constexpr int rp = mf + NFRAG * 512 * (int)sizeof(In);  // row sums of the tiles
-  static constexpr int cp = rp + NTILE * 16 * 4;                 // column sums
-  static constexpr int yp = cp + NTILE * 16 * 4;                 // dy . S C by strip
-  static constexpr int up = yp + NS * Q * 4;                     // x . L B by strip
-  static constexpr int cs = up + NS * Q * 4;
-  static constexpr int ec = cs + Q * 4;
-  static constexpr int ww = ec + Q * 4;
-  static constexpr int wd = ww + Q * 4;
-  static constexpr int th = wd + Q * 4;    // <L, S> by strip
-  static constexpr int dd = th + 8 * 4;    // x . dy by diagonal tile
+  static constexpr int rp = mf + NFRAG * 512 * (int)sizeof(In);  // row sums by column tile (token, tile)
+  static constexpr int cp = rp + Q * NTT * 4;                    // column sums by row tile (token, tile)
+  static constexpr int yp = cp + Q * NTT * 4;                    // dy . S C by strip (token, strip)
+  static constexpr int up = yp + NS * Q * 4;                     // x . L B by strip (token, strip)
+  static constexpr int tok = up + NS * Q * 4;                    // per-token values, two turns' worth
+  static constexpr int th = tok + 2 * 6 * Q * 4;                 // <L, S> by strip
+  static constexpr int dd = th + 8 * 4;                          // x . dy by diagonal tile
   static constexpr int total = dd + 8 * 4;
   static_assert(total <= 163840, "LDS");
 };
@@ -99,7 +96,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   constexpr int Q = O::Q, NTT = O::NTT, H = O::H, NS = O::NS, NK = NT / 32;
   constexpr int TPN = 8 / NS, TT = NTT / TPN;       // token parts of the strips, tiles per part
   constexpr int SLOTS = (O::NTILE + 7) / 8;         // Gram tiles per wave
-  constexpr int PL = Q / 64;                        // tokens per lane of wave 0
+  constexpr int PL = Q / 64;                        // tokens per lane of a wave
   extern __shared__ __align__(16) char lds[];
   const typename O::BT bs{reinterpret_cast<In*>(lds + O::bs)}, cm{reinterpret_cast<In*>(lds + O::cm)};
   const typename O::XT xs{reinterpret_cast<In*>(lds + O::xs)}, ys{reinterpret_cast<In*>(lds + O::ys)};
@@ -109,24 +106,22 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   float* cp = reinterpret_cast<float*>(lds + O::cp);
   float* yp = reinterpret_cast<float*>(lds + O::yp);
   float* up = reinterpret_cast<float*>(lds + O::up);
-  float* cs = reinterpret_cast<float*>(lds + O::cs);
-  float* ec = reinterpret_cast<float*>(lds + O::ec);
-  float* ww = reinterpret_cast<float*>(lds + O::ww);
-  float* wd = reinterpret_cast<float*>(lds + O::wd);
+  float* tok = reinterpret_cast<float*>(lds + O::tok);
   float* th = reinterpret_cast<float*>(lds + O::th);
   float* ddp = reinterpret_cast<float*>(lds + O::dd);
 
   const HeadsArgs& a = ba.h;
-  int64_t id = blockIdx.x;
-  const int64_t blk = id % ba.nblk;
-  id /= ba.nblk;
-  const int hb = (int)(id % ba.nhb);
-  id /= ba.nhb;
-  const int grp = (int)(id % ba.groups);
-  const int64_t b = id / ba.groups;
+  uint32_t id = blockIdx.x;  // (sequence, group, head run, block), the block fastest; below 2^31
+  const uint32_t nb = (uint32_t)ba.nblk;
+  const int64_t blk = __builtin_amdgcn_readfirstlane(id % nb);
+  id /= nb;
+  const int hb = __builtin_amdgcn_readfirstlane(id % (uint32_t)ba.nhb);
+  id /= (uint32_t)ba.nhb;
+  const int grp = __builtin_amdgcn_readfirstlane(id % (uint32_t)ba.groups);
+  const int64_t b = __builtin_amdgcn_readfirstlane(id / (uint32_t)ba.groups);
   const int lane0 = threadIdx.x & 63, wv = wave_index(), g0 = lane0 >> 4, c0 = lane0 & 15;
   int lane = lane0, g = g0, c = c0;
-  const int ns = wv % NS, tp = wv / NS;
+  const int ns = wv % NS, tp = TPN == 1 ? 0 : wv / NS;
   const int64_t t0 = blk * Q;
   const int rows = (int)(a.L - t0 < Q ? a.L - t0 : Q);
   const int64_t hp = (int64_t)a.heads * a.headdim;
@@ -144,25 +139,62 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
     br.store(bs);
     cr.store(cm);
   }
-  for (int i = threadIdx.x; i < O::NFRAG * 512; i += 512) mf[i] = In(0);  // halves above the diagonal stay 0
+  // what lies above the diagonal stays 0
+  for (int i = threadIdx.x; i < O::NFRAG * 512; i += 512) mf[i] = In(0);
+  for (int i = threadIdx.x; i < Q * NTT; i += 512) rp[i] = cp[i] = 0.0f;
+  // and what lies past the sequence: its token tiles are left out below
+  for (int i = threadIdx.x; i < Q * NS; i += 512) yp[i] = up[i] = 0.0f;
+  if (threadIdx.x < 8) ddp[threadIdx.x] = 0.0f;
 
   TileRegs<In, Q, kTP, 512, VEC> xr, yr;
-  In draw[PL];  // as loaded: a conversion there would wait for every load before it
   auto issue = [&](int hd, int pt) {
-    const bool on = hd < hd1;
-    const int cols = a.headdim - pt * kTP;
+    const int on = hd < hd1 ? rows : 0, cols = a.headdim - pt * kTP;
     const int64_t col = (int64_t)hd * a.headdim + pt * kTP;
-    xr.load(static_cast<const In*>(a.x) + b * a.x_batch + t0 * a.x_token + col, a.x_token, on ? rows : 0,
-            cols < kTP ? cols : kTP);
-    yr.load(static_cast<const In*>(a.dy) + (b * a.L + t0) * hp + col, hp, on ? rows : 0, cols < kTP ? cols : kTP);
-    if (a.delta && wv == 0 && on) {
-#pragma unroll
-      for (int k = 0; k < PL; ++k)
-        if (k * 64 + lane < rows)
-          draw[k] = static_cast<const In*>(a.delta)[b * a.d_batch + (t0 + k * 64 + lane) * a.d_token + hd];
-    }
+    xr.load(static_cast<const In*>(a.x) + b * a.x_batch + t0 * a.x_token + col, a.x_token, on, cols < kTP ? cols : kTP);
+    yr.load(static_cast<const In*>(a.dy) + (b * a.L + t0) * hp + col, hp, on, cols < kTP ? cols : kTP);
   };
+  // The last wave forms a head's per-token values a turn ahead: running log2
+  // decay, its exponential, input weight, decay to the block's end, step, and
+  // the step's derivative.
+  // (from steps loaded another turn earlier, kept as loaded).
+  In draw[PL];
+  auto issue_step = [&](int hd) {
+    if (wv != 7 || hd >= hd1 || !a.delta) return;
+#pragma unroll
+    for (int k = 0; k < PL; ++k)
+      if (k * 64 + lane < rows)
+        draw[k] = static_cast<const In*>(a.delta)[b * a.d_batch + (t0 + k * 64 + lane) * a.d_token + hd];
+  };
+  // the head of the turn after (hd, pt)
+  auto after = [&](int hd, int pt) { return pt + 1 == a.ptiles ? hd + 1 : hd; };
+  auto decays = [&](int hd, int buf) {
+    if (wv != 7 || hd >= hd1) return;
+    const float bias = a.dbias ? a.dbias[hd] : 0.0f, a2 = a.A[hd] * kLog2e;
+    float* o = tok + buf * 6 * Q;
+    float base = 0.0f, cl[PL];
+#pragma unroll
+    for (int k = 0; k < PL; ++k) {
+      const int t = k * 64 + lane;
+      const bool on = t < rows;
+      const float v = to_f32(draw[k]) + bias;
+      const float sv = on ? step_of(a, to_f32(draw[k]), bias) : 0.0f;
+      cl[k] = base + wave_scan(on ? clamp_log2(sv * a2) : 0.0f);
+      base = last_lane(cl[k]);
+      o[t] = cl[k];
+      o[Q + t] = fast_exp2(cl[k]);
+      o[2 * Q + t] = on ? (a.unit ? 1.0f : sv) : 0.0f;
+      o[4 * Q + t] = sv;
+      o[5 * Q + t] = a.softplus ? fast_rcp(1.0f + fast_exp2(-v * kLog2e)) : 1.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < PL; ++k) o[3 * Q + k * 64 + lane] = fast_exp2(base - cl[k]);
+  };
+#pragma unroll
+  for (int k = 0; k < PL; ++k) draw[k] = In(0);
+  issue_step(hd0);
   issue(hd0, 0);
+  decays(hd0, 0);
+  issue_step(after(hd0, 0));
   __syncthreads();
 
   // Gram tiles of this wave (rows t of tile I, columns s of tile J <= I)
@@ -188,15 +220,61 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
 #pragma unroll
   for (int i = 0; i < TT; ++i) dC[i] = dB[i] = f32x4{0, 0, 0, 0};
 
-  float acc_g[PL], acc_ds[PL], acc_d = 0.0f;  // wave 0: sums over the channel tiles of a head
+  float acc_g[PL], acc_ds[PL], acc_d = 0.0f;  // wave 4: sums over the channel tiles of a head
 #pragma unroll
   for (int k = 0; k < PL; ++k) acc_g[k] = acc_ds[k] = 0.0f;
 
+  // dx of a turn is stored in the next one, behind the wait for its inputs
+  // (stores before it would be waited for as well)
+  Four<In> dxv[NTT / 2];
+  auto put_dx = [&](int hd, int pt) {
+    const int q = wv & 3, pleft = a.headdim - pt * kTP;
+    In* const base = static_cast<In*>(ba.dx) + (b * a.L + t0) * hp + (int64_t)hd * a.headdim + pt * kTP + 16 * q;
+    const uint32_t off = ((uint32_t)c * (uint32_t)hp + 4 * g) * (uint32_t)sizeof(In);
+    const int p = 16 * q + 4 * g;
+    if (VEC && rows == Q && pleft >= kTP) {
+#pragma unroll
+      for (int i = 0; i < NTT / 2; ++i) dxv[i].store(scalar_base(base + 16 * (2 * i + (wv >> 2)) * hp) + off);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < NTT / 2; ++i) {
+      const int s0 = 16 * (2 * i + (wv >> 2));
+      if (s0 + c < rows) {
+        const gbytes dp = scalar_base(base + s0 * hp) + off;
+        if constexpr (VEC) {
+          if (p < pleft) dxv[i].store(dp);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (p + r < pleft) reinterpret_cast<In __attribute__((address_space(1)))*>(dp)[r] = dxv[i].get(r);
+        }
+      }
+    }
+  };
+  // A head's stored states (S; L lies nblk rows tiles behind).  touch() reads
+  // one word of each of their cache lines a turn ahead, so that they come from
+  // L2 when the operands are loaded: held in registers from there on, they
+  // would not leave room for the sums.
+  constexpr int64_t kTile = (int64_t)kTP * NT * (sizeof(In) == 2 ? 2 : 1);
+  auto state_at = [&](int hd, int pt) {
+    const int64_t row = (b * a.heads + hd) * (int64_t)a.ptiles + pt;
+    return static_cast<const In*>(a.planes) + (blk * ba.rows + row) * kTile;
+  };
+  uint32_t touched = 0;
+  auto touch = [&](int hd, int pt) {
+    constexpr int kLines = (int)(kTile * sizeof(In) / 128);
+    static_assert(kLines <= 256, "one line of S and L per thread");
+    if (hd < hd1 && (threadIdx.x & 255) < kLines) {
+      const In* sp = state_at(hd, pt) + (threadIdx.x >> 8) * (ba.nblk * ba.rows * kTile);
+      touched = reinterpret_cast<const uint32_t*>(sp)[(threadIdx.x & 255) * 32];
+    }
+  };
+  int buf = 0;
   for (int hd = hd0; hd < hd1; ++hd) {
-    const float bias = a.dbias ? a.dbias[hd] : 0.0f;
-    const float Ah = a.A[hd], a2 = Ah * kLog2e;
+    const float Ah = a.A[hd];
     const float dsk = a.D ? a.D[hd] : 0.0f;
-    for (int pt = 0; pt < a.ptiles; ++pt) {
+    for (int pt = 0; pt < a.ptiles; ++pt, buf ^= 1) {
       const bool last_pt = pt + 1 == a.ptiles;
       // LDS addresses are formed again in every turn: kept across it they
       // would not leave room for the sums
@@ -205,57 +283,41 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       g = lane >> 4; c = lane & 15;
       const int x_row = O::XT::row_lane(g, c), b_row = O::BT::row_lane(g, c);
       const int p0 = pt * kTP, pleft = a.headdim - p0;
+      asm volatile("" ::"v"(touched));
       xr.mask(rows, pleft < kTP ? pleft : kTP);
       yr.mask(rows, pleft < kTP ? pleft : kTP);
       xr.store(xs);
       yr.store(ys);
-      float sv[PL], vd[PL];  // wave 0: the tokens' steps and their derivatives
-      if (wv == 0) {
-        float base = 0.0f, cl[PL];
-#pragma unroll
-        for (int k = 0; k < PL; ++k) {
-          const bool on = k * 64 + lane < rows;
-          const float v = (on && a.delta ? to_f32(draw[k]) : 0.0f) + bias;
-          sv[k] = on ? step_of(a, to_f32(draw[k]), bias) : 0.0f;
-          vd[k] = a.softplus ? fast_rcp(1.0f + fast_exp2(-v * kLog2e)) : 1.0f;
-          cl[k] = base + wave_scan(on ? clamp_log2(sv[k] * a2) : 0.0f);
-          base = last_lane(cl[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < PL; ++k) {
-          const int t = k * 64 + lane;
-          cs[t] = cl[k];
-          ec[t] = fast_exp2(cl[k]);
-          ww[t] = t < rows ? (a.unit ? 1.0f : sv[k]) : 0.0f;
-          wd[t] = fast_exp2(base - cl[k]);
-        }
-      }
-      // states entering the block: this wave's strip of n, all 64 channels
-      Pair<In> Sf[2], Lf[2];
-      {
-        const int64_t row = ((b * a.heads + hd) * (int64_t)a.ptiles + pt);
-        constexpr int64_t kTile = (int64_t)kTP * NT * (sizeof(In) == 2 ? 2 : 1);
-        const In* sp = static_cast<const In*>(a.planes) + (blk * ba.rows + row) * kTile;
-        const In* lp = sp + ba.nblk * ba.rows * kTile;
-#pragma unroll
-        for (int pp = 0; pp < 2; ++pp) {
-          const int64_t at = ((ns * 2 + pp) * 64) * 8;
-          Sf[pp].hi = lane_frag(sp + at, lane);
-          Lf[pp].hi = lane_frag(lp + at, lane);
-          if constexpr (sizeof(In) == 2) {
-            Sf[pp].lo = lane_frag(sp + kTP * NT + at, lane);
-            Lf[pp].lo = lane_frag(lp + kTP * NT + at, lane);
-          }
-        }
-      }
+      if (hd > hd0 || pt > 0) put_dx(pt > 0 ? hd : hd - 1, pt > 0 ? pt - 1 : a.ptiles - 1);
+      const float* cs = tok + buf * 6 * Q;
+      const float *ec = cs + Q, *ww = cs + 2 * Q, *wd = cs + 3 * Q;
       __syncthreads();
-      issue(last_pt ? hd + 1 : hd, last_pt ? 0 : pt + 1);
+      decays(after(hd, pt), buf ^ 1);
+      issue_step(last_pt ? after(hd + 1, 0) : after(hd, pt + 1));
+      touch(after(hd, pt), last_pt ? 0 : pt + 1);
 
       // inside the block
+      Pair<In> Sf[2], Lf[2];
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k) {
+        if (k == SLOTS - 1) {
+          // states entering the block: this wave's strip of n, all 64 channels
+          // (touched a turn ago: they come from L2)
+          const In* sp = state_at(hd, pt) + ns * 1024;
+          const In* lp = sp + ba.nblk * ba.rows * kTile;
+          const uint32_t off = (uint32_t)lane * 8 * (uint32_t)sizeof(In);
+#pragma unroll
+          for (int pp = 0; pp < 2; ++pp) {
+            load_frag(scalar_base(sp + pp * 512) + off, Sf[pp].hi);
+            load_frag(scalar_base(lp + pp * 512) + off, Lf[pp].hi);
+            if constexpr (sizeof(In) == 2) {
+              load_frag(scalar_base(sp + kTP * NT + pp * 512) + off, Sf[pp].lo);
+              load_frag(scalar_base(lp + kTP * NT + pp * 512) + off, Lf[pp].lo);
+            }
+          }
+        }
         const int n = 8 * k + wv;
-        if (n < O::NTILE) {
+        if (n < O::NTILE && 16 * tI[k] < rows) {
           const int I = tI[k], J = tJ[k];
           f32x4 X = {0, 0, 0, 0};
 #pragma unroll
@@ -280,16 +342,41 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
           store_vec<In, 4>(mf + frag_at<H>(J, I >> 1) * 512 + lane * 8 + 4 * (I & 1), m);
 #pragma unroll
           for (int r = 0; r < 4; ++r) er[r] = row_sum(er[r]);
-          if (c == 0) store_vec<float, 4>(rp + n * 16 + 4 * g, er);
-          col = half_sum(pair_row_sum(col));
-          if (g == 0) cp[n * 16 + c] = col;
-          if (I == J && ba.want_d) {
-            diag = wave_sum(diag);
-            if (lane == 0) ddp[I] = diag;
-          }
+          // (every lane of a sum writes it: the same value to the same place)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) rp[(16 * I + 4 * g + r) * NTT + J] = er[r];
+          cp[(16 * J + c) * NTT + I] = half_sum(pair_row_sum(col));
+          if (I == J && ba.want_d) ddp[I] = wave_sum(diag);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      // from before and to after the block
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        const int t = 16 * (tp * TT + i) + c;
+        if (t - c >= rows) continue;
+        f32x4 U = {0, 0, 0, 0}, V = {0, 0, 0, 0};
+#pragma unroll
+        for (int pp = 0; pp < 2; ++pp) {
+          U = mma_pair(Sf[pp], ys.row(x_row, t - c, pp), U);
+          V = mma_pair(Lf[pp], xs.row(x_row, t - c, pp), V);
+        }
+        float cv[4], bv[4], sy = 0.0f, su = 0.0f;
+        cm.four(t, 4 * ns + g, cv);
+        bs.four(t, 4 * ns + g, bv);
+        const float e = ec[t], f = wd[t], fw = ww[t] * f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sy = __builtin_fmaf(cv[r], U[r], sy);
+          su = __builtin_fmaf(bv[r], V[r], su);
+          dC[i][r] = __builtin_fmaf(e, U[r], dC[i][r]);
+          dB[i][r] = __builtin_fmaf(fw, V[r], dB[i][r]);
+        }
+        yp[t * NS + ns] = e * half_sum(pair_row_sum(sy));
+        up[t * NS + ns] = f * half_sum(pair_row_sum(su));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+
       if (tp == 0) {
 #pragma unroll
         for (int pp = 0; pp < 2; ++pp) {
@@ -308,40 +395,10 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
             if constexpr (sizeof(In) == 2) { sf += frag_f32(Sf[pp].lo, e); lf += frag_f32(Lf[pp].lo, e); }
             s = __builtin_fmaf(sf, lf, s);
           }
-        s = wave_sum(s);
-        if (lane == 0) th[ns] = s;
+        th[ns] = wave_sum(s);
       }
       __syncthreads();
-
-      // from before and to after the block
-#pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        const int t = 16 * (tp * TT + i) + c;
-        f32x4 U = {0, 0, 0, 0}, V = {0, 0, 0, 0};
-#pragma unroll
-        for (int pp = 0; pp < 2; ++pp) {
-          U = mma_pair(Sf[pp], ys.row(x_row, t - c, pp), U);
-          V = mma_pair(Lf[pp], xs.row(x_row, t - c, pp), V);
-        }
-        float cv[4], bv[4], sy = 0.0f, su = 0.0f;
-        cm.four(t, 4 * ns + g, cv);
-        bs.four(t, 4 * ns + g, bv);
-        const float e = ec[t], f = wd[t], fw = ww[t] * f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          sy = __builtin_fmaf(cv[r], U[r], sy);
-          su = __builtin_fmaf(bv[r], V[r], su);
-          dC[i][r] = __builtin_fmaf(e, U[r], dC[i][r]);
-          dB[i][r] = __builtin_fmaf(fw, V[r], dB[i][r]);
-        }
-        sy = half_sum(pair_row_sum(sy));
-        su = half_sum(pair_row_sum(su));
-        if (g == 0) {
-          yp[ns * Q + t] = e * sy;
-          up[ns * Q + t] = f * su;
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      issue(after(hd, pt), last_pt ? 0 : pt + 1);
 
       // dx, transposed: channels of tile q, tokens of tiles J
       {
@@ -352,51 +409,51 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
         for (int kk = 0; kk < NK; ++kk) lq[kk] = lm.col(l_col, q, kk, g, c);
 #pragma unroll
         for (int kk = 0; kk < H; ++kk) yq[kk] = ys.col(q, kk, g, c);
-        const int p = 16 * q + 4 * g;
 #pragma unroll
         for (int i = 0; i < NTT / 2; ++i) {
           const int J = 2 * i + (wv >> 2), s = 16 * J + c;
+          if (16 * J >= rows) continue;
           f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
           for (int kk = 0; kk < NK; ++kk) acc = mma(lq[kk], bs.row(b_row, 16 * J, kk), acc);
           acc *= ww[s] * wd[s];
 #pragma unroll
           for (int kk = i; kk < H; ++kk) acc = mma(yq[kk], lane_frag(mf + frag_at<H>(J, kk) * 512, lane), acc);
-          float dyv[4], o[4];
+          float dyv[4];
           ys.four(s, 4 * q + g, dyv);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(dsk, dyv[r], acc[r]);
-          if (s < rows) {
-            In* dp = static_cast<In*>(ba.dx) + (b * a.L + t0 + s) * hp + (int64_t)hd * a.headdim + p0 + p;
-            if constexpr (VEC) {
-              if (p < pleft) store_vec<In, 4>(dp, o);
-            } else {
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (p + r < pleft) dp[r] = from_f32<In>(o[r]);
-            }
-          }
+          for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(dsk, dyv[r], acc[r]);
+          const float o[4] = {acc[0], acc[1], acc[2], acc[3]};
+          dxv[i].set(o);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       __syncthreads();
 
-      // wave 0: the decay's and the step's gradients; the others go on to
-      // stage the next tile (nothing that is read here is written before the
-      // next barrier but by wave 0 itself)
-      if (wv == 0) {
+      // wave 4: the decay's and the step's gradients; the others go on to stage
+      // the next tile (what is read here is written again only after the next
+      // barrier, the tokens' values a turn later)
+      if (wv == 4) {
         float R[PL], K[PL], Yi[PL], Ui[PL];
 #pragma unroll
         for (int k = 0; k < PL; ++k) {
-          const int t = k * 64 + lane, I = t >> 4, e = t & 15;
-          R[k] = K[k] = Yi[k] = Ui[k] = 0.0f;
+          const int t = k * 64 + lane;
+          float v[4][8];
 #pragma unroll
-          for (int J = 0; J < NTT; ++J) {
-            if (J <= I) R[k] += rp[(I * (I + 1) / 2 + J) * 16 + e];
-            if (J >= I) K[k] += cp[(J * (J + 1) / 2 + I) * 16 + e];
+          for (int j = 0; j < NTT; j += 4) {
+            *reinterpret_cast<float4*>(&v[0][j]) = *reinterpret_cast<const float4*>(rp + t * NTT + j);
+            *reinterpret_cast<float4*>(&v[1][j]) = *reinterpret_cast<const float4*>(cp + t * NTT + j);
           }
 #pragma unroll
-          for (int n = 0; n < NS; ++n) { Yi[k] += yp[n * Q + t]; Ui[k] += up[n * Q + t]; }
+          for (int j = 0; j < NS; j += 2) {
+            *reinterpret_cast<float2*>(&v[2][j]) = *reinterpret_cast<const float2*>(yp + t * NS + j);
+            *reinterpret_cast<float2*>(&v[3][j]) = *reinterpret_cast<const float2*>(up + t * NS + j);
+          }
+          R[k] = K[k] = Yi[k] = Ui[k] = 0.0f;
+#pragma unroll
+          for (int j = 0; j < NTT; ++j) { R[k] += v[0][j]; K[k] += v[1][j]; }
+#pragma unroll
+          for (int j = 0; j < NS; ++j) { Yi[k] += v[2][j]; Ui[k] += v[3][j]; }
         }
         float through = 0.0f;
 #pragma unroll
@@ -429,9 +486,9 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
 #pragma unroll
           for (int k = 0; k < PL; ++k) {
             const int t = k * 64 + lane;
-            const float dv = acc_ds[k] * vd[k];
+            const float dv = acc_ds[k] * cs[5 * Q + t];
             if (t < rows) {
-              sa = __builtin_fmaf(sv[k], acc_g[k], sa);
+              sa = __builtin_fmaf(cs[4 * Q + t], acc_g[k], sa);
               sb += dv;
               if (ba.ddelta)
                 static_cast<In*>(ba.ddelta)[(b * a.L + t0 + t) * a.heads + hd] = from_f32<In>(dv);
@@ -451,6 +508,8 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       }
     }
   }
+
+  put_dx(hd1 - 1, a.ptiles - 1);
 
   // dC += P B and dB += P^T C with P summed over the heads (x and dy are done:
   // every wave is past the last barrier), P rounded to the input type
@@ -474,6 +533,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       const int it = tp * TT + i;
+      if (16 * it >= rows) continue;
       for (int kk = 0; kk <= it / 2; ++kk)
         dC[i] = mma(bs.col(ns, kk, g, c), pm.row(p_row, 16 * it, kk), dC[i]);
       for (int kk = it / 2; kk < H; ++kk)

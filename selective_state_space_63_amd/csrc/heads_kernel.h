@@ -228,13 +228,51 @@ __device__ __forceinline__ Frag<In> lane_frag(const In* p, int lane) {
 // the pointer for a generic one, and flat accesses wait on LDS too.)
 typedef char __attribute__((address_space(1)))* gbytes;
 __device__ __forceinline__ gbytes scalar_base(const void* p) {
-  uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  uint64_t v = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
+               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
   asm volatile("" : "+s"(v));
   return reinterpret_cast<gbytes>(v);
 }
 typedef unsigned int gu32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int gu32x4 __attribute__((ext_vector_type(4)));
 typedef float gf32x4 __attribute__((ext_vector_type(4)));
+
+// Eight values at a global address as an operand.
+__device__ __forceinline__ void load_frag(gbytes p, Frag<uint16_t>& o) {
+  o.v = __builtin_bit_cast(bf16x8, *reinterpret_cast<const gu32x4 __attribute__((address_space(1)))*>(p));
+}
+__device__ __forceinline__ void load_frag(gbytes p, Frag<float>& o) {
+  const auto* q = reinterpret_cast<const gf32x4 __attribute__((address_space(1)))*>(p);
+  const gf32x4 x = q[0], y = q[1];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) { o.v[j] = x[j]; o.v[4 + j] = y[j]; }
+}
+
+// Four values in the input type, kept as such.
+template <typename In>
+struct Four;
+template <>
+struct Four<uint16_t> {
+  uint32_t w[2];
+  __device__ __forceinline__ void set(const float (&f)[4]) { w[0] = bf_pack(f[0], f[1]); w[1] = bf_pack(f[2], f[3]); }
+  __device__ __forceinline__ uint16_t get(int r) const { return (uint16_t)(w[r >> 1] >> (16 * (r & 1))); }
+  __device__ __forceinline__ void store(gbytes p) const {
+    *reinterpret_cast<gu32x2 __attribute__((address_space(1)))*>(p) = gu32x2{w[0], w[1]};
+  }
+};
+template <>
+struct Four<float> {
+  float w[4];
+  __device__ __forceinline__ void set(const float (&f)[4]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) w[r] = f[r];
+  }
+  __device__ __forceinline__ float get(int r) const { return w[r]; }
+  __device__ __forceinline__ void store(gbytes p) const {
+    *reinterpret_cast<gf32x4 __attribute__((address_space(1)))*>(p) = gf32x4{w[0], w[1], w[2], w[3]};
+  }
+};
 
 // Four values in the input type.
 template <typename In>
