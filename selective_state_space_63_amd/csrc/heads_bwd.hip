@@ -75,8 +75,8 @@ struct BwdLds {
   static constexpr int cp = rp + Q * NTT * 4;                    // column sums by row tile (token, tile)
   static constexpr int yp = cp + Q * NTT * 4;                    // dy . S C by strip (token, strip)
   static constexpr int up = yp + NS * Q * 4;                     // x . L B by strip (token, strip)
-  static constexpr int tok = up + NS * Q * 4;                    // per-token values, two turns' worth
-  static constexpr int th = tok + 2 * 6 * Q * 4;                 // <L, S> by strip
+  static constexpr int tok = up + NS * Q * 4;                    // per-token values, three turns' worth
+  static constexpr int th = tok + 3 * 6 * Q * 4;                 // <L, S> by strip
   static constexpr int dd = th + 8 * 4;                          // x . dy by diagonal tile
   static constexpr int total = dd + 8 * 4;
   static_assert(total <= 163840, "LDS");
@@ -270,11 +270,59 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       touched = reinterpret_cast<const uint32_t*>(sp)[(threadIdx.x & 255) * 32];
     }
   };
+  // Wave 4, for the turn before: the decay's and the step's gradients.
+  float e_in[PL], e_y[PL], e_u[PL], e_w[PL], through = 0.0f;
+  int done_hd = -1, done_buf = 0;
+  bool done_last = false;
+  auto finish = [&]() {
+    if (wv != 4 || done_hd < 0) return;
+    const float Ah = a.A[done_hd];
+    float in0 = 0.0f, y0 = 0.0f, u0 = 0.0f;  // running totals of the 64-token halves
+    float in[PL], ysum[PL], usum[PL];
+#pragma unroll
+    for (int k = 0; k < PL; ++k) {
+      const float si = wave_scan(e_in[k]), sy = wave_scan(e_y[k]), su = wave_scan(e_u[k]);
+      in[k] = in0 + (si - e_in[k]);   // exclusive
+      usum[k] = u0 + (su - e_u[k]);   // exclusive
+      ysum[k] = y0 + (sy - e_y[k]);   // exclusive; the suffix is the total less this
+      in0 += last_lane(si); u0 += last_lane(su); y0 += last_lane(sy);
+    }
+#pragma unroll
+    for (int k = 0; k < PL; ++k) {
+      const float G = (in[k] + usum[k]) + ((y0 - ysum[k]) + through);
+      acc_g[k] += G;
+      acc_ds[k] = __builtin_fmaf(Ah, G, acc_ds[k]) + (a.unit ? 0.0f : e_w[k]);
+    }
+    if (!done_last) return;
+    const float* o = tok + done_buf * 6 * Q;
+    float sa = 0.0f, sb = 0.0f;
+#pragma unroll
+    for (int k = 0; k < PL; ++k) {
+      const int t = k * 64 + lane;
+      const float dv = acc_ds[k] * o[5 * Q + t];
+      if (t < rows) {
+        sa = __builtin_fmaf(o[4 * Q + t], acc_g[k], sa);
+        sb += dv;
+        if (ba.ddelta)
+          static_cast<In*>(ba.ddelta)[(b * a.L + t0 + t) * a.heads + done_hd] = from_f32<In>(dv);
+      }
+      acc_g[k] = acc_ds[k] = 0.0f;
+    }
+    sa = wave_sum(sa);
+    sb = wave_sum(sb);
+    if (lane == 0) {
+      const int64_t n = a.batch * ba.nblk, at = (b * ba.nblk + blk) * a.heads + done_hd;
+      ba.parts[at] = sa;
+      ba.parts[n * a.heads + at] = acc_d;
+      ba.parts[2 * n * a.heads + at] = sb;
+    }
+    acc_d = 0.0f;
+  };
   int buf = 0;
+  auto next = [](int i) { return i == 2 ? 0 : i + 1; };
   for (int hd = hd0; hd < hd1; ++hd) {
-    const float Ah = a.A[hd];
     const float dsk = a.D ? a.D[hd] : 0.0f;
-    for (int pt = 0; pt < a.ptiles; ++pt, buf ^= 1) {
+    for (int pt = 0; pt < a.ptiles; ++pt, buf = next(buf)) {
       const bool last_pt = pt + 1 == a.ptiles;
       // LDS addresses are formed again in every turn: kept across it they
       // would not leave room for the sums
@@ -288,11 +336,12 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       yr.mask(rows, pleft < kTP ? pleft : kTP);
       xr.store(xs);
       yr.store(ys);
+      decays(after(hd, pt), next(buf));
       if (hd > hd0 || pt > 0) put_dx(pt > 0 ? hd : hd - 1, pt > 0 ? pt - 1 : a.ptiles - 1);
       const float* cs = tok + buf * 6 * Q;
       const float *ec = cs + Q, *ww = cs + 2 * Q, *wd = cs + 3 * Q;
       __syncthreads();
-      decays(after(hd, pt), buf ^ 1);
+      finish();
       issue_step(last_pt ? after(hd + 1, 0) : after(hd, pt + 1));
       touch(after(hd, pt), last_pt ? 0 : pt + 1);
 
@@ -430,11 +479,9 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       }
       __syncthreads();
 
-      // wave 4: the decay's and the step's gradients; the others go on to stage
-      // the next tile (what is read here is written again only after the next
-      // barrier, the tokens' values a turn later)
+      // wave 4 takes the sums over tiles and strips now (they are written again
+      // after the next barrier) and finishes them behind that barrier
       if (wv == 4) {
-        float R[PL], K[PL], Yi[PL], Ui[PL];
 #pragma unroll
         for (int k = 0; k < PL; ++k) {
           const int t = k * 64 + lane;
@@ -449,66 +496,33 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
             *reinterpret_cast<float2*>(&v[2][j]) = *reinterpret_cast<const float2*>(yp + t * NS + j);
             *reinterpret_cast<float2*>(&v[3][j]) = *reinterpret_cast<const float2*>(up + t * NS + j);
           }
-          R[k] = K[k] = Yi[k] = Ui[k] = 0.0f;
+          float R = 0.0f, K = 0.0f, Y = 0.0f, U = 0.0f;
 #pragma unroll
-          for (int j = 0; j < NTT; ++j) { R[k] += v[0][j]; K[k] += v[1][j]; }
+          for (int j = 0; j < NTT; ++j) { R += v[0][j]; K += v[1][j]; }
 #pragma unroll
-          for (int j = 0; j < NS; ++j) { Yi[k] += v[2][j]; Ui[k] += v[3][j]; }
+          for (int j = 0; j < NS; ++j) { Y += v[2][j]; U += v[3][j]; }
+          const float w = ww[t];
+          e_in[k] = w * K - R;
+          e_y[k] = Y;
+          e_u[k] = w * U;
+          e_w[k] = K + U;
         }
-        float through = 0.0f;
+        through = 0.0f;
 #pragma unroll
         for (int n = 0; n < NS; ++n) through += th[n];
         through *= ec[Q - 1];
-        float in0 = 0.0f, y0 = 0.0f, u0 = 0.0f;  // running totals of the 64-token halves
-        float in[PL], ysum[PL], usum[PL];
-#pragma unroll
-        for (int k = 0; k < PL; ++k) {
-          const float w = ww[k * 64 + lane];
-          const float di = w * K[k] - R[k], du = w * Ui[k];
-          const float si = wave_scan(di), sy = wave_scan(Yi[k]), su = wave_scan(du);
-          in[k] = in0 + (si - di);        // exclusive
-          usum[k] = u0 + (su - du);       // exclusive
-          ysum[k] = y0 + (sy - Yi[k]);    // exclusive; the suffix is the total less this
-          in0 += last_lane(si); u0 += last_lane(su); y0 += last_lane(sy);
-        }
-#pragma unroll
-        for (int k = 0; k < PL; ++k) {
-          const float G = (in[k] + usum[k]) + ((y0 - ysum[k]) + through);
-          acc_g[k] += G;
-          acc_ds[k] = __builtin_fmaf(Ah, G, acc_ds[k]) + (a.unit ? 0.0f : K[k] + Ui[k]);
-        }
         if (ba.want_d) {
 #pragma unroll
           for (int I = 0; I < NTT; ++I) acc_d += ddp[I];
         }
-        if (last_pt) {
-          float sa = 0.0f, sb = 0.0f;
-#pragma unroll
-          for (int k = 0; k < PL; ++k) {
-            const int t = k * 64 + lane;
-            const float dv = acc_ds[k] * cs[5 * Q + t];
-            if (t < rows) {
-              sa = __builtin_fmaf(cs[4 * Q + t], acc_g[k], sa);
-              sb += dv;
-              if (ba.ddelta)
-                static_cast<In*>(ba.ddelta)[(b * a.L + t0 + t) * a.heads + hd] = from_f32<In>(dv);
-            }
-            acc_g[k] = acc_ds[k] = 0.0f;
-          }
-          sa = wave_sum(sa);
-          sb = wave_sum(sb);
-          if (lane == 0) {
-            const int64_t n = a.batch * ba.nblk, at = (b * ba.nblk + blk) * a.heads + hd;
-            ba.parts[at] = sa;
-            ba.parts[n * a.heads + at] = acc_d;
-            ba.parts[2 * n * a.heads + at] = sb;
-          }
-          acc_d = 0.0f;
-        }
+        done_hd = hd;
+        done_last = last_pt;
+        done_buf = buf;
       }
     }
   }
 
+  finish();
   put_dx(hd1 - 1, a.ptiles - 1);
 
   // dC += P B and dB += P^T C with P summed over the heads (x and dy are done:
