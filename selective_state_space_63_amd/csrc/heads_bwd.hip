@@ -162,8 +162,8 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
     if (wv != 7 || hd >= hd1 || !a.delta) return;
 #pragma unroll
     for (int k = 0; k < PL; ++k)
-      if (k * 64 + lane < rows)
-        draw[k] = static_cast<const In*>(a.delta)[b * a.d_batch + (t0 + k * 64 + lane) * a.d_token + hd];
+      load_step<In, VEC>(draw[k], static_cast<const In*>(a.delta) + b * a.d_batch + (t0 + k * 64) * a.d_token + hd,
+                         a.d_token, lane, rows - k * 64);
   };
   // the head of the turn after (hd, pt)
   auto after = [&](int hd, int pt) { return pt + 1 == a.ptiles ? hd + 1 : hd; };
@@ -227,27 +227,24 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   // dx of a turn is stored in the next one, behind the wait for its inputs
   // (stores before it would be waited for as well)
   Four<In> dxv[NTT / 2];
+  const uint32_t x_row = (uint32_t)hp * (uint32_t)sizeof(In);
   auto put_dx = [&](int hd, int pt) {
-    const int q = wv & 3, pleft = a.headdim - pt * kTP;
-    In* const base = static_cast<In*>(ba.dx) + (b * a.L + t0) * hp + (int64_t)hd * a.headdim + pt * kTP + 16 * q;
-    const uint32_t off = ((uint32_t)c * (uint32_t)hp + 4 * g) * (uint32_t)sizeof(In);
-    const int p = 16 * q + 4 * g;
-    if (VEC && rows == Q && pleft >= kTP) {
+    const int p = 16 * (wv & 3) + 4 * g, pleft = a.headdim - pt * kTP;
+    In* const base = static_cast<In*>(ba.dx) + (b * a.L + t0) * hp + (int64_t)hd * a.headdim + pt * kTP;
+    if constexpr (VEC) {  // rows past the sequence and channels past the head are dropped
+      const __amdgpu_buffer_rsrc_t db =
+          buffer_of(base, (uint32_t)(rows - 1) * x_row + (uint32_t)(pleft < kTP ? pleft : kTP) * (uint32_t)sizeof(In));
+      const uint32_t off = (uint32_t)(16 * (wv >> 2) + c) * x_row + (uint32_t)p * (uint32_t)sizeof(In);
 #pragma unroll
-      for (int i = 0; i < NTT / 2; ++i) dxv[i].store(scalar_base(base + 16 * (2 * i + (wv >> 2)) * hp) + off);
-      return;
-    }
+      for (int i = 0; i < NTT / 2; ++i) dxv[i].store(db, p < pleft ? off + (uint32_t)(32 * i) * x_row : kNowhere);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NTT / 2; ++i) {
-      const int s0 = 16 * (2 * i + (wv >> 2));
-      if (s0 + c < rows) {
-        const gbytes dp = scalar_base(base + s0 * hp) + off;
-        if constexpr (VEC) {
-          if (p < pleft) dxv[i].store(dp);
-        } else {
+      for (int i = 0; i < NTT / 2; ++i) {
+        const int s = 16 * (2 * i + (wv >> 2)) + c;
+        if (s < rows) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (p + r < pleft) reinterpret_cast<In __attribute__((address_space(1)))*>(dp)[r] = dxv[i].get(r);
+            if (p + r < pleft) base[s * hp + p + r] = dxv[i].get(r);
         }
       }
     }

@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   // decay, its exponential, input weight, weight decayed to the chunk's end.
   In draw = In(0);  // as loaded: a conversion here would wait for every load before it
   auto issue_step = [&](int64_t t0) {
-    if (wv == 3 && dl && lane < rows_at(t0)) draw = dl[(t0 + lane) * a.d_token];
+    if (wv == 3 && dl) load_step<In, VEC>(draw, dl + t0 * a.d_token, a.d_token, lane, rows_at(t0));
   };
   auto decays = [&](int64_t t0, int buf) {
     if (wv != 3) return;
@@ -128,10 +128,34 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   issue_step(t_lo + kHQ);
   __syncthreads();
   int buf = 0;
-  const uint32_t y_off = ((uint32_t)c * (uint32_t)hp + 16 * wv + 4 * g) * (uint32_t)sizeof(In);
+  // a lane's place in a tile of y: channels 16 wv + 4 g .., token c
+  const uint32_t y_row = (uint32_t)hp * (uint32_t)sizeof(In);
+  const uint32_t y_off =
+      16 * wv + 4 * g < pleft ? (uint32_t)c * y_row + (uint32_t)(16 * wv + 4 * g) * (uint32_t)sizeof(In) : kNowhere;
   // lane parts of the LDS addresses; x's column tile is the wave's own
   int b_row = L::BT::row_lane(g, c), b_col = L::BT::col_lane(g, c), c_row = L::CT::row_lane(g, c);
   const int x_col = L::XT::col_lane(g, c);
+  Four<In> yv[4];  // a chunk's y: channels 16 wv + 4 g .., token 16 I + c
+
+  auto put_y = [&](int64_t t0) {
+    const int rows = rows_at(t0);
+    In* const base = Y + t0 * hp;
+    if constexpr (VEC) {  // rows past the sequence and channels past the head are dropped
+      const __amdgpu_buffer_rsrc_t yb =
+          buffer_of(base, (uint32_t)(rows - 1) * y_row + (uint32_t)(pleft < kTP ? pleft : kTP) * (uint32_t)sizeof(In));
+#pragma unroll
+      for (int I = 0; I < 4; ++I) yv[I].store(yb, y_off == kNowhere ? kNowhere : y_off + (uint32_t)(16 * I) * y_row);
+    } else {
+      const int p = 16 * wv + 4 * g;
+#pragma unroll
+      for (int I = 0; I < 4; ++I)
+        if (16 * I + c < rows) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (p + r < pleft) base[(16 * I + c) * hp + p + r] = yv[I].get(r);
+        }
+    }
+  };
   for (int64_t t0 = t_lo; t0 < t_hi; t0 += kHQ, buf ^= 1) {
     const int rows = rows_at(t0);
     // the units' XORs are done in every turn: their results kept over it would
@@ -194,7 +218,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
         to_frag(f, sf[kk]);  // bf16: y is rounded to bf16 anyway
       }
       const bool dirty = *any != 0;
-      float o[4][4];
+      const int p = 16 * wv + 4 * g;
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
         f32x4 acc = {0, 0, 0, 0};
@@ -203,33 +227,19 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
         acc *= ec[16 * I + c];
 #pragma unroll
         for (int kk = 0; kk <= I / 2; ++kk) acc = mma(xf[kk], lane_frag(pf + (I * 2 + kk) * 512, lane), acc);
-        float xv[4];
+        float xv[4], o[4];
         xs.four(16 * I + c, 4 * wv + g, xv);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[I][r] = __builtin_fmaf(dsk, xv[r], acc[r]);
+        for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(dsk, xv[r], acc[r]);
+        yv[I].set(o);
       }
-      const int p = 16 * wv + 4 * g;
       if (dirty) {
 #pragma unroll
-        for (int I = 0; I < 4; ++I)
+        for (int I = 0; I < 4; ++I) {
+          float o[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (16 * I + c >= bad[p + r]) o[I][r] = __builtin_nanf("");
-      }
-      const bool full = VEC && rows == kHQ && pleft >= kTP;
-#pragma unroll
-      for (int I = 0; I < 4; ++I) {
-        if (full) {
-          store_four<In>(scalar_base(Y + (t0 + 16 * I) * hp) + y_off, o[I]);
-        } else if (16 * I + c < rows) {
-          In* yp = Y + (t0 + 16 * I + c) * hp + p;
-          if constexpr (VEC) {
-            if (p < pleft) store_vec<In, 4>(yp, o[I]);
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (p + r < pleft) yp[r] = from_f32<In>(o[I][r]);
-          }
+          for (int r = 0; r < 4; ++r) o[r] = 16 * I + c >= bad[p + r] ? __builtin_nanf("") : to_f32(yv[I].get(r));
+          yv[I].set(o);
         }
       }
       if (dirty && bad[ps] < kHQ) {
@@ -238,6 +248,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
       }
     }
 
+    put_y(t0);
     const float dec = ec[kHQ - 1];
 #pragma unroll
     for (int q = 0; q < NQ; ++q) S[q] *= dec;
@@ -322,8 +333,12 @@ HeadsPlan heads_plan(const s6_heads_dims& d, int in_dtype, const void* x, const 
           d.b_token % u == 0 && d.c_batch % u == 0 && d.c_token % u == 0 && aligned(x, 16) && aligned(Bm, 16) &&
           aligned(Cm, 16) && aligned(dy, 16);
   // offsets within a tile of up to 128 rows in 32 bits
-  const int64_t strides[] = {d.x_token, d.b_token, d.c_token};
+  const int64_t hp = d.heads * d.headdim, gn = d.groups * d.dstate;
+  const int64_t strides[] = {d.x_token, d.b_token, d.c_token, d.delta_token, hp};
   for (int64_t s : strides) p.vec = p.vec && s < (int64_t(1) << 31) / (128 * 4);
+  // a tile's buffer ends with its last token: rows past it must lie past that
+  // end (not so where tokens share their row, as in a broadcast)
+  p.vec = p.vec && d.x_token >= hp && d.b_token >= gn && d.c_token >= gn;
   return p;
 }
 
@@ -343,16 +358,20 @@ HeadsArgs heads_args(const s6_heads_dims& d, const HeadsPlan& p, int flags, cons
   return a;
 }
 
-// Few rows leave CUs idle: with fewer rows than one workgroup per CU the
-// sequence is cut into segments, enough for two workgroups per CU, of at
-// least four chunks each.
+// Few rows leave CUs idle: with at most one row per CU the sequence is cut
+// into segments, up to three workgroups per CU (what the kernel's registers
+// allow at N > 64), of at least two chunks each.  Measured, us of scan + state
+// walk + fold, at targets of two and three per CU and at least four and two
+// chunks: 65536 tokens of 24 heads of 64, N 64: 302 and 270; 2 x 2048 tokens
+// of 24 heads of 64, N 128: 50 and 50; 3 x 777 tokens of 10 fp32 heads of 40,
+// N 24: 42 and 31.
 void heads_segments(int64_t rows, int64_t L, int64_t unit, int64_t* nseg, int64_t* seg_len) {
   *nseg = 1;
   *seg_len = L;
   const int64_t cus = cu_count();
-  if (rows <= 0 || rows >= cus) return;
-  int64_t s = 2 * cus / rows;
-  const int64_t most = L / (4 * kHQ);
+  if (rows <= 0 || rows > cus) return;
+  int64_t s = 3 * cus / rows;
+  const int64_t most = L / (2 * kHQ);
   if (s > most) s = most;
   if (s <= 1) return;
   const int64_t len = ((L + s - 1) / s + unit - 1) / unit * unit;

@@ -238,6 +238,19 @@ typedef unsigned int gu32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int gu32x4 __attribute__((ext_vector_type(4)));
 typedef float gf32x4 __attribute__((ext_vector_type(4)));
 
+// A part of a tensor as a buffer of `bytes` from p on: loads past its end
+// return 0 and stores are dropped, so that tiles need no branches at the ends
+// of a sequence (branches around loads make the compiler wait for them in
+// turn).  Offsets are unsigned 32-bit bytes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  const uint64_t v = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(v), 0, __builtin_amdgcn_readfirstlane(bytes),
+                                           0x00027000);
+}
+constexpr uint32_t kNowhere = 0xfffffff0u;  // an offset past every buffer
+
 // Eight values at a global address as an operand.
 __device__ __forceinline__ void load_frag(gbytes p, Frag<uint16_t>& o) {
   o.v = __builtin_bit_cast(bf16x8, *reinterpret_cast<const gu32x4 __attribute__((address_space(1)))*>(p));
@@ -257,8 +270,8 @@ struct Four<uint16_t> {
   uint32_t w[2];
   __device__ __forceinline__ void set(const float (&f)[4]) { w[0] = bf_pack(f[0], f[1]); w[1] = bf_pack(f[2], f[3]); }
   __device__ __forceinline__ uint16_t get(int r) const { return (uint16_t)(w[r >> 1] >> (16 * (r & 1))); }
-  __device__ __forceinline__ void store(gbytes p) const {
-    *reinterpret_cast<gu32x2 __attribute__((address_space(1)))*>(p) = gu32x2{w[0], w[1]};
+  __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
+    __builtin_amdgcn_raw_buffer_store_b64(gu32x2{w[0], w[1]}, r, off, 0, 0);
   }
 };
 template <>
@@ -269,19 +282,10 @@ struct Four<float> {
     for (int r = 0; r < 4; ++r) w[r] = f[r];
   }
   __device__ __forceinline__ float get(int r) const { return w[r]; }
-  __device__ __forceinline__ void store(gbytes p) const {
-    *reinterpret_cast<gf32x4 __attribute__((address_space(1)))*>(p) = gf32x4{w[0], w[1], w[2], w[3]};
+  __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(gu32x4, gf32x4{w[0], w[1], w[2], w[3]}), r, off, 0, 0);
   }
 };
-
-// Four values in the input type.
-template <typename In>
-__device__ __forceinline__ void store_four(gbytes p, const float (&f)[4]) {
-  if constexpr (sizeof(In) == 2)
-    *reinterpret_cast<gu32x2 __attribute__((address_space(1)))*>(p) = gu32x2{bf_pack(f[0], f[1]), bf_pack(f[2], f[3])};
-  else
-    *reinterpret_cast<gf32x4 __attribute__((address_space(1)))*>(p) = gf32x4{f[0], f[1], f[2], f[3]};
-}
 
 // Eight consecutive columns of one row.
 template <typename In>
@@ -295,9 +299,9 @@ struct Piece<uint16_t> {
     v = make_uint4(part(v.x, 0), part(v.y, 1), part(v.z, 2), part(v.w, 3));
   }
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void load_at(gbytes p) {
-    const gu32x4 w = *reinterpret_cast<const gu32x4 __attribute__((address_space(1)))*>(p);
-    v = make_uint4(w.x, w.y, w.z, w.w);
+  __device__ __forceinline__ void load_at(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    v = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void set(const uint16_t (&e)[8]) {
     v = make_uint4(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16), e[4] | ((uint32_t)e[5] << 16),
@@ -336,9 +340,9 @@ struct Piece<float> {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
   }
-  __device__ __forceinline__ void load_at(gbytes p) {
-    const auto* q = reinterpret_cast<const gf32x4 __attribute__((address_space(1)))*>(p);
-    const gf32x4 x = q[0], y = q[1];
+  __device__ __forceinline__ void load_at(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    const gf32x4 x = __builtin_bit_cast(gf32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    const gf32x4 y = __builtin_bit_cast(gf32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16, 0, 0));
     a = make_float4(x.x, x.y, x.z, x.w);
     b = make_float4(y.x, y.y, y.z, y.w);
   }
@@ -362,9 +366,9 @@ struct Piece<float> {
 
 // A ROWS x COLS tile through the registers of THREADS threads: load() issues
 // the global loads, mask() zeroes what lies past the sequence or the width,
-// store() writes the LDS tile.  VEC: 16-byte loads (rows 16-byte aligned, width
-// a multiple of 8); their addresses are held inside the tensor instead of
-// skipped, so that a full tile takes no branches.
+// store() writes the LDS tile.  VEC: 16-byte buffer loads (rows 16-byte
+// aligned, width a multiple of 8, offsets in 32 bits); rows past the sequence
+// read 0.
 template <typename In, int ROWS, int COLS, int THREADS, bool VEC>
 struct TileRegs {
   static constexpr int kPer = COLS / 8;                       // pieces of a row
@@ -388,31 +392,22 @@ struct TileRegs {
     return t;
   }
   // base: row 0, column 0 of the tile; `rows` of it are in the sequence (0:
-  // nothing is loaded) and `cols` >= 1 columns are in the width.  A whole tile
-  // is loaded from scalar bases and one 32-bit offset of the thread (the host
-  // sends strides for which it would not fit to the other form).
+  // nothing is loaded) and `cols` >= 1 columns are in the width
   __device__ __forceinline__ void load(const In* base, int64_t stride, int rows, int cols) {
-    if (rows == 0) return;
-    if constexpr (VEC && ROWS * kPer % THREADS == 0) {
-      if (rows == ROWS && cols >= COLS) {
-        const uint32_t off = ((uint32_t)row_of(0) * (uint32_t)stride + (uint32_t)col_of()) * (uint32_t)sizeof(In);
+    if constexpr (VEC) {
+      const uint32_t st = (uint32_t)stride * (uint32_t)sizeof(In);
+      const uint32_t off = (uint32_t)row_of(0) * st + (uint32_t)col_of() * (uint32_t)sizeof(In);
+      const __amdgpu_buffer_rsrc_t buf =
+          buffer_of(base, rows > 0 ? (uint32_t)(rows - 1) * st + (uint32_t)cols * (uint32_t)sizeof(In) : 0u);
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          r[k].load_at(scalar_base(base + (int64_t)(k * (THREADS / kPer)) * stride) + off);
-        }
-        return;
-      }
-    }
-    const int tid = fresh_tid();
+      for (int k = 0; k < kN; ++k) r[k].load_at(buf, off + (uint32_t)(k * (THREADS / kPer)) * st);
+    } else {
+      if (rows == 0) return;
+      const int tid = fresh_tid();
 #pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      int row = row_of(k, tid), col = col_of(tid);
-      row = row < rows ? row : rows - 1;
-      if constexpr (VEC) {
-        col = col < cols ? col : cols - 8;
-        r[k].load(base + (int64_t)row * stride + col);
-      } else {
-        const In* p = base + (int64_t)row * stride;
+      for (int k = 0; k < kN; ++k) {
+        const int row = row_of(k, tid), col = col_of(tid);
+        const In* p = base + (int64_t)(row < rows ? row : rows - 1) * stride;
         In e[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) e[j] = p[col + j < cols ? col + j : cols - 1];
@@ -421,7 +416,7 @@ struct TileRegs {
     }
   }
   __device__ __forceinline__ void mask(int rows, int cols) {
-    if (rows >= ROWS && cols >= COLS) return;
+    if ((VEC || rows >= ROWS) && cols >= COLS) return;
     const int tid = fresh_tid();
 #pragma unroll
     for (int k = 0; k < kN; ++k) r[k].keep(row_of(k, tid) < rows ? cols - col_of(tid) : 0);
@@ -512,6 +507,22 @@ __device__ __forceinline__ HeadRow head_row(const HeadsArgs& a, int64_t row) {
   o.hd = (int)(bh - o.b * a.heads);
   o.grp = o.hd / a.hpg;
   return o;
+}
+
+// The stored step of token `lane` of `rows`, at p with stride `st` (elements).
+template <typename In, bool VEC>
+__device__ __forceinline__ void load_step(In& raw, const In* p, int64_t st, int lane, int rows) {
+  if constexpr (VEC) {
+    const __amdgpu_buffer_rsrc_t buf =
+        buffer_of(p, rows > 0 ? ((uint32_t)(rows - 1) * (uint32_t)st + 1) * (uint32_t)sizeof(In) : 0u);
+    const uint32_t off = (uint32_t)lane * (uint32_t)st * (uint32_t)sizeof(In);
+    if constexpr (sizeof(In) == 2)
+      raw = __builtin_amdgcn_raw_buffer_load_b16(buf, off, 0, 0);
+    else
+      raw = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buf, off, 0, 0));
+  } else {
+    if (lane < rows) raw = p[lane * st];
+  }
 }
 
 // Step of a token of head hd: raw is the stored delta (or unused).

@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
     const int rows = k < 0 || k >= nch ? 0 : (int)(t_hi - t0 < kHQ ? t_hi - t0 : kHQ);
     xr.load(X + t0 * xt, xt, rows, pleft < kTP ? pleft : kTP);
     br.load(B + t0 * bt, bt, rows, a.dstate);
-    if (dl && (int)threadIdx.x < rows) draw = dl[(t0 + threadIdx.x) * a.d_token];
+    if (wv == 0 && dl) load_step<In, VEC>(draw, dl + t0 * a.d_token, a.d_token, lane, rows);
   };
   const int64_t first = dir ? nch - 1 : 0, step = dir ? -1 : 1;
   issue(first);
