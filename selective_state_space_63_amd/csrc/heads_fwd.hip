@@ -260,10 +260,14 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = frag_f32(xf[kk], e) * w[e];
-      Pair<In> xd;
-      to_pair(f, xd);
+      Whole<In> xd;
+      to_whole(f, xd);
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) S[q] = mma_pair(bs.col(b_col, q, kk, g, c), xd, S[q]);
+      for (int q = 0; q < NQ; ++q) {
+        const Frag<In> bf = bs.col(b_col, q, kk, g, c);
+#pragma unroll
+        for (int i = Whole<In>::kParts - 1; i >= 0; --i) S[q] = mma(bf, xd.part[i], S[q]);
+      }
     }
     __syncthreads();
   }

@@ -96,6 +96,28 @@ __device__ __forceinline__ f32x4 mma_pair(const Frag<uint16_t>& a, const Pair<ui
 __device__ __forceinline__ f32x4 mma_pair(const Pair<float>& a, const Frag<float>& b, f32x4 d) { return mma(a.hi, b, d); }
 __device__ __forceinline__ f32x4 mma_pair(const Frag<float>& a, const Pair<float>& b, f32x4 d) { return mma(a, b.hi, d); }
 
+// Eight floats as the exact sum of operands: three bf16 parts hold the 24 bits
+// of a float (down to the smallest bf16), one float part itself.  For what
+// the state keeps: two parts would leave 2^-17 of every term in it.
+template <typename In>
+struct Whole {
+  static constexpr int kParts = sizeof(In) == 2 ? 3 : 1;
+  Frag<In> part[kParts];
+};
+__device__ __forceinline__ void to_whole(const float (&f)[8], Whole<uint16_t>& o) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float rest = f[j];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const __bf16 h = (__bf16)rest;
+      o.part[i].v[j] = h;
+      rest -= (float)h;
+    }
+  }
+}
+__device__ __forceinline__ void to_whole(const float (&f)[8], Whole<float>& o) { to_frag(f, o.part[0]); }
+
 // ------------------------------------------------------------- LDS tiles --
 // Eight consecutive values of LDS as an operand.
 __device__ __forceinline__ Frag<uint16_t> eight(const uint16_t* p) {

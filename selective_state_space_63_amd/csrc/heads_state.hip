@@ -11,7 +11,7 @@
 //
 // A workgroup of four waves owns one row (64 channels of a head): wave w the
 // channel tiles 2 (w & 1), + 1 and half of the state columns, in registers.
-// The scaled inputs enter as two bf16 parts, so the state is good to fp32
+// The scaled inputs enter as three bf16 parts, so the state is good to fp32
 // accumulation.
 #include "heads_kernel.h"
 
@@ -152,20 +152,22 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
       const float4 w0 = *reinterpret_cast<const float4*>(wt + 32 * kk + 4 * g);
       const float4 w1 = *reinterpret_cast<const float4*>(wt + 32 * kk + 16 + 4 * g);
       const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-      Pair<In> xd[2];
+      Whole<In> xd[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const Frag<In> xf = xs.col(x_col, 2 * pp + j, kk, g, c);
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = frag_f32(xf, e) * w[e];
-        to_pair(f, xd[j]);
+        to_whole(f, xd[j]);
       }
 #pragma unroll
       for (int q = 0; q < NW; ++q) {
         const Frag<In> bf = bs.col(b_col, nh * NW + q, kk, g, c);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) T[q][j] = mma_pair(xd[j], bf, T[q][j]);
+        for (int i = Whole<In>::kParts - 1; i >= 0; --i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) T[q][j] = mma(xd[j].part[i], bf, T[q][j]);
       }
     }
     __syncthreads();
