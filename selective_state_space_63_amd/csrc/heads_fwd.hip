@@ -34,7 +34,8 @@ struct ScanLds {
   static constexpr int cm = bs + BT::size(kHQ) * (int)sizeof(In);
   static constexpr int pf = cm + CT::size(kHQ) * (int)sizeof(In);
   static constexpr int tok = pf + 4096 * (int)sizeof(In);
-  static constexpr int bad = tok + 2 * 4 * kHQ * 4;
+  static constexpr int dg = tok + 2 * 4 * kHQ * 4;
+  static constexpr int bad = dg + kHQ * 4;
   static constexpr int total = bad + (kTP + 4) * 4;
 };
 
@@ -48,6 +49,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   const typename L::CT cm{reinterpret_cast<In*>(lds + L::cm)};
   In* pf = reinterpret_cast<In*>(lds + L::pf);             // [4 t tiles][2][lane][8]
   float* tok = reinterpret_cast<float*>(lds + L::tok);     // per-token values, two chunks' worth
+  float* dg = reinterpret_cast<float*>(lds + L::dg);       // the Gram matrix's diagonal times the weights
   int* bad = reinterpret_cast<int*>(lds + L::bad);         // first token whose input is not finite
   int* any = bad + kTP;
   // consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of
@@ -199,7 +201,12 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
         float p[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          p[r] = I != J || c >= 4 * g + r ? G[r] * (fast_exp2(ct - cj[r]) * wj[r]) : 0.0f;
+          p[r] = I != J || c > 4 * g + r ? G[r] * (fast_exp2(ct - cj[r]) * wj[r]) : 0.0f;
+        if (I == J) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (c == 4 * g + r) dg[16 * I + c] = G[r] * wj[r];
+        }
         store_vec<In, 4>(pf + ((I * 2 + (J >> 1)) * 64 + lane) * 8 + 4 * (J & 1), p);
       }
     }
@@ -229,8 +236,11 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
         for (int kk = 0; kk <= I / 2; ++kk) acc = mma(xf[kk], lane_frag(pf + (I * 2 + kk) * 512, lane), acc);
         float xv[4], o[4];
         xs.four(16 * I + c, 4 * wv + g, xv);
+        // a token's own input enters in fp32, with the skip: it is the largest
+        // term of heads that forget fast, which would meet two roundings
+        const float own = dsk + dg[16 * I + c];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(dsk, xv[r], acc[r]);
+        for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(own, xv[r], acc[r]);
         yv[I].set(o);
       }
       if (dirty) {

@@ -433,3 +433,22 @@ def test_tokens_that_share_their_rows(torch_cuda, dtype):
             want = ref.scan_bwd(n[0], None, *n[1:])
             for k in ("dx", "dA", "dBm", "dCm"):
                 close(got[k], *want[k], bar(dtype, k == "dA"), f"{k} {L} {strides}")
+
+
+@pytest.mark.parametrize("shape", [
+    (8, 500, 128, 8, 2, 16, "bf16", "softplus", False, True, False, 0),
+    (8, 449, 128, 8, 1, 72, "f32", "delta", True, False, False, 0),
+    (1, 8200, 64, 8, 2, 40, "bf16", "softplus", False, True, True, 8),   # and segments
+    (2, 8192, 32, 8, 1, 24, "f32", "none", True, True, False, 0),
+    (1, 8192, 32, 68, 1, 8, "bf16", "softplus", False, False, False, 0),  # headdim off the 16-byte loads
+], ids=IDS)
+def test_many_heads_of_a_group(torch_cuda, shape):
+    """Many outputs: many heads of one group, lengths that end inside a tile."""
+    b, L, H, P, G, N, dtype, step, unit, h0, packed, pad = shape
+    print(f"[case] heads scan {shape}", flush=True)
+    d, n = case(torch_cuda, b, L, H, P, G, N, dtype, step, h0, 1, packed, pad)
+    y, hl = fwd(d, step, unit)
+    ry, my, rh, mh = ref.scan(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], n["D"], n["h0"], n["bias"],
+                              step == "softplus", unit)
+    close(y, ry, my, bar(dtype), "y")
+    close(hl, rh, mh, bar(dtype, True), "h_last")
