@@ -37,12 +37,16 @@
  *
  * Arithmetic: sums, states, decays and steps in fp32.  fp32 inputs: fp32
  * products.  bf16 inputs: bf16 matrix products with fp32 accumulation; the
- * products of inputs are exact, an fp32 factor enters as two bf16 parts
- * (within 2^-17) where the result is kept in fp32 (states, gradients of
- * states, steps and parameters) and as one where it is rounded to bf16
- * anyway (y, dx, dBm, dCm).  A decay e^{c_t - c_s} is taken from sums within
- * a chunk of tokens, so its relative error is about 2^-24 times the chunk's
- * largest |c|.  Repeated calls give identical bits.
+ * products of inputs are exact; an fp32 factor enters in full in the states
+ * (three bf16 parts), as two bf16 parts (within 2^-17) where the result is a
+ * gradient of steps or parameters, and as one where it is rounded to bf16
+ * anyway (y, dx, dBm, dCm; a token's own input enters its y in fp32).  A
+ * decay e^{c_t - c_s} is taken from sums within a chunk of tokens, so its
+ * relative error is about 2^-24 times the chunk's largest |c|.  Repeated calls
+ * give identical bits.
+ * An x that is not finite makes its channel NaN from its token on; other
+ * channels and earlier tokens keep their values.  In the backward such a value
+ * may also reach the other tokens of its block of 128 (fp32: 64).
  */
 #ifndef S6_BLOCK_H_
 #define S6_BLOCK_H_

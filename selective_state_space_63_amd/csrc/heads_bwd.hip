@@ -31,7 +31,21 @@
 //
 // Waves: wave w owns the 16 state columns n of strip w % NS in the products
 // with S and L (dC, dB: rows n, columns t), all of them in registers, and
-// for dx the channel tile w % 4 of every second token tile.
+// for dx the channel tile w % 4 of every second token tile.  Wave 7 forms the
+// next head's decays, wave 4 finishes the last head's step gradients behind
+// the next turn's barrier, so neither is waited for.
+//
+// Roundings (bf16 inputs): P, the decayed Gram matrix and, for dx, L are taken
+// in bf16 (dx, dB, dC are rounded to it); the step's and the decay's gradients
+// come from fp32 products and from S and L in two bf16 parts (within 2^-17).
+//
+// What bounds it: one workgroup of eight waves fits a CU (242 VGPRs, 157 KB of
+// LDS), so a turn is the sum of its phases' latencies: 11 us at 128 tokens x 64
+// channels x N 128.  8 x 2048 tokens of 80 heads of 64, N 128: 442 - 475 us, of
+// which HBM needs 190 (1.2 GB).  Register spills cost the most on the way here
+// (802 us with 163 of them): reloads wait behind the prefetches of the next
+// turn, so those are L2 touches for the states, and token tiles past the
+// sequence are left out by branches.
 #include "heads_kernel.h"
 
 namespace s6i {

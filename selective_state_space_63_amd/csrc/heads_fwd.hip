@@ -17,6 +17,22 @@
 // token, the decay of its token is one scalar per lane, and the state's
 // registers are the operand of the product with C as they are.  The decayed
 // Gram tiles are shared out among the waves and meet in LDS in operand order.
+//
+// Roundings (bf16 inputs): the decayed Gram matrix and the state's copy for
+// the product with C to bf16, as y is rounded to bf16 anyway; the diagonal
+// (a token's own input) stays in fp32 with the skip; the inputs of the state
+// itself enter in full, as three bf16 parts.
+//
+// What bounds it: the latency of a chunk's chain (stage -> Gram -> y -> state,
+// three barriers), not a unit: at 8 x 2048 tokens of 80 heads of 64, N 128,
+// 196 us alone in a queue (222 - 245 us between other kernels), 1.7 TB/s of
+// the 6.2 TB/s that a copy reaches, with the vector units 39 % and the matrix
+// units 23 % busy and LDS 30 %; a workgroup alone on its CU takes 10.6
+// thousand cycles per chunk, each of three takes 13 thousand.  So what counts
+// is workgroups per CU: 168 VGPRs and 51 KB of LDS let three in.  Measured and
+// not kept: Gram tiles of a wave side by side (+6 %), Gram tiles formed once
+// per group by a launch of their own (+2 %, registers), four workgroups per
+// CU (spills).
 #include "heads_kernel.h"
 
 namespace s6i {

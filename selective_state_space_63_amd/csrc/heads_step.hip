@@ -11,6 +11,10 @@
 // before the first is used; B and C are the same for all of a lane's rows
 // and stay in registers.  The row's dot product with C is added over its
 // lanes with DPP.
+//
+// 256 sequences of 80 heads of 64, N 128: 248 us, 5.4 TB/s of the 6.2 TB/s
+// that a copy reaches (265 us with the inputs loaded behind the state's use);
+// one sequence of 24 heads: 4 us of kernel, 12.6 us with the call.
 #include "block_internal.h"
 
 namespace s6i {
