@@ -86,15 +86,11 @@ __device__ __forceinline__ void to_pair(const float (&f)[8], Pair<uint16_t>& o) 
 }
 __device__ __forceinline__ void to_pair(const float (&f)[8], Pair<float>& o) { to_frag(f, o.hi); }
 
-// d += (hi + lo) b  and  d += a (hi + lo)
+// d += (hi + lo) b
 __device__ __forceinline__ f32x4 mma_pair(const Pair<uint16_t>& a, const Frag<uint16_t>& b, f32x4 d) {
   return mma(a.lo, b, mma(a.hi, b, d));
 }
-__device__ __forceinline__ f32x4 mma_pair(const Frag<uint16_t>& a, const Pair<uint16_t>& b, f32x4 d) {
-  return mma(a, b.lo, mma(a, b.hi, d));
-}
 __device__ __forceinline__ f32x4 mma_pair(const Pair<float>& a, const Frag<float>& b, f32x4 d) { return mma(a.hi, b, d); }
-__device__ __forceinline__ f32x4 mma_pair(const Frag<float>& a, const Pair<float>& b, f32x4 d) { return mma(a, b.hi, d); }
 
 // Eight floats as the exact sum of operands: three bf16 parts hold the 24 bits
 // of a float (down to the smallest bf16), one float part itself.  For what
