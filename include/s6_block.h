@@ -41,9 +41,10 @@
  * (three bf16 parts), as two bf16 parts (within 2^-17) where the result is a
  * gradient of steps or parameters, and as one where it is rounded to bf16
  * anyway (y, dx, dBm, dCm; a token's own input enters its y in fp32).  A
- * decay e^{c_t - c_s} is taken from sums within a chunk of tokens, so its
- * relative error is about 2^-24 times the chunk's largest |c|.  Repeated calls
- * give identical bits.
+ * decay e^{c_t - c_s} between two tokens of a chunk is taken from running sums
+ * held in two floats each: its relative error is about 2^-24 times its own
+ * exponent, whatever decays lie before it (sequences packed closely one after
+ * another lose nothing).  Repeated calls give identical bits.
  * An x that is not finite makes its channel NaN from its token on; other
  * channels and earlier tokens keep their values.  In the backward such a value
  * may also reach the other tokens of its block of 128 (fp32: 64).

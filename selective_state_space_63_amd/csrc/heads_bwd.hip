@@ -90,7 +90,7 @@ struct BwdLds {
   static constexpr int yp = cp + Q * NTT * 4;                    // dy . S C by strip (token, strip)
   static constexpr int up = yp + NS * Q * 4;                     // x . L B by strip (token, strip)
   static constexpr int tok = up + NS * Q * 4;                    // per-token values, three turns' worth
-  static constexpr int th = tok + 3 * 6 * Q * 4;                 // <L, S> by strip
+  static constexpr int th = tok + 3 * 7 * Q * 4;                 // <L, S> by strip
   static constexpr int dd = th + 8 * 4;                          // x . dy by diagonal tile
   static constexpr int total = dd + 8 * 4;
   static_assert(total <= 163840, "LDS");
@@ -167,10 +167,10 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
     xr.load(static_cast<const In*>(a.x) + b * a.x_batch + t0 * a.x_token + col, a.x_token, on, cols < kTP ? cols : kTP);
     yr.load(static_cast<const In*>(a.dy) + (b * a.L + t0) * hp + col, hp, on, cols < kTP ? cols : kTP);
   };
-  // The last wave forms a head's per-token values a turn ahead: running log2
-  // decay, its exponential, input weight, decay to the block's end, step, and
-  // the step's derivative.
-  // (from steps loaded another turn earlier, kept as loaded).
+  // The last wave forms a head's per-token values a turn ahead, from steps
+  // loaded another turn earlier and kept as loaded: running log2 decay (its
+  // second part is the last value), its exponential, input weight, decay to the
+  // block's end, step, and the step's derivative.
   In draw[PL];
   auto issue_step = [&](int hd) {
     if (wv != 7 || hd >= hd1 || !a.delta) return;
@@ -184,24 +184,26 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   auto decays = [&](int hd, int buf) {
     if (wv != 7 || hd >= hd1) return;
     const float bias = a.dbias ? a.dbias[hd] : 0.0f, a2 = a.A[hd] * kLog2e;
-    float* o = tok + buf * 6 * Q;
-    float base = 0.0f, cl[PL];
+    float* o = tok + buf * 7 * Q;
+    LogSum base = {0.0f, 0.0f}, cl[PL];
 #pragma unroll
     for (int k = 0; k < PL; ++k) {
       const int t = k * 64 + lane;
       const bool on = t < rows;
       const float v = to_f32(draw[k]) + bias;
       const float sv = on ? step_of(a, to_f32(draw[k]), bias) : 0.0f;
-      cl[k] = base + wave_scan(on ? clamp_log2(sv * a2) : 0.0f);
+      const LogSum sum = log_scan(on ? clamp_log2(sv * a2) : 0.0f);
+      cl[k] = {base.hi + sum.hi, base.lo + sum.lo};
       base = last_lane(cl[k]);
-      o[t] = cl[k];
-      o[Q + t] = fast_exp2(cl[k]);
+      o[t] = cl[k].hi;
+      o[6 * Q + t] = cl[k].lo;
+      o[Q + t] = fast_exp2(cl[k].hi + cl[k].lo);
       o[2 * Q + t] = on ? (a.unit ? 1.0f : sv) : 0.0f;
       o[4 * Q + t] = sv;
       o[5 * Q + t] = a.softplus ? fast_rcp(1.0f + fast_exp2(-v * kLog2e)) : 1.0f;
     }
 #pragma unroll
-    for (int k = 0; k < PL; ++k) o[3 * Q + k * 64 + lane] = fast_exp2(base - cl[k]);
+    for (int k = 0; k < PL; ++k) o[3 * Q + k * 64 + lane] = decay_between(base, cl[k]);
   };
 #pragma unroll
   for (int k = 0; k < PL; ++k) draw[k] = In(0);
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       acc_ds[k] = __builtin_fmaf(Ah, G, acc_ds[k]) + (a.unit ? 0.0f : e_w[k]);
     }
     if (!done_last) return;
-    const float* o = tok + done_buf * 6 * Q;
+    const float* o = tok + done_buf * 7 * Q;
     float sa = 0.0f, sb = 0.0f;
 #pragma unroll
     for (int k = 0; k < PL; ++k) {
@@ -349,8 +351,8 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       yr.store(ys);
       decays(after(hd, pt), next(buf));
       if (hd > hd0 || pt > 0) put_dx(pt > 0 ? hd : hd - 1, pt > 0 ? pt - 1 : a.ptiles - 1);
-      const float* cs = tok + buf * 6 * Q;
-      const float *ec = cs + Q, *ww = cs + 2 * Q, *wd = cs + 3 * Q;
+      const float* cs = tok + buf * 7 * Q;
+      const float *ec = cs + Q, *ww = cs + 2 * Q, *wd = cs + 3 * Q, *cl = cs + 6 * Q;
       __syncthreads();
       finish();
       issue_step(last_pt ? after(hd + 1, 0) : after(hd, pt + 1));
@@ -384,13 +386,14 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
           for (int kk = 0; kk < 2; ++kk)
             X = mma(ys.row(x_row, 16 * I, kk), xs.row(x_row, 16 * J, kk), X);
           const float4 ct4 = *reinterpret_cast<const float4*>(cs + 16 * I + 4 * g);
-          const float ct[4] = {ct4.x, ct4.y, ct4.z, ct4.w};
-          const float cj = cs[16 * J + c], wj = ww[16 * J + c];
+          const float4 lt4 = *reinterpret_cast<const float4*>(cl + 16 * I + 4 * g);
+          const float ct[4] = {ct4.x, ct4.y, ct4.z, ct4.w}, lt[4] = {lt4.x, lt4.y, lt4.z, lt4.w};
+          const float cj = cs[16 * J + c], lj = cl[16 * J + c], wj = ww[16 * J + c];
           float m[4], er[4], col = 0.0f, diag = 0.0f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const bool on = I != J || 4 * g + r >= c;
-            const float l = fast_exp2(ct[r] - cj);
+            const float l = decay_between(ct[r], lt[r], cj, lj);
             const float m0 = on ? CB[k][r] * l : 0.0f;
             const float e0 = on ? m0 * X[r] : 0.0f;
             m[r] = m0 * wj;

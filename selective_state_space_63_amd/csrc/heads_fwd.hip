@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   };
   // The last wave (it has the fewest Gram tiles) forms the tokens' decays and
   // weights a chunk ahead, from steps loaded two chunks ahead: running log2
-  // decay, its exponential, input weight, weight decayed to the chunk's end.
+  // decay in two parts, input weight, weight decayed to the chunk's end.
   In draw = In(0);  // as loaded: a conversion here would wait for every load before it
   auto issue_step = [&](int64_t t0) {
     if (wv == 3 && dl) load_step<In, VEC>(draw, dl + t0 * a.d_token, a.d_token, lane, rows_at(t0));
@@ -132,13 +132,13 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
     if (wv != 3) return;
     const bool on = lane < rows_at(t0);
     const float s = on ? step_of(a, to_f32(draw), bias) : 0.0f;
-    const float v = wave_scan(on ? clamp_log2(s * a2) : 0.0f);
+    const LogSum v = log_scan(on ? clamp_log2(s * a2) : 0.0f);
     const float w = on ? (a.unit ? 1.0f : s) : 0.0f;
     float* o = tok + buf * 4 * kHQ;
-    o[lane] = v;
-    o[kHQ + lane] = fast_exp2(v);
+    o[lane] = v.hi;
+    o[kHQ + lane] = v.lo;
     o[2 * kHQ + lane] = w;
-    o[3 * kHQ + lane] = w * fast_exp2(last_lane(v) - v);
+    o[3 * kHQ + lane] = w * decay_between(last_lane(v), v);
   };
   issue_step(t_lo);
   issue(t_lo);
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
     // cost a workgroup per CU
     asm volatile("" : "+v"(b_row), "+v"(b_col), "+v"(c_row));
     const float* cs = tok + buf * 4 * kHQ;
-    const float *ec = cs + kHQ, *ww = cs + 2 * kHQ, *wd = cs + 3 * kHQ;
+    const float *cl = cs + kHQ, *ww = cs + 2 * kHQ, *wd = cs + 3 * kHQ;
     // An input that is not finite would reach earlier tokens through the
     // zeros of the Gram matrix (0 x inf): it is taken out here and its channel
     // set to NaN from its token on.
@@ -210,14 +210,16 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk)
           G = mma(bs.row(b_row, 16 * J, kk), cm.row(c_row, 16 * I, kk), G);
-        const float ct = cs[16 * I + c];
+        const float ct = cs[16 * I + c], lt = cl[16 * I + c];
         const float4 cv = *reinterpret_cast<const float4*>(cs + 16 * J + 4 * g);
+        const float4 lv = *reinterpret_cast<const float4*>(cl + 16 * J + 4 * g);
         const float4 wv4 = *reinterpret_cast<const float4*>(ww + 16 * J + 4 * g);
-        const float cj[4] = {cv.x, cv.y, cv.z, cv.w}, wj[4] = {wv4.x, wv4.y, wv4.z, wv4.w};
+        const float cj[4] = {cv.x, cv.y, cv.z, cv.w}, lj[4] = {lv.x, lv.y, lv.z, lv.w};
+        const float wj[4] = {wv4.x, wv4.y, wv4.z, wv4.w};
         float p[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          p[r] = I != J || c > 4 * g + r ? G[r] * (fast_exp2(ct - cj[r]) * wj[r]) : 0.0f;
+          p[r] = I != J || c > 4 * g + r ? G[r] * (decay_between(ct, lt, cj[r], lj[r]) * wj[r]) : 0.0f;
         if (I == J) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -247,7 +249,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) acc = mma(sf[kk], cm.row(c_row, 16 * I, kk), acc);
-        acc *= ec[16 * I + c];
+        acc *= fast_exp2(cs[16 * I + c] + cl[16 * I + c]);
 #pragma unroll
         for (int kk = 0; kk <= I / 2; ++kk) acc = mma(xf[kk], lane_frag(pf + (I * 2 + kk) * 512, lane), acc);
         float xv[4], o[4];
@@ -275,7 +277,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
     }
 
     put_y(t0);
-    const float dec = ec[kHQ - 1];
+    const float dec = fast_exp2(cs[kHQ - 1] + cl[kHQ - 1]);
 #pragma unroll
     for (int q = 0; q < NQ; ++q) S[q] *= dec;
 #pragma unroll

@@ -486,6 +486,25 @@ __device__ __forceinline__ float last_lane(float v) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
 
+// A running sum of log2 decays in two floats.  `hi` sums multiples of 2^-9,
+// exactly up to 2^15 (128 tokens of at most 150), `lo` the rests of at most
+// 2^-10 each.  So the difference of two sums is good to 2^-24 of itself, however
+// much the chunk decays beside it: one float would leave 2^-24 of the chunk's
+// whole sum in every decay, 7e-5 of it behind eight resets.
+struct LogSum {
+  float hi, lo;
+};
+__device__ __forceinline__ LogSum log_scan(float v) {
+  const float hi = rintf(v * 512.0f) * (1.0f / 512.0f);
+  return {wave_scan(hi), wave_scan(v - hi)};
+}
+__device__ __forceinline__ LogSum last_lane(LogSum v) { return {last_lane(v.hi), last_lane(v.lo)}; }
+// The decay from sum b on to sum a.
+__device__ __forceinline__ float decay_between(float a_hi, float a_lo, float b_hi, float b_lo) {
+  return fast_exp2((a_hi - b_hi) + (a_lo - b_lo));
+}
+__device__ __forceinline__ float decay_between(LogSum a, LogSum b) { return decay_between(a.hi, a.lo, b.hi, b.lo); }
+
 struct HeadsArgs {
   const void* x;
   const void* delta;      // or null (step 1)

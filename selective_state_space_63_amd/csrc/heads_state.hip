@@ -138,11 +138,10 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
     if (wv == 0) {
       const bool on = lane < rows;
       const float s = on ? step_of(a, to_f32(draw), bias) : 0.0f;
-      const float cs = wave_scan(on ? clamp_log2(s * a2) : 0.0f);
-      const float cq = last_lane(cs);
+      const LogSum cs = log_scan(on ? clamp_log2(s * a2) : 0.0f), cq = last_lane(cs);
       const float w = on ? (a.unit ? 1.0f : s) : 0.0f;
-      wt[lane] = dir ? fast_exp2(cs) : w * fast_exp2(cq - cs);
-      if (lane == 0) total_s = cq;
+      wt[lane] = dir ? fast_exp2(cs.hi + cs.lo) : w * decay_between(cq, cs);
+      if (lane == 0) total_s = cq.hi + cq.lo;
     }
     __syncthreads();
     issue(k + step);
