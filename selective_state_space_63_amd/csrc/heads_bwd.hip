@@ -15,9 +15,14 @@
 //        + sum_{u >= t} e^{c_u} dy_u . S C_u              (from before the block)
 //        + sum_{s < t} w_s e^{c_Q - c_s} x_s . L B_s      (to after the block)
 //        + e^{c_Q} <L, S>                                 (through it)
-// The four parts of G are sums of like terms, not differences of running
-// totals over the sequence, so G keeps its relative accuracy where the decay
-// is strong.
+// Where a decay is strong G_t is far smaller than what lies on either side of
+// t, so no part of it is taken as a difference of running totals: the sums over
+// u >= t and over s < t run from their own ends, and the part inside the block
+// is added up from 16 x 16 tiles of w E with t in tile T: the tiles with rows
+// after T and columns before T, the rows from t on of the tiles left of (T, T),
+// the columns before t of the tiles below it, and the corner of (T, T) itself.
+// (From totals and prefixes, a fp32 head with A = -20 and steps of 1 missed dA by
+// 4e-3 of its terms, and a reset's step added rounding noise times itself.)
 //
 // Two phases.  s6_heads_state_kernel walks the sequence in both directions
 // and stores S and L entering every block (bf16 inputs: as two bf16 planes in
@@ -32,8 +37,8 @@
 // Waves: wave w owns the 16 state columns n of strip w % NS in the products
 // with S and L (dC, dB: rows n, columns t), all of them in registers, and
 // for dx the channel tile w % 4 of every second token tile.  Wave 7 forms the
-// next head's decays, wave 4 finishes the last head's step gradients behind
-// the next turn's barrier, so neither is waited for.
+// next head's decays, waves 4 and 5 finish the last head's step gradients
+// behind the next turn's barrier, so neither is waited for.
 //
 // Roundings (bf16 inputs): P, the decayed Gram matrix and, for dx, L are taken
 // in bf16 (dx, dB, dC are rounded to it); the step's and the decay's gradients
@@ -61,7 +66,7 @@ struct HeadsBwdArgs {
   void* ddelta;           // or null
   void* dB;
   void* dC;
-  float* parts;           // (3, batch * nblk, heads): dA, dD, dbias per block
+  float* parts;           // (3, batch * nblk * Q / 64, heads): dA, dD, dbias per 64 tokens
   float* bc;              // (nhb, 2, batch * L, groups, NT) partial dB, dC, or null (one head run)
   int64_t nblk, rows;
   int groups, nhb, hpb;   // head runs of a group and heads per run
@@ -92,7 +97,8 @@ struct BwdLds {
   static constexpr int tok = up + NS * Q * 4;                    // per-token values, three turns' worth
   static constexpr int th = tok + 3 * 7 * Q * 4;                 // <L, S> by strip
   static constexpr int dd = th + 8 * 4;                          // x . dy by diagonal tile
-  static constexpr int total = dd + 8 * 4;
+  static constexpr int tb = dd + 8 * 4;                          // by token tile, see finish()
+  static constexpr int total = tb + (2 * NTT + NTT * NTT) * 4;
   static_assert(total <= 163840, "LDS");
 };
 
@@ -123,6 +129,9 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   float* tok = reinterpret_cast<float*>(lds + O::tok);
   float* th = reinterpret_cast<float*>(lds + O::th);
   float* ddp = reinterpret_cast<float*>(lds + O::dd);
+  float* const tb_y = reinterpret_cast<float*>(lds + O::tb);  // dy . S C of a token tile
+  float* const tb_u = tb_y + NTT;                             // w x . L B of a token tile
+  float* const tb_in = tb_u + NTT;                            // (j, T): w E, rows of tile T, columns before tile j
 
   const HeadsArgs& a = ba.h;
   uint32_t id = blockIdx.x;  // (sequence, group, head run, block), the block fastest; below 2^31
@@ -159,6 +168,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   // and what lies past the sequence: its token tiles are left out below
   for (int i = threadIdx.x; i < Q * NS; i += 512) yp[i] = up[i] = 0.0f;
   if (threadIdx.x < 8) ddp[threadIdx.x] = 0.0f;
+  if (threadIdx.x < NTT * NTT) tb_in[threadIdx.x] = 0.0f;
 
   TileRegs<In, Q, kTP, 512, VEC> xr, yr;
   auto issue = [&](int hd, int pt) {
@@ -236,9 +246,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
 #pragma unroll
   for (int i = 0; i < TT; ++i) dC[i] = dB[i] = f32x4{0, 0, 0, 0};
 
-  float acc_g[PL], acc_ds[PL], acc_d = 0.0f;  // wave 4: sums over the channel tiles of a head
-#pragma unroll
-  for (int k = 0; k < PL; ++k) acc_g[k] = acc_ds[k] = 0.0f;
+  float acc_g = 0.0f, acc_ds = 0.0f, acc_d = 0.0f;  // sums over the channel tiles of a head
 
   // dx of a turn is stored in the next one, behind the wait for its inputs
   // (stores before it would be waited for as well)
@@ -283,53 +291,48 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       touched = reinterpret_cast<const uint32_t*>(sp)[(threadIdx.x & 255) * 32];
     }
   };
-  // Wave 4, for the turn before: the decay's and the step's gradients.
-  float e_in[PL], e_y[PL], e_u[PL], e_w[PL], through = 0.0f;
+  // Waves 4 and 5 (fp32: 4), 64 tokens each, for the turn before: the decay's and
+  // the step's gradients.  What a token needs of the other tiles of tokens is
+  // left in LDS by tile (tb_*).
+  const bool tokens_wave = wv >= 4 && wv < 4 + PL;
+  float e_in = 0.0f, e_row = 0.0f, e_col = 0.0f, e_y = 0.0f, e_u = 0.0f, e_w = 0.0f, through = 0.0f;
   int done_hd = -1, done_buf = 0;
   bool done_last = false;
   auto finish = [&]() {
-    if (wv != 4 || done_hd < 0) return;
+    if (!tokens_wave || done_hd < 0) return;
     const float Ah = a.A[done_hd];
-    float in0 = 0.0f, y0 = 0.0f, u0 = 0.0f;  // running totals of the 64-token halves
-    float in[PL], ysum[PL], usum[PL];
+    const int T = 4 * (wv - 4) + (lane >> 4);
+    float in = e_in + row_from(e_row) + row_before(e_col), y = row_from(e_y), u = row_before(e_u);
+    float v[3][NTT];
 #pragma unroll
-    for (int k = 0; k < PL; ++k) {
-      const float si = wave_scan(e_in[k]), sy = wave_scan(e_y[k]), su = wave_scan(e_u[k]);
-      in[k] = in0 + (si - e_in[k]);   // exclusive
-      usum[k] = u0 + (su - e_u[k]);   // exclusive
-      ysum[k] = y0 + (sy - e_y[k]);   // exclusive; the suffix is the total less this
-      in0 += last_lane(si); u0 += last_lane(su); y0 += last_lane(sy);
+    for (int j = 0; j < NTT; j += 4) {
+      *reinterpret_cast<float4*>(&v[0][j]) = *reinterpret_cast<const float4*>(tb_in + T * NTT + j);
+      *reinterpret_cast<float4*>(&v[1][j]) = *reinterpret_cast<const float4*>(tb_y + j);
+      *reinterpret_cast<float4*>(&v[2][j]) = *reinterpret_cast<const float4*>(tb_u + j);
     }
 #pragma unroll
-    for (int k = 0; k < PL; ++k) {
-      const float G = (in[k] + usum[k]) + ((y0 - ysum[k]) + through);
-      acc_g[k] += G;
-      acc_ds[k] = __builtin_fmaf(Ah, G, acc_ds[k]) + (a.unit ? 0.0f : e_w[k]);
+    for (int j = 0; j < NTT; ++j) {
+      in += v[0][j];
+      y += j > T ? v[1][j] : 0.0f;
+      u += j < T ? v[2][j] : 0.0f;
     }
+    const float G = (in + u) + (y + through);
+    acc_g += G;
+    acc_ds = __builtin_fmaf(Ah, G, acc_ds) + (a.unit ? 0.0f : e_w);
     if (!done_last) return;
     const float* o = tok + done_buf * 7 * Q;
-    float sa = 0.0f, sb = 0.0f;
-#pragma unroll
-    for (int k = 0; k < PL; ++k) {
-      const int t = k * 64 + lane;
-      const float dv = acc_ds[k] * o[5 * Q + t];
-      if (t < rows) {
-        sa = __builtin_fmaf(o[4 * Q + t], acc_g[k], sa);
-        sb += dv;
-        if (ba.ddelta)
-          static_cast<In*>(ba.ddelta)[(b * a.L + t0 + t) * a.heads + done_hd] = from_f32<In>(dv);
-      }
-      acc_g[k] = acc_ds[k] = 0.0f;
-    }
-    sa = wave_sum(sa);
-    sb = wave_sum(sb);
+    const int t = 64 * (wv - 4) + lane;
+    const float dv = acc_ds * o[5 * Q + t];
+    if (t < rows && ba.ddelta)
+      static_cast<In*>(ba.ddelta)[(b * a.L + t0 + t) * a.heads + done_hd] = from_f32<In>(dv);
+    const float sa = wave_sum(t < rows ? o[4 * Q + t] * acc_g : 0.0f), sb = wave_sum(t < rows ? dv : 0.0f);
     if (lane == 0) {
-      const int64_t n = a.batch * ba.nblk, at = (b * ba.nblk + blk) * a.heads + done_hd;
+      const int64_t n = a.batch * ba.nblk * PL, at = ((b * ba.nblk + blk) * PL + (wv - 4)) * a.heads + done_hd;
       ba.parts[at] = sa;
       ba.parts[n * a.heads + at] = acc_d;
       ba.parts[2 * n * a.heads + at] = sb;
     }
-    acc_d = 0.0f;
+    acc_g = acc_ds = acc_d = 0.0f;
   };
   int buf = 0;
   auto next = [](int i) { return i == 2 ? 0 : i + 1; };
@@ -403,6 +406,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
             if (I == J && 4 * g + r == c) diag = X[r];
           }
           store_vec<In, 4>(mf + frag_at<H>(J, I >> 1) * 512 + lane * 8 + 4 * (I & 1), m);
+          if (I == J) corner(er, g, c);  // a row's own part of G, in the place of its sum
 #pragma unroll
           for (int r = 0; r < 4; ++r) er[r] = row_sum(er[r]);
           // (every lane of a sum writes it: the same value to the same place)
@@ -493,39 +497,48 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       }
       __syncthreads();
 
-      // wave 4 takes the sums over tiles and strips now (they are written again
-      // after the next barrier) and finishes them behind that barrier
-      if (wv == 4) {
+      // Waves 4 and 5 take the sums over tiles and strips now (they are written
+      // again after the next barrier) and finish them behind that barrier.  A
+      // row's sums right of its tile and a column's above it are 0.
+      if (tokens_wave) {
+        const int t = 64 * (wv - 4) + lane, T = t >> 4;
+        float v[2][NTT];
 #pragma unroll
-        for (int k = 0; k < PL; ++k) {
-          const int t = k * 64 + lane;
-          float v[4][8];
-#pragma unroll
-          for (int j = 0; j < NTT; j += 4) {
-            *reinterpret_cast<float4*>(&v[0][j]) = *reinterpret_cast<const float4*>(rp + t * NTT + j);
-            *reinterpret_cast<float4*>(&v[1][j]) = *reinterpret_cast<const float4*>(cp + t * NTT + j);
-          }
-#pragma unroll
-          for (int j = 0; j < NS; j += 2) {
-            *reinterpret_cast<float2*>(&v[2][j]) = *reinterpret_cast<const float2*>(yp + t * NS + j);
-            *reinterpret_cast<float2*>(&v[3][j]) = *reinterpret_cast<const float2*>(up + t * NS + j);
-          }
-          float R = 0.0f, K = 0.0f, Y = 0.0f, U = 0.0f;
-#pragma unroll
-          for (int j = 0; j < NTT; ++j) { R += v[0][j]; K += v[1][j]; }
-#pragma unroll
-          for (int j = 0; j < NS; ++j) { Y += v[2][j]; U += v[3][j]; }
-          const float w = ww[t];
-          e_in[k] = w * K - R;
-          e_y[k] = Y;
-          e_u[k] = w * U;
-          e_w[k] = K + U;
+        for (int j = 0; j < NTT; j += 4) {
+          *reinterpret_cast<float4*>(&v[0][j]) = *reinterpret_cast<const float4*>(rp + t * NTT + j);
+          *reinterpret_cast<float4*>(&v[1][j]) = *reinterpret_cast<const float4*>(cp + t * NTT + j);
         }
+        float R = 0.0f, K = 0.0f, own = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NTT; ++j) {
+          // the rows of tile T, columns before tile j < T
+          if (j > 0 && j < NTT - 1) tb_in[j * NTT + T] = row_sum(j < T ? R : 0.0f);
+          R += j < T ? v[0][j] : 0.0f;
+          K += j > T ? v[1][j] : 0.0f;
+          e_in = j == T ? v[0][j] : e_in;
+          own = j == T ? v[1][j] : own;
+        }
+        float w[2][NS], Y = 0.0f, U = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NS; j += 2) {
+          *reinterpret_cast<float2*>(&w[0][j]) = *reinterpret_cast<const float2*>(yp + t * NS + j);
+          *reinterpret_cast<float2*>(&w[1][j]) = *reinterpret_cast<const float2*>(up + t * NS + j);
+        }
+#pragma unroll
+        for (int j = 0; j < NS; ++j) { Y += w[0][j]; U += w[1][j]; }
+        const float wt = ww[t];
+        e_row = R;
+        e_col = wt * K;
+        e_y = Y;
+        e_u = wt * U;
+        e_w = (K + own) + U;
+        tb_y[T] = row_sum(e_y);
+        tb_u[T] = row_sum(e_u);
         through = 0.0f;
 #pragma unroll
         for (int n = 0; n < NS; ++n) through += th[n];
         through *= ec[Q - 1];
-        if (ba.want_d) {
+        if (ba.want_d && wv == 4) {
 #pragma unroll
           for (int I = 0; I < NTT; ++I) acc_d += ddp[I];
         }
@@ -536,6 +549,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
     }
   }
 
+  __syncthreads();
   finish();
   put_dx(hd1 - 1, a.ptiles - 1);
 
@@ -670,7 +684,7 @@ BwdWs bwd_ws(const s6_heads_dims& d, const HeadsPlan& p, int in_dtype) {
   o.sd = o.agg + (o.nseg > 1 ? up256(2 * (size_t)o.nseg * tile) : 0);
   o.hin = o.sd + (o.nseg > 1 ? up256(2 * (size_t)o.nseg * p.rows * sizeof(float)) : 0);
   o.parts = o.hin + (o.nseg > 1 ? up256(2 * (size_t)o.nseg * tile) : 0);
-  o.bc = o.parts + up256(3 * (size_t)d.batch * o.nblk * d.heads * sizeof(float));
+  o.bc = o.parts + up256(3 * (size_t)d.batch * o.nblk * (q / 64) * d.heads * sizeof(float));
   o.total = o.bc + (o.nhb > 1 ? up256((size_t)o.nhb * 2 * d.batch * d.seqlen * d.groups * p.NT * sizeof(float)) : 0);
   return o;
 }
@@ -707,7 +721,7 @@ int launch_sums(const HeadsBwdArgs& a, const HeadsPlan& p, float* dA, float* dD,
     S6_HIP(hipGetLastError(), "s6_heads_sum_bc launch");
   }
   hipLaunchKernelGGL(s6_heads_sum_parts, dim3((unsigned)a.h.heads, 3), dim3(256), 0, st, a.parts, dA, dD, dbias,
-                     a.h.batch * a.nblk, a.h.heads);
+                     a.h.batch * a.nblk * (kBQ<In> / 64), a.h.heads);
   S6_HIP(hipGetLastError(), "s6_heads_sum_parts launch");
   return S6_OK;
 }

@@ -486,6 +486,42 @@ __device__ __forceinline__ float last_lane(float v) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
 
+// Sums over the lanes of a 16-lane row: this lane and those after it; those
+// before it (from their own terms alone: neither is the difference of two sums).
+__device__ __forceinline__ float row_from(float v) {
+  v += dpp_f<0x101>(v);  // row_shl:1, 2, 4, 8
+  v += dpp_f<0x102>(v);
+  v += dpp_f<0x104>(v);
+  v += dpp_f<0x108>(v);
+  return v;
+}
+__device__ __forceinline__ float row_before(float v) {
+  v += dpp_f<0x111>(v);  // row_shr:1, 2, 4, 8
+  v += dpp_f<0x112>(v);
+  v += dpp_f<0x114>(v);
+  v += dpp_f<0x118>(v);
+  return dpp_f<0x111>(v);
+}
+// Rows 4 g .. 4 g + 3 of column c, as a lane holds them of a 16 x 16 tile: for
+// each row t the column's sum over row t and those after it, 0 unless c < t.
+// Added over a row's lanes this is the tile's part with rows from t on and
+// columns before t.
+__device__ __forceinline__ void corner(float (&v)[4], int g, int c) {
+  float run = 0.0f;
+#pragma unroll
+  for (int r = 3; r >= 0; --r) {
+    run += c < 4 * g + r ? v[r] : 0.0f;
+    v[r] = run;
+  }
+  // the later row groups: the other of the pair, then the upper pair
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(run), __float_as_uint(run), false, false);
+  const float both = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(both), __float_as_uint(both), false, false);
+  const float later = ((g & 1) ? 0.0f : __uint_as_float(p[1])) + (g < 2 ? __uint_as_float(q[1]) : 0.0f);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = c < 4 * g + r ? v[r] + later : 0.0f;
+}
+
 // A running sum of log2 decays in two floats.  `hi` sums multiples of 2^-9,
 // exactly up to 2^15 (128 tokens of at most 150), `lo` the rests of at most
 // 2^-10 each.  So the difference of two sums is good to 2^-24 of itself, however

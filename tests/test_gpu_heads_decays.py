@@ -65,3 +65,29 @@ def test_forward_with_many_resets(torch_cuda, dtype):
         ry, my, _, _ = ref.scan(part["x"], part["delta"], part["A"], part["Bm"], part["Cm"], part["D"], None, None, False,
                                 True)
         close(y[:, lo:hi], ry, my, bar(dtype), f"y from {lo}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("unit", [True, False])
+@pytest.mark.parametrize("a", [-4.0, -8.0, -12.0, -16.0, -20.0])
+def test_strong_decays(torch_cuda, dtype, unit, a):
+    """Heads that forget within a token beside one that does not."""
+    torch = torch_cuda
+    d, n = case(torch, 1, 150, 3, 24, 1, 32, dtype, "softplus", True, 32)
+    d["bias"].fill_(0.6)   # steps of about 1
+    n["bias"][:] = np.float32(0.6)
+    A = np.array([a, 0.75 * a, -1e-3], np.float32)
+    d["A"].copy_(torch.from_numpy(A))
+    n["A"] = A.astype(np.float64)
+    both(torch, d, n, "softplus", unit, dtype, 33)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [3.0e3, 1.0e30])
+def test_gradients_with_resets(torch_cuda, dtype, value):
+    """Sequences packed one after another: nothing reaches across a reset, and
+    the reset's own step has no gradient."""
+    torch = torch_cuda
+    d, n = case(torch, 2, 300, 2, 64, 1, 64, dtype, "delta", True, 34)
+    resets(d, n, (0, 1, 17, 40, 63, 64, 130, 131, 160, 255, 256, 299), value)
+    both(torch, d, n, "delta", True, dtype, 35)
