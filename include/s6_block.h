@@ -21,7 +21,9 @@
  * and the heads' B and C in groups; S6_UNIT_INPUT makes s_t A a plain log
  * decay of linear attention (keys B, queries C, values x), and a NULL delta
  * a fixed decay per head.  A sequence packed after another starts from an
- * empty state where s_t A = -infinity (or below about -100).
+ * empty state where s_t A = -infinity (or below about -104; such a decay is 0
+ * and has no gradient).  Steps that large go with S6_UNIT_INPUT, since
+ * otherwise they scale the sequence's first input as well.
  *
  * Layout: token-major, last index fastest.
  *   x, y, dy, dx : (batch, seqlen, heads, headdim)   delta : (batch, seqlen, heads)

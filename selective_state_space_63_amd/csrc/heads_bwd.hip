@@ -316,16 +316,20 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       y += j > T ? v[1][j] : 0.0f;
       u += j < T ? v[2][j] : 0.0f;
     }
-    const float G = (in + u) + (y + through);
-    acc_g += G;
-    acc_ds = __builtin_fmaf(Ah, G, acc_ds) + (a.unit ? 0.0f : e_w);
-    if (!done_last) return;
     const float* o = tok + done_buf * 7 * Q;
     const int t = 64 * (wv - 4) + lane;
+    // A decay taken as 0 (see clamp_log2) has no gradient, and the products of its
+    // step and A, either of which may be infinite, with 0 are left out.
+    const float step = o[4 * Q + t];
+    const bool gone = step * (Ah * kLog2e) <= kMinLog2;
+    const float G = gone ? 0.0f : (in + u) + (y + through);
+    acc_g += G;
+    acc_ds = (gone ? acc_ds : __builtin_fmaf(Ah, G, acc_ds)) + (a.unit ? 0.0f : e_w);
+    if (!done_last) return;
     const float dv = acc_ds * o[5 * Q + t];
     if (t < rows && ba.ddelta)
       static_cast<In*>(ba.ddelta)[(b * a.L + t0 + t) * a.heads + done_hd] = from_f32<In>(dv);
-    const float sa = wave_sum(t < rows ? o[4 * Q + t] * acc_g : 0.0f), sb = wave_sum(t < rows ? dv : 0.0f);
+    const float sa = wave_sum(t < rows && !gone ? step * acc_g : 0.0f), sb = wave_sum(t < rows ? dv : 0.0f);
     if (lane == 0) {
       const int64_t n = a.batch * ba.nblk * PL, at = ((b * ba.nblk + blk) * PL + (wv - 4)) * a.heads + done_hd;
       ba.parts[at] = sa;

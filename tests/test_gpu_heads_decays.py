@@ -91,3 +91,26 @@ def test_gradients_with_resets(torch_cuda, dtype, value):
     d, n = case(torch, 2, 300, 2, 64, 1, 64, dtype, "delta", True, 34)
     resets(d, n, (0, 1, 17, 40, 63, 64, 130, 131, 160, 255, 256, 299), value)
     both(torch, d, n, "delta", True, dtype, 35)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_with_infinite_steps(torch_cuda, dtype):
+    """A reset by a step of +infinity: the limit of large steps, whose gradients
+    are 0 at that token and what they are without it elsewhere."""
+    torch = torch_cuda
+    d, n = case(torch, 1, 150, 2, 64, 1, 64, dtype, "delta", True, 36)
+    for t in (50, 97, 128):
+        d["delta"][:, t] = float("inf")
+        n["delta"][:, t] = 1.0e30
+    both(torch, d, n, "delta", True, dtype, 37)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("unit", [True, False])
+def test_gradients_with_infinite_decay(torch_cuda, dtype, unit):
+    """A head with A = -infinity keeps nothing: its decay has no gradient."""
+    torch = torch_cuda
+    d, n = case(torch, 2, 140, 2, 16, 1, 16, dtype, "softplus", True, 38)
+    d["A"][1] = float("-inf")
+    n["A"][1] = -1.0e30
+    both(torch, d, n, "softplus", unit, dtype, 39)
