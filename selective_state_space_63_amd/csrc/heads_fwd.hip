@@ -19,9 +19,9 @@
 // Gram tiles are shared out among the waves and meet in LDS in operand order.
 //
 // Roundings (bf16 inputs): the decayed Gram matrix and the state's copy for
-// the product with C to bf16, as y is rounded to bf16 anyway; the diagonal
-// (a token's own input) stays in fp32 with the skip; the inputs of the state
-// itself enter in full, as three bf16 parts.
+// the product with C enter as two bf16 parts (within 2^-17), so that y meets one
+// rounding, its own; the diagonal (a token's own input) stays in fp32 with the
+// skip; the inputs of the state itself enter in full, as three bf16 parts.
 //
 // What bounds it: the latency of a chunk's chain (stage -> Gram -> y -> state,
 // three barriers), not a unit: at 8 x 2048 tokens of 80 heads of 64, N 128,
@@ -39,6 +39,23 @@ namespace s6i {
 
 namespace {
 
+// The decayed Gram matrix in LDS: the ten tiles J <= I of 256 values, in operand
+// order: two tiles J = 2 kk, 2 kk + 1 per operand, or the diagonal tile of an even
+// I alone (what is right of it is 0).
+constexpr int kGram = 2560;
+__device__ __forceinline__ int gram_at(int I, int kk) { return (I == 0 ? 0 : I == 1 ? 256 : I == 2 ? 768 : 1536) + 512 * kk; }
+template <typename In>
+__device__ __forceinline__ Frag<In> gram_frag(const In* p, int I, int kk, int lane) {
+  if (kk < I / 2 || (I & 1)) return lane_frag(p + gram_at(I, kk), lane);
+  float f[4], e[8];
+  load_vec<In, 4>(p + gram_at(I, kk) + 4 * lane, f);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) e[r] = r < 4 ? f[r] : 0.0f;
+  Frag<In> o;
+  to_frag(e, o);
+  return o;
+}
+
 // Offsets in LDS (bytes).
 template <typename In, int NT>
 struct ScanLds {
@@ -49,11 +66,13 @@ struct ScanLds {
   static constexpr int bs = xs + XT::size(kHQ) * (int)sizeof(In);
   static constexpr int cm = bs + BT::size(kHQ) * (int)sizeof(In);
   static constexpr int pf = cm + CT::size(kHQ) * (int)sizeof(In);
-  static constexpr int tok = pf + 4096 * (int)sizeof(In);
+  static constexpr int tok = pf + (sizeof(In) == 2 ? 2 : 1) * kGram * (int)sizeof(In);
   static constexpr int dg = tok + 2 * 4 * kHQ * 4;
   static constexpr int bad = dg + kHQ * 4;
-  static constexpr int total = bad + (kTP + 4) * 4;
+  static constexpr int total = bad + kTP * 4;
 };
+// Three workgroups of bf16 fit a CU (LDS is given out in pieces of 1280 bytes).
+static_assert(3 * ((ScanLds<uint16_t, 128>::total + 1279) / 1280 * 1280) <= 163840, "LDS");
 
 template <typename In, int NT, bool VEC>
 __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_heads_scan_kernel(HeadsArgs a) {
@@ -63,11 +82,10 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   const typename L::XT xs{reinterpret_cast<In*>(lds + L::xs)};
   const typename L::BT bs{reinterpret_cast<In*>(lds + L::bs)};
   const typename L::CT cm{reinterpret_cast<In*>(lds + L::cm)};
-  In* pf = reinterpret_cast<In*>(lds + L::pf);             // [4 t tiles][2][lane][8]
+  In* pf = reinterpret_cast<In*>(lds + L::pf);             // decayed Gram matrix; bf16: two parts of kGram
   float* tok = reinterpret_cast<float*>(lds + L::tok);     // per-token values, two chunks' worth
   float* dg = reinterpret_cast<float*>(lds + L::dg);       // the Gram matrix's diagonal times the weights
   int* bad = reinterpret_cast<int*>(lds + L::bad);         // first token whose input is not finite
-  int* any = bad + kTP;
   // consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of
   // rows, whose B and C come through one L2
   const int64_t nrows = gridDim.x;
@@ -89,8 +107,6 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   const float dsk = a.D ? a.D[hr.hd] : 0.0f;
 
   if (threadIdx.x < kTP) bad[threadIdx.x] = kHQ;
-  if (threadIdx.x == 0) *any = 0;
-  for (int i = threadIdx.x; i < 4 * 2 * 512; i += 256) pf[i] = In(0);  // tiles above the diagonal stay 0
 
   // state tiles: rows n = 16 q + 4 g + r, column p = 16 wv + c
   f32x4 S[NQ];
@@ -188,7 +204,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
     xr.mask(rows, cols);
     br.mask(rows, a.dstate);
     cr.mask(rows, a.dstate);
-    xr.clean(bad, any);
+    xr.clean(bad);
     xr.store(xs);
     br.store(bs);
     cr.store(cm);
@@ -225,7 +241,14 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
           for (int r = 0; r < 4; ++r)
             if (c == 4 * g + r) dg[16 * I + c] = G[r] * wj[r];
         }
-        store_vec<In, 4>(pf + ((I * 2 + (J >> 1)) * 64 + lane) * 8 + 4 * (J & 1), p);
+        In* at = pf + gram_at(I, J >> 1) + (I == J && !(I & 1) ? 4 * lane : 8 * lane + 4 * (J & 1));
+        store_vec<In, 4>(at, p);
+        if constexpr (sizeof(In) == 2) {
+          float lo[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) lo[r] = p[r] - (float)(__bf16)p[r];
+          store_vec<In, 4>(at + kGram, lo);
+        }
       }
     }
     __syncthreads();
@@ -234,24 +257,32 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) xf[kk] = xs.col(x_col, wv, kk, g, c);
     {
-      Frag<In> sf[NK];
+      f32x4 out[4];
+#pragma unroll
+      for (int I = 0; I < 4; ++I) out[I] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk) {
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = S[2 * kk + (e >> 2)][e & 3];
-        to_frag(f, sf[kk]);  // bf16: y is rounded to bf16 anyway
+        Pair<In> sf;
+        to_pair(f, sf);
+#pragma unroll
+        for (int I = 0; I < 4; ++I) out[I] = mma_pair(sf, cm.row(c_row, 16 * I, kk), out[I]);
       }
-      const bool dirty = *any != 0;
+      __builtin_amdgcn_sched_barrier(0);  // (mixed with what follows it would spill)
+      const bool dirty = __builtin_amdgcn_ballot_w64(bad[lane] != kHQ) != 0;
       const int p = 16 * wv + 4 * g;
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
-        f32x4 acc = {0, 0, 0, 0};
+        f32x4 acc = out[I] * fast_exp2(cs[16 * I + c] + cl[16 * I + c]);
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) acc = mma(sf[kk], cm.row(c_row, 16 * I, kk), acc);
-        acc *= fast_exp2(cs[16 * I + c] + cl[16 * I + c]);
-#pragma unroll
-        for (int kk = 0; kk <= I / 2; ++kk) acc = mma(xf[kk], lane_frag(pf + (I * 2 + kk) * 512, lane), acc);
+        for (int kk = 0; kk <= I / 2; ++kk) {
+          Pair<In> gm;
+          gm.hi = gram_frag(pf, I, kk, lane);
+          if constexpr (sizeof(In) == 2) gm.lo = gram_frag(pf + kGram, I, kk, lane);
+          acc = mma_pair(xf[kk], gm, acc);
+        }
         float xv[4], o[4];
         xs.four(16 * I + c, 4 * wv + g, xv);
         // a token's own input enters in fp32, with the skip: it is the largest

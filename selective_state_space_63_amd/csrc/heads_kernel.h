@@ -91,6 +91,11 @@ __device__ __forceinline__ f32x4 mma_pair(const Pair<uint16_t>& a, const Frag<ui
   return mma(a.lo, b, mma(a.hi, b, d));
 }
 __device__ __forceinline__ f32x4 mma_pair(const Pair<float>& a, const Frag<float>& b, f32x4 d) { return mma(a.hi, b, d); }
+// d += a (hi + lo)
+__device__ __forceinline__ f32x4 mma_pair(const Frag<uint16_t>& a, const Pair<uint16_t>& b, f32x4 d) {
+  return mma(a, b.lo, mma(a, b.hi, d));
+}
+__device__ __forceinline__ f32x4 mma_pair(const Frag<float>& a, const Pair<float>& b, f32x4 d) { return mma(a, b.hi, d); }
 
 // Eight floats as the exact sum of operands: three bf16 parts hold the 24 bits
 // of a float (down to the smallest bf16), one float part itself.  For what
@@ -446,8 +451,8 @@ struct TileRegs {
       if (ROWS * kPer % THREADS == 0 || row_of(k) < ROWS) r[k].put(tile, row_of(k), col_of() / 8);
   }
   // Values that are not finite become 0; first[column] receives the first
-  // row that held one, *any is set.  Returns whether there was one.
-  __device__ __forceinline__ void clean(int* first, int* any) {
+  // row that held one.
+  __device__ __forceinline__ void clean(int* first) {
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
       if (r[k].nonfinite()) {
@@ -461,7 +466,6 @@ struct TileRegs {
             atomicMin(first + col_of(tid) + j, row_of(k, tid));
           }
         r[k].set(e);
-        *any = 1;
       }
     }
   }

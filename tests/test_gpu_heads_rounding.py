@@ -1,0 +1,45 @@
+"""bf16 results of the multi-head scan and its gradients meet one rounding, that
+of the result: what is rounded on the way keeps two bf16 parts at least.
+
+Bar: before its rounding a result is within 2^-15 of its magnitude m (the sum of
+its terms' absolute values; the bar of results kept in fp32 in
+test_gpu_heads_scan.py).  Rounding v to 8 significant bits is off by at most
+2^-8 |v| (just above a power of two the spacing is 2^-7 |v|).  So a result is
+within 2^-8 |v| + 1.01 * 2^-15 m of the value v of its definition; where terms
+cancel this is far less than a rounding of the terms.
+"""
+import numpy as np
+import pytest
+
+import block_ref as ref
+from test_gpu_heads_scan import IDS, KEPT_BAR, case, fwd, torch_cuda  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [
+    # batch, L, heads, headdim, groups, dstate, dtype, step, unit, h0, packed, pad
+    (2, 333, 4, 64, 1, 128, "bf16", "softplus", False, True, True, 0),
+    (2, 200, 6, 64, 2, 64, "bf16", "delta", False, False, False, 0),
+    (3, 129, 4, 40, 2, 24, "bf16", "none", True, True, False, 0),
+    (2, 200, 3, 72, 1, 33, "bf16", "softplus", False, True, True, 3),
+    (1, 2000, 2, 64, 1, 128, "bf16", "softplus", False, True, False, 0),   # segments
+    (8, 300, 40, 16, 1, 128, "bf16", "softplus", False, True, False, 0),   # runs of several heads
+]
+
+
+def rounded_once(got, want, mag, what):
+    got = got.detach().double().cpu().numpy()
+    room = 2.0 ** -8 * np.abs(want) + 1.01 * KEPT_BAR * mag
+    worst = float(np.max(np.abs(got - want) / np.maximum(room, 1e-30)))
+    assert worst <= 1.0, f"{what}: {worst:.3f} of a rounding"
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_y_is_rounded_once(torch_cuda, shape):
+    b, L, H, P, G, N, dtype, step, unit, h0, packed, pad = shape
+    print(f"[case] heads scan {shape}", flush=True)
+    d, n = case(torch_cuda, b, L, H, P, G, N, dtype, step, h0, 61, packed, pad)
+    y, _ = fwd(d, step, unit)
+    ry, my, _, _ = ref.scan(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], n["D"], n["h0"], n["bias"], step == "softplus",
+                            unit)
+    rounded_once(y, ry, my, "y")
