@@ -40,9 +40,9 @@
 // next head's decays, waves 4 and 5 finish the last head's step gradients
 // behind the next turn's barrier, so neither is waited for.
 //
-// Roundings (bf16 inputs): P, the decayed Gram matrix and, for dx, L are taken
-// in bf16 (dx, dB, dC are rounded to it); the step's and the decay's gradients
-// come from fp32 products and from S and L in two bf16 parts (within 2^-17).
+// Roundings (bf16 inputs): the decayed Gram matrix and, for dx, L are taken in
+// bf16 (dx is rounded to it); P, S and L otherwise as two bf16 parts (within
+// 2^-17), and the step's and the decay's gradients come from fp32 products.
 //
 // What bounds it: one workgroup of eight waves fits a CU (242 VGPRs, 157 KB of
 // LDS), so a turn is the sum of its phases' latencies: 11 us at 128 tokens x 64
@@ -557,22 +557,27 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   finish();
   put_dx(hd1 - 1, a.ptiles - 1);
 
-  // dC += P B and dB += P^T C with P summed over the heads (x and dy are done:
-  // every wave is past the last barrier), P rounded to the input type
+  // dC += P B and dB += P^T C with P summed over the heads.  Every wave is past
+  // the last barrier, so all but the tokens' values is free: P lies in the place of
+  // x and dy, its second bf16 part in that of L and the decayed Gram matrix.
   {
-    const typename O::PT pm{xs.t};
+    const typename O::PT pm{xs.t}, pl{lm.t};
     static_assert(O::PT::size(Q) <= 2 * O::XT::size(Q), "P fits x and dy");
+    static_assert(sizeof(In) == 4 || O::PT::size(Q) * 2 <= O::tok - O::lm, "and its second part");
+    auto put = [&](int at, float v) {
+      pm.t[at] = from_f32<In>(v);
+      if constexpr (sizeof(In) == 2) pl.t[at] = from_f32<In>(v - (float)(__bf16)v);
+    };
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k) {
       if (8 * k + wv < O::NTILE) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          pm.t[pm.at(16 * tI[k] + 4 * g + r, 4 * tJ[k] + (c >> 2)) + (c & 3)] = from_f32<In>(P[k][r]);
+        for (int r = 0; r < 4; ++r) put(pm.at(16 * tI[k] + 4 * g + r, 4 * tJ[k] + (c >> 2)) + (c & 3), P[k][r]);
       }
     }
     if (wv < H) {  // the tile right of an even diagonal tile shares an operand with it
 #pragma unroll
-      for (int r = 0; r < 4; ++r) pm.t[pm.at(32 * wv + 4 * g + r, 4 * (2 * wv + 1) + (c >> 2)) + (c & 3)] = In(0);
+      for (int r = 0; r < 4; ++r) put(pm.at(32 * wv + 4 * g + r, 4 * (2 * wv + 1) + (c >> 2)) + (c & 3), 0.0f);
     }
     __syncthreads();
     const int p_row = O::PT::row_lane(g, c);
@@ -580,10 +585,17 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
     for (int i = 0; i < TT; ++i) {
       const int it = tp * TT + i;
       if (16 * it >= rows) continue;
-      for (int kk = 0; kk <= it / 2; ++kk)
-        dC[i] = mma(bs.col(ns, kk, g, c), pm.row(p_row, 16 * it, kk), dC[i]);
-      for (int kk = it / 2; kk < H; ++kk)
-        dB[i] = mma(cm.col(ns, kk, g, c), pm.col(it, kk, g, c), dB[i]);
+      Pair<In> p;
+      for (int kk = 0; kk <= it / 2; ++kk) {
+        p.hi = pm.row(p_row, 16 * it, kk);
+        if constexpr (sizeof(In) == 2) p.lo = pl.row(p_row, 16 * it, kk);
+        dC[i] = mma_pair(bs.col(ns, kk, g, c), p, dC[i]);
+      }
+      for (int kk = it / 2; kk < H; ++kk) {
+        p.hi = pm.col(it, kk, g, c);
+        if constexpr (sizeof(In) == 2) p.lo = pl.col(it, kk, g, c);
+        dB[i] = mma_pair(cm.col(ns, kk, g, c), p, dB[i]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < TT; ++i) {

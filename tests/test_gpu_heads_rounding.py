@@ -12,7 +12,7 @@ import numpy as np
 import pytest
 
 import block_ref as ref
-from test_gpu_heads_scan import IDS, KEPT_BAR, case, fwd, torch_cuda  # noqa: F401
+from test_gpu_heads_scan import IDS, KEPT_BAR, case, fwd, opts, torch_cuda  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,24 @@ def test_y_is_rounded_once(torch_cuda, shape):
     ry, my, _, _ = ref.scan(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], n["D"], n["h0"], n["bias"], step == "softplus",
                             unit)
     rounded_once(y, ry, my, "y")
+
+
+def gradients(torch, shape):
+    from selective_state_space_63_amd import block
+    b, L, H, P, G, N, dtype, step, unit, h0, packed, pad = shape
+    print(f"[case] heads scan gradients {shape}", flush=True)
+    d, n = case(torch, b, L, H, P, G, N, dtype, step, h0, 62, packed, pad)
+    g = np.random.default_rng(63)
+    dy = torch.from_numpy(g.standard_normal((b, L, H, P)).astype(np.float32)).cuda().to(d["x"].dtype)
+    dh = torch.from_numpy(g.standard_normal((b, H, P, N)).astype(np.float32)).cuda() if h0 else None
+    got = block.heads_scan_bwd(d["x"], d["delta"], d["A"], d["Bm"], d["Cm"], dy, dh_last=dh, **opts(d, step, unit))
+    want = ref.scan_bwd(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], dy.double().cpu().numpy(), n["D"], n["h0"],
+                        None if dh is None else dh.double().cpu().numpy(), n["bias"], step == "softplus", unit)
+    return got, want
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_gradients_of_B_and_C_are_rounded_once(torch_cuda, shape):
+    got, want = gradients(torch_cuda, shape)
+    for k in ("dBm", "dCm"):
+        rounded_once(got[k], *want[k], k)
