@@ -40,9 +40,9 @@
 // next head's decays, waves 4 and 5 finish the last head's step gradients
 // behind the next turn's barrier, so neither is waited for.
 //
-// Roundings (bf16 inputs): the decayed Gram matrix and, for dx, L are taken in
-// bf16 (dx is rounded to it); P, S and L otherwise as two bf16 parts (within
-// 2^-17), and the step's and the decay's gradients come from fp32 products.
+// Roundings (bf16 inputs): the decayed Gram matrix, P, S and L enter products as
+// two bf16 parts (within 2^-17), so that dx, dB and dC meet one rounding, their
+// own; the step's and the decay's gradients come from fp32 products.
 //
 // What bounds it: one workgroup of eight waves fits a CU (242 VGPRs, 157 KB of
 // LDS), so a turn is the sum of its phases' latencies: 11 us at 128 tokens x 64
@@ -365,8 +365,18 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       issue_step(last_pt ? after(hd + 1, 0) : after(hd, pt + 1));
       touch(after(hd, pt), last_pt ? 0 : pt + 1);
 
+      // the decays of Gram tile (I, J) of this wave
+      auto tile_decays = [&](int I, int J, float (&l)[4]) {
+        const float4 ct4 = *reinterpret_cast<const float4*>(cs + 16 * I + 4 * g);
+        const float4 lt4 = *reinterpret_cast<const float4*>(cl + 16 * I + 4 * g);
+        const float ct[4] = {ct4.x, ct4.y, ct4.z, ct4.w}, lt[4] = {lt4.x, lt4.y, lt4.z, lt4.w};
+        const float cj = cs[16 * J + c], lj = cl[16 * J + c];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) l[r] = decay_between(ct[r], lt[r], cj, lj);
+      };
       // inside the block
       Pair<In> Sf[2], Lf[2];
+      Four<In> m_lo[SLOTS];  // second parts of the decayed Gram tiles
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k) {
         if (k == SLOTS - 1) {
@@ -392,24 +402,26 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
             X = mma(ys.row(x_row, 16 * I, kk), xs.row(x_row, 16 * J, kk), X);
-          const float4 ct4 = *reinterpret_cast<const float4*>(cs + 16 * I + 4 * g);
-          const float4 lt4 = *reinterpret_cast<const float4*>(cl + 16 * I + 4 * g);
-          const float ct[4] = {ct4.x, ct4.y, ct4.z, ct4.w}, lt[4] = {lt4.x, lt4.y, lt4.z, lt4.w};
-          const float cj = cs[16 * J + c], lj = cl[16 * J + c], wj = ww[16 * J + c];
-          float m[4], er[4], col = 0.0f, diag = 0.0f;
+          const float wj = ww[16 * J + c];
+          float l[4], m[4], er[4], col = 0.0f, diag = 0.0f;
+          tile_decays(I, J, l);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const bool on = I != J || 4 * g + r >= c;
-            const float l = decay_between(ct[r], lt[r], cj, lj);
-            const float m0 = on ? CB[k][r] * l : 0.0f;
+            const float m0 = on ? CB[k][r] * l[r] : 0.0f;
             const float e0 = on ? m0 * X[r] : 0.0f;
             m[r] = m0 * wj;
             er[r] = e0 * wj;
             col += e0;
-            P[k][r] += on ? X[r] * (l * wj) : 0.0f;
+            P[k][r] += on ? X[r] * (l[r] * wj) : 0.0f;
             if (I == J && 4 * g + r == c) diag = X[r];
           }
           store_vec<In, 4>(mf + frag_at<H>(J, I >> 1) * 512 + lane * 8 + 4 * (I & 1), m);
+          if constexpr (sizeof(In) == 2) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m[r] -= (float)(__bf16)m[r];
+            m_lo[k].set(m);
+          }
           if (I == J) corner(er, g, c);  // a row's own part of G, in the place of its sum
 #pragma unroll
           for (int r = 0; r < 4; ++r) er[r] = row_sum(er[r]);
@@ -448,15 +460,23 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
         __builtin_amdgcn_sched_barrier(0);
       }
 
-      if (tp == 0) {
+      // a part of L by states, this wave's strip
+      auto put_l = [&](const typename O::LT& to, bool second) {
+        if (tp != 0) return;
 #pragma unroll
         for (int pp = 0; pp < 2; ++pp) {
           float f[4], h[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) { f[e] = frag_f32(Lf[pp].hi, e); h[e] = frag_f32(Lf[pp].hi, 4 + e); }
-          store_vec<In, 4>(lm.t + lm.at(16 * ns + c, 8 * pp + g), f);
-          store_vec<In, 4>(lm.t + lm.at(16 * ns + c, 8 * pp + 4 + g), h);
+          for (int e = 0; e < 4; ++e) {
+            f[e] = frag_f32(second ? Lf[pp].lo : Lf[pp].hi, e);
+            h[e] = frag_f32(second ? Lf[pp].lo : Lf[pp].hi, 4 + e);
+          }
+          store_vec<In, 4>(to.t + to.at(16 * ns + c, 8 * pp + g), f);
+          store_vec<In, 4>(to.t + to.at(16 * ns + c, 8 * pp + 4 + g), h);
         }
+      };
+      put_l(lm, false);
+      if (tp == 0) {
         float s = 0.0f;
 #pragma unroll
         for (int pp = 0; pp < 2; ++pp)
@@ -471,32 +491,68 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
       __syncthreads();
       issue(after(hd, pt), last_pt ? 0 : pt + 1);
 
-      // dx, transposed: channels of tile q, tokens of tiles J
+      // dx, transposed: channels of tile q, tokens of tiles J.  bf16: the second
+      // part of L takes the place of x, which is done, and that of the decayed Gram
+      // matrix the place of the first, once that is.
       {
         const int q = wv & 3;
         const auto l_col = O::LT::col_lane(g, c);
-        Frag<In> lq[NK], yq[H];
+        const typename O::LT ll{xs.t};
+        f32x4 acc[NTT / 2];
+        Frag<In> yq[H];
+        auto inside = [&]() {  // acc += dy^T M, for the part of M that is there
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) lq[kk] = lm.col(l_col, q, kk, g, c);
+          for (int i = 0; i < NTT / 2; ++i) {
+            const int J = 2 * i + (wv >> 2);
+            if (16 * J >= rows) continue;
+#pragma unroll
+            for (int kk = i; kk < H; ++kk) acc[i] = mma(yq[kk], lane_frag(mf + frag_at<H>(J, kk) * 512, lane), acc[i]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        };
+        if constexpr (sizeof(In) == 2) put_l(ll, true);
 #pragma unroll
         for (int kk = 0; kk < H; ++kk) yq[kk] = ys.col(q, kk, g, c);
 #pragma unroll
         for (int i = 0; i < NTT / 2; ++i) {
-          const int J = 2 * i + (wv >> 2), s = 16 * J + c;
-          if (16 * J >= rows) continue;
-          f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-          for (int kk = 0; kk < NK; ++kk) acc = mma(lq[kk], bs.row(b_row, 16 * J, kk), acc);
-          acc *= ww[s] * wd[s];
-#pragma unroll
-          for (int kk = i; kk < H; ++kk) acc = mma(yq[kk], lane_frag(mf + frag_at<H>(J, kk) * 512, lane), acc);
           float dyv[4];
-          ys.four(s, 4 * q + g, dyv);
+          ys.four(16 * (2 * i + (wv >> 2)) + c, 4 * q + g, dyv);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(dsk, dyv[r], acc[r]);
-          const float o[4] = {acc[0], acc[1], acc[2], acc[3]};
-          dxv[i].set(o);
+          for (int r = 0; r < 4; ++r) acc[i][r] = dsk * dyv[r];
+        }
+        inside();
+        if constexpr (sizeof(In) == 2) {
+          __syncthreads();
+#pragma unroll
+          for (int k = 0; k < SLOTS; ++k)
+            if (8 * k + wv < O::NTILE && 16 * tI[k] < rows)
+              m_lo[k].put(mf + frag_at<H>(tJ[k], tI[k] >> 1) * 512 + lane * 8 + 4 * (tI[k] & 1));
+        }
+        f32x4 lb[NTT / 2];  // B L, from after the block
+#pragma unroll
+        for (int i = 0; i < NTT / 2; ++i) lb[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+          Pair<In> lq;
+          lq.hi = lm.col(l_col, q, kk, g, c);
+          if constexpr (sizeof(In) == 2) lq.lo = ll.col(l_col, q, kk, g, c);
+#pragma unroll
+          for (int i = 0; i < NTT / 2; ++i) lb[i] = mma_pair(lq, bs.row(b_row, 16 * (2 * i + (wv >> 2)), kk), lb[i]);
           __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < NTT / 2; ++i) {
+          const int s = 16 * (2 * i + (wv >> 2)) + c;
+          acc[i] += lb[i] * (ww[s] * wd[s]);
+        }
+        if constexpr (sizeof(In) == 2) {
+          __syncthreads();
+          inside();
+        }
+#pragma unroll
+        for (int i = 0; i < NTT / 2; ++i) {
+          const float o[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+          dxv[i].set(o);
         }
       }
       __syncthreads();

@@ -293,6 +293,7 @@ struct Four<uint16_t> {
   uint32_t w[2];
   __device__ __forceinline__ void set(const float (&f)[4]) { w[0] = bf_pack(f[0], f[1]); w[1] = bf_pack(f[2], f[3]); }
   __device__ __forceinline__ uint16_t get(int r) const { return (uint16_t)(w[r >> 1] >> (16 * (r & 1))); }
+  __device__ __forceinline__ void put(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]); }
   __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
     __builtin_amdgcn_raw_buffer_store_b64(gu32x2{w[0], w[1]}, r, off, 0, 0);
   }

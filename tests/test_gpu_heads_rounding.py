@@ -64,3 +64,11 @@ def test_gradients_of_B_and_C_are_rounded_once(torch_cuda, shape):
     got, want = gradients(torch_cuda, shape)
     for k in ("dBm", "dCm"):
         rounded_once(got[k], *want[k], k)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_gradients_of_x_and_the_step_are_rounded_once(torch_cuda, shape):
+    got, want = gradients(torch_cuda, shape)
+    for k in ("dx", "ddelta"):
+        if k in got:
+            rounded_once(got[k], *want[k], k)

@@ -1,0 +1,45 @@
+"""Gradients of the multi-head scan where a workgroup walks several heads of a
+group: sums of dBm and dCm over them, values carried from one head to the next,
+shorter last runs, and several channel tiles per head.  The bars are those of
+test_gpu_heads_scan.py; a sum over h heads adds h roundings of fp32 (at most
+64 * 2^-24 = 2^-18 of the magnitude), which they leave room for.
+"""
+import numpy as np
+import pytest
+
+import block_ref as ref
+from test_gpu_heads_scan import IDS, bar, case, close, opts, torch_cuda  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [
+    # batch, L, heads, headdim, groups, dstate, dtype, step, unit, h0, packed, pad
+    (8, 500, 128, 8, 2, 16, "bf16", "softplus", False, True, False, 0),    # runs of 16 heads
+    (8, 250, 100, 8, 2, 16, "f32", "softplus", False, True, True, 8),      # runs of 13, the last shorter
+    (8, 450, 100, 8, 2, 40, "bf16", "delta", True, True, True, 8),         # (a second width of the state)
+    (64, 500, 3, 8, 1, 8, "bf16", "softplus", False, True, False, 0),      # one run of all heads
+    (64, 250, 3, 8, 1, 8, "f32", "none", True, False, False, 0),
+    (32, 300, 6, 72, 1, 8, "bf16", "softplus", False, True, False, 0),     # two channel tiles, runs of several heads
+    (32, 150, 8, 72, 1, 8, "f32", "softplus", False, True, False, 0),
+    (16, 260, 40, 7, 2, 5, "bf16", "softplus", False, True, True, 3),      # rows off the 16-byte loads
+    (16, 130, 40, 66, 2, 3, "f32", "delta", False, True, False, 0),
+    (8, 300, 48, 16, 1, 128, "bf16", "softplus", False, False, False, 0),  # the widest state
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_gradients_over_runs_of_heads(torch_cuda, shape):
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    b, L, H, P, G, N, dtype, step, unit, h0, packed, pad = shape
+    print(f"[case] heads scan gradients {shape}", flush=True)
+    d, n = case(torch, b, L, H, P, G, N, dtype, step, h0, 41, packed, pad)
+    g = np.random.default_rng(42)
+    dy = torch.from_numpy(g.standard_normal((b, L, H, P)).astype(np.float32)).cuda().to(d["x"].dtype)
+    dh = torch.from_numpy(g.standard_normal((b, H, P, N)).astype(np.float32)).cuda() if h0 else None
+    got = block.heads_scan_bwd(d["x"], d["delta"], d["A"], d["Bm"], d["Cm"], dy, dh_last=dh, **opts(d, step, unit))
+    torch.cuda.synchronize()
+    want = ref.scan_bwd(n["x"], n["delta"], n["A"], n["Bm"], n["Cm"], dy.double().cpu().numpy(), n["D"], n["h0"],
+                        None if dh is None else dh.double().cpu().numpy(), n["bias"], step == "softplus", unit)
+    for k in sorted(got):
+        close(got[k], *want[k], bar(dtype, k not in ("dx", "dBm", "dCm", "ddelta")), k)
