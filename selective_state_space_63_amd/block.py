@@ -4,7 +4,8 @@ norms before and after it.
 
 As in ``s6``: argument marshalling only, torch device tensors in and out, work
 enqueued on the current stream of the tensors' device.  ``HeadsScan``,
-``AddNorm`` and ``GatedNorm`` are the same operators for torch autograd.
+``AddNorm`` and ``GatedNorm`` are the same operators for torch autograd (once
+differentiable: a gradient of their gradients is an error).
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import s6
 from .s6 import _DT, _check
@@ -412,6 +414,7 @@ class HeadsScan(torch.autograd.Function):
         return heads_scan_fwd(x, delta, A, Bm, Cm, D=D, h0=h0, return_last_state=True, delta_bias=delta_bias, **ctx.opts)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh_last):
         x, delta, A, Bm, Cm, D, h0, delta_bias = ctx.saved_tensors
         dy = torch.zeros_like(x, memory_format=torch.contiguous_format) if dy is None else dy.contiguous()
@@ -434,6 +437,7 @@ class AddNorm(torch.autograd.Function):
         return out, res
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout, dres):
         res, weight, gamma, x = ctx.saved_tensors
         dout = torch.zeros(res.shape, dtype=ctx.dt, device=res.device) if dout is None else dout.contiguous()
@@ -453,6 +457,7 @@ class GatedNorm(torch.autograd.Function):
         return gated_norm_fwd(y, z, weight, **ctx.opts)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         y, z, weight = ctx.saved_tensors
         g = gated_norm_bwd(dout.contiguous(), y, z, weight, **ctx.opts)

@@ -11,6 +11,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libs6.so")
@@ -520,6 +521,7 @@ class SelectiveScan(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, delta, A, Bm, Cm, D, z, h0, delta_bias, ck = ctx.saved_tensors
         g = scan_bwd(x, delta, A, Bm, Cm, dy.contiguous().to(torch.float32), D=D, z=z, h0=h0,
