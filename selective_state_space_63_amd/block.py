@@ -219,11 +219,12 @@ def heads_scan_fwd(x, delta, A, Bm, Cm, D=None, h0=None, return_last_state=False
 
 
 def heads_scan_bwd(x, delta, A, Bm, Cm, dy, D=None, h0=None, dh_last=None, delta_bias=None, delta_softplus=False,
-                   unit_input=False):
+                   unit_input=False, skip=()):
     """Gradients of <dy, y> + <dh_last, h_last> for heads_scan_fwd with the
     same inputs.  dy: like y, contiguous; dh_last: like h_last or None.
     Returns a dict: dx, ddelta (where delta is given), dBm, dCm in the input
-    dtype; dA, and where their input is given dD, ddelta_bias, dh0 in fp32."""
+    dtype; dA, and where their input is given dD, ddelta_bias, dh0 in fp32.
+    skip: names among the last three to leave out."""
     dims, dt, flags = _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, True)
     sshape = (dims.batch, dims.heads, dims.headdim, dims.dstate)
     _whole(h0, "h0", sshape)
@@ -232,8 +233,10 @@ def heads_scan_bwd(x, delta, A, Bm, Cm, dy, D=None, h0=None, dh_last=None, delta
     _same_device(x, h0, dh_last, dy)
     new = lambda t: torch.empty_like(t, memory_format=torch.contiguous_format)  # noqa: E731
     g = {"dx": new(x), "dBm": new(Bm), "dCm": new(Cm), "dA": new(A)}
-    for name, t in (("ddelta", delta), ("dD", D), ("ddelta_bias", delta_bias), ("dh0", h0)):
-        if t is not None:
+    if delta is not None:
+        g["ddelta"] = new(delta)
+    for name, t in (("dD", D), ("ddelta_bias", delta_bias), ("dh0", h0)):
+        if t is not None and name not in skip:
             g[name] = new(t)
     lib = _load()
     ref = ctypes.byref(dims)
@@ -324,10 +327,11 @@ def add_norm_fwd(x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5, resi
     return out, residual_out
 
 
-def add_norm_bwd(dout, residual_out, weight, dresidual_out=None, x=None, gamma=None, scale=1.0, eps=1e-5):
+def add_norm_bwd(dout, residual_out, weight, dresidual_out=None, x=None, gamma=None, scale=1.0, eps=1e-5, skip=()):
     """Gradients of <dout, out> + <dresidual_out, r'> for add_norm_fwd, from
     the r' it returned.  Returns a dict: dx (dout's dtype), dresidual (r''s
-    dtype), dweight, and dgamma where gamma is given (then x is needed)."""
+    dtype), dweight, and dgamma where gamma is given (then x is needed).
+    skip: names among dx, dresidual and dweight, not all three, to leave out."""
     dt = _dtype(dout, "dout")
     rt = residual_out.dtype
     dim = dout.shape[-1]
@@ -342,15 +346,16 @@ def add_norm_bwd(dout, residual_out, weight, dresidual_out=None, x=None, gamma=N
     if gamma is not None:
         stride = _flat(x, "x", dout.shape, dt)
     _same_device(dout, residual_out, dresidual_out, weight, gamma, x)
-    g = {"dx": torch.empty_like(dout), "dresidual": torch.empty_like(residual_out), "dweight": torch.empty_like(weight)}
+    like = {"dx": dout, "dresidual": residual_out, "dweight": weight}
+    g = {name: torch.empty_like(t) for name, t in like.items() if name not in skip}
     if gamma is not None:
         g["dgamma"] = torch.empty_like(gamma)
     lib = _load()
     rows = math.prod(dout.shape[:-1])
     keep, wsp, wsn = _workspace(lib.s6_add_norm_bwd_workspace_size, dout, rows, dim)
     _launch(lib.s6_add_norm_bwd, dout, rows, dim, _DT[dt], _DT[rt], _at(dout), _at(dresidual_out), _at(residual_out),
-            _at(x) if gamma is not None else None, stride, _at(weight), _at(gamma), scale, eps, _at(g["dx"]),
-            _at(g["dresidual"]), _at(g["dweight"]), _at(g.get("dgamma")), wsp, wsn)
+            _at(x) if gamma is not None else None, stride, _at(weight), _at(gamma), scale, eps, _at(g.get("dx")),
+            _at(g.get("dresidual")), _at(g.get("dweight")), _at(g.get("dgamma")), wsp, wsn)
     del keep
     return g
 
@@ -383,22 +388,31 @@ def gated_norm_fwd(y, z, weight, groups=1, gate_after=False, eps=1e-5, out=None)
     return out
 
 
-def gated_norm_bwd(dout, y, z, weight, groups=1, gate_after=False, eps=1e-5):
+def gated_norm_bwd(dout, y, z, weight, groups=1, gate_after=False, eps=1e-5, skip=()):
     """Gradients of <dout, out> for gated_norm_fwd: a dict of dy, dz (where z
-    is given) in y's dtype and dweight in fp32."""
+    is given) in y's dtype and dweight in fp32 (left out where skip names it)."""
     dt, dim, ys, zs = _gated_args(y, z, weight, groups)
     _whole(_need(dout, "dout", y.shape, dt), "dout", y.shape, dt)
     _same_device(y, dout)
-    g = {"dy": torch.empty_like(dout), "dweight": torch.empty_like(weight)}
+    g = {"dy": torch.empty_like(dout)}
+    if "dweight" not in skip:
+        g["dweight"] = torch.empty_like(weight)
     if z is not None:
         g["dz"] = torch.empty_like(dout)
     lib = _load()
     rows = math.prod(y.shape[:-1])
     keep, wsp, wsn = _workspace(lib.s6_gated_norm_bwd_workspace_size, y, rows, dim, groups)
     _launch(lib.s6_gated_norm_bwd, y, rows, dim, groups, _DT[dt], S6_GATE_AFTER if gate_after else 0, _at(dout),
-            _at(y), ys, _at(z), zs, _at(weight), eps, _at(g["dy"]), _at(g.get("dz")), _at(g["dweight"]), wsp, wsn)
+            _at(y), ys, _at(z), zs, _at(weight), eps, _at(g["dy"]), _at(g.get("dz")), _at(g.get("dweight")), wsp, wsn)
     del keep
     return g
+
+
+def _unasked(ctx, names):
+    """The gradients that autograd does not ask for; names: theirs, in the order
+    of apply's arguments (of which the last may not have been given)."""
+    asked = ctx.needs_input_grad
+    return [name for i, name in enumerate(names) if i >= len(asked) or not asked[i]]
 
 
 class HeadsScan(torch.autograd.Function):
@@ -418,10 +432,11 @@ class HeadsScan(torch.autograd.Function):
     def backward(ctx, dy, dh_last):
         x, delta, A, Bm, Cm, D, h0, delta_bias = ctx.saved_tensors
         dy = torch.zeros_like(x, memory_format=torch.contiguous_format) if dy is None else dy.contiguous()
+        names = ("dx", "ddelta", "dA", "dBm", "dCm", "dD", "dh0", "ddelta_bias")
         g = heads_scan_bwd(x, delta, A, Bm, Cm, dy, D=D, h0=h0, delta_bias=delta_bias,
-                           dh_last=None if dh_last is None else dh_last.contiguous(), **ctx.opts)
-        return (g["dx"], g.get("ddelta"), g["dA"], g["dBm"], g["dCm"], g.get("dD"), g.get("dh0"), g.get("ddelta_bias"),
-                None, None)
+                           dh_last=None if dh_last is None else dh_last.contiguous(), skip=_unasked(ctx, names),
+                           **ctx.opts)
+        return (*(g.get(name) for name in names), None, None)
 
 
 class AddNorm(torch.autograd.Function):
@@ -432,7 +447,7 @@ class AddNorm(torch.autograd.Function):
     def forward(ctx, x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5):
         out, res = add_norm_fwd(x, weight, residual=residual, gamma=gamma, scale=scale, eps=eps)
         ctx.save_for_backward(res, weight, gamma, x if gamma is not None else None)
-        ctx.scale, ctx.eps, ctx.has_residual, ctx.dt = scale, eps, residual is not None, x.dtype
+        ctx.scale, ctx.eps, ctx.dt = scale, eps, x.dtype
         ctx.set_materialize_grads(False)
         return out, res
 
@@ -441,9 +456,13 @@ class AddNorm(torch.autograd.Function):
     def backward(ctx, dout, dres):
         res, weight, gamma, x = ctx.saved_tensors
         dout = torch.zeros(res.shape, dtype=ctx.dt, device=res.device) if dout is None else dout.contiguous()
+        names = ("dx", "dweight", "dresidual", "dgamma")
+        skip = _unasked(ctx, names)
+        if len(set(skip) - {"dgamma"}) == 3:  # gamma's alone is asked for: one of the others comes with it
+            skip.remove("dweight")
         g = add_norm_bwd(dout, res, weight, dresidual_out=None if dres is None else dres.contiguous(), x=x, gamma=gamma,
-                         scale=ctx.scale, eps=ctx.eps)
-        return g["dx"], g["dweight"], g["dresidual"] if ctx.has_residual else None, g.get("dgamma"), None, None
+                         scale=ctx.scale, eps=ctx.eps, skip=skip)
+        return (*(g.get(name) for name in names), None, None)
 
 
 class GatedNorm(torch.autograd.Function):
@@ -460,5 +479,6 @@ class GatedNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         y, z, weight = ctx.saved_tensors
-        g = gated_norm_bwd(dout.contiguous(), y, z, weight, **ctx.opts)
-        return g["dy"], g.get("dz"), g["dweight"], None, None, None
+        names = ("dy", "dz", "dweight")
+        g = gated_norm_bwd(dout.contiguous(), y, z, weight, skip=_unasked(ctx, names), **ctx.opts)
+        return (*(g.get(name) for name in names), None, None, None)

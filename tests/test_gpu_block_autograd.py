@@ -43,3 +43,45 @@ def test_gradients_of_gradients_are_refused(torch_cuda):
         g, = torch.autograd.grad((out * out).sum(), inp, create_graph=True)
         with pytest.raises(RuntimeError, match="once_differentiable|twice"):
             (g * g).sum().backward()
+
+
+def test_gradients_that_nobody_asks_for_are_not_taken(torch_cuda):
+    """Without a residual, AddNorm's backward makes no residual's gradient (the
+    largest tensor of it); weights that are not trained get none."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    rows, dim = 4096, 2048
+    x = torch.randn(rows, dim, device="cuda").to(torch.bfloat16).requires_grad_()
+    w = torch.ones(dim, device="cuda")
+    out, _ = block.AddNorm.apply(x, w)
+    dout = torch.randn_like(out)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    dx, = torch.autograd.grad(out, x, dout)
+    # dx, and room for the column sums' parts that the query asks for
+    assert torch.cuda.max_memory_allocated() - before <= 2 * rows * dim + 2 * 1024 * dim * 4 + (1 << 20)
+    del dx
+    g = torch.Generator("cuda").manual_seed(72)
+    y, z, r = (torch.randn(50, 64, device="cuda", generator=g) for _ in range(3))
+    w, gm = (torch.randn(64, device="cuda", generator=g) for _ in range(2))
+    do = torch.randn(50, 64, device="cuda", generator=g)
+    for fn, args in ((block.AddNorm, (y, w, r, gm, 0.5)), (block.GatedNorm, (y, z, w, 2))):
+        names = [i for i, a in enumerate(args) if torch.is_tensor(a)]
+        full = [a.clone().requires_grad_() if i in names else a for i, a in enumerate(args)]
+        res = fn.apply(*full)
+        all_ = torch.autograd.grad(res if torch.is_tensor(res) else res[0], [full[i] for i in names], do)
+        for i, want in zip(names, all_):  # each alone, the same bits
+            one = [a.clone().requires_grad_() if j == i else a for j, a in enumerate(args)]
+            res = fn.apply(*one)
+            got, = torch.autograd.grad(res if torch.is_tensor(res) else res[0], one[i], do)
+            assert torch.equal(got, want), (fn, i)
+    d = heads_inputs(torch)
+    names = ("x", "delta", "A", "Bm", "Cm", "D", "h0", "bias")
+    dy = torch.randn_like(d["x"])
+    full = [d[k].clone().requires_grad_() for k in names]
+    all_ = torch.autograd.grad(block.HeadsScan.apply(*full, True, False)[0], full, dy)
+    for i, want in enumerate(all_):
+        one = [d[k].clone().requires_grad_() if j == i else d[k] for j, k in enumerate(names)]
+        got, = torch.autograd.grad(block.HeadsScan.apply(*one, True, False)[0], one[i], dy)
+        assert torch.equal(got, want), names[i]
