@@ -14,6 +14,7 @@ import math
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import s6
 from .s6 import _DT, _check
@@ -91,6 +92,14 @@ def _same_device(first, *others):
     for t in others:
         if t is not None and t.device != d:
             raise ValueError(f"tensors on {d} and {t.device}")
+
+
+def _written(*tensors):
+    """Tells autograd of tensors of the caller that a kernel writes: a backward
+    that saved one of them then refuses what is no longer its value."""
+    for t in tensors:
+        if t is not None:
+            increment_version(t)
 
 
 def _workspace(query, like, *args):
@@ -202,13 +211,14 @@ def heads_scan_fwd(x, delta, A, Bm, Cm, D=None, h0=None, return_last_state=False
     dims, dt, flags = _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, True)
     sshape = (dims.batch, dims.heads, dims.headdim, dims.dstate)
     _whole(h0, "h0", sshape)
-    if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
     _whole(y, "y", x.shape, x.dtype)
-    if return_last_state and h_last is None:
-        h_last = torch.empty(sshape, dtype=torch.float32, device=x.device)
     _whole(h_last, "h_last", sshape)
     _same_device(x, h0, y, h_last)
+    _written(y, h_last)
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if return_last_state and h_last is None:
+        h_last = torch.empty(sshape, dtype=torch.float32, device=x.device)
     lib = _load()
     ref = ctypes.byref(dims)
     keep, wsp, wsn = _workspace(lib.s6_heads_scan_fwd_workspace_size, x, ref, dt)
@@ -256,11 +266,11 @@ def heads_state_update(h, x, delta, A, Bm, Cm, D=None, delta_bias=None, delta_so
     dims, dt, flags = _heads_dims(x, delta, A, Bm, Cm, D, delta_bias, delta_softplus, unit_input, False)
     sshape = (*x.shape, Bm.shape[-1])
     _whole(_need(h, "h", sshape, torch.float32), "h", sshape)
+    _whole(y, "y", x.shape, x.dtype)
+    _same_device(x, h, y)
+    _written(h, y)
     if y is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    else:
-        _whole(y, "y", x.shape, x.dtype)
-    _same_device(x, h, y)
     _launch(_load().s6_heads_state_update, x, ctypes.byref(dims), dt, flags, _at(h), _at(x), _at(delta),
             _at(delta_bias), _at(A), _at(Bm), _at(Cm), _at(D), _at(y))
     return y
@@ -313,15 +323,14 @@ def add_norm_fwd(x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5, resi
     _whole(residual, "residual", x.shape, rt)
     _weight(weight, dim)
     _whole(gamma, "gamma", (dim,))
+    _whole(out, "out", x.shape, dt)
+    _whole(residual_out, "residual_out", x.shape, rt)
+    _same_device(x, weight, residual, gamma, out, residual_out)
+    _written(out, residual_out)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    else:
-        _whole(out, "out", x.shape, dt)
     if residual_out is None:
         residual_out = torch.empty_like(x, dtype=rt, memory_format=torch.contiguous_format)
-    else:
-        _whole(residual_out, "residual_out", x.shape, rt)
-    _same_device(x, weight, residual, gamma, out, residual_out)
     _launch(_load().s6_add_norm_fwd, x, math.prod(x.shape[:-1]), dim, _DT[dt], _DT[rt], _at(x), stride, _at(residual),
             _at(weight), _at(gamma), scale, eps, _at(out), _at(residual_out))
     return out, residual_out
@@ -378,11 +387,11 @@ def gated_norm_fwd(y, z, weight, groups=1, gate_after=False, eps=1e-5, out=None)
     gate_after.  y and z (None: no gate) may be slices of wider rows.  Returns
     a contiguous tensor in y's dtype."""
     dt, dim, ys, zs = _gated_args(y, z, weight, groups)
+    _whole(out, "out", y.shape, dt)
+    _same_device(y, out)
+    _written(out)
     if out is None:
         out = torch.empty_like(y, memory_format=torch.contiguous_format)
-    else:
-        _whole(out, "out", y.shape, dt)
-        _same_device(y, out)
     _launch(_load().s6_gated_norm_fwd, y, math.prod(y.shape[:-1]), dim, groups, _DT[dt],
             S6_GATE_AFTER if gate_after else 0, _at(y), ys, _at(z), zs, _at(weight), eps, _at(out))
     return out

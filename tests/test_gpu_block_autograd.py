@@ -85,3 +85,37 @@ def test_gradients_that_nobody_asks_for_are_not_taken(torch_cuda):
         one = [d[k].clone().requires_grad_() if j == i else d[k] for j, k in enumerate(names)]
         got, = torch.autograd.grad(block.HeadsScan.apply(*one, True, False)[0], one[i], dy)
         assert torch.equal(got, want), names[i]
+
+
+def test_tensors_written_in_place_are_marked(torch_cuda):
+    """A backward that saved a state, a residual or an output buffer refuses it
+    after a call has written there, as with torch's own in-place operations;
+    tensors of inference mode have nothing to mark and are taken as before."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    d = heads_inputs(torch)
+    w = torch.ones(64, device="cuda")
+
+    def saved(t, call):
+        p = torch.ones_like(t, requires_grad=True)
+        loss = (t * p).sum()  # keeps t for p's gradient
+        call(t)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+
+    one = [d[k][:, 0].contiguous() for k in ("x", "delta")] + [d["A"]] + [d[k][:, 0].contiguous() for k in ("Bm", "Cm")]
+    seq = [d[k] for k in ("x", "delta", "A", "Bm", "Cm")]
+    rows = torch.randn(5, 64, device="cuda")
+    saved(d["h0"].clone(), lambda t: block.heads_state_update(t, *one))
+    saved(torch.zeros_like(one[0]), lambda t: block.heads_state_update(d["h0"].clone(), *one, y=t))
+    saved(torch.zeros_like(d["x"]), lambda t: block.heads_scan_fwd(*seq, y=t))
+    saved(torch.zeros_like(d["h0"]), lambda t: block.heads_scan_fwd(*seq, h_last=t))
+    saved(rows.clone(), lambda t: block.add_norm_fwd(rows, w, residual=t, residual_out=t))
+    saved(rows.clone(), lambda t: block.add_norm_fwd(rows, w, out=t))
+    saved(rows.clone(), lambda t: block.gated_norm_fwd(rows, rows, w, out=t))
+    with torch.inference_mode():
+        h = d["h0"].clone()
+    want = d["h0"].clone()
+    block.heads_state_update(h, *one)
+    block.heads_state_update(want, *one)
+    assert torch.equal(h, want)
