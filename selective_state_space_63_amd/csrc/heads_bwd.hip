@@ -681,7 +681,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   }
 }
 
-// dB, dC: the head runs' parts added in order, four states per thread.
+// dB, dC: the head runs' parts added in order (0 of none), four states per thread.
 template <typename In>
 __global__ __launch_bounds__(256) void s6_heads_sum_bc(const float* bc, In* dB, In* dC, int64_t rows, int NT, int N,
                                                        int nhb) {
@@ -785,12 +785,19 @@ int launch_bwd_in(const HeadsBwdArgs& a, const HeadsPlan& p, bool vec, hipStream
 }
 
 template <typename In>
+int launch_sum_bc(const float* bc, void* dB, void* dC, int64_t rows, int NT, int N, int nhb, hipStream_t st) {
+  const int64_t n = rows * (NT / 4);
+  hipLaunchKernelGGL((s6_heads_sum_bc<In>), dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, st, bc,
+                     static_cast<In*>(dB), static_cast<In*>(dC), rows, NT, N, nhb);
+  S6_HIP(hipGetLastError(), "s6_heads_sum_bc launch");
+  return S6_OK;
+}
+
+template <typename In>
 int launch_sums(const HeadsBwdArgs& a, const HeadsPlan& p, float* dA, float* dD, float* dbias, hipStream_t st) {
   if (a.bc) {
-    const int64_t rows = a.h.batch * a.h.L * a.groups, n = rows * (p.NT / 4);
-    hipLaunchKernelGGL((s6_heads_sum_bc<In>), dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, st, a.bc,
-                       static_cast<In*>(a.dB), static_cast<In*>(a.dC), rows, p.NT, a.h.dstate, a.nhb);
-    S6_HIP(hipGetLastError(), "s6_heads_sum_bc launch");
+    const int rc = launch_sum_bc<In>(a.bc, a.dB, a.dC, a.h.batch * a.h.L * a.groups, p.NT, a.h.dstate, a.nhb, st);
+    if (rc) return rc;
   }
   hipLaunchKernelGGL(s6_heads_sum_parts, dim3((unsigned)a.h.heads, 3), dim3(256), 0, st, a.parts, dA, dD, dbias,
                      a.h.batch * a.nblk * (kBQ<In> / 64), a.h.heads);
@@ -840,6 +847,12 @@ int s6_heads_scan_bwd(const s6_heads_dims* d, int in_dtype, int flags, const voi
     fill(dD, 0.0f, d->heads, st);
     fill(ddelta_bias, 0.0f, d->heads, st);
     S6_HIP(hipGetLastError(), "fill launch");
+    if (len > 0 && dBm && dCm) {  // no heads
+      const int n = (int)d->dstate, wide = (n + 3) / 4 * 4;
+      rc = in_dtype == S6_BF16 ? launch_sum_bc<uint16_t>(nullptr, dBm, dCm, len * d->groups, wide, n, 0, st)
+                               : launch_sum_bc<float>(nullptr, dBm, dCm, len * d->groups, wide, n, 0, st);
+      if (rc) return rc;
+    }
     return dh0 ? launch_copy_state(dh_last, dh0, d->batch * d->heads * d->headdim * d->dstate, st) : S6_OK;
   }
   const HeadsPlan p = heads_plan(*d, in_dtype, x, Bm, Cm, dy);
