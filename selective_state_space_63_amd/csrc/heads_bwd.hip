@@ -69,8 +69,9 @@ struct HeadsBwdArgs {
   float* parts;           // (3, batch * nblk * Q / 64, heads): dA, dD, dbias per 64 tokens
   float* bc;              // (nhb, 2, batch * L, groups, NT) partial dB, dC, or null (one head run)
   int64_t nblk, rows;
+  uint32_t id0;           // first workgroup of this launch
   int groups, nhb, hpb;   // head runs of a group and heads per run
-  int want_d, want_bias;
+  int want_d;
 };
 
 // Offsets in LDS (bytes).
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   float* const tb_in = tb_u + NTT;                            // (j, T): w E, rows of tile T, columns before tile j
 
   const HeadsArgs& a = ba.h;
-  uint32_t id = blockIdx.x;  // (sequence, group, head run, block), the block fastest; below 2^31
+  uint32_t id = ba.id0 + blockIdx.x;  // (sequence, group, head run, block), the block fastest; below 2^31
   const uint32_t nb = (uint32_t)ba.nblk;
   const int64_t blk = __builtin_amdgcn_readfirstlane(id % nb);
   id /= nb;
@@ -681,27 +682,28 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   }
 }
 
-// dB, dC: the head runs' parts added in order (0 of none), four states per thread.
+// dB, dC: the head runs' parts added in order (0 of none), four states per thread
+// and turn.
 template <typename In>
 __global__ __launch_bounds__(256) void s6_heads_sum_bc(const float* bc, In* dB, In* dC, int64_t rows, int NT, int N,
                                                        int nhb) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int per = NT / 4;
-  const int64_t row = i / per;
-  const int n = (int)(i % per) * 4;
-  if (row >= rows || n >= N) return;
-  const int m = blockIdx.y;
-  float s[4] = {0, 0, 0, 0};
-  for (int h = 0; h < nhb; ++h) {
-    float v[4];
-    load_vec<float, 4>(bc + ((int64_t)(h * 2 + m) * rows + row) * NT + n, v);
+  const int per = NT / 4, m = blockIdx.y;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per;
+    const int n = (int)(i - row * per) * 4;
+    if (n >= N) continue;
+    float s[4] = {0, 0, 0, 0};
+    for (int h = 0; h < nhb; ++h) {
+      float v[4];
+      load_vec<float, 4>(bc + ((int64_t)(h * 2 + m) * rows + row) * NT + n, v);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s[r] += v[r];
+      for (int r = 0; r < 4; ++r) s[r] += v[r];
+    }
+    In* o = (m ? dC : dB) + row * N + n;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n + r < N) o[r] = from_f32<In>(s[r]);
   }
-  In* o = (m ? dC : dB) + row * N + n;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (n + r < N) o[r] = from_f32<In>(s[r]);
 }
 
 // dA, dD, dbias: the blocks' parts of one head added in a fixed order.
@@ -762,15 +764,18 @@ BwdWs bwd_ws(const s6_heads_dims& d, const HeadsPlan& p, int in_dtype) {
 }
 
 template <typename In, int NT, bool VEC>
-int launch_bwd_v(const HeadsBwdArgs& a, hipStream_t st) {
+int launch_bwd_v(HeadsBwdArgs a, hipStream_t st) {
   const auto kern = s6_heads_bwd_kernel<In, NT, VEC>;
   constexpr int lds = BwdLds<In, NT>::total;
   if constexpr (lds > 65536)
     S6_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds),
            "s6_heads_bwd_kernel LDS size");
   const int64_t n = a.nblk * a.nhb * a.groups * a.h.batch;
-  hipLaunchKernelGGL(kern, dim3((unsigned)n), dim3(512), lds, st, a);
-  S6_HIP(hipGetLastError(), "s6_heads_bwd_kernel launch");
+  for (int64_t at = 0; at < n; at += kMaxBlocks) {
+    a.id0 = (uint32_t)at;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(n - at < kMaxBlocks ? n - at : kMaxBlocks)), dim3(512), lds, st, a);
+    S6_HIP(hipGetLastError(), "s6_heads_bwd_kernel launch");
+  }
   return S6_OK;
 }
 template <typename In, int NT>
@@ -786,8 +791,8 @@ int launch_bwd_in(const HeadsBwdArgs& a, const HeadsPlan& p, bool vec, hipStream
 
 template <typename In>
 int launch_sum_bc(const float* bc, void* dB, void* dC, int64_t rows, int NT, int N, int nhb, hipStream_t st) {
-  const int64_t n = rows * (NT / 4);
-  hipLaunchKernelGGL((s6_heads_sum_bc<In>), dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, st, bc,
+  const int64_t n = (rows * (NT / 4) + 255) / 256;
+  hipLaunchKernelGGL((s6_heads_sum_bc<In>), dim3((unsigned)(n < kMaxBlocks ? n : kMaxBlocks), 2), dim3(256), 0, st, bc,
                      static_cast<In*>(dB), static_cast<In*>(dC), rows, NT, N, nhb);
   S6_HIP(hipGetLastError(), "s6_heads_sum_bc launch");
   return S6_OK;
@@ -882,7 +887,7 @@ int s6_heads_scan_bwd(const s6_heads_dims* d, int in_dtype, int flags, const voi
   ba.parts = reinterpret_cast<float*>(w + ws.parts);
   ba.bc = ws.nhb > 1 ? reinterpret_cast<float*>(w + ws.bc) : nullptr;
   ba.nblk = ws.nblk; ba.rows = p.rows; ba.groups = (int)d->groups; ba.nhb = ws.nhb; ba.hpb = ws.hpb;
-  ba.want_d = dD != nullptr; ba.want_bias = ddelta_bias != nullptr;
+  ba.want_d = dD != nullptr;
   // dx, dB and dC are stored four values at a time
   const bool vec = p.vec && aligned(dx, 4 * esz) && aligned(dBm, 4 * esz) && aligned(dCm, 4 * esz);
   rc = in_dtype == S6_BF16 ? launch_bwd_in<uint16_t>(ba, p, vec, st) : launch_bwd_in<float>(ba, p, vec, st);

@@ -88,9 +88,9 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   int* bad = reinterpret_cast<int*>(lds + L::bad);         // first token whose input is not finite
   // consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of
   // rows, whose B and C come through one L2
-  const int64_t nrows = gridDim.x;
-  const int64_t rid = nrows % 8 == 0 ? (blockIdx.x % 8) * (nrows / 8) + blockIdx.x / 8 : blockIdx.x;
-  const HeadRow hr = head_row(a, rid);
+  const uint32_t here = gridDim.x;
+  const uint32_t rid = here % 8 == 0 ? (blockIdx.x % 8) * (here / 8) + blockIdx.x / 8 : blockIdx.x;
+  const HeadRow hr = head_row(a, a.row0 + rid);
   const int64_t seg = blockIdx.y;
   const int lane = threadIdx.x & 63, wv = wave_index(), g = lane >> 4, c = lane & 15;
   const int p0 = hr.pt * kTP, pleft = a.headdim - p0;
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
     const int n = 16 * q + 4 * g;
     if (a.hin) {
       float v[4];
-      load_vec<float, 4>(a.hin + (seg * nrows + hr.row) * (int64_t)(kTP * NT) + ps * NT + n, v);
+      load_vec<float, 4>(a.hin + (seg * a.rows + hr.row) * (int64_t)(kTP * NT) + ps * NT + n, v);
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[q][r] = v[r];
     } else if (a.h0 && ps < pleft) {
@@ -344,14 +344,17 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
 }
 
 template <typename In, int NT, bool VEC>
-int launch_scan_v(const HeadsArgs& a, const HeadsPlan& p, hipStream_t st) {
+int launch_scan_v(HeadsArgs a, const HeadsPlan& p, hipStream_t st) {
   const auto kern = s6_heads_scan_kernel<In, NT, VEC>;
   constexpr int lds = ScanLds<In, NT>::total;
   if constexpr (lds > 65536)
     S6_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds),
            "s6_heads_scan_kernel LDS size");
-  hipLaunchKernelGGL(kern, dim3((unsigned)p.rows, (unsigned)a.nseg), dim3(256), lds, st, a);
-  S6_HIP(hipGetLastError(), "s6_heads_scan_kernel launch");
+  for (a.row0 = 0; a.row0 < p.rows; a.row0 += kMaxBlocks) {
+    const int64_t n = p.rows - a.row0 < kMaxBlocks ? p.rows - a.row0 : kMaxBlocks;
+    hipLaunchKernelGGL(kern, dim3((unsigned)n, (unsigned)a.nseg), dim3(256), lds, st, a);
+    S6_HIP(hipGetLastError(), "s6_heads_scan_kernel launch");
+  }
   return S6_OK;
 }
 template <typename In, int NT>
@@ -415,7 +418,7 @@ HeadsArgs heads_args(const s6_heads_dims& d, const HeadsPlan& p, int flags, cons
   a.unit = (flags & S6_UNIT_INPUT) != 0;
   a.heads = (int)d.heads; a.headdim = (int)d.headdim; a.ptiles = (int)p.ptiles; a.hpg = (int)(d.heads / d.groups);
   a.dstate = (int)d.dstate;
-  a.batch = d.batch; a.L = d.seqlen;
+  a.batch = d.batch; a.L = d.seqlen; a.rows = p.rows;
   a.x_batch = d.x_batch; a.x_token = d.x_token; a.d_batch = d.delta_batch; a.d_token = d.delta_token;
   a.b_batch = d.b_batch; a.b_token = d.b_token; a.c_batch = d.c_batch; a.c_token = d.c_token;
   return a;

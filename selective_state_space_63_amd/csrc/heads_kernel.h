@@ -563,6 +563,7 @@ struct HeadsArgs {
   int softplus, unit;
   int heads, headdim, ptiles, hpg, dstate;  // ptiles: 64-channel tiles of a head; hpg: heads per group
   int64_t batch, L;
+  int64_t rows, row0;     // rows of the call, first row of this launch
   int64_t x_batch, x_token, d_batch, d_token, b_batch, b_token, c_batch, c_token;
   int64_t nseg, seg_len;  // segments along L (a multiple of the stored blocks)
   float* agg;             // segment states from zero (dir, seg, row, 64, NT)
@@ -621,6 +622,10 @@ HeadsPlan heads_plan(const s6_heads_dims& d, int in_dtype, const void* x, const 
 HeadsArgs heads_args(const s6_heads_dims& d, const HeadsPlan& p, int flags, const void* x, const void* delta,
                      const float* dbias, const float* A, const void* Bm, const void* Cm, const float* D,
                      const float* h0);
+
+// Launches of at most this many workgroups: a launch counts its work items in 32
+// bits, and one of more wraps without an error.
+constexpr int64_t kMaxBlocks = int64_t(1) << 22;
 
 // Segments along L for `rows` rows, each a multiple of `unit` tokens.
 void heads_segments(int64_t rows, int64_t L, int64_t unit, int64_t* nseg, int64_t* seg_len);

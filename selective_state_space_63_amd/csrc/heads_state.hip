@@ -40,8 +40,8 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
   const BT bs{bmem};
   __shared__ __align__(16) float wt[kHQ];
   __shared__ float total_s;
-  const HeadRow hr = head_row(a, blockIdx.x);
-  const int64_t nrows = gridDim.x;
+  const HeadRow hr = head_row(a, a.row0 + blockIdx.x);
+  const int64_t nrows = a.rows;
   const int dir = blockIdx.z;
   const int64_t seg = mode == 0 && dir ? blockIdx.y + 1 : blockIdx.y;
   const int lane = threadIdx.x & 63, wv = wave_index(), g = lane >> 4, c = lane & 15;
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
 // thread; the aggregates do not depend on the chain, so eight of them are
 // loaded before each batch of it.
 template <int NT>
-__global__ __launch_bounds__(256) void s6_heads_fold_kernel(HeadsArgs a, int64_t nrows) {
+__global__ __launch_bounds__(256) void s6_heads_fold_kernel(HeadsArgs a, int64_t nrows) {  // (few rows: one launch)
   const int64_t row = blockIdx.x;
   const int dir = blockIdx.z;
   const int e = (blockIdx.y * 256 + threadIdx.x) * 4;  // in the row's 64 x NT tile
@@ -243,13 +243,16 @@ __global__ __launch_bounds__(256) void s6_heads_fold_kernel(HeadsArgs a, int64_t
 }
 
 template <typename In, int NT>
-int launch_state_t(const HeadsArgs& a, const HeadsPlan& p, int mode, int dirs, hipStream_t st) {
-  const dim3 grid((unsigned)p.rows, (unsigned)(mode == 0 ? a.nseg - 1 : a.nseg), (unsigned)dirs);
-  if (p.vec)
-    hipLaunchKernelGGL((s6_heads_state_kernel<In, NT, true>), grid, dim3(256), 0, st, a, mode);
-  else
-    hipLaunchKernelGGL((s6_heads_state_kernel<In, NT, false>), grid, dim3(256), 0, st, a, mode);
-  S6_HIP(hipGetLastError(), "s6_heads_state_kernel launch");
+int launch_state_t(HeadsArgs a, const HeadsPlan& p, int mode, int dirs, hipStream_t st) {
+  for (a.row0 = 0; a.row0 < p.rows; a.row0 += kMaxBlocks) {
+    const int64_t n = p.rows - a.row0 < kMaxBlocks ? p.rows - a.row0 : kMaxBlocks;
+    const dim3 grid((unsigned)n, (unsigned)(mode == 0 ? a.nseg - 1 : a.nseg), (unsigned)dirs);
+    if (p.vec)
+      hipLaunchKernelGGL((s6_heads_state_kernel<In, NT, true>), grid, dim3(256), 0, st, a, mode);
+    else
+      hipLaunchKernelGGL((s6_heads_state_kernel<In, NT, false>), grid, dim3(256), 0, st, a, mode);
+    S6_HIP(hipGetLastError(), "s6_heads_state_kernel launch");
+  }
   return S6_OK;
 }
 

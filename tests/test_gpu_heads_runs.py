@@ -60,3 +60,37 @@ def test_no_heads(torch_cuda, dtype):
     for k in ("dBm", "dCm"):
         assert torch.equal(got[k], torch.zeros_like(B)), k
     assert got["dx"].shape == x.shape and got["dA"].shape == (0,)
+
+
+def test_more_rows_than_a_launch_counts(torch_cuda):
+    """2^24 rows and a few more, 256 work items each: past the 32 bits in which a
+    launch counts them."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    b, H = (1 << 18) + 1, 64
+    g = torch.Generator("cuda").manual_seed(43)
+    x = torch.randn(b, 1, H, 1, device="cuda", generator=g).to(torch.bfloat16)
+    B, C = (torch.randn(b, 1, 1, 1, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    y = torch.full_like(x, float("nan"))
+    block.heads_scan_fwd(x, None, -torch.ones(H, device="cuda"), B, C, y=y)
+    want = x.double() * (B.double() * C.double())
+    assert bool(((y.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -15) * want.abs()).all())
+
+
+def test_more_blocks_than_a_launch_counts(torch_cuda):
+    """The same for the gradients: 2^23 sequences and a few more, of one token,
+    512 work items each (their states take 137 GB)."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("less than 160 GiB of free device memory")
+    b = (1 << 23) + 3
+    g = torch.Generator("cuda").manual_seed(44)
+    x, B, C, dy = (torch.randn(b, 1, 1, 1, device="cuda", generator=g).to(torch.bfloat16) for _ in range(4))
+    got = block.heads_scan_bwd(x, None, -torch.ones(1, device="cuda"), B, C, dy)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    x, B, C, dy = (t.double() for t in (x, B, C, dy))
+    for k, want in (("dx", dy * C * B), ("dBm", dy * C * x), ("dCm", dy * x * B)):
+        assert bool(((got[k].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -15) * want.abs()).all()), k
