@@ -417,11 +417,14 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
             P[k][r] += on ? X[r] * (l[r] * wj) : 0.0f;
             if (I == J && 4 * g + r == c) diag = X[r];
           }
-          store_vec<In, 4>(mf + frag_at<H>(J, I >> 1) * 512 + lane * 8 + 4 * (I & 1), m);
+          In* const at = mf + frag_at<H>(J, I >> 1) * 512 + lane * 8 + 4 * (I & 1);
           if constexpr (sizeof(In) == 2) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) m[r] -= (float)(__bf16)m[r];
+            Four<In> hi;
+            hi.split(m);
+            hi.put(at);
             m_lo[k].set(m);
+          } else {
+            store_vec<In, 4>(at, m);
           }
           if (I == J) corner(er, g, c);  // a row's own part of G, in the place of its sum
 #pragma unroll

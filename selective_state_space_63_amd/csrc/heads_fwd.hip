@@ -242,12 +242,13 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
             if (c == 4 * g + r) dg[16 * I + c] = G[r] * wj[r];
         }
         In* at = pf + gram_at(I, J >> 1) + (I == J && !(I & 1) ? 4 * lane : 8 * lane + 4 * (J & 1));
-        store_vec<In, 4>(at, p);
         if constexpr (sizeof(In) == 2) {
-          float lo[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) lo[r] = p[r] - (float)(__bf16)p[r];
-          store_vec<In, 4>(at + kGram, lo);
+          Four<In> hi;
+          hi.split(p);
+          hi.put(at);
+          store_vec<In, 4>(at + kGram, p);
+        } else {
+          store_vec<In, 4>(at, p);
         }
       }
     }

@@ -76,13 +76,27 @@ template <typename In>
 struct Pair {
   Frag<In> hi, lo;
 };
+// The rests of two floats after their packed bf16 parts; the parts as an
+// operand.  (Two values at a time: the compiler converts a value that is also
+// read back as a float by itself, and once more to pack it.)
+__device__ __forceinline__ uint32_t split2(float& a, float& b) {
+  uint32_t p = bf_pack(a, b);
+  asm("" : "+v"(p));
+  a -= bf_low(p);
+  b -= bf_high(p);
+  return p;
+}
+typedef unsigned int gu32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void to_pair(const float (&f)[8], Pair<uint16_t>& o) {
+  gu32x4 hi, lo;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const __bf16 h = (__bf16)f[j];
-    o.hi.v[j] = h;
-    o.lo.v[j] = (__bf16)(f[j] - (float)h);
+  for (int j = 0; j < 4; ++j) {
+    float a = f[2 * j], b = f[2 * j + 1];
+    hi[j] = split2(a, b);
+    lo[j] = bf_pack(a, b);
   }
+  o.hi.v = __builtin_bit_cast(bf16x8, hi);
+  o.lo.v = __builtin_bit_cast(bf16x8, lo);
 }
 __device__ __forceinline__ void to_pair(const float (&f)[8], Pair<float>& o) { to_frag(f, o.hi); }
 
@@ -106,16 +120,16 @@ struct Whole {
   Frag<In> part[kParts];
 };
 __device__ __forceinline__ void to_whole(const float (&f)[8], Whole<uint16_t>& o) {
+  gu32x4 w[3];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float rest = f[j];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const __bf16 h = (__bf16)rest;
-      o.part[i].v[j] = h;
-      rest -= (float)h;
-    }
+  for (int j = 0; j < 4; ++j) {
+    float a = f[2 * j], b = f[2 * j + 1];
+    w[0][j] = split2(a, b);
+    w[1][j] = split2(a, b);
+    w[2][j] = bf_pack(a, b);
   }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) o.part[i].v = __builtin_bit_cast(bf16x8, w[i]);
 }
 __device__ __forceinline__ void to_whole(const float (&f)[8], Whole<float>& o) { to_frag(f, o.part[0]); }
 
@@ -258,7 +272,6 @@ __device__ __forceinline__ gbytes scalar_base(const void* p) {
   return reinterpret_cast<gbytes>(v);
 }
 typedef unsigned int gu32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned int gu32x4 __attribute__((ext_vector_type(4)));
 typedef float gf32x4 __attribute__((ext_vector_type(4)));
 
 // A part of a tensor as a buffer of `bytes` from p on: loads past its end
@@ -292,6 +305,8 @@ template <>
 struct Four<uint16_t> {
   uint32_t w[2];
   __device__ __forceinline__ void set(const float (&f)[4]) { w[0] = bf_pack(f[0], f[1]); w[1] = bf_pack(f[2], f[3]); }
+  // as set, and f becomes what is left
+  __device__ __forceinline__ void split(float (&f)[4]) { w[0] = split2(f[0], f[1]); w[1] = split2(f[2], f[3]); }
   __device__ __forceinline__ uint16_t get(int r) const { return (uint16_t)(w[r >> 1] >> (16 * (r & 1))); }
   __device__ __forceinline__ void put(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]); }
   __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
@@ -306,6 +321,7 @@ struct Four<float> {
     for (int r = 0; r < 4; ++r) w[r] = f[r];
   }
   __device__ __forceinline__ float get(int r) const { return w[r]; }
+  __device__ __forceinline__ void put(float* p) const { store_vec<float, 4>(p, w); }
   __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(gu32x4, gf32x4{w[0], w[1], w[2], w[3]}), r, off, 0, 0);
   }
