@@ -338,7 +338,6 @@ struct Piece<uint16_t> {
     auto part = [&](uint32_t w, int i) { return w & (n >= 2 * i + 2 ? ~0u : n == 2 * i + 1 ? 0xffffu : 0u); };
     v = make_uint4(part(v.x, 0), part(v.y, 1), part(v.z, 2), part(v.w, 3));
   }
-  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void load_at(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
     v = make_uint4(w[0], w[1], w[2], w[3]);
@@ -375,10 +374,6 @@ struct Piece<float> {
   __device__ __forceinline__ void keep(int n) {
     a = make_float4(n > 0 ? a.x : 0.0f, n > 1 ? a.y : 0.0f, n > 2 ? a.z : 0.0f, n > 3 ? a.w : 0.0f);
     b = make_float4(n > 4 ? b.x : 0.0f, n > 5 ? b.y : 0.0f, n > 6 ? b.z : 0.0f, n > 7 ? b.w : 0.0f);
-  }
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
   }
   __device__ __forceinline__ void load_at(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     const gf32x4 x = __builtin_bit_cast(gf32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
