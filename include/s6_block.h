@@ -40,9 +40,10 @@
  * Arithmetic: sums, states, decays and steps in fp32.  fp32 inputs: fp32
  * products.  bf16 inputs: bf16 matrix products with fp32 accumulation; the
  * products of inputs are exact; an fp32 factor enters in full in the states
- * (three bf16 parts) and as two bf16 parts (within 2^-17) elsewhere.  So y, dx,
- * dBm, dCm and ddelta meet one rounding to bf16, that of the result.  A
- * decay e^{c_t - c_s} between two tokens of a chunk is taken from running sums
+ * (three bf16 parts) and in the gradients of steps and parameters, and as two bf16
+ * parts (within 2^-17) in y, dx, dBm and dCm.  So all of these and ddelta meet one
+ * rounding to bf16, that of the result.
+ * A decay e^{c_t - c_s} between two tokens of a chunk is taken from running sums
  * held in two floats each: its relative error is about 2^-24 times its own
  * exponent, whatever decays lie before it (sequences packed closely one after
  * another lose nothing).  Repeated calls give identical bits.

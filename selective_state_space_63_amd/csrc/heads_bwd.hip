@@ -25,8 +25,7 @@
 // 4e-3 of its terms, and a reset's step added rounding noise times itself.)
 //
 // Two phases.  s6_heads_state_kernel walks the sequence in both directions
-// and stores S and L entering every block (bf16 inputs: as two bf16 planes in
-// operand order).  Then a workgroup of eight waves owns one block of one
+// and stores S and L entering every block (fp32, in operand order).  Then a workgroup of eight waves owns one block of one
 // sequence and a run of a group's heads: B, C, their Gram matrix and the
 // sums over heads -- dB, dC and P -- stay on chip while it goes through the
 // heads, so x, dy and the states are read once and dx is written once.  The
@@ -40,9 +39,12 @@
 // next head's decays, waves 4 and 5 finish the last head's step gradients
 // behind the next turn's barrier, so neither is waited for.
 //
-// Roundings (bf16 inputs): the decayed Gram matrix, P, S and L enter products as
-// two bf16 parts (within 2^-17), so that dx, dB and dC meet one rounding, their
-// own; the step's and the decay's gradients come from fp32 products.
+// Roundings (bf16 inputs): the decayed Gram matrix, P and, for dx, L enter products
+// as two bf16 parts (within 2^-17), so that dx, dB and dC meet one rounding, their
+// own.  The step's and the decay's gradients come from fp32 products and from S and
+// L in full (three bf16 parts): two left 2e-6 to 3e-6 in dA, where fp32 sums leave
+// 3e-7, and take the block kernel 494 us instead of 524 (8 x 2048 tokens of 80
+// heads of 64, N 128).
 //
 // What bounds it: one workgroup of eight waves fits a CU (242 VGPRs, 157 KB of
 // LDS), so a turn is the sum of its phases' latencies: 11 us at 128 tokens x 64
@@ -278,17 +280,17 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
   // one word of each of their cache lines a turn ahead, so that they come from
   // L2 when the operands are loaded: held in registers from there on, they
   // would not leave room for the sums.
-  constexpr int64_t kTile = (int64_t)kTP * NT * (sizeof(In) == 2 ? 2 : 1);
+  constexpr int64_t kTile = (int64_t)kTP * NT;
   auto state_at = [&](int hd, int pt) {
     const int64_t row = (b * a.heads + hd) * (int64_t)a.ptiles + pt;
-    return static_cast<const In*>(a.planes) + (blk * ba.rows + row) * kTile;
+    return a.planes + (blk * ba.rows + row) * kTile;
   };
   uint32_t touched = 0;
   auto touch = [&](int hd, int pt) {
-    constexpr int kLines = (int)(kTile * sizeof(In) / 128);
+    constexpr int kLines = (int)(kTile * sizeof(float) / 128);
     static_assert(kLines <= 256, "one line of S and L per thread");
     if (hd < hd1 && (threadIdx.x & 255) < kLines) {
-      const In* sp = state_at(hd, pt) + (threadIdx.x >> 8) * (ba.nblk * ba.rows * kTile);
+      const float* sp = state_at(hd, pt) + (threadIdx.x >> 8) * (ba.nblk * ba.rows * kTile);
       touched = reinterpret_cast<const uint32_t*>(sp)[(threadIdx.x & 255) * 32];
     }
   };
@@ -376,24 +378,20 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
         for (int r = 0; r < 4; ++r) l[r] = decay_between(ct[r], lt[r], cj, lj);
       };
       // inside the block
-      Pair<In> Sf[2], Lf[2];
+      Frag<float> Sf[2], Lf[2];
       Four<In> m_lo[SLOTS];  // second parts of the decayed Gram tiles
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k) {
         if (k == SLOTS - 1) {
           // states entering the block: this wave's strip of n, all 64 channels
           // (touched a turn ago: they come from L2)
-          const In* sp = state_at(hd, pt) + ns * 1024;
-          const In* lp = sp + ba.nblk * ba.rows * kTile;
-          const uint32_t off = (uint32_t)lane * 8 * (uint32_t)sizeof(In);
+          const float* sp = state_at(hd, pt) + ns * 1024;
+          const float* lp = sp + ba.nblk * ba.rows * kTile;
+          const uint32_t off = (uint32_t)lane * 16;
 #pragma unroll
           for (int pp = 0; pp < 2; ++pp) {
-            load_frag(scalar_base(sp + pp * 512) + off, Sf[pp].hi);
-            load_frag(scalar_base(lp + pp * 512) + off, Lf[pp].hi);
-            if constexpr (sizeof(In) == 2) {
-              load_frag(scalar_base(sp + kTP * NT + pp * 512) + off, Sf[pp].lo);
-              load_frag(scalar_base(lp + kTP * NT + pp * 512) + off, Lf[pp].lo);
-            }
+            load_halves(scalar_base(sp + pp * 512) + off, Sf[pp]);
+            load_halves(scalar_base(lp + pp * 512) + off, Lf[pp]);
           }
         }
         const int n = 8 * k + wv;
@@ -437,61 +435,77 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      // from before and to after the block
+      if (tp == 0) {
+        float s = 0.0f;
+#pragma unroll
+        for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s = __builtin_fmaf(Sf[pp].v[e], Lf[pp].v[e], s);
+        th[ns] = wave_sum(s);
+      }
+      // from before the block
+      {
+        Whole<In> sw[2];
+#pragma unroll
+        for (int pp = 0; pp < 2; ++pp) to_whole(Sf[pp].v, sw[pp]);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+          const int t = 16 * (tp * TT + i) + c;
+          if (t - c >= rows) continue;
+          f32x4 U = {0, 0, 0, 0};
+#pragma unroll
+          for (int pp = 0; pp < 2; ++pp) U = mma_whole(sw[pp], ys.row(x_row, t - c, pp), U);
+          float cv[4], sy = 0.0f;
+          cm.four(t, 4 * ns + g, cv);
+          const float e = ec[t];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sy = __builtin_fmaf(cv[r], U[r], sy);
+            dC[i][r] = __builtin_fmaf(e, U[r], dC[i][r]);
+          }
+          yp[t * NS + ns] = e * half_sum(pair_row_sum(sy));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      // to after the block
+      Whole<In> lw[2];
+#pragma unroll
+      for (int pp = 0; pp < 2; ++pp) to_whole(Lf[pp].v, lw[pp]);
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
         const int t = 16 * (tp * TT + i) + c;
         if (t - c >= rows) continue;
-        f32x4 U = {0, 0, 0, 0}, V = {0, 0, 0, 0};
+        f32x4 V = {0, 0, 0, 0};
 #pragma unroll
-        for (int pp = 0; pp < 2; ++pp) {
-          U = mma_pair(Sf[pp], ys.row(x_row, t - c, pp), U);
-          V = mma_pair(Lf[pp], xs.row(x_row, t - c, pp), V);
-        }
-        float cv[4], bv[4], sy = 0.0f, su = 0.0f;
-        cm.four(t, 4 * ns + g, cv);
+        for (int pp = 0; pp < 2; ++pp) V = mma_whole(lw[pp], xs.row(x_row, t - c, pp), V);
+        float bv[4], su = 0.0f;
         bs.four(t, 4 * ns + g, bv);
-        const float e = ec[t], f = wd[t], fw = ww[t] * f;
+        const float f = wd[t], fw = ww[t] * f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          sy = __builtin_fmaf(cv[r], U[r], sy);
           su = __builtin_fmaf(bv[r], V[r], su);
-          dC[i][r] = __builtin_fmaf(e, U[r], dC[i][r]);
           dB[i][r] = __builtin_fmaf(fw, V[r], dB[i][r]);
         }
-        yp[t * NS + ns] = e * half_sum(pair_row_sum(sy));
         up[t * NS + ns] = f * half_sum(pair_row_sum(su));
         __builtin_amdgcn_sched_barrier(0);
       }
 
       // a part of L by states, this wave's strip
-      auto put_l = [&](const typename O::LT& to, bool second) {
+      auto put_l = [&](const typename O::LT& to, int part) {
         if (tp != 0) return;
 #pragma unroll
         for (int pp = 0; pp < 2; ++pp) {
           float f[4], h[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            f[e] = frag_f32(second ? Lf[pp].lo : Lf[pp].hi, e);
-            h[e] = frag_f32(second ? Lf[pp].lo : Lf[pp].hi, 4 + e);
+            f[e] = frag_f32(lw[pp].part[part], e);
+            h[e] = frag_f32(lw[pp].part[part], 4 + e);
           }
           store_vec<In, 4>(to.t + to.at(16 * ns + c, 8 * pp + g), f);
           store_vec<In, 4>(to.t + to.at(16 * ns + c, 8 * pp + 4 + g), h);
         }
       };
-      put_l(lm, false);
-      if (tp == 0) {
-        float s = 0.0f;
-#pragma unroll
-        for (int pp = 0; pp < 2; ++pp)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float sf = frag_f32(Sf[pp].hi, e), lf = frag_f32(Lf[pp].hi, e);
-            if constexpr (sizeof(In) == 2) { sf += frag_f32(Sf[pp].lo, e); lf += frag_f32(Lf[pp].lo, e); }
-            s = __builtin_fmaf(sf, lf, s);
-          }
-        th[ns] = wave_sum(s);
-      }
+      put_l(lm, 0);
       __syncthreads();
       issue(after(hd, pt), last_pt ? 0 : pt + 1);
 
@@ -514,7 +528,7 @@ __global__ __launch_bounds__(512) void s6_heads_bwd_kernel(HeadsBwdArgs ba) {
             __builtin_amdgcn_sched_barrier(0);
           }
         };
-        if constexpr (sizeof(In) == 2) put_l(ll, true);
+        if constexpr (sizeof(In) == 2) put_l(ll, 1);
 #pragma unroll
         for (int kk = 0; kk < H; ++kk) yq[kk] = ys.col(q, kk, g, c);
 #pragma unroll
@@ -755,7 +769,7 @@ BwdWs bwd_ws(const s6_heads_dims& d, const HeadsPlan& p, int in_dtype) {
   o.nblk = (d.seqlen + q - 1) / q;
   head_runs(d.batch * d.groups * o.nblk, d.heads / d.groups, &o.nhb, &o.hpb);
   heads_segments(2 * p.rows, d.seqlen, q, &o.nseg, &o.seg_len);
-  const size_t tile = (size_t)p.rows * kTP * p.NT * sizeof(float);  // bf16: two planes of two bytes
+  const size_t tile = (size_t)p.rows * kTP * p.NT * sizeof(float);
   o.planes = 0;
   o.agg = up256(2 * (size_t)o.nblk * tile);
   o.sd = o.agg + (o.nseg > 1 ? up256(2 * (size_t)o.nseg * tile) : 0);
@@ -883,7 +897,7 @@ int s6_heads_scan_bwd(const s6_heads_dims* d, int in_dtype, int flags, const voi
     if (rc == S6_OK) rc = launch_heads_fold(a, p, 2, st);
     if (rc) return rc;
   }
-  a.planes = w + ws.planes;
+  a.planes = reinterpret_cast<float*>(w + ws.planes);
   rc = launch_heads_state(in_dtype, a, p, 1, 2, st);
   if (rc) return rc;
   ba.dx = dx; ba.ddelta = ddelta; ba.dB = dBm; ba.dC = dCm;

@@ -132,6 +132,13 @@ __device__ __forceinline__ void to_whole(const float (&f)[8], Whole<uint16_t>& o
   for (int i = 0; i < 3; ++i) o.part[i].v = __builtin_bit_cast(bf16x8, w[i]);
 }
 __device__ __forceinline__ void to_whole(const float (&f)[8], Whole<float>& o) { to_frag(f, o.part[0]); }
+// d += a b, the smallest parts first
+template <typename In>
+__device__ __forceinline__ f32x4 mma_whole(const Whole<In>& a, const Frag<In>& b, f32x4 d) {
+#pragma unroll
+  for (int i = Whole<In>::kParts - 1; i >= 0; --i) d = mma(a.part[i], b, d);
+  return d;
+}
 
 // ------------------------------------------------------------- LDS tiles --
 // Eight consecutive values of LDS as an operand.
@@ -287,13 +294,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint3
 }
 constexpr uint32_t kNowhere = 0xfffffff0u;  // an offset past every buffer
 
-// Eight values at a global address as an operand.
-__device__ __forceinline__ void load_frag(gbytes p, Frag<uint16_t>& o) {
-  o.v = __builtin_bit_cast(bf16x8, *reinterpret_cast<const gu32x4 __attribute__((address_space(1)))*>(p));
-}
-__device__ __forceinline__ void load_frag(gbytes p, Frag<float>& o) {
+// Eight floats, four and four of which 64 lanes lie side by side.
+__device__ __forceinline__ void load_halves(gbytes p, Frag<float>& o) {
   const auto* q = reinterpret_cast<const gf32x4 __attribute__((address_space(1)))*>(p);
-  const gf32x4 x = q[0], y = q[1];
+  const gf32x4 x = q[0], y = q[64];
 #pragma unroll
   for (int j = 0; j < 4; ++j) { o.v[j] = x[j]; o.v[4 + j] = y[j]; }
 }
@@ -580,7 +584,7 @@ struct HeadsArgs {
   float* agg;             // segment states from zero (dir, seg, row, 64, NT)
   float* sd;              // and their summed log2 decays (dir, seg, row)
   float* hin;             // state entering each segment (dir, seg, row, 64, NT) or null
-  void* planes;           // stored states of the backward, see heads_bwd.hip
+  float* planes;          // stored states of the backward, see heads_bwd.hip
 };
 
 // A row of the launch: one 64-channel tile of one head of one sequence.

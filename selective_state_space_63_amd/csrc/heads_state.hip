@@ -18,7 +18,7 @@
 // 128: 0.34 GB read (x, dy) and 0.67 GB of states stored in both directions in
 // 232 us, 4.3 TB/s.  Over segments (nothing stored) by a chunk's latency, as the
 // scan: 65536 tokens of 24 heads of 64, N 64: 100 us.  The channel tiles of a
-// wave pair lie side by side in the stored planes, so a lane stores 16 bytes.
+// wave pair lie side by side in the stored planes, 16 bytes per lane and store.
 #include "heads_kernel.h"
 
 namespace s6i {
@@ -112,22 +112,14 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? (VEC ? 3 : 2) : 1) void s6_h
     const bool enter = dir ? ((k + 1) % kPerBlock == 0 || k == nch - 1) : k % kPerBlock == 0;
     if (mode == 1 && a.planes && enter) {
       const int64_t blk = t0 / kBlockTokens<In>, nblk = (a.L + kBlockTokens<In> - 1) / kBlockTokens<In>;
-      // operand order: [state tile][channel half][lane][8], see heads_bwd.hip
-      In* pl = static_cast<In*>(a.planes) +
-               ((dir * nblk + blk) * nrows + hr.row) * (int64_t)(kTP * NT) * (sizeof(In) == 2 ? 2 : 1);
+      // operand order: [state tile][channel half][four of eight][lane][4], see heads_bwd.hip
+      float* pl = a.planes + ((dir * nblk + blk) * nrows + hr.row) * (int64_t)(kTP * NT);
 #pragma unroll
       for (int q = 0; q < NW; ++q) {
-        float f[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) f[r] = T[q][r >> 2][r & 3];
-        Pair<In> o;
-        to_pair(f, o);
-        In* at = pl + (((nh * NW + q) * 2 + pp) * 64 + lane) * 8;
-        if constexpr (sizeof(In) == 2) {
-          *reinterpret_cast<bf16x8*>(at) = o.hi.v;
-          *reinterpret_cast<bf16x8*>(at + kTP * NT) = o.lo.v;
-        } else {
-          store_vec<float, 8>(at, o.hi.v);
+        for (int j = 0; j < 2; ++j) {
+          const float f[4] = {T[q][j][0], T[q][j][1], T[q][j][2], T[q][j][3]};
+          store_vec<float, 4>(pl + ((((nh * NW + q) * 2 + pp) * 2 + j) * 64 + lane) * 4, f);
         }
       }
     }

@@ -27,6 +27,28 @@ SHAPES = [
 ]
 
 
+@pytest.mark.parametrize("L", [1, 5, 130])
+def test_gradient_of_the_decay_keeps_fp32(torch_cuda, L):
+    """dA of bf16 inputs comes from states in fp32.  One channel and one state
+    column, so that an error of a stored state is that of every term it is in.
+    Weak decays (exponents of at most 6 in all): a term meets about a dozen
+    roundings of fp32, a decay off by 2^-22, and sums of up to 9 levels and
+    2 blocks: 32 * 2^-24 = 2^-19 of the magnitude."""
+    from selective_state_space_63_amd import block
+    torch = torch_cuda
+    d, n = case(torch, 1, L, 64, 1, 1, 1, "bf16", "none", True, 64)
+    d["A"].mul_(0.05)
+    n["A"] = d["A"].double().cpu().numpy()
+    g = np.random.default_rng(65)
+    dy = torch.from_numpy(g.standard_normal((1, L, 64, 1)).astype(np.float32)).cuda().to(torch.bfloat16)
+    dh = torch.from_numpy(g.standard_normal((1, 64, 1, 1)).astype(np.float32)).cuda()
+    got = block.heads_scan_bwd(d["x"], None, d["A"], d["Bm"], d["Cm"], dy, dh_last=dh, **opts(d, "none", False))
+    want, mag = ref.scan_bwd(n["x"], None, n["A"], n["Bm"], n["Cm"], dy.double().cpu().numpy(), n["D"], n["h0"],
+                             dh.double().cpu().numpy())["dA"]
+    worst = float(np.max(np.abs(got["dA"].double().cpu().numpy() - want) / mag))
+    assert worst <= 2.0 ** -19, worst
+
+
 def rounded_once(got, want, mag, what):
     got = got.detach().double().cpu().numpy()
     room = 2.0 ** -8 * np.abs(want) + 1.01 * KEPT_BAR * mag
