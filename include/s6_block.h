@@ -47,7 +47,7 @@
  * held in two floats each: its relative error is about 2^-24 times its own
  * exponent, whatever decays lie before it (sequences packed closely one after
  * another lose nothing).  Repeated calls give identical bits.
- * An x that is not finite makes its channel NaN from its token on; other
+ * An x that is not finite leaves its channel not finite from its token on; other
  * channels and earlier tokens keep their values.  In the backward such a value
  * may also reach the other tokens of its block of 128 (fp32: 64).
  */

@@ -66,9 +66,9 @@ const char* s6_status_str(int status) {
   switch (status) {
     case S6_OK: return "ok";
     case S6_ERR_NULL: return "a required pointer is NULL";
-    case S6_ERR_SHAPE: return "invalid size (negative, or the element count overflows)";
+    case S6_ERR_SHAPE: return "invalid size (negative, an element count that overflows, or groups that do not divide)";
     case S6_ERR_DTYPE: return "in_dtype must be S6_F32 or S6_BF16";
-    case S6_ERR_UNSUPPORTED: return "unsupported: dstate outside 1..32, filter width outside 1..4, or an option this entry point lacks";
+    case S6_ERR_UNSUPPORTED: return "unsupported: dstate outside 1..32 (s6_heads_*: 1..128), filter width outside 1..4, or an option this entry point lacks";
     case S6_ERR_ALIGN: return "a pointer is not aligned to its element size";
     case S6_ERR_FLAGS: return "unknown option bits in flags";
     case S6_ERR_WORKSPACE:

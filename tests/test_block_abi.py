@@ -201,3 +201,10 @@ def test_binding_refuses(lib):
         block.add_norm_fwd(x, torch.ones(8))
     with pytest.raises(ValueError, match="groups"):
         block.gated_norm_fwd(x, x, torch.ones(8), groups=3)
+
+
+def test_status_texts_hold_for_the_block_operators(lib):
+    """What a refusal says is true of these entry points too."""
+    text = lambda rc: lib.s6_status_str(rc).decode()  # noqa: E731
+    assert fwd(lib, dims(dstate=129)) == UNSUP and "1..128" in text(UNSUP)
+    assert fwd(lib, dims(heads=5)) == SHAPE and "groups" in text(SHAPE)
