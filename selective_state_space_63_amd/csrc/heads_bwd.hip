@@ -46,13 +46,15 @@
 // 3e-7, and take the block kernel 494 us instead of 524 (8 x 2048 tokens of 80
 // heads of 64, N 128).
 //
-// What bounds it: one workgroup of eight waves fits a CU (242 VGPRs, 157 KB of
-// LDS), so a turn is the sum of its phases' latencies: 11 us at 128 tokens x 64
-// channels x N 128.  8 x 2048 tokens of 80 heads of 64, N 128: 442 - 475 us, of
-// which HBM needs 190 (1.2 GB).  Register spills cost the most on the way here
-// (802 us with 163 of them): reloads wait behind the prefetches of the next
-// turn, so those are L2 touches for the states, and token tiles past the
-// sequence are left out by branches.
+// What bounds it: one workgroup of eight waves fits a CU (242 VGPRs, 159 KB of
+// LDS), so a turn is the sum of its phases' latencies: 13 us at 128 tokens x 64
+// channels x N 128.  8 x 2048 tokens of 80 heads of 64, N 128: 522 - 555 us, of
+// which HBM needs 190 (1.2 GB); vector units 50 %, matrix units 17 %, LDS 31 %
+// busy (31 % of that bank conflicts), half of the waves' cycles are waits.  Of it
+// the second parts for dx, with their two barriers, are 43 us.  Register spills
+// cost the most on the way here (802 us with 163 of them): reloads wait behind the
+// prefetches of the next turn, so those are L2 touches for the states, and token
+// tiles past the sequence are left out by branches.
 #include "heads_kernel.h"
 
 namespace s6i {

@@ -25,14 +25,15 @@
 //
 // What bounds it: the latency of a chunk's chain (stage -> Gram -> y -> state,
 // three barriers), not a unit: at 8 x 2048 tokens of 80 heads of 64, N 128,
-// 196 us alone in a queue (222 - 245 us between other kernels), 1.7 TB/s of
-// the 6.2 TB/s that a copy reaches, with the vector units 39 % and the matrix
-// units 23 % busy and LDS 30 %; a workgroup alone on its CU takes 10.6
-// thousand cycles per chunk, each of three takes 13 thousand.  So what counts
-// is workgroups per CU: 168 VGPRs and 51 KB of LDS let three in.  Measured and
-// not kept: Gram tiles of a wave side by side (+6 %), Gram tiles formed once
-// per group by a launch of their own (+2 %, registers), four workgroups per
-// CU (spills).
+// 235 us in a queue of its own (245 - 270 us between other kernels), 1.6 TB/s
+// of the 6.2 TB/s that a copy reaches, with the vector units 44 % and the
+// matrix units 24 % busy and LDS 31 %; a chunk takes 7.3 us with three
+// workgroups on a CU.  So what counts is workgroups per CU: 168 VGPRs and 52.5
+// KB of LDS let three in.  The second parts in y cost 11 % of the scan with one
+// (10 % at N 64, 2 % for few long rows).  Measured and not kept: Gram tiles of a
+// wave side by side (+6 %), Gram tiles formed once per group by a launch of their
+// own (+2 %, registers), the state's part of y beside the Gram tiles instead of
+// behind them (+1 to +4 %), four workgroups per CU (spills; at N 64 +6 %).
 #include "heads_kernel.h"
 
 namespace s6i {
@@ -426,12 +427,12 @@ HeadsArgs heads_args(const s6_heads_dims& d, const HeadsPlan& p, int flags, cons
 }
 
 // Few rows leave CUs idle: with at most one row per CU the sequence is cut
-// into segments, up to three workgroups per CU (what the kernel's registers
-// allow at N > 64), of at least two chunks each.  Measured, us of scan + state
-// walk + fold, at targets of two and three per CU and at least four and two
-// chunks: 65536 tokens of 24 heads of 64, N 64: 302 and 270; 2 x 2048 tokens
-// of 24 heads of 64, N 128: 50 and 50; 3 x 777 tokens of 10 fp32 heads of 40,
-// N 24: 42 and 31.
+// into segments, up to three workgroups per CU (what the scan's registers
+// allow; the state walk's allow four at N <= 64), of at least two chunks each.
+// Measured, us of the call at targets of two, three and four per CU: 65536
+// tokens of 24 heads of 64, N 64: 332, 304 and 318; 2 x 2048 tokens of 24 heads
+// of 64, N 128: 57, 54 and 54; 3 x 777 tokens of 10 fp32 heads of 40, N 24: 31
+// each (42 with segments of at least four chunks).
 void heads_segments(int64_t rows, int64_t L, int64_t unit, int64_t* nseg, int64_t* seg_len) {
   *nseg = 1;
   *seg_len = L;

@@ -16,8 +16,8 @@
 //
 // For the backward it is bound by HBM: 8 x 2048 tokens of 80 heads of 64, N
 // 128: 0.34 GB read (x, dy) and 0.67 GB of states stored in both directions in
-// 232 us, 4.3 TB/s.  Over segments (nothing stored) by a chunk's latency, as the
-// scan: 65536 tokens of 24 heads of 64, N 64: 100 us.  The channel tiles of a
+// 231 us, 4.4 TB/s.  Over segments (nothing stored) by a chunk's latency, as the
+// scan: 65536 tokens of 24 heads of 64, N 64: 84 - 100 us.  The channel tiles of a
 // wave pair lie side by side in the stored planes, 16 bytes per lane and store.
 #include "heads_kernel.h"
 

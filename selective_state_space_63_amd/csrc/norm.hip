@@ -8,8 +8,9 @@
 //   dw_k = sum over rows of dout_k u_k i
 // Both sums of the backward, sum u^2 and sum dh u, need the inputs alone, so
 // each direction reads its inputs once, keeps them in registers, adds across
-// the row's threads once and writes its outputs: the kernels are bound by
-// HBM.  Sums and statistics are fp32.
+// the row's threads once and writes its outputs: the forward is bound by HBM,
+// the backward by the few rows that its registers let a CU hold at once (see
+// norm_plan).  Sums and statistics are fp32.
 //
 // Layout: a row is a workgroup's (as many waves as hold it), or, for narrow
 // rows, a wave's with four rows per workgroup.  Each thread keeps K pieces of V
@@ -23,7 +24,8 @@
 //
 // Training passes (forward, backward and column sums), bf16: 16384 rows of
 // 2560 with an fp32 residual 271 us (4.6 TB/s), gated 16384 rows of 5120 325 us
-// (4.1 TB/s); 256 rows of 2560: 3.7 us of kernel, 10.4 us with the call.
+// (4.1 TB/s), of which the backward kernels 158 and 215 us (4.7 and 3.9 TB/s);
+// 256 rows of 2560: 3.7 us of kernel, 10.6 us with the call.
 #include "block_internal.h"
 
 namespace s6i {
@@ -648,8 +650,11 @@ NormPlan norm_plan(int64_t rows, int64_t width, bool vec, bool sums) {
   p.per = p.multi ? 4 : 1;
   p.wide = !p.multi && np > (int64_t)p.K * p.threads;
   const int64_t need = (rows + p.per - 1) / p.per;
-  // enough workgroups to fill the CUs with 2048 threads each, where column sums
-  // are taken at most kParts walkers
+  // Enough workgroups for 2048 threads per CU, where column sums are taken at most
+  // kParts walkers.  The forward kernels are resident so; the backward kernels'
+  // 104 to 128 VGPRs hold 1024 threads per CU: bf16 rows of 5120 are ten waves, of
+  // which one workgroup fits, rows of 2560 five, of which three fit (1024 walkers
+  // are then a round and a third).
   int64_t most = (int64_t)cu_count() * (2048 / p.threads);
   if (sums && most > kParts / p.per) most = kParts / p.per;
   p.blocks = need < most ? need : most;
