@@ -1,0 +1,839 @@
+// gated.hip -- the gated linear recurrence (include/s6_gated.h): whole
+// sequences, gradients and the single-token step.
+//
+// Per channel, with r = sigmoid(ga + ba), i = sigmoid(gx + bx), v = A r,
+// a = e^v, b = sqrt(1 - a^2):
+//   h_t = a_t h_{t-1} + u_t,  u_t = b_t i_t x_t
+//   lam_t = dy_t + mu_{t+1},  mu_t = a_t lam_t       (adjoint of h_t, backwards)
+//   dv = lam (a h_{t-1} - (a^2 / b) i x),  dga = dv A r (1 - r)
+//   dx = lam b i,  dgx = lam b x i (1 - i),  dA = sum dv r
+// Both recurrences are runs of maps h -> P h + H, which compose, so a tile of
+// 128 tokens x 64 channels is reduced to one (P, H) per channel without
+// knowing the state that enters it.
+//
+// One pass: a workgroup loads its tile into registers once, publishes the
+// tile's (P, H), takes the state entering the tile from the tiles before it (look_back)
+// and writes the tile's outputs.  Inputs are read once and outputs written once,
+// at any number of rows and any length.  Workgroups draw their tiles in order
+// from a counter, so the tiles that one waits for belong to workgroups that
+// run already: every wait ends.  The state entering tile k is always formed as
+// P_{k-1} s_{k-1} + H_{k-1}, whichever of these a workgroup reads or forms
+// itself, so repeated calls give identical bits.
+#include "s6_gated.h"
+
+#include "block_internal.h"
+
+namespace s6i {
+
+namespace {
+
+constexpr int kGC = 64;                // channels of a tile
+constexpr int kGT = S6_GATED_TOKENS;   // tokens of a tile
+constexpr int kWaves = 8;              // waves of a workgroup
+constexpr int64_t kMaxTiles = 1 << 22; // workgroups of a launch (threads below 2^32)
+
+struct GatedArgs {
+  const void* x; const void* ga; const void* gx;
+  const float* A; const float* ba; const float* bx;
+  const uint8_t* starts;
+  const float* first;    // h0 (forward), dh_last (backward); nullable
+  const float* states;   // backward: the state entering every tile
+  float* states_out;     // forward, nullable
+  void* y;               // forward, nullable
+  float* last;           // h_last (forward), dh0 (backward); nullable
+  const void* dy; void* dx; void* dga; void* dgx;
+  float* parts;          // column sums' parts (tiles, 3, kGC), nullable
+  uint64_t* slots;       // (cols, chunks, kGC), null where a sequence is one tile
+  unsigned long long* ticket;
+  int64_t batch, L, dim;
+  int64_t x_batch, x_token, a_batch, a_token, g_batch, g_token;
+  int64_t cblocks, cols, chunks, tiles;
+  int64_t base;          // first tile of the launch (one tile per sequence)
+  int unit;
+};
+
+// ------------------------------------------------------------- look back --
+// A tile's word: {P, H} of the tile, {kState, s} once the state s after the
+// tile is known, or kEmpty (both halves written at once).
+constexpr uint32_t kEmpty = 0xffffffffu, kState = 0xfffffffeu;
+constexpr int kWindow = 16;     // tiles looked at together
+constexpr int kMaxPolls = 1 << 21;
+
+__device__ __forceinline__ uint64_t word(uint32_t lo, float h) {
+  return (uint64_t)__float_as_uint(h) << 32 | lo;
+}
+__device__ __forceinline__ uint32_t low(uint64_t w) { return (uint32_t)w; }
+__device__ __forceinline__ float high(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32)); }
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void post(uint64_t* p, uint64_t w) {
+  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// P h + H; a P with its sign set is 0 by a start: nothing of h passes, not
+// even a NaN.
+__device__ __forceinline__ float pass(float P, float H, float h) {
+  return (__float_as_uint(P) >> 31) ? H : __builtin_fmaf(P, h, H);
+}
+
+// The state entering tile q > 0 for this lane's channel (whole waves call it).
+// slot: the lane's word of this tile; the tile before it is kGC words lower.
+__device__ float look_back(uint64_t* slot, int64_t q) {
+  const int n = q < kWindow ? (int)q : kWindow;
+  for (int polls = 0; polls < kMaxPolls; ++polls) {
+    const uint64_t w0 = peek(slot - kGC);
+    if (__ballot(low(w0) == kState) == ~0ull) return high(w0);
+    uint64_t w[kWindow];
+    w[0] = w0;
+#pragma unroll
+    for (int i = 1; i < kWindow; ++i) w[i] = i < n ? peek(slot - (int64_t)(i + 1) * kGC) : ~0ull;
+    int found = -1;
+    bool go = true;
+#pragma unroll
+    for (int i = 0; i < kWindow; ++i) {
+      const uint64_t state = __ballot(low(w[i]) == kState), none = __ballot(low(w[i]) == kEmpty);
+      if (go && state == ~0ull) found = i;
+      go = go && state == 0 && none == 0;
+    }
+    if (found >= 0) {
+      float h = 0.0f;
+#pragma unroll
+      for (int i = kWindow - 1; i >= 0; --i) {
+        if (i == found) h = high(w[i]);
+        if (i < found) h = pass(__uint_as_float(low(w[i])), high(w[i]), h);
+      }
+      return h;
+    }
+    __builtin_amdgcn_s_sleep(2);
+  }
+  return __builtin_nanf("");  // not reached: see the file's head
+}
+
+__device__ __forceinline__ uint32_t publishable(float P) { return P != P ? 0x7fc00000u : __float_as_uint(P); }
+
+// ---------------------------------------------------------------- pieces --
+// VEC consecutive channels of a token as loaded.
+template <typename In, int VEC>
+struct Piece {
+  In e[VEC];
+  __device__ __forceinline__ void load(const In* p) {
+    if constexpr (VEC == 1) {
+      e[0] = *p;
+    } else if constexpr (sizeof(In) == 2) {
+      const uint32_t w = *reinterpret_cast<gptr<uint32_t>>(reinterpret_cast<uintptr_t>(p));
+      __builtin_memcpy(e, &w, 4);
+    } else {
+      const float2 w = *reinterpret_cast<const float2*>(p);
+      __builtin_memcpy(e, &w, 8);
+    }
+  }
+  __device__ __forceinline__ float get(int v) const { return to_f32(e[v]); }
+};
+template <typename In, int VEC>
+__device__ __forceinline__ void put(In* p, const float (&f)[VEC]) {
+  if constexpr (VEC == 1)
+    *p = from_f32<In>(f[0]);
+  else if constexpr (sizeof(In) == 2)
+    *reinterpret_cast<uint32_t*>(p) = bf_pack(f[0], f[1]);
+  else
+    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+}
+
+__device__ __forceinline__ float gate_f(float g, float bias_l2) {  // bias_l2 = -bias log2(e)
+  return fast_rcp(1.0f + fast_exp2(__builtin_fmaf(g, -kLog2e, bias_l2)));
+}
+
+// 1 - e^{2 v} for v = v2 ln 2 <= 0 and a = e^v: by its series where e^{2v} is
+// near 1 (|2 v| < 0.18, five terms, next one 2.6e-7 of the sum), else from a
+// (a's rounding there is at most 7e-7 of the difference).
+__device__ __forceinline__ float one_less_square(float v2, float a) {
+  constexpr float k = 2.0f * kLn2;
+  float s = __builtin_fmaf(v2, k * k * k * k * k / 120.0f, k * k * k * k / 24.0f);
+  s = __builtin_fmaf(v2, s, k * k * k / 6.0f);
+  s = __builtin_fmaf(v2, s, k * k / 2.0f);
+  s = __builtin_fmaf(v2, s, k);
+  return v2 > -0.13f ? -v2 * s : __builtin_fmaf(-a, a, 1.0f);
+}
+
+// Where a lane's tokens lie: kWaves * VEC groups of T tokens, VEC groups to a
+// wave (64 / VEC lanes of VEC channels each).
+template <int VEC>
+struct Place {
+  static constexpr int G = kWaves * VEC, T = kGT / G;
+  int group, cl, nt;        // nt: tokens of the group that exist
+  int64_t col, q, k, b, c, t0;
+  bool on;                  // the lane's channels exist
+};
+template <int VEC, bool BACK>
+__device__ __forceinline__ Place<VEC> place_of(const GatedArgs& a, int64_t tile) {
+  using P = Place<VEC>;
+  P p;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int half = VEC == 2 ? lane >> 5 : 0;
+  p.cl = (VEC == 2 ? lane & 31 : lane) * VEC;
+  p.group = wave * VEC + half;
+  p.q = tile / a.cols;
+  p.col = tile - p.q * a.cols;
+  p.k = BACK ? a.chunks - 1 - p.q : p.q;
+  p.b = p.col / a.cblocks;
+  p.c = (p.col - p.b * a.cblocks) * kGC + p.cl;
+  p.on = p.c < a.dim;
+  p.t0 = p.k * kGT + p.group * P::T;
+  const int64_t left = a.L - p.t0;
+  p.nt = left < 0 ? 0 : left < P::T ? (int)left : P::T;
+  return p;
+}
+
+// The tile of this workgroup.
+__device__ __forceinline__ int64_t draw_tile(const GatedArgs& a, unsigned long long* shared) {
+  if (!a.slots) return a.base + blockIdx.x;
+  if (threadIdx.x == 0) *shared = atomicAdd(a.ticket, 1ull);
+  __syncthreads();
+  const uint64_t t = *shared;
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(t >> 32)) << 32 |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)t));
+}
+
+// A group's rows of one input.  Lanes past dim take the last channels again,
+// tokens past the end the last token again.
+template <typename In, int VEC>
+__device__ __forceinline__ void load_rows(Piece<In, VEC> (&o)[Place<VEC>::T], const void* base, int64_t batch_stride,
+                                          int64_t token_stride, const GatedArgs& a, const Place<VEC>& p, bool whole) {
+  constexpr int T = Place<VEC>::T;
+  const int64_t c = p.on ? p.c : a.dim - VEC;
+  const In* row = static_cast<const In*>(base) + p.b * batch_stride + c;
+  if (whole) {
+    const In* r = row + p.t0 * token_stride;
+#pragma unroll
+    for (int t = 0; t < T; ++t) o[t].load(r + t * token_stride);
+  } else {
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const int64_t at = p.t0 + t < a.L ? p.t0 + t : a.L - 1;
+      o[t].load(row + at * token_stride);
+    }
+  }
+}
+
+// Bit t: token t of the lane's group starts a sequence.
+template <int VEC>
+__device__ __forceinline__ uint32_t starts_of(const GatedArgs& a, const Place<VEC>& p) {
+  constexpr int T = Place<VEC>::T;
+  const int lane = threadIdx.x & 63, t = lane & (T - 1);
+  const uint64_t all = __ballot(t < p.nt && a.starts[p.b * a.L + p.t0 + (t < p.nt ? t : 0)] != 0);
+  return (uint32_t)(VEC == 2 && lane >= 32 ? all >> 32 : all) & ((1u << T) - 1);
+}
+
+// --------------------------------------------------------------- forward --
+template <typename In, int VEC, bool UNIT, bool STARTS>
+__global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_kernel(GatedArgs a) {
+  using P = Place<VEC>;
+  constexpr int G = P::G, T = P::T;
+  __shared__ float2 agg[G][kGC];
+  __shared__ float hin[G][kGC];
+  __shared__ unsigned long long drawn;
+  const int64_t tile = draw_tile(a, &drawn);
+  if (tile >= a.tiles) return;
+  const P p = place_of<VEC, false>(a, tile);
+  const bool whole = (p.k + 1) * kGT <= a.L;
+  Piece<In, VEC> xr[T], ar[T], gr[T];
+  load_rows<In, VEC>(ar, a.ga, a.a_batch, a.a_token, a, p, whole);
+  load_rows<In, VEC>(xr, a.x, a.x_batch, a.x_token, a, p, whole);
+  if (a.gx) load_rows<In, VEC>(gr, a.gx, a.g_batch, a.g_token, a, p, whole);
+  uint32_t starts = 0;
+  if constexpr (STARTS) starts = p.nt > 0 ? starts_of<VEC>(a, p) : 0;
+  float A2[VEC], ba[VEC], bx[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const int64_t c = (p.on ? p.c : a.dim - VEC) + v;
+    A2[v] = a.A[c] * kLog2e;
+    ba[v] = a.ba ? -a.ba[c] * kLog2e : 0.0f;
+    bx[v] = a.bx ? -a.bx[c] * kLog2e : 0.0f;
+  }
+  float av[T][VEC], uv[T][VEC], Pl[VEC], Hl[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) { Pl[v] = 1.0f; Hl[v] = 0.0f; }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const bool st = STARTS && (starts >> t & 1);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      const float v2 = A2[v] * gate_f(ar[t].get(v), ba[v]);
+      float d = fast_exp2(v2);
+      float u = xr[t].get(v);
+      if (a.gx) u *= gate_f(gr[t].get(v), bx[v]);
+      if constexpr (!UNIT) {
+        const float b = __builtin_amdgcn_sqrtf(one_less_square(v2, d));
+        u = st ? u : b * u;
+      }
+      if (!whole && t >= p.nt) { d = 1.0f; u = 0.0f; }
+      av[t][v] = d;
+      uv[t][v] = u;
+      if constexpr (STARTS) {
+        d = __builtin_fabsf(d);
+        Pl[v] = st ? -0.0f : Pl[v] * d;
+        Hl[v] = st ? u : __builtin_fmaf(d, Hl[v], u);
+      } else {
+        Pl[v] *= d;
+        Hl[v] = __builtin_fmaf(d, Hl[v], u);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) agg[p.group][p.cl + v] = make_float2(Pl[v], Hl[v]);
+  __syncthreads();
+  if (threadIdx.x < 64) {  // the first wave: one channel per lane
+    const int lane = threadIdx.x;
+    const int64_t c = p.c - p.cl + lane;
+    float Pt = 1.0f, Ht = 0.0f;
+    float2 g[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      g[i] = agg[i][lane];
+      Ht = pass(g[i].x, g[i].y, Ht);
+      Pt = (STARTS && __float_as_uint(g[i].x) >> 31) ? g[i].x : g[i].x * Pt;
+    }
+    uint64_t* slot = a.slots ? a.slots + (p.col * a.chunks + p.q) * kGC + lane : nullptr;
+    float h;
+    if (p.q == 0) {
+      h = a.first && c < a.dim ? a.first[p.b * a.dim + c] : 0.0f;
+    } else {
+      post(slot, word(publishable(Pt), Ht));
+      h = look_back(slot, p.q);
+    }
+    if (p.q + 1 < a.chunks) post(slot, word(kState, pass(Pt, Ht, h)));
+    if (a.states_out && c < a.dim) a.states_out[(p.b * a.chunks + p.k) * a.dim + c] = h;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      hin[i][lane] = h;
+      h = pass(g[i].x, g[i].y, h);
+    }
+  }
+  __syncthreads();
+  if (!a.y) return;
+  float h[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) h[v] = hin[p.group][p.cl + v];
+  In* y = static_cast<In*>(a.y) + (p.b * a.L + p.t0) * a.dim + p.c;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+      h[v] = STARTS && (starts >> t & 1) ? uv[t][v] : __builtin_fmaf(av[t][v], h[v], uv[t][v]);
+    if (p.on && (whole || t < p.nt)) put<In, VEC>(y + t * a.dim, h);
+  }
+  if (a.last && p.k + 1 == a.chunks && p.group == G - 1 && p.on)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) a.last[p.b * a.dim + p.c + v] = h[v];
+}
+
+// -------------------------------------------------------------- backward --
+template <typename In, int VEC, bool UNIT, bool STARTS>
+__global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_bwd_kernel(GatedArgs a) {
+  using P = Place<VEC>;
+  constexpr int G = P::G, T = P::T;
+  __shared__ float agg[3][G][kGC];   // P, H, M of the groups; later the column sums
+  __shared__ float ent[2][G][kGC];   // the state entering a group, the adjoint leaving it
+  __shared__ unsigned long long drawn;
+  const int64_t tile = draw_tile(a, &drawn);
+  if (tile >= a.tiles) return;
+  const P p = place_of<VEC, true>(a, tile);
+  const bool whole = (p.k + 1) * kGT <= a.L;
+  Piece<In, VEC> xr[T], ar[T], gr[T], yr[T];
+  load_rows<In, VEC>(ar, a.ga, a.a_batch, a.a_token, a, p, whole);
+  load_rows<In, VEC>(yr, a.dy, a.L * a.dim, a.dim, a, p, whole);
+  load_rows<In, VEC>(xr, a.x, a.x_batch, a.x_token, a, p, whole);
+  if (a.gx) load_rows<In, VEC>(gr, a.gx, a.g_batch, a.g_token, a, p, whole);
+  uint32_t starts = 0;
+  if constexpr (STARTS) starts = p.nt > 0 ? starts_of<VEC>(a, p) : 0;
+  float Ac[VEC], ba[VEC], bx[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const int64_t c = (p.on ? p.c : a.dim - VEC) + v;
+    Ac[v] = a.A[c];
+    ba[v] = a.ba ? -a.ba[c] * kLog2e : 0.0f;
+    bx[v] = a.bx ? -a.bx[c] * kLog2e : 0.0f;
+  }
+  // the gates, decays and input factors, and the group's map of the state
+  float av[T][VEC], rv[T][VEC], iv[T][VEC], bv[T][VEC];
+  float Pl[VEC], Hl[VEC], Ml[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) { Pl[v] = 1.0f; Hl[v] = Ml[v] = 0.0f; }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const bool st = STARTS && (starts >> t & 1), none = !whole && t >= p.nt;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      rv[t][v] = gate_f(ar[t].get(v), ba[v]);
+      iv[t][v] = a.gx ? gate_f(gr[t].get(v), bx[v]) : 1.0f;
+      const float v2 = Ac[v] * kLog2e * rv[t][v];
+      float d = fast_exp2(v2);
+      bv[t][v] = 1.0f;
+      if constexpr (!UNIT) {
+        const float s = one_less_square(v2, d);
+        bv[t][v] = st ? 1.0f : __builtin_amdgcn_sqrtf(s);
+      }
+      float u = bv[t][v] * iv[t][v] * xr[t].get(v);
+      if (none) { d = 1.0f; u = 0.0f; }
+      if constexpr (STARTS) d = __builtin_fabsf(d);
+      av[t][v] = d;
+      if constexpr (STARTS) {
+        Pl[v] = st ? -0.0f : Pl[v] * d;
+        Hl[v] = st ? u : __builtin_fmaf(d, Hl[v], u);
+      } else {
+        Pl[v] *= d;
+        Hl[v] = __builtin_fmaf(d, Hl[v], u);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = T - 1; t >= 0; --t) {
+    const bool st = STARTS && (starts >> t & 1), none = !whole && t >= p.nt;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      const float m = av[t][v] * ((none ? 0.0f : yr[t].get(v)) + Ml[v]);
+      Ml[v] = st ? 0.0f : m;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    agg[0][p.group][p.cl + v] = Pl[v];
+    agg[1][p.group][p.cl + v] = Hl[v];
+    agg[2][p.group][p.cl + v] = Ml[v];
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    const int64_t c = p.c - p.cl + lane;
+    const bool on = c < a.dim;
+    float gp[G], gm[G];
+    float h = on ? a.states[(p.b * a.chunks + p.k) * a.dim + c] : 0.0f;
+    float Pt = 1.0f, Mt = 0.0f;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      gp[i] = agg[0][i][lane];
+      gm[i] = agg[2][i][lane];
+      ent[0][i][lane] = h;
+      h = pass(gp[i], agg[1][i][lane], h);
+    }
+#pragma unroll
+    for (int i = G - 1; i >= 0; --i) {
+      Mt = pass(gp[i], gm[i], Mt);
+      Pt = (STARTS && __float_as_uint(gp[i]) >> 31) ? gp[i] : gp[i] * Pt;
+    }
+    uint64_t* slot = a.slots ? a.slots + (p.col * a.chunks + p.q) * kGC + lane : nullptr;
+    float m;
+    if (p.q == 0) {
+      m = a.first && on ? a.first[p.b * a.dim + c] : 0.0f;
+    } else {
+      post(slot, word(publishable(Pt), Mt));
+      m = look_back(slot, p.q);
+    }
+    if (p.q + 1 < a.chunks) post(slot, word(kState, pass(Pt, Mt, m)));
+#pragma unroll
+    for (int i = G - 1; i >= 0; --i) {
+      ent[1][i][lane] = m;
+      m = pass(gp[i], gm[i], m);
+    }
+    if (a.last && p.q + 1 == a.chunks && on) a.last[p.b * a.dim + c] = m;
+  }
+  __syncthreads();
+  // the state before each token, then backwards with the adjoint
+  float hp[T][VEC], h[VEC], m[VEC], sA[VEC], sa[VEC], sx[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    h[v] = ent[0][p.group][p.cl + v];
+    m[v] = ent[1][p.group][p.cl + v];
+    sA[v] = sa[v] = sx[v] = 0.0f;
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      hp[t][v] = h[v];
+      const float u = bv[t][v] * iv[t][v] * xr[t].get(v);
+      h[v] = STARTS && (starts >> t & 1) ? u : __builtin_fmaf(av[t][v], h[v], u);
+    }
+  const int64_t at = (p.b * a.L + p.t0) * a.dim + p.c;
+  In* dx = static_cast<In*>(a.dx) + at;
+  In* dga = static_cast<In*>(a.dga) + at;
+  In* dgx = static_cast<In*>(a.dgx) + at;
+#pragma unroll
+  for (int t = T - 1; t >= 0; --t) {
+    const bool st = STARTS && (starts >> t & 1), none = !whole && t >= p.nt;
+    float ox[VEC], oa[VEC], og[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      const float x = xr[t].get(v), d = av[t][v], r = rv[t][v], i = iv[t][v], b = bv[t][v];
+      const float lam = (none ? 0.0f : yr[t].get(v)) + m[v];
+      m[v] = st ? 0.0f : d * lam;
+      float w = d * hp[t][v];
+      if constexpr (!UNIT) w = __builtin_fmaf(b > 0.0f ? -d * d * fast_rcp(b) : 0.0f, i * x, w);
+      const float dv = st || none ? 0.0f : lam * w;
+      ox[v] = lam * b * i;
+      oa[v] = dv * Ac[v] * r * (1.0f - r);
+      og[v] = ox[v] * x * (1.0f - i);
+      sA[v] = __builtin_fmaf(dv, r, sA[v]);
+      sa[v] += oa[v];
+      sx[v] += none ? 0.0f : og[v];
+    }
+    if (p.on && (whole || t < p.nt)) {
+      put<In, VEC>(dx + t * a.dim, ox);
+      put<In, VEC>(dga + t * a.dim, oa);
+      if (a.gx) put<In, VEC>(dgx + t * a.dim, og);
+    }
+  }
+  if (!a.parts) return;
+  // (the groups' maps were read before the barrier above)
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    agg[0][p.group][p.cl + v] = sA[v];
+    agg[1][p.group][p.cl + v] = sa[v];
+    agg[2][p.group][p.cl + v] = sx[v];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3 * kGC) {
+    const int which = threadIdx.x / kGC, l = threadIdx.x % kGC;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < G; ++i) s += agg[which][i][l];
+    a.parts[((p.col * a.chunks + p.k) * 3 + which) * kGC + l] = s;
+  }
+}
+
+// Sums of the parts over rows and chunks.  blockIdx.x: block of 64 channels;
+// blockIdx.y: which sum; blockIdx.z: a slice of the parts.
+// part (n, 3, kGC) of channel block cb: index (b * cblocks + cb) * chunks + k.
+struct SumArgs {
+  const float* parts;
+  float* out[3];       // nullable
+  float* slices;       // (slices, cblocks, 3, kGC) where there are several
+  int64_t batch, chunks, cblocks, dim, per;  // per: parts of a slice
+};
+__global__ __launch_bounds__(512) void s6_gated_colsum_kernel(SumArgs a) {
+  __shared__ float buf[8][kGC];
+  const int which = blockIdx.y, l = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t n = a.batch * a.chunks, cb = blockIdx.x;
+  const int64_t lo = blockIdx.z * a.per, hi = lo + a.per < n ? lo + a.per : n;
+  float s = 0.0f;
+#pragma unroll 4
+  for (int64_t i = lo + w; i < hi; i += 8) {
+    const int64_t b = i / a.chunks, k = i - b * a.chunks;
+    s += a.parts[(((b * a.cblocks + cb) * a.chunks + k) * 3 + which) * kGC + l];
+  }
+  buf[w][l] = s;
+  __syncthreads();
+  if (w) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += buf[i][l];
+  const int64_t c = cb * kGC + l;
+  if (a.slices)
+    a.slices[((blockIdx.z * a.cblocks + cb) * 3 + which) * kGC + l] = s;
+  else if (a.out[which] && c < a.dim)
+    a.out[which][c] = s;
+}
+__global__ __launch_bounds__(64) void s6_gated_slices_kernel(SumArgs a, int64_t slices) {
+  const int which = blockIdx.y, l = threadIdx.x;
+  const int64_t cb = blockIdx.x, c = cb * kGC + l;
+  float s = 0.0f;
+#pragma unroll 4
+  for (int64_t i = 0; i < slices; ++i) s += a.slices[((i * a.cblocks + cb) * 3 + which) * kGC + l];
+  if (a.out[which] && c < a.dim) a.out[which][c] = s;
+}
+
+// Empty words and a counter at 0.
+__global__ void s6_gated_init_kernel(uint64_t* slots, int64_t n, unsigned long long* ticket) {
+  const int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i0 == 0) *ticket = 0;
+  for (int64_t i = i0; i < n; i += (int64_t)gridDim.x * blockDim.x) slots[i] = ~0ull;
+}
+
+// ------------------------------------------------------------------ step --
+template <typename In, int VEC>
+__global__ __launch_bounds__(256) void s6_gated_step_kernel(GatedArgs a, float* hs) {
+  const int64_t per = (a.dim + VEC - 1) / VEC, i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t b = a.base + blockIdx.y;
+  const int64_t c = i0 * VEC;
+  if (i0 >= per) return;
+  Piece<In, VEC> xr, ar, gr;
+  xr.load(static_cast<const In*>(a.x) + b * a.x_batch + c);
+  ar.load(static_cast<const In*>(a.ga) + b * a.a_batch + c);
+  if (a.gx) gr.load(static_cast<const In*>(a.gx) + b * a.g_batch + c);
+  Piece<float, VEC> hr;
+  hr.load(hs + b * a.dim + c);
+  float h[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const float v2 = a.A[c + v] * kLog2e * gate_f(ar.get(v), a.ba ? -a.ba[c + v] * kLog2e : 0.0f);
+    const float d = fast_exp2(v2);
+    float u = xr.get(v);
+    if (a.gx) u *= gate_f(gr.get(v), a.bx ? -a.bx[c + v] * kLog2e : 0.0f);
+    if (!a.unit) u *= __builtin_amdgcn_sqrtf(one_less_square(v2, d));
+    h[v] = __builtin_fmaf(d, hr.get(v), u);
+  }
+  put<float, VEC>(hs + b * a.dim + c, h);
+  put<In, VEC>(static_cast<In*>(a.y) + b * a.dim + c, h);
+}
+
+// ------------------------------------------------------------------ host --
+int check_gated(const s6_gated_dims* d, int in_dtype, int flags, bool gx, bool tokens) {
+  if (!d) return S6_ERR_NULL;
+  if (in_dtype != S6_F32 && in_dtype != S6_BF16) return S6_ERR_DTYPE;
+  if (flags & ~S6_UNIT_INPUT) return S6_ERR_FLAGS;
+  if (d->batch < 0 || d->dim < 0 || (tokens && d->seqlen < 0)) return S6_ERR_SHAPE;
+  if (d->batch == 0 || d->dim == 0) return S6_OK;
+  const int64_t len = tokens && d->seqlen > 0 ? d->seqlen : 1;
+  // element counts with headroom for padded tiles and byte sizes
+  int64_t t;
+  if (d->dim > (1 << 28) || d->batch > INT32_MAX || !mul_ok(d->batch, d->dim, &t) || !mul_ok(t, 64 * 16, &t) ||
+      !mul_ok(t, len + kGT, &t))
+    return S6_ERR_SHAPE;
+  const int64_t str[] = {d->x_batch, d->x_token, d->a_batch, d->a_token, d->g_batch, d->g_token};
+  for (int i = 0; i < (gx ? 6 : 4); ++i) {
+    if ((i & 1) && !tokens) continue;
+    if (str[i] < 0) return S6_ERR_SHAPE;
+    if (!mul_ok(str[i], (i & 1) ? len : d->batch, &t) || !mul_ok(t, 16, &t)) return S6_ERR_SHAPE;
+  }
+  return S6_OK;
+}
+
+struct GatedWs {
+  int64_t cblocks, cols, chunks, tiles, slices, per;
+  size_t slots, states, parts, sums, total;  // byte offsets; the counter lies at 0
+};
+GatedWs gated_ws(const s6_gated_dims& d, bool back, bool has_states) {
+  GatedWs w;
+  w.cblocks = (d.dim + kGC - 1) / kGC;
+  w.cols = d.batch * w.cblocks;
+  w.chunks = (d.seqlen + kGT - 1) / kGT;
+  w.tiles = w.cols * w.chunks;
+  const int64_t n = d.batch * w.chunks;
+  // column sums: slices of at least 256 parts, at most 64
+  w.slices = n / 256 < 1 ? 1 : n / 256 > 64 ? 64 : n / 256;
+  w.per = (n + w.slices - 1) / w.slices;
+  w.slots = 256;
+  size_t at = w.chunks > 1 ? 256 + (size_t)w.tiles * kGC * sizeof(uint64_t) : 0;
+  w.states = w.parts = w.sums = 0;
+  if (back) {
+    w.states = up256(at);
+    at = w.states + (has_states ? 0 : (size_t)n * d.dim * sizeof(float));
+    w.parts = up256(at);
+    at = w.parts + (size_t)w.tiles * 3 * kGC * sizeof(float);
+    w.sums = up256(at);
+    at = w.sums + (w.slices > 1 ? (size_t)w.slices * w.cblocks * 3 * kGC * sizeof(float) : 0);
+  }
+  w.total = up256(at);
+  return w;
+}
+
+template <typename In, int VEC>
+int launch_gated(GatedArgs a, bool back, hipStream_t st) {
+  if (a.slots) {
+    const int64_t n = a.tiles * kGC;
+    const int64_t blocks = (n + 1023) / 1024;
+    hipLaunchKernelGGL(s6_gated_init_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, a.slots, n,
+                       a.ticket);
+    S6_HIP(hipGetLastError(), "s6_gated_init_kernel launch");
+  }
+  for (a.base = 0; a.base < a.tiles; a.base += kMaxTiles) {
+    const dim3 grid((unsigned)(a.tiles - a.base < kMaxTiles ? a.tiles - a.base : kMaxTiles)), block(kWaves * 64);
+#define S6_GATED_LAUNCH(UNIT, STARTS)                                                              \
+  if (back)                                                                                        \
+    hipLaunchKernelGGL((s6_gated_scan_bwd_kernel<In, VEC, UNIT, STARTS>), grid, block, 0, st, a);  \
+  else                                                                                             \
+    hipLaunchKernelGGL((s6_gated_scan_kernel<In, VEC, UNIT, STARTS>), grid, block, 0, st, a);
+    if (a.unit && a.starts) { S6_GATED_LAUNCH(true, true) }
+    else if (a.unit) { S6_GATED_LAUNCH(true, false) }
+    else if (a.starts) { S6_GATED_LAUNCH(false, true) }
+    else { S6_GATED_LAUNCH(false, false) }
+#undef S6_GATED_LAUNCH
+    S6_HIP(hipGetLastError(), "s6_gated_scan kernel launch");
+  }
+  return S6_OK;
+}
+template <typename In>
+int launch_gated_in(const GatedArgs& a, bool back, bool vec, hipStream_t st) {
+  return vec ? launch_gated<In, 2>(a, back, st) : launch_gated<In, 1>(a, back, st);
+}
+
+GatedArgs gated_args(const s6_gated_dims& d, int flags, const void* x, const void* ga, const float* ba, const void* gx,
+                     const float* bx, const float* A) {
+  GatedArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.ga = ga; a.gx = gx; a.A = A; a.ba = ba; a.bx = bx;
+  a.batch = d.batch; a.L = d.seqlen; a.dim = d.dim;
+  a.x_batch = d.x_batch; a.x_token = d.x_token; a.a_batch = d.a_batch; a.a_token = d.a_token;
+  a.g_batch = d.g_batch; a.g_token = d.g_token;
+  a.unit = (flags & S6_UNIT_INPUT) != 0;
+  return a;
+}
+
+// Two channels per lane: every row begins at a multiple of two elements.
+bool pairs_ok(const s6_gated_dims& d, bool gx, bool tokens, size_t esz, const void* const* ptrs, int n) {
+  bool ok = d.dim % 2 == 0 && d.x_batch % 2 == 0 && d.a_batch % 2 == 0 && (!gx || d.g_batch % 2 == 0);
+  if (tokens) ok = ok && d.x_token % 2 == 0 && d.a_token % 2 == 0 && (!gx || d.g_token % 2 == 0);
+  for (int i = 0; i < n; ++i) ok = ok && aligned(ptrs[i], 2 * esz);
+  return ok;
+}
+
+int check_ptrs(const void* const* ins, int n, size_t esz, const void* const* f32s, int m) {
+  for (int i = 0; i < n; ++i)
+    if (!aligned(ins[i], esz)) return S6_ERR_ALIGN;
+  for (int i = 0; i < m; ++i)
+    if (!aligned(f32s[i], 4)) return S6_ERR_ALIGN;
+  return S6_OK;
+}
+
+}  // namespace
+
+}  // namespace s6i
+
+using namespace s6i;
+
+extern "C" {
+
+int s6_gated_scan_fwd_workspace_size(const s6_gated_dims* d, size_t* bytes) {
+  if (!bytes) return S6_ERR_NULL;
+  const int rc = check_gated(d, S6_F32, 0, true, true);
+  if (rc) return rc;
+  *bytes = d->batch == 0 || d->dim == 0 || d->seqlen == 0 ? 0 : gated_ws(*d, false, true).total;
+  return S6_OK;
+}
+
+int s6_gated_scan_fwd(const s6_gated_dims* d, int in_dtype, int flags, const void* x, const void* gate_a,
+                      const float* bias_a, const void* gate_x, const float* bias_x, const float* A,
+                      const uint8_t* starts, const float* h0, void* y, float* h_last, float* states, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int rc = check_gated(d, in_dtype, flags, gate_x != nullptr, true);
+  if (rc) return rc;
+  if (d->batch == 0 || d->dim == 0) return S6_OK;
+  const size_t esz = in_dtype == S6_BF16 ? 2 : 4;
+  if (d->seqlen > 0 && (!x || !gate_a || !A || !y || (bias_x && !gate_x))) return S6_ERR_NULL;
+  const void* ins[] = {x, gate_a, gate_x, y};
+  const void* f32s[] = {bias_a, bias_x, A, h0, h_last, states};
+  if ((rc = check_ptrs(ins, 4, esz, f32s, 6))) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (d->seqlen == 0) return h_last ? launch_copy_state(h0, h_last, d->batch * d->dim, st) : S6_OK;
+  const GatedWs w = gated_ws(*d, false, true);
+  if (w.total > 0) {
+    if (!workspace || workspace_bytes < w.total) return S6_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return S6_ERR_ALIGN;
+  }
+  GatedArgs a = gated_args(*d, flags, x, gate_a, bias_a, gate_x, bias_x, A);
+  a.starts = starts; a.first = h0; a.states_out = states; a.y = y; a.last = h_last;
+  a.cblocks = w.cblocks; a.cols = w.cols; a.chunks = w.chunks; a.tiles = w.tiles;
+  if (w.chunks > 1) {
+    a.ticket = static_cast<unsigned long long*>(workspace);
+    a.slots = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + w.slots);
+  }
+  const bool vec = pairs_ok(*d, gate_x != nullptr, true, esz, ins, 4);
+  return in_dtype == S6_BF16 ? launch_gated_in<uint16_t>(a, false, vec, st) : launch_gated_in<float>(a, false, vec, st);
+}
+
+int s6_gated_scan_bwd_workspace_size(const s6_gated_dims* d, int has_states, size_t* bytes) {
+  if (!bytes) return S6_ERR_NULL;
+  const int rc = check_gated(d, S6_F32, 0, true, true);
+  if (rc) return rc;
+  *bytes = d->batch == 0 || d->dim == 0 || d->seqlen == 0 ? 0 : gated_ws(*d, true, has_states != 0).total;
+  return S6_OK;
+}
+
+int s6_gated_scan_bwd(const s6_gated_dims* d, int in_dtype, int flags, const void* x, const void* gate_a,
+                      const float* bias_a, const void* gate_x, const float* bias_x, const float* A,
+                      const uint8_t* starts, const float* h0, const float* states, const void* dy,
+                      const float* dh_last, void* dx, void* dgate_a, void* dgate_x, float* dA, float* dbias_a,
+                      float* dbias_x, float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_gated(d, in_dtype, flags, gate_x != nullptr, true);
+  if (rc) return rc;
+  const size_t esz = in_dtype == S6_BF16 ? 2 : 4;
+  const bool work = d->batch > 0 && d->dim > 0 && d->seqlen > 0;
+  if (work && (!x || !gate_a || !A || !dy || !dx || !dgate_a || (gate_x && !dgate_x) ||
+               ((bias_x || dbias_x || dgate_x) && !gate_x)))
+    return S6_ERR_NULL;
+  const void* ins[] = {x, gate_a, gate_x, dy, dx, dgate_a, dgate_x};
+  const void* f32s[] = {bias_a, bias_x, A, h0, states, dh_last, dA, dbias_a, dbias_x, dh0};
+  if ((rc = check_ptrs(ins, 7, esz, f32s, 10))) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (!work) {  // sums of nothing
+    fill(dA, 0.0f, d->dim, st);
+    fill(dbias_a, 0.0f, d->dim, st);
+    fill(dbias_x, 0.0f, d->dim, st);
+    if ((dA || dbias_a || dbias_x) && d->dim > 0) S6_HIP(hipGetLastError(), "s6_fill launch");
+    return dh0 && d->batch * d->dim > 0 ? launch_copy_state(dh_last, dh0, d->batch * d->dim, st) : S6_OK;
+  }
+  const GatedWs w = gated_ws(*d, true, states != nullptr);
+  if (!workspace || workspace_bytes < w.total) return S6_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return S6_ERR_ALIGN;
+  char* ws = static_cast<char*>(workspace);
+  GatedArgs a = gated_args(*d, flags, x, gate_a, bias_a, gate_x, bias_x, A);
+  a.starts = starts;
+  a.cblocks = w.cblocks; a.cols = w.cols; a.chunks = w.chunks; a.tiles = w.tiles;
+  if (w.chunks > 1) {
+    a.ticket = reinterpret_cast<unsigned long long*>(ws);
+    a.slots = reinterpret_cast<uint64_t*>(ws + w.slots);
+  }
+  const bool vec = pairs_ok(*d, gate_x != nullptr, true, esz, ins, 7);
+  const auto launch = [&](bool back) {
+    return in_dtype == S6_BF16 ? launch_gated_in<uint16_t>(a, back, vec, st) : launch_gated_in<float>(a, back, vec, st);
+  };
+  if (!states) {  // the forward without y
+    a.first = h0;
+    a.states_out = reinterpret_cast<float*>(ws + w.states);
+    if ((rc = launch(false))) return rc;
+    a.states_out = nullptr;
+    states = reinterpret_cast<float*>(ws + w.states);
+  }
+  a.states = states; a.first = dh_last; a.last = dh0;
+  a.dy = dy; a.dx = dx; a.dga = dgate_a; a.dgx = dgate_x;
+  const bool sums = dA || dbias_a || dbias_x;
+  a.parts = sums ? reinterpret_cast<float*>(ws + w.parts) : nullptr;
+  if ((rc = launch(true))) return rc;
+  if (!sums) return S6_OK;
+  SumArgs s;
+  s.parts = a.parts;
+  s.out[0] = dA; s.out[1] = dbias_a; s.out[2] = dbias_x;
+  s.slices = w.slices > 1 ? reinterpret_cast<float*>(ws + w.sums) : nullptr;
+  s.batch = d->batch; s.chunks = w.chunks; s.cblocks = w.cblocks; s.dim = d->dim; s.per = w.per;
+  hipLaunchKernelGGL(s6_gated_colsum_kernel, dim3((unsigned)w.cblocks, 3, (unsigned)w.slices), dim3(512), 0, st, s);
+  S6_HIP(hipGetLastError(), "s6_gated_colsum_kernel launch");
+  if (w.slices > 1) {
+    hipLaunchKernelGGL(s6_gated_slices_kernel, dim3((unsigned)w.cblocks, 3), dim3(64), 0, st, s, w.slices);
+    S6_HIP(hipGetLastError(), "s6_gated_slices_kernel launch");
+  }
+  return S6_OK;
+}
+
+int s6_gated_state_update(const s6_gated_dims* d, int in_dtype, int flags, float* h, const void* x,
+                          const void* gate_a, const float* bias_a, const void* gate_x, const float* bias_x,
+                          const float* A, void* y, void* stream) {
+  int rc = check_gated(d, in_dtype, flags, gate_x != nullptr, false);
+  if (rc) return rc;
+  if (d->batch == 0 || d->dim == 0) return S6_OK;
+  if (!h || !x || !gate_a || !A || !y || (bias_x && !gate_x)) return S6_ERR_NULL;
+  const size_t esz = in_dtype == S6_BF16 ? 2 : 4;
+  const void* ins[] = {x, gate_a, gate_x, y};
+  const void* f32s[] = {h, bias_a, bias_x, A};
+  if ((rc = check_ptrs(ins, 4, esz, f32s, 4))) return rc;
+  GatedArgs a = gated_args(*d, flags, x, gate_a, bias_a, gate_x, bias_x, A);
+  a.y = y;
+  const bool vec = pairs_ok(*d, gate_x != nullptr, false, esz, ins, 4) && aligned(h, 8);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const int64_t per = vec ? (d->dim + 1) / 2 : d->dim;
+  for (a.base = 0; a.base < d->batch; a.base += 65535) {
+    const int64_t rows = d->batch - a.base < 65535 ? d->batch - a.base : 65535;
+    const dim3 grid((unsigned)((per + 255) / 256), (unsigned)rows);
+    if (in_dtype == S6_BF16) {
+      if (vec) hipLaunchKernelGGL((s6_gated_step_kernel<uint16_t, 2>), grid, dim3(256), 0, st, a, h);
+      else hipLaunchKernelGGL((s6_gated_step_kernel<uint16_t, 1>), grid, dim3(256), 0, st, a, h);
+    } else {
+      if (vec) hipLaunchKernelGGL((s6_gated_step_kernel<float, 2>), grid, dim3(256), 0, st, a, h);
+      else hipLaunchKernelGGL((s6_gated_step_kernel<float, 1>), grid, dim3(256), 0, st, a, h);
+    }
+    S6_HIP(hipGetLastError(), "s6_gated_step_kernel launch");
+  }
+  return S6_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,377 @@
+"""The gated recurrence (include/s6_gated.h) against the plain 64-bit
+reference of gated_ref.py: sequences, gradients, the single-token step, layouts,
+starts, and the calls a program makes (streams, graphs, autograd).
+
+A value is within bar(L) of its magnitude (derived there), and bf16 results one
+rounding, 2^-8 of the value, besides.
+"""
+import numpy as np
+import pytest
+
+import gated_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch_cuda():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from selective_state_space_63_amd import s6
+    s6.load_library()
+    return torch
+
+
+f64 = lambda t: None if t is None else t.detach().double().cpu().numpy()  # noqa: E731
+
+
+def close(got, want, mag, L, what):
+    half = ref.HALF_STEP["bf16" if "bfloat16" in str(got.dtype) else "f32"]
+    g = f64(got)
+    assert g.shape == want.shape and np.isfinite(g).all(), what
+    allowed = ref.bar(L) * mag + half * np.abs(want) + 1e-37
+    worst = float(np.max(np.abs(g - want) / allowed)) if g.size else 0.0
+    assert worst <= 1.0, f"{what}: {worst:.2f} of what is allowed"
+
+
+def inputs(torch, b, L, d, dtype, seed, wide=0, gx=True, bias=True, h0=True, starts=None, decay=(0.9, 0.999)):
+    g = np.random.default_rng([seed, b, L, d])
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+
+    def rows():
+        t = torch.from_numpy(g.standard_normal((b, L, d + wide)).astype(np.float32)).cuda().to(dt)
+        return t[..., wide:] if wide else t
+
+    vec = lambda v: torch.from_numpy(np.ascontiguousarray(v, np.float32)).cuda()  # noqa: E731
+    k = dict(x=rows(), gate_a=rows(), gate_x=rows() if gx else None, A=vec(4 * np.log(g.uniform(*decay, d))),
+             bias_a=vec(0.5 * g.standard_normal(d)) if bias else None,
+             bias_x=vec(0.5 * g.standard_normal(d)) if bias and gx else None,
+             h0=vec(g.standard_normal((b, d))) if h0 else None, starts=None)
+    if starts is not None:
+        k["starts"] = torch.from_numpy(g.random((b, L)) < starts).cuda()
+    dy = torch.from_numpy(g.standard_normal((b, L, d)).astype(np.float32)).cuda().to(dt)
+    dh = vec(g.standard_normal((b, d)))
+    return k, dy, dh
+
+
+def host(k, unit):
+    n = dict(x="x", ga="gate_a", gx="gate_x", A="A", ba="bias_a", bx="bias_x", h0="h0")
+    out = {o: f64(k[i]) for o, i in n.items()}
+    out["starts"] = None if k["starts"] is None else k["starts"].cpu().numpy()
+    return dict(out, unit=unit)
+
+
+def check(torch, k, dy, dh, unit=False):
+    """Forward and backward of one call against the reference; the results."""
+    from selective_state_space_63_amd import gated
+    L = k["x"].shape[1]
+    h = host(k, unit)
+    y, hl, states = gated.gated_scan_fwd(**k, unit_input=unit, return_last_state=True, return_states=True)
+    want, mag = ref.scan(**h)
+    close(y, want, mag, L, "y")
+    close(hl, want[:, -1], mag[:, -1], L, "h_last")
+    first = np.zeros_like(want[:, :1]) if k["h0"] is None else h["h0"][:, None]
+    enter = np.concatenate([first, want], 1)[:, :L:gated.TOKENS]
+    close(states, enter, np.concatenate([np.abs(first), mag], 1)[:, :L:gated.TOKENS], L, "states")
+    back = dict(h, dh_last=f64(dh))
+    g = gated.gated_scan_bwd(**k, dy=dy, unit_input=unit, dh_last=dh, states=states)
+    for name, (w, m) in ref.scan_bwd(dy=f64(dy), **back).items():
+        if name in g:
+            close(g[name], w, m, L, name)
+        else:
+            given = dict(dh0=k["h0"], dbias_a=k["bias_a"], dbias_x=k["bias_x"], dgate_x=k["gate_x"])
+            assert given[name] is None, name
+    # without the forward's states: the same bits
+    again = gated.gated_scan_bwd(**k, dy=dy, unit_input=unit, dh_last=dh)
+    for name in g:
+        assert torch.equal(g[name], again[name]), name
+    return y, hl, g
+
+
+SIZES = [
+    # batch, seqlen, dim, dtype, extra columns of the rows before the slice
+    (1, 1, 1, "f32", 0),
+    (2, 1, 64, "bf16", 0),
+    (3, 7, 66, "bf16", 2),
+    (2, 128, 64, "f32", 0),
+    (2, 129, 65, "bf16", 0),       # odd rows: one channel per lane
+    (1, 255, 130, "bf16", 1),      # slices that begin at odd elements
+    (3, 777, 101, "f32", 0),
+    (2, 1024, 192, "bf16", 64),
+    (1, 5003, 24, "f32", 0),       # more tiles than are looked at together
+    (9, 600, 514, "bf16", 0),
+]
+
+
+@pytest.mark.parametrize("size", SIZES, ids=str)
+@pytest.mark.parametrize("unit", [False, True], ids=["root", "unit"])
+def test_sequences(torch_cuda, size, unit):
+    b, L, d, dtype, wide = size
+    print(f"[case] gated {size} unit {unit}", flush=True)
+    k, dy, dh = inputs(torch_cuda, b, L, d, dtype, 31, wide=wide)
+    check(torch_cuda, k, dy, dh, unit)
+
+
+@pytest.mark.parametrize("opts", [dict(gx=False), dict(bias=False), dict(h0=False), dict(gx=False, bias=False, h0=False)],
+                         ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_without(torch_cuda, opts, dtype):
+    print(f"[case] gated without {opts} {dtype}", flush=True)
+    k, dy, _ = inputs(torch_cuda, 2, 300, 70, dtype, 32, **opts)
+    check(torch_cuda, k, dy, None)
+
+
+@pytest.mark.parametrize("rate", [0.0, 0.01, 0.3, 1.0])
+@pytest.mark.parametrize("dim,dtype", [(66, "bf16"), (33, "f32")])
+@pytest.mark.parametrize("unit", [False, True], ids=["root", "unit"])
+def test_starts(torch_cuda, rate, dim, dtype, unit):
+    print(f"[case] gated starts {rate} {dim} {dtype} {unit}", flush=True)
+    k, dy, dh = inputs(torch_cuda, 3, 700, dim, dtype, 33, starts=rate)
+    y, hl, g = check(torch_cuda, k, dy, dh, unit)
+    if rate == 1.0:
+        assert float(g["dgate_a"].abs().max()) == 0 and float(g["dA"].abs().max()) == 0
+    if rate == 0.0:
+        from selective_state_space_63_amd import gated
+        plain = gated.gated_scan_fwd(**dict(k, starts=None), unit_input=unit)
+        assert torch_cuda.equal(plain, y)
+
+
+def test_packed_sequences_are_apart(torch_cuda):
+    """Sequences packed into one row give the bits of each alone where their
+    tiles agree, and nothing that is not finite crosses a start."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    k, dy, _ = inputs(torch, 1, 512, 64, "f32", 34, h0=False)
+    starts = torch.zeros(1, 512, dtype=torch.bool, device="cuda")
+    starts[0, [0, 200, 384]] = True
+    k["starts"] = starts
+    y = gated.gated_scan_fwd(**k)
+    alone = {n: k[n][:, 384:] for n in ("x", "gate_a", "gate_x")}
+    tail = dict(k, **alone, starts=starts[:, 384:].contiguous())
+    assert torch.equal(gated.gated_scan_fwd(**tail), y[:, 384:])
+    x = k["x"].clone()
+    x[0, 150, 3] = float("nan")
+    x[0, 151, 4] = float("inf")
+    bad = dict(k, x=x)
+    yb, hl = gated.gated_scan_fwd(**bad, return_last_state=True)
+    assert torch.equal(yb[:, 200:], y[:, 200:]) and torch.equal(yb[:, :150], y[:, :150])
+    assert not bool(torch.isfinite(yb[0, 150:200, 3]).any()) and not bool(torch.isfinite(yb[0, 151:200, 4]).any())
+    others = [c for c in range(64) if c not in (3, 4)]
+    assert torch.equal(yb[..., others], y[..., others])
+    d = dy.clone()
+    d[0, 300, 5] = float("nan")
+    g, gb = (gated.gated_scan_bwd(**k, dy=v) for v in (dy, d))
+    for name in ("dx", "dgate_a", "dgate_x"):
+        assert torch.equal(g[name][:, :200], gb[name][:, :200]) and torch.equal(g[name][:, 301:], gb[name][:, 301:])
+        assert torch.equal(g[name][..., 6:], gb[name][..., 6:])
+
+
+def test_gates_at_their_ends(torch_cuda):
+    """Gates far out on both sides, decays of 1 (A = 0, and a shut gate) and of 0."""
+    torch = torch_cuda
+    k, dy, dh = inputs(torch, 2, 260, 96, "f32", 35)
+    k["gate_a"][:, :, 0:32] *= 30
+    k["gate_x"][:, :, 16:48] *= 30
+    k["gate_a"][:, ::3, 48] = -200.0
+    k["A"][48] = -0.5
+    k["A"][49] = 0.0
+    k["A"][50] = -1e-6
+    k["A"][51] = -60.0
+    k["A"][52] = -1e4
+    check(torch, k, dy, dh)
+    check(torch, k, dy, dh, unit=True)
+
+
+def test_memory_of_a_whole_sequence(torch_cuda):
+    """Decays close to 1: 1 - a^2 keeps its accuracy."""
+    k, dy, dh = inputs(torch_cuda, 2, 1500, 64, "f32", 36, decay=(0.99999, 0.9999999))
+    check(torch_cuda, k, dy, dh)
+
+
+def test_layouts(torch_cuda):
+    """Seqlen before batch, broadcast rows, overlapping token rows."""
+    torch = torch_cuda
+    k, dy, dh = inputs(torch, 3, 150, 66, "bf16", 37)
+    want = check(torch, k, dy, dh)
+    t = {n: k[n].transpose(0, 1).contiguous().transpose(0, 1) for n in ("x", "gate_a", "gate_x")}
+    got = check(torch, dict(k, **t), dy, dh)
+    assert torch.equal(want[0], got[0]) and all(torch.equal(want[2][n], got[2][n]) for n in want[2])
+    b = {n: k[n][:1, :1].expand(3, 150, 66) for n in ("gate_a", "gate_x")}
+    check(torch, dict(k, **b), dy, dh)
+    flat = torch.randn(3 * 150 * 8 + 66, device="cuda")
+    over = flat.as_strided((3, 150, 66), (150 * 8, 8, 1))
+    f = {n: k[n].float() for n in ("gate_a", "gate_x")}
+    check(torch, dict(k, x=over, **f), dy.float(), dh)
+
+
+@pytest.mark.parametrize("dim,dtype,wide", [(1, "f32", 0), (64, "bf16", 0), (770, "bf16", 2), (129, "bf16", 0),
+                                            (514, "f32", 3)])
+@pytest.mark.parametrize("unit", [False, True], ids=["root", "unit"])
+def test_step(torch_cuda, dim, dtype, wide, unit):
+    """One token at a time is the whole sequence."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    k, _, _ = inputs(torch, 5, 6, dim, dtype, 38, wide=wide)
+    h = k["h0"].clone()
+    want, mag = ref.scan(**host(k, unit))
+    opts = dict(A=k["A"], bias_a=k["bias_a"], bias_x=k["bias_x"], unit_input=unit)
+    for t in range(6):
+        y = gated.gated_state_update(h, k["x"][:, t], k["gate_a"][:, t], k["gate_x"][:, t], **opts)
+        close(y, want[:, t], mag[:, t], 6, f"y of token {t}")
+        close(h, want[:, t], mag[:, t], 6, f"state after token {t}")
+    h2 = k["h0"].clone()
+    y = gated.gated_state_update(h2, k["x"][:, 0], k["gate_a"][:, 0], None, k["A"], unit_input=unit)
+    plain = dict(host(k, unit), gx=None, ba=None, bx=None)
+    want, mag = ref.scan(**plain)
+    close(y, want[:, 0], mag[:, 0], 1, "y without a gate on x")
+
+
+def test_empty(torch_cuda):
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    for b, L, d in ((0, 5, 8), (2, 0, 8), (2, 5, 0)):
+        k, dy, dh = inputs(torch, b, L, d, "bf16", 39)
+        y, hl = gated.gated_scan_fwd(**k, return_last_state=True)
+        assert y.shape == (b, L, d) and (L > 0 or torch.equal(hl, k["h0"]))
+        g = gated.gated_scan_bwd(**k, dy=dy, dh_last=dh)
+        for n in ("dA", "dbias_a", "dbias_x"):
+            assert float(g[n].abs().sum()) == 0
+        assert L > 0 or torch.equal(g["dh0"], dh)
+        y, hl = gated.gated_scan_fwd(**dict(k, h0=None), return_last_state=True)
+        assert L > 0 or float(hl.abs().sum()) == 0
+
+
+def test_repeated_calls_and_streams(torch_cuda):
+    """The same bits every time, also for two calls at once on two streams."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    k, dy, dh = inputs(torch, 2, 3000, 320, "bf16", 40, starts=0.002)
+    call = lambda: (*gated.gated_scan_fwd(**k, return_last_state=True),  # noqa: E731
+                    *gated.gated_scan_bwd(**k, dy=dy, dh_last=dh).values())
+    want = call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(call())
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+def test_graph(torch_cuda):
+    """A captured forward and backward, replayed on new values between eager work."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    k, dy, dh = inputs(torch, 2, 700, 96, "bf16", 41)
+    new = inputs(torch, 2, 700, 96, "bf16", 42)[0]
+    run = lambda: (*gated.gated_scan_fwd(**k, return_last_state=True),  # noqa: E731
+                   *gated.gated_scan_bwd(**k, dy=dy, dh_last=dh).values())
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for i in range(4):
+        if i == 2:
+            for n in ("x", "gate_a", "h0"):
+                k[n].copy_(new[n])
+        want = run()
+        torch.cuda.synchronize()
+        for o in out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
+@pytest.mark.parametrize("unit", [False, True], ids=["root", "unit"])
+def test_autograd(torch_cuda, unit):
+    """GatedScan's gradients are those of the entry point, and differences of
+    the loss in 64 bits agree with them."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    k, dy, dh = inputs(torch, 2, 200, 34, "f32", 43, starts=0.01)
+    names = ("x", "gate_a", "gate_x", "A", "bias_a", "bias_x", "h0")
+    leaf = {n: k[n].clone().requires_grad_() for n in names}
+    y, hl = gated.GatedScan.apply(*(leaf[n] for n in names), k["starts"], unit)
+    torch.autograd.backward([y, hl], [dy, dh])
+    g = gated.gated_scan_bwd(**k, dy=dy, dh_last=dh, unit_input=unit)
+    for n in names:
+        assert torch.equal(leaf[n].grad, g["d" + n]), n
+    # along a direction: central differences of the reference, exact to about
+    # e^2 = 1e-8 of the sums' magnitude
+    h = host(k, unit)
+    key = dict(x="x", gate_a="ga", gate_x="gx", A="A", bias_a="ba", bias_x="bx", h0="h0")
+    gen = np.random.default_rng(44)
+    mags = {n: m for n, (_, m) in ref.scan_bwd(dy=f64(dy), dh_last=f64(dh), **h).items()}
+    for n in names:
+        v = gen.standard_normal(h[key[n]].shape)
+        e = 1e-4
+        loss = []
+        for s in (e, -e):
+            yy, _ = ref.scan(**dict(h, **{key[n]: h[key[n]] + s * v * (np.abs(h["A"]) if n == "A" else 1.0)}))
+            loss.append((yy * f64(dy)).sum() + (yy[:, -1] * f64(dh)).sum())
+        v = v * (np.abs(h["A"]) if n == "A" else 1.0)
+        got = float((f64(g["d" + n]) * v).sum())
+        room = (mags["d" + n] * np.abs(v)).sum()
+        assert abs((loss[0] - loss[1]) / (2 * e) - got) <= (ref.bar(200) + 1e-6) * room, n
+    # only what is asked for, and no second derivative
+    x = k["x"].clone().requires_grad_()
+    y, _ = gated.GatedScan.apply(x, k["gate_a"], k["gate_x"], k["A"])
+    (gx,) = torch.autograd.grad((y * y).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable|twice"):
+        (gx * gx).sum().backward()
+
+
+def test_written_in_place_is_noticed(torch_cuda):
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    k, _, _ = inputs(torch, 2, 40, 32, "f32", 45)
+    h = k["h0"].clone().requires_grad_()
+    y, _ = gated.GatedScan.apply(k["x"], k["gate_a"], k["gate_x"], k["A"], None, None, h)
+    gated.gated_state_update(h.detach(), k["x"][:, 0], k["gate_a"][:, 0], k["gate_x"][:, 0], k["A"])
+    with pytest.raises(RuntimeError, match="modified"):
+        y.sum().backward()
+
+
+def test_more_tiles_than_one_launch(torch_cuda):
+    """Rows past 2^22 workgroups, one and two tiles each."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    for b, L in (((1 << 22) + 3, 1), ((1 << 21) + 1, 130)):
+        print(f"[case] gated rows {b} of {L}", flush=True)
+        g = torch.Generator("cuda").manual_seed(b)
+        x, ga = (torch.randn(b, L, 1, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+        A = torch.tensor([-0.3], device="cuda")
+        y, hl = gated.gated_scan_fwd(x, ga, None, A, return_last_state=True)
+        a = torch.exp(A.double() / (1 + torch.exp(-ga.double())))[..., 0]
+        u = (torch.sqrt(1 - a * a) * x[..., 0].double())
+        h = torch.zeros(b, dtype=torch.float64, device="cuda")
+        m = torch.zeros_like(h)
+        worst = 0.0
+        for t in range(L):
+            h, m = a[:, t] * h + u[:, t], a[:, t] * m + u[:, t].abs()
+            worst = max(worst, float(((y[:, t, 0].double() - h).abs() / (ref.bar(L) * m + 2.0 ** -8 * h.abs() + 1e-37)).max()))
+        assert worst <= 1 and bool(((hl[:, 0].double() - h).abs() <= ref.bar(L) * m + 1e-37).all())
+        del x, ga, y, hl, a, u, h, m
+
+
+def test_long_row(torch_cuda):
+    """One sequence of many tiles and few channels, past 2^31 bytes, against the
+    reference of its last tokens (decays so strong that the tokens before do
+    not matter)."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    L, d = 17_000_001, 66
+    g = torch.Generator("cuda").manual_seed(46)
+    x, ga = (torch.randn(1, L, d, device="cuda", generator=g, dtype=torch.bfloat16) for _ in range(2))
+    A = torch.full((d,), -20.0, device="cuda")
+    y, hl = gated.gated_scan_fwd(x, ga, None, A, return_last_state=True)
+    for at in (1000, L // 2, L):  # each from 300 tokens before
+        k = dict(x=f64(x[:, at - 300:at]), ga=f64(ga[:, at - 300:at]), gx=None, A=f64(A))
+        want, mag = ref.scan(**k)
+        close(y[:, at - 100:at], want[:, -100:], mag[:, -100:], 300, f"y before {at}")
+    close(hl, want[:, -1], mag[:, -1], 300, "h_last")
