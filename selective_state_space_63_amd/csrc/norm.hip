@@ -27,12 +27,14 @@
 // (4.1 TB/s), of which the backward kernels 158 and 215 us (4.7 and 3.9 TB/s);
 // 256 rows of 2560: 3.7 us of kernel, 10.6 us with the call.
 #include "block_internal.h"
+#include "s6_q4.h"
 
 namespace s6i {
 
 namespace {
 
 constexpr int kMaxT = 1024;        // threads of a workgroup
+constexpr float kTopQ8 = 448.0f;   // largest e4m3 value
 constexpr int64_t kParts = 1024;   // most row walkers where column sums are taken (each leaves a part)
 
 struct NormArgs {
@@ -52,6 +54,7 @@ struct NormArgs {
   void* o2;                     // residual_out / dresidual / dz
   float* dw;                    // parts (walkers, dim), nullable
   float* dg;                    // parts (walkers, dim), nullable
+  float* row_scale;             // scales of an 8-bit output
 };
 
 // V values of a row as loaded.
@@ -224,6 +227,175 @@ __global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_add_norm_kernel(NormA
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = v[j] * inv * ww[j];
       store_vec<In, V>(out + i * V, v);
+    }
+  }
+}
+
+// -------------------------------------------------- add norm, 8-bit output --
+// The largest of unsigned values over the threads of a row, as row_sum2; as
+// bits of |v|, an infinity is above all numbers and a NaN above that.
+template <bool MULTI>
+__device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t (*buf)[kMaxT / 64], int par) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t o = __shfl_xor(m, d);
+    m = o > m ? o : m;
+  }
+  if constexpr (!MULTI) {
+    const int w = threadIdx.x >> 6, n = blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) buf[par][w] = m;
+    __syncthreads();
+    m = 0;
+    for (int i = 0; i < n; ++i) m = buf[par][i] > m ? buf[par][i] : m;
+  }
+  return m;
+}
+
+// V values times f as e4m3; all NaN where nan is set.
+template <int V>
+__device__ __forceinline__ void store_q8(uint8_t* p, const float (&v)[V], float f, bool nan) {
+  if constexpr (V == 1) {
+    *p = nan ? 0x7f : (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[0] * f, 0.0f, 0, false);
+  } else {
+    uint32_t o[V / 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * f, v[4 * i + 1] * f, 0, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * f, v[4 * i + 3] * f, w, true);
+      o[i] = nan ? 0x7f7f7f7fu : (uint32_t)w;
+    }
+    if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+  }
+}
+
+// As s6_add_norm_kernel, with the row's largest output found before any is
+// stored: the outputs stay in registers, or are formed again past them.
+template <typename In, typename Res, int V, int K, bool MULTI, bool WIDE>
+__global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_add_norm_q8_kernel(NormArgs a) {
+  __shared__ float buf[2][2][kMaxT / 64];
+  __shared__ uint32_t mbuf[2][kMaxT / 64];
+  const Walk wk = walk_of<MULTI>(a.rows);
+  const int64_t np = (a.dim + V - 1) / V;
+  const float inv_d = 1.0f / (float)a.dim;
+  float w[K][V], ga[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t i = (int64_t)k * wk.tpr + wk.t;
+#pragma unroll
+    for (int j = 0; j < V; ++j) ga[k][j] = a.scale;
+    if (i < np) {
+      load_vec<float, V>(a.w + i * V, w[k]);
+      if (a.gamma) {
+        load_vec<float, V>(a.gamma + i * V, ga[k]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) ga[k][j] *= a.scale;
+      }
+    }
+  }
+  Raw<In, V> xr[K];
+  Raw<Res, V> rr[K];
+  auto issue = [&](int64_t row) {
+    if (row >= a.rows) return;
+    const In* x = static_cast<const In*>(a.a) + row * a.a_stride;
+    const Res* r = static_cast<const Res*>(a.b) + row * a.dim;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      if (i < np) {
+        xr[k].load(x + i * V);
+        if (a.b) rr[k].load(r + i * V);
+      }
+    }
+  };
+  issue(wk.wk);
+  for (int64_t q = 0; q < wk.turns; ++q) {
+    const int64_t row = q * wk.nw + wk.wk;
+    const bool on = row < a.rows;
+    const In* x = static_cast<const In*>(a.a) + row * a.a_stride;
+    const Res* r = a.b ? static_cast<const Res*>(a.b) + row * a.dim : nullptr;
+    uint8_t* out = static_cast<uint8_t*>(a.o1) + row * a.dim;
+    Res* ro = static_cast<Res*>(a.o2) + row * a.dim;
+    float u[K][V];
+    float s = 0.0f, unused = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      if (on && i < np) {
+        float rv[V];
+        xr[k].get(u[k]);
+        if (r) rr[k].get(rv);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          u[k][j] = r ? __builtin_fmaf(ga[k][j], u[k][j], rv[j]) : ga[k][j] * u[k][j];
+          s = __builtin_fmaf(u[k][j], u[k][j], s);
+        }
+        store_vec<Res, V>(ro + i * V, u[k]);
+      }
+    }
+    issue(row + wk.nw);
+    // a piece past the registers, formed again in each phase and stored in the last
+    auto wide = [&](int64_t i, float (&v)[V]) {
+      float rv[V], gg[V];
+      load_vec<In, V>(x + i * V, v);
+      if (r) load_vec<Res, V>(r + i * V, rv);
+      if (a.gamma) load_vec<float, V>(a.gamma + i * V, gg);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float g = a.gamma ? gg[j] * a.scale : a.scale;
+        v[j] = r ? __builtin_fmaf(g, v[j], rv[j]) : g * v[j];
+      }
+    };
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
+      float v[V];
+      wide(i, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s = __builtin_fmaf(v[j], v[j], s);
+    }
+    row_sum2<MULTI>(s, unused, buf, (int)(q & 1));
+    const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(s, inv_d, a.eps));
+    uint32_t top = 0;
+    auto larger = [&](const float (&v)[V]) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint32_t m = __float_as_uint(v[j]) & 0x7fffffffu;
+        top = m > top ? m : top;
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      if (on && i < np) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) u[k][j] = u[k][j] * inv * w[k][j];
+        larger(u[k]);
+      }
+    }
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
+      float v[V], ww[V];
+      wide(i, v);
+      load_vec<float, V>(a.w + i * V, ww);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = v[j] * inv * ww[j];
+      larger(v);
+    }
+    top = row_max<MULTI>(top, mbuf, (int)(q & 1));
+    const bool nan = top >= 0x7f800000u;
+    const float most = top < 0x0d800000u ? 0.0f : __uint_as_float(top);  // 2^-100
+    const float f = most > 0.0f ? kTopQ8 * fast_rcp(most) : 0.0f;
+    if (on && wk.t == 0) a.row_scale[row] = nan ? __builtin_nanf("") : most * (1.0f / kTopQ8);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = (int64_t)k * wk.tpr + wk.t;
+      if (on && i < np) store_q8<V>(out + i * V, u[k], f, nan);
+    }
+    for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
+      float v[V], ww[V];
+      wide(i, v);
+      load_vec<float, V>(a.w + i * V, ww);
+      store_vec<Res, V>(ro + i * V, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = v[j] * inv * ww[j];
+      store_q8<V>(out + i * V, v, f, nan);
     }
   }
 }
@@ -732,6 +904,33 @@ int s6_add_norm_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, cons
   if (in_dtype == S6_F32) S6_LAUNCH_NORM(s6_add_norm_kernel, float, float);
   else if (res_dtype == S6_F32) S6_LAUNCH_NORM(s6_add_norm_kernel, uint16_t, float);
   else S6_LAUNCH_NORM(s6_add_norm_kernel, uint16_t, uint16_t);
+  return S6_OK;
+}
+
+int s6_add_norm_q8_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, const void* x, int64_t x_stride,
+                       const void* residual, const float* weight, const float* gamma, float scale, float eps, void* out,
+                       float* out_scale, void* residual_out, void* stream) {
+  const int rc = check_norm(rows, dim, 1, in_dtype, x_stride, dim);
+  if (rc) return rc;
+  if (res_dtype != S6_F32 && res_dtype != in_dtype) return S6_ERR_DTYPE;
+  if (rows == 0) return S6_OK;
+  if (!x || !weight || !out || !out_scale || !residual_out) return S6_ERR_NULL;
+  const size_t esz = in_dtype == S6_BF16 ? 2 : 4, rsz = res_dtype == S6_BF16 ? 2 : 4;
+  if (!aligned(x, esz) || !aligned(out_scale, 4) || !aligned(residual, rsz) || !aligned(residual_out, rsz) ||
+      !aligned(weight, 4) || !aligned(gamma, 4))
+    return S6_ERR_ALIGN;
+  const bool vec = dim % 8 == 0 && row_vec(x, x_stride, esz) && aligned(out, 8) && aligned(residual, 16) &&
+                   aligned(residual_out, 16) && aligned(weight, 16) && aligned(gamma, 16);
+  NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.rows = rows; a.dim = dim; a.gd = dim; a.a = x; a.a_stride = x_stride; a.b = residual; a.w = weight; a.gamma = gamma;
+  a.scale = scale; a.eps = eps; a.o1 = out; a.o2 = residual_out; a.row_scale = out_scale;
+  const NormPlan p = norm_plan(rows, dim, vec, false);
+  const dim3 grid((unsigned)p.blocks);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (in_dtype == S6_F32) S6_LAUNCH_NORM(s6_add_norm_q8_kernel, float, float);
+  else if (res_dtype == S6_F32) S6_LAUNCH_NORM(s6_add_norm_q8_kernel, uint16_t, float);
+  else S6_LAUNCH_NORM(s6_add_norm_q8_kernel, uint16_t, uint16_t);
   return S6_OK;
 }
 

@@ -1,0 +1,130 @@
+"""Python binding of the projections in few bits (include/s6_q4.h): products
+with 4-bit weights and group scales, their packing, and the norm before a
+block with an 8-bit output.
+
+As in ``block``: argument marshalling only, torch device tensors in and out,
+work enqueued on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import s6
+from .block import _at, _dtype, _flat, _launch, _need, _same_device, _weight, _whole, _workspace, _written
+from .s6 import _DT
+
+S6_E4M3 = 2
+GROUPS = (32, 64, 128)
+_XT = {**_DT, torch.float8_e4m3fn: S6_E4M3}
+
+_lib = None
+
+
+def _load():
+    global _lib
+    if _lib is None:
+        lib = s6.load_library()
+        i64, vp, i32, f32, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        for name, args in {
+            "s6_q4_pack": [i64, i64, i64, i32, vp, i64, vp, vp, vp],
+            "s6_q4_linear": [i64, i64, i64, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp, sz, vp],
+            "s6_q4_linear_workspace_size": [i64, i64, i64, i64, i32, ctypes.POINTER(sz)],
+            "s6_add_norm_q8_fwd": [i64, i64, i32, i32, vp, i64, vp, vp, vp, f32, f32, vp, vp, vp, vp],
+        }.items():
+            fn = getattr(lib, name)
+            fn.restype = i32
+            fn.argtypes = args
+        _lib = lib
+    return _lib
+
+
+def q4_pack(w, group=128):
+    """4-bit codes and group scales of w (outer, inner) in float32 or bfloat16
+    (rows may be slices of wider ones): (weight, scales), uint8 (outer, inner /
+    2) and bfloat16 (outer, inner / group).  group: 32, 64 or 128, a divisor of
+    inner."""
+    dt = _dtype(w, "w")
+    if w.dim() != 2:
+        raise ValueError("w is (outer, inner)")
+    outer, inner = w.shape
+    if group not in GROUPS or inner % group or inner == 0:
+        raise ValueError(f"groups of {group} columns: expected 32, 64 or 128, a divisor of {inner}")
+    stride = _flat(w, "w", w.shape, dt)
+    weight = torch.empty((outer, inner // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((outer, inner // group), dtype=torch.bfloat16, device=w.device)
+    _launch(_load().s6_q4_pack, w, outer, inner, group, _DT[dt], _at(w), stride, _at(weight), _at(scales))
+    return weight, scales
+
+
+def q4_linear(x, weight, scales, x_scale=None, out_dtype=None, y=None):
+    """x W^T for 4-bit weights as q4_pack leaves them.  x: (..., inner) in
+    float32, bfloat16, or float8_e4m3fn with one fp32 factor per row in
+    x_scale (...), as add_norm_q8_fwd leaves them; x may be a slice of wider
+    rows.  Returns (..., outer) in out_dtype, float32 or bfloat16 (unless
+    given: x's, bfloat16 for 8-bit rows)."""
+    dt = x.dtype
+    if dt not in _XT:
+        raise ValueError(f"unsupported x dtype {dt}")
+    yt = out_dtype or (torch.bfloat16 if dt == torch.float8_e4m3fn else dt)
+    if yt not in _DT:
+        raise ValueError(f"unsupported out_dtype {yt}")
+    if weight.dim() != 2 or scales.dim() != 2 or x.dim() < 1:
+        raise ValueError("x is (..., inner), weight (outer, inner / 2), scales (outer, inner / group)")
+    inner, outer, ngroups = x.shape[-1], weight.shape[0], scales.shape[1]
+    if ngroups == 0 or inner % ngroups or inner // ngroups not in GROUPS:
+        raise ValueError(f"{ngroups} scales for {inner} columns: groups have 32, 64 or 128")
+    lead = x.shape[:-1]
+    stride = _flat(x, "x", x.shape, dt)
+    _whole(weight, "weight", (outer, inner // 2), torch.uint8)
+    _whole(scales, "scales", (outer, ngroups), torch.bfloat16)
+    if x_scale is not None:
+        if dt != torch.float8_e4m3fn:
+            raise ValueError("x_scale goes with 8-bit rows")
+        _whole(x_scale, "x_scale", lead)
+    _whole(y, "y", (*lead, outer), yt)
+    _same_device(x, weight, scales, x_scale, y)
+    _written(y)
+    if y is None:
+        y = torch.empty((*lead, outer), dtype=yt, device=x.device)
+    lib = _load()
+    rows = math.prod(lead)
+    args = (rows, inner, outer, inner // ngroups, _XT[dt])
+    keep, wsp, wsn = _workspace(lib.s6_q4_linear_workspace_size, x, *args)
+    _launch(lib.s6_q4_linear, x, *args, _DT[yt], _at(x), stride, _at(x_scale), _at(weight), _at(scales), _at(y), wsp, wsn)
+    del keep
+    return y
+
+
+def add_norm_q8_fwd(x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5, residual_dtype=None, out=None,
+                    out_scale=None, residual_out=None):
+    """block.add_norm_fwd with its output in 8 bits: per row of the last
+    dimension, r' = residual + scale * gamma * x, o = r' / sqrt(mean(r'^2) +
+    eps) * weight, out_scale = max|o| / 448, out = o / out_scale.  Returns
+    (out in float8_e4m3fn, out_scale (...) fp32, r' in the residual's dtype);
+    residual_out may be the residual itself."""
+    dt = _dtype(x)
+    stride = _flat(x, "x", x.shape, dt)
+    rt = residual.dtype if residual is not None else residual_dtype or torch.float32
+    if rt not in (torch.float32, dt):
+        raise ValueError(f"residual dtype {rt}: expected float32 or {dt}")
+    dim, lead = x.shape[-1], x.shape[:-1]
+    _whole(residual, "residual", x.shape, rt)
+    _weight(weight, dim)
+    _whole(gamma, "gamma", (dim,))
+    _whole(out, "out", x.shape, torch.float8_e4m3fn)
+    _whole(out_scale, "out_scale", lead)
+    _whole(residual_out, "residual_out", x.shape, rt)
+    _same_device(x, weight, residual, gamma, out, out_scale, residual_out)
+    _written(out, out_scale, residual_out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    if out_scale is None:
+        out_scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=rt, device=x.device)
+    _launch(_load().s6_add_norm_q8_fwd, x, math.prod(lead), dim, _DT[dt], _DT[rt], _at(x), stride, _at(residual),
+            _at(weight), _at(gamma), scale, eps, _at(out), _at(out_scale), _at(residual_out))
+    return out, out_scale, residual_out
