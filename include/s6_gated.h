@@ -24,7 +24,9 @@
  * strides (elements) are given, the rows themselves are contiguous.  Every
  * other tensor is contiguous.  in_dtype is that of x, the gates, y, dy and the
  * gradients of x and the gates; all else is fp32.
- * batch, seqlen and dim may be 0 (no work; h_last is then h0 or zeros).
+ * batch, seqlen and dim may be 0 (no work; h_last is then h0 or zeros).  dim
+ * and the token strides are at most 2^24, and there are fewer than about 2^31
+ * tiles of 128 tokens by 64 channels.
  *
  * Arithmetic: gates, decays, states, adjoints and sums in fp32; y and the
  * gradients in in_dtype meet one rounding, that of the result.  1 - a^2 keeps

@@ -30,7 +30,10 @@ namespace {
 constexpr int kGC = 64;                // channels of a tile
 constexpr int kGT = S6_GATED_TOKENS;   // tokens of a tile
 constexpr int kWaves = 8;              // waves of a workgroup
-constexpr int64_t kMaxTiles = 1 << 22; // workgroups of a launch (threads below 2^32)
+constexpr int kMaxTiles = 1 << 22; // workgroups of a launch (threads below 2^32)
+constexpr int kFwdWaves = 6, kBwdWaves = 4;  // waves per SIMD that the registers leave room for
+constexpr int kClasses = 64;           // counters of tiles, each in a line of its own
+constexpr int kTicketStep = 32;        // words from one to the next
 
 struct GatedArgs {
   const void* x; const void* ga; const void* gx;
@@ -44,11 +47,13 @@ struct GatedArgs {
   const void* dy; void* dx; void* dga; void* dgx;
   float* parts;          // column sums' parts (tiles, 3, kGC), nullable
   uint64_t* slots;       // (cols, chunks, kGC), null where a sequence is one tile
-  unsigned long long* ticket;
-  int64_t batch, L, dim;
+  uint32_t* ticket;
+  int64_t L;
   int64_t x_batch, x_token, a_batch, a_token, g_batch, g_token;
-  int64_t cblocks, cols, chunks, tiles;
-  int64_t base;          // first tile of the launch (one tile per sequence)
+  int dim;
+  int cblocks, cols, chunks, tiles;
+  int classes;           // counters in use
+  int base;              // first workgroup of the launch
   int unit;
 };
 
@@ -56,7 +61,8 @@ struct GatedArgs {
 // A tile's word: {P, H} of the tile, {kState, s} once the state s after the
 // tile is known, or kEmpty (both halves written at once).
 constexpr uint32_t kEmpty = 0xffffffffu, kState = 0xfffffffeu;
-constexpr int kWindow = 16;     // tiles looked at together
+constexpr int kBatch = 8;       // tiles looked at together
+constexpr int kStash = 32;      // tiles whose maps are kept on the way to a known state
 constexpr int kMaxPolls = 1 << 21;
 
 __device__ __forceinline__ uint64_t word(uint32_t lo, float h) {
@@ -79,33 +85,44 @@ __device__ __forceinline__ float pass(float P, float H, float h) {
 
 // The state entering tile q > 0 for this lane's channel (whole waves call it).
 // slot: the lane's word of this tile; the tile before it is kGC words lower.
-__device__ float look_back(uint64_t* slot, int64_t q) {
-  const int n = q < kWindow ? (int)q : kWindow;
+// w0: that one's word, as seen some time ago.  Goes back over maps, kept in
+// stash, to the first tile whose state is known, and forward from there.
+__device__ __forceinline__ float look_back(const uint64_t* slot, int64_t q, uint64_t w0, uint64_t (*stash)[kGC]) {
+  if (__ballot(low(w0) == kState) == ~0ull) return high(w0);
+  const int lane = threadIdx.x & 63;
+  int done = 0;  // maps in the stash: tiles q - 1 to q - done
   for (int polls = 0; polls < kMaxPolls; ++polls) {
-    const uint64_t w0 = peek(slot - kGC);
-    if (__ballot(low(w0) == kState) == ~0ull) return high(w0);
-    uint64_t w[kWindow];
-    w[0] = w0;
+    uint64_t w[kBatch];
 #pragma unroll
-    for (int i = 1; i < kWindow; ++i) w[i] = i < n ? peek(slot - (int64_t)(i + 1) * kGC) : ~0ull;
-    int found = -1;
-    bool go = true;
+    for (int i = 0; i < kBatch; ++i) w[i] = done + i < q ? peek(slot - (int64_t)(done + i + 1) * kGC) : ~0ull;
+    int step = 0;
+    bool found = false;
+    float h = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWindow; ++i) {
+    for (int i = 0; i < kBatch; ++i) {
       const uint64_t state = __ballot(low(w[i]) == kState), none = __ballot(low(w[i]) == kEmpty);
-      if (go && state == ~0ull) found = i;
-      go = go && state == 0 && none == 0;
+      if (step == i && !found) {
+        if (state == ~0ull) {
+          found = true;
+          h = high(w[i]);
+        } else if (state == 0 && none == 0) {
+          stash[done + i][lane] = w[i];
+          step = i + 1;
+        }
+      }
     }
-    if (found >= 0) {
-      float h = 0.0f;
-#pragma unroll
-      for (int i = kWindow - 1; i >= 0; --i) {
-        if (i == found) h = high(w[i]);
-        if (i < found) h = pass(__uint_as_float(low(w[i])), high(w[i]), h);
+    done += step;
+    if (found) {
+#pragma unroll 4
+      for (int i = done - 1; i >= 0; --i) {
+        const uint64_t m = stash[i][lane];
+        h = pass(__uint_as_float(low(m)), high(m), h);
       }
       return h;
     }
-    __builtin_amdgcn_s_sleep(2);
+    // a full stash: the farthest tiles are looked at again until a state is known
+    if (done > kStash - kBatch) done = kStash - kBatch;
+    if (step < kBatch) __builtin_amdgcn_s_sleep(1);
   }
   return __builtin_nanf("");  // not reached: see the file's head
 }
@@ -118,26 +135,51 @@ template <typename In, int VEC>
 struct Piece {
   In e[VEC];
   __device__ __forceinline__ void load(const In* p) {
-    if constexpr (VEC == 1) {
-      e[0] = *p;
-    } else if constexpr (sizeof(In) == 2) {
-      const uint32_t w = *reinterpret_cast<gptr<uint32_t>>(reinterpret_cast<uintptr_t>(p));
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) e[v] = p[v];
+  }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t wave) {
+    if constexpr (sizeof(e) == 8) {
+      const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, lane, wave, 0);
+      __builtin_memcpy(e, &w, 8);
+    } else if constexpr (sizeof(e) == 4) {
+      const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(r, lane, wave, 0);
       __builtin_memcpy(e, &w, 4);
     } else {
-      const float2 w = *reinterpret_cast<const float2*>(p);
-      __builtin_memcpy(e, &w, 8);
+      e[0] = __builtin_amdgcn_raw_buffer_load_b16(r, lane, wave, 0);
     }
   }
   __device__ __forceinline__ float get(int v) const { return to_f32(e[v]); }
+  // What is formed from the values before is formed again after this, instead
+  // of being kept in registers.
+  __device__ __forceinline__ void again() {
+    if constexpr (sizeof(e) == 8) {
+      uint64_t w;
+      __builtin_memcpy(&w, e, 8);
+      asm volatile("" : "+v"(w));
+      __builtin_memcpy(e, &w, 8);
+    } else if constexpr (sizeof(e) == 4) {
+      uint32_t w;
+      __builtin_memcpy(&w, e, 4);
+      asm volatile("" : "+v"(w));
+      __builtin_memcpy(e, &w, 4);
+    } else {
+      asm volatile("" : "+v"(e[0]));
+    }
+  }
 };
+// VEC channels of a token, rounded to In.
 template <typename In, int VEC>
-__device__ __forceinline__ void put(In* p, const float (&f)[VEC]) {
-  if constexpr (VEC == 1)
-    *p = from_f32<In>(f[0]);
-  else if constexpr (sizeof(In) == 2)
-    *reinterpret_cast<uint32_t*>(p) = bf_pack(f[0], f[1]);
+__device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t wave, const float (&f)[VEC]) {
+  typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+  if constexpr (VEC == 2 && sizeof(In) == 4)
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(f[0]), __float_as_uint(f[1])}, r, lane, wave, 0);
+  else if constexpr (VEC == 2)
+    __builtin_amdgcn_raw_buffer_store_b32(bf_pack(f[0], f[1]), r, lane, wave, 0);
+  else if constexpr (sizeof(In) == 4)
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, lane, wave, 0);
   else
-    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+    __builtin_amdgcn_raw_buffer_store_b16(from_f32<In>(f[0]), r, lane, wave, 0);
 }
 
 __device__ __forceinline__ float gate_f(float g, float bias_l2) {  // bias_l2 = -bias log2(e)
@@ -157,63 +199,83 @@ __device__ __forceinline__ float one_less_square(float v2, float a) {
 }
 
 // Where a lane's tokens lie: kWaves * VEC groups of T tokens, VEC groups to a
-// wave (64 / VEC lanes of VEC channels each).
+// wave (64 / VEC lanes of VEC channels each).  Tiles and columns of tiles are
+// counted in 32 bits (the host sees to it).
 template <int VEC>
 struct Place {
   static constexpr int G = kWaves * VEC, T = kGT / G;
-  int group, cl, nt;        // nt: tokens of the group that exist
-  int64_t col, q, k, b, c, t0;
+  int group, half, cl, nt;  // half: the group in its wave; nt: tokens of the group that exist
+  int col, q, k, b, c0;     // c0: first channel of the tile
+  int64_t w0;               // first token of the wave
   bool on;                  // the lane's channels exist
 };
 template <int VEC, bool BACK>
-__device__ __forceinline__ Place<VEC> place_of(const GatedArgs& a, int64_t tile) {
+__device__ __forceinline__ Place<VEC> place_of(const GatedArgs& a, int tile) {
   using P = Place<VEC>;
   P p;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int half = VEC == 2 ? lane >> 5 : 0;
+  p.half = VEC == 2 ? lane >> 5 : 0;
   p.cl = (VEC == 2 ? lane & 31 : lane) * VEC;
-  p.group = wave * VEC + half;
+  p.group = wave * VEC + p.half;
   p.q = tile / a.cols;
   p.col = tile - p.q * a.cols;
   p.k = BACK ? a.chunks - 1 - p.q : p.q;
   p.b = p.col / a.cblocks;
-  p.c = (p.col - p.b * a.cblocks) * kGC + p.cl;
-  p.on = p.c < a.dim;
-  p.t0 = p.k * kGT + p.group * P::T;
-  const int64_t left = a.L - p.t0;
+  p.c0 = (p.col - p.b * a.cblocks) * kGC;
+  p.on = p.c0 + p.cl < a.dim;
+  p.w0 = (int64_t)p.k * kGT + wave * (VEC * P::T);
+  const int64_t left = a.L - p.w0 - p.half * P::T;
   p.nt = left < 0 ? 0 : left < P::T ? (int)left : P::T;
   return p;
 }
 
-// The tile of this workgroup.
-__device__ __forceinline__ int64_t draw_tile(const GatedArgs& a, unsigned long long* shared) {
-  if (!a.slots) return a.base + blockIdx.x;
-  if (threadIdx.x == 0) *shared = atomicAdd(a.ticket, 1ull);
+// The tile of this workgroup, or a.tiles or more: none is left.  Columns (of
+// tiles along a sequence) are dealt to kClasses counters, so that a tile and
+// those before it come from one counter, in order: one counter for all took
+// 11 ns a tile.
+__device__ __forceinline__ int draw_tile(const GatedArgs& a, uint32_t* shared) {
+  const int wg = a.base + (int)blockIdx.x;
+  if (!a.slots) return wg;
+  const int c = wg % a.classes;
+  if (threadIdx.x == 0) *shared = atomicAdd(a.ticket + c * kTicketStep, 1u);
   __syncthreads();
-  const uint64_t t = *shared;
-  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(t >> 32)) << 32 |
-                   (uint32_t)__builtin_amdgcn_readfirstlane((int)t));
+  const int n = __builtin_amdgcn_readfirstlane((int)*shared);
+  const int mine = (a.cols - c + a.classes - 1) / a.classes;  // the class's columns: c, c + classes, ...
+  const int q = n / mine;
+  return q < a.chunks ? q * a.cols + (n - q * mine) * a.classes + c : a.tiles;
 }
 
-// A group's rows of one input.  Lanes past dim take the last channels again,
-// tokens past the end the last token again.
+// A wave's part of one tensor as a buffer: its tokens of the tile's channels.
+// Past its end loads return 0 and stores are dropped, so that tiles need no
+// branches at the end of a sequence; a lane past dim may load what lies beside
+// the row, and stores nothing.  A tensor that is not given is an empty buffer:
+// without gate_x the gate is 0 with a bias of infinity, which makes i = 1.
+struct Rows {
+  __amdgpu_buffer_rsrc_t buf;
+  uint32_t lane, step;  // bytes: of the lane's first piece, from token to token
+};
 template <typename In, int VEC>
-__device__ __forceinline__ void load_rows(Piece<In, VEC> (&o)[Place<VEC>::T], const void* base, int64_t batch_stride,
-                                          int64_t token_stride, const GatedArgs& a, const Place<VEC>& p, bool whole) {
-  constexpr int T = Place<VEC>::T;
-  const int64_t c = p.on ? p.c : a.dim - VEC;
-  const In* row = static_cast<const In*>(base) + p.b * batch_stride + c;
-  if (whole) {
-    const In* r = row + p.t0 * token_stride;
+__device__ __forceinline__ Rows rows_of(const void* base, int64_t batch_stride, int64_t token_stride, const GatedArgs& a,
+                                        const Place<VEC>& p) {
+  constexpr int n = VEC * Place<VEC>::T;
+  const int64_t left = a.L - p.w0;
+  const uint32_t rows = left < 0 || !base ? 0 : left < n ? (uint32_t)left : n;
+  const uint32_t cols = a.dim - p.c0 < kGC ? (uint32_t)(a.dim - p.c0) : kGC;
+  const uint64_t u = reinterpret_cast<uint64_t>(static_cast<const In*>(base) + p.b * batch_stride + p.w0 * token_stride + p.c0);
+  const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
+                      (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
+  Rows r;
+  r.step = (uint32_t)token_stride * (uint32_t)sizeof(In);
+  r.buf = __builtin_amdgcn_make_buffer_rsrc(
+      reinterpret_cast<void*>(at), 0,
+      __builtin_amdgcn_readfirstlane(rows > 0 ? (rows - 1) * r.step + cols * (uint32_t)sizeof(In) : 0u), 0x00027000);
+  r.lane = p.half * (Place<VEC>::T * r.step) + p.cl * (uint32_t)sizeof(In);
+  return r;
+}
+template <typename In, int VEC>
+__device__ __forceinline__ void load_rows(Piece<In, VEC> (&o)[Place<VEC>::T], const Rows& r) {
 #pragma unroll
-    for (int t = 0; t < T; ++t) o[t].load(r + t * token_stride);
-  } else {
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const int64_t at = p.t0 + t < a.L ? p.t0 + t : a.L - 1;
-      o[t].load(row + at * token_stride);
-    }
-  }
+  for (int t = 0; t < Place<VEC>::T; ++t) o[t].load(r.buf, r.lane, t * r.step);
 }
 
 // Bit t: token t of the lane's group starts a sequence.
@@ -221,39 +283,44 @@ template <int VEC>
 __device__ __forceinline__ uint32_t starts_of(const GatedArgs& a, const Place<VEC>& p) {
   constexpr int T = Place<VEC>::T;
   const int lane = threadIdx.x & 63, t = lane & (T - 1);
-  const uint64_t all = __ballot(t < p.nt && a.starts[p.b * a.L + p.t0 + (t < p.nt ? t : 0)] != 0);
+  bool st = false;
+  if (t < p.nt) st = a.starts[p.b * a.L + p.w0 + p.half * T + t] != 0;
+  const uint64_t all = __ballot(st);
   return (uint32_t)(VEC == 2 && lane >= 32 ? all >> 32 : all) & ((1u << T) - 1);
 }
 
 // --------------------------------------------------------------- forward --
 template <typename In, int VEC, bool UNIT, bool STARTS>
-__global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_kernel(GatedArgs a) {
+__global__ __launch_bounds__(kWaves * 64, kFwdWaves) void s6_gated_scan_kernel(GatedArgs a) {
   using P = Place<VEC>;
   constexpr int G = P::G, T = P::T;
   __shared__ float2 agg[G][kGC];
   __shared__ float hin[G][kGC];
-  __shared__ unsigned long long drawn;
-  const int64_t tile = draw_tile(a, &drawn);
+  __shared__ uint64_t stash[kStash][kGC];
+  __shared__ uint32_t drawn;
+  const int tile = draw_tile(a, &drawn);
   if (tile >= a.tiles) return;
   const P p = place_of<VEC, false>(a, tile);
-  const bool whole = (p.k + 1) * kGT <= a.L;
+  uint64_t* const slot = a.slots + ((int64_t)p.col * a.chunks + p.q) * kGC + (threadIdx.x & 63);
+  const uint64_t before = p.q > 0 && threadIdx.x < 64 ? peek(slot - kGC) : ~0ull;
   Piece<In, VEC> xr[T], ar[T], gr[T];
-  load_rows<In, VEC>(ar, a.ga, a.a_batch, a.a_token, a, p, whole);
-  load_rows<In, VEC>(xr, a.x, a.x_batch, a.x_token, a, p, whole);
-  if (a.gx) load_rows<In, VEC>(gr, a.gx, a.g_batch, a.g_token, a, p, whole);
+  load_rows<In, VEC>(ar, rows_of<In, VEC>(a.ga, a.a_batch, a.a_token, a, p));
+  load_rows<In, VEC>(xr, rows_of<In, VEC>(a.x, a.x_batch, a.x_token, a, p));
+  load_rows<In, VEC>(gr, rows_of<In, VEC>(a.gx, a.g_batch, a.g_token, a, p));
   uint32_t starts = 0;
-  if constexpr (STARTS) starts = p.nt > 0 ? starts_of<VEC>(a, p) : 0;
+  if constexpr (STARTS) starts = starts_of<VEC>(a, p);
   float A2[VEC], ba[VEC], bx[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
-    const int64_t c = (p.on ? p.c : a.dim - VEC) + v;
+    const int c = p.on ? p.c0 + p.cl + v : a.dim - 1;
     A2[v] = a.A[c] * kLog2e;
     ba[v] = a.ba ? -a.ba[c] * kLog2e : 0.0f;
-    bx[v] = a.bx ? -a.bx[c] * kLog2e : 0.0f;
+    bx[v] = !a.gx ? -__builtin_inff() : a.bx ? -a.bx[c] * kLog2e : 0.0f;
   }
   float av[T][VEC], uv[T][VEC], Pl[VEC], Hl[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) { Pl[v] = 1.0f; Hl[v] = 0.0f; }
+  // (tokens past the end make the last tile's map meaningless: nobody reads it)
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     const bool st = STARTS && (starts >> t & 1);
@@ -261,13 +328,11 @@ __global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_kernel(GatedArgs a)
     for (int v = 0; v < VEC; ++v) {
       const float v2 = A2[v] * gate_f(ar[t].get(v), ba[v]);
       float d = fast_exp2(v2);
-      float u = xr[t].get(v);
-      if (a.gx) u *= gate_f(gr[t].get(v), bx[v]);
+      float u = xr[t].get(v) * gate_f(gr[t].get(v), bx[v]);
       if constexpr (!UNIT) {
         const float b = __builtin_amdgcn_sqrtf(one_less_square(v2, d));
         u = st ? u : b * u;
       }
-      if (!whole && t >= p.nt) { d = 1.0f; u = 0.0f; }
       av[t][v] = d;
       uv[t][v] = u;
       if constexpr (STARTS) {
@@ -284,100 +349,113 @@ __global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_kernel(GatedArgs a)
   for (int v = 0; v < VEC; ++v) agg[p.group][p.cl + v] = make_float2(Pl[v], Hl[v]);
   __syncthreads();
   if (threadIdx.x < 64) {  // the first wave: one channel per lane
-    const int lane = threadIdx.x;
-    const int64_t c = p.c - p.cl + lane;
+    const int lane = threadIdx.x, c = p.c0 + lane;
     float Pt = 1.0f, Ht = 0.0f;
-    float2 g[G];
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < G; ++i) {
-      g[i] = agg[i][lane];
-      Ht = pass(g[i].x, g[i].y, Ht);
-      Pt = (STARTS && __float_as_uint(g[i].x) >> 31) ? g[i].x : g[i].x * Pt;
+      const float2 g = agg[i][lane];
+      Ht = pass(g.x, g.y, Ht);
+      Pt = (STARTS && __float_as_uint(g.x) >> 31) ? g.x : g.x * Pt;
     }
-    uint64_t* slot = a.slots ? a.slots + (p.col * a.chunks + p.q) * kGC + lane : nullptr;
     float h;
     if (p.q == 0) {
-      h = a.first && c < a.dim ? a.first[p.b * a.dim + c] : 0.0f;
+      h = a.first && c < a.dim ? a.first[(int64_t)p.b * a.dim + c] : 0.0f;
     } else {
       post(slot, word(publishable(Pt), Ht));
-      h = look_back(slot, p.q);
+      h = look_back(slot, p.q, before, stash);
     }
     if (p.q + 1 < a.chunks) post(slot, word(kState, pass(Pt, Ht, h)));
-    if (a.states_out && c < a.dim) a.states_out[(p.b * a.chunks + p.k) * a.dim + c] = h;
-#pragma unroll
+    if (a.states_out && c < a.dim) a.states_out[((int64_t)p.b * a.chunks + p.k) * a.dim + c] = h;
+#pragma unroll 4
     for (int i = 0; i < G; ++i) {
+      const float2 g = agg[i][lane];
       hin[i][lane] = h;
-      h = pass(g[i].x, g[i].y, h);
+      h = pass(g.x, g.y, h);
     }
   }
   __syncthreads();
-  if (!a.y) return;
+  if (!a.y || !p.on) return;
   float h[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) h[v] = hin[p.group][p.cl + v];
-  In* y = static_cast<In*>(a.y) + (p.b * a.L + p.t0) * a.dim + p.c;
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
+  auto next = [&](int t) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v)
       h[v] = STARTS && (starts >> t & 1) ? uv[t][v] : __builtin_fmaf(av[t][v], h[v], uv[t][v]);
-    if (p.on && (whole || t < p.nt)) put<In, VEC>(y + t * a.dim, h);
-  }
-  if (a.last && p.k + 1 == a.chunks && p.group == G - 1 && p.on)
+  };
+  if (a.last && p.k + 1 == a.chunks) {  // the state after the last token
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) a.last[p.b * a.dim + p.c + v] = h[v];
+    for (int t = 0; t < T; ++t) {
+      next(t);
+      if (p.w0 + p.half * T + t + 1 == a.L) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) a.last[(int64_t)p.b * a.dim + p.c0 + p.cl + v] = h[v];
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = hin[p.group][p.cl + v];
+  }
+  const Rows y = rows_of<In, VEC>(a.y, a.L * a.dim, a.dim, a, p);
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    next(t);
+    put<In, VEC>(y.buf, y.lane, t * y.step, h);
+  }
 }
 
 // -------------------------------------------------------------- backward --
 template <typename In, int VEC, bool UNIT, bool STARTS>
-__global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_bwd_kernel(GatedArgs a) {
+__global__ __launch_bounds__(kWaves * 64, kBwdWaves) void s6_gated_scan_bwd_kernel(GatedArgs a) {
   using P = Place<VEC>;
   constexpr int G = P::G, T = P::T;
   __shared__ float agg[3][G][kGC];   // P, H, M of the groups; later the column sums
   __shared__ float ent[2][G][kGC];   // the state entering a group, the adjoint leaving it
-  __shared__ unsigned long long drawn;
-  const int64_t tile = draw_tile(a, &drawn);
+  __shared__ uint64_t stash[kStash][kGC];
+  __shared__ uint32_t drawn;
+  const int tile = draw_tile(a, &drawn);
   if (tile >= a.tiles) return;
   const P p = place_of<VEC, true>(a, tile);
-  const bool whole = (p.k + 1) * kGT <= a.L;
+  uint64_t* const slot = a.slots + ((int64_t)p.col * a.chunks + p.q) * kGC + (threadIdx.x & 63);
+  const uint64_t before = p.q > 0 && threadIdx.x < 64 ? peek(slot - kGC) : ~0ull;
   Piece<In, VEC> xr[T], ar[T], gr[T], yr[T];
-  load_rows<In, VEC>(ar, a.ga, a.a_batch, a.a_token, a, p, whole);
-  load_rows<In, VEC>(yr, a.dy, a.L * a.dim, a.dim, a, p, whole);
-  load_rows<In, VEC>(xr, a.x, a.x_batch, a.x_token, a, p, whole);
-  if (a.gx) load_rows<In, VEC>(gr, a.gx, a.g_batch, a.g_token, a, p, whole);
+  load_rows<In, VEC>(ar, rows_of<In, VEC>(a.ga, a.a_batch, a.a_token, a, p));
+  load_rows<In, VEC>(xr, rows_of<In, VEC>(a.x, a.x_batch, a.x_token, a, p));
+  load_rows<In, VEC>(gr, rows_of<In, VEC>(a.gx, a.g_batch, a.g_token, a, p));
+  load_rows<In, VEC>(yr, rows_of<In, VEC>(a.dy, a.L * a.dim, a.dim, a, p));
   uint32_t starts = 0;
-  if constexpr (STARTS) starts = p.nt > 0 ? starts_of<VEC>(a, p) : 0;
+  if constexpr (STARTS) starts = starts_of<VEC>(a, p);
   float Ac[VEC], ba[VEC], bx[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
-    const int64_t c = (p.on ? p.c : a.dim - VEC) + v;
+    const int c = p.on ? p.c0 + p.cl + v : a.dim - 1;
     Ac[v] = a.A[c];
     ba[v] = a.ba ? -a.ba[c] * kLog2e : 0.0f;
-    bx[v] = a.bx ? -a.bx[c] * kLog2e : 0.0f;
+    bx[v] = !a.gx ? -__builtin_inff() : a.bx ? -a.bx[c] * kLog2e : 0.0f;
   }
-  // the gates, decays and input factors, and the group's map of the state
-  float av[T][VEC], rv[T][VEC], iv[T][VEC], bv[T][VEC];
+  // the gates, decays and inputs, and the group's maps
+  float av[T][VEC], rv[T][VEC], iv[T][VEC], uv[T][VEC];
   float Pl[VEC], Hl[VEC], Ml[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) { Pl[v] = 1.0f; Hl[v] = Ml[v] = 0.0f; }
+  // (a token past the end, with a = 1 and dy = 0, hands the adjoint on)
 #pragma unroll
   for (int t = 0; t < T; ++t) {
-    const bool st = STARTS && (starts >> t & 1), none = !whole && t >= p.nt;
+    const bool st = STARTS && (starts >> t & 1);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
       rv[t][v] = gate_f(ar[t].get(v), ba[v]);
-      iv[t][v] = a.gx ? gate_f(gr[t].get(v), bx[v]) : 1.0f;
+      iv[t][v] = gate_f(gr[t].get(v), bx[v]);
       const float v2 = Ac[v] * kLog2e * rv[t][v];
       float d = fast_exp2(v2);
-      bv[t][v] = 1.0f;
+      float u = iv[t][v] * xr[t].get(v);
       if constexpr (!UNIT) {
-        const float s = one_less_square(v2, d);
-        bv[t][v] = st ? 1.0f : __builtin_amdgcn_sqrtf(s);
+        const float b = __builtin_amdgcn_sqrtf(one_less_square(v2, d));
+        u = st ? u : b * u;
       }
-      float u = bv[t][v] * iv[t][v] * xr[t].get(v);
-      if (none) { d = 1.0f; u = 0.0f; }
+      if (t >= p.nt) d = 1.0f;
       if constexpr (STARTS) d = __builtin_fabsf(d);
       av[t][v] = d;
+      uv[t][v] = u;
       if constexpr (STARTS) {
         Pl[v] = st ? -0.0f : Pl[v] * d;
         Hl[v] = st ? u : __builtin_fmaf(d, Hl[v], u);
@@ -389,10 +467,10 @@ __global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_bwd_kernel(GatedArg
   }
 #pragma unroll
   for (int t = T - 1; t >= 0; --t) {
-    const bool st = STARTS && (starts >> t & 1), none = !whole && t >= p.nt;
+    const bool st = STARTS && (starts >> t & 1);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      const float m = av[t][v] * ((none ? 0.0f : yr[t].get(v)) + Ml[v]);
+      const float m = av[t][v] * (yr[t].get(v) + Ml[v]);
       Ml[v] = st ? 0.0f : m;
     }
   }
@@ -404,43 +482,41 @@ __global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_bwd_kernel(GatedArg
   }
   __syncthreads();
   if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    const int64_t c = p.c - p.cl + lane;
+    const int lane = threadIdx.x, c = p.c0 + lane;
     const bool on = c < a.dim;
-    float gp[G], gm[G];
-    float h = on ? a.states[(p.b * a.chunks + p.k) * a.dim + c] : 0.0f;
+    float h = on ? a.states[((int64_t)p.b * a.chunks + p.k) * a.dim + c] : 0.0f;
     float Pt = 1.0f, Mt = 0.0f;
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < G; ++i) {
-      gp[i] = agg[0][i][lane];
-      gm[i] = agg[2][i][lane];
       ent[0][i][lane] = h;
-      h = pass(gp[i], agg[1][i][lane], h);
+      h = pass(agg[0][i][lane], agg[1][i][lane], h);
     }
-#pragma unroll
+#pragma unroll 4
     for (int i = G - 1; i >= 0; --i) {
-      Mt = pass(gp[i], gm[i], Mt);
-      Pt = (STARTS && __float_as_uint(gp[i]) >> 31) ? gp[i] : gp[i] * Pt;
+      const float gp = agg[0][i][lane];
+      Mt = pass(gp, agg[2][i][lane], Mt);
+      Pt = (STARTS && __float_as_uint(gp) >> 31) ? gp : gp * Pt;
     }
-    uint64_t* slot = a.slots ? a.slots + (p.col * a.chunks + p.q) * kGC + lane : nullptr;
     float m;
     if (p.q == 0) {
-      m = a.first && on ? a.first[p.b * a.dim + c] : 0.0f;
+      m = a.first && on ? a.first[(int64_t)p.b * a.dim + c] : 0.0f;
     } else {
       post(slot, word(publishable(Pt), Mt));
-      m = look_back(slot, p.q);
+      m = look_back(slot, p.q, before, stash);
     }
     if (p.q + 1 < a.chunks) post(slot, word(kState, pass(Pt, Mt, m)));
-#pragma unroll
+#pragma unroll 4
     for (int i = G - 1; i >= 0; --i) {
       ent[1][i][lane] = m;
-      m = pass(gp[i], gm[i], m);
+      m = pass(agg[0][i][lane], agg[2][i][lane], m);
     }
-    if (a.last && p.q + 1 == a.chunks && on) a.last[p.b * a.dim + c] = m;
+    if (a.last && p.q + 1 == a.chunks && on) a.last[(int64_t)p.b * a.dim + c] = m;
   }
   __syncthreads();
-  // the state before each token, then backwards with the adjoint
-  float hp[T][VEC], h[VEC], m[VEC], sA[VEC], sa[VEC], sx[VEC];
+  // The state before each token (in place of the inputs), then backwards with
+  // the adjoint.  b is formed again from r and a: kept beside the rest it
+  // would cost half of the waves.
+  float h[VEC], m[VEC], sA[VEC], sa[VEC], sx[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
     h[v] = ent[0][p.group][p.cl + v];
@@ -448,40 +524,49 @@ __global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_bwd_kernel(GatedArg
     sA[v] = sa[v] = sx[v] = 0.0f;
   }
 #pragma unroll
-  for (int t = 0; t < T; ++t)
+  for (int t = 0; t < T; ++t) {
+    xr[t].again();
+    yr[t].again();
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      hp[t][v] = h[v];
-      const float u = bv[t][v] * iv[t][v] * xr[t].get(v);
+      const float u = uv[t][v];
+      uv[t][v] = h[v];
       h[v] = STARTS && (starts >> t & 1) ? u : __builtin_fmaf(av[t][v], h[v], u);
+      asm volatile("" : "+v"(rv[t][v]), "+v"(iv[t][v]));
     }
-  const int64_t at = (p.b * a.L + p.t0) * a.dim + p.c;
-  In* dx = static_cast<In*>(a.dx) + at;
-  In* dga = static_cast<In*>(a.dga) + at;
-  In* dgx = static_cast<In*>(a.dgx) + at;
+  }
+  const Rows dx = rows_of<In, VEC>(a.dx, a.L * a.dim, a.dim, a, p);
+  const Rows dga = rows_of<In, VEC>(a.dga, a.L * a.dim, a.dim, a, p);
+  const Rows dgx = rows_of<In, VEC>(a.dgx, a.L * a.dim, a.dim, a, p);
+  if (p.on) {
 #pragma unroll
-  for (int t = T - 1; t >= 0; --t) {
-    const bool st = STARTS && (starts >> t & 1), none = !whole && t >= p.nt;
-    float ox[VEC], oa[VEC], og[VEC];
+    for (int t = T - 1; t >= 0; --t) {
+      const bool st = STARTS && (starts >> t & 1), none = t >= p.nt;
+      float ox[VEC], oa[VEC], og[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float x = xr[t].get(v), d = av[t][v], r = rv[t][v], i = iv[t][v], b = bv[t][v];
-      const float lam = (none ? 0.0f : yr[t].get(v)) + m[v];
-      m[v] = st ? 0.0f : d * lam;
-      float w = d * hp[t][v];
-      if constexpr (!UNIT) w = __builtin_fmaf(b > 0.0f ? -d * d * fast_rcp(b) : 0.0f, i * x, w);
-      const float dv = st || none ? 0.0f : lam * w;
-      ox[v] = lam * b * i;
-      oa[v] = dv * Ac[v] * r * (1.0f - r);
-      og[v] = ox[v] * x * (1.0f - i);
-      sA[v] = __builtin_fmaf(dv, r, sA[v]);
-      sa[v] += oa[v];
-      sx[v] += none ? 0.0f : og[v];
-    }
-    if (p.on && (whole || t < p.nt)) {
-      put<In, VEC>(dx + t * a.dim, ox);
-      put<In, VEC>(dga + t * a.dim, oa);
-      if (a.gx) put<In, VEC>(dgx + t * a.dim, og);
+      for (int v = 0; v < VEC; ++v) {
+        const float x = xr[t].get(v), d = av[t][v], r = rv[t][v], i = iv[t][v];
+        float lam = yr[t].get(v) + m[v];
+        m[v] = st ? 0.0f : d * lam;
+        lam = none ? 0.0f : lam;
+        float w = d * uv[t][v], bi = i;
+        if constexpr (!UNIT) {
+          const float s = one_less_square(Ac[v] * kLog2e * r, d);
+          const float inv = s >= 0x1p-126f ? __builtin_amdgcn_rsqf(s) : 0.0f;  // 1 / b
+          w = __builtin_fmaf(-d * d * inv, i * x, w);
+          bi = st ? i : s * inv * i;
+        }
+        const float dv = st ? 0.0f : lam * w;
+        ox[v] = lam * bi;
+        oa[v] = dv * (Ac[v] * r) * (1.0f - r);
+        og[v] = ox[v] * x * (1.0f - i);
+        sA[v] = __builtin_fmaf(dv, r, sA[v]);
+        sa[v] += oa[v];
+        sx[v] += og[v];
+      }
+      put<In, VEC>(dx.buf, dx.lane, t * dx.step, ox);
+      put<In, VEC>(dga.buf, dga.lane, t * dga.step, oa);
+      put<In, VEC>(dgx.buf, dgx.lane, t * dgx.step, og);
     }
   }
   if (!a.parts) return;
@@ -498,7 +583,7 @@ __global__ __launch_bounds__(kWaves * 64) void s6_gated_scan_bwd_kernel(GatedArg
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < G; ++i) s += agg[which][i][l];
-    a.parts[((p.col * a.chunks + p.k) * 3 + which) * kGC + l] = s;
+    a.parts[(((int64_t)p.col * a.chunks + p.k) * 3 + which) * kGC + l] = s;
   }
 }
 
@@ -543,18 +628,18 @@ __global__ __launch_bounds__(64) void s6_gated_slices_kernel(SumArgs a, int64_t 
   if (a.out[which] && c < a.dim) a.out[which][c] = s;
 }
 
-// Empty words and a counter at 0.
-__global__ void s6_gated_init_kernel(uint64_t* slots, int64_t n, unsigned long long* ticket) {
-  const int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i0 == 0) *ticket = 0;
-  for (int64_t i = i0; i < n; i += (int64_t)gridDim.x * blockDim.x) slots[i] = ~0ull;
+// Counters at 0 and empty words, two of them per store.
+__global__ __launch_bounds__(256) void s6_gated_init_kernel(u32x4* slots, int64_t pairs, uint32_t* ticket) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < kClasses) ticket[i * kTicketStep] = 0;
+  if (i < pairs) slots[i] = u32x4{kEmpty, kEmpty, kEmpty, kEmpty};
 }
 
 // ------------------------------------------------------------------ step --
 template <typename In, int VEC>
 __global__ __launch_bounds__(256) void s6_gated_step_kernel(GatedArgs a, float* hs) {
   const int64_t per = (a.dim + VEC - 1) / VEC, i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t b = a.base + blockIdx.y;
+  const int64_t b = (int64_t)a.base + blockIdx.y;
   const int64_t c = i0 * VEC;
   if (i0 >= per) return;
   Piece<In, VEC> xr, ar, gr;
@@ -573,11 +658,20 @@ __global__ __launch_bounds__(256) void s6_gated_step_kernel(GatedArgs a, float* 
     if (!a.unit) u *= __builtin_amdgcn_sqrtf(one_less_square(v2, d));
     h[v] = __builtin_fmaf(d, hr.get(v), u);
   }
-  put<float, VEC>(hs + b * a.dim + c, h);
-  put<In, VEC>(static_cast<In*>(a.y) + b * a.dim + c, h);
+  In* y = static_cast<In*>(a.y) + b * a.dim + c;
+  if constexpr (VEC == 2) {
+    *reinterpret_cast<float2*>(hs + b * a.dim + c) = make_float2(h[0], h[1]);
+    if constexpr (sizeof(In) == 2) *reinterpret_cast<uint32_t*>(y) = bf_pack(h[0], h[1]);
+    else *reinterpret_cast<float2*>(y) = make_float2(h[0], h[1]);
+  } else {
+    hs[b * a.dim + c] = h[0];
+    *y = from_f32<In>(h[0]);
+  }
 }
 
 // ------------------------------------------------------------------ host --
+constexpr int64_t kMaxRow = 1 << 24;  // elements from token to token: a wave's 16 tokens in 32 bits
+
 int check_gated(const s6_gated_dims* d, int in_dtype, int flags, bool gx, bool tokens) {
   if (!d) return S6_ERR_NULL;
   if (in_dtype != S6_F32 && in_dtype != S6_BF16) return S6_ERR_DTYPE;
@@ -587,13 +681,16 @@ int check_gated(const s6_gated_dims* d, int in_dtype, int flags, bool gx, bool t
   const int64_t len = tokens && d->seqlen > 0 ? d->seqlen : 1;
   // element counts with headroom for padded tiles and byte sizes
   int64_t t;
-  if (d->dim > (1 << 28) || d->batch > INT32_MAX || !mul_ok(d->batch, d->dim, &t) || !mul_ok(t, 64 * 16, &t) ||
+  if (d->dim > kMaxRow || d->batch > INT32_MAX || !mul_ok(d->batch, d->dim, &t) || !mul_ok(t, 64 * 16, &t) ||
       !mul_ok(t, len + kGT, &t))
+    return S6_ERR_SHAPE;
+  // tiles and workgroups in 32 bits, a class's last tiles included
+  if (!mul_ok(d->batch * ((d->dim + kGC - 1) / kGC) + kClasses, (len + kGT - 1) / kGT, &t) || t > INT32_MAX - kMaxTiles)
     return S6_ERR_SHAPE;
   const int64_t str[] = {d->x_batch, d->x_token, d->a_batch, d->a_token, d->g_batch, d->g_token};
   for (int i = 0; i < (gx ? 6 : 4); ++i) {
     if ((i & 1) && !tokens) continue;
-    if (str[i] < 0) return S6_ERR_SHAPE;
+    if (str[i] < 0 || ((i & 1) && len > 1 && str[i] > kMaxRow)) return S6_ERR_SHAPE;
     if (!mul_ok(str[i], (i & 1) ? len : d->batch, &t) || !mul_ok(t, 16, &t)) return S6_ERR_SHAPE;
   }
   return S6_OK;
@@ -601,7 +698,7 @@ int check_gated(const s6_gated_dims* d, int in_dtype, int flags, bool gx, bool t
 
 struct GatedWs {
   int64_t cblocks, cols, chunks, tiles, slices, per;
-  size_t slots, states, parts, sums, total;  // byte offsets; the counter lies at 0
+  size_t slots, states, parts, sums, total;  // byte offsets; the counters lie at 0
 };
 GatedWs gated_ws(const s6_gated_dims& d, bool back, bool has_states) {
   GatedWs w;
@@ -613,8 +710,8 @@ GatedWs gated_ws(const s6_gated_dims& d, bool back, bool has_states) {
   // column sums: slices of at least 256 parts, at most 64
   w.slices = n / 256 < 1 ? 1 : n / 256 > 64 ? 64 : n / 256;
   w.per = (n + w.slices - 1) / w.slices;
-  w.slots = 256;
-  size_t at = w.chunks > 1 ? 256 + (size_t)w.tiles * kGC * sizeof(uint64_t) : 0;
+  w.slots = kClasses * kTicketStep * sizeof(uint32_t);
+  size_t at = w.chunks > 1 ? w.slots + (size_t)w.tiles * kGC * sizeof(uint64_t) : 0;
   w.states = w.parts = w.sums = 0;
   if (back) {
     w.states = up256(at);
@@ -631,14 +728,19 @@ GatedWs gated_ws(const s6_gated_dims& d, bool back, bool has_states) {
 template <typename In, int VEC>
 int launch_gated(GatedArgs a, bool back, hipStream_t st) {
   if (a.slots) {
-    const int64_t n = a.tiles * kGC;
-    const int64_t blocks = (n + 1023) / 1024;
-    hipLaunchKernelGGL(s6_gated_init_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, a.slots, n,
-                       a.ticket);
-    S6_HIP(hipGetLastError(), "s6_gated_init_kernel launch");
+    // 8 tiles a workgroup
+    for (int64_t t = 0; t < a.tiles; t += (int64_t)8 * kMaxTiles) {
+      const int64_t n = a.tiles - t < (int64_t)8 * kMaxTiles ? a.tiles - t : (int64_t)8 * kMaxTiles;
+      hipLaunchKernelGGL(s6_gated_init_kernel, dim3((unsigned)((n + 7) / 8)), dim3(256), 0, st,
+                         reinterpret_cast<u32x4*>(a.slots + t * kGC), n * (kGC / 2), a.ticket);
+      S6_HIP(hipGetLastError(), "s6_gated_init_kernel launch");
+    }
   }
-  for (a.base = 0; a.base < a.tiles; a.base += kMaxTiles) {
-    const dim3 grid((unsigned)(a.tiles - a.base < kMaxTiles ? a.tiles - a.base : kMaxTiles)), block(kWaves * 64);
+  // a class with one column less leaves workgroups without a tile
+  a.classes = a.cols < kClasses ? a.cols : kClasses;
+  const int wgs = a.slots ? (a.cols + a.classes - 1) / a.classes * a.classes * a.chunks : a.tiles;
+  for (a.base = 0; a.base < wgs; a.base += kMaxTiles) {
+    const dim3 grid((unsigned)(wgs - a.base < kMaxTiles ? wgs - a.base : kMaxTiles)), block(kWaves * 64);
 #define S6_GATED_LAUNCH(UNIT, STARTS)                                                              \
   if (back)                                                                                        \
     hipLaunchKernelGGL((s6_gated_scan_bwd_kernel<In, VEC, UNIT, STARTS>), grid, block, 0, st, a);  \
@@ -663,7 +765,7 @@ GatedArgs gated_args(const s6_gated_dims& d, int flags, const void* x, const voi
   GatedArgs a;
   memset(&a, 0, sizeof(a));
   a.x = x; a.ga = ga; a.gx = gx; a.A = A; a.ba = ba; a.bx = bx;
-  a.batch = d.batch; a.L = d.seqlen; a.dim = d.dim;
+  a.L = d.seqlen; a.dim = (int)d.dim;
   a.x_batch = d.x_batch; a.x_token = d.x_token; a.a_batch = d.a_batch; a.a_token = d.a_token;
   a.g_batch = d.g_batch; a.g_token = d.g_token;
   a.unit = (flags & S6_UNIT_INPUT) != 0;
@@ -723,9 +825,9 @@ int s6_gated_scan_fwd(const s6_gated_dims* d, int in_dtype, int flags, const voi
   }
   GatedArgs a = gated_args(*d, flags, x, gate_a, bias_a, gate_x, bias_x, A);
   a.starts = starts; a.first = h0; a.states_out = states; a.y = y; a.last = h_last;
-  a.cblocks = w.cblocks; a.cols = w.cols; a.chunks = w.chunks; a.tiles = w.tiles;
+  a.cblocks = (int)w.cblocks; a.cols = (int)w.cols; a.chunks = (int)w.chunks; a.tiles = (int)w.tiles;
   if (w.chunks > 1) {
-    a.ticket = static_cast<unsigned long long*>(workspace);
+    a.ticket = static_cast<uint32_t*>(workspace);
     a.slots = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + w.slots);
   }
   const bool vec = pairs_ok(*d, gate_x != nullptr, true, esz, ins, 4);
@@ -769,9 +871,9 @@ int s6_gated_scan_bwd(const s6_gated_dims* d, int in_dtype, int flags, const voi
   char* ws = static_cast<char*>(workspace);
   GatedArgs a = gated_args(*d, flags, x, gate_a, bias_a, gate_x, bias_x, A);
   a.starts = starts;
-  a.cblocks = w.cblocks; a.cols = w.cols; a.chunks = w.chunks; a.tiles = w.tiles;
+  a.cblocks = (int)w.cblocks; a.cols = (int)w.cols; a.chunks = (int)w.chunks; a.tiles = (int)w.tiles;
   if (w.chunks > 1) {
-    a.ticket = reinterpret_cast<unsigned long long*>(ws);
+    a.ticket = reinterpret_cast<uint32_t*>(ws);
     a.slots = reinterpret_cast<uint64_t*>(ws + w.slots);
   }
   const bool vec = pairs_ok(*d, gate_x != nullptr, true, esz, ins, 7);
@@ -821,8 +923,9 @@ int s6_gated_state_update(const s6_gated_dims* d, int in_dtype, int flags, float
   const bool vec = pairs_ok(*d, gate_x != nullptr, false, esz, ins, 4) && aligned(h, 8);
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t per = vec ? (d->dim + 1) / 2 : d->dim;
-  for (a.base = 0; a.base < d->batch; a.base += 65535) {
-    const int64_t rows = d->batch - a.base < 65535 ? d->batch - a.base : 65535;
+  for (int64_t b0 = 0; b0 < d->batch; b0 += 65535) {
+    a.base = (int)b0;
+    const int64_t rows = d->batch - b0 < 65535 ? d->batch - b0 : 65535;
     const dim3 grid((unsigned)((per + 255) / 256), (unsigned)rows);
     if (in_dtype == S6_BF16) {
       if (vec) hipLaunchKernelGGL((s6_gated_step_kernel<uint16_t, 2>), grid, dim3(256), 0, st, a, h);
