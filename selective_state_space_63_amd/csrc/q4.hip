@@ -30,6 +30,8 @@ struct Q4Args {
   int group;      // columns of a scale
   int ngroups;    // inner / group
   int64_t base;   // first tile of weight rows of the launch
+  int64_t slice;  // blocks of columns of a slice
+  float* parts;   // the slices' sums (slices, rows, outer), or null
 };
 
 // Eight codes as bf16.
@@ -49,21 +51,41 @@ __device__ __forceinline__ bf16x8 bytes8(uint32_t lo, uint32_t hi) {
   return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+// A part of a tensor as a buffer of `bytes` from p on: loads past its end
+// return 0.  Offsets are unsigned 32-bit bytes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, uint32_t bytes) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  const uint64_t v = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(v), 0, __builtin_amdgcn_readfirstlane(bytes),
+                                           0x00027000);
+}
+constexpr uint32_t kNowhere = 0xf0000000u;  // an offset past every buffer, also with 32 bytes added
+
 // Eight consecutive values of x as loaded, and as bf16 parts whose sum they are.
 template <typename XT, bool XV>
 struct X8 {
   static constexpr int kParts = sizeof(XT) == 4 ? 3 : 1;
   alignas(16) XT e[8];
-  __device__ __forceinline__ void load(const XT* p) {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     if constexpr (XV && sizeof(XT) == 1) {
-      *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+      __builtin_memcpy(e, &v, 8);
     } else if constexpr (XV) {
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(XT) / 2; ++i)
-        reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
+      for (int i = 0; i < (int)sizeof(XT) / 2; ++i) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off + 16 * i, 0, 0);
+        __builtin_memcpy(reinterpret_cast<char*>(e) + 16 * i, &v, 16);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = p[i];
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(XT) == 4) e[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off + 4 * i, 0, 0));
+        else if constexpr (sizeof(XT) == 2) e[i] = __builtin_amdgcn_raw_buffer_load_b16(r, off + 2 * i, 0, 0);
+        else e[i] = __builtin_amdgcn_raw_buffer_load_b8(r, off + i, 0, 0);
+      }
     }
   }
   __device__ __forceinline__ void get(bf16x8 (&o)[kParts]) const {
@@ -80,9 +102,10 @@ struct X8 {
         o[2][i] = (__bf16)(r - (float)m);
       }
     } else if constexpr (sizeof(XT) == 2) {
-      o[0] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(e));
+      __builtin_memcpy(&o[0], e, 16);
     } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(e);
+      uint2 v;
+      __builtin_memcpy(&v, e, 8);
       o[0] = bytes8(v.x, v.y);
     }
   }
@@ -105,71 +128,113 @@ __device__ __forceinline__ void transpose4(uint32_t (&c)[4]) {
 
 constexpr int kBlk = 128;  // columns of a block: 16 bytes of codes per lane, four matrix instructions
 
-// Few rows.  A workgroup has 16 weight rows and 16 NT rows of x; its W waves
-// take the blocks of columns in turn and add their sums in LDS in a fixed order.  Lane
-// l holds weight row l % 16 (operand), x row l % 16, and the sums of weight
-// rows 4 (l / 16) to + 3.  FINE: groups of 32 or 64 columns: the codes are
-// transposed so that an instruction's 32 columns lie in one group (else its
-// columns are four runs of 8 from the block, all in the block's group).
+// 16 weight rows from n0 on.  Lane l has row l % 16 and, of a block of
+// columns, 32 codes from 32 (l / 16) on.  FINE (groups of 32 or 64): the codes are
+// transposed so that step j's 32 columns, 32 j to + 31, lie in one group; else
+// step j takes columns 8 j to + 7 of each lane's 32, all in the block's group.
+template <bool FINE>
+struct WRows {
+  __amdgpu_buffer_rsrc_t codes, scales;
+  uint32_t code_at, scale_at;
+  int64_t inner;
+  int ngroups, per;  // per: groups of a block
+  __device__ __forceinline__ WRows(const Q4Args& a, int64_t n0) {
+    const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+    const int64_t left = a.outer - n0;
+    const uint32_t rows = left < 0 ? 0 : left < 16 ? (uint32_t)left : 16;
+    const uint32_t row = (uint32_t)(a.inner >> 1);
+    codes = buffer_at(a.codes + n0 * (a.inner >> 1), rows * row);
+    scales = buffer_at(a.scales + n0 * a.ngroups, rows * (uint32_t)a.ngroups * 2);
+    code_at = i * row + 16 * q;
+    scale_at = i * (uint32_t)a.ngroups * 2;
+    inner = a.inner;
+    ngroups = a.ngroups;
+    per = kBlk / a.group;
+  }
+  struct Block {
+    uint32_t c[4];
+    uint32_t s[FINE ? 4 : 1];  // scales of the block's groups (one per step of 32 columns)
+  };
+  // Block b; one past the last is 0.
+  __device__ __forceinline__ void load(Block& o, int64_t b) const {
+    const int q = (threadIdx.x & 63) >> 4;
+    const bool on = b * kBlk + (FINE ? 32 * q : 0) < inner;
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(codes, on ? code_at + (uint32_t)b * 64 : kNowhere, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o.c[j] = v[j];
+    if constexpr (FINE) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t g = (b * 4 + j) * per >> 2;  // group of step j
+        o.s[j] = __builtin_amdgcn_raw_buffer_load_b16(scales, g < ngroups ? scale_at + (uint32_t)g * 2 : kNowhere, 0, 0);
+      }
+    } else {
+      o.s[0] = __builtin_amdgcn_raw_buffer_load_b16(scales, b < ngroups ? scale_at + (uint32_t)b * 2 : kNowhere, 0, 0);
+    }
+  }
+};
+
+// Few rows.  A workgroup has 16 weight rows and 16 NT rows of x; its waves
+// take the blocks of columns in turn, U of them loaded together, and their
+// sums meet in LDS in a fixed order.  An instruction multiplies 16 rows of x
+// (first operand) by 16 weight rows: lane l gets the sums of x rows 4 (l / 16)
+// to + 3 and weight row l % 16, whose scale is then the lane's own.  Rows and
+// columns that do not exist are loaded as 0 through the buffers' ends.
 template <typename XT, int NT, bool FINE, bool XV, typename YT>
 __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
   extern __shared__ float part[];  // (W - 1, NT, 64, 4)
+  using X = X8<XT, XV>;
+  constexpr int U = sizeof(XT) == 4 ? (NT == 1 ? 2 : 1) : 4 / NT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
   const int i = lane & 15, q = lane >> 4;
   const int64_t n0 = (a.base + blockIdx.x) * 16, t0 = (int64_t)blockIdx.y * (16 * NT);
-  const int64_t n = n0 + i < a.outer ? n0 + i : a.outer - 1;
-  const uint8_t* wrow = a.codes + n * (a.inner >> 1);
-  const XT* xrow[NT];
-#pragma unroll
-  for (int u = 0; u < NT; ++u) {
-    const int64_t t = t0 + 16 * u + i;
-    xrow[u] = static_cast<const XT*>(a.x) + (t < a.rows ? t : a.rows - 1) * a.x_stride;
-  }
-  const uint16_t* srow[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t m = n0 + 4 * q + r;
-    srow[r] = a.scales + (m < a.outer ? m : a.outer - 1) * a.ngroups;
-  }
+  const WRows<FINE> wr(a, n0);
+  const int64_t rows = a.rows - t0 < 16 * NT ? a.rows - t0 : 16 * NT;
+  const uint32_t step = (uint32_t)a.x_stride * (uint32_t)sizeof(XT);
+  const __amdgpu_buffer_rsrc_t xb = buffer_at(static_cast<const XT*>(a.x) + t0 * a.x_stride,
+                                              (uint32_t)(rows - 1) * step + (uint32_t)a.inner * (uint32_t)sizeof(XT));
+  const uint32_t x_at = (FINE ? 8 : 32) * q * (uint32_t)sizeof(XT);
   f32x4 sum[NT];
 #pragma unroll
   for (int u = 0; u < NT; ++u) sum[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int64_t nb = (a.inner + kBlk - 1) / kBlk;
-  using X = X8<XT, XV>;
-  for (int64_t b = wave; b < nb; b += W) {
-    const int64_t k0 = b * kBlk;
-    uint32_t c[4] = {0, 0, 0, 0};
-    if (!FINE || k0 + 32 * q < a.inner) {
-      const uint4 v = *reinterpret_cast<const uint4*>(wrow + (k0 >> 1) + 16 * q);
-      c[0] = v.x; c[1] = v.y; c[2] = v.z; c[3] = v.w;
-    }
-    if constexpr (FINE) transpose4(c);
-    f32x4 acc[NT];
+  for (int64_t b0 = wave; b0 < nb; b0 += (int64_t)U * W) {
+    typename WRows<FINE>::Block wb[U];
+    X xr[U][4][NT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (FINE && k0 + 32 * j >= a.inner) break;
-      const int64_t k = k0 + (FINE ? 32 * j + 8 * q : 32 * q + 8 * j);
-      const bool begin = FINE ? (k0 + 32 * j) % a.group == 0 : j == 0;
-      const bool end = FINE ? (k0 + 32 * (j + 1)) % a.group == 0 : j == 3;
-      const bf16x8 w = values8(c[j]);
+    for (int v = 0; v < U; ++v) wr.load(wb[v], b0 + (int64_t)v * W);
 #pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        X xr;
-        bf16x8 xp[X::kParts];
-        xr.load(xrow[u] + k);
-        xr.get(xp);
-        if (begin) acc[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int v = 0; v < U; ++v) {
+      const int64_t k0 = (b0 + (int64_t)v * W) * kBlk;
 #pragma unroll
-        for (int p = X::kParts - 1; p >= 0; --p)
-          acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xp[p], acc[u], 0, 0, 0);
+      for (int j = 0; j < 4; ++j) {
+        const int64_t k = k0 + (FINE ? 32 : 8) * j;
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+          xr[v][j][u].load(xb, k < a.inner && 16 * u + i < rows ? (16 * u + i) * step + x_at + (uint32_t)k * (uint32_t)sizeof(XT)
+                                                               : kNowhere);
       }
-      if (end) {
-        const int64_t g = FINE ? (k0 + 32 * j) / a.group : b;
+    }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float s = to_f32(srow[r][g]);
+    for (int v = 0; v < U; ++v) {
+      if constexpr (FINE) transpose4(wb[v].c);
+      f32x4 acc[NT];
 #pragma unroll
-          for (int u = 0; u < NT; ++u) sum[u][r] = __builtin_fmaf(s, acc[u][r], sum[u][r]);
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 w = values8(wb[v].c[j]);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          bf16x8 xp[X::kParts];
+          xr[v][j][u].get(xp);
+          if (FINE || j == 0) acc[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int p = X::kParts - 1; p >= 0; --p)
+            acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xp[p], w, acc[u], 0, 0, 0);
+          if (FINE || j == 3) {
+            const float s = __uint_as_float(wb[v].s[FINE ? j : 0] << 16);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[u][r] = __builtin_fmaf(s, acc[u][r], sum[u][r]);
+          }
         }
       }
     }
@@ -180,18 +245,125 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
     for (int u = 0; u < NT; ++u) parts[((wave - 1) * NT + u) * 64 + lane] = sum[u];
   }
   __syncthreads();
-  if (wave > 0) return;
+  if (wave > 0 || n0 + i >= a.outer) return;
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
+#pragma unroll 4
     for (int w = 0; w + 1 < W; ++w) sum[u] += parts[(w * NT + u) * 64 + lane];
-    const int64_t t = t0 + 16 * u + i;
-    if (t >= a.rows) continue;
-    const float xs = a.x_scale ? a.x_scale[t] : 1.0f;
-    YT* y = static_cast<YT*>(a.y) + t * a.outer;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (n0 + 4 * q + r < a.outer) y[n0 + 4 * q + r] = from_f32<YT>(sum[u][r] * xs);
+    for (int r = 0; r < 4; ++r) {
+      const int64_t t = t0 + 16 * u + 4 * q + r;
+      if (t >= a.rows) continue;
+      const float xs = a.x_scale ? a.x_scale[t] : 1.0f;
+      static_cast<YT*>(a.y)[t * a.outer + n0 + i] = from_f32<YT>(sum[u][r] * xs);
+    }
   }
+}
+
+// More rows.  A workgroup has 128 weight rows, 32 to a wave, and 64 rows of x,
+// whose blocks of columns pass through LDS as bf16, one ahead; a wave
+// multiplies each piece of x by both of its tiles of weight rows.  blockIdx.z:
+// a slice of the columns, its sums left in the workspace where there are
+// several.
+constexpr int kBM = 64, kBN = 128;
+constexpr int kXP = kBlk + 8;  // pitch of a row of x in LDS: 16 rows in 16 bytes meet all banks once
+template <typename XT, bool FINE, bool XV, typename YT>
+__global__ __launch_bounds__(256) void s6_q4_many_kernel(Q4Args a) {
+  __shared__ __attribute__((aligned(16))) uint16_t xt[2][kBM][kXP];
+  using X = X8<XT, XV>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, q = lane >> 4;
+  const int64_t n0 = (a.base + blockIdx.x) * kBN + 32 * wave, t0 = (int64_t)blockIdx.y * kBM;
+  const WRows<FINE> w0(a, n0), w1(a, n0 + 16);
+  const int64_t rows = a.rows - t0 < kBM ? a.rows - t0 : kBM;
+  const uint32_t step = (uint32_t)a.x_stride * (uint32_t)sizeof(XT);
+  const __amdgpu_buffer_rsrc_t xb = buffer_at(static_cast<const XT*>(a.x) + t0 * a.x_stride,
+                                              (uint32_t)(rows - 1) * step + (uint32_t)a.inner * (uint32_t)sizeof(XT));
+  const int64_t nb = (a.inner + kBlk - 1) / kBlk;
+  const int64_t lo = blockIdx.z * a.slice, hi = lo + a.slice < nb ? lo + a.slice : nb;
+  // staging: thread c has eight columns, 8 (c % 16) on, of rows c / 16 + 16 m
+  const int sc = 8 * (threadIdx.x & 15), sr = threadIdx.x >> 4;
+  X xr[4];
+  typename WRows<FINE>::Block b0, b1;
+  auto load = [&](int64_t b) {
+    w0.load(b0, b);
+    w1.load(b1, b);
+    const int64_t k = b * kBlk + sc;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      xr[m].load(xb, k < a.inner && sr + 16 * m < rows ? (sr + 16 * m) * step + (uint32_t)k * (uint32_t)sizeof(XT) : kNowhere);
+  };
+  f32x4 sum[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sum[h][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  load(lo);
+  for (int64_t b = lo; b < hi; ++b) {
+    uint16_t(*x)[kXP] = xt[(b - lo) & 1];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      bf16x8 v[1];
+      xr[m].get(v);
+      *reinterpret_cast<bf16x8*>(&x[sr + 16 * m][sc]) = v[0];
+    }
+    typename WRows<FINE>::Block c0 = b0, c1 = b1;
+    __syncthreads();
+    if (b + 1 < hi) load(b + 1);
+    if constexpr (FINE) {
+      transpose4(c0.c);
+      transpose4(c1.c);
+    }
+    f32x4 acc[2][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bf16x8 v0 = values8(c0.c[j]), v1 = values8(c1.c[j]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bf16x8 xv = *reinterpret_cast<const bf16x8*>(&x[16 * u + i][FINE ? 32 * j + 8 * q : 32 * q + 8 * j]);
+        if (FINE || j == 0) acc[0][u] = acc[1][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        acc[0][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, v0, acc[0][u], 0, 0, 0);
+        acc[1][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, v1, acc[1][u], 0, 0, 0);
+      }
+      if (FINE || j == 3) {
+        const float s0 = __uint_as_float(c0.s[FINE ? j : 0] << 16), s1 = __uint_as_float(c1.s[FINE ? j : 0] << 16);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sum[0][u][r] = __builtin_fmaf(s0, acc[0][u][r], sum[0][u][r]);
+            sum[1][u][r] = __builtin_fmaf(s1, acc[1][u][r], sum[1][u][r]);
+          }
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t n = n0 + 16 * h + i;
+    if (n >= a.outer) continue;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t t = t0 + 16 * u + 4 * q + r;
+        if (t >= a.rows) continue;
+        if (a.parts)
+          a.parts[((int64_t)blockIdx.z * a.rows + t) * a.outer + n] = sum[h][u][r];
+        else
+          static_cast<YT*>(a.y)[t * a.outer + n] = from_f32<YT>(sum[h][u][r] * (a.x_scale ? a.x_scale[t] : 1.0f));
+      }
+  }
+}
+
+// y from the slices' sums, in a fixed order.
+template <typename YT>
+__global__ __launch_bounds__(256) void s6_q4_join_kernel(Q4Args a, int slices) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x, t = blockIdx.y, all = a.rows * a.outer;
+  if (n >= a.outer) return;
+  float s = 0.0f;
+#pragma unroll 4
+  for (int z = 0; z < slices; ++z) s += a.parts[z * all + t * a.outer + n];
+  static_cast<YT*>(a.y)[t * a.outer + n] = from_f32<YT>(s * (a.x_scale ? a.x_scale[t] : 1.0f));
 }
 
 // ------------------------------------------------------------------ pack --
@@ -236,12 +408,13 @@ __global__ __launch_bounds__(256) void s6_q4_pack_kernel(const In* w, int64_t st
 }
 
 // ------------------------------------------------------------------ host --
+constexpr int64_t kMaxStride = 1 << 24;   // elements from row to row: a tile's 64 rows in 32 bits
 constexpr int64_t kMaxGrid = 1 << 22;  // workgroups of a launch in x (threads below 2^32)
 
 int check_q4(int64_t rows, int64_t inner, int64_t outer, int64_t group, int64_t stride) {
   if (rows < 0 || outer < 0 || inner < 1 || stride < 0) return S6_ERR_SHAPE;
   if (group != 32 && group != 64 && group != 128) return S6_ERR_UNSUPPORTED;
-  if (inner % group || inner > (1 << 28) || outer > INT32_MAX || (rows > 1 && stride < inner)) return S6_ERR_SHAPE;
+  if (inner % group || inner > kMaxStride || outer > INT32_MAX || (rows > 1 && stride < inner)) return S6_ERR_SHAPE;
   int64_t t;
   if (!mul_ok(outer, inner, &t) || !mul_ok(t, 8, &t) || !mul_ok(rows, stride, &t) || !mul_ok(t, 8, &t) ||
       !mul_ok(rows, outer, &t) || !mul_ok(t, 64, &t))
@@ -249,33 +422,71 @@ int check_q4(int64_t rows, int64_t inner, int64_t outer, int64_t group, int64_t 
   return S6_OK;
 }
 
+constexpr int64_t kFewRows = 32;          // most rows of the first kernel (fp32: any number)
+constexpr int64_t kLaunchRows = 32768;    // most rows of a launch of the second
+
+// Slices of the columns for the second kernel: two workgroups per CU where
+// there are columns for it, of at least four blocks each.  They cost a pass over
+// their sums.
+int64_t slices_of(int64_t rows, int64_t inner, int64_t outer, int64_t* slice) {
+  const int64_t nb = (inner + kBlk - 1) / kBlk, n = rows < kLaunchRows ? rows : kLaunchRows;
+  const int64_t tiles = ((outer + kBN - 1) / kBN) * ((n + kBM - 1) / kBM);
+  int64_t s = cu_count() / (tiles > 0 ? tiles : 1);
+  if (s > nb / 4) s = nb / 4;
+  if (s < 1) s = 1;
+  *slice = (nb + s - 1) / s;
+  return (nb + *slice - 1) / *slice;
+}
+
 template <typename XT, int NT, bool FINE, bool XV, typename YT>
 int launch_few(Q4Args a, hipStream_t st) {
   const int64_t nb = (a.inner + kBlk - 1) / kBlk, tiles = (a.outer + 15) / 16;
   const int64_t ty = (a.rows + 16 * NT - 1) / (16 * NT);
-  // waves: about five blocks each
-  const int W = nb > 40 ? 16 : nb > 20 ? 8 : nb > 2 ? 4 : nb > 1 ? 2 : 1;
+  // waves: as many as load the columns at once, four blocks each
+  int64_t W = (nb + 3) / 4;
+  if (W > 16) W = 16;
   const size_t lds = (size_t)(W - 1) * NT * 64 * sizeof(f32x4);
   for (a.base = 0; a.base < tiles; a.base += kMaxGrid) {
     const dim3 grid((unsigned)(tiles - a.base < kMaxGrid ? tiles - a.base : kMaxGrid), (unsigned)ty);
-    hipLaunchKernelGGL((s6_q4_few_kernel<XT, NT, FINE, XV, YT>), grid, dim3(64 * W), lds, st, a);
+    hipLaunchKernelGGL((s6_q4_few_kernel<XT, NT, FINE, XV, YT>), grid, dim3(64 * (unsigned)W), lds, st, a);
     S6_HIP(hipGetLastError(), "s6_q4_few_kernel launch");
   }
   return S6_OK;
 }
 template <typename XT, bool FINE, bool XV, typename YT>
-int launch_rows(Q4Args a, hipStream_t st) {
-  // at most 65535 tiles of rows a launch
-  const int64_t rows = a.rows, step = 65535 * 16;
-  for (int64_t r = 0; r < rows; r += step) {
+int launch_many(Q4Args a, int64_t slices, hipStream_t st) {
+  if constexpr (sizeof(XT) < 4) {
+    const int64_t tiles = (a.outer + kBN - 1) / kBN;
+    for (a.base = 0; a.base < tiles; a.base += kMaxGrid) {
+      const dim3 grid((unsigned)(tiles - a.base < kMaxGrid ? tiles - a.base : kMaxGrid),
+                      (unsigned)((a.rows + kBM - 1) / kBM), (unsigned)slices);
+      hipLaunchKernelGGL((s6_q4_many_kernel<XT, FINE, XV, YT>), grid, dim3(256), 0, st, a);
+      S6_HIP(hipGetLastError(), "s6_q4_many_kernel launch");
+    }
+    if (slices > 1) {
+      hipLaunchKernelGGL(s6_q4_join_kernel<YT>, dim3((unsigned)((a.outer + 255) / 256), (unsigned)a.rows), dim3(256), 0, st,
+                         a, (int)slices);
+      S6_HIP(hipGetLastError(), "s6_q4_join_kernel launch");
+    }
+  }
+  return S6_OK;
+}
+template <typename XT, bool FINE, bool XV, typename YT>
+int launch_rows(const Q4Args& a, hipStream_t st) {
+  const bool few = sizeof(XT) == 4 || a.rows <= kFewRows;
+  int64_t slice = 0;
+  const int64_t slices = few ? 1 : slices_of(a.rows, a.inner, a.outer, &slice);
+  for (int64_t r = 0; r < a.rows; r += kLaunchRows) {
     Q4Args b = a;
-    b.rows = rows - r < step ? rows - r : step;
+    b.rows = a.rows - r < kLaunchRows ? a.rows - r : kLaunchRows;
     b.x = static_cast<const XT*>(a.x) + r * a.x_stride;
     b.x_scale = a.x_scale ? a.x_scale + r : nullptr;
     b.y = static_cast<YT*>(a.y) + r * a.outer;
-    const int rc = b.rows <= 16 ? launch_few<XT, 1, FINE, XV, YT>(b, st)
-                   : b.rows <= 32 ? launch_few<XT, 2, FINE, XV, YT>(b, st)
-                                  : launch_few<XT, 4, FINE, XV, YT>(b, st);
+    b.slice = slice;
+    if (slices == 1) b.parts = nullptr;
+    const int rc = !few          ? launch_many<XT, FINE, XV, YT>(b, slices, st)
+                   : b.rows > 16 ? launch_few<XT, 2, FINE, XV, YT>(b, st)
+                                 : launch_few<XT, 1, FINE, XV, YT>(b, st);
     if (rc) return rc;
   }
   return S6_OK;
@@ -284,6 +495,14 @@ template <typename XT, typename YT>
 int launch_q4(const Q4Args& a, bool vec, hipStream_t st) {
   if (a.group == 128) return vec ? launch_rows<XT, false, true, YT>(a, st) : launch_rows<XT, false, false, YT>(a, st);
   return vec ? launch_rows<XT, true, true, YT>(a, st) : launch_rows<XT, true, false, YT>(a, st);
+}
+
+size_t q4_ws(int64_t rows, int64_t inner, int64_t outer, int x_dtype) {
+  if (rows <= kFewRows || outer == 0 || x_dtype == S6_F32) return 0;
+  int64_t slice;
+  const int64_t s = slices_of(rows, inner, outer, &slice);
+  const int64_t n = rows < kLaunchRows ? rows : kLaunchRows;
+  return s > 1 ? up256((size_t)s * n * outer * sizeof(float)) : 0;
 }
 
 }  // namespace
@@ -324,7 +543,7 @@ int s6_q4_linear_workspace_size(int64_t rows, int64_t inner, int64_t outer, int6
   if (x_dtype != S6_F32 && x_dtype != S6_BF16 && x_dtype != S6_E4M3) return S6_ERR_DTYPE;
   const int rc = check_q4(rows, inner, outer, group, inner);
   if (rc) return rc;
-  *bytes = 0;
+  *bytes = q4_ws(rows, inner, outer, x_dtype);
   return S6_OK;
 }
 
@@ -335,19 +554,25 @@ int s6_q4_linear(int64_t rows, int64_t inner, int64_t outer, int64_t group, int 
   if (y_dtype != S6_F32 && y_dtype != S6_BF16) return S6_ERR_DTYPE;
   const int rc = check_q4(rows, inner, outer, group, x_stride);
   if (rc) return rc;
+  if (rows > 1 && x_stride > kMaxStride) return S6_ERR_SHAPE;
   if (x_scale && x_dtype != S6_E4M3) return S6_ERR_UNSUPPORTED;
   if (rows == 0 || outer == 0) return S6_OK;
   if (!x || !codes || !scales || !y) return S6_ERR_NULL;
   const size_t xsz = x_dtype == S6_F32 ? 4 : x_dtype == S6_BF16 ? 2 : 1, ysz = y_dtype == S6_BF16 ? 2 : 4;
   if (!aligned(x, xsz) || !aligned(y, ysz) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(x_scale, 4))
     return S6_ERR_ALIGN;
-  (void)workspace; (void)workspace_bytes;
+  const size_t need = q4_ws(rows, inner, outer, x_dtype);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return S6_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return S6_ERR_ALIGN;
+  }
   Q4Args a;
   memset(&a, 0, sizeof(a));
   a.x = x; a.x_scale = x_scale; a.codes = static_cast<const uint8_t*>(codes);
   a.scales = static_cast<const uint16_t*>(scales); a.y = y;
   a.rows = rows; a.inner = inner; a.outer = outer; a.x_stride = x_stride;
   a.group = (int)group; a.ngroups = (int)(inner / group);
+  a.parts = static_cast<float*>(workspace);
   const bool vec = aligned(x, 16) && (x_stride * (int64_t)xsz) % 16 == 0;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (x_dtype == S6_F32)
