@@ -11,7 +11,7 @@
  * 4-bit weights.  A matrix (outer, inner) as codes, two in a byte with the
  * lower index in the lower half, rows of inner / 2 bytes, and one bf16 scale
  * per `group` consecutive columns of a row, (outer, inner / group); group is
- * 32, 64 or 128 and divides inner, which is at most 2^24.  A weight is value(code) * scale; the
+ * 32, 64 or 128 and divides inner, which is at most 2^20.  A weight is value(code) * scale; the
  * values of codes 0 to 7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6 and those of 8 to 15
  * the same with a minus (the 4-bit float with two exponent bits and one
  * mantissa bit).
@@ -39,7 +39,7 @@ int s6_q4_pack(int64_t outer, int64_t inner, int64_t group, int in_dtype, const 
  * with S6_E4M3); y (rows, outer) contiguous, in y_dtype S6_F32 or S6_BF16.
  * Products are exact, sums fp32, scales fp32; an fp32 x enters in full (three
  * bf16 parts).  Any number of rows; made for the few rows of single tokens.
- * codes are 16-byte aligned, x_stride is at most 2^24.  workspace: s6_q4_linear_workspace_size bytes.
+ * codes are 16-byte aligned, x_stride is at most 2^20.  workspace: s6_q4_linear_workspace_size bytes.
  * Repeated calls give identical bits. */
 int s6_q4_linear(int64_t rows, int64_t inner, int64_t outer, int64_t group, int x_dtype, int y_dtype, const void* x,
                  int64_t x_stride, const float* x_scale, const void* codes, const void* scales, void* y,

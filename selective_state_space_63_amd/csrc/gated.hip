@@ -138,15 +138,15 @@ struct Piece {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) e[v] = p[v];
   }
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t wave) {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     if constexpr (sizeof(e) == 8) {
-      const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, lane, wave, 0);
+      const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
       __builtin_memcpy(e, &w, 8);
     } else if constexpr (sizeof(e) == 4) {
-      const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(r, lane, wave, 0);
+      const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
       __builtin_memcpy(e, &w, 4);
     } else {
-      e[0] = __builtin_amdgcn_raw_buffer_load_b16(r, lane, wave, 0);
+      e[0] = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
     }
   }
   __device__ __forceinline__ float get(int v) const { return to_f32(e[v]); }
@@ -170,16 +170,16 @@ struct Piece {
 };
 // VEC channels of a token, rounded to In.
 template <typename In, int VEC>
-__device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t wave, const float (&f)[VEC]) {
+__device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[VEC]) {
   typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
   if constexpr (VEC == 2 && sizeof(In) == 4)
-    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(f[0]), __float_as_uint(f[1])}, r, lane, wave, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(f[0]), __float_as_uint(f[1])}, r, off, 0, 0);
   else if constexpr (VEC == 2)
-    __builtin_amdgcn_raw_buffer_store_b32(bf_pack(f[0], f[1]), r, lane, wave, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(bf_pack(f[0], f[1]), r, off, 0, 0);
   else if constexpr (sizeof(In) == 4)
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, lane, wave, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, off, 0, 0);
   else
-    __builtin_amdgcn_raw_buffer_store_b16(from_f32<In>(f[0]), r, lane, wave, 0);
+    __builtin_amdgcn_raw_buffer_store_b16(from_f32<In>(f[0]), r, off, 0, 0);
 }
 
 __device__ __forceinline__ float gate_f(float g, float bias_l2) {  // bias_l2 = -bias log2(e)
@@ -246,6 +246,7 @@ __device__ __forceinline__ int draw_tile(const GatedArgs& a, uint32_t* shared) {
 }
 
 // A wave's part of one tensor as a buffer: its tokens of the tile's channels.
+// Offsets are the lanes' own: a scalar offset need not be bounds-checked.
 // Past its end loads return 0 and stores are dropped, so that tiles need no
 // branches at the end of a sequence; a lane past dim may load what lies beside
 // the row, and stores nothing.  A tensor that is not given is an empty buffer:
@@ -275,7 +276,7 @@ __device__ __forceinline__ Rows rows_of(const void* base, int64_t batch_stride, 
 template <typename In, int VEC>
 __device__ __forceinline__ void load_rows(Piece<In, VEC> (&o)[Place<VEC>::T], const Rows& r) {
 #pragma unroll
-  for (int t = 0; t < Place<VEC>::T; ++t) o[t].load(r.buf, r.lane, t * r.step);
+  for (int t = 0; t < Place<VEC>::T; ++t) o[t].load(r.buf, r.lane + t * r.step);
 }
 
 // Bit t: token t of the lane's group starts a sequence.
@@ -399,7 +400,7 @@ __global__ __launch_bounds__(kWaves * 64, kFwdWaves) void s6_gated_scan_kernel(G
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     next(t);
-    put<In, VEC>(y.buf, y.lane, t * y.step, h);
+    put<In, VEC>(y.buf, y.lane + t * y.step, h);
   }
 }
 
@@ -564,9 +565,9 @@ __global__ __launch_bounds__(kWaves * 64, kBwdWaves) void s6_gated_scan_bwd_kern
         sa[v] += oa[v];
         sx[v] += og[v];
       }
-      put<In, VEC>(dx.buf, dx.lane, t * dx.step, ox);
-      put<In, VEC>(dga.buf, dga.lane, t * dga.step, oa);
-      put<In, VEC>(dgx.buf, dgx.lane, t * dgx.step, og);
+      put<In, VEC>(dx.buf, dx.lane + t * dx.step, ox);
+      put<In, VEC>(dga.buf, dga.lane + t * dga.step, oa);
+      put<In, VEC>(dgx.buf, dgx.lane + t * dgx.step, og);
     }
   }
   if (!a.parts) return;

@@ -26,11 +26,12 @@ struct Q4Args {
   const uint8_t* codes;
   const uint16_t* scales;
   void* y;
-  int64_t rows, inner, outer, x_stride;
-  int group;      // columns of a scale
+  int64_t rows, outer, x_stride;
+  int inner;
+  int fine;       // log2(128 / group)
   int ngroups;    // inner / group
   int64_t base;   // first tile of weight rows of the launch
-  int64_t slice;  // blocks of columns of a slice
+  int slice;      // blocks of columns of a slice
   float* parts;   // the slices' sums (slices, rows, outer), or null
 };
 
@@ -62,7 +63,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, uint3
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(v), 0, __builtin_amdgcn_readfirstlane(bytes),
                                            0x00027000);
 }
-constexpr uint32_t kNowhere = 0xf0000000u;  // an offset past every buffer, also with 32 bytes added
+// Offsets past every buffer (the host keeps buffers below 2^28 bytes): of a
+// row that does not exist, and of columns; their sum is one too.
+constexpr uint32_t kNoRow = 0x80000000u, kNoColumn = 0x40000000u;
 
 // Eight consecutive values of x as loaded, and as bf16 parts whose sum they are.
 template <typename XT, bool XV>
@@ -136,43 +139,54 @@ template <bool FINE>
 struct WRows {
   __amdgpu_buffer_rsrc_t codes, scales;
   uint32_t code_at, scale_at;
-  int64_t inner;
-  int ngroups, per;  // per: groups of a block
+  int inner, q32, fine;  // q32: first of the lane's columns in a block; fine: log2 of 128 / group
   __device__ __forceinline__ WRows(const Q4Args& a, int64_t n0) {
-    const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+    const int lane = threadIdx.x & 63, i = lane & 15;
+    q32 = 2 * (lane & 48);
     const int64_t left = a.outer - n0;
     const uint32_t rows = left < 0 ? 0 : left < 16 ? (uint32_t)left : 16;
-    const uint32_t row = (uint32_t)(a.inner >> 1);
-    codes = buffer_at(a.codes + n0 * (a.inner >> 1), rows * row);
+    const uint32_t row = (uint32_t)a.inner >> 1;
+    codes = buffer_at(a.codes + n0 * row, rows * row);
     scales = buffer_at(a.scales + n0 * a.ngroups, rows * (uint32_t)a.ngroups * 2);
-    code_at = i * row + 16 * q;
+    code_at = i * row + (q32 >> 1);
     scale_at = i * (uint32_t)a.ngroups * 2;
     inner = a.inner;
-    ngroups = a.ngroups;
-    per = kBlk / a.group;
+    fine = a.fine;
   }
   struct Block {
     uint32_t c[4];
-    uint32_t s[FINE ? 4 : 1];  // scales of the block's groups (one per step of 32 columns)
+    uint32_t s;  // scale: of the block's group, or (FINE) of the group of the lane's 32 columns
   };
-  // Block b; one past the last is 0.
-  __device__ __forceinline__ void load(Block& o, int64_t b) const {
-    const int q = (threadIdx.x & 63) >> 4;
-    const bool on = b * kBlk + (FINE ? 32 * q : 0) < inner;
-    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(codes, on ? code_at + (uint32_t)b * 64 : kNowhere, 0, 0);
+  // Block b; what lies past the last column is 0.
+  __device__ __forceinline__ void load(Block& o, int b) const {
+    const int k = b * kBlk;
+    uint32_t at = code_at + (k < inner ? (uint32_t)k >> 1 : kNoColumn), sat;
+    if constexpr (FINE) {
+      const bool on = k + q32 < inner;
+      at = on ? at : kNoColumn;
+      sat = on ? scale_at + ((uint32_t)(k + q32) >> 7 - fine) * 2 : kNoColumn;
+    } else {
+      sat = scale_at + (k < inner ? (uint32_t)b * 2 : kNoColumn);
+    }
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(codes, at, 0, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) o.c[j] = v[j];
-    if constexpr (FINE) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t g = (b * 4 + j) * per >> 2;  // group of step j
-        o.s[j] = __builtin_amdgcn_raw_buffer_load_b16(scales, g < ngroups ? scale_at + (uint32_t)g * 2 : kNowhere, 0, 0);
-      }
-    } else {
-      o.s[0] = __builtin_amdgcn_raw_buffer_load_b16(scales, b < ngroups ? scale_at + (uint32_t)b * 2 : kNowhere, 0, 0);
-    }
+    o.s = __builtin_amdgcn_raw_buffer_load_b16(scales, sat, 0, 0);
   }
 };
+// The scales of the four steps of a block (FINE), or of the block.
+template <bool FINE>
+__device__ __forceinline__ void scales_of(uint32_t s, float (&f)[4]) {
+  if constexpr (FINE) {  // the four rows of 16 lanes to all of them
+    const auto a = __builtin_amdgcn_permlane16_swap(s << 16, s << 16, false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(a[0], a[0], false, false);
+    const auto c = __builtin_amdgcn_permlane32_swap(a[1], a[1], false, false);
+    f[0] = __uint_as_float(b[0]); f[1] = __uint_as_float(c[0]);
+    f[2] = __uint_as_float(b[1]); f[3] = __uint_as_float(c[1]);
+  } else {
+    f[3] = __uint_as_float(s << 16);
+  }
+}
 
 // Few rows.  A workgroup has 16 weight rows and 16 NT rows of x; its waves
 // take the blocks of columns in turn, U of them loaded together, and their
@@ -185,39 +199,41 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
   extern __shared__ float part[];  // (W - 1, NT, 64, 4)
   using X = X8<XT, XV>;
   constexpr int U = sizeof(XT) == 4 ? (NT == 1 ? 2 : 1) : 4 / NT;
+  constexpr uint32_t kE = sizeof(XT);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
   const int i = lane & 15, q = lane >> 4;
   const int64_t n0 = (a.base + blockIdx.x) * 16, t0 = (int64_t)blockIdx.y * (16 * NT);
   const WRows<FINE> wr(a, n0);
-  const int64_t rows = a.rows - t0 < 16 * NT ? a.rows - t0 : 16 * NT;
-  const uint32_t step = (uint32_t)a.x_stride * (uint32_t)sizeof(XT);
-  const __amdgpu_buffer_rsrc_t xb = buffer_at(static_cast<const XT*>(a.x) + t0 * a.x_stride,
-                                              (uint32_t)(rows - 1) * step + (uint32_t)a.inner * (uint32_t)sizeof(XT));
-  const uint32_t x_at = (FINE ? 8 : 32) * q * (uint32_t)sizeof(XT);
+  const int rows = a.rows - t0 < 16 * NT ? (int)(a.rows - t0) : 16 * NT;
+  const uint32_t step = (uint32_t)a.x_stride * kE;
+  const __amdgpu_buffer_rsrc_t xb =
+      buffer_at(static_cast<const XT*>(a.x) + t0 * a.x_stride, (uint32_t)(rows - 1) * step + (uint32_t)a.inner * kE);
+  uint32_t x_at[NT];
+#pragma unroll
+  for (int u = 0; u < NT; ++u) x_at[u] = 16 * u + i < rows ? (16 * u + i) * step + (FINE ? 8 : 32) * q * kE : kNoRow;
   f32x4 sum[NT];
 #pragma unroll
   for (int u = 0; u < NT; ++u) sum[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t nb = (a.inner + kBlk - 1) / kBlk;
-  for (int64_t b0 = wave; b0 < nb; b0 += (int64_t)U * W) {
+  const int nb = (a.inner + kBlk - 1) / kBlk;
+  for (int b0 = wave; b0 < nb; b0 += U * W) {
     typename WRows<FINE>::Block wb[U];
     X xr[U][4][NT];
 #pragma unroll
-    for (int v = 0; v < U; ++v) wr.load(wb[v], b0 + (int64_t)v * W);
+    for (int v = 0; v < U; ++v) wr.load(wb[v], b0 + v * W);
 #pragma unroll
-    for (int v = 0; v < U; ++v) {
-      const int64_t k0 = (b0 + (int64_t)v * W) * kBlk;
+    for (int v = 0; v < U; ++v)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t k = k0 + (FINE ? 32 : 8) * j;
+        const int k = (b0 + v * W) * kBlk + (FINE ? 32 : 8) * j;
+        const uint32_t at = k < a.inner ? (uint32_t)k * kE : kNoColumn;
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
-          xr[v][j][u].load(xb, k < a.inner && 16 * u + i < rows ? (16 * u + i) * step + x_at + (uint32_t)k * (uint32_t)sizeof(XT)
-                                                               : kNowhere);
+        for (int u = 0; u < NT; ++u) xr[v][j][u].load(xb, x_at[u] + at);
       }
-    }
 #pragma unroll
     for (int v = 0; v < U; ++v) {
       if constexpr (FINE) transpose4(wb[v].c);
+      float sc[4];
+      scales_of<FINE>(wb[v].s, sc);
       f32x4 acc[NT];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -231,9 +247,8 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
           for (int p = X::kParts - 1; p >= 0; --p)
             acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xp[p], w, acc[u], 0, 0, 0);
           if (FINE || j == 3) {
-            const float s = __uint_as_float(wb[v].s[FINE ? j : 0] << 16);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sum[u][r] = __builtin_fmaf(s, acc[u][r], sum[u][r]);
+            for (int r = 0; r < 4; ++r) sum[u][r] = __builtin_fmaf(sc[j], acc[u][r], sum[u][r]);
           }
         }
       }
@@ -275,23 +290,26 @@ __global__ __launch_bounds__(256) void s6_q4_many_kernel(Q4Args a) {
   const int i = lane & 15, q = lane >> 4;
   const int64_t n0 = (a.base + blockIdx.x) * kBN + 32 * wave, t0 = (int64_t)blockIdx.y * kBM;
   const WRows<FINE> w0(a, n0), w1(a, n0 + 16);
-  const int64_t rows = a.rows - t0 < kBM ? a.rows - t0 : kBM;
-  const uint32_t step = (uint32_t)a.x_stride * (uint32_t)sizeof(XT);
-  const __amdgpu_buffer_rsrc_t xb = buffer_at(static_cast<const XT*>(a.x) + t0 * a.x_stride,
-                                              (uint32_t)(rows - 1) * step + (uint32_t)a.inner * (uint32_t)sizeof(XT));
-  const int64_t nb = (a.inner + kBlk - 1) / kBlk;
-  const int64_t lo = blockIdx.z * a.slice, hi = lo + a.slice < nb ? lo + a.slice : nb;
+  constexpr uint32_t kE = sizeof(XT);
+  const int rows = a.rows - t0 < kBM ? (int)(a.rows - t0) : kBM;
+  const uint32_t step = (uint32_t)a.x_stride * kE;
+  const __amdgpu_buffer_rsrc_t xb =
+      buffer_at(static_cast<const XT*>(a.x) + t0 * a.x_stride, (uint32_t)(rows - 1) * step + (uint32_t)a.inner * kE);
+  const int nb = (a.inner + kBlk - 1) / kBlk;
+  const int lo = blockIdx.z * a.slice, hi = lo + a.slice < nb ? lo + a.slice : nb;
   // staging: thread c has eight columns, 8 (c % 16) on, of rows c / 16 + 16 m
   const int sc = 8 * (threadIdx.x & 15), sr = threadIdx.x >> 4;
   X xr[4];
   typename WRows<FINE>::Block b0, b1;
-  auto load = [&](int64_t b) {
+  uint32_t x_at[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) x_at[m] = sr + 16 * m < rows ? (sr + 16 * m) * step + sc * kE : kNoRow;
+  auto load = [&](int b) {
     w0.load(b0, b);
     w1.load(b1, b);
-    const int64_t k = b * kBlk + sc;
+    const int k = b * kBlk;
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-      xr[m].load(xb, k < a.inner && sr + 16 * m < rows ? (sr + 16 * m) * step + (uint32_t)k * (uint32_t)sizeof(XT) : kNowhere);
+    for (int m = 0; m < 4; ++m) xr[m].load(xb, !FINE || k + sc < a.inner ? x_at[m] + (uint32_t)k * kE : kNoColumn);
   };
   f32x4 sum[2][4];
 #pragma unroll
@@ -299,7 +317,7 @@ __global__ __launch_bounds__(256) void s6_q4_many_kernel(Q4Args a) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) sum[h][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   load(lo);
-  for (int64_t b = lo; b < hi; ++b) {
+  for (int b = lo; b < hi; ++b) {
     uint16_t(*x)[kXP] = xt[(b - lo) & 1];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -314,6 +332,9 @@ __global__ __launch_bounds__(256) void s6_q4_many_kernel(Q4Args a) {
       transpose4(c0.c);
       transpose4(c1.c);
     }
+    float s0[4], s1[4];
+    scales_of<FINE>(c0.s, s0);
+    scales_of<FINE>(c1.s, s1);
     f32x4 acc[2][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -326,13 +347,12 @@ __global__ __launch_bounds__(256) void s6_q4_many_kernel(Q4Args a) {
         acc[1][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, v1, acc[1][u], 0, 0, 0);
       }
       if (FINE || j == 3) {
-        const float s0 = __uint_as_float(c0.s[FINE ? j : 0] << 16), s1 = __uint_as_float(c1.s[FINE ? j : 0] << 16);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            sum[0][u][r] = __builtin_fmaf(s0, acc[0][u][r], sum[0][u][r]);
-            sum[1][u][r] = __builtin_fmaf(s1, acc[1][u][r], sum[1][u][r]);
+            sum[0][u][r] = __builtin_fmaf(s0[j], acc[0][u][r], sum[0][u][r]);
+            sum[1][u][r] = __builtin_fmaf(s1[j], acc[1][u][r], sum[1][u][r]);
           }
       }
     }
@@ -408,7 +428,7 @@ __global__ __launch_bounds__(256) void s6_q4_pack_kernel(const In* w, int64_t st
 }
 
 // ------------------------------------------------------------------ host --
-constexpr int64_t kMaxStride = 1 << 24;   // elements from row to row: a tile's 64 rows in 32 bits
+constexpr int64_t kMaxStride = 1 << 20;   // columns, and elements from row to row: a tile's 64 rows below 2^28 bytes
 constexpr int64_t kMaxGrid = 1 << 22;  // workgroups of a launch in x (threads below 2^32)
 
 int check_q4(int64_t rows, int64_t inner, int64_t outer, int64_t group, int64_t stride) {
@@ -482,7 +502,7 @@ int launch_rows(const Q4Args& a, hipStream_t st) {
     b.x = static_cast<const XT*>(a.x) + r * a.x_stride;
     b.x_scale = a.x_scale ? a.x_scale + r : nullptr;
     b.y = static_cast<YT*>(a.y) + r * a.outer;
-    b.slice = slice;
+    b.slice = (int)slice;
     if (slices == 1) b.parts = nullptr;
     const int rc = !few          ? launch_many<XT, FINE, XV, YT>(b, slices, st)
                    : b.rows > 16 ? launch_few<XT, 2, FINE, XV, YT>(b, st)
@@ -493,7 +513,7 @@ int launch_rows(const Q4Args& a, hipStream_t st) {
 }
 template <typename XT, typename YT>
 int launch_q4(const Q4Args& a, bool vec, hipStream_t st) {
-  if (a.group == 128) return vec ? launch_rows<XT, false, true, YT>(a, st) : launch_rows<XT, false, false, YT>(a, st);
+  if (a.fine == 0) return vec ? launch_rows<XT, false, true, YT>(a, st) : launch_rows<XT, false, false, YT>(a, st);
   return vec ? launch_rows<XT, true, true, YT>(a, st) : launch_rows<XT, true, false, YT>(a, st);
 }
 
@@ -570,8 +590,8 @@ int s6_q4_linear(int64_t rows, int64_t inner, int64_t outer, int64_t group, int 
   memset(&a, 0, sizeof(a));
   a.x = x; a.x_scale = x_scale; a.codes = static_cast<const uint8_t*>(codes);
   a.scales = static_cast<const uint16_t*>(scales); a.y = y;
-  a.rows = rows; a.inner = inner; a.outer = outer; a.x_stride = x_stride;
-  a.group = (int)group; a.ngroups = (int)(inner / group);
+  a.rows = rows; a.inner = (int)inner; a.outer = outer; a.x_stride = x_stride;
+  a.fine = group == 128 ? 0 : group == 64 ? 1 : 2; a.ngroups = (int)(inner / group);
   a.parts = static_cast<float*>(workspace);
   const bool vec = aligned(x, 16) && (x_stride * (int64_t)xsz) % 16 == 0;
   hipStream_t st = static_cast<hipStream_t>(stream);
