@@ -68,12 +68,14 @@ def _raw_stream(index):
 # The handle of the current stream without a Stream object around it, where
 # this torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+# The current device without a check for the runtime (device tensors are there).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(fn, like, *args):
     """fn(*args, stream) on `like`'s device and its current stream."""
-    index = like.device.index
-    if torch.cuda.current_device() == index:
+    index = like.get_device()
+    if _current_device() == index:
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -105,8 +107,8 @@ def _written(*tensors):
 def _workspace(query, like, *args):
     """(tensor, pointer, bytes) of a fresh workspace on the current stream."""
     out = ctypes.c_size_t(0)
-    index = like.device.index
-    if torch.cuda.current_device() == index:
+    index = like.get_device()
+    if _current_device() == index:
         rc = query(*args, ctypes.byref(out))
     else:
         with torch.cuda.device(index):
@@ -136,6 +138,12 @@ def _need(t, name, shape, dtype):
     if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     return t
+
+
+def _plain(t, shape, dtype, index):
+    """Whether t is a contiguous tensor of this shape and type on device
+    `index`: the quick way past the checks below, which name what is wrong."""
+    return t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == index
 
 
 def _whole(t, name, shape, dtype=torch.float32):

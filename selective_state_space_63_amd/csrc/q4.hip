@@ -31,6 +31,7 @@ struct Q4Args {
   int fine;       // log2(128 / group)
   int ngroups;    // inner / group
   int64_t base;   // first tile of weight rows of the launch
+  int wide;       // rows of y begin at 16 bytes
   int slice;      // blocks of columns of a slice
   float* parts;   // the slices' sums (slices, rows, outer), or null
 };
@@ -139,7 +140,7 @@ template <bool FINE>
 struct WRows {
   __amdgpu_buffer_rsrc_t codes, scales;
   uint32_t code_at, scale_at;
-  int inner, q32, fine;  // q32: first of the lane's columns in a block; fine: log2 of 128 / group
+  int q32, fine;  // q32: first of the lane's columns in a block; fine: log2 of 128 / group
   __device__ __forceinline__ WRows(const Q4Args& a, int64_t n0) {
     const int lane = threadIdx.x & 63, i = lane & 15;
     q32 = 2 * (lane & 48);
@@ -150,23 +151,22 @@ struct WRows {
     scales = buffer_at(a.scales + n0 * a.ngroups, rows * (uint32_t)a.ngroups * 2);
     code_at = i * row + (q32 >> 1);
     scale_at = i * (uint32_t)a.ngroups * 2;
-    inner = a.inner;
     fine = a.fine;
   }
   struct Block {
     uint32_t c[4];
     uint32_t s;  // scale: of the block's group, or (FINE) of the group of the lane's 32 columns
   };
-  // Block b; what lies past the last column is 0.
-  __device__ __forceinline__ void load(Block& o, int b) const {
+  // Block b; what lies past column `end` is 0.
+  __device__ __forceinline__ void load(Block& o, int b, int end) const {
     const int k = b * kBlk;
-    uint32_t at = code_at + (k < inner ? (uint32_t)k >> 1 : kNoColumn), sat;
+    uint32_t at = code_at + (k < end ? (uint32_t)k >> 1 : kNoColumn), sat;
     if constexpr (FINE) {
-      const bool on = k + q32 < inner;
+      const bool on = k + q32 < end;
       at = on ? at : kNoColumn;
       sat = on ? scale_at + ((uint32_t)(k + q32) >> 7 - fine) * 2 : kNoColumn;
     } else {
-      sat = scale_at + (k < inner ? (uint32_t)b * 2 : kNoColumn);
+      sat = scale_at + (k < end ? (uint32_t)b * 2 : kNoColumn);
     }
     const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(codes, at, 0, 0);
 #pragma unroll
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
     typename WRows<FINE>::Block wb[U];
     X xr[U][4][NT];
 #pragma unroll
-    for (int v = 0; v < U; ++v) wr.load(wb[v], b0 + v * W);
+    for (int v = 0; v < U; ++v) wr.load(wb[v], b0 + v * W, a.inner);
 #pragma unroll
     for (int v = 0; v < U; ++v)
 #pragma unroll
@@ -275,59 +275,82 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
   }
 }
 
-// More rows.  A workgroup has 128 weight rows, 32 to a wave, and 64 rows of x,
-// whose blocks of columns pass through LDS as bf16, one ahead; a wave
-// multiplies each piece of x by both of its tiles of weight rows.  blockIdx.z:
-// a slice of the columns, its sums left in the workspace where there are
-// several.
-constexpr int kBM = 64, kBN = 128;
+// More rows.  A workgroup has 128 weight rows and BM rows of x, and takes two
+// blocks of columns a turn, four waves to each (32 weight rows to a wave): the
+// blocks of x pass through LDS as bf16, a turn's loads under way during the turn
+// before, and each piece that a wave reads meets both of its tiles of weight
+// rows.  The two halves' sums meet in LDS, from where y is stored in whole
+// lines.  blockIdx.z: a slice of the columns, its sums left in the workspace
+// where there are several.
+//
+// 256 8-bit rows of 2560 to 10576, groups of 128: 27 us, of which 3 the launch,
+// 5 before and after the turns.  LDS reads, conversions and products would take
+// 7.4, 6.5 and 5.5 us of each CU; with two waves per SIMD that meet at every
+// turn they mostly go one after another.  One block a turn without halves: 34 us;
+// x straight to registers, every wave all of a tile's rows: 42 us (16 bytes of
+// each of 16 rows a load); more blocks under way from memory: no change.
+constexpr int kBN = 128;
 constexpr int kXP = kBlk + 8;  // pitch of a row of x in LDS: 16 rows in 16 bytes meet all banks once
-template <typename XT, bool FINE, bool XV, typename YT>
-__global__ __launch_bounds__(256) void s6_q4_many_kernel(Q4Args a) {
-  __shared__ __attribute__((aligned(16))) uint16_t xt[2][kBM][kXP];
+constexpr int kYP = kBN + 4;   // pitch of a row of sums
+constexpr size_t many_lds(int bm) { return (size_t)2 * 2 * bm * kXP * sizeof(uint16_t); }
+static_assert(many_lds(32) >= 32 * kYP * sizeof(float), "the sums take the place of x");
+template <typename XT, int BM, bool FINE, bool XV, typename YT>
+__global__ __launch_bounds__(512, 4) void s6_q4_many_kernel(Q4Args a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   using X = X8<XT, XV>;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int i = lane & 15, q = lane >> 4;
-  const int64_t n0 = (a.base + blockIdx.x) * kBN + 32 * wave, t0 = (int64_t)blockIdx.y * kBM;
-  const WRows<FINE> w0(a, n0), w1(a, n0 + 16);
+  using Tile = uint16_t(*)[kXP];
   constexpr uint32_t kE = sizeof(XT);
-  const int rows = a.rows - t0 < kBM ? (int)(a.rows - t0) : kBM;
+  constexpr int M = BM / 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 2;
+  const int i = lane & 15, q = lane >> 4;
+  const int64_t m0 = (a.base + blockIdx.x) * kBN, t0 = (int64_t)blockIdx.y * BM;
+  const int n0 = 32 * (wave & 3);
+  const WRows<FINE> w0(a, m0 + n0), w1(a, m0 + n0 + 16);
+  const int rows = a.rows - t0 < BM ? (int)(a.rows - t0) : BM;
   const uint32_t step = (uint32_t)a.x_stride * kE;
   const __amdgpu_buffer_rsrc_t xb =
       buffer_at(static_cast<const XT*>(a.x) + t0 * a.x_stride, (uint32_t)(rows - 1) * step + (uint32_t)a.inner * kE);
   const int nb = (a.inner + kBlk - 1) / kBlk;
   const int lo = blockIdx.z * a.slice, hi = lo + a.slice < nb ? lo + a.slice : nb;
-  // staging: thread c has eight columns, 8 (c % 16) on, of rows c / 16 + 16 m
-  const int sc = 8 * (threadIdx.x & 15), sr = threadIdx.x >> 4;
-  X xr[4];
-  typename WRows<FINE>::Block b0, b1;
-  uint32_t x_at[4];
+  // what lies past the slice is 0 (no branch around loads, which would make
+  // them wait for one another)
+  const int end = (int64_t)hi * kBlk < a.inner ? hi * kBlk : a.inner;
+  // staging: a thread has eight columns, 8 (c % 16) on, of rows c / 16 + 16 m of
+  // its half's block
+  const int c = threadIdx.x & 255, sc = 8 * (c & 15), sr = c >> 4;
+  X xr[M];
+  typename WRows<FINE>::Block wb[2];
+  uint32_t x_at[M];
 #pragma unroll
-  for (int m = 0; m < 4; ++m) x_at[m] = sr + 16 * m < rows ? (sr + 16 * m) * step + sc * kE : kNoRow;
+  for (int m = 0; m < M; ++m) x_at[m] = sr + 16 * m < rows ? (sr + 16 * m) * step + sc * kE : kNoRow;
   auto load = [&](int b) {
-    w0.load(b0, b);
-    w1.load(b1, b);
+    w0.load(wb[0], b, end);
+    w1.load(wb[1], b, end);
     const int k = b * kBlk;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) xr[m].load(xb, !FINE || k + sc < a.inner ? x_at[m] + (uint32_t)k * kE : kNoColumn);
+    for (int m = 0; m < M; ++m)
+      xr[m].load(xb, FINE ? (k + sc < end ? x_at[m] + (uint32_t)k * kE : kNoColumn)
+                          : x_at[m] + (k < end ? (uint32_t)k * kE : kNoColumn));
   };
-  f32x4 sum[2][4];
+  f32x4 sum[2][M];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) sum[h][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  load(lo);
-  for (int b = lo; b < hi; ++b) {
-    uint16_t(*x)[kXP] = xt[(b - lo) & 1];
+    for (int u = 0; u < M; ++u) sum[h][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  load(lo + half);
+  for (int b = lo; b < hi; b += 2) {
+    Tile x = reinterpret_cast<Tile>(lds) + (((b - lo) & 2) + half) * BM;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int m = 0; m < M; ++m) {
       bf16x8 v[1];
       xr[m].get(v);
       *reinterpret_cast<bf16x8*>(&x[sr + 16 * m][sc]) = v[0];
     }
-    typename WRows<FINE>::Block c0 = b0, c1 = b1;
+    typename WRows<FINE>::Block c0 = wb[0], c1 = wb[1];
+    // (a turn's tiles were last read two turns ago, before the barrier of the
+    // turn between)
     __syncthreads();
-    if (b + 1 < hi) load(b + 1);
+    load(b + 2 + half);
     if constexpr (FINE) {
       transpose4(c0.c);
       transpose4(c1.c);
@@ -335,12 +358,12 @@ __global__ __launch_bounds__(256) void s6_q4_many_kernel(Q4Args a) {
     float s0[4], s1[4];
     scales_of<FINE>(c0.s, s0);
     scales_of<FINE>(c1.s, s1);
-    f32x4 acc[2][4];
+    f32x4 acc[2][M];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bf16x8 v0 = values8(c0.c[j]), v1 = values8(c1.c[j]);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < M; ++u) {
         const bf16x8 xv = *reinterpret_cast<const bf16x8*>(&x[16 * u + i][FINE ? 32 * j + 8 * q : 32 * q + 8 * j]);
         if (FINE || j == 0) acc[0][u] = acc[1][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         acc[0][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, v0, acc[0][u], 0, 0, 0);
@@ -348,7 +371,7 @@ __global__ __launch_bounds__(256) void s6_q4_many_kernel(Q4Args a) {
       }
       if (FINE || j == 3) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < M; ++u)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             sum[0][u][r] = __builtin_fmaf(s0[j], acc[0][u][r], sum[0][u][r]);
@@ -357,21 +380,48 @@ __global__ __launch_bounds__(256) void s6_q4_many_kernel(Q4Args a) {
       }
     }
   }
+  float(*ys)[kYP] = reinterpret_cast<float(*)[kYP]>(lds);
+  __syncthreads();
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t n = n0 + 16 * h + i;
-    if (n >= a.outer) continue;
+  for (int pass = 0; pass < 2; ++pass) {
+    if (half == pass) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t t = t0 + 16 * u + 4 * q + r;
-        if (t >= a.rows) continue;
-        if (a.parts)
-          a.parts[((int64_t)blockIdx.z * a.rows + t) * a.outer + n] = sum[h][u][r];
-        else
-          static_cast<YT*>(a.y)[t * a.outer + n] = from_f32<YT>(sum[h][u][r] * (a.x_scale ? a.x_scale[t] : 1.0f));
-      }
+        for (int u = 0; u < M; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float* p = &ys[16 * u + 4 * q + r][n0 + 16 * h + i];
+            *p = pass == 0 ? sum[h][u][r] : *p + sum[h][u][r];
+          }
+    }
+    __syncthreads();
+  }
+  // eight columns of a row to a thread
+  const int64_t left = a.outer - m0;
+  const bool wide = a.wide && left >= kBN;
+#pragma unroll
+  for (int m = 0; m < BM / 32; ++m) {
+    const int t = (threadIdx.x >> 4) + 32 * m, n = 8 * (threadIdx.x & 15);
+    if (t >= rows) continue;
+    float v[8];
+    load_vec<float, 8>(&ys[t][n], v);
+    const float xs = a.x_scale && !a.parts ? a.x_scale[t0 + t] : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= xs;
+    const int64_t at = (t0 + t) * a.outer + m0 + n;
+    if (a.parts) {
+      float* p = a.parts + (int64_t)blockIdx.z * a.rows * a.outer + at;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (n + e < left) p[e] = v[e];
+    } else if (wide) {
+      store_vec<YT, 8>(static_cast<YT*>(a.y) + at, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (n + e < left) static_cast<YT*>(a.y)[at + e] = from_f32<YT>(v[e]);
+    }
   }
 }
 
@@ -445,12 +495,17 @@ int check_q4(int64_t rows, int64_t inner, int64_t outer, int64_t group, int64_t 
 constexpr int64_t kFewRows = 32;          // most rows of the first kernel (fp32: any number)
 constexpr int64_t kLaunchRows = 32768;    // most rows of a launch of the second
 
-// Slices of the columns for the second kernel: two workgroups per CU where
-// there are columns for it, of at least four blocks each.  They cost a pass over
-// their sums.
+// Rows of x to a workgroup of the second kernel.  Measured with 32 and with 64, us:
+// 64 bf16 rows of 2560 to 10576: 16 and 21; 128 of 5120 to 2560, groups of 32: 18
+// and 21; 256 of 2560 to 10576: 34 and 29.
+int64_t many_rows(int64_t rows) { return rows <= 128 ? 32 : 64; }
+
+// Slices of the columns for the second kernel: a workgroup per CU where there
+// are columns for it, of at least four blocks each.  They cost a pass over their
+// sums.
 int64_t slices_of(int64_t rows, int64_t inner, int64_t outer, int64_t* slice) {
-  const int64_t nb = (inner + kBlk - 1) / kBlk, n = rows < kLaunchRows ? rows : kLaunchRows;
-  const int64_t tiles = ((outer + kBN - 1) / kBN) * ((n + kBM - 1) / kBM);
+  const int64_t nb = (inner + kBlk - 1) / kBlk, n = rows < kLaunchRows ? rows : kLaunchRows, bm = many_rows(n);
+  const int64_t tiles = ((outer + kBN - 1) / kBN) * ((n + bm - 1) / bm);
   int64_t s = cu_count() / (tiles > 0 ? tiles : 1);
   if (s > nb / 4) s = nb / 4;
   if (s < 1) s = 1;
@@ -473,21 +528,24 @@ int launch_few(Q4Args a, hipStream_t st) {
   }
   return S6_OK;
 }
-template <typename XT, bool FINE, bool XV, typename YT>
+template <typename XT, int BM, bool FINE, bool XV, typename YT>
 int launch_many(Q4Args a, int64_t slices, hipStream_t st) {
-  if constexpr (sizeof(XT) < 4) {
-    const int64_t tiles = (a.outer + kBN - 1) / kBN;
-    for (a.base = 0; a.base < tiles; a.base += kMaxGrid) {
-      const dim3 grid((unsigned)(tiles - a.base < kMaxGrid ? tiles - a.base : kMaxGrid),
-                      (unsigned)((a.rows + kBM - 1) / kBM), (unsigned)slices);
-      hipLaunchKernelGGL((s6_q4_many_kernel<XT, FINE, XV, YT>), grid, dim3(256), 0, st, a);
-      S6_HIP(hipGetLastError(), "s6_q4_many_kernel launch");
-    }
-    if (slices > 1) {
-      hipLaunchKernelGGL(s6_q4_join_kernel<YT>, dim3((unsigned)((a.outer + 255) / 256), (unsigned)a.rows), dim3(256), 0, st,
-                         a, (int)slices);
-      S6_HIP(hipGetLastError(), "s6_q4_join_kernel launch");
-    }
+  const auto kern = s6_q4_many_kernel<XT, BM, FINE, XV, YT>;
+  constexpr size_t lds = many_lds(BM);
+  if constexpr (lds > 65536)
+    S6_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds),
+           "s6_q4_many_kernel LDS size");
+  const int64_t tiles = (a.outer + kBN - 1) / kBN;
+  for (a.base = 0; a.base < tiles; a.base += kMaxGrid) {
+    const dim3 grid((unsigned)(tiles - a.base < kMaxGrid ? tiles - a.base : kMaxGrid), (unsigned)((a.rows + BM - 1) / BM),
+                    (unsigned)slices);
+    hipLaunchKernelGGL(kern, grid, dim3(512), lds, st, a);
+    S6_HIP(hipGetLastError(), "s6_q4_many_kernel launch");
+  }
+  if (slices > 1) {
+    hipLaunchKernelGGL(s6_q4_join_kernel<YT>, dim3((unsigned)((a.outer + 255) / 256), (unsigned)a.rows), dim3(256), 0, st,
+                       a, (int)slices);
+    S6_HIP(hipGetLastError(), "s6_q4_join_kernel launch");
   }
   return S6_OK;
 }
@@ -504,9 +562,13 @@ int launch_rows(const Q4Args& a, hipStream_t st) {
     b.y = static_cast<YT*>(a.y) + r * a.outer;
     b.slice = (int)slice;
     if (slices == 1) b.parts = nullptr;
-    const int rc = !few          ? launch_many<XT, FINE, XV, YT>(b, slices, st)
-                   : b.rows > 16 ? launch_few<XT, 2, FINE, XV, YT>(b, st)
-                                 : launch_few<XT, 1, FINE, XV, YT>(b, st);
+    int rc;
+    if (few) {
+      rc = b.rows > 16 ? launch_few<XT, 2, FINE, XV, YT>(b, st) : launch_few<XT, 1, FINE, XV, YT>(b, st);
+    } else if constexpr (sizeof(XT) < 4) {
+      rc = many_rows(a.rows < kLaunchRows ? a.rows : kLaunchRows) == 32 ? launch_many<XT, 32, FINE, XV, YT>(b, slices, st)
+                                                                        : launch_many<XT, 64, FINE, XV, YT>(b, slices, st);
+    }
     if (rc) return rc;
   }
   return S6_OK;
@@ -593,6 +655,7 @@ int s6_q4_linear(int64_t rows, int64_t inner, int64_t outer, int64_t group, int 
   a.rows = rows; a.inner = (int)inner; a.outer = outer; a.x_stride = x_stride;
   a.fine = group == 128 ? 0 : group == 64 ? 1 : 2; a.ngroups = (int)(inner / group);
   a.parts = static_cast<float*>(workspace);
+  a.wide = aligned(y, 16) && (outer * (int64_t)ysz) % 16 == 0;
   const bool vec = aligned(x, 16) && (x_stride * (int64_t)xsz) % 16 == 0;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (x_dtype == S6_F32)

@@ -8,12 +8,14 @@ the recurrence for torch autograd (once differentiable).
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import s6
-from .block import _at, _dtype, _launch, _need, _rows, _same_device, _unasked, _whole, _workspace, _written
+from .block import (_at, _dtype, _launch, _need, _plain, _rows, _same_device, _unasked, _whole, _workspace,
+                    _written)
 from .s6 import _DT
 
 S6_UNIT_INPUT = 4
@@ -25,6 +27,13 @@ class GatedDims(ctypes.Structure):
 
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("batch", "seqlen", "dim", "x_batch", "x_token", "a_batch", "a_token", "g_batch", "g_token")]
+
+
+@functools.lru_cache(maxsize=256)
+def _struct(*sizes):
+    """(the dims of these sizes and strides, a reference to them)."""
+    d = GatedDims(*sizes)
+    return d, ctypes.byref(d)
 
 
 _lib = None
@@ -54,27 +63,37 @@ def _gated_dims(x, gate_a, gate_x, A, bias_a, bias_x, unit_input, tokens):
     dt = _dtype(x)
     if x.dim() != (3 if tokens else 2):
         raise ValueError("x and the gates are (batch, seqlen, dim); (batch, dim) for a single token")
-    shape = x.shape
-    xs = _rows(x, "x", shape, dt, 1)
-    gs = _rows(gate_a, "gate_a", shape, dt, 1)
+    shape, index = x.shape, x.get_device()
+    xs = _strides(x, "x", shape, dt, index)
+    gs = _strides(gate_a, "gate_a", shape, dt, index)
     if gate_x is None:
         if bias_x is not None:
             raise ValueError("bias_x needs a gate_x")
         ys = (0,) * len(xs)
     else:
-        ys = _rows(gate_x, "gate_x", shape, dt, 1)
+        ys = _strides(gate_x, "gate_x", shape, dt, index)
+    channels = shape[-1:]
     if A is None:
         raise ValueError("A is required")
-    channels = shape[-1:]
-    _whole(A, "A", channels)
-    _whole(bias_a, "bias_a", channels)
-    _whole(bias_x, "bias_x", channels)
-    _same_device(x, gate_a, gate_x, A, bias_a, bias_x)
+    for t, name in ((A, "A"), (bias_a, "bias_a"), (bias_x, "bias_x")):
+        if t is not None and not _plain(t, channels, torch.float32, index):
+            _whole(t, name, channels)
+            _same_device(x, t)
     if tokens:
-        dims = GatedDims(*shape, *xs, *gs, *ys)
+        dims, ref = _struct(*shape, *xs, *gs, *ys)
     else:
-        dims = GatedDims(shape[0], 1, shape[1], xs[0], 0, gs[0], 0, ys[0], 0)
-    return dims, _DT[dt], S6_UNIT_INPUT if unit_input else 0
+        dims, ref = _struct(shape[0], 1, shape[1], xs[0], 0, gs[0], 0, ys[0], 0)
+    return dims, ref, _DT[dt], S6_UNIT_INPUT if unit_input else 0
+
+
+def _strides(t, name, shape, dt, index):
+    """Strides of the leading dimensions."""
+    if t is not None and index >= 0 and _plain(t, shape, dt, index):
+        return t.stride()[:-1]
+    st = _rows(t, name, shape, dt, 1)
+    if t.get_device() != index:
+        raise ValueError(f"tensors on cuda:{index} and {t.device}")
+    return st
 
 
 def _starts(starts, x):
@@ -103,24 +122,29 @@ def gated_scan_fwd(x, gate_a, gate_x, A, bias_a=None, bias_x=None, h0=None, star
     tokens that begin a sequence of their own.  Returns y like x (contiguous);
     h_last (batch, dim) fp32 if requested; with return_states the state
     entering every 128 tokens, for gated_scan_bwd."""
-    dims, dt, flags = _gated_dims(x, gate_a, gate_x, A, bias_a, bias_x, unit_input, True)
+    dims, ref, dt, flags = _gated_dims(x, gate_a, gate_x, A, bias_a, bias_x, unit_input, True)
     sshape = (dims.batch, dims.dim)
     starts = _starts(starts, x)
-    _whole(h0, "h0", sshape)
-    _whole(y, "y", x.shape, x.dtype)
-    _whole(h_last, "h_last", sshape)
-    _whole(states, "states", _states_shape(x))
-    _same_device(x, h0, y, h_last, states)
-    _written(y, h_last, states)
+    if h0 is not None:
+        _whole(h0, "h0", sshape)
+        _same_device(x, h0)
+    if y is not None or h_last is not None or states is not None:
+        _whole(y, "y", x.shape, x.dtype)
+        _whole(h_last, "h_last", sshape)
+        _whole(states, "states", _states_shape(x))
+        _same_device(x, y, h_last, states)
+        _written(y, h_last, states)
     if y is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
     if return_last_state and h_last is None:
-        h_last = torch.empty(sshape, dtype=torch.float32, device=x.device)
+        h_last = x.new_empty(sshape, dtype=torch.float32)
     if return_states and states is None:
-        states = torch.empty(_states_shape(x), dtype=torch.float32, device=x.device)
+        states = x.new_empty(_states_shape(x), dtype=torch.float32)
     lib = _load()
-    ref = ctypes.byref(dims)
-    keep, wsp, wsn = _workspace(lib.s6_gated_scan_fwd_workspace_size, x, ref)
+    keep = wsp = None
+    wsn = 0
+    if dims.seqlen > TOKENS:
+        keep, wsp, wsn = _workspace(lib.s6_gated_scan_fwd_workspace_size, x, ref)
     _launch(lib.s6_gated_scan_fwd, x, ref, dt, flags, _at(x), _at(gate_a), _at(bias_a), _at(gate_x), _at(bias_x), _at(A),
             _at(starts), _at(h0), _at(y), _at(h_last), _at(states), wsp, wsn)
     del keep
@@ -136,7 +160,7 @@ def gated_scan_bwd(x, gate_a, gate_x, A, dy, bias_a=None, bias_x=None, h0=None, 
     dgate_a, and where gate_x is given dgate_x, in the input dtype; dA, and
     where their input is given dbias_a, dbias_x, dh0 in fp32.  skip: names
     among the last four to leave out."""
-    dims, dt, flags = _gated_dims(x, gate_a, gate_x, A, bias_a, bias_x, unit_input, True)
+    dims, ref, dt, flags = _gated_dims(x, gate_a, gate_x, A, bias_a, bias_x, unit_input, True)
     sshape = (dims.batch, dims.dim)
     starts = _starts(starts, x)
     _whole(h0, "h0", sshape)
@@ -151,7 +175,6 @@ def gated_scan_bwd(x, gate_a, gate_x, A, dy, bias_a=None, bias_x=None, h0=None, 
         if t is not None and name not in skip:
             g[name] = torch.empty_like(t)
     lib = _load()
-    ref = ctypes.byref(dims)
     keep, wsp, wsn = _workspace(lib.s6_gated_scan_bwd_workspace_size, x, ref, int(states is not None))
     _launch(lib.s6_gated_scan_bwd, x, ref, dt, flags, _at(x), _at(gate_a), _at(bias_a), _at(gate_x), _at(bias_x), _at(A),
             _at(starts), _at(h0), _at(states), _at(dy), _at(dh_last), _at(g["dx"]), _at(g["dgate_a"]),
@@ -164,14 +187,17 @@ def gated_scan_bwd(x, gate_a, gate_x, A, dy, bias_a=None, bias_x=None, h0=None, 
 def gated_state_update(h, x, gate_a, gate_x, A, bias_a=None, bias_x=None, unit_input=False, y=None):
     """One token of every sequence: h (batch, dim) fp32 is advanced in place;
     x, gate_a, gate_x: (batch, dim).  Returns y (batch, dim) in x's dtype."""
-    dims, dt, flags = _gated_dims(x, gate_a, gate_x, A, bias_a, bias_x, unit_input, False)
-    _whole(_need(h, "h", x.shape, torch.float32), "h", x.shape)
-    _whole(y, "y", x.shape, x.dtype)
-    _same_device(x, h, y)
+    dims, ref, dt, flags = _gated_dims(x, gate_a, gate_x, A, bias_a, bias_x, unit_input, False)
+    if h is None or not _plain(h, x.shape, torch.float32, x.get_device()):
+        _whole(_need(h, "h", x.shape, torch.float32), "h", x.shape)
+        _same_device(x, h)
+    if y is not None:
+        _whole(y, "y", x.shape, x.dtype)
+        _same_device(x, y)
     _written(h, y)
     if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    _launch(_load().s6_gated_state_update, x, ctypes.byref(dims), dt, flags, _at(h), _at(x), _at(gate_a), _at(bias_a),
+        y = x.new_empty(x.shape)
+    _launch(_load().s6_gated_state_update, x, ref, dt, flags, _at(h), _at(x), _at(gate_a), _at(bias_a),
             _at(gate_x), _at(bias_x), _at(A), _at(y))
     return y
 

@@ -13,11 +13,12 @@ import math
 import torch
 
 from . import s6
-from .block import _at, _dtype, _flat, _launch, _need, _same_device, _weight, _whole, _workspace, _written
+from .block import _at, _dtype, _flat, _launch, _plain, _same_device, _weight, _whole, _workspace, _written
 from .s6 import _DT
 
 S6_E4M3 = 2
 GROUPS = (32, 64, 128)
+FEW = 32  # rows that need no workspace
 _XT = {**_DT, torch.float8_e4m3fn: S6_E4M3}
 
 _lib = None
@@ -77,23 +78,34 @@ def q4_linear(x, weight, scales, x_scale=None, out_dtype=None, y=None):
     if ngroups == 0 or inner % ngroups or inner // ngroups not in GROUPS:
         raise ValueError(f"{ngroups} scales for {inner} columns: groups have 32, 64 or 128")
     lead = x.shape[:-1]
-    stride = _flat(x, "x", x.shape, dt)
-    _whole(weight, "weight", (outer, inner // 2), torch.uint8)
-    _whole(scales, "scales", (outer, ngroups), torch.bfloat16)
+    index = x.get_device()
+    stride = inner if index >= 0 and x.is_contiguous() else _flat(x, "x", x.shape, dt)
+    if not (_plain(weight, (outer, inner // 2), torch.uint8, index) and
+            _plain(scales, (outer, ngroups), torch.bfloat16, index)):
+        _whole(weight, "weight", (outer, inner // 2), torch.uint8)
+        _whole(scales, "scales", (outer, ngroups), torch.bfloat16)
+        _same_device(x, weight, scales)
     if x_scale is not None:
         if dt != torch.float8_e4m3fn:
             raise ValueError("x_scale goes with 8-bit rows")
-        _whole(x_scale, "x_scale", lead)
-    _whole(y, "y", (*lead, outer), yt)
-    _same_device(x, weight, scales, x_scale, y)
-    _written(y)
-    if y is None:
-        y = torch.empty((*lead, outer), dtype=yt, device=x.device)
+        if not _plain(x_scale, lead, torch.float32, index):
+            _whole(x_scale, "x_scale", lead)
+            _same_device(x, x_scale)
+    if y is not None:
+        _whole(y, "y", (*lead, outer), yt)
+        _same_device(x, y)
+        _written(y)
+    else:
+        y = x.new_empty((*lead, outer), dtype=yt)
     lib = _load()
     rows = math.prod(lead)
-    args = (rows, inner, outer, inner // ngroups, _XT[dt])
-    keep, wsp, wsn = _workspace(lib.s6_q4_linear_workspace_size, x, *args)
-    _launch(lib.s6_q4_linear, x, *args, _DT[yt], _at(x), stride, _at(x_scale), _at(weight), _at(scales), _at(y), wsp, wsn)
+    group = inner // ngroups
+    keep = wsp = None
+    wsn = 0
+    if rows > FEW:
+        keep, wsp, wsn = _workspace(lib.s6_q4_linear_workspace_size, x, rows, inner, outer, group, _XT[dt])
+    _launch(lib.s6_q4_linear, x, rows, inner, outer, group, _XT[dt], _DT[yt], x.data_ptr(), stride, _at(x_scale),
+            weight.data_ptr(), scales.data_ptr(), y.data_ptr(), wsp, wsn)
     del keep
     return y
 
@@ -106,25 +118,33 @@ def add_norm_q8_fwd(x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5, r
     (out in float8_e4m3fn, out_scale (...) fp32, r' in the residual's dtype);
     residual_out may be the residual itself."""
     dt = _dtype(x)
-    stride = _flat(x, "x", x.shape, dt)
+    stride = x.shape[-1] if x.is_contiguous() and x.is_cuda else _flat(x, "x", x.shape, dt)
     rt = residual.dtype if residual is not None else residual_dtype or torch.float32
     if rt not in (torch.float32, dt):
         raise ValueError(f"residual dtype {rt}: expected float32 or {dt}")
     dim, lead = x.shape[-1], x.shape[:-1]
-    _whole(residual, "residual", x.shape, rt)
-    _weight(weight, dim)
-    _whole(gamma, "gamma", (dim,))
-    _whole(out, "out", x.shape, torch.float8_e4m3fn)
-    _whole(out_scale, "out_scale", lead)
-    _whole(residual_out, "residual_out", x.shape, rt)
-    _same_device(x, weight, residual, gamma, out, out_scale, residual_out)
-    _written(out, out_scale, residual_out)
+    index = x.get_device()
+    if residual is not None and not _plain(residual, x.shape, rt, index):
+        _whole(residual, "residual", x.shape, rt)
+        _same_device(x, residual)
+    if weight is None or not _plain(weight, (dim,), torch.float32, index):
+        _weight(weight, dim)
+        _same_device(x, weight)
+    if gamma is not None and not _plain(gamma, (dim,), torch.float32, index):
+        _whole(gamma, "gamma", (dim,))
+        _same_device(x, gamma)
+    if out is not None or out_scale is not None or residual_out is not None:
+        _whole(out, "out", x.shape, torch.float8_e4m3fn)
+        _whole(out_scale, "out_scale", lead)
+        _whole(residual_out, "residual_out", x.shape, rt)
+        _same_device(x, out, out_scale, residual_out)
+        _written(out, out_scale, residual_out)
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        out = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
     if out_scale is None:
-        out_scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+        out_scale = x.new_empty(lead, dtype=torch.float32)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=rt, device=x.device)
-    _launch(_load().s6_add_norm_q8_fwd, x, math.prod(lead), dim, _DT[dt], _DT[rt], _at(x), stride, _at(residual),
-            _at(weight), _at(gamma), scale, eps, _at(out), _at(out_scale), _at(residual_out))
+        residual_out = x.new_empty(x.shape, dtype=rt)
+    _launch(_load().s6_add_norm_q8_fwd, x, math.prod(lead), dim, _DT[dt], _DT[rt], x.data_ptr(), stride, _at(residual),
+            weight.data_ptr(), _at(gamma), scale, eps, out.data_ptr(), out_scale.data_ptr(), residual_out.data_ptr())
     return out, out_scale, residual_out
