@@ -14,9 +14,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import s6
-from .block import (_at, _dtype, _launch, _need, _plain, _rows, _same_device, _unasked, _whole, _workspace,
-                    _written)
-from .s6 import _DT
+from .block import _at, _dtype, _launch, _need, _plain, _rows, _same_device, _unasked, _whole, _written
+from .s6 import _DT, _check
 
 S6_UNIT_INPUT = 4
 TOKENS = 128  # tokens from one stored state to the next (S6_GATED_TOKENS)
@@ -34,6 +33,29 @@ def _struct(*sizes):
     """(the dims of these sizes and strides, a reference to them)."""
     d = GatedDims(*sizes)
     return d, ctypes.byref(d)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(index, batch, seqlen, dim, back, has_states):
+    """Bytes of workspace for these sizes on device `index`."""
+    d, ref = _struct(batch, seqlen, dim, 0, 0, 0, 0, 0, 0)
+    out = ctypes.c_size_t(0)
+    lib = _load()
+    with torch.cuda.device(index):
+        if back:
+            _check(lib.s6_gated_scan_bwd_workspace_size(ref, has_states, ctypes.byref(out)))
+        else:
+            _check(lib.s6_gated_scan_fwd_workspace_size(ref, ctypes.byref(out)))
+    return out.value
+
+
+def _workspace(x, dims, back=False, has_states=False):
+    """(tensor, pointer, bytes) of a fresh workspace on the current stream."""
+    n = _workspace_bytes(x.get_device(), dims.batch, dims.seqlen, dims.dim, back, has_states)
+    if n == 0:
+        return None, None, 0
+    t = x.new_empty(n, dtype=torch.uint8)
+    return t, t.data_ptr(), n
 
 
 _lib = None
@@ -88,8 +110,10 @@ def _gated_dims(x, gate_a, gate_x, A, bias_a, bias_x, unit_input, tokens):
 
 def _strides(t, name, shape, dt, index):
     """Strides of the leading dimensions."""
-    if t is not None and index >= 0 and _plain(t, shape, dt, index):
-        return t.stride()[:-1]
+    if t is not None and index >= 0 and t.shape == shape and t.dtype is dt and t.get_device() == index:
+        st = t.stride()
+        if st[-1] == 1 and 1 not in shape:
+            return st[:-1]
     st = _rows(t, name, shape, dt, 1)
     if t.get_device() != index:
         raise ValueError(f"tensors on cuda:{index} and {t.device}")
@@ -141,10 +165,7 @@ def gated_scan_fwd(x, gate_a, gate_x, A, bias_a=None, bias_x=None, h0=None, star
     if return_states and states is None:
         states = x.new_empty(_states_shape(x), dtype=torch.float32)
     lib = _load()
-    keep = wsp = None
-    wsn = 0
-    if dims.seqlen > TOKENS:
-        keep, wsp, wsn = _workspace(lib.s6_gated_scan_fwd_workspace_size, x, ref)
+    keep, wsp, wsn = _workspace(x, dims)
     _launch(lib.s6_gated_scan_fwd, x, ref, dt, flags, _at(x), _at(gate_a), _at(bias_a), _at(gate_x), _at(bias_x), _at(A),
             _at(starts), _at(h0), _at(y), _at(h_last), _at(states), wsp, wsn)
     del keep
@@ -175,7 +196,7 @@ def gated_scan_bwd(x, gate_a, gate_x, A, dy, bias_a=None, bias_x=None, h0=None, 
         if t is not None and name not in skip:
             g[name] = torch.empty_like(t)
     lib = _load()
-    keep, wsp, wsn = _workspace(lib.s6_gated_scan_bwd_workspace_size, x, ref, int(states is not None))
+    keep, wsp, wsn = _workspace(x, dims, True, states is not None)
     _launch(lib.s6_gated_scan_bwd, x, ref, dt, flags, _at(x), _at(gate_a), _at(bias_a), _at(gate_x), _at(bias_x), _at(A),
             _at(starts), _at(h0), _at(states), _at(dy), _at(dh_last), _at(g["dx"]), _at(g["dgate_a"]),
             _at(g.get("dgate_x")), _at(g.get("dA")), _at(g.get("dbias_a")), _at(g.get("dbias_x")), _at(g.get("dh0")), wsp,
