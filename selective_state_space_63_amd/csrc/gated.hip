@@ -29,9 +29,16 @@ namespace {
 
 constexpr int kGC = 64;                // channels of a tile
 constexpr int kGT = S6_GATED_TOKENS;   // tokens of a tile
-constexpr int kWaves = 8;              // waves of a workgroup
 constexpr int kMaxTiles = 1 << 22; // workgroups of a launch (threads below 2^32)
-constexpr int kFwdWaves = 6, kBwdWaves = 4;  // waves per SIMD that the registers leave room for
+// Waves of a workgroup, and of a SIMD, which the registers leave room for.  The
+// forward on pairs of bf16: four of 16 tokens by two channels per lane, 124
+// VGPRs (eight of 8 tokens, six per SIMD: 65536 tokens of 1536 237 us, else 222);
+// fp32 would spill there.
+template <typename In, int VEC>
+constexpr int kFwdW = sizeof(In) == 2 && VEC == 2 ? 4 : 8;
+template <typename In, int VEC>
+constexpr int kFwdWaves = kFwdW<In, VEC> == 4 ? 4 : 6;
+constexpr int kBwdW = 8, kBwdWaves = 4;
 constexpr int kClasses = 64;           // counters of tiles, each in a line of its own
 constexpr int kTicketStep = 32;        // words from one to the next
 
@@ -198,20 +205,20 @@ __device__ __forceinline__ float one_less_square(float v2, float a) {
   return v2 > -0.13f ? -v2 * s : __builtin_fmaf(-a, a, 1.0f);
 }
 
-// Where a lane's tokens lie: kWaves * VEC groups of T tokens, VEC groups to a
+// Where a lane's tokens lie: W * VEC groups of T tokens, VEC groups to a
 // wave (64 / VEC lanes of VEC channels each).  Tiles and columns of tiles are
 // counted in 32 bits (the host sees to it).
-template <int VEC>
+template <int VEC, int W>
 struct Place {
-  static constexpr int G = kWaves * VEC, T = kGT / G;
+  static constexpr int G = W * VEC, T = kGT / G;
   int group, half, cl, nt;  // half: the group in its wave; nt: tokens of the group that exist
   int col, q, k, b, c0;     // c0: first channel of the tile
   int64_t w0;               // first token of the wave
   bool on;                  // the lane's channels exist
 };
-template <int VEC, bool BACK>
-__device__ __forceinline__ Place<VEC> place_of(const GatedArgs& a, int tile) {
-  using P = Place<VEC>;
+template <int VEC, int W, bool BACK>
+__device__ __forceinline__ Place<VEC, W> place_of(const GatedArgs& a, int tile) {
+  using P = Place<VEC, W>;
   P p;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   p.half = VEC == 2 ? lane >> 5 : 0;
@@ -255,10 +262,10 @@ struct Rows {
   __amdgpu_buffer_rsrc_t buf;
   uint32_t lane, step;  // bytes: of the lane's first piece, from token to token
 };
-template <typename In, int VEC>
+template <typename In, int VEC, int W>
 __device__ __forceinline__ Rows rows_of(const void* base, int64_t batch_stride, int64_t token_stride, const GatedArgs& a,
-                                        const Place<VEC>& p) {
-  constexpr int n = VEC * Place<VEC>::T;
+                                        const Place<VEC, W>& p) {
+  constexpr int n = VEC * Place<VEC, W>::T;
   const int64_t left = a.L - p.w0;
   const uint32_t rows = left < 0 || !base ? 0 : left < n ? (uint32_t)left : n;
   const uint32_t cols = a.dim - p.c0 < kGC ? (uint32_t)(a.dim - p.c0) : kGC;
@@ -270,30 +277,31 @@ __device__ __forceinline__ Rows rows_of(const void* base, int64_t batch_stride, 
   r.buf = __builtin_amdgcn_make_buffer_rsrc(
       reinterpret_cast<void*>(at), 0,
       __builtin_amdgcn_readfirstlane(rows > 0 ? (rows - 1) * r.step + cols * (uint32_t)sizeof(In) : 0u), 0x00027000);
-  r.lane = p.half * (Place<VEC>::T * r.step) + p.cl * (uint32_t)sizeof(In);
+  r.lane = p.half * (Place<VEC, W>::T * r.step) + p.cl * (uint32_t)sizeof(In);
   return r;
 }
-template <typename In, int VEC>
-__device__ __forceinline__ void load_rows(Piece<In, VEC> (&o)[Place<VEC>::T], const Rows& r) {
+template <typename In, int VEC, int T>
+__device__ __forceinline__ void load_rows(Piece<In, VEC> (&o)[T], const Rows& r) {
 #pragma unroll
-  for (int t = 0; t < Place<VEC>::T; ++t) o[t].load(r.buf, r.lane + t * r.step);
+  for (int t = 0; t < T; ++t) o[t].load(r.buf, r.lane + t * r.step);
 }
 
 // Bit t: token t of the lane's group starts a sequence.
-template <int VEC>
-__device__ __forceinline__ uint32_t starts_of(const GatedArgs& a, const Place<VEC>& p) {
-  constexpr int T = Place<VEC>::T;
+template <int VEC, int W>
+__device__ __forceinline__ uint32_t starts_of(const GatedArgs& a, const Place<VEC, W>& p) {
+  constexpr int T = Place<VEC, W>::T;
   const int lane = threadIdx.x & 63, t = lane & (T - 1);
   bool st = false;
   if (t < p.nt) st = a.starts[p.b * a.L + p.w0 + p.half * T + t] != 0;
   const uint64_t all = __ballot(st);
-  return (uint32_t)(VEC == 2 && lane >= 32 ? all >> 32 : all) & ((1u << T) - 1);
+  return (uint32_t)(VEC == 2 && lane >= 32 ? all >> 32 : all) & (uint32_t)((1ull << T) - 1);
 }
 
 // --------------------------------------------------------------- forward --
 template <typename In, int VEC, bool UNIT, bool STARTS>
-__global__ __launch_bounds__(kWaves * 64, kFwdWaves) void s6_gated_scan_kernel(GatedArgs a) {
-  using P = Place<VEC>;
+__global__ __launch_bounds__((kFwdW<In, VEC> * 64), (kFwdWaves<In, VEC>)) void s6_gated_scan_kernel(GatedArgs a) {
+  constexpr int W = kFwdW<In, VEC>;
+  using P = Place<VEC, W>;
   constexpr int G = P::G, T = P::T;
   __shared__ float2 agg[G][kGC];
   __shared__ float hin[G][kGC];
@@ -301,15 +309,15 @@ __global__ __launch_bounds__(kWaves * 64, kFwdWaves) void s6_gated_scan_kernel(G
   __shared__ uint32_t drawn;
   const int tile = draw_tile(a, &drawn);
   if (tile >= a.tiles) return;
-  const P p = place_of<VEC, false>(a, tile);
+  const P p = place_of<VEC, W, false>(a, tile);
   uint64_t* const slot = a.slots + ((int64_t)p.col * a.chunks + p.q) * kGC + (threadIdx.x & 63);
   const uint64_t before = p.q > 0 && threadIdx.x < 64 ? peek(slot - kGC) : ~0ull;
   Piece<In, VEC> xr[T], ar[T], gr[T];
-  load_rows<In, VEC>(ar, rows_of<In, VEC>(a.ga, a.a_batch, a.a_token, a, p));
-  load_rows<In, VEC>(xr, rows_of<In, VEC>(a.x, a.x_batch, a.x_token, a, p));
-  load_rows<In, VEC>(gr, rows_of<In, VEC>(a.gx, a.g_batch, a.g_token, a, p));
+  load_rows(ar, rows_of<In>(a.ga, a.a_batch, a.a_token, a, p));
+  load_rows(xr, rows_of<In>(a.x, a.x_batch, a.x_token, a, p));
+  load_rows(gr, rows_of<In>(a.gx, a.g_batch, a.g_token, a, p));
   uint32_t starts = 0;
-  if constexpr (STARTS) starts = starts_of<VEC>(a, p);
+  if constexpr (STARTS) starts = starts_of(a, p);
   float A2[VEC], ba[VEC], bx[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
@@ -327,25 +335,20 @@ __global__ __launch_bounds__(kWaves * 64, kFwdWaves) void s6_gated_scan_kernel(G
     const bool st = STARTS && (starts >> t & 1);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      const float v2 = A2[v] * gate_f(ar[t].get(v), ba[v]);
-      float d = fast_exp2(v2);
+      // (at a start v = -infinity: a = 0, b = 1)
+      const float v2 = st ? -__builtin_inff() : A2[v] * gate_f(ar[t].get(v), ba[v]);
+      const float d = fast_exp2(v2);
       float u = xr[t].get(v) * gate_f(gr[t].get(v), bx[v]);
-      if constexpr (!UNIT) {
-        const float b = __builtin_amdgcn_sqrtf(one_less_square(v2, d));
-        u = st ? u : b * u;
-      }
+      if constexpr (!UNIT) u *= __builtin_amdgcn_sqrtf(one_less_square(v2, d));
       av[t][v] = d;
       uv[t][v] = u;
-      if constexpr (STARTS) {
-        d = __builtin_fabsf(d);
-        Pl[v] = st ? -0.0f : Pl[v] * d;
-        Hl[v] = st ? u : __builtin_fmaf(d, Hl[v], u);
-      } else {
-        Pl[v] *= d;
-        Hl[v] = __builtin_fmaf(d, Hl[v], u);
-      }
+      Pl[v] *= d;
+      Hl[v] = st ? u : __builtin_fmaf(d, Hl[v], u);
     }
   }
+  if constexpr (STARTS)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) Pl[v] = starts ? -0.0f : __builtin_fabsf(Pl[v]);
 #pragma unroll
   for (int v = 0; v < VEC; ++v) agg[p.group][p.cl + v] = make_float2(Pl[v], Hl[v]);
   __syncthreads();
@@ -396,7 +399,7 @@ __global__ __launch_bounds__(kWaves * 64, kFwdWaves) void s6_gated_scan_kernel(G
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h[v] = hin[p.group][p.cl + v];
   }
-  const Rows y = rows_of<In, VEC>(a.y, a.L * a.dim, a.dim, a, p);
+  const Rows y = rows_of<In>(a.y, a.L * a.dim, a.dim, a, p);
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     next(t);
@@ -406,8 +409,8 @@ __global__ __launch_bounds__(kWaves * 64, kFwdWaves) void s6_gated_scan_kernel(G
 
 // -------------------------------------------------------------- backward --
 template <typename In, int VEC, bool UNIT, bool STARTS>
-__global__ __launch_bounds__(kWaves * 64, kBwdWaves) void s6_gated_scan_bwd_kernel(GatedArgs a) {
-  using P = Place<VEC>;
+__global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kernel(GatedArgs a) {
+  using P = Place<VEC, kBwdW>;
   constexpr int G = P::G, T = P::T;
   __shared__ float agg[3][G][kGC];   // P, H, M of the groups; later the column sums
   __shared__ float ent[2][G][kGC];   // the state entering a group, the adjoint leaving it
@@ -415,16 +418,16 @@ __global__ __launch_bounds__(kWaves * 64, kBwdWaves) void s6_gated_scan_bwd_kern
   __shared__ uint32_t drawn;
   const int tile = draw_tile(a, &drawn);
   if (tile >= a.tiles) return;
-  const P p = place_of<VEC, true>(a, tile);
+  const P p = place_of<VEC, kBwdW, true>(a, tile);
   uint64_t* const slot = a.slots + ((int64_t)p.col * a.chunks + p.q) * kGC + (threadIdx.x & 63);
   const uint64_t before = p.q > 0 && threadIdx.x < 64 ? peek(slot - kGC) : ~0ull;
   Piece<In, VEC> xr[T], ar[T], gr[T], yr[T];
-  load_rows<In, VEC>(ar, rows_of<In, VEC>(a.ga, a.a_batch, a.a_token, a, p));
-  load_rows<In, VEC>(xr, rows_of<In, VEC>(a.x, a.x_batch, a.x_token, a, p));
-  load_rows<In, VEC>(gr, rows_of<In, VEC>(a.gx, a.g_batch, a.g_token, a, p));
-  load_rows<In, VEC>(yr, rows_of<In, VEC>(a.dy, a.L * a.dim, a.dim, a, p));
+  load_rows(ar, rows_of<In>(a.ga, a.a_batch, a.a_token, a, p));
+  load_rows(xr, rows_of<In>(a.x, a.x_batch, a.x_token, a, p));
+  load_rows(gr, rows_of<In>(a.gx, a.g_batch, a.g_token, a, p));
+  load_rows(yr, rows_of<In>(a.dy, a.L * a.dim, a.dim, a, p));
   uint32_t starts = 0;
-  if constexpr (STARTS) starts = starts_of<VEC>(a, p);
+  if constexpr (STARTS) starts = starts_of(a, p);
   float Ac[VEC], ba[VEC], bx[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
@@ -446,26 +449,20 @@ __global__ __launch_bounds__(kWaves * 64, kBwdWaves) void s6_gated_scan_bwd_kern
     for (int v = 0; v < VEC; ++v) {
       rv[t][v] = gate_f(ar[t].get(v), ba[v]);
       iv[t][v] = gate_f(gr[t].get(v), bx[v]);
-      const float v2 = Ac[v] * kLog2e * rv[t][v];
+      const float v2 = st ? -__builtin_inff() : Ac[v] * kLog2e * rv[t][v];
       float d = fast_exp2(v2);
       float u = iv[t][v] * xr[t].get(v);
-      if constexpr (!UNIT) {
-        const float b = __builtin_amdgcn_sqrtf(one_less_square(v2, d));
-        u = st ? u : b * u;
-      }
+      if constexpr (!UNIT) u *= __builtin_amdgcn_sqrtf(one_less_square(v2, d));
       if (t >= p.nt) d = 1.0f;
-      if constexpr (STARTS) d = __builtin_fabsf(d);
       av[t][v] = d;
       uv[t][v] = u;
-      if constexpr (STARTS) {
-        Pl[v] = st ? -0.0f : Pl[v] * d;
-        Hl[v] = st ? u : __builtin_fmaf(d, Hl[v], u);
-      } else {
-        Pl[v] *= d;
-        Hl[v] = __builtin_fmaf(d, Hl[v], u);
-      }
+      Pl[v] *= d;
+      Hl[v] = st ? u : __builtin_fmaf(d, Hl[v], u);
     }
   }
+  if constexpr (STARTS)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) Pl[v] = starts ? -0.0f : __builtin_fabsf(Pl[v]);
 #pragma unroll
   for (int t = T - 1; t >= 0; --t) {
     const bool st = STARTS && (starts >> t & 1);
@@ -536,9 +533,9 @@ __global__ __launch_bounds__(kWaves * 64, kBwdWaves) void s6_gated_scan_bwd_kern
       asm volatile("" : "+v"(rv[t][v]), "+v"(iv[t][v]));
     }
   }
-  const Rows dx = rows_of<In, VEC>(a.dx, a.L * a.dim, a.dim, a, p);
-  const Rows dga = rows_of<In, VEC>(a.dga, a.L * a.dim, a.dim, a, p);
-  const Rows dgx = rows_of<In, VEC>(a.dgx, a.L * a.dim, a.dim, a, p);
+  const Rows dx = rows_of<In>(a.dx, a.L * a.dim, a.dim, a, p);
+  const Rows dga = rows_of<In>(a.dga, a.L * a.dim, a.dim, a, p);
+  const Rows dgx = rows_of<In>(a.dgx, a.L * a.dim, a.dim, a, p);
   if (p.on) {
 #pragma unroll
     for (int t = T - 1; t >= 0; --t) {
@@ -741,7 +738,7 @@ int launch_gated(GatedArgs a, bool back, hipStream_t st) {
   a.classes = a.cols < kClasses ? a.cols : kClasses;
   const int wgs = a.slots ? (a.cols + a.classes - 1) / a.classes * a.classes * a.chunks : a.tiles;
   for (a.base = 0; a.base < wgs; a.base += kMaxTiles) {
-    const dim3 grid((unsigned)(wgs - a.base < kMaxTiles ? wgs - a.base : kMaxTiles)), block(kWaves * 64);
+    const dim3 grid((unsigned)(wgs - a.base < kMaxTiles ? wgs - a.base : kMaxTiles)), block(64 * (back ? kBwdW : kFwdW<In, VEC>));
 #define S6_GATED_LAUNCH(UNIT, STARTS)                                                              \
   if (back)                                                                                        \
     hipLaunchKernelGGL((s6_gated_scan_bwd_kernel<In, VEC, UNIT, STARTS>), grid, block, 0, st, a);  \
