@@ -68,7 +68,6 @@ struct GatedArgs {
 // A tile's word: {P, H} of the tile, {kState, s} once the state s after the
 // tile is known, or kEmpty (both halves written at once).
 constexpr uint32_t kEmpty = 0xffffffffu, kState = 0xfffffffeu;
-constexpr int kBatch = 8;       // tiles looked at together
 constexpr int kStash = 32;      // tiles whose maps are kept on the way to a known state
 constexpr int kMaxPolls = 1 << 21;
 
@@ -93,33 +92,16 @@ __device__ __forceinline__ float pass(float P, float H, float h) {
 // The state entering tile q > 0 for this lane's channel (whole waves call it).
 // slot: the lane's word of this tile; the tile before it is kGC words lower.
 // w0: that one's word, as seen some time ago.  Goes back over maps, kept in
-// stash, to the first tile whose state is known, and forward from there.
-__device__ __forceinline__ float look_back(const uint64_t* slot, int64_t q, uint64_t w0, uint64_t (*stash)[kGC]) {
-  if (__ballot(low(w0) == kState) == ~0ull) return high(w0);
+// stash, to the first tile whose state is known, and forward from there: one
+// tile at a time, since the words compete with the inputs for memory (65536
+// tokens of 1536: 8 at a time 223 us, 4 215, 2 210, 1 208).
+__device__ __forceinline__ float look_back(const uint64_t* slot, int q, uint64_t w0, uint64_t (*stash)[kGC]) {
   const int lane = threadIdx.x & 63;
   int done = 0;  // maps in the stash: tiles q - 1 to q - done
+  uint64_t w = w0;
   for (int polls = 0; polls < kMaxPolls; ++polls) {
-    uint64_t w[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) w[i] = done + i < q ? peek(slot - (int64_t)(done + i + 1) * kGC) : ~0ull;
-    int step = 0;
-    bool found = false;
-    float h = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const uint64_t state = __ballot(low(w[i]) == kState), none = __ballot(low(w[i]) == kEmpty);
-      if (step == i && !found) {
-        if (state == ~0ull) {
-          found = true;
-          h = high(w[i]);
-        } else if (state == 0 && none == 0) {
-          stash[done + i][lane] = w[i];
-          step = i + 1;
-        }
-      }
-    }
-    done += step;
-    if (found) {
+    if (__ballot(low(w) == kState) == ~0ull) {
+      float h = high(w);
 #pragma unroll 4
       for (int i = done - 1; i >= 0; --i) {
         const uint64_t m = stash[i][lane];
@@ -127,9 +109,10 @@ __device__ __forceinline__ float look_back(const uint64_t* slot, int64_t q, uint
       }
       return h;
     }
-    // a full stash: the farthest tiles are looked at again until a state is known
-    if (done > kStash - kBatch) done = kStash - kBatch;
-    if (step < kBatch) __builtin_amdgcn_s_sleep(1);
+    // a map in every lane (a tile's word is read while it is written, too): on
+    // to the tile before, of which there is one, or with a full stash again
+    if (__ballot(low(w) == kEmpty || low(w) == kState) == 0 && done < kStash && done + 1 < q) stash[done++][lane] = w;
+    w = peek(slot - (int64_t)(done + 1) * kGC);
   }
   return __builtin_nanf("");  // not reached: see the file's head
 }
