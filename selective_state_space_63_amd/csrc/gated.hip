@@ -62,6 +62,7 @@ struct GatedArgs {
   int classes;           // counters in use
   int base;              // first workgroup of the launch
   int unit;
+  int stream;            // outputs' rows are whole lines
 };
 
 // ------------------------------------------------------------- look back --
@@ -158,18 +159,27 @@ struct Piece {
     }
   }
 };
-// VEC channels of a token, rounded to In.
-template <typename In, int VEC>
-__device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[VEC]) {
+// VEC channels of a token, rounded to In.  AUX: 2 for a streaming store.
+template <typename In, int VEC, int AUX>
+__device__ __forceinline__ void put_as(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[VEC]) {
   typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
   if constexpr (VEC == 2 && sizeof(In) == 4)
-    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(f[0]), __float_as_uint(f[1])}, r, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(f[0]), __float_as_uint(f[1])}, r, off, 0, AUX);
   else if constexpr (VEC == 2)
-    __builtin_amdgcn_raw_buffer_store_b32(bf_pack(f[0], f[1]), r, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(bf_pack(f[0], f[1]), r, off, 0, AUX);
   else if constexpr (sizeof(In) == 4)
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, off, 0, AUX);
   else
-    __builtin_amdgcn_raw_buffer_store_b16(from_f32<In>(f[0]), r, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b16(from_f32<In>(f[0]), r, off, 0, AUX);
+}
+// Whole lines are stored past the caches, which the inputs need (8 x 2048 x
+// 5120: 166 -> 159 us, gradients 331 -> 313); lines that two columns share wait there for one another.
+template <typename In, int VEC>
+__device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[VEC], int stream) {
+  if (VEC == 2 && stream)
+    put_as<In, VEC, 2>(r, off, f);
+  else
+    put_as<In, VEC, 0>(r, off, f);
 }
 
 __device__ __forceinline__ float gate_f(float g, float bias_l2) {  // bias_l2 = -bias log2(e)
@@ -219,20 +229,26 @@ __device__ __forceinline__ Place<VEC, W> place_of(const GatedArgs& a, int tile) 
   return p;
 }
 
-// The tile of this workgroup, or a.tiles or more: none is left.  Columns (of
-// tiles along a sequence) are dealt to kClasses counters, so that a tile and
-// those before it come from one counter, in order: one counter for all took
-// 11 ns a tile.
+// The tile of this workgroup, or a.tiles: it has none.  Workgroups go to the
+// eight XCDs in turn, and each XCD takes a run of neighbouring columns (of tiles
+// along a sequence), since rows that do not begin at a line's start have lines
+// that two columns share (8 x 2048 x 5000: 184 -> 169 us).  An XCD's columns are
+// dealt to counters, up to eight of them, so that a tile and those before it
+// come from one counter, in order (one counter for all took 11 ns a tile).
 __device__ __forceinline__ int draw_tile(const GatedArgs& a, uint32_t* shared) {
   const int wg = a.base + (int)blockIdx.x;
-  if (!a.slots) return wg;
-  const int c = wg % a.classes;
-  if (threadIdx.x == 0) *shared = atomicAdd(a.ticket + c * kTicketStep, 1u);
-  __syncthreads();
-  const int n = __builtin_amdgcn_readfirstlane((int)*shared);
-  const int mine = (a.cols - c + a.classes - 1) / a.classes;  // the class's columns: c, c + classes, ...
-  const int q = n / mine;
-  return q < a.chunks ? q * a.cols + (n - q * mine) * a.classes + c : a.tiles;
+  const int c = wg % a.classes, x = c & 7, sub = c >> 3, subs = a.classes >> 3;
+  const int lo = (int)((int64_t)a.cols * x >> 3), n = (int)((int64_t)a.cols * (x + 1) >> 3) - lo;
+  const int mine = n > sub ? (n - sub + subs - 1) / subs : 0;  // columns lo + sub, lo + sub + subs, ...
+  int t = wg / a.classes;
+  if (a.slots) {
+    if (threadIdx.x == 0) *shared = atomicAdd(a.ticket + c * kTicketStep, 1u);
+    __syncthreads();
+    t = __builtin_amdgcn_readfirstlane((int)*shared);
+  }
+  if (t >= mine * a.chunks) return a.tiles;
+  const int q = t / mine;
+  return q * a.cols + lo + (t - q * mine) * subs + sub;
 }
 
 // A wave's part of one tensor as a buffer: its tokens of the tile's channels.
@@ -386,7 +402,7 @@ __global__ __launch_bounds__((kFwdW<In, VEC> * 64), (kFwdWaves<In, VEC>)) void s
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     next(t);
-    put<In, VEC>(y.buf, y.lane + t * y.step, h);
+    put<In, VEC>(y.buf, y.lane + t * y.step, h, a.stream);
   }
 }
 
@@ -420,7 +436,7 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
     bx[v] = !a.gx ? -__builtin_inff() : a.bx ? -a.bx[c] * kLog2e : 0.0f;
   }
   // the gates, decays and inputs, and the group's maps
-  float av[T][VEC], rv[T][VEC], iv[T][VEC], uv[T][VEC];
+  float av[T][VEC], rv[T][VEC], iv[T][VEC], uv[T][VEC], sv[T][VEC];
   float Pl[VEC], Hl[VEC], Ml[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) { Pl[v] = 1.0f; Hl[v] = Ml[v] = 0.0f; }
@@ -435,7 +451,10 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
       const float v2 = st ? -__builtin_inff() : Ac[v] * kLog2e * rv[t][v];
       float d = fast_exp2(v2);
       float u = iv[t][v] * xr[t].get(v);
-      if constexpr (!UNIT) u *= __builtin_amdgcn_sqrtf(one_less_square(v2, d));
+      if constexpr (!UNIT) {
+        sv[t][v] = one_less_square(v2, d);
+        u *= __builtin_amdgcn_sqrtf(sv[t][v]);
+      }
       if (t >= p.nt) d = 1.0f;
       av[t][v] = d;
       uv[t][v] = u;
@@ -495,8 +514,7 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
   }
   __syncthreads();
   // The state before each token (in place of the inputs), then backwards with
-  // the adjoint.  b is formed again from r and a: kept beside the rest it
-  // would cost half of the waves.
+  // the adjoint.
   float h[VEC], m[VEC], sA[VEC], sa[VEC], sx[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
@@ -532,10 +550,10 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
         lam = none ? 0.0f : lam;
         float w = d * uv[t][v], bi = i;
         if constexpr (!UNIT) {
-          const float s = one_less_square(Ac[v] * kLog2e * r, d);
+          const float s = sv[t][v];
           const float inv = s >= 0x1p-126f ? __builtin_amdgcn_rsqf(s) : 0.0f;  // 1 / b
           w = __builtin_fmaf(-d * d * inv, i * x, w);
-          bi = st ? i : s * inv * i;
+          bi = s * inv * i;
         }
         const float dv = st ? 0.0f : lam * w;
         ox[v] = lam * bi;
@@ -545,9 +563,9 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
         sa[v] += oa[v];
         sx[v] += og[v];
       }
-      put<In, VEC>(dx.buf, dx.lane + t * dx.step, ox);
-      put<In, VEC>(dga.buf, dga.lane + t * dga.step, oa);
-      put<In, VEC>(dgx.buf, dgx.lane + t * dgx.step, og);
+      put<In, VEC>(dx.buf, dx.lane + t * dx.step, ox, a.stream);
+      put<In, VEC>(dga.buf, dga.lane + t * dga.step, oa, a.stream);
+      put<In, VEC>(dgx.buf, dgx.lane + t * dgx.step, og, a.stream);
     }
   }
   if (!a.parts) return;
@@ -666,7 +684,7 @@ int check_gated(const s6_gated_dims* d, int in_dtype, int flags, bool gx, bool t
       !mul_ok(t, len + kGT, &t))
     return S6_ERR_SHAPE;
   // tiles and workgroups in 32 bits, a class's last tiles included
-  if (!mul_ok(d->batch * ((d->dim + kGC - 1) / kGC) + kClasses, (len + kGT - 1) / kGT, &t) || t > INT32_MAX - kMaxTiles)
+  if (!mul_ok(d->batch * ((d->dim + kGC - 1) / kGC) + 2 * kClasses, (len + kGT - 1) / kGT, &t) || t > INT32_MAX - kMaxTiles)
     return S6_ERR_SHAPE;
   const int64_t str[] = {d->x_batch, d->x_token, d->a_batch, d->a_token, d->g_batch, d->g_token};
   for (int i = 0; i < (gx ? 6 : 4); ++i) {
@@ -717,9 +735,10 @@ int launch_gated(GatedArgs a, bool back, hipStream_t st) {
       S6_HIP(hipGetLastError(), "s6_gated_init_kernel launch");
     }
   }
-  // a class with one column less leaves workgroups without a tile
-  a.classes = a.cols < kClasses ? a.cols : kClasses;
-  const int wgs = a.slots ? (a.cols + a.classes - 1) / a.classes * a.classes * a.chunks : a.tiles;
+  // as many workgroups for each counter as the one with the most tiles needs
+  const int most = (a.cols + 7) / 8, subs = most < kClasses / 8 ? most : kClasses / 8;
+  a.classes = 8 * subs;
+  const int wgs = (most + subs - 1) / subs * a.classes * a.chunks;
   for (a.base = 0; a.base < wgs; a.base += kMaxTiles) {
     const dim3 grid((unsigned)(wgs - a.base < kMaxTiles ? wgs - a.base : kMaxTiles)), block(64 * (back ? kBwdW : kFwdW<In, VEC>));
 #define S6_GATED_LAUNCH(UNIT, STARTS)                                                              \
@@ -751,6 +770,13 @@ GatedArgs gated_args(const s6_gated_dims& d, int flags, const void* x, const voi
   a.g_batch = d.g_batch; a.g_token = d.g_token;
   a.unit = (flags & S6_UNIT_INPUT) != 0;
   return a;
+}
+
+// Rows of outputs are whole lines.
+int lines_ok(const s6_gated_dims& d, size_t esz, const void* const* ptrs, int n) {
+  bool ok = d.dim * (int64_t)esz % 128 == 0;
+  for (int i = 0; i < n; ++i) ok = ok && aligned(ptrs[i], 128);
+  return ok;
 }
 
 // Two channels per lane: every row begins at a multiple of two elements.
@@ -811,6 +837,7 @@ int s6_gated_scan_fwd(const s6_gated_dims* d, int in_dtype, int flags, const voi
     a.ticket = static_cast<uint32_t*>(workspace);
     a.slots = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + w.slots);
   }
+  a.stream = lines_ok(*d, esz, ins + 3, 1);
   const bool vec = pairs_ok(*d, gate_x != nullptr, true, esz, ins, 4);
   return in_dtype == S6_BF16 ? launch_gated_in<uint16_t>(a, false, vec, st) : launch_gated_in<float>(a, false, vec, st);
 }
@@ -857,6 +884,7 @@ int s6_gated_scan_bwd(const s6_gated_dims* d, int in_dtype, int flags, const voi
     a.ticket = reinterpret_cast<uint32_t*>(ws);
     a.slots = reinterpret_cast<uint64_t*>(ws + w.slots);
   }
+  a.stream = lines_ok(*d, esz, ins + 4, 3);
   const bool vec = pairs_ok(*d, gate_x != nullptr, true, esz, ins, 7);
   const auto launch = [&](bool back) {
     return in_dtype == S6_BF16 ? launch_gated_in<uint16_t>(a, back, vec, st) : launch_gated_in<float>(a, back, vec, st);
