@@ -39,7 +39,7 @@ constexpr int kFwdW = sizeof(In) == 2 && VEC == 2 ? 4 : 8;
 template <typename In, int VEC>
 constexpr int kFwdWaves = kFwdW<In, VEC> == 4 ? 4 : 6;
 constexpr int kBwdW = 8, kBwdWaves = 4;
-constexpr int kClasses = 64;           // counters of tiles, each in a line of its own
+constexpr int kXcds = 8;               // counters of tiles, each in a line of its own
 constexpr int kTicketStep = 32;        // words from one to the next
 
 struct GatedArgs {
@@ -59,7 +59,7 @@ struct GatedArgs {
   int64_t x_batch, x_token, a_batch, a_token, g_batch, g_token;
   int dim;
   int cblocks, cols, chunks, tiles;
-  int classes;           // counters in use
+  int xcds;              // log2 of the runs of columns, each with a counter
   int base;              // first workgroup of the launch
   int unit;
   int stream;            // outputs' rows are whole lines
@@ -232,23 +232,22 @@ __device__ __forceinline__ Place<VEC, W> place_of(const GatedArgs& a, int tile) 
 // The tile of this workgroup, or a.tiles: it has none.  Workgroups go to the
 // eight XCDs in turn, and each XCD takes a run of neighbouring columns (of tiles
 // along a sequence), since rows that do not begin at a line's start have lines
-// that two columns share (8 x 2048 x 5000: 184 -> 169 us).  An XCD's columns are
-// dealt to counters, up to eight of them, so that a tile and those before it
-// come from one counter, in order (one counter for all took 11 ns a tile).
+// that two columns share (training of 8 x 2048 x 5000: 567 -> 455 us with one
+// counter per XCD, 482 with eight of them; 8 x 2048 x 5120 479 -> 450).  A tile and those before it come
+// from one counter, in order.
 __device__ __forceinline__ int draw_tile(const GatedArgs& a, uint32_t* shared) {
   const int wg = a.base + (int)blockIdx.x;
-  const int c = wg % a.classes, x = c & 7, sub = c >> 3, subs = a.classes >> 3;
-  const int lo = (int)((int64_t)a.cols * x >> 3), n = (int)((int64_t)a.cols * (x + 1) >> 3) - lo;
-  const int mine = n > sub ? (n - sub + subs - 1) / subs : 0;  // columns lo + sub, lo + sub + subs, ...
-  int t = wg / a.classes;
+  const int x = wg & ((1 << a.xcds) - 1);
+  const int lo = (int)((int64_t)a.cols * x >> a.xcds), mine = (int)((int64_t)a.cols * (x + 1) >> a.xcds) - lo;
+  int t = wg >> a.xcds;
   if (a.slots) {
-    if (threadIdx.x == 0) *shared = atomicAdd(a.ticket + c * kTicketStep, 1u);
+    if (threadIdx.x == 0) *shared = atomicAdd(a.ticket + x * kTicketStep, 1u);
     __syncthreads();
     t = __builtin_amdgcn_readfirstlane((int)*shared);
   }
   if (t >= mine * a.chunks) return a.tiles;
   const int q = t / mine;
-  return q * a.cols + lo + (t - q * mine) * subs + sub;
+  return q * a.cols + lo + (t - q * mine);
 }
 
 // A wave's part of one tensor as a buffer: its tokens of the tile's channels.
@@ -630,7 +629,7 @@ __global__ __launch_bounds__(64) void s6_gated_slices_kernel(SumArgs a, int64_t 
 // Counters at 0 and empty words, two of them per store.
 __global__ __launch_bounds__(256) void s6_gated_init_kernel(u32x4* slots, int64_t pairs, uint32_t* ticket) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < kClasses) ticket[i * kTicketStep] = 0;
+  if (i < kXcds) ticket[i * kTicketStep] = 0;
   if (i < pairs) slots[i] = u32x4{kEmpty, kEmpty, kEmpty, kEmpty};
 }
 
@@ -683,8 +682,9 @@ int check_gated(const s6_gated_dims* d, int in_dtype, int flags, bool gx, bool t
   if (d->dim > kMaxRow || d->batch > INT32_MAX || !mul_ok(d->batch, d->dim, &t) || !mul_ok(t, 64 * 16, &t) ||
       !mul_ok(t, len + kGT, &t))
     return S6_ERR_SHAPE;
-  // tiles and workgroups in 32 bits, a class's last tiles included
-  if (!mul_ok(d->batch * ((d->dim + kGC - 1) / kGC) + 2 * kClasses, (len + kGT - 1) / kGT, &t) || t > INT32_MAX - kMaxTiles)
+  // tiles and workgroups in 32 bits, those without a tile included
+  const int64_t cols = d->batch * ((d->dim + kGC - 1) / kGC);
+  if (!mul_ok(cols + cols / 8 + kXcds, (len + kGT - 1) / kGT, &t) || t > INT32_MAX - kMaxTiles)
     return S6_ERR_SHAPE;
   const int64_t str[] = {d->x_batch, d->x_token, d->a_batch, d->a_token, d->g_batch, d->g_token};
   for (int i = 0; i < (gx ? 6 : 4); ++i) {
@@ -709,7 +709,7 @@ GatedWs gated_ws(const s6_gated_dims& d, bool back, bool has_states) {
   // column sums: slices of at least 256 parts, at most 64
   w.slices = n / 256 < 1 ? 1 : n / 256 > 64 ? 64 : n / 256;
   w.per = (n + w.slices - 1) / w.slices;
-  w.slots = kClasses * kTicketStep * sizeof(uint32_t);
+  w.slots = kXcds * kTicketStep * sizeof(uint32_t);
   size_t at = w.chunks > 1 ? w.slots + (size_t)w.tiles * kGC * sizeof(uint64_t) : 0;
   w.states = w.parts = w.sums = 0;
   if (back) {
@@ -735,10 +735,11 @@ int launch_gated(GatedArgs a, bool back, hipStream_t st) {
       S6_HIP(hipGetLastError(), "s6_gated_init_kernel launch");
     }
   }
-  // as many workgroups for each counter as the one with the most tiles needs
-  const int most = (a.cols + 7) / 8, subs = most < kClasses / 8 ? most : kClasses / 8;
-  a.classes = 8 * subs;
-  const int wgs = (most + subs - 1) / subs * a.classes * a.chunks;
+  // runs of columns for the XCDs, where they come out even; as many workgroups
+  // for each as the longest run needs
+  const int most = (a.cols + kXcds - 1) / kXcds;
+  a.xcds = (int64_t)most * kXcds <= a.cols + a.cols / 8 ? 3 : 0;
+  const int wgs = (a.xcds ? most * kXcds : a.cols) * a.chunks;
   for (a.base = 0; a.base < wgs; a.base += kMaxTiles) {
     const dim3 grid((unsigned)(wgs - a.base < kMaxTiles ? wgs - a.base : kMaxTiles)), block(64 * (back ? kBwdW : kFwdW<In, VEC>));
 #define S6_GATED_LAUNCH(UNIT, STARTS)                                                              \
