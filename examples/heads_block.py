@@ -1,13 +1,16 @@
-"""A small model of multi-head scan layers: training, a prompt, single tokens.
+"""A small model of scan layers: training, a prompt, single tokens.
 
-Each layer is the norm with its residual add (AddNorm), one projection into
-z, x, B, C and the step, the multi-head scan (HeadsScan), the norm with the
-gate (GatedNorm) and the projection back.  The model learns to answer with the
-token it saw `LAG` positions before; then a prompt is run as a whole, its states are
-kept, and the tokens after it go through the single-token entry points.  Both
-ways give the same logits up to rounding.
+Each layer is the norm with its residual add (AddNorm), one projection, a
+recurrence, the norm with the gate (GatedNorm) and the projection back.  The
+recurrence is the multi-head scan (HeadsScan; the projection gives z, x, B, C
+and the step) or the gated one (GatedScan; z, x and its two gates).  The model
+learns to answer with the token it saw `LAG` positions before; then a prompt is
+run as a whole, its states are kept, and the tokens after it go through the
+single-token entry points.  Both ways give the same logits up to rounding.
+With 4-bit weights the single tokens' projections are q4_linear's, the first
+of each layer on rows that the norm leaves in 8 bits.
 
-    python examples/heads_block.py [--steps 200] [--dtype bf16|f32]
+    python examples/heads_block.py [--steps 200] [--dtype bf16|f32] [--layers heads,gated] [--four-bit]
 """
 import argparse
 import math
@@ -20,12 +23,41 @@ from torch.nn import functional as F
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from selective_state_space_63_amd import block  # noqa: E402
+from selective_state_space_63_amd import block, gated, q4  # noqa: E402
 
 LAG = 2
 
 
-class HeadsLayer(nn.Module):
+class Projections(nn.Module):
+    """What layers share: the norm, the projections and their 4-bit weights.
+    w_in, w_out, norm, widths and dtype are the layer's."""
+
+    packed = None
+
+    def pack(self, group=64):
+        """4-bit weights for the single tokens from here on."""
+        with torch.no_grad():
+            self.packed = q4.q4_pack(self.w_in, group), q4.q4_pack(self.w_out, group)
+
+    def split(self, row):
+        return row[..., :sum(self.widths)].split(self.widths, -1)
+
+    def enter(self, u, residual):
+        """The norm and the first projection of single tokens: the row's parts,
+        and the residual."""
+        if self.packed is None:
+            u, residual = block.add_norm_fwd(u, self.norm, residual=residual)
+            return self.split(F.linear(u, self.w_in.to(self.dtype))), residual
+        u, scale, residual = q4.add_norm_q8_fwd(u, self.norm, residual=residual)
+        return self.split(q4.q4_linear(u, *self.packed[0], x_scale=scale, out_dtype=self.dtype)), residual
+
+    def leave(self, out):
+        if self.packed is None:
+            return F.linear(out, self.w_out.to(self.dtype))
+        return q4.q4_linear(out, *self.packed[1])
+
+
+class HeadsLayer(Projections):
     def __init__(self, dim, heads, headdim, groups, dstate, dtype):
         super().__init__()
         self.heads, self.headdim, self.groups, self.dstate = heads, headdim, groups, dstate
@@ -41,10 +73,8 @@ class HeadsLayer(nn.Module):
         self.delta_bias = nn.Parameter(torch.full((heads,), -1.0))
         self.dtype = dtype
 
-    def project(self, u):
+    def parts(self, z, x, B, C, delta):
         """z, x, delta, B, C as slices of one row per token."""
-        row = F.linear(u, self.w_in.to(self.dtype))
-        z, x, B, C, delta = row[..., :sum(self.widths)].split(self.widths, -1)
         groups = (self.groups, self.dstate)
         return z, x.unflatten(-1, (self.heads, self.headdim)), delta, B.unflatten(-1, groups), C.unflatten(-1, groups)
 
@@ -52,27 +82,59 @@ class HeadsLayer(nn.Module):
         """u, residual: (batch, seqlen, dim) -> the same, and the states after
         the last token."""
         u, residual = block.AddNorm.apply(u, self.norm, residual)
-        z, x, delta, B, C = self.project(u)
+        z, x, delta, B, C = self.parts(*self.split(F.linear(u, self.w_in.to(self.dtype))))
         y, h = block.HeadsScan.apply(x, delta, -self.A_log.exp(), B, C, self.D, h0, self.delta_bias, True)
         out = block.GatedNorm.apply(y.flatten(-2), z, self.gate_norm)
         return F.linear(out, self.w_out.to(self.dtype)), residual, h
 
     def step(self, u, residual, h):
         """One token: u, residual: (batch, dim); h is advanced in place."""
-        u, residual = block.add_norm_fwd(u, self.norm, residual=residual)
-        z, x, delta, B, C = self.project(u)
+        row, residual = self.enter(u, residual)
+        z, x, delta, B, C = self.parts(*row)
         y = block.heads_state_update(h, x, delta, -self.A_log.exp(), B, C, D=self.D, delta_bias=self.delta_bias,
                                      delta_softplus=True)
         out = block.gated_norm_fwd(y.flatten(-2), z, self.gate_norm)
-        return F.linear(out, self.w_out.to(self.dtype)), residual
+        return self.leave(out), residual
+
+
+class GatedLayer(Projections):
+    def __init__(self, dim, inner, dtype):
+        super().__init__()
+        self.inner = inner
+        self.norm = nn.Parameter(torch.ones(dim))
+        self.gate_norm = nn.Parameter(torch.ones(inner))
+        self.widths = [inner] * 4
+        self.w_in = nn.Parameter(torch.randn(4 * inner, dim) / math.sqrt(dim))
+        self.w_out = nn.Parameter(torch.randn(dim, inner) / math.sqrt(inner))
+        # decays from exp(-4) to exp(-1/8) per token where the gate is open
+        self.A_log = nn.Parameter(torch.linspace(-math.log(8), math.log(4), inner))
+        self.bias_a = nn.Parameter(torch.zeros(inner))
+        self.bias_x = nn.Parameter(torch.zeros(inner))
+        self.dtype = dtype
+
+    def forward(self, u, residual, h0=None):
+        u, residual = block.AddNorm.apply(u, self.norm, residual)
+        z, x, gate_a, gate_x = self.split(F.linear(u, self.w_in.to(self.dtype)))
+        y, h = gated.GatedScan.apply(x, gate_a, gate_x, -self.A_log.exp(), self.bias_a, self.bias_x, h0)
+        out = block.GatedNorm.apply(y, z, self.gate_norm)
+        return F.linear(out, self.w_out.to(self.dtype)), residual, h
+
+    def step(self, u, residual, h):
+        (z, x, gate_a, gate_x), residual = self.enter(u, residual)
+        y = gated.gated_state_update(h, x, gate_a, gate_x, -self.A_log.exp(), bias_a=self.bias_a, bias_x=self.bias_x)
+        return self.leave(block.gated_norm_fwd(y, z, self.gate_norm)), residual
 
 
 class Model(nn.Module):
-    def __init__(self, vocab=32, dim=128, layers=2, heads=4, headdim=64, groups=1, dstate=64, dtype=torch.bfloat16):
+    def __init__(self, vocab=32, dim=128, layers=2, heads=4, headdim=64, groups=1, dstate=64, dtype=torch.bfloat16,
+                 kinds=("heads",)):
+        """kinds: of the layers, in turn."""
         super().__init__()
         self.dtype = dtype
         self.embed = nn.Parameter(torch.randn(vocab, dim))
-        self.layers = nn.ModuleList(HeadsLayer(dim, heads, headdim, groups, dstate, dtype) for _ in range(layers))
+        self.layers = nn.ModuleList(HeadsLayer(dim, heads, headdim, groups, dstate, dtype)
+                                    if kinds[i % len(kinds)] == "heads" else GatedLayer(dim, heads * headdim, dtype)
+                                    for i in range(layers))
         self.norm = nn.Parameter(torch.ones(dim))
         self.head = nn.Parameter(torch.randn(vocab, dim) / math.sqrt(dim))
 
@@ -122,13 +184,21 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--dtype", choices=("bf16", "f32"), default="bf16")
+    ap.add_argument("--layers", default="heads", help="kinds of the layers in turn: heads, gated")
+    ap.add_argument("--four-bit", action="store_true", help="4-bit weights for the single tokens")
     a = ap.parse_args()
+    kinds = a.layers.split(",")
+    if set(kinds) - {"heads", "gated"}:
+        ap.error("--layers takes heads and gated")
     torch.manual_seed(0)
-    model = Model(dtype=torch.bfloat16 if a.dtype == "bf16" else torch.float32).cuda()
+    model = Model(dtype=torch.bfloat16 if a.dtype == "bf16" else torch.float32, kinds=kinds).cuda()
     losses = train(model, a.steps)
     for i in range(0, len(losses), max(1, len(losses) // 10)):
         print(f"step {i}: loss {losses[i]:.3f}")
     tokens = torch.randint(32, (4, 120), device="cuda")
+    if a.four_bit:
+        for layer in model.layers:
+            layer.pack()
     got = prompt_then_tokens(model, tokens, 70)
     with torch.no_grad():
         want = model(tokens)[0][:, 70:]
