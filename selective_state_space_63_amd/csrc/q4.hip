@@ -292,15 +292,15 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
 constexpr int kBN = 128;
 constexpr int kXP = kBlk + 8;  // pitch of a row of x in LDS: 16 rows in 16 bytes meet all banks once
 constexpr int kYP = kBN + 4;   // pitch of a row of sums
-constexpr size_t many_lds(int bm) { return (size_t)2 * 2 * bm * kXP * sizeof(uint16_t); }
-static_assert(many_lds(32) >= 32 * kYP * sizeof(float), "the sums take the place of x");
+constexpr size_t many_lds(int bm, int parts) { return (size_t)2 * 2 * parts * bm * kXP * sizeof(uint16_t); }
+static_assert(many_lds(32, 1) >= 32 * kYP * sizeof(float), "the sums take the place of x");
 template <typename XT, int BM, bool FINE, bool XV, typename YT>
 __global__ __launch_bounds__(512, 4) void s6_q4_many_kernel(Q4Args a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using X = X8<XT, XV>;
   using Tile = uint16_t(*)[kXP];
   constexpr uint32_t kE = sizeof(XT);
-  constexpr int M = BM / 16;
+  constexpr int M = BM / 16, NP = X::kParts;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 2;
   const int i = lane & 15, q = lane >> 4;
   const int64_t m0 = (a.base + blockIdx.x) * kBN, t0 = (int64_t)blockIdx.y * BM;
@@ -339,12 +339,13 @@ __global__ __launch_bounds__(512, 4) void s6_q4_many_kernel(Q4Args a) {
     for (int u = 0; u < M; ++u) sum[h][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   load(lo + half);
   for (int b = lo; b < hi; b += 2) {
-    Tile x = reinterpret_cast<Tile>(lds) + (((b - lo) & 2) + half) * BM;
+    Tile x = reinterpret_cast<Tile>(lds) + (((b - lo) & 2) + half) * (NP * BM);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      bf16x8 v[1];
+      bf16x8 v[NP];
       xr[m].get(v);
-      *reinterpret_cast<bf16x8*>(&x[sr + 16 * m][sc]) = v[0];
+#pragma unroll
+      for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(&x[p * BM + sr + 16 * m][sc]) = v[p];
     }
     typename WRows<FINE>::Block c0 = wb[0], c1 = wb[1];
     // (a turn's tiles were last read two turns ago, before the barrier of the
@@ -364,10 +365,14 @@ __global__ __launch_bounds__(512, 4) void s6_q4_many_kernel(Q4Args a) {
       const bf16x8 v0 = values8(c0.c[j]), v1 = values8(c1.c[j]);
 #pragma unroll
       for (int u = 0; u < M; ++u) {
-        const bf16x8 xv = *reinterpret_cast<const bf16x8*>(&x[16 * u + i][FINE ? 32 * j + 8 * q : 32 * q + 8 * j]);
         if (FINE || j == 0) acc[0][u] = acc[1][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        acc[0][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, v0, acc[0][u], 0, 0, 0);
-        acc[1][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, v1, acc[1][u], 0, 0, 0);
+#pragma unroll
+        for (int p = NP - 1; p >= 0; --p) {
+          const bf16x8 xv =
+              *reinterpret_cast<const bf16x8*>(&x[p * BM + 16 * u + i][FINE ? 32 * j + 8 * q : 32 * q + 8 * j]);
+          acc[0][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, v0, acc[0][u], 0, 0, 0);
+          acc[1][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, v1, acc[1][u], 0, 0, 0);
+        }
       }
       if (FINE || j == 3) {
 #pragma unroll
@@ -492,19 +497,20 @@ int check_q4(int64_t rows, int64_t inner, int64_t outer, int64_t group, int64_t 
   return S6_OK;
 }
 
-constexpr int64_t kFewRows = 32;          // most rows of the first kernel (fp32: any number)
+constexpr int64_t kFewRows = 32;          // most rows of the first kernel
 constexpr int64_t kLaunchRows = 32768;    // most rows of a launch of the second
 
 // Rows of x to a workgroup of the second kernel.  Measured with 32 and with 64, us:
 // 64 bf16 rows of 2560 to 10576: 16 and 21; 128 of 5120 to 2560, groups of 32: 18
 // and 21; 256 of 2560 to 10576: 34 and 29.
-int64_t many_rows(int64_t rows) { return rows <= 128 ? 32 : 64; }
+// (fp32 rows, three parts: 32, for the LDS).
+int64_t many_rows(int64_t rows, int x_dtype) { return rows <= 128 || x_dtype == S6_F32 ? 32 : 64; }
 
 // Slices of the columns for the second kernel: a workgroup per CU where there
 // are columns for it, of at least four blocks each.  They cost a pass over their
 // sums.
-int64_t slices_of(int64_t rows, int64_t inner, int64_t outer, int64_t* slice) {
-  const int64_t nb = (inner + kBlk - 1) / kBlk, n = rows < kLaunchRows ? rows : kLaunchRows, bm = many_rows(n);
+int64_t slices_of(int64_t rows, int64_t inner, int64_t outer, int x_dtype, int64_t* slice) {
+  const int64_t nb = (inner + kBlk - 1) / kBlk, n = rows < kLaunchRows ? rows : kLaunchRows, bm = many_rows(n, x_dtype);
   const int64_t tiles = ((outer + kBN - 1) / kBN) * ((n + bm - 1) / bm);
   int64_t s = cu_count() / (tiles > 0 ? tiles : 1);
   if (s > nb / 4) s = nb / 4;
@@ -531,7 +537,7 @@ int launch_few(Q4Args a, hipStream_t st) {
 template <typename XT, int BM, bool FINE, bool XV, typename YT>
 int launch_many(Q4Args a, int64_t slices, hipStream_t st) {
   const auto kern = s6_q4_many_kernel<XT, BM, FINE, XV, YT>;
-  constexpr size_t lds = many_lds(BM);
+  constexpr size_t lds = many_lds(BM, sizeof(XT) == 4 ? 3 : 1);
   if constexpr (lds > 65536)
     S6_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds),
            "s6_q4_many_kernel LDS size");
@@ -551,9 +557,11 @@ int launch_many(Q4Args a, int64_t slices, hipStream_t st) {
 }
 template <typename XT, bool FINE, bool XV, typename YT>
 int launch_rows(const Q4Args& a, hipStream_t st) {
-  const bool few = sizeof(XT) == 4 || a.rows <= kFewRows;
+  constexpr int dt = sizeof(XT) == 4 ? S6_F32 : sizeof(XT) == 2 ? S6_BF16 : S6_E4M3;
+  const bool few = a.rows <= kFewRows;
   int64_t slice = 0;
-  const int64_t slices = few ? 1 : slices_of(a.rows, a.inner, a.outer, &slice);
+  const int64_t slices = few ? 1 : slices_of(a.rows, a.inner, a.outer, dt, &slice);
+  const int64_t bm = many_rows(a.rows < kLaunchRows ? a.rows : kLaunchRows, dt);
   for (int64_t r = 0; r < a.rows; r += kLaunchRows) {
     Q4Args b = a;
     b.rows = a.rows - r < kLaunchRows ? a.rows - r : kLaunchRows;
@@ -565,9 +573,11 @@ int launch_rows(const Q4Args& a, hipStream_t st) {
     int rc;
     if (few) {
       rc = b.rows > 16 ? launch_few<XT, 2, FINE, XV, YT>(b, st) : launch_few<XT, 1, FINE, XV, YT>(b, st);
-    } else if constexpr (sizeof(XT) < 4) {
-      rc = many_rows(a.rows < kLaunchRows ? a.rows : kLaunchRows) == 32 ? launch_many<XT, 32, FINE, XV, YT>(b, slices, st)
-                                                                        : launch_many<XT, 64, FINE, XV, YT>(b, slices, st);
+    } else if (bm == 32) {
+      rc = launch_many<XT, 32, FINE, XV, YT>(b, slices, st);
+    } else {
+      if constexpr (sizeof(XT) == 4) return S6_ERR_UNSUPPORTED;  // not reached: many_rows
+      else rc = launch_many<XT, 64, FINE, XV, YT>(b, slices, st);
     }
     if (rc) return rc;
   }
@@ -580,9 +590,9 @@ int launch_q4(const Q4Args& a, bool vec, hipStream_t st) {
 }
 
 size_t q4_ws(int64_t rows, int64_t inner, int64_t outer, int x_dtype) {
-  if (rows <= kFewRows || outer == 0 || x_dtype == S6_F32) return 0;
+  if (rows <= kFewRows || outer == 0) return 0;
   int64_t slice;
-  const int64_t s = slices_of(rows, inner, outer, &slice);
+  const int64_t s = slices_of(rows, inner, outer, x_dtype, &slice);
   const int64_t n = rows < kLaunchRows ? rows : kLaunchRows;
   return s > 1 ? up256((size_t)s * n * outer * sizeof(float)) : 0;
 }
