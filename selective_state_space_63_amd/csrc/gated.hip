@@ -19,6 +19,14 @@
 // run already: every wait ends.  The state entering tile k is always formed as
 // P_{k-1} s_{k-1} + H_{k-1}, whichever of these a workgroup reads or forms
 // itself, so repeated calls give identical bits.
+//
+// Measured (bf16, us; floor: the bytes of one pass at 5.1 TB/s, a large copy's):
+// 8 x 2048 tokens of 5120 channels 146 (floor 132; 4.6 TB/s), 65536 tokens of 1536
+// 194 (158), 2 x 2048 of 1536 18 (10), the gradients of 8 x 2048 x 5120 306 (230).
+// HBM, and beside it the VALU: 33 instructions an element, six of them
+// transcendental, 63 % of the busy cycles (gradients 80 and 67 %).  Passes that
+// first reduce segments and then read all inputs again would take 1.75 times the
+// bytes.
 #include "s6_gated.h"
 
 #include "block_internal.h"
@@ -32,8 +40,9 @@ constexpr int kGT = S6_GATED_TOKENS;   // tokens of a tile
 constexpr int kMaxTiles = 1 << 22; // workgroups of a launch (threads below 2^32)
 // Waves of a workgroup, and of a SIMD, which the registers leave room for.  The
 // forward on pairs of bf16: four of 16 tokens by two channels per lane, 124
-// VGPRs (eight of 8 tokens, six per SIMD: 65536 tokens of 1536 237 us, else 222);
-// fp32 would spill there.
+// VGPRs (eight of 8 tokens, six per SIMD: 65536 tokens of 1536 205 us, else 194;
+// 8 x 2048 of 5120 155, else 146); fp32 would spill there.  Gradients with 16
+// waves a workgroup: training of 8 x 2048 x 5120 605 us, with eight 449.
 template <typename In, int VEC>
 constexpr int kFwdW = sizeof(In) == 2 && VEC == 2 ? 4 : 8;
 template <typename In, int VEC>
@@ -95,7 +104,8 @@ __device__ __forceinline__ float pass(float P, float H, float h) {
 // w0: that one's word, as seen some time ago.  Goes back over maps, kept in
 // stash, to the first tile whose state is known, and forward from there: one
 // tile at a time, since the words compete with the inputs for memory (65536
-// tokens of 1536: 8 at a time 223 us, 4 215, 2 210, 1 208).
+// tokens of 1536, before the outputs passed the caches: 8 at a time 223 us, 4
+// 215, 2 210, 1 208).
 __device__ __forceinline__ float look_back(const uint64_t* slot, int q, uint64_t w0, uint64_t (*stash)[kGC]) {
   const int lane = threadIdx.x & 63;
   int done = 0;  // maps in the stash: tiles q - 1 to q - done
@@ -172,8 +182,9 @@ __device__ __forceinline__ void put_as(__amdgpu_buffer_rsrc_t r, uint32_t off, c
   else
     __builtin_amdgcn_raw_buffer_store_b16(from_f32<In>(f[0]), r, off, 0, AUX);
 }
-// Whole lines are stored past the caches, which the inputs need (8 x 2048 x
-// 5120: 166 -> 159 us, gradients 331 -> 313); lines that two columns share wait there for one another.
+// Whole lines are stored past the caches, which the inputs need (8 x 2048 x 5120:
+// 153 -> 146 us, training 470 -> 449); lines that two columns share wait there
+// for one another (8 x 2048 x 5000 past the caches as well: 158 -> 183 us).
 template <typename In, int VEC>
 __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[VEC], int stream) {
   if (VEC == 2 && stream)
@@ -232,9 +243,9 @@ __device__ __forceinline__ Place<VEC, W> place_of(const GatedArgs& a, int tile) 
 // The tile of this workgroup, or a.tiles: it has none.  Workgroups go to the
 // eight XCDs in turn, and each XCD takes a run of neighbouring columns (of tiles
 // along a sequence), since rows that do not begin at a line's start have lines
-// that two columns share (training of 8 x 2048 x 5000: 567 -> 455 us with one
-// counter per XCD, 482 with eight of them; 8 x 2048 x 5120 479 -> 450).  A tile and those before it come
-// from one counter, in order.
+// that two columns share.  A tile and those before it come from one counter, in
+// order.  One run and one counter for all: 2 x 2048 x 1536 26.8 us, else 18.5;
+// 8 x 2048 x 5120 159, else 146; training of 8 x 2048 x 5000 516, else 454.
 __device__ __forceinline__ int draw_tile(const GatedArgs& a, uint32_t* shared) {
   const int wg = a.base + (int)blockIdx.x;
   const int x = wg & ((1 << a.xcds) - 1);
@@ -634,6 +645,8 @@ __global__ __launch_bounds__(256) void s6_gated_init_kernel(u32x4* slots, int64_
 }
 
 // ------------------------------------------------------------------ step --
+// A channel to a lane, or two.  256 x 5120: 6.1 us (floor 4.1: 21 MB), one row of
+// 1536 2.6, the launch.
 template <typename In, int VEC>
 __global__ __launch_bounds__(256) void s6_gated_step_kernel(GatedArgs a, float* hs) {
   const int64_t per = (a.dim + VEC - 1) / VEC, i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;

@@ -217,9 +217,9 @@ def gated_state_update(h, x, gate_a, gate_x, A, bias_a=None, bias_x=None, unit_i
         _same_device(x, y)
     _written(h, y)
     if y is None:
-        y = x.new_empty(x.shape)
-    _launch(_load().s6_gated_state_update, x, ref, dt, flags, _at(h), _at(x), _at(gate_a), _at(bias_a),
-            _at(gate_x), _at(bias_x), _at(A), _at(y))
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _launch(_load().s6_gated_state_update, x, ref, dt, flags, h.data_ptr(), x.data_ptr(), gate_a.data_ptr(), _at(bias_a),
+            _at(gate_x), _at(bias_x), A.data_ptr(), y.data_ptr())
     return y
 
 
