@@ -286,7 +286,7 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
 // lines.  blockIdx.z: a slice of the columns, its sums left in the workspace
 // where there are several.
 //
-// 256 8-bit rows of 2560 to 10576, groups of 128: 27 us, of which 3 the launch,
+// 256 8-bit rows of 2560 to 10576, groups of 128: 26 us, of which 3 the launch,
 // 5 before and after the turns.  LDS reads, conversions and products would take
 // 7.4, 6.5 and 5.5 us of each CU; with two waves per SIMD that meet at every
 // turn they mostly go one after another.  One block a turn without halves: 34 us;
@@ -297,8 +297,12 @@ constexpr int kXP = kBlk + 8;  // pitch of a row of x in LDS: 16 rows in 16 byte
 constexpr int kYP = kBN + 4;   // pitch of a row of sums
 constexpr size_t many_lds(int bm, int parts) { return (size_t)2 * 2 * parts * bm * kXP * sizeof(uint16_t); }
 static_assert(many_lds(32, 1) >= 32 * kYP * sizeof(float), "the sums take the place of x");
+// Waves per SIMD, which the registers leave room for (smaller groups of bf16 rows
+// spill at four: 136 rows of 2560 to 10576, groups of 32, 27.5 us, else 22.2).
+template <typename XT, int BM, bool FINE>
+constexpr int kManyWaves = BM > 64 || (BM == 64 && FINE && sizeof(XT) == 2) ? 2 : 4;
 template <typename XT, int BM, bool FINE, bool XV, typename YT>
-__global__ __launch_bounds__(512, 4) void s6_q4_many_kernel(Q4Args a) {
+__global__ __launch_bounds__(512, (kManyWaves<XT, BM, FINE>)) void s6_q4_many_kernel(Q4Args a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using X = X8<XT, XV>;
   using Tile = uint16_t(*)[kXP];
@@ -505,15 +509,22 @@ constexpr int64_t kLaunchRows = 32768;    // most rows of a launch of the second
 
 // Rows of x to a workgroup of the second kernel.  Measured with 32 and with 64, us:
 // 64 bf16 rows of 2560 to 10576: 16 and 21; 128 of 5120 to 2560, groups of 32: 18
-// and 21; 256 of 2560 to 10576: 34 and 29.
-// (fp32 rows, three parts: 32, for the LDS).
-int64_t many_rows(int64_t rows, int x_dtype) { return rows <= 128 || x_dtype == S6_F32 ? 32 : 64; }
+// and 21; 256 of 2560 to 10576: 34 and 29 (fp32 rows, three parts: 32, for the
+// LDS).  96 where a CU then has fewer rows in turn.  With 64 and with 96, groups of
+// 32: 256 of 2560 to 10576 (128 rows in turn and 96) 38 and 27, 384 (128 and 192)
+// 39 and 48, 1024 of 5120 to 2560 (128 and 96) 67 and 46.
+int64_t many_rows(int64_t rows, int64_t outer, int x_dtype) {
+  if (rows <= 128 || x_dtype == S6_F32) return 32;
+  const int64_t tiles = (outer + kBN - 1) / kBN, cus = cu_count();
+  auto in_turn = [&](int64_t bm) { return (tiles * ((rows + bm - 1) / bm) + cus - 1) / cus * bm; };
+  return in_turn(96) < in_turn(64) ? 96 : 64;
+}
 
 // Slices of the columns for the second kernel: a workgroup per CU where there
 // are columns for it, of at least four blocks each.  They cost a pass over their
 // sums.
 int64_t slices_of(int64_t rows, int64_t inner, int64_t outer, int x_dtype, int64_t* slice) {
-  const int64_t nb = (inner + kBlk - 1) / kBlk, n = rows < kLaunchRows ? rows : kLaunchRows, bm = many_rows(n, x_dtype);
+  const int64_t nb = (inner + kBlk - 1) / kBlk, n = rows < kLaunchRows ? rows : kLaunchRows, bm = many_rows(n, outer, x_dtype);
   const int64_t tiles = ((outer + kBN - 1) / kBN) * ((n + bm - 1) / bm);
   int64_t s = cu_count() / (tiles > 0 ? tiles : 1);
   if (s > nb / 4) s = nb / 4;
@@ -564,7 +575,7 @@ int launch_rows(const Q4Args& a, hipStream_t st) {
   const bool few = a.rows <= kFewRows;
   int64_t slice = 0;
   const int64_t slices = few ? 1 : slices_of(a.rows, a.inner, a.outer, dt, &slice);
-  const int64_t bm = many_rows(a.rows < kLaunchRows ? a.rows : kLaunchRows, dt);
+  const int64_t bm = many_rows(a.rows < kLaunchRows ? a.rows : kLaunchRows, a.outer, dt);
   for (int64_t r = 0; r < a.rows; r += kLaunchRows) {
     Q4Args b = a;
     b.rows = a.rows - r < kLaunchRows ? a.rows - r : kLaunchRows;
@@ -580,7 +591,7 @@ int launch_rows(const Q4Args& a, hipStream_t st) {
       rc = launch_many<XT, 32, FINE, XV, YT>(b, slices, st);
     } else {
       if constexpr (sizeof(XT) == 4) return S6_ERR_UNSUPPORTED;  // not reached: many_rows
-      else rc = launch_many<XT, 64, FINE, XV, YT>(b, slices, st);
+      else rc = bm == 64 ? launch_many<XT, 64, FINE, XV, YT>(b, slices, st) : launch_many<XT, 96, FINE, XV, YT>(b, slices, st);
     }
     if (rc) return rc;
   }

@@ -107,6 +107,24 @@ def test_products(torch_cuda, size, dtype):
         check(torch_cuda, x, None, w, s)
 
 
+@pytest.mark.parametrize("size", [
+    # where the tiles of rows are 96 high on 256 CUs: the last of 1 to 66 rows,
+    # one and several blocks of columns; odd columns, rows that wide loads do not fit
+    (256, 384, 8333, 128, 0),
+    (258, 256, 8448, 64, 0),
+    (193, 160, 10101, 32, 1),
+    (1000, 288, 2560, 32, 0),
+], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3"])
+def test_products_of_many_tiles(torch_cuda, size, dtype):
+    m, k, n, group, wide = size
+    print(f"[case] q4 {size} {dtype}", flush=True)
+    w, s = weights(torch_cuda, n, k, group, 61)
+    x, xs = rows(torch_cuda, m, k, dtype, 62, wide)
+    y = check(torch_cuda, x, xs, w, s)
+    assert torch_cuda.equal(y, check(torch_cuda, x, xs, w, s))
+
+
 def test_every_code_and_place(torch_cuda):
     """One column of x at a time is the column of the weights, exactly."""
     from selective_state_space_63_amd import q4
