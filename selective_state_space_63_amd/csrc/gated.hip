@@ -22,7 +22,7 @@
 //
 // Measured (bf16, us; floor: the bytes of one pass at 5.1 TB/s, a large copy's):
 // 8 x 2048 tokens of 5120 channels 146 (floor 132; 4.6 TB/s), 65536 tokens of 1536
-// 194 (158), 2 x 2048 of 1536 18 (10), the gradients of 8 x 2048 x 5120 306 (230).
+// 194 (158), 2 x 2048 of 1536 18 (10), the gradients of 8 x 2048 x 5120 300 (230).
 // HBM, and beside it the VALU: 33 instructions an element, six of them
 // transcendental, 63 % of the busy cycles (gradients 80 and 67 %).  Passes that
 // first reduce segments and then read all inputs again would take 1.75 times the
