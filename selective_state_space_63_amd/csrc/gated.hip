@@ -539,7 +539,7 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
       const float u = uv[t][v];
-      uv[t][v] = h[v];
+      uv[t][v] = t < p.nt ? h[v] : 0.0f;  // (a last state that is infinite goes no further)
       h[v] = STARTS && (starts >> t & 1) ? u : __builtin_fmaf(av[t][v], h[v], u);
       asm volatile("" : "+v"(rv[t][v]), "+v"(iv[t][v]));
     }

@@ -183,6 +183,25 @@ def test_gates_at_their_ends(torch_cuda):
     check(torch, k, dy, dh, unit=True)
 
 
+@pytest.mark.parametrize("L", [5, 130])
+@pytest.mark.parametrize("d,dtype", [(66, "bf16"), (33, "f32")])
+def test_last_state_infinite(torch_cuda, L, d, dtype):
+    """The state after the last token enters no gradient of a sequence whose
+    dh_last is not given: nothing of it may come back when it overflows."""
+    from selective_state_space_63_amd import gated
+    print(f"[case] gated last state infinite {L} {d} {dtype}", flush=True)
+    k, dy, _ = inputs(torch_cuda, 2, L, d, dtype, 31, gx=False, decay=(0.999, 0.9999))
+    k["x"][0, L - 2:, 3] = 3e38  # the last state is 3e38 a + 3e38
+    dy[0, L - 2:, 3] = 0
+    y, states = gated.gated_scan_fwd(**k, unit_input=True, return_states=True)
+    assert torch_cuda.isfinite(y[0, L - 2, 3]) and torch_cuda.isinf(y[0, L - 1, 3])
+    want = ref.scan_bwd(dy=f64(dy), **host(k, True))
+    for st in (states, None):
+        g = gated.gated_scan_bwd(dy=dy, states=st, unit_input=True, **k)
+        for name, t in g.items():
+            close(t, *want[name], L, name)
+
+
 def test_memory_of_a_whole_sequence(torch_cuda):
     """Decays close to 1: 1 - a^2 keeps its accuracy."""
     k, dy, dh = inputs(torch_cuda, 2, 1500, 64, "f32", 36, decay=(0.99999, 0.9999999))
