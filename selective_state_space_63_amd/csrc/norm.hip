@@ -384,8 +384,9 @@ __global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_add_norm_q8_kernel(No
     top = row_max<MULTI>(top, mbuf, (int)(q & 1));
     const bool nan = top >= 0x7f800000u;
     const float most = top < 0x0d800000u ? 0.0f : __uint_as_float(top);  // 2^-100
-    const float f = most > 0.0f ? kTopQ8 * fast_rcp(most) : 0.0f;
-    if (on && wk.t == 0) a.row_scale[row] = nan ? __builtin_nanf("") : most * (1.0f / kTopQ8);
+    const float unit = most * (1.0f / kTopQ8);  // 0, or its reciprocal is a normal number, too
+    const float f = most > 0.0f ? fast_rcp(unit) : 0.0f;
+    if (on && wk.t == 0) a.row_scale[row] = nan ? __builtin_nanf("") : unit;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int64_t i = (int64_t)k * wk.tpr + wk.t;

@@ -308,6 +308,20 @@ def test_add_norm_q8_rows_of_nothing_and_not_finite(torch_cuda):
     assert e[0].shape == (0, 64) and e[1].shape == (0,)
 
 
+@pytest.mark.parametrize("largest", [2.0 ** -99, 1e-20, 1e30, 2.0 ** 127])
+def test_add_norm_q8_of_any_size(torch_cuda, largest):
+    """Rows of +-1: outputs are the weight's size, stored as 448 of
+    the scale, whatever that size is."""
+    from selective_state_space_63_amd import q4
+    print(f"[case] add_norm_q8 largest {largest}", flush=True)
+    g = np.random.default_rng(81)
+    x = torch_cuda.from_numpy(g.choice([-1.0, 1.0], (3, 64)).astype(np.float32)).cuda()
+    w = torch_cuda.full((64,), largest, dtype=torch_cuda.float32, device="cuda")
+    out, scale, _ = q4.add_norm_q8_fwd(x, w, eps=0.0)
+    assert torch_cuda.equal(out.float(), 448 * x)
+    assert float((scale.double() * 448 / largest - 1).abs().max()) <= 2.0 ** -18
+
+
 def test_norm_then_products(torch_cuda):
     """The two as they are used: rows in 8 bits with their factors go into the
     products; against the products of the norm's own output the result is off by
