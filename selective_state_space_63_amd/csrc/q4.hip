@@ -96,10 +96,13 @@ struct X8 {
     if constexpr (sizeof(XT) == 4) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        // what a part leaves is exact; a value that is not finite stays in the first
-        const __bf16 h = (__bf16)e[i];
-        float r = e[i] - (float)h;
-        r = __builtin_fabsf(r) < __builtin_inff() ? r : 0.0f;
+        // the first part is cut, which rounds nothing up to infinity, and what a
+        // part leaves is exact; a value that is not finite stays in the first
+        const float cut = __uint_as_float(__float_as_uint(e[i]) & 0xffff0000u);
+        const float left = e[i] - cut;
+        const bool fin = __builtin_fabsf(left) < __builtin_inff();
+        const float r = fin ? left : 0.0f;
+        const __bf16 h = (__bf16)(fin ? cut : e[i]);
         const __bf16 m = (__bf16)r;
         o[0][i] = h;
         o[1][i] = m;
