@@ -40,7 +40,7 @@ int s6_q4_pack(int64_t outer, int64_t inner, int64_t group, int in_dtype, const 
  * Products are exact, sums fp32, scales fp32; an fp32 x enters in full (three
  * bf16 parts).  Any number of rows; made for the few rows of single tokens.
  * codes are 16-byte aligned, x_stride is at most 2^20.  workspace: s6_q4_linear_workspace_size bytes, 0
- * up to 32 rows.  Repeated calls give identical bits. */
+ * up to 16 rows (of fp32: 6).  Repeated calls give identical bits. */
 int s6_q4_linear(int64_t rows, int64_t inner, int64_t outer, int64_t group, int x_dtype, int y_dtype, const void* x,
                  int64_t x_stride, const float* x_scale, const void* codes, const void* scales, void* y,
                  void* workspace, size_t workspace_bytes, void* stream);

@@ -191,8 +191,8 @@ __device__ __forceinline__ void scales_of(uint32_t s, float (&f)[4]) {
   }
 }
 
-// Few rows.  A workgroup has 16 weight rows and 16 NT rows of x; its waves
-// take the blocks of columns in turn, U of them loaded together, and their
+// Few rows, 16 at most.  A workgroup has 16 weight rows; its waves take the
+// blocks of columns in turn, U of them loaded together, and their
 // sums meet in LDS in a fixed order.  An instruction multiplies 16 rows of x
 // (first operand) by 16 weight rows: lane l gets the sums of x rows 4 (l / 16)
 // to + 3 and weight row l % 16, whose scale is then the lane's own.  Rows and
@@ -200,30 +200,25 @@ __device__ __forceinline__ void scales_of(uint32_t s, float (&f)[4]) {
 // One bf16 row of 2560 to 10576: 6.4 us (floor 2.8: 14 MB of codes), 16 rows of
 // 5120 to 2560, groups of 32: 9.6 (1.5), a launch and the latency of loads that
 // are all under way at once.
-template <typename XT, int NT, bool FINE, bool XV, typename YT>
+template <typename XT, bool FINE, bool XV, typename YT>
 __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
-  extern __shared__ float part[];  // (W - 1, NT, 64, 4)
+  extern __shared__ float part[];  // (W - 1, 64, 4)
   using X = X8<XT, XV>;
-  constexpr int U = sizeof(XT) == 4 ? (NT == 1 ? 2 : 1) : 4 / NT;
+  constexpr int U = sizeof(XT) == 4 ? 2 : 4;
   constexpr uint32_t kE = sizeof(XT);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
   const int i = lane & 15, q = lane >> 4;
-  const int64_t n0 = (a.base + blockIdx.x) * 16, t0 = (int64_t)blockIdx.y * (16 * NT);
+  const int64_t n0 = (a.base + blockIdx.x) * 16;
   const WRows<FINE> wr(a, n0);
-  const int rows = a.rows - t0 < 16 * NT ? (int)(a.rows - t0) : 16 * NT;
+  const int rows = (int)a.rows;
   const uint32_t step = (uint32_t)a.x_stride * kE;
-  const __amdgpu_buffer_rsrc_t xb =
-      buffer_at(static_cast<const XT*>(a.x) + t0 * a.x_stride, (uint32_t)(rows - 1) * step + (uint32_t)a.inner * kE);
-  uint32_t x_at[NT];
-#pragma unroll
-  for (int u = 0; u < NT; ++u) x_at[u] = 16 * u + i < rows ? (16 * u + i) * step + (FINE ? 8 : 32) * q * kE : kNoRow;
-  f32x4 sum[NT];
-#pragma unroll
-  for (int u = 0; u < NT; ++u) sum[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const __amdgpu_buffer_rsrc_t xb = buffer_at(a.x, (uint32_t)(rows - 1) * step + (uint32_t)a.inner * kE);
+  const uint32_t x_at = i < rows ? i * step + (FINE ? 8 : 32) * q * kE : kNoRow;
+  f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
   const int nb = (a.inner + kBlk - 1) / kBlk;
   for (int b0 = wave; b0 < nb; b0 += U * W) {
     typename WRows<FINE>::Block wb[U];
-    X xr[U][4][NT];
+    X xr[U][4];
 #pragma unroll
     for (int v = 0; v < U; ++v) wr.load(wb[v], b0 + v * W, a.inner);
 #pragma unroll
@@ -231,53 +226,41 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int k = (b0 + v * W) * kBlk + (FINE ? 32 : 8) * j;
-        const uint32_t at = k < a.inner ? (uint32_t)k * kE : kNoColumn;
-#pragma unroll
-        for (int u = 0; u < NT; ++u) xr[v][j][u].load(xb, x_at[u] + at);
+        xr[v][j].load(xb, x_at + (k < a.inner ? (uint32_t)k * kE : kNoColumn));
       }
 #pragma unroll
     for (int v = 0; v < U; ++v) {
       if constexpr (FINE) transpose4(wb[v].c);
       float sc[4];
       scales_of<FINE>(wb[v].s, sc);
-      f32x4 acc[NT];
+      f32x4 acc;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bf16x8 w = values8(wb[v].c[j]);
+        bf16x8 xp[X::kParts];
+        xr[v][j].get(xp);
+        if (FINE || j == 0) acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
-          bf16x8 xp[X::kParts];
-          xr[v][j][u].get(xp);
-          if (FINE || j == 0) acc[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int p = X::kParts - 1; p >= 0; --p) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xp[p], w, acc, 0, 0, 0);
+        if (FINE || j == 3) {
 #pragma unroll
-          for (int p = X::kParts - 1; p >= 0; --p)
-            acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xp[p], w, acc[u], 0, 0, 0);
-          if (FINE || j == 3) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) sum[u][r] = __builtin_fmaf(sc[j], acc[u][r], sum[u][r]);
-          }
+          for (int r = 0; r < 4; ++r) sum[r] = __builtin_fmaf(sc[j], acc[r], sum[r]);
         }
       }
     }
   }
   f32x4* parts = reinterpret_cast<f32x4*>(part);
-  if (wave > 0) {
-#pragma unroll
-    for (int u = 0; u < NT; ++u) parts[((wave - 1) * NT + u) * 64 + lane] = sum[u];
-  }
+  if (wave > 0) parts[(wave - 1) * 64 + lane] = sum;
   __syncthreads();
   if (wave > 0 || n0 + i >= a.outer) return;
-#pragma unroll
-  for (int u = 0; u < NT; ++u) {
 #pragma unroll 4
-    for (int w = 0; w + 1 < W; ++w) sum[u] += parts[(w * NT + u) * 64 + lane];
+  for (int w = 0; w + 1 < W; ++w) sum += parts[w * 64 + lane];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t t = t0 + 16 * u + 4 * q + r;
-      if (t >= a.rows) continue;
-      const float xs = a.x_scale ? a.x_scale[t] : 1.0f;
-      static_cast<YT*>(a.y)[t * a.outer + n0 + i] = from_f32<YT>(sum[u][r] * xs);
-    }
+  for (int r = 0; r < 4; ++r) {
+    const int64_t t = 4 * q + r;
+    if (t >= a.rows) continue;
+    const float xs = a.x_scale ? a.x_scale[t] : 1.0f;
+    static_cast<YT*>(a.y)[t * a.outer + n0 + i] = from_f32<YT>(sum[r] * xs);
   }
 }
 
@@ -507,7 +490,11 @@ int check_q4(int64_t rows, int64_t inner, int64_t outer, int64_t group, int64_t 
   return S6_OK;
 }
 
-constexpr int64_t kFewRows = 32;          // most rows of the first kernel
+// Most rows of the first kernel, which reads x again for every 16 weight rows.
+// With it and with the second, us: fp32 of 5120 to 2560, groups of 32, 6 rows 11.8
+// and 10.5, 16 14.8 and 11.7, of 2560 to 10576 6 rows 14.5 both; bf16 of 2560 to
+// 10576, 8 rows 8.9 and 10.5, 16 11.5 both, 24 (two tiles of rows) 16 and 13.
+int64_t few_rows(int x_dtype) { return x_dtype == S6_F32 ? 6 : 16; }
 constexpr int64_t kLaunchRows = 32768;    // most rows of a launch of the second
 
 // Rows of x to a workgroup of the second kernel.  Measured with 32 and with 64, us:
@@ -536,17 +523,16 @@ int64_t slices_of(int64_t rows, int64_t inner, int64_t outer, int x_dtype, int64
   return (nb + *slice - 1) / *slice;
 }
 
-template <typename XT, int NT, bool FINE, bool XV, typename YT>
+template <typename XT, bool FINE, bool XV, typename YT>
 int launch_few(Q4Args a, hipStream_t st) {
   const int64_t nb = (a.inner + kBlk - 1) / kBlk, tiles = (a.outer + 15) / 16;
-  const int64_t ty = (a.rows + 16 * NT - 1) / (16 * NT);
   // waves: as many as load the columns at once, four blocks each
   int64_t W = (nb + 3) / 4;
   if (W > 16) W = 16;
-  const size_t lds = (size_t)(W - 1) * NT * 64 * sizeof(f32x4);
+  const size_t lds = (size_t)(W - 1) * 64 * sizeof(f32x4);
   for (a.base = 0; a.base < tiles; a.base += kMaxGrid) {
-    const dim3 grid((unsigned)(tiles - a.base < kMaxGrid ? tiles - a.base : kMaxGrid), (unsigned)ty);
-    hipLaunchKernelGGL((s6_q4_few_kernel<XT, NT, FINE, XV, YT>), grid, dim3(64 * (unsigned)W), lds, st, a);
+    const dim3 grid((unsigned)(tiles - a.base < kMaxGrid ? tiles - a.base : kMaxGrid));
+    hipLaunchKernelGGL((s6_q4_few_kernel<XT, FINE, XV, YT>), grid, dim3(64 * (unsigned)W), lds, st, a);
     S6_HIP(hipGetLastError(), "s6_q4_few_kernel launch");
   }
   return S6_OK;
@@ -575,9 +561,9 @@ int launch_many(Q4Args a, int64_t slices, hipStream_t st) {
 template <typename XT, bool FINE, bool XV, typename YT>
 int launch_rows(const Q4Args& a, hipStream_t st) {
   constexpr int dt = sizeof(XT) == 4 ? S6_F32 : sizeof(XT) == 2 ? S6_BF16 : S6_E4M3;
-  const bool few = a.rows <= kFewRows;
-  int64_t slice = 0;
-  const int64_t slices = few ? 1 : slices_of(a.rows, a.inner, a.outer, dt, &slice);
+  if (a.rows <= few_rows(dt)) return launch_few<XT, FINE, XV, YT>(a, st);
+  int64_t slice;
+  const int64_t slices = slices_of(a.rows, a.inner, a.outer, dt, &slice);
   const int64_t bm = many_rows(a.rows < kLaunchRows ? a.rows : kLaunchRows, a.outer, dt);
   for (int64_t r = 0; r < a.rows; r += kLaunchRows) {
     Q4Args b = a;
@@ -588,9 +574,7 @@ int launch_rows(const Q4Args& a, hipStream_t st) {
     b.slice = (int)slice;
     if (slices == 1) b.parts = nullptr;
     int rc;
-    if (few) {
-      rc = b.rows > 16 ? launch_few<XT, 2, FINE, XV, YT>(b, st) : launch_few<XT, 1, FINE, XV, YT>(b, st);
-    } else if (bm == 32) {
+    if (bm == 32) {
       rc = launch_many<XT, 32, FINE, XV, YT>(b, slices, st);
     } else {
       if constexpr (sizeof(XT) == 4) return S6_ERR_UNSUPPORTED;  // not reached: many_rows
@@ -607,7 +591,7 @@ int launch_q4(const Q4Args& a, bool vec, hipStream_t st) {
 }
 
 size_t q4_ws(int64_t rows, int64_t inner, int64_t outer, int x_dtype) {
-  if (rows <= kFewRows || outer == 0) return 0;
+  if (rows <= few_rows(x_dtype) || outer == 0) return 0;
   int64_t slice;
   const int64_t s = slices_of(rows, inner, outer, x_dtype, &slice);
   const int64_t n = rows < kLaunchRows ? rows : kLaunchRows;

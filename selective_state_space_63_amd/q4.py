@@ -18,7 +18,7 @@ from .s6 import _DT
 
 S6_E4M3 = 2
 GROUPS = (32, 64, 128)
-FEW = 32  # rows that need no workspace
+FEW = {torch.float32: 6, torch.bfloat16: 16, torch.float8_e4m3fn: 16}  # rows that need no workspace
 _XT = {**_DT, torch.float8_e4m3fn: S6_E4M3}
 
 _lib = None
@@ -102,7 +102,7 @@ def q4_linear(x, weight, scales, x_scale=None, out_dtype=None, y=None):
     group = inner // ngroups
     keep = wsp = None
     wsn = 0
-    if rows > FEW:
+    if rows > FEW[dt]:
         keep, wsp, wsn = _workspace(lib.s6_q4_linear_workspace_size, x, rows, inner, outer, group, _XT[dt])
     _launch(lib.s6_q4_linear, x, rows, inner, outer, group, _XT[dt], _DT[yt], x.data_ptr(), stride, _at(x_scale),
             weight.data_ptr(), scales.data_ptr(), y.data_ptr(), wsp, wsn)

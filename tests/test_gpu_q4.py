@@ -80,9 +80,14 @@ SIZES = [
     (1, 128, 17, 128, 0),
     (2, 96, 33, 32, 8),
     (3, 192, 50, 64, 1),          # rows that 16-byte loads do not fit
+    (6, 384, 40, 128, 0),
+    (7, 1088, 99, 64, 0),
     (15, 2560, 130, 128, 0),
     (16, 1024, 257, 32, 0),
     (17, 640, 100, 128, 16),
+    (24, 1664, 150, 64, 0),
+    (25, 2560, 333, 128, 0),
+    (32, 352, 130, 32, 5),
     (33, 8192, 20, 64, 0),
     (64, 256, 77, 128, 0),
     (65, 1152, 48, 32, 3),
