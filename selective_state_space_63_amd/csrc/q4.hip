@@ -272,7 +272,7 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
 // lines.  blockIdx.z: a slice of the columns, its sums left in the workspace
 // where there are several.
 //
-// 256 8-bit rows of 2560 to 10576, groups of 128: 26 us, of which 3 the launch,
+// 256 8-bit rows of 2560 to 10576, groups of 128: 26 to 27 us, of which 3 the launch,
 // 5 before and after the turns.  LDS reads, conversions and products would take
 // 7.4, 6.5 and 5.5 us of each CU; with two waves per SIMD that meet at every
 // turn they mostly go one after another.  One block a turn without halves: 34 us;
