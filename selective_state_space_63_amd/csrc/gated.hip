@@ -193,8 +193,9 @@ __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t off, cons
     put_as<In, VEC, 0>(r, off, f);
 }
 
-__device__ __forceinline__ float gate_f(float g, float bias_l2) {  // bias_l2 = -bias log2(e)
-  return fast_rcp(1.0f + fast_exp2(__builtin_fmaf(g, -kLog2e, bias_l2)));
+// sigmoid(g + bias); the sum first, which leaves nothing of either where they cancel.
+__device__ __forceinline__ float gate_f(float g, float bias) {
+  return fast_rcp(1.0f + fast_exp2((g + bias) * -kLog2e));
 }
 
 // 1 - e^{2 v} for v = v2 ln 2 <= 0 and a = e^v: by its series where e^{2v} is
@@ -332,8 +333,8 @@ __global__ __launch_bounds__((kFwdW<In, VEC> * 64), (kFwdWaves<In, VEC>)) void s
   for (int v = 0; v < VEC; ++v) {
     const int c = p.on ? p.c0 + p.cl + v : a.dim - 1;
     A2[v] = a.A[c] * kLog2e;
-    ba[v] = a.ba ? -a.ba[c] * kLog2e : 0.0f;
-    bx[v] = !a.gx ? -__builtin_inff() : a.bx ? -a.bx[c] * kLog2e : 0.0f;
+    ba[v] = a.ba ? a.ba[c] : 0.0f;
+    bx[v] = !a.gx ? __builtin_inff() : a.bx ? a.bx[c] : 0.0f;
   }
   float av[T][VEC], uv[T][VEC], Pl[VEC], Hl[VEC];
 #pragma unroll
@@ -442,8 +443,8 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
   for (int v = 0; v < VEC; ++v) {
     const int c = p.on ? p.c0 + p.cl + v : a.dim - 1;
     Ac[v] = a.A[c];
-    ba[v] = a.ba ? -a.ba[c] * kLog2e : 0.0f;
-    bx[v] = !a.gx ? -__builtin_inff() : a.bx ? -a.bx[c] * kLog2e : 0.0f;
+    ba[v] = a.ba ? a.ba[c] : 0.0f;
+    bx[v] = !a.gx ? __builtin_inff() : a.bx ? a.bx[c] : 0.0f;
   }
   // the gates, decays and inputs, and the group's maps
   float av[T][VEC], rv[T][VEC], iv[T][VEC], uv[T][VEC], sv[T][VEC];
@@ -662,10 +663,10 @@ __global__ __launch_bounds__(256) void s6_gated_step_kernel(GatedArgs a, float* 
   float h[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
-    const float v2 = a.A[c + v] * kLog2e * gate_f(ar.get(v), a.ba ? -a.ba[c + v] * kLog2e : 0.0f);
+    const float v2 = a.A[c + v] * kLog2e * gate_f(ar.get(v), a.ba ? a.ba[c + v] : 0.0f);
     const float d = fast_exp2(v2);
     float u = xr.get(v);
-    if (a.gx) u *= gate_f(gr.get(v), a.bx ? -a.bx[c + v] * kLog2e : 0.0f);
+    if (a.gx) u *= gate_f(gr.get(v), a.bx ? a.bx[c + v] : 0.0f);
     if (!a.unit) u *= __builtin_amdgcn_sqrtf(one_less_square(v2, d));
     h[v] = __builtin_fmaf(d, hr.get(v), u);
   }
