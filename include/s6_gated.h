@@ -34,6 +34,8 @@
  * 2^-126 (a gate below about -87): there b may be 0 (off by at most 2^-63
  * sqrt(1 + 2 |A|)), and where it is, its share of the gradients of the gate
  * and of A is 0.
+ * 1 - r and 1 - i, factors of the gates' gradients, keep theirs as r and i
+ * approach 1, until they are below 2^-126 (a gate above about 87) and may be 0.
  * Repeated calls give identical bits.
  */
 #ifndef S6_GATED_H_

@@ -6,7 +6,7 @@
 //   h_t = a_t h_{t-1} + u_t,  u_t = b_t i_t x_t
 //   lam_t = dy_t + mu_{t+1},  mu_t = a_t lam_t       (adjoint of h_t, backwards)
 //   dv = lam (a h_{t-1} - (a^2 / b) i x),  dga = dv A r (1 - r)
-//   dx = lam b i,  dgx = lam b x i (1 - i),  dA = sum dv r
+//   dx = lam b i,  dgx = lam b x i (1 - i),  dA = sum dv r,  1 - r as e^-z r (z = ga + ba)
 // Both recurrences are runs of maps h -> P h + H, which compose, so a tile of
 // 128 tokens x 64 channels is reduced to one (P, H) per channel without
 // knowing the state that enters it.
@@ -196,6 +196,21 @@ __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t off, cons
 // sigmoid(g + bias); the sum first, which leaves nothing of either where they cancel.
 __device__ __forceinline__ float gate_f(float g, float bias) {
   return fast_rcp(1.0f + fast_exp2((g + bias) * -kLog2e));
+}
+
+// A gate in one register, for the gradients, which take r and 1 - r, each to its
+// own accuracy near 0: r below one half, else -(1 - r), as e r with e = e^{-(g +
+// bias)}.  1 - r from r would keep nothing of an open gate (at g + bias = 12 it is 1 %
+// off, from 17 on 0).  The 2^-149 keeps its sign where it is 0.
+__device__ __forceinline__ float split_gate(float g, float bias, float& r) {
+  const float e = fast_exp2((g + bias) * -kLog2e);
+  r = fast_rcp(1.0f + e);
+  return r < 0.5f ? r : -__builtin_fmaf(e, r, 0x1p-149f);
+}
+__device__ __forceinline__ float whole_gate(float s) { return __builtin_amdgcn_fractf(s); }  // r, at most 1 - 2^-24
+__device__ __forceinline__ float gate_slope(float s) {  // r (1 - r)
+  const float m = __builtin_fabsf(s);
+  return __builtin_fmaf(-m, m, m);
 }
 
 // 1 - e^{2 v} for v = v2 ln 2 <= 0 and a = e^v: by its series where e^{2v} is
@@ -457,11 +472,15 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
     const bool st = STARTS && (starts >> t & 1);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      rv[t][v] = gate_f(ar[t].get(v), ba[v]);
-      iv[t][v] = gate_f(gr[t].get(v), bx[v]);
-      const float v2 = st ? -__builtin_inff() : Ac[v] * kLog2e * rv[t][v];
+      float r, i;
+      rv[t][v] = split_gate(ar[t].get(v), ba[v], r);
+      iv[t][v] = split_gate(gr[t].get(v), bx[v], i);
+      // formed here, not where they are used next with e and r kept until then
+      // (training of 8 x 2048 x 5120 586 us, else 445)
+      asm volatile("" : "+v"(rv[t][v]), "+v"(iv[t][v]));
+      const float v2 = st ? -__builtin_inff() : Ac[v] * kLog2e * r;
       float d = fast_exp2(v2);
-      float u = iv[t][v] * xr[t].get(v);
+      float u = i * xr[t].get(v);
       if constexpr (!UNIT) {
         sv[t][v] = one_less_square(v2, d);
         u *= __builtin_amdgcn_sqrtf(sv[t][v]);
@@ -542,7 +561,6 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
       const float u = uv[t][v];
       uv[t][v] = t < p.nt ? h[v] : 0.0f;  // (a last state that is infinite goes no further)
       h[v] = STARTS && (starts >> t & 1) ? u : __builtin_fmaf(av[t][v], h[v], u);
-      asm volatile("" : "+v"(rv[t][v]), "+v"(iv[t][v]));
     }
   }
   const Rows dx = rows_of<In>(a.dx, a.L * a.dim, a.dim, a, p);
@@ -555,21 +573,21 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
       float ox[VEC], oa[VEC], og[VEC];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float x = xr[t].get(v), d = av[t][v], r = rv[t][v], i = iv[t][v];
+        const float x = xr[t].get(v), d = av[t][v], r = whole_gate(rv[t][v]), i = whole_gate(iv[t][v]);
         float lam = yr[t].get(v) + m[v];
         m[v] = st ? 0.0f : d * lam;
         lam = none ? 0.0f : lam;
-        float w = d * uv[t][v], bi = i;
+        float w = d * uv[t][v], lb = lam;  // lb: lam b
         if constexpr (!UNIT) {
           const float s = sv[t][v];
           const float inv = s >= 0x1p-126f ? __builtin_amdgcn_rsqf(s) : 0.0f;  // 1 / b
           w = __builtin_fmaf(-d * d * inv, i * x, w);
-          bi = s * inv * i;
+          lb *= s * inv;
         }
         const float dv = st ? 0.0f : lam * w;
-        ox[v] = lam * bi;
-        oa[v] = dv * (Ac[v] * r) * (1.0f - r);
-        og[v] = ox[v] * x * (1.0f - i);
+        ox[v] = lb * i;
+        oa[v] = dv * (Ac[v] * gate_slope(rv[t][v]));
+        og[v] = lb * x * gate_slope(iv[t][v]);
         sA[v] = __builtin_fmaf(dv, r, sA[v]);
         sa[v] += oa[v];
         sx[v] += og[v];
