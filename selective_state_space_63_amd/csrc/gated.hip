@@ -72,6 +72,7 @@ struct GatedArgs {
   int base;              // first workgroup of the launch
   int unit;
   int stream;            // outputs' rows are whole lines
+  int overlap;           // backward: token rows of an input overlap within a tile
 };
 
 // ------------------------------------------------------------- look back --
@@ -151,6 +152,10 @@ struct Piece {
     }
   }
   __device__ __forceinline__ float get(int v) const { return to_f32(e[v]); }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) e[v] = 0;
+  }
   // What is formed from the values before is formed again after this, instead
   // of being kept in registers.
   __device__ __forceinline__ void again() {
@@ -451,6 +456,11 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
   load_rows(xr, rows_of<In>(a.x, a.x_batch, a.x_token, a, p));
   load_rows(gr, rows_of<In>(a.gx, a.g_batch, a.g_token, a, p));
   load_rows(yr, rows_of<In>(a.dy, a.L * a.dim, a.dim, a, p));
+  if (a.overlap) {  // (a row past the end then lies in part before the buffer's)
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      if (t >= p.nt) { ar[t].clear(); xr[t].clear(); gr[t].clear(); }
+  }
   uint32_t starts = 0;
   if constexpr (STARTS) starts = starts_of(a, p);
   float Ac[VEC], ba[VEC], bx[VEC];
@@ -812,6 +822,12 @@ int lines_ok(const s6_gated_dims& d, size_t esz, const void* const* ptrs, int n)
   return ok;
 }
 
+// Token rows of an input that are closer than a tile's columns are wide.
+int rows_overlap(const s6_gated_dims& d, bool gx) {
+  const int64_t cols = d.dim < kGC ? d.dim : kGC;
+  return d.seqlen > 1 && (d.x_token < cols || d.a_token < cols || (gx && d.g_token < cols));
+}
+
 // Two channels per lane: every row begins at a multiple of two elements.
 bool pairs_ok(const s6_gated_dims& d, bool gx, bool tokens, size_t esz, const void* const* ptrs, int n) {
   bool ok = d.dim % 2 == 0 && d.x_batch % 2 == 0 && d.a_batch % 2 == 0 && (!gx || d.g_batch % 2 == 0);
@@ -930,6 +946,7 @@ int s6_gated_scan_bwd(const s6_gated_dims* d, int in_dtype, int flags, const voi
     states = reinterpret_cast<float*>(ws + w.states);
   }
   a.states = states; a.first = dh_last; a.last = dh0;
+  a.overlap = rows_overlap(*d, gate_x != nullptr);
   a.dy = dy; a.dx = dx; a.dga = dgate_a; a.dgx = dgate_x;
   const bool sums = dA || dbias_a || dbias_x;
   a.parts = sums ? reinterpret_cast<float*>(ws + w.parts) : nullptr;

@@ -1,6 +1,6 @@
 """The gates of the gated recurrence (include/s6_gated.h) where they are hard to
 form: gates and biases that cancel, and gates far open, whose gradients have the
-factor 1 - r.
+factor 1 - r; and values that enter no gradient.
 
 Bars: bar(L) of gated_ref.py.  1 - r is e r with e = e^{-z}, z = g + bias: a sum
 and two products that round once each, each off by |z| 2^-24 in the exponent.
@@ -136,3 +136,30 @@ def test_gates_that_are_not_finite(torch_cuda):
     assert float(out["dx"][0, 4, 3]) == 0
     assert bool(torch.isnan(out["dgate_a"][0, 4, 4])) and bool(torch.isnan(out["dA"][4]))
     assert bool(torch.isnan(out["dgate_x"][0, 4, 5])) and bool(torch.isnan(out["dx"][0, 4, 5]))
+
+
+@pytest.mark.parametrize("which", ["x", "gate_a", "gate_x"])
+@pytest.mark.parametrize("dim,step,dtype", [(66, 8, "bf16"), (66, 8, "f32"), (33, 7, "bf16"), (40, 1, "f32")])
+@pytest.mark.parametrize("L", [5, 130])
+def test_overlapping_rows_end_at_the_last_token(torch_cuda, L, dim, step, dtype, which):
+    """Token rows closer than they are wide: what a tile's places past the last
+    token would hold lies in the tensor, and enters nothing."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    print(f"[case] overlapping rows {L} {dim} {step} {dtype} {which}", flush=True)
+    g = np.random.default_rng([74, dim, L])
+    k = {n: rows(torch, g, (1, L, dim), dtype) for n in ("x", "gate_a", "gate_x")}
+    dy, A = rows(torch, g, (1, L, dim), dtype), -torch.from_numpy(g.uniform(0.05, 0.5, dim).astype(np.float32)).cuda()
+    flat = rows(torch, g, ((L - 1) * step + dim,), dtype)
+    at = dim // 2
+    flat[(L - 1) * step + at] = float("nan")   # channel `at` of the last token
+    k[which] = flat.as_strided((1, L, dim), (L * step, step, 1))
+    zero = torch.zeros(dim, device="cuda")
+    got = gated.gated_scan_bwd(**k, A=A, dy=dy, bias_a=zero, bias_x=zero)
+    reads = torch.isnan(k[which]).any(1)[0]    # channels that hold the value at some token
+    flat[(L - 1) * step + at] = 1.0            # (the same layout: rows that are whole may be summed in pairs)
+    want = gated.gated_scan_bwd(**k, A=A, dy=dy, bias_a=zero, bias_x=zero)
+    assert 0 < int(reads.sum()) < dim
+    for n in got:
+        assert bool(torch.isfinite(got[n][..., ~reads]).all()), n
+        assert torch.equal(got[n][..., ~reads], want[n][..., ~reads]), n
