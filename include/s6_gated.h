@@ -14,7 +14,7 @@
  *   h_t = a_t h_{t-1} + b_t i_t x_t,   y_t = h_t
  * A is at most 0 and finite.  A token whose byte in starts is not 0 begins a
  * sequence of its own: there a_t = 0 and b_t = 1, whatever the state before it
- * holds, and nothing flows back over it.
+ * and gate_a hold, and nothing flows back over it.
  *
  * Layout: token-major, last index fastest.
  *   x, gate_a, gate_x, y, dy, dx, dgate_a, dgate_x : (batch, seqlen, dim)

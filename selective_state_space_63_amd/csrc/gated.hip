@@ -485,6 +485,7 @@ __global__ __launch_bounds__(kBwdW * 64, kBwdWaves) void s6_gated_scan_bwd_kerne
       float r, i;
       rv[t][v] = split_gate(ar[t].get(v), ba[v], r);
       iv[t][v] = split_gate(gr[t].get(v), bx[v], i);
+      if (st) rv[t][v] = 0.0f;  // (a start's gate enters nothing, not as 0 times a NaN either)
       // formed here, not where they are used next with e and r kept until then
       // (training of 8 x 2048 x 5120 586 us, else 445)
       asm volatile("" : "+v"(rv[t][v]), "+v"(iv[t][v]));

@@ -163,3 +163,32 @@ def test_overlapping_rows_end_at_the_last_token(torch_cuda, L, dim, step, dtype,
     for n in got:
         assert bool(torch.isfinite(got[n][..., ~reads]).all()), n
         assert torch.equal(got[n][..., ~reads], want[n][..., ~reads]), n
+
+
+@pytest.mark.parametrize("unit", [False, True], ids=["root", "unit"])
+@pytest.mark.parametrize("dim,dtype", [(66, "bf16"), (33, "f32")])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_gate_of_a_start_enters_nothing(torch_cuda, value, dim, dtype, unit):
+    """At a start a = 0 and b = 1 whatever the gate holds: the bits of a gate of 0."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    print(f"[case] gate of a start {value} {dim} {dtype} {unit}", flush=True)
+    b, L = 2, 150
+    g = np.random.default_rng([75, dim])
+    x, dy, ga, gx = (rows(torch, g, (b, L, dim), dtype) for _ in range(4))
+    A = -torch.from_numpy(g.uniform(0.05, 0.5, dim).astype(np.float32)).cuda()
+    starts = torch.zeros(b, L, dtype=torch.bool, device="cuda")
+    starts[0, [0, 60, 140]] = True
+    starts[1, [5, 6, 149]] = True
+    h0, zero = torch.ones(b, dim, device="cuda"), torch.zeros(dim, device="cuda")
+
+    def call(fill):
+        k = dict(x=x, gate_a=ga.masked_fill(starts[..., None], fill), gate_x=gx, A=A, bias_a=zero, bias_x=zero, h0=h0,
+                 starts=starts, unit_input=unit)
+        out = gated.gated_scan_bwd(**k, dy=dy)
+        out["y"], out["h_last"] = gated.gated_scan_fwd(**k, return_last_state=True)
+        return out
+
+    want, got = call(0.0), call(value)
+    for n in want:
+        assert torch.equal(want[n], got[n]), n
