@@ -9,6 +9,12 @@
 // weight rows by 16 rows of x, 32 columns an instruction.  A code's value is
 // exact in bf16, so are its products with bf16 (fp32 sums); the scales, which
 // are not, multiply the sums of their groups in fp32.
+//
+// A group's sum may be 128 * 6 times the largest x before its scale makes it
+// small: values are converted as 2^-10 of themselves where x is fp32 or bf16,
+// whose largest is fp32's, and the result is multiplied by 2^10.  Both are exact:
+// bf16 are multiples of 2^-133, so the products are of 2^-144; a result below 2^-116
+// rounds to 2^-139.
 #include "s6_q4.h"
 
 #include "block_internal.h"
@@ -34,14 +40,20 @@ struct Q4Args {
   int wide;       // rows of y begin at 16 bytes
   int slice;      // blocks of columns of a slice
   float* parts;   // the slices' sums (slices, rows, outer), or null
+  float up;       // what sums are multiplied by without x_scale: 1 / kDown of x's type
 };
 
+// What values are multiplied by when they are converted.
+template <typename XT>
+constexpr float kDown = sizeof(XT) == 1 ? 1.0f : 0x1p-10f;
+
 // Eight codes as bf16.
+template <typename XT>
 __device__ __forceinline__ bf16x8 values8(uint32_t c) {
-  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 0);
-  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 1);
-  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 2);
-  const bf16x2_t e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 3);
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, kDown<XT>, 0);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, kDown<XT>, 1);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, kDown<XT>, 2);
+  const bf16x2_t e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, kDown<XT>, 3);
   return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 // Eight e4m3 values as bf16.
@@ -236,7 +248,7 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
       f32x4 acc;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bf16x8 w = values8(wb[v].c[j]);
+        const bf16x8 w = values8<XT>(wb[v].c[j]);
         bf16x8 xp[X::kParts];
         xr[v][j].get(xp);
         if (FINE || j == 0) acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -259,7 +271,7 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
   for (int r = 0; r < 4; ++r) {
     const int64_t t = 4 * q + r;
     if (t >= a.rows) continue;
-    const float xs = a.x_scale ? a.x_scale[t] : 1.0f;
+    const float xs = a.x_scale ? a.x_scale[t] : a.up;
     static_cast<YT*>(a.y)[t * a.outer + n0 + i] = from_f32<YT>(sum[r] * xs);
   }
 }
@@ -355,7 +367,7 @@ __global__ __launch_bounds__(512, (kManyWaves<XT, BM, FINE>)) void s6_q4_many_ke
     f32x4 acc[2][M];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bf16x8 v0 = values8(c0.c[j]), v1 = values8(c1.c[j]);
+      const bf16x8 v0 = values8<XT>(c0.c[j]), v1 = values8<XT>(c1.c[j]);
 #pragma unroll
       for (int u = 0; u < M; ++u) {
         if (FINE || j == 0) acc[0][u] = acc[1][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -404,7 +416,7 @@ __global__ __launch_bounds__(512, (kManyWaves<XT, BM, FINE>)) void s6_q4_many_ke
     if (t >= rows) continue;
     float v[8];
     load_vec<float, 8>(&ys[t][n], v);
-    const float xs = a.x_scale && !a.parts ? a.x_scale[t0 + t] : 1.0f;
+    const float xs = a.parts ? 1.0f : a.x_scale ? a.x_scale[t0 + t] : a.up;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= xs;
     const int64_t at = (t0 + t) * a.outer + m0 + n;
@@ -431,7 +443,7 @@ __global__ __launch_bounds__(256) void s6_q4_join_kernel(Q4Args a, int slices) {
   float s = 0.0f;
 #pragma unroll 4
   for (int z = 0; z < slices; ++z) s += a.parts[z * all + t * a.outer + n];
-  static_cast<YT*>(a.y)[t * a.outer + n] = from_f32<YT>(s * (a.x_scale ? a.x_scale[t] : 1.0f));
+  static_cast<YT*>(a.y)[t * a.outer + n] = from_f32<YT>(s * (a.x_scale ? a.x_scale[t] : a.up));
 }
 
 // ------------------------------------------------------------------ pack --
@@ -585,7 +597,8 @@ int launch_rows(const Q4Args& a, hipStream_t st) {
   return S6_OK;
 }
 template <typename XT, typename YT>
-int launch_q4(const Q4Args& a, bool vec, hipStream_t st) {
+int launch_q4(Q4Args a, bool vec, hipStream_t st) {
+  a.up = 1.0f / kDown<XT>;
   if (a.fine == 0) return vec ? launch_rows<XT, false, true, YT>(a, st) : launch_rows<XT, false, false, YT>(a, st);
   return vec ? launch_rows<XT, true, true, YT>(a, st) : launch_rows<XT, true, false, YT>(a, st);
 }
