@@ -251,17 +251,23 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t (*buf)[kMaxT / 
   return m;
 }
 
-// V values times f as e4m3; all NaN where nan is set.
+// v / unit with f = 1 / unit but for a rounding or two: what the product lacks of v
+// corrects it, so a value between two codes goes to the one that the quotient does.
+__device__ __forceinline__ float over(float v, float unit, float f) {
+  const float q = v * f;
+  return __builtin_fmaf(__builtin_fmaf(-q, unit, v), f, q);
+}
+// V values over unit as e4m3; all NaN where nan is set.
 template <int V>
-__device__ __forceinline__ void store_q8(uint8_t* p, const float (&v)[V], float f, bool nan) {
+__device__ __forceinline__ void store_q8(uint8_t* p, const float (&v)[V], float unit, float f, bool nan) {
   if constexpr (V == 1) {
-    *p = nan ? 0x7f : (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[0] * f, 0.0f, 0, false);
+    *p = nan ? 0x7f : (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(over(v[0], unit, f), 0.0f, 0, false);
   } else {
     uint32_t o[V / 4];
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
-      int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * f, v[4 * i + 1] * f, 0, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * f, v[4 * i + 3] * f, w, true);
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(over(v[4 * i], unit, f), over(v[4 * i + 1], unit, f), 0, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(over(v[4 * i + 2], unit, f), over(v[4 * i + 3], unit, f), w, true);
       o[i] = nan ? 0x7f7f7f7fu : (uint32_t)w;
     }
     if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
@@ -384,13 +390,13 @@ __global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_add_norm_q8_kernel(No
     top = row_max<MULTI>(top, mbuf, (int)(q & 1));
     const bool nan = top >= 0x7f800000u;
     const float most = top < 0x0d800000u ? 0.0f : __uint_as_float(top);  // 2^-100
-    const float unit = most * (1.0f / kTopQ8);  // 0, or its reciprocal is a normal number, too
+    const float unit = most / kTopQ8;  // 0, or its reciprocal is a normal number, too
     const float f = most > 0.0f ? fast_rcp(unit) : 0.0f;
     if (on && wk.t == 0) a.row_scale[row] = nan ? __builtin_nanf("") : unit;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int64_t i = (int64_t)k * wk.tpr + wk.t;
-      if (on && i < np) store_q8<V>(out + i * V, u[k], f, nan);
+      if (on && i < np) store_q8<V>(out + i * V, u[k], unit, f, nan);
     }
     for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
       float v[V], ww[V];
@@ -399,7 +405,7 @@ __global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_add_norm_q8_kernel(No
       store_vec<Res, V>(ro + i * V, v);
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = v[j] * inv * ww[j];
-      store_q8<V>(out + i * V, v, f, nan);
+      store_q8<V>(out + i * V, v, unit, f, nan);
     }
   }
 }
