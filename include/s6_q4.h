@@ -52,8 +52,9 @@ int s6_q4_linear_workspace_size(int64_t rows, int64_t inner, int64_t outer, int6
 /* s6_add_norm_fwd (s6_block.h) with its output in 8 bits: per row,
  *   r' = r + scale * gamma o x,  o = r' / sqrt(mean(r'^2) + eps) o weight,
  *   out_scale = max|o| / 448,  out = o / out_scale rounded to e4m3.
- * out: (rows, dim) bytes; out_scale: (rows) fp32.  o is fp32: it meets one
- * rounding.  A row whose largest |o| is below 2^-100 is stored as zeros with
+ * out: (rows, dim) bytes; out_scale: (rows) fp32.  o, out_scale and the quotient
+ * are fp32, the quotient is rounded to e4m3 once; the mean is formed without
+ * overflow and without loss of small squares.  A row whose largest |o| is below 2^-100 is stored as zeros with
  * out_scale 0; one that holds a value that is not finite as NaN with
  * out_scale NaN. */
 int s6_add_norm_q8_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, const void* x, int64_t x_stride,

@@ -279,9 +279,12 @@ __device__ __forceinline__ void store_q8(uint8_t* p, const float (&v)[V], float 
 // 16384 bf16 rows of 2560 with an fp32 residual: 104 us (4.4 TB/s), bound by HBM;
 // 256 rows: 4.2 us.  Stores past the caches: 88 us, but what reads the outputs
 // next then loses more (with two such readers 262 us for 255).
+// Six waves per SIMD where a thread has one bf16 piece of a row: 16384 x 2560 98 us, with
+// the five that the registers would leave 104 (fp32 would spill).
 template <typename In, typename Res, int V, int K, bool MULTI, bool WIDE>
-__global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_add_norm_q8_kernel(NormArgs a) {
-  __shared__ float buf[2][2][kMaxT / 64];
+__global__ __launch_bounds__((K == 2 ? 512 : kMaxT), (V == 8 && K == 1 && sizeof(In) == 2 ? 6 : 1))
+void s6_add_norm_q8_kernel(NormArgs a) {
+  __shared__ float buf[2][2][kMaxT / 64], again[2][2][kMaxT / 64];
   __shared__ uint32_t mbuf[2][kMaxT / 64];
   const Walk wk = walk_of<MULTI>(a.rows);
   const int64_t np = (a.dim + V - 1) / V;
@@ -361,7 +364,28 @@ __global__ __launch_bounds__(K == 2 ? 512 : kMaxT) void s6_add_norm_q8_kernel(No
       for (int j = 0; j < V; ++j) s = __builtin_fmaf(v[j], v[j], s);
     }
     row_sum2<MULTI>(s, unused, buf, (int)(q & 1));
-    const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(s, inv_d, a.eps));
+    const float mean = __builtin_fmaf(s, inv_d, a.eps);
+    float inv = __builtin_amdgcn_rsqf(mean);
+    if (!(s < __builtin_inff() && mean >= 0x1p-90f)) {
+      // squares past the range of fp32 (the whole row sees the same sum): again,
+      // of values that are not
+      const float p = mean < 1.0f ? 0x1p90f : 0x1p-80f;
+      s = 0.0f;
+      auto square = [&](const float (&v)[V]) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s = __builtin_fmaf(v[j] * p, v[j] * p, s);
+      };
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (on && (int64_t)k * wk.tpr + wk.t < np) square(u[k]);
+      for (int64_t i = (int64_t)K * wk.tpr + wk.t; WIDE && on && i < np; i += wk.tpr) {
+        float v[V];
+        wide(i, v);
+        square(v);
+      }
+      row_sum2<MULTI>(s, unused, again, (int)(q & 1));
+      inv = __builtin_amdgcn_rsqf(__builtin_fmaf(s, inv_d, a.eps * p * p)) * p;
+    }
     uint32_t top = 0;
     auto larger = [&](const float (&v)[V]) {
 #pragma unroll

@@ -1,5 +1,5 @@
 """The norm with an 8-bit output (include/s6_q4.h): which code a value between two
-gets."""
+gets, and rows whose squares are no fp32 numbers."""
 import numpy as np
 import pytest
 
@@ -45,3 +45,40 @@ def test_codes_are_those_of_the_quotient(torch_cuda, dim, dtype):
         want = (x * wt / sc[:, None]).to(torch.float8_e4m3fn)
         wrong += int((out.view(torch.uint8) != want.view(torch.uint8)).sum())
     assert wrong == 0
+
+
+@pytest.mark.parametrize("size,eps", [(1e20, 1e-5), (1e37, 1e-5), (1e-22, 0.0), (1e-30, 0.0), (1e-16, 1e-33)])
+@pytest.mark.parametrize("rows,dim", [(5, 64), (3, 1000), (5, 2560), (2, 20000), (3000, 96)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_whose_squares_overflow_or_vanish(torch_cuda, dtype, rows, dim, size, eps):
+    """The outputs are of the weight's size whatever that of the row, among rows of
+    ordinary size.  Bars as the norm's other tests: 2^-18 of the largest output for the
+    scale, half a step of a code for the codes."""
+    from selective_state_space_63_amd import q4
+    torch = torch_cuda
+    print(f"[case] squares past fp32 {size} {eps} {rows} {dim} {dtype}", flush=True)
+    g = np.random.default_rng([102, dim, rows])
+    x = g.standard_normal((rows, dim))
+    x[::2] *= size
+    x = torch.from_numpy(x.astype(np.float32)).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    w = torch.from_numpy((1 + 0.3 * g.standard_normal(dim)).astype(np.float32)).cuda()
+    out, sc, res = q4.add_norm_q8_fwd(x, w, eps=eps)
+    r = x.double()
+    o = r / torch.sqrt((r * r).mean(-1, keepdim=True) + eps) * w.double()
+    assert torch.equal(res.double(), r)
+    top = o.abs().amax(-1)
+    assert bool(((sc.double() * 448 - top).abs() <= 2.0 ** -18 * top).all())
+    v = o / sc.double()[:, None]
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp_min(2.0 ** -6))) - 3)
+    assert bool(((out.double() - v).abs() <= step / 2 + 2.0 ** -17 * v.abs()).all())
+
+
+def test_infinite_rows_are_nan(torch_cuda):
+    from selective_state_space_63_amd import q4
+    torch = torch_cuda
+    for dim in (64, 2560, 20000):
+        x = torch.randn(4, dim, device="cuda") * 1e20
+        x[1, 5], x[2, 7] = float("inf"), float("nan")
+        out, sc, _ = q4.add_norm_q8_fwd(x, torch.ones(dim, device="cuda"))
+        assert torch.isnan(sc).tolist() == [False, True, True, False]
+        assert torch.isnan(out.float()).all(-1).tolist() == [False, True, True, False]
