@@ -3,7 +3,9 @@ with 4-bit weights and group scales, their packing, and the norm before a
 block with an 8-bit output.
 
 As in ``block``: argument marshalling only, torch device tensors in and out,
-work enqueued on the current stream of the tensors' device.
+work enqueued on the current stream of the tensors' device.  These operators are
+for answering, not for training: they have no gradients, and q4_linear and
+add_norm_q8_fwd refuse inputs that ask for one (unless under torch.no_grad).
 """
 from __future__ import annotations
 
@@ -42,6 +44,12 @@ def _load():
     return _lib
 
 
+def _no_gradient(name, *tensors):
+    """Refuses inputs whose gradient would be lost."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{name} has no gradient and an input requires one: detach it, or call under torch.no_grad()")
+
+
 def q4_pack(w, group=128):
     """4-bit codes and group scales of w (outer, inner) in float32 or bfloat16
     (rows may be slices of wider ones): (weight, scales), uint8 (outer, inner /
@@ -66,6 +74,7 @@ def q4_linear(x, weight, scales, x_scale=None, out_dtype=None, y=None):
     x_scale (...), as add_norm_q8_fwd leaves them; x may be a slice of wider
     rows.  Returns (..., outer) in out_dtype, float32 or bfloat16 (unless
     given: x's, bfloat16 for 8-bit rows)."""
+    _no_gradient("q4_linear", x, scales, x_scale)
     dt = x.dtype
     if dt not in _XT:
         raise ValueError(f"unsupported x dtype {dt}")
@@ -117,6 +126,7 @@ def add_norm_q8_fwd(x, weight, residual=None, gamma=None, scale=1.0, eps=1e-5, r
     eps) * weight, out_scale = max|o| / 448, out = o / out_scale.  Returns
     (out in float8_e4m3fn, out_scale (...) fp32, r' in the residual's dtype);
     residual_out may be the residual itself."""
+    _no_gradient("add_norm_q8_fwd", x, weight, residual, gamma)
     dt = _dtype(x)
     stride = x.shape[-1] if x.is_contiguous() and x.is_cuda else _flat(x, "x", x.shape, dt)
     rt = residual.dtype if residual is not None else residual_dtype or torch.float32
