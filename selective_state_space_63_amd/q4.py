@@ -46,8 +46,10 @@ def _load():
 
 def _no_gradient(name, *tensors):
     """Refuses inputs whose gradient would be lost."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError(f"{name} has no gradient and an input requires one: detach it, or call under torch.no_grad()")
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} has no gradient and an input requires one: detach it, or call under "
+                             "torch.no_grad()")
 
 
 def q4_pack(w, group=128):
