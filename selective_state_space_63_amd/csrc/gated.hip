@@ -810,8 +810,10 @@ GatedArgs gated_args(const s6_gated_dims& d, int flags, const void* x, const voi
   memset(&a, 0, sizeof(a));
   a.x = x; a.ga = ga; a.gx = gx; a.A = A; a.ba = ba; a.bx = bx;
   a.L = d.seqlen; a.dim = (int)d.dim;
-  a.x_batch = d.x_batch; a.x_token = d.x_token; a.a_batch = d.a_batch; a.a_token = d.a_token;
-  a.g_batch = d.g_batch; a.g_token = d.g_token;
+  a.x_batch = d.x_batch; a.a_batch = d.a_batch; a.g_batch = d.g_batch;
+  // (a stride along a single token may be anything)
+  const bool one = d.seqlen == 1;
+  a.x_token = one ? d.dim : d.x_token; a.a_token = one ? d.dim : d.a_token; a.g_token = one ? d.dim : d.g_token;
   a.unit = (flags & S6_UNIT_INPUT) != 0;
   return a;
 }

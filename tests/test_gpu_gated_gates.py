@@ -192,3 +192,26 @@ def test_gate_of_a_start_enters_nothing(torch_cuda, value, dim, dtype, unit):
     want, got = call(0.0), call(value)
     for n in want:
         assert torch.equal(want[n], got[n]), n
+
+
+@pytest.mark.parametrize("which", ["x", "gate_a", "gate_x"])
+@pytest.mark.parametrize("step", [0, 8, (1 << 30) + 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_token_stride_of_a_single_token_is_not_read(torch_cuda, dtype, step, which):
+    """One token of rows that overlap, or whose stride is past 32 bits of bytes."""
+    from selective_state_space_63_amd import gated
+    torch = torch_cuda
+    print(f"[case] stride of a single token {step} {dtype} {which}", flush=True)
+    dim = 66
+    g = np.random.default_rng(76)
+    k = {n: rows(torch, g, (1, 1, dim), dtype) for n in ("x", "gate_a", "gate_x")}
+    dy, A = rows(torch, g, (1, 1, dim), dtype), -torch.from_numpy(g.uniform(0.05, 0.5, dim).astype(np.float32)).cuda()
+    zero = torch.zeros(dim, device="cuda")
+    k[which][0, 0, 40] = float("nan")
+    want = gated.gated_scan_bwd(**k, A=A, dy=dy, bias_a=zero, bias_x=zero)
+    k[which] = k[which].flatten().as_strided((1, 1, dim), (dim, step, 1))
+    got = gated.gated_scan_bwd(**k, A=A, dy=dy, bias_a=zero, bias_x=zero)
+    others = [c for c in range(dim) if c != 40]
+    for n in want:
+        assert bool(torch.isfinite(got[n][..., others]).all()), n
+        assert torch.equal(got[n][..., others], want[n][..., others]), n
