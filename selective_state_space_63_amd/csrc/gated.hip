@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kGC = 64;                // channels of a tile
 constexpr int kGT = S6_GATED_TOKENS;   // tokens of a tile
+constexpr int64_t kMaxRow = 1 << 24;   // most elements from token to token
 constexpr int kMaxTiles = 1 << 22; // workgroups of a launch (threads below 2^32)
 // Waves of a workgroup, and of a SIMD, which the registers leave room for.  The
 // forward on pairs of bf16: four of 16 tokens by two channels per lane, 124
@@ -296,6 +297,8 @@ template <typename In, int VEC, int W>
 __device__ __forceinline__ Rows rows_of(const void* base, int64_t batch_stride, int64_t token_stride, const GatedArgs& a,
                                         const Place<VEC, W>& p) {
   constexpr int n = VEC * Place<VEC, W>::T;
+  // offsets past the rows' end pass the buffer's and do not wrap
+  static_assert((uint64_t)(n + 1) * kMaxRow * sizeof(In) < 1ull << 32, "a wave's tokens lie within 32 bits");
   const int64_t left = a.L - p.w0;
   const uint32_t rows = left < 0 || !base ? 0 : left < n ? (uint32_t)left : n;
   const uint32_t cols = a.dim - p.c0 < kGC ? (uint32_t)(a.dim - p.c0) : kGC;
@@ -711,8 +714,6 @@ __global__ __launch_bounds__(256) void s6_gated_step_kernel(GatedArgs a, float* 
 }
 
 // ------------------------------------------------------------------ host --
-constexpr int64_t kMaxRow = 1 << 24;  // elements from token to token: a wave's 16 tokens in 32 bits
-
 int check_gated(const s6_gated_dims* d, int in_dtype, int flags, bool gx, bool tokens) {
   if (!d) return S6_ERR_NULL;
   if (in_dtype != S6_F32 && in_dtype != S6_BF16) return S6_ERR_DTYPE;

@@ -24,7 +24,6 @@ namespace s6i {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 struct Q4Args {
   const void* x;
@@ -76,9 +75,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, uint3
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(v), 0, __builtin_amdgcn_readfirstlane(bytes),
                                            0x00027000);
 }
-// Offsets past every buffer (the host keeps buffers below 2^28 bytes): of a
-// row that does not exist, and of columns; their sum is one too.
+// Offsets past every buffer (each is below 2^28 bytes): of a row that does not
+// exist, and of columns; their sum is one too.
 constexpr uint32_t kNoRow = 0x80000000u, kNoColumn = 0x40000000u;
+constexpr int64_t kMaxStride = 1 << 20;   // most columns, and elements from row to row
+template <typename XT>
+constexpr bool rows_fit(int rows) { return rows * kMaxStride * (int64_t)sizeof(XT) < 1 << 28; }
+static_assert(16 * (kMaxStride / 2) < 1 << 28 && 16 * (kMaxStride / 32) * 2 < 1 << 28, "16 weight rows, and their scales");
+constexpr int kFewRows = 16;              // most rows of the few-row kernel
 
 // Eight consecutive values of x as loaded, and as bf16 parts whose sum they are.
 template <typename XT, bool XV>
@@ -222,6 +226,7 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
   const int i = lane & 15, q = lane >> 4;
   const int64_t n0 = (a.base + blockIdx.x) * 16;
   const WRows<FINE> wr(a, n0);
+  static_assert(rows_fit<XT>(kFewRows), "x's buffer");
   const int rows = (int)a.rows;
   const uint32_t step = (uint32_t)a.x_stride * kE;
   const __amdgpu_buffer_rsrc_t xb = buffer_at(a.x, (uint32_t)(rows - 1) * step + (uint32_t)a.inner * kE);
@@ -291,7 +296,10 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
 // x straight to registers, every wave all of a tile's rows: 42 us (16 bytes of
 // each of 16 rows a load); more blocks under way from memory: no change.
 constexpr int kBN = 128;
-constexpr int kXP = kBlk + 8;  // pitch of a row of x in LDS: 16 rows in 16 bytes meet all banks once
+// Pitch of a row of x in LDS: 16 bytes of each of 16 rows lie in all banks once.
+// Some accesses meet all the same, as lanes are not served in the order of rows:
+// SQ_LDS_BANK_CONFLICT is 14 % of the busy cycles (256 8-bit rows of 2560 to 10576).
+constexpr int kXP = kBlk + 8;
 constexpr int kYP = kBN + 4;   // pitch of a row of sums
 constexpr size_t many_lds(int bm, int parts) { return (size_t)2 * 2 * parts * bm * kXP * sizeof(uint16_t); }
 static_assert(many_lds(32, 1) >= 32 * kYP * sizeof(float), "the sums take the place of x");
@@ -306,6 +314,7 @@ __global__ __launch_bounds__(512, (kManyWaves<XT, BM, FINE>)) void s6_q4_many_ke
   using Tile = uint16_t(*)[kXP];
   constexpr uint32_t kE = sizeof(XT);
   constexpr int M = BM / 16, NP = X::kParts;
+  static_assert(rows_fit<XT>(BM), "x's buffer");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 2;
   const int i = lane & 15, q = lane >> 4;
   const int64_t m0 = (a.base + blockIdx.x) * kBN, t0 = (int64_t)blockIdx.y * BM;
@@ -488,7 +497,6 @@ __global__ __launch_bounds__(256) void s6_q4_pack_kernel(const In* w, int64_t st
 }
 
 // ------------------------------------------------------------------ host --
-constexpr int64_t kMaxStride = 1 << 20;   // columns, and elements from row to row: a tile's 64 rows below 2^28 bytes
 constexpr int64_t kMaxGrid = 1 << 22;  // workgroups of a launch in x (threads below 2^32)
 
 int check_q4(int64_t rows, int64_t inner, int64_t outer, int64_t group, int64_t stride) {
@@ -506,7 +514,7 @@ int check_q4(int64_t rows, int64_t inner, int64_t outer, int64_t group, int64_t 
 // With it and with the second, us: fp32 of 5120 to 2560, groups of 32, 6 rows 11.8
 // and 10.5, 16 14.8 and 11.7, of 2560 to 10576 6 rows 14.5 both; bf16 of 2560 to
 // 10576, 8 rows 8.9 and 10.5, 16 11.5 both, 24 (two tiles of rows) 16 and 13.
-int64_t few_rows(int x_dtype) { return x_dtype == S6_F32 ? 6 : 16; }
+int64_t few_rows(int x_dtype) { return x_dtype == S6_F32 ? 6 : kFewRows; }
 constexpr int64_t kLaunchRows = 32768;    // most rows of a launch of the second
 
 // Rows of x to a workgroup of the second kernel.  Measured with 32 and with 64, us:
