@@ -48,7 +48,7 @@ def test_codes_are_those_of_the_quotient(torch_cuda, dim, dtype):
 
 
 @pytest.mark.parametrize("size,eps", [(1e20, 1e-5), (1e37, 1e-5), (1e-22, 0.0), (1e-30, 0.0), (1e-16, 1e-33)])
-@pytest.mark.parametrize("rows,dim", [(5, 64), (3, 1000), (5, 2560), (2, 20000), (3000, 96)])
+@pytest.mark.parametrize("rows,dim", [(5, 64), (3, 77), (3, 1000), (5, 2560), (2, 4099), (2, 20000), (3000, 96)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_whose_squares_overflow_or_vanish(torch_cuda, dtype, rows, dim, size, eps):
     """The outputs are of the weight's size whatever that of the row, among rows of
