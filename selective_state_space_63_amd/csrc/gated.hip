@@ -20,13 +20,16 @@
 // P_{k-1} s_{k-1} + H_{k-1}, whichever of these a workgroup reads or forms
 // itself, so repeated calls give identical bits.
 //
-// Measured (bf16, us; floor: the bytes of one pass at 5.1 TB/s, a large copy's):
-// 8 x 2048 tokens of 5120 channels 146 (floor 132; 4.6 TB/s), 65536 tokens of 1536
-// 194 (158), 2 x 2048 of 1536 18 (10), the gradients of 8 x 2048 x 5120 300 (230).
-// HBM, and beside it the VALU: 33 instructions an element, six of them
-// transcendental, 63 % of the busy cycles (gradients 80 and 67 %).  Passes that
-// first reduce segments and then read all inputs again would take 1.75 times the
-// bytes.
+// (A single-pass prefix scan with decoupled look-back, a published method.)
+//
+// Measured (bf16, us; floor: the bytes of one pass at 6.25 TB/s, what a large
+// elementwise pass reaches): 8 x 2048 tokens of 5120 channels 137 (floor 107; 4.9
+// TB/s), 65536 tokens of 1536 183 (129), 2 x 2048 of 1536 18 (8), the gradients of
+// 8 x 2048 x 5120 301 (188; 3.9 TB/s).  Neither HBM nor the VALU is full: 35
+// instructions an element, six of them transcendental, take 71 % of the busy cycles
+// (gradients 92 and 76 %); loads, walk and stores of a workgroup follow one
+// another.  Passes that first reduce segments and then read all inputs again would
+// take 1.75 times the bytes.
 #include "s6_gated.h"
 
 #include "block_internal.h"
@@ -41,9 +44,9 @@ constexpr int64_t kMaxRow = 1 << 24;   // most elements from token to token
 constexpr int kMaxTiles = 1 << 22; // workgroups of a launch (threads below 2^32)
 // Waves of a workgroup, and of a SIMD, which the registers leave room for.  The
 // forward on pairs of bf16: four of 16 tokens by two channels per lane, 124
-// VGPRs (eight of 8 tokens, six per SIMD: 65536 tokens of 1536 205 us, else 194;
-// 8 x 2048 of 5120 155, else 146); fp32 would spill there.  Gradients with 16
-// waves a workgroup: training of 8 x 2048 x 5120 605 us, with eight 449.
+// VGPRs (eight of 8 tokens, six per SIMD: 65536 tokens of 1536 187 us, else 183;
+// 8 x 2048 of 5120 141, else 137); fp32 would spill there.  Gradients with 16
+// waves a workgroup: training of 8 x 2048 x 5120 599 us, with eight 443.
 template <typename In, int VEC>
 constexpr int kFwdW = sizeof(In) == 2 && VEC == 2 ? 4 : 8;
 template <typename In, int VEC>
@@ -189,8 +192,8 @@ __device__ __forceinline__ void put_as(__amdgpu_buffer_rsrc_t r, uint32_t off, c
     __builtin_amdgcn_raw_buffer_store_b16(from_f32<In>(f[0]), r, off, 0, AUX);
 }
 // Whole lines are stored past the caches, which the inputs need (8 x 2048 x 5120:
-// 153 -> 146 us, training 470 -> 449); lines that two columns share wait there
-// for one another (8 x 2048 x 5000 past the caches as well: 158 -> 183 us).
+// 143 -> 137 us, training 459 -> 443); lines that two columns share wait there
+// for one another (8 x 2048 x 5000 past the caches as well: 159 -> 184 us).
 template <typename In, int VEC>
 __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[VEC], int stream) {
   if (VEC == 2 && stream)
@@ -266,8 +269,8 @@ __device__ __forceinline__ Place<VEC, W> place_of(const GatedArgs& a, int tile) 
 // eight XCDs in turn, and each XCD takes a run of neighbouring columns (of tiles
 // along a sequence), since rows that do not begin at a line's start have lines
 // that two columns share.  A tile and those before it come from one counter, in
-// order.  One run and one counter for all: 2 x 2048 x 1536 26.8 us, else 18.5;
-// 8 x 2048 x 5120 159, else 146; training of 8 x 2048 x 5000 516, else 454.
+// order.  One run and one counter for all: 2 x 2048 x 1536 25.9 us, else 18.0;
+// 8 x 2048 x 5120 154, else 137; training of 8 x 2048 x 5000 522, else 466.
 __device__ __forceinline__ int draw_tile(const GatedArgs& a, uint32_t* shared) {
   const int wg = a.base + (int)blockIdx.x;
   const int x = wg & ((1 << a.xcds) - 1);
@@ -678,8 +681,8 @@ __global__ __launch_bounds__(256) void s6_gated_init_kernel(u32x4* slots, int64_
 }
 
 // ------------------------------------------------------------------ step --
-// A channel to a lane, or two.  256 x 5120: 6.1 us (floor 4.1: 21 MB), one row of
-// 1536 2.6, the launch.
+// A channel to a lane, or two.  256 x 5120: 6.0 us (floor 3.4: 21 MB), one row of
+// 1536 2.5, the launch.
 template <typename In, int VEC>
 __global__ __launch_bounds__(256) void s6_gated_step_kernel(GatedArgs a, float* hs) {
   const int64_t per = (a.dim + VEC - 1) / VEC, i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;

@@ -276,9 +276,10 @@ __device__ __forceinline__ void store_q8(uint8_t* p, const float (&v)[V], float 
 
 // As s6_add_norm_kernel, with the row's largest output found before any is
 // stored: the outputs stay in registers, or are formed again past them.
-// 16384 bf16 rows of 2560 with an fp32 residual: 104 us (4.4 TB/s), bound by HBM;
-// 256 rows: 4.2 us.  Stores past the caches: 88 us, but what reads the outputs
-// next then loses more (with two such readers 262 us for 255).
+// 16384 bf16 rows of 2560 with an fp32 residual: 98 us (4.7 TB/s, floor 74), bound
+// by HBM; 256 rows: 4.3 us.  Stores past the caches took 88 us where these took
+// 104, but a sum of the codes and an addition to the residual right after took
+// longer by more (262 us for 255 in all); not timed where a layer lies between.
 // Six waves per SIMD where a thread has one bf16 piece of a row: 16384 x 2560 98 us, with
 // the five that the registers would leave 104 (fp32 would spill).
 template <typename In, typename Res, int V, int K, bool MULTI, bool WIDE>

@@ -213,9 +213,10 @@ __device__ __forceinline__ void scales_of(uint32_t s, float (&f)[4]) {
 // (first operand) by 16 weight rows: lane l gets the sums of x rows 4 (l / 16)
 // to + 3 and weight row l % 16, whose scale is then the lane's own.  Rows and
 // columns that do not exist are loaded as 0 through the buffers' ends.
-// One bf16 row of 2560 to 10576: 6.4 us (floor 2.8: 14 MB of codes), 16 rows of
-// 5120 to 2560, groups of 32: 9.6 (1.5), a launch and the latency of loads that
-// are all under way at once.
+// One bf16 row of 2560 to 10576: 6.3 us (floor 2.2: 14 MB of codes), a launch and
+// the latency of loads that are all under way at once; 16 rows 11.4, 16 of 5120 to
+// 2560 in groups of 32 9.4 (1.2): x is read again for every 16 weight rows, 54 MB
+// of it for 16 rows of 2560 to 10576.  One fp32 row 12.6: it is split again there too.
 template <typename XT, bool FINE, bool XV, typename YT>
 __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
   extern __shared__ float part[];  // (W - 1, 64, 4)
@@ -289,7 +290,7 @@ __global__ __launch_bounds__(1024) void s6_q4_few_kernel(Q4Args a) {
 // lines.  blockIdx.z: a slice of the columns, its sums left in the workspace
 // where there are several.
 //
-// 256 8-bit rows of 2560 to 10576, groups of 128: 26 to 27 us, of which 3 the launch,
+// 256 8-bit rows of 2560 to 10576, groups of 128: 27 us (floor 10), of which 3 the launch,
 // 5 before and after the turns.  LDS reads, conversions and products would take
 // 7.4, 6.5 and 5.5 us of each CU; with two waves per SIMD that meet at every
 // turn they mostly go one after another.  One block a turn without halves: 34 us;
@@ -457,7 +458,8 @@ __global__ __launch_bounds__(256) void s6_q4_join_kernel(Q4Args a, int slices) {
 
 // ------------------------------------------------------------------ pack --
 // A thread has 32 columns of a row; the group's largest |w| meets over its
-// one, two or four threads (neighbours: a wave holds whole groups).
+// one, two or four threads (neighbours: a wave holds whole groups).  10576 x 2560:
+// bf16 17.8 us (floor 11), fp32 20.5 (20).
 template <typename In>
 __global__ __launch_bounds__(256) void s6_q4_pack_kernel(const In* w, int64_t stride, uint8_t* codes, uint16_t* scales,
                                                          int64_t base, int64_t total, int64_t per, int group) {
@@ -512,8 +514,9 @@ int check_q4(int64_t rows, int64_t inner, int64_t outer, int64_t group, int64_t 
 
 // Most rows of the first kernel, which reads x again for every 16 weight rows.
 // With it and with the second, us: fp32 of 5120 to 2560, groups of 32, 6 rows 11.8
-// and 10.5, 16 14.8 and 11.7, of 2560 to 10576 6 rows 14.5 both; bf16 of 2560 to
-// 10576, 8 rows 8.9 and 10.5, 16 11.5 both, 24 (two tiles of rows) 16 and 13.
+// and 10.5, 16 14.8 and 11.7, of 2560 to 10576 6 rows 13.9 and 14.2; bf16 of 2560 to
+// 10576, 8 rows 8.9 and 10.5, 16 11.4 both, 24 (two tiles of rows) 16 and 13; of 8192
+// to 3305, where the first loses sooner, 16 rows 13.6 and 17 with the second 12.4.
 int64_t few_rows(int x_dtype) { return x_dtype == S6_F32 ? 6 : kFewRows; }
 constexpr int64_t kLaunchRows = 32768;    // most rows of a launch of the second
 
