@@ -38,11 +38,12 @@ int s6_q4_pack(int64_t outer, int64_t inner, int64_t group, int in_dtype, const 
  * S6_BF16, or S6_E4M3 with one fp32 factor per row in x_scale (NULL: 1; only
  * with S6_E4M3); y (rows, outer) contiguous, in y_dtype S6_F32 or S6_BF16.
  * Products are exact, sums fp32, scales fp32; an fp32 x enters in full (three
- * bf16 parts; below 2^-109 up to 2^-134).  The sum of a group is finite whatever
- * x holds: what overflows is the result or a sum of scaled groups past 2^138 (8-bit x:
- * 2^128).  Any number of rows; made for the few rows of single tokens.
- * codes are 16-byte aligned, x_stride is at most 2^20.  workspace: s6_q4_linear_workspace_size bytes, 0
- * up to 16 rows (of fp32: 6).  Repeated calls give identical bits. */
+ * bf16 parts; below 2^-109 up to 2^-134).  The sum of a group of finite values is
+ * finite: what overflows is the result, or a sum of scaled groups past 2^138 (8-bit
+ * x: 2^128).  Any number of rows; made for the few rows of single tokens.  codes
+ * are 16-byte aligned, x_stride is at most 2^20.  workspace:
+ * s6_q4_linear_workspace_size bytes, 0 up to 16 rows (of fp32: 6).  Repeated calls
+ * give identical bits. */
 int s6_q4_linear(int64_t rows, int64_t inner, int64_t outer, int64_t group, int x_dtype, int y_dtype, const void* x,
                  int64_t x_stride, const float* x_scale, const void* codes, const void* scales, void* y,
                  void* workspace, size_t workspace_bytes, void* stream);
@@ -54,9 +55,9 @@ int s6_q4_linear_workspace_size(int64_t rows, int64_t inner, int64_t outer, int6
  *   out_scale = max|o| / 448,  out = o / out_scale rounded to e4m3.
  * out: (rows, dim) bytes; out_scale: (rows) fp32.  o, out_scale and the quotient
  * are fp32, the quotient is rounded to e4m3 once; the mean is formed without
- * overflow and without loss of small squares.  A row whose largest |o| is below 2^-100 is stored as zeros with
- * out_scale 0; one that holds a value that is not finite as NaN with
- * out_scale NaN. */
+ * overflow and without loss of small squares.  A row whose largest |o| is below
+ * 2^-100 is stored as zeros with out_scale 0; one that holds a value that is not
+ * finite as NaN with out_scale NaN. */
 int s6_add_norm_q8_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, const void* x, int64_t x_stride,
                        const void* residual, const float* weight, const float* gamma, float scale, float eps, void* out,
                        float* out_scale, void* residual_out, void* stream);
